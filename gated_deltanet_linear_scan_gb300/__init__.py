@@ -7,7 +7,8 @@ sm_103a kernels; there is no fallback. If libgdn.so has not been built, the
 first call raises (``build_if_needed()`` builds it with nvcc).
 
 Tensors are torch CUDA tensors (float32, or int32 for slot ids), contiguous,
-with the layouts documented in include/gdn.h.
+with the layouts documented in include/gdn.h. The attention calls also take
+float16 and bfloat16, and q, k, v that are slices of a wider row.
 """
 import ctypes
 import os
@@ -33,6 +34,10 @@ __all__ = [
     "gdn_block_prefill_chunked_varlen_workspace_size", "gdn_block_prefill_varlen",
     "gdn_block_prefill_chunked_varlen", "gdn_block_prefill_snapshots_varlen",
     "gdn_snapshot_restore_varlen", "gdn_selftest_bounded_wait",
+    "gdn_kv_append", "gdn_attn_decode_workspace_size", "gdn_attn_decode",
+    "gdn_attn_prefill_workspace_size", "gdn_attn_prefill", "gdn_pages_workspace_size",
+    "gdn_pages_copy", "gdn_pages_reserve", "gdn_pages_fork", "gdn_pages_truncate",
+    "gdn_pages_compact",
 ]
 
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_NULL", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_UNSUPPORTED",
@@ -104,7 +109,26 @@ _SIGS = {
     "gdn_block_prefill_snapshots_varlen": ([_P] * 14 + [_I] * 7 + [_F, _F, _F, _P, _I, _P, _P,
                                                                  ctypes.c_size_t, _P], _I),
     "gdn_snapshot_restore_varlen": ([_P] * 6 + [_I] * 7 + [_P, _I, _P, _P], _I),
+    "gdn_kv_append": ([_P] * 7 + [_I] * 10 + [_P, _I, _P, _P], _I),
+    "gdn_attn_decode_workspace_size": ([_I] * 5, ctypes.c_size_t),
+    "gdn_attn_decode": ([_P] * 6 + [_I] * 10 + [_F, _I, _I, _P, _I, _P, _P, ctypes.c_size_t, _P],
+                        _I),
+    "gdn_attn_prefill_workspace_size": ([_I] * 5, ctypes.c_size_t),
+    "gdn_attn_prefill": ([_P] * 7 + [_I] * 11 + [_F, _I, _I, _P, _I, _P, _P, ctypes.c_size_t, _P],
+                         _I),
+    "gdn_pages_workspace_size": ([_I, _I], ctypes.c_size_t),
+    "gdn_pages_copy": ([_P] * 3 + [_I] * 3 + [ctypes.c_size_t, _P, _P], _I),
+    "gdn_pages_reserve": ([_P] * 5 + [_I] * 4 + [ctypes.c_size_t, _I, _P, _I, _P, _P,
+                                                 ctypes.c_size_t, _P], _I),
+    "gdn_pages_fork": ([_P] * 6 + [_I] * 4 + [ctypes.c_size_t, _I, _I, _P, _P, ctypes.c_size_t,
+                                              _P], _I),
+    "gdn_pages_truncate": ([_P] * 4 + [_I] * 4 + [_P, _I, _P, _P], _I),
+    "gdn_pages_compact": ([_P] * 4 + [_I] * 3 + [ctypes.c_size_t, _I, _I, _P, _P,
+                                                 ctypes.c_size_t, _P], _I),
 }
+
+# gdn_dtype codes by torch type name.
+_DTYPES = {"float32": 0, "float16": 1, "bfloat16": 2}
 
 # Size of the fixed device scratch of gdn_block_prefill_noalloc (include/gdn.h).
 PREFILL_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -178,6 +202,34 @@ def _ptr(t, name, dtype=None, optional=False):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _dtype(t, name):
+    """The gdn_dtype code of a tensor's type."""
+    code = _DTYPES.get(str(getattr(t, "dtype", None)).rpartition(".")[2])
+    if code is None:
+        raise TypeError(f"{name} must be a float32, float16 or bfloat16 tensor")
+    return code
+
+
+def _rows(t, name, dtype, heads, head_dim):
+    """(data pointer, elements from row to row) of [rows][heads][head_dim], dense in its last
+    two dimensions; the rows may be slices of wider ones."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.is_contiguous():
+        return t.data_ptr(), heads * head_dim
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
+        raise ValueError(f"{name} must be contiguous or have shape [rows, {heads}, {head_dim}]")
+    row, head, elem = t.stride()
+    if (head_dim > 1 and elem != 1) or (heads > 1 and head != head_dim):
+        raise ValueError(f"{name} must be dense in its last two dimensions")
+    return t.data_ptr(), row if t.shape[0] > 1 else max(row, heads * head_dim)
 
 
 def _slots(slots):
@@ -637,3 +689,132 @@ def gdn_snapshot_restore_varlen(state, snaps, accepted, cu_seqlens, n_seqs, tota
         _ptr(conv_snaps, "conv_snaps", optional=True), _ptr(accepted, "accepted", torch.int32),
         _cu(cu_seqlens), n_seqs, total_tokens, max_tokens, n_v_heads, state_size, conv_dim,
         conv_kernel, _slots(slots), pool, _errc(err_count), _stream(stream)))
+
+
+# ------------------------------------------------------------------ attention layers
+
+def gdn_kv_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, n_seqs, total_tokens,
+                  n_kv_heads, head_dim, page_size, n_pages, max_pages, slots=None, pool=None,
+                  err_count=None, stream=None):
+    """Write new tokens' keys and values into the pages (cu_seqlens None: the same number of
+    rows for every sequence). k and v may be slices of wider rows."""
+    pool = _pool(pool, n_seqs, slots)
+    i32 = _torch().int32
+    kp, k_stride = _rows(k, "k", k_pages.dtype, n_kv_heads, head_dim)
+    vp, v_stride = _rows(v, "v", k_pages.dtype, n_kv_heads, head_dim)
+    _check("gdn_kv_append", library().gdn_kv_append(
+        kp, vp, _ptr(k_pages, "k_pages", k_pages.dtype), _ptr(v_pages, "v_pages", k_pages.dtype),
+        _ptr(page_table, "page_table", i32), _ptr(kv_lens, "kv_lens", i32),
+        _ptr(cu_seqlens, "cu_seqlens", i32, optional=True), n_seqs, total_tokens, n_kv_heads,
+        head_dim, page_size, n_pages, max_pages, k_stride, v_stride, _dtype(k_pages, "k_pages"),
+        _slots(slots), pool, _errc(err_count), _stream(stream)))
+
+
+def gdn_attn_decode_workspace_size(n_seqs, n_tokens, n_q_heads, n_kv_heads, head_dim):
+    return library().gdn_attn_decode_workspace_size(n_seqs, n_tokens, n_q_heads, n_kv_heads,
+                                                    head_dim)
+
+
+def gdn_attn_decode(q, k_pages, v_pages, page_table, kv_lens, out, n_seqs, n_tokens, n_q_heads,
+                    n_kv_heads, head_dim, page_size, n_pages, max_pages, window, n_sinks, scale,
+                    workspace, slots=None, pool=None, err_count=None, stream=None):
+    """Attention of each sequence's last n_tokens tokens over its paged cache."""
+    pool = _pool(pool, n_seqs, slots)
+    i32, dt = _torch().int32, k_pages.dtype
+    qp, q_stride = _rows(q, "q", dt, n_q_heads, head_dim)
+    _check("gdn_attn_decode", library().gdn_attn_decode(
+        qp, _ptr(k_pages, "k_pages", dt), _ptr(v_pages, "v_pages", dt),
+        _ptr(page_table, "page_table", i32), _ptr(kv_lens, "kv_lens", i32), _ptr(out, "out", dt),
+        n_seqs, n_tokens, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages, window,
+        n_sinks, scale, q_stride, _dtype(k_pages, "k_pages"), _slots(slots), pool,
+        _errc(err_count), _ws_ptr(workspace), _ws_bytes(workspace), _stream(stream)))
+
+
+def gdn_attn_prefill_workspace_size(n_seqs, total_tokens, n_q_heads, n_kv_heads, head_dim):
+    return library().gdn_attn_prefill_workspace_size(n_seqs, total_tokens, n_q_heads, n_kv_heads,
+                                                     head_dim)
+
+
+def gdn_attn_prefill(q, k_pages, v_pages, page_table, kv_lens, out, cu_seqlens, n_seqs,
+                     total_tokens, max_tokens, n_q_heads, n_kv_heads, head_dim, page_size,
+                     n_pages, max_pages, window, n_sinks, scale, workspace=None, slots=None,
+                     pool=None, err_count=None, stream=None):
+    """Attention of a ragged batch of prompts (or chunks of prompts) over the paged cache."""
+    pool = _pool(pool, n_seqs, slots)
+    i32, dt = _torch().int32, k_pages.dtype
+    qp, q_stride = _rows(q, "q", dt, n_q_heads, head_dim)
+    _check("gdn_attn_prefill", library().gdn_attn_prefill(
+        qp, _ptr(k_pages, "k_pages", dt), _ptr(v_pages, "v_pages", dt),
+        _ptr(page_table, "page_table", i32), _ptr(kv_lens, "kv_lens", i32), _ptr(out, "out", dt),
+        _ptr(cu_seqlens, "cu_seqlens", i32), n_seqs, total_tokens, max_tokens, n_q_heads,
+        n_kv_heads, head_dim, page_size, n_pages, max_pages, window, n_sinks, scale, q_stride,
+        _dtype(k_pages, "k_pages"), _slots(slots), pool, _errc(err_count),
+        None if workspace is None else _ws_ptr(workspace),
+        0 if workspace is None else _ws_bytes(workspace), _stream(stream)))
+
+
+def gdn_pages_workspace_size(n_seqs, n_pages):
+    return library().gdn_pages_workspace_size(n_seqs, n_pages)
+
+
+def _page_data(pages):
+    """The pages of every plane, of any type."""
+    return _ptr(pages, "pages", pages.dtype)
+
+
+def gdn_pages_copy(pages, src, dst, n_copies, n_planes, n_pages, page_bytes, err_count=None,
+                   stream=None):
+    """Page dst[i] <- page src[i] in every plane."""
+    i32 = _torch().int32
+    _check("gdn_pages_copy", library().gdn_pages_copy(
+        _page_data(pages), _ptr(src, "src", i32), _ptr(dst, "dst", i32), n_copies, n_planes,
+        n_pages, page_bytes, _errc(err_count), _stream(stream)))
+
+
+def gdn_pages_reserve(pages, page_table, kv_lens, page_refs, n_new, n_seqs, page_size, n_planes,
+                      n_pages, page_bytes, max_pages, workspace, slots=None, pool=None,
+                      err_count=None, stream=None):
+    """Pages for n_new[n] more tokens of every sequence; kv_lens grow."""
+    pool = _pool(pool, n_seqs, slots)
+    i32 = _torch().int32
+    _check("gdn_pages_reserve", library().gdn_pages_reserve(
+        _page_data(pages), _ptr(page_table, "page_table", i32), _ptr(kv_lens, "kv_lens", i32),
+        _ptr(page_refs, "page_refs", i32), _ptr(n_new, "n_new", i32), n_seqs, page_size, n_planes,
+        n_pages, page_bytes, max_pages, _slots(slots), pool, _errc(err_count),
+        _ws_ptr(workspace), _ws_bytes(workspace), _stream(stream)))
+
+
+def gdn_pages_fork(pages, page_table, kv_lens, page_refs, parents, children, n_forks, page_size,
+                   n_planes, n_pages, page_bytes, max_pages, pool, workspace, err_count=None,
+                   stream=None):
+    """Slot children[i] becomes a copy of slot parents[i], sharing its full pages."""
+    i32 = _torch().int32
+    _check("gdn_pages_fork", library().gdn_pages_fork(
+        _page_data(pages), _ptr(page_table, "page_table", i32), _ptr(kv_lens, "kv_lens", i32),
+        _ptr(page_refs, "page_refs", i32), _ptr(parents, "parents", i32),
+        _ptr(children, "children", i32), n_forks, page_size, n_planes, n_pages, page_bytes,
+        max_pages, pool, _errc(err_count), _ws_ptr(workspace), _ws_bytes(workspace),
+        _stream(stream)))
+
+
+def gdn_pages_truncate(page_table, kv_lens, page_refs, new_lens, n_seqs, page_size, n_pages,
+                       max_pages, slots=None, pool=None, err_count=None, stream=None):
+    """Cut sequences to new_lens[n] tokens (None: free them); their pages past it lose a
+    holder."""
+    pool = _pool(pool, n_seqs, slots)
+    i32 = _torch().int32
+    _check("gdn_pages_truncate", library().gdn_pages_truncate(
+        _ptr(page_table, "page_table", i32), _ptr(kv_lens, "kv_lens", i32),
+        _ptr(page_refs, "page_refs", i32), _ptr(new_lens, "new_lens", i32, optional=True), n_seqs,
+        page_size, n_pages, max_pages, _slots(slots), pool, _errc(err_count), _stream(stream)))
+
+
+def gdn_pages_compact(pages, page_table, kv_lens, page_refs, page_size, n_planes, n_pages,
+                      page_bytes, max_pages, pool, workspace, n_live=None, stream=None):
+    """Move the pages in use to the pool's start; n_live (int32 tensor) receives their count."""
+    i32 = _torch().int32
+    _check("gdn_pages_compact", library().gdn_pages_compact(
+        _page_data(pages), _ptr(page_table, "page_table", i32), _ptr(kv_lens, "kv_lens", i32),
+        _ptr(page_refs, "page_refs", i32), page_size, n_planes, n_pages, page_bytes, max_pages,
+        pool, _ptr(n_live, "n_live", i32, optional=True), _ws_ptr(workspace),
+        _ws_bytes(workspace), _stream(stream)))

@@ -1,0 +1,941 @@
+// gdn_attn_decode.cu -- attention of one new token, or a few draft tokens, of every
+// sequence over its paged key/value cache (sm_103a).
+//
+//   s_j = scale q.k_j over the visible keys, o = sum_j e^{s_j - m} v_j / sum_j e^{s_j - m}
+//
+// Every visible key and value is read once, so HBM bounds the call; the arithmetic has to
+// stay out of the way. All query heads of a key head (times the draft tokens) form the rows
+// of one small matrix product, so a key byte is read once for all of them.
+//
+// Work split. A unit is (sequence, key head, group of at most 16 rows); its keys are cut in
+// tiles (64 keys of a 16-bit type, 32 of fp32). The tiles of all units, in order, are dealt
+// out evenly as one contiguous range per CTA, whatever the lengths: a ragged batch, one long
+// sequence and many short ones all keep every SM equally busy, with no host knowledge of the
+// lengths. A unit that crosses a range boundary leaves partial results (m, l, o) in the
+// workspace; the CTA that arrives last on it joins them in CTA order, so the bits do not
+// depend on timing.
+//
+// Inside a CTA one warp walks the range and issues the TMA loads of the tiles' pages (and of
+// q at a unit's first tile) into a ring of stages; four warps compute. Each of the four
+// takes a quarter of a tile's keys for S = Q K^T, the row maxima are exchanged through
+// shared memory, and each then takes a quarter of the head's columns for O += P V, so the
+// running maximum is shared and O needs no join across warps.
+#include <atomic>
+#include <ctime>
+
+#include "gdn_paged.cuh"
+
+namespace gdn {
+namespace {
+
+__device__ unsigned g_watchdog_attn_decode;
+
+constexpr int kWarps = 4;                       // computing warps
+constexpr int kCompute = 32 * kWarps;           // their threads
+constexpr int kThreads = kCompute + 32;         // and the loading warp
+constexpr int kRows = 16;                       // rows of a unit
+constexpr int kSMs = 152;
+constexpr int kMaxCtas = 2 * kSMs;
+
+// kHead: the unit's first tile lies in this CTA's range.
+enum : int { kFirst = 1, kLast = 2, kWhole = 4, kHead = 8 };
+
+// What the loading warp tells the computing warps about a stage.
+struct Stage {
+    int seq, unit, len, key0, flags;
+    unsigned blocks;  // bit b: keys key0 + 8b .. + 7 lie in a page that was loaded
+    int c0, c1;       // CTAs sharing the unit (when it is not whole here)
+};
+
+struct Params {
+    PagedCache cache;
+    AttnMask mask;
+    void *out;
+    int n_seqs, n_tokens, n_q_heads, group;  // group: query heads of a key head
+    int heads_per_unit, tokens_per_unit;     // rows of a unit: tokens x heads
+    int head_groups, token_groups;
+    float scale_log2;
+    int32_t *err_count;
+    float *partials;                 // [grid][2] records of kRows * (D + 2) floats
+    unsigned long long *counters;    // [grid]
+    unsigned long long nonce;
+};
+
+// RT: rows the arithmetic is laid out for (16-bit types: always 16, one matrix fragment).
+template <typename T, int D, int RT>
+struct Geometry {
+    static constexpr bool kF32 = sizeof(T) == 4;
+    static constexpr int KT = kF32 ? 32 : 64;                              // keys of a tile
+    static constexpr int kCols = D * static_cast<int>(sizeof(T)) / 128;    // 128-byte columns
+    static constexpr int kPlane = KT * D * static_cast<int>(sizeof(T));    // a K (or V) tile
+    static constexpr int QR = RT < 8 ? 8 : RT;                             // q rows kept (whole swizzle atoms)
+    static constexpr int kQ = QR * D * static_cast<int>(sizeof(T));
+    static constexpr int kExtra = kF32 ? 2 * KT * RT * 4             // S, then P [key][row], two buffers
+                                       : 2 * kRows * (KT + 8) * 2;   // P hi and lo [row][key]
+    static constexpr int kCtas = D == 256 ? 1 : 2;                   // per SM
+    // shared memory of a CTA, less alignment slack and the static part
+    static constexpr int kBudget = (kCtas == 1 ? 232448 : 115712) - 1024 - 2560;
+    static constexpr int kStages = (kBudget - 2 * kQ - kExtra) / (2 * kPlane);
+    static constexpr int kSmem = kStages * 2 * kPlane + 2 * kQ + kExtra + 1024;
+    static_assert(kStages >= 2, "two stages at least");
+};
+
+// ------------------------------------------------------------------ waits
+
+// Bounded wait; once one gave up the CTA's later waits return at once and nothing of the
+// units concerned is written.
+__device__ __forceinline__ void wait_or_flag(uint64_t *bar, uint32_t parity, volatile int *dead) {
+    if (*dead) return;
+    if (!mbar_wait(bar, parity)) {
+        *dead = 1;
+        atomicOr(&g_watchdog_attn_decode, WD_STAGE_COPY);
+    }
+}
+
+// One more of the `n` CTAs of a unit has stored its partial result. True in the CTA that
+// completes the count, which also clears the word. A word whose upper bits are not this
+// call's nonce counts as 0, so the workspace needs no initialisation; a captured call keeps
+// its nonce over its replays, each of which leaves the words cleared.
+__device__ __forceinline__ bool last_arrival(unsigned long long *word, unsigned long long nonce,
+                                             int n) {
+    unsigned long long seen = *reinterpret_cast<volatile unsigned long long *>(word);
+    for (;;) {
+        const int count = (seen >> 16) == nonce ? static_cast<int>(seen & 0xFFFFu) : 0;
+        const unsigned long long next = count + 1 == n ? 0 : (nonce << 16) | (count + 1);
+        const unsigned long long was = atomicCAS(word, seen, next);
+        if (was == seen) return count + 1 == n;
+        seen = was;
+    }
+}
+
+// ------------------------------------------------------------------ matrix fragments
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4],
+                                                        uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (&a)[4],
+                                                 uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Byte offset of 16-byte chunk `chunk` of row `row` in a tile of `rows` rows stored as
+// 128-byte columns with the 128-byte swizzle.
+__device__ __forceinline__ uint32_t swizzled(int rows, int row, int chunk) {
+    return static_cast<uint32_t>((chunk >> 3) * rows * 128 + row * 128 +
+                                 (((chunk & 7) ^ (row & 7)) << 4));
+}
+
+// ------------------------------------------------------------------ the mask of one tile
+
+// Keys of the tile that no row of the unit sees: their V rows are cleared, so that whatever
+// the page holds there (an infinity, a NaN) cannot reach the sum through a weight of 0.
+__device__ __forceinline__ bool key_dead(const Params &p, const Stage &st, int i) {
+    const int key = st.key0 + i;
+    const int p_first = st.len - p.n_tokens, p_last = st.len - 1;
+    return !((st.blocks >> (i >> 3)) & 1u) || key > p_last ||
+           !(p_first - key < p.mask.window || key < p.mask.sinks);
+}
+
+// A row's output from its sums; a row that saw nothing is 0.
+__device__ __forceinline__ float finish(float o, float l, float inv) { return l == 0.0f ? 0.0f : o * inv; }
+
+template <int LANES>
+__device__ __forceinline__ float group_max(float x) {
+#pragma unroll
+    for (int o = LANES / 2; o >= 1; o >>= 1) x = fmaxf(x, __shfl_xor_sync(FULL_MASK, x, o));
+    return x;
+}
+
+template <int LANES>
+__device__ __forceinline__ float group_sum(float x) {
+#pragma unroll
+    for (int o = LANES / 2; o >= 1; o >>= 1) x += __shfl_xor_sync(FULL_MASK, x, o);
+    return x;
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(kThreads, Geometry<T, D, RT>::kCtas)
+attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
+                   const __grid_constant__ CUtensorMap k_map,
+                   const __grid_constant__ CUtensorMap v_map, const Params p) {
+    using G = Geometry<T, D, RT>;
+    constexpr int KT = G::KT;
+    constexpr int kRecord = kRows * (D + 2);  // floats of a partial result: o, then m, then l
+    extern __shared__ uint8_t dyn[];
+    uint8_t *smem =
+        reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+    uint8_t *q_smem = smem + G::kStages * 2 * G::kPlane;
+    uint8_t *extra = q_smem + 2 * G::kQ;
+
+    __shared__ __align__(8) uint64_t full[G::kStages], empty[G::kStages], q_empty[2];
+    __shared__ Stage stages[G::kStages];
+    __shared__ long long slab_sum[kThreads];
+    __shared__ long long sh_total, sh_seq_begin;
+    __shared__ int sh_seq, sh_dead, sh_join;
+    __shared__ float red[kWarps][kRows];
+    __shared__ __align__(16) float row_m[kRows], row_l[kRows];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int subs = p.head_groups * p.token_groups;
+    const int units = p.cache.n_kv_heads * subs;
+
+    if (tid == 0) {
+        for (int s = 0; s < G::kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], kWarps);
+        }
+        mbar_init(&q_empty[0], kWarps);
+        mbar_init(&q_empty[1], kWarps);
+        fence_mbar_init();
+        sh_dead = 0;
+        sh_seq = -1;
+        tma_prefetch_map(&q_map);
+        tma_prefetch_map(&k_map);
+        tma_prefetch_map(&v_map);
+    }
+
+    // Tiles of one unit of sequence n (1 when it sees nothing: its rows are zeros), 0 when
+    // the sequence is skipped.
+    auto tiles_of = [&](int n, int &slot, int &len) -> int {
+        if (!p.cache.lookup(n, slot, len)) return 0;
+        return max(1, walk_tiles<KT>(p.mask, len - p.n_tokens, len - 1).count);
+    };
+
+    // ---- this CTA's range of tiles: sums over slabs of sequences, then their prefixes
+    const int per = (p.n_seqs + kThreads - 1) / kThreads;
+    const int n0 = min(tid * per, p.n_seqs), n1 = min(n0 + per, p.n_seqs);
+    long long sum = 0;
+    for (int n = n0; n < n1; ++n) {
+        int slot, len;
+        const int t = tiles_of(n, slot, len);
+        if (t == 0 && blockIdx.x == 0 && p.err_count) atomicAdd(p.err_count, 1);
+        sum += static_cast<long long>(t) * units;
+    }
+    slab_sum[tid] = sum;
+    __syncthreads();
+    if (warp == 0) {
+        long long run = 0;
+        for (int base = 0; base < kThreads; base += 32) {
+            const long long own = slab_sum[base + lane];
+            long long x = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(FULL_MASK, x, o);
+                if (lane >= o) x += y;
+            }
+            slab_sum[base + lane] = run + x - own;
+            run += __shfl_sync(FULL_MASK, x, 31);
+        }
+        if (lane == 0) sh_total = run;
+    }
+    __syncthreads();
+    const long long total = sh_total;
+    // no range is empty: the CTAs of a split unit are consecutive and all of them arrive
+    const int ranges = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+    if (static_cast<int>(blockIdx.x) >= ranges) return;
+    auto range_begin = [&](int c) { return total * c / ranges; };
+    const long long begin = range_begin(blockIdx.x), end = range_begin(blockIdx.x + 1);
+    if (begin >= slab_sum[tid] && begin < slab_sum[tid] + sum) {
+        long long at = slab_sum[tid];
+        for (int n = n0; n < n1; ++n) {
+            int slot, len;
+            const long long w = static_cast<long long>(tiles_of(n, slot, len)) * units;
+            if (begin < at + w) {
+                sh_seq = n;
+                sh_seq_begin = at;
+                break;
+            }
+            at += w;
+        }
+    }
+    __syncthreads();
+
+    auto k_tile = [&](int s) { return smem + s * 2 * G::kPlane; };
+    auto v_tile = [&](int s) { return smem + s * 2 * G::kPlane + G::kPlane; };
+
+    if (warp == kWarps) {
+        // ---------------------------------------------------------- the loading warp
+        const int ps = 1 << p.cache.log2_ps;
+        const int box = min(ps, KT);  // rows of one load
+        const int n_box = KT / box;   // loads of a tile's 128-byte column, one lane each
+        int n = sh_seq, slot = 0, len = 0;
+        long long seq_begin = sh_seq_begin, at = begin;
+        int tiles = tiles_of(n, slot, len);
+        TileWalk walk = walk_tiles<KT>(p.mask, len - p.n_tokens, len - 1);
+        int it = 0, seg = 0;
+        while (at < end) {
+            const int unit = static_cast<int>((at - seq_begin) / tiles);
+            const long long unit_begin = seq_begin + static_cast<long long>(unit) * tiles;
+            const long long unit_end = unit_begin + tiles;
+            const long long seg_end = unit_end < end ? unit_end : end;
+            const int kvh = unit / subs, sub = unit % subs;
+            const int hg = sub / p.token_groups, tg = sub % p.token_groups;
+            const bool whole = at == unit_begin && seg_end == unit_end;
+            int c0 = 0, c1 = 0;
+            if (!whole) {
+                auto owner = [&](long long x) {
+                    int c = static_cast<int>(x * ranges / total);
+                    while (c + 1 < ranges && range_begin(c + 1) <= x) ++c;
+                    while (c > 0 && range_begin(c) > x) --c;
+                    return c;
+                };
+                c0 = owner(unit_begin);
+                c1 = owner(unit_end - 1);
+            }
+            int i = static_cast<int>(at - unit_begin);
+            // page of this lane's box of tile i, looked up one tile ahead of its load
+            auto page_at = [&](int idx) -> int {
+                if (walk.count == 0 || lane >= n_box) return -1;
+                const int key = walk.tile(idx) * KT + lane * box;
+                const int p_first = len - p.n_tokens;
+                if (key > len - 1) return -1;
+                // pages wholly before the window may be gone already: not looked up
+                if (!(p_first - (key + box - 1) < p.mask.window || key < p.mask.sinks)) return -1;
+                const int page = p.cache.page_of(slot, key);
+                if (p.cache.page_ok(page)) return page;
+                if (p.err_count && unit == 0) atomicAdd(p.err_count, 1);
+                return -1;
+            };
+            int page = page_at(i);
+            for (bool first = true; at < seg_end; ++at, ++i, ++it, first = false) {
+                const int s = it % G::kStages;
+                const int next_page = at + 1 < seg_end ? page_at(i + 1) : -1;
+                if (it >= G::kStages)
+                    wait_or_flag(&empty[s], ((it / G::kStages) - 1) & 1, &sh_dead);
+                if (first && seg >= 2) wait_or_flag(&q_empty[seg & 1], ((seg >> 1) - 1) & 1, &sh_dead);
+                const unsigned have = __ballot_sync(FULL_MASK, page >= 0);
+                const int key0 = walk.count ? walk.tile(i) * KT : 0;
+                if (lane == 0) {
+                    Stage st;
+                    st.seq = n;
+                    st.unit = unit;
+                    st.len = len;
+                    st.key0 = key0;
+                    st.flags = (first ? kFirst : 0) | (at + 1 == seg_end ? kLast : 0) |
+                               (whole ? kWhole : 0) | (unit_begin >= begin ? kHead : 0);
+                    st.blocks = 0;
+                    for (int b = 0; b < KT / 8; ++b)
+                        if ((have >> (b * 8 / box)) & 1u) st.blocks |= 1u << b;
+                    st.c0 = c0;
+                    st.c1 = c1;
+                    stages[s] = st;
+                    const int q_rows = p.heads_per_unit * p.tokens_per_unit;
+                    mbar_arrive_expect_tx(
+                        &full[s], static_cast<uint32_t>(__popc(have) * box) * D * sizeof(T) * 2u +
+                                      (first ? static_cast<uint32_t>(q_rows) * D * sizeof(T) : 0u));
+                    if (first) {
+                        const int head0 = kvh * p.group + hg * p.heads_per_unit;
+                        const int token0 = n * p.n_tokens + tg * p.tokens_per_unit;
+#pragma unroll
+                        for (int cb = 0; cb < G::kCols; ++cb)
+                            tma_load_3d(q_smem + (seg & 1) * G::kQ + cb * G::QR * 128, &q_map,
+                                        cb * static_cast<int>(128 / sizeof(T)), head0, token0,
+                                        &full[s]);
+                    }
+                }
+                __syncwarp();
+                if (page >= 0) {
+                    const int row = (page * p.cache.n_kv_heads + kvh) * ps +
+                                    (ps > KT ? (key0 & (ps - 1)) : 0);
+#pragma unroll
+                    for (int cb = 0; cb < G::kCols; ++cb)
+                        tma_load_2d(k_tile(s) + cb * KT * 128 + lane * box * 128, &k_map,
+                                    cb * static_cast<int>(128 / sizeof(T)), row, &full[s]);
+#pragma unroll
+                    for (int cb = 0; cb < G::kCols; ++cb)
+                        tma_load_2d(v_tile(s) + cb * KT * 128 + lane * box * 128, &v_map,
+                                    cb * static_cast<int>(128 / sizeof(T)), row, &full[s]);
+                }
+                page = next_page;
+            }
+            ++seg;
+            if (at == unit_end && unit == units - 1 && at < end) {
+                seq_begin = unit_end;
+                do {
+                    tiles = tiles_of(++n, slot, len);
+                } while (tiles == 0 && n + 1 < p.n_seqs);
+                if (tiles == 0) break;  // not reached: the range says tiles are left
+                walk = walk_tiles<KT>(p.mask, len - p.n_tokens, len - 1);
+            }
+        }
+        return;
+    }
+
+    // -------------------------------------------------------------- the computing warps
+    const int n_tiles = static_cast<int>(end - begin);
+    // 16-bit: NT tiles of 8 columns (a quarter of the head), rows lane/4 and lane/4 + 8
+    constexpr int NT = D / 32;
+    float o16[G::kF32 ? 1 : NT][4];
+    uint32_t qf[G::kF32 ? 1 : D / 16][4];
+    // fp32: LPR threads to a row in the softmax; in P V a lane holds 4 columns, C4 lanes
+    // span the quarter and NKG groups of lanes split the keys
+    constexpr int LPR = kCompute / RT;
+    constexpr int C4 = D / 16;
+    constexpr int NKG = 32 / C4;
+    float o32[G::kF32 ? RT : 1][4];
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+    int seg = 0;
+
+    for (int it = 0; it < n_tiles; ++it) {
+        const int s = it % G::kStages;
+        wait_or_flag(&full[s], (it / G::kStages) & 1, &sh_dead);
+        const Stage st = stages[s];
+        const int kvh = st.unit / subs, sub = st.unit % subs;
+        const int hg = sub / p.token_groups, tg = sub % p.token_groups;
+        const int p_first = st.len - p.n_tokens, p_last = st.len - 1;
+        const bool clean = st.blocks == (1u << (KT / 8)) - 1u && st.key0 + KT - 1 <= p_first &&
+                           (p_last - st.key0 < p.mask.window || st.key0 + KT <= p.mask.sinks);
+        // position of row r of the unit
+        auto position = [&](int r) { return p_first + tg * p.tokens_per_unit + r / p.heads_per_unit; };
+        auto sees = [&](int r, int i) {
+            return ((st.blocks >> (i >> 3)) & 1u) && p.mask.sees(position(r), st.key0 + i);
+        };
+        if (st.flags & kFirst) {
+            m0 = m1 = -INFINITY;
+            l0 = l1 = 0.0f;
+        }
+        if (!clean) {
+            // this warp's keys of the tile
+            for (int i = warp * (KT / kWarps); i < (warp + 1) * (KT / kWarps); ++i) {
+                if (key_dead(p, st, i))
+                    for (int c = lane; c < G::kCols * 8; c += 32)
+                        *reinterpret_cast<uint4 *>(v_tile(s) + swizzled(KT, i, c)) =
+                            make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();  // before the stage's next copy overwrites them
+        }
+        const uint8_t *q_here = q_smem + (seg & 1) * G::kQ;
+
+        if constexpr (!G::kF32) {
+            const uint32_t ks = smem_addr(k_tile(s)), vs = smem_addr(v_tile(s));
+            if (st.flags & kFirst) {
+                const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    ldsm4(qf[kk], smem_addr(q_here) + swizzled(G::QR, r, 2 * kk + (lane >> 4)));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_empty[seg & 1]);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o16[j][e] = 0.0f;
+            }
+            // S = Q K^T for 16 keys, two chains of products per 8 keys
+            float acc[2][2][4] = {};
+            const int key = warp * 16 + (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                uint32_t b[4];
+                ldsm4(b, ks + swizzled(KT, key, 2 * kk + ((lane >> 3) & 1)));
+                mma16816<T>(acc[kk & 1][0], qf[kk], b[0], b[1]);
+                mma16816<T>(acc[kk & 1][1], qf[kk], b[2], b[3]);
+            }
+            const int r0 = lane >> 2;
+            float sc[2][4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sc[b][e] = (acc[0][b][e] + acc[1][b][e]) * p.scale_log2;
+                    if (!clean && !sees(e < 2 ? r0 : r0 + 8,
+                                        warp * 16 + b * 8 + 2 * (lane & 3) + (e & 1)))
+                        sc[b][e] = -INFINITY;
+                }
+            const float t0 =
+                group_max<4>(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1])));
+            const float t1 =
+                group_max<4>(fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3])));
+            if ((lane & 3) == 0) {
+                red[warp][r0] = t0;
+                red[warp][r0 + 8] = t1;
+            }
+            named_barrier_sync(1, kCompute);
+            const float old0 = m0, old1 = m1;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                m0 = fmaxf(m0, red[w][r0]);
+                m1 = fmaxf(m1, red[w][r0 + 8]);
+            }
+            // a row that has seen nothing yet keeps its weights at 2^-inf = 0
+            const float base0 = m0 == -INFINITY ? 0.0f : m0;
+            const float base1 = m1 == -INFINITY ? 0.0f : m1;
+            const float corr0 = fast_exp2(old0 - base0), corr1 = fast_exp2(old1 - base1);
+            // P is kept in two parts of the cache's type, hi + lo, so that rounding the
+            // weights adds nothing to the output's own rounding; the tensor pipe has room
+            uint8_t *ph = extra, *pl = extra + kRows * (KT + 8) * 2;
+            l0 *= corr0;
+            l1 *= corr1;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const float x0 = fast_exp2(sc[b][0] - base0), x1 = fast_exp2(sc[b][1] - base0);
+                const float y0 = fast_exp2(sc[b][2] - base1), y1 = fast_exp2(sc[b][3] - base1);
+                l0 += x0 + x1;
+                l1 += y0 + y1;
+                const int col = warp * 16 + b * 8 + 2 * (lane & 3);
+                const uint32_t oa = static_cast<uint32_t>(r0 * (KT + 8) + col) * 2u;
+                const uint32_t ob = oa + 8 * (KT + 8) * 2u;
+                const uint32_t xh = Elem<T>::pack(x0, x1), yh = Elem<T>::pack(y0, y1);
+                const float2 xf = Elem<T>::unpack(xh), yf = Elem<T>::unpack(yh);
+                *reinterpret_cast<uint32_t *>(ph + oa) = xh;
+                *reinterpret_cast<uint32_t *>(ph + ob) = yh;
+                *reinterpret_cast<uint32_t *>(pl + oa) = Elem<T>::pack(x0 - xf.x, x1 - xf.y);
+                *reinterpret_cast<uint32_t *>(pl + ob) = Elem<T>::pack(y0 - yf.x, y1 - yf.y);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                o16[j][0] *= corr0;
+                o16[j][1] *= corr0;
+                o16[j][2] *= corr1;
+                o16[j][3] *= corr1;
+            }
+            named_barrier_sync(2, kCompute);
+            const uint32_t poff = static_cast<uint32_t>(
+                ((lane & 7) + ((lane >> 3) & 1) * 8) * (KT + 8) + (lane >> 4) * 8) * 2u;
+#pragma unroll
+            for (int kk = 0; kk < KT / 16; ++kk) {
+                uint32_t ah[4], al[4];
+                ldsm4(ah, smem_addr(ph) + poff + kk * 32);
+                ldsm4(al, smem_addr(pl) + poff + kk * 32);
+                const int vrow = kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+                for (int j = 0; j < NT; j += 2) {
+                    uint32_t b[4];
+                    ldsm4_trans(b, vs + swizzled(KT, vrow, warp * NT + j + (lane >> 4)));
+                    mma16816<T>(o16[j], ah, b[0], b[1]);
+                    mma16816<T>(o16[j + 1], ah, b[2], b[3]);
+                    mma16816<T>(o16[j], al, b[0], b[1]);
+                    mma16816<T>(o16[j + 1], al, b[2], b[3]);
+                }
+            }
+        } else {
+            // fp32: the products on the FP32 pipes, every operand read once per warp
+            // S, then P: [KT][RT]. Two buffers in turn: a warp may start on the next tile's
+            // S while another still reads this tile's P
+            float *sp = reinterpret_cast<float *>(extra) + (it & 1) * KT * RT;
+            if (st.flags & kFirst) {
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o32[r][e] = 0.0f;
+            }
+            {
+                // lane: one key of the warp's 8 and a quarter of the dot product
+                const int i = warp * 8 + (lane & 7), quarter = lane >> 3;
+                // the quarters' lanes start at chunks in different banks
+                const int turn = D >= 128 ? 2 * quarter : quarter >> 1;
+                float acc[RT];
+#pragma unroll
+                for (int r = 0; r < RT; ++r) acc[r] = 0.0f;
+#pragma unroll 4
+                for (int c = 0; c < D / 16; ++c) {
+                    const int chunk = quarter * (D / 16) + (c ^ turn);
+                    const float4 kv =
+                        *reinterpret_cast<const float4 *>(k_tile(s) + swizzled(KT, i, chunk));
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        const float4 qv =
+                            *reinterpret_cast<const float4 *>(q_here + swizzled(G::QR, r, chunk));
+                        acc[r] = fmaf(qv.x, kv.x, acc[r]);
+                        acc[r] = fmaf(qv.y, kv.y, acc[r]);
+                        acc[r] = fmaf(qv.z, kv.z, acc[r]);
+                        acc[r] = fmaf(qv.w, kv.w, acc[r]);
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    acc[r] += __shfl_xor_sync(FULL_MASK, acc[r], 8);
+                    acc[r] += __shfl_xor_sync(FULL_MASK, acc[r], 16);
+                    if ((r & 3) == quarter)
+                        sp[i * RT + r] = clean || sees(r, i) ? acc[r] * p.scale_log2 : -INFINITY;
+                }
+            }
+            named_barrier_sync(1, kCompute);
+            {
+                const int r = tid / LPR, part = tid % LPR;
+                float x[KT / LPR];
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < KT / LPR; ++i) {
+                    x[i] = sp[(part + i * LPR) * RT + r];
+                    top = fmaxf(top, x[i]);
+                }
+                const float old = m0;
+                m0 = fmaxf(m0, group_max<LPR>(top));
+                const float base = m0 == -INFINITY ? 0.0f : m0;
+                const float corr = fast_exp2(old - base);
+                l0 *= corr;
+#pragma unroll
+                for (int i = 0; i < KT / LPR; ++i) {
+                    x[i] = fast_exp2(x[i] - base);
+                    l0 += x[i];
+                    sp[(part + i * LPR) * RT + r] = x[i];
+                }
+                if (part == 0) row_m[r] = corr;
+            }
+            named_barrier_sync(2, kCompute);
+            {
+                const int c4 = lane % C4, kg = lane / C4;
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const float corr = row_m[r];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o32[r][e] *= corr;
+                }
+#pragma unroll 2
+                for (int j = 0; j < KT / NKG; ++j) {
+                    // for D = 64 two keys share a quarter-warp's read: 4 apart, so that
+                    // the swizzle keeps them in different banks
+                    const int i = NKG == 8 ? (kg >> 1) + 4 * (kg & 1) + 8 * j : kg + NKG * j;
+                    const float4 vv = *reinterpret_cast<const float4 *>(
+                        v_tile(s) + swizzled(KT, i, warp * C4 + c4));
+#pragma unroll
+                    for (int r = 0; r < RT; r += 4) {
+                        const float4 w = *reinterpret_cast<const float4 *>(sp + i * RT + r);
+                        const float ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) {
+                            o32[r + a][0] = fmaf(ws[a], vv.x, o32[r + a][0]);
+                            o32[r + a][1] = fmaf(ws[a], vv.y, o32[r + a][1]);
+                            o32[r + a][2] = fmaf(ws[a], vv.z, o32[r + a][2]);
+                            o32[r + a][3] = fmaf(ws[a], vv.w, o32[r + a][3]);
+                        }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+        if (!(st.flags & kLast)) continue;
+
+        // ---------------------------------------------------------- the segment's end
+        if constexpr (G::kF32) {
+            if (lane == 0) mbar_arrive(&q_empty[seg & 1]);
+        }
+        ++seg;
+        named_barrier_sync(1, kCompute);  // the last tile's corrections have been read
+        if constexpr (!G::kF32) {
+            const float a = group_sum<4>(l0), b = group_sum<4>(l1);
+            if ((lane & 3) == 0) {
+                red[warp][lane >> 2] = a;
+                red[warp][(lane >> 2) + 8] = b;
+                if (warp == 0) {
+                    row_m[lane >> 2] = m0;
+                    row_m[(lane >> 2) + 8] = m1;
+                }
+            }
+            named_barrier_sync(2, kCompute);
+            if (tid < kRows) row_l[tid] = (red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid]);
+        } else {
+            const float a = group_sum<LPR>(l0);
+            if (tid % LPR == 0) {
+                row_m[tid / LPR] = m0;
+                row_l[tid / LPR] = a;
+            }
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int o = C4; o < 32; o <<= 1)
+                        o32[r][e] += __shfl_xor_sync(FULL_MASK, o32[r][e], o);
+        }
+        named_barrier_sync(1, kCompute);
+
+        const int heads = min(p.heads_per_unit, p.group - hg * p.heads_per_unit);
+        const int tokens = min(p.tokens_per_unit, p.n_tokens - tg * p.tokens_per_unit);
+        // output row of row r of the unit, or -1 for a row it has not
+        auto out_row = [&](int r) -> long long {
+            const int t = r / p.heads_per_unit, h = r % p.heads_per_unit;
+            if (t >= tokens || h >= heads) return -1;
+            return (static_cast<long long>(st.seq) * p.n_tokens + tg * p.tokens_per_unit + t) *
+                       p.n_q_heads + kvh * p.group + hg * p.heads_per_unit + h;
+        };
+        T *out = static_cast<T *>(p.out);
+        const bool whole = st.flags & kWhole;
+        float *record = p.partials +
+                        static_cast<size_t>(2 * blockIdx.x + ((st.flags & kHead) ? 1 : 0)) * kRecord;
+        if constexpr (!G::kF32) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int r = (lane >> 2) + 8 * half;
+                const long long row = out_row(r);
+                if (row < 0) continue;
+                const float l = row_l[r], inv = 1.0f / l;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const int col = (warp * NT + j) * 8 + 2 * (lane & 3);
+                    const float x = o16[j][2 * half], y = o16[j][2 * half + 1];
+                    if (whole) {
+                        if (!sh_dead)
+                            *reinterpret_cast<uint32_t *>(out + row * D + col) =
+                                Elem<T>::pack(finish(x, l, inv), finish(y, l, inv));
+                    } else {
+                        __stcg(reinterpret_cast<float2 *>(record + r * D + col), make_float2(x, y));
+                    }
+                }
+            }
+        } else {
+            if (lane / C4 == 0) {
+                const int col = (warp * C4 + lane) * 4;
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const long long row = out_row(r);
+                    if (row < 0) continue;
+                    if (whole) {
+                        const float l = row_l[r], inv = 1.0f / l;
+                        if (!sh_dead)
+                            *reinterpret_cast<float4 *>(out + row * D + col) =
+                                make_float4(finish(o32[r][0], l, inv), finish(o32[r][1], l, inv),
+                                            finish(o32[r][2], l, inv), finish(o32[r][3], l, inv));
+                    } else {
+                        __stcg(reinterpret_cast<float4 *>(record + r * D + col),
+                               make_float4(o32[r][0], o32[r][1], o32[r][2], o32[r][3]));
+                    }
+                }
+            }
+        }
+        if (whole) continue;
+
+        // ---------------------------------------------------------- the join
+        if (tid < kRows) {
+            __stcg(record + kRows * D + tid, row_m[tid]);
+            // a length below zero marks a result that a wait gave up on
+            __stcg(record + kRows * D + kRows + tid, sh_dead ? -1.0f : row_l[tid]);
+        }
+        __threadfence();
+        named_barrier_sync(2, kCompute);
+        if (tid == 0) {
+            sh_join = last_arrival(p.counters + st.c0, p.nonce, st.c1 - st.c0 + 1);
+            __threadfence();
+        }
+        named_barrier_sync(1, kCompute);
+        if (!sh_join) continue;
+        auto record_of = [&](int c) {
+            // the first CTA holds the unit in its second record: it begins in its range
+            return p.partials + static_cast<size_t>(2 * c + (c == st.c0 ? 1 : 0)) * kRecord;
+        };
+        for (int x = tid; x < kRows * (D / 4); x += kCompute) {
+            const int r = x / (D / 4), col = (x % (D / 4)) * 4;
+            const long long row = out_row(r);
+            if (row < 0) continue;
+            float top = -INFINITY;
+            bool dead = false;
+#pragma unroll 4
+            for (int c = st.c0; c <= st.c1; ++c) {
+                top = fmaxf(top, __ldcg(record_of(c) + kRows * D + r));
+                dead |= __ldcg(record_of(c) + kRows * D + kRows + r) < 0.0f;
+            }
+            const float base = top == -INFINITY ? 0.0f : top;
+            float l = 0.0f;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int c = st.c0; c <= st.c1; ++c) {
+                const float w = fast_exp2(__ldcg(record_of(c) + kRows * D + r) - base);
+                const float4 a = __ldcg(reinterpret_cast<const float4 *>(record_of(c) + r * D + col));
+                l = fmaf(w, __ldcg(record_of(c) + kRows * D + kRows + r), l);
+                o.x = fmaf(w, a.x, o.x);
+                o.y = fmaf(w, a.y, o.y);
+                o.z = fmaf(w, a.z, o.z);
+                o.w = fmaf(w, a.w, o.w);
+            }
+            if (dead) continue;
+            const float inv = 1.0f / l;
+            o = make_float4(finish(o.x, l, inv), finish(o.y, l, inv), finish(o.z, l, inv),
+                            finish(o.w, l, inv));
+            if constexpr (G::kF32) {
+                *reinterpret_cast<float4 *>(out + row * D + col) = o;
+            } else {
+                *reinterpret_cast<uint2 *>(out + row * D + col) =
+                    make_uint2(Elem<T>::pack(o.x, o.y), Elem<T>::pack(o.z, o.w));
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+// Rows of a unit: all query heads of a key head (groups of 16 when there are more), and as
+// many draft tokens as fit beside them.
+struct Split {
+    int heads, tokens, head_groups, token_groups;
+};
+
+Split split_rows(int n_tokens, int group) {
+    Split s;
+    s.heads = group < kRows ? group : kRows;
+    s.tokens = kRows / s.heads < n_tokens ? kRows / s.heads : n_tokens;
+    s.head_groups = (group + s.heads - 1) / s.heads;
+    s.token_groups = (n_tokens + s.tokens - 1) / s.tokens;
+    return s;
+}
+
+constexpr size_t kCounterBytes = kMaxCtas * sizeof(unsigned long long);
+
+size_t workspace_bytes_for(int head_dim) {
+    return kCounterBytes + static_cast<size_t>(kMaxCtas) * 2 * kRows * (head_dim + 2) * sizeof(float);
+}
+
+// A value of its own for every call (48 bits, never 0).
+unsigned long long next_nonce() {
+    static std::atomic<unsigned long long> calls{0};
+    static const unsigned long long seed = [] {
+        timespec t{};
+        clock_gettime(CLOCK_REALTIME, &t);
+        return static_cast<unsigned long long>(t.tv_sec) * 1000000000ull + t.tv_nsec;
+    }();
+    unsigned long long z = seed + 0x9E3779B97F4A7C15ull * (calls.fetch_add(1) + 1);
+    z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;  // splitmix64
+    z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+    return ((z ^ (z >> 31)) >> 16) | 1ull;
+}
+
+template <typename T, int D, int RT>
+gdn_status launch(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, const Params &p,
+                  cudaStream_t s) {
+    using G = Geometry<T, D, RT>;
+    auto kernel = attn_decode_kernel<T, D, RT>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem) !=
+        cudaSuccess)
+        return GDN_ERR_LAUNCH;
+    kernel<<<kSMs * G::kCtas, kThreads, G::kSmem, s>>>(q, k, v, p);
+    return launch_status();
+}
+
+template <typename T, int D>
+gdn_status launch_rows(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                       const Params &p, cudaStream_t s) {
+    if constexpr (sizeof(T) == 4) {
+        const int rows = p.heads_per_unit * p.tokens_per_unit;
+        if (rows <= 4) return launch<T, D, 4>(q, k, v, p, s);
+        if (rows <= 8) return launch<T, D, 8>(q, k, v, p, s);
+    }
+    return launch<T, D, 16>(q, k, v, p, s);
+}
+
+template <typename T>
+gdn_status launch_dim(int d, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                      const Params &p, cudaStream_t s) {
+    switch (d) {
+        case 64: return launch_rows<T, 64>(q, k, v, p, s);
+        case 128: return launch_rows<T, 128>(q, k, v, p, s);
+        default: return launch_rows<T, 256>(q, k, v, p, s);
+    }
+}
+
+}  // namespace
+
+unsigned read_and_clear_watchdog_attn_decode(cudaStream_t s) {
+    unsigned flags = 0;
+    const unsigned zero = 0;
+    cudaMemcpyFromSymbolAsync(&flags, g_watchdog_attn_decode, sizeof(flags), 0,
+                              cudaMemcpyDeviceToHost, s);
+    cudaMemcpyToSymbolAsync(g_watchdog_attn_decode, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
+    cudaStreamSynchronize(s);
+    return flags;
+}
+
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+size_t gdn_attn_decode_workspace_size(int n_seqs, int n_tokens, int n_q_heads, int n_kv_heads,
+                                      int head_dim) {
+    if (n_seqs < 0 || n_tokens < 1 || n_kv_heads < 1 || n_q_heads < 1 ||
+        n_q_heads % n_kv_heads != 0 || !supported_head_dim(head_dim))
+        return 0;
+    return workspace_bytes_for(head_dim);
+}
+
+gdn_status gdn_attn_decode(const void *q, const void *k_pages, const void *v_pages,
+                           const int32_t *page_table, const int32_t *kv_lens, void *out,
+                           int n_seqs, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim,
+                           int page_size, int n_pages, int max_pages, int window, int n_sinks,
+                           float scale, int q_stride, int dtype, const int32_t *slots, int pool,
+                           int32_t *err_count, void *workspace, size_t workspace_bytes,
+                           gdn_stream_t stream) {
+    if (!q || !k_pages || !v_pages || !page_table || !kv_lens || !out) return GDN_ERR_NULL;
+    if (n_seqs < 0 || n_tokens < 1 || n_q_heads < 1 || window < 0 || n_sinks < 0) return GDN_ERR_SHAPE;
+    GDN_TRY(check_cache(n_kv_heads, head_dim, page_size, n_pages, max_pages, dtype));
+    if (n_q_heads % n_kv_heads != 0) return GDN_ERR_SHAPE;
+    if (static_cast<long long>(n_q_heads) * head_dim > q_stride) return GDN_ERR_SHAPE;
+    if (n_tokens > 64 || static_cast<long long>(n_seqs) * n_tokens > 0x7fffffffLL)
+        return GDN_ERR_UNSUPPORTED;
+    GDN_TRY(check_pool(n_seqs, slots, pool));
+    const int es = dtype_bytes(dtype);
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) ||
+        (static_cast<long long>(q_stride) * es) % 16 != 0)
+        return GDN_ERR_ALIGN;
+    if (n_seqs == 0) return GDN_OK;
+    if (!workspace) return GDN_ERR_NULL;
+    if (!aligned16(workspace)) return GDN_ERR_ALIGN;
+    if (workspace_bytes < workspace_bytes_for(head_dim)) return GDN_ERR_SHAPE;
+
+    const int group = n_q_heads / n_kv_heads;
+    const Split sp = split_rows(n_tokens, group);
+    Params p{};
+    p.cache = PagedCache{page_table, kv_lens, slots, pool, max_pages, n_pages, n_kv_heads,
+                         log2_of(page_size)};
+    p.mask = make_mask(window, n_sinks);
+    p.out = out;
+    p.n_seqs = n_seqs;
+    p.n_tokens = n_tokens;
+    p.n_q_heads = n_q_heads;
+    p.group = group;
+    p.heads_per_unit = sp.heads;
+    p.tokens_per_unit = sp.tokens;
+    p.head_groups = sp.head_groups;
+    p.token_groups = sp.token_groups;
+    p.scale_log2 = scale * kLog2E;
+    p.err_count = err_count;
+    p.counters = static_cast<unsigned long long *>(workspace);
+    p.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + kCounterBytes);
+    p.nonce = next_nonce();
+
+    CUtensorMap q_map, k_map, v_map;
+    const uint64_t rows = static_cast<uint64_t>(n_pages) * n_kv_heads * page_size;
+    const int kt = dtype == GDN_F32 ? 32 : 64;
+    const int box = page_size < kt ? page_size : kt;
+    GDN_TRY(encode_heads_map(&q_map, q, dtype, head_dim, n_q_heads,
+                             static_cast<uint64_t>(n_seqs) * n_tokens,
+                             static_cast<uint64_t>(q_stride) * es, sp.heads, sp.tokens));
+    GDN_TRY(encode_rows_map(&k_map, k_pages, dtype, head_dim, rows,
+                            static_cast<uint64_t>(head_dim) * es, box));
+    GDN_TRY(encode_rows_map(&v_map, v_pages, dtype, head_dim, rows,
+                            static_cast<uint64_t>(head_dim) * es, box));
+    const cudaStream_t s = as_cuda(stream);
+    switch (dtype) {
+        case GDN_F32: return launch_dim<float>(head_dim, q_map, k_map, v_map, p, s);
+        case GDN_F16: return launch_dim<__half>(head_dim, q_map, k_map, v_map, p, s);
+        default: return launch_dim<__nv_bfloat16>(head_dim, q_map, k_map, v_map, p, s);
+    }
+}
+
+}  // extern "C"

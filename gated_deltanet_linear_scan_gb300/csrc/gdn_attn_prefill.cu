@@ -1,0 +1,341 @@
+// gdn_attn_prefill.cu -- attention of a ragged batch of prompts, or chunks of prompts, over
+// the paged key/value cache (sm_103a).
+//
+//   o_i = sum_j w_ij v_j / sum_j w_ij,  w_ij = e^{scale q_i.k_j - m_i} over the keys i sees
+//
+// All query heads of a key head share its keys, so a tile of rows is (tokens x heads of one
+// key head): the keys are read once for all of them, and a tile spans few positions, which
+// keeps the work wasted at the causal diagonal and at the window's edge small.
+#include "gdn_paged.cuh"
+
+namespace gdn {
+namespace {
+
+__device__ unsigned g_watchdog_attn_prefill;
+
+struct PrefillParams {
+    PagedCache cache;
+    AttnMask mask;
+    SeqMap seqs;
+    const void *q, *k_pages, *v_pages;
+    void *out;
+    int n_seqs, n_q_heads, group, q_stride;
+    int heads_per_tile, tokens_per_tile, head_groups;
+    float scale_log2;
+    int32_t *err_count;
+};
+
+// The rows of one CTA: tokens token0 .. of sequence n, heads head0 .. .
+struct RowTile {
+    int slot, len;        // of the sequence, in the cache
+    int new_tokens;       // of the sequence in this call
+    size_t row0;          // packed row of the sequence's first new token
+    int token0, tokens;   // of this tile
+    int kvh, head0, heads;
+    int p_first, p_last;  // positions of the tile's first and last token
+};
+
+// Finds the tile of this CTA (blockIdx.x: a tile slot, blockIdx.y: key head and head group);
+// false when it has none. Called by whole warps. Also counts the skipped sequences once.
+__device__ __forceinline__ bool find_tile(const PrefillParams &p, RowTile &t) {
+    const int x = blockIdx.x;
+    if (blockIdx.y == 0 && x < p.n_seqs && threadIdx.x == 0 && p.err_count) {
+        size_t r0;
+        int m, slot, len;
+        if (!p.seqs.range(x, r0, m) || !p.cache.lookup(x, slot, len)) atomicAdd(p.err_count, 1);
+    }
+    const int n = warp_seq_of_slot(p.seqs.cu, p.n_seqs, p.tokens_per_tile, x);
+    if (n < 0 || !p.seqs.range(n, t.row0, t.new_tokens) || !p.cache.lookup(n, t.slot, t.len))
+        return false;
+    const int block = x - (static_cast<int>(t.row0) / p.tokens_per_tile + n);
+    t.token0 = block * p.tokens_per_tile;
+    if (t.token0 >= t.new_tokens) return false;
+    t.tokens = min(p.tokens_per_tile, t.new_tokens - t.token0);
+    t.kvh = blockIdx.y / p.head_groups;
+    const int hg = blockIdx.y % p.head_groups;
+    t.head0 = t.kvh * p.group + hg * p.heads_per_tile;
+    t.heads = min(p.heads_per_tile, p.group - hg * p.heads_per_tile);
+    t.p_first = t.len - t.new_tokens + t.token0;
+    t.p_last = t.p_first + t.tokens - 1;
+    return true;
+}
+
+// ------------------------------------------------------------------ on the FP32 pipes
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T *p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float *p) {
+    return *reinterpret_cast<const float4 *>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4<__half>(const __half *p) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    const float2 a = Elem<__half>::unpack(v.x), b = Elem<__half>::unpack(v.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    const float2 a = Elem<__nv_bfloat16>::unpack(v.x), b = Elem<__nv_bfloat16>::unpack(v.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+template <typename T>
+__device__ __forceinline__ void store4(T *p, float4 v) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(Elem<T>::pack(v.x, v.y), Elem<T>::pack(v.z, v.w));
+}
+
+constexpr int kSimtThreads = 128;
+constexpr int kSimtRows = 64;
+constexpr int kSimtKeys = 32;
+
+template <int D>
+constexpr int simt_smem() {
+    return ((kSimtRows + 2 * kSimtKeys) * (D + 4) + kSimtRows * (kSimtKeys + 4)) * 4;
+}
+
+// 64 rows by 32 keys a step, everything in fp32: a thread holds 4 rows x 4 keys of S (8
+// lanes span the keys) and 4 rows x D/8 columns of O. Rows of shared memory are padded by 16
+// bytes, so the 8 lanes of a quarter-warp read different banks.
+template <typename T, int D>
+__global__ void __launch_bounds__(kSimtThreads)
+attn_prefill_simt_kernel(const PrefillParams p) {
+    constexpr int P = D + 4, PP = kSimtKeys + 4;
+    extern __shared__ __align__(16) float sm[];
+    float *sq = sm, *sk = sq + kSimtRows * P, *sv = sk + kSimtKeys * P, *sp = sv + kSimtKeys * P;
+    RowTile t;
+    if (!find_tile(p, t)) return;
+    const int tid = threadIdx.x, tx = tid & 7, ty = tid >> 3;
+    const T *q = static_cast<const T *>(p.q);
+    const T *k_pages = static_cast<const T *>(p.k_pages), *v_pages = static_cast<const T *>(p.v_pages);
+    const int ps = 1 << p.cache.log2_ps;
+
+    for (int x = tid; x < kSimtRows * (D / 4); x += kSimtThreads) {
+        const int r = x / (D / 4), c = (x % (D / 4)) * 4;
+        const int tok = r / p.heads_per_tile, h = r % p.heads_per_tile;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (tok < t.tokens && h < t.heads)
+            v = load4(q + (t.row0 + t.token0 + tok) * p.q_stride + static_cast<size_t>(t.head0 + h) * D + c);
+        *reinterpret_cast<float4 *>(sq + r * P + c) = v;
+    }
+    float o[4][D / 8], m[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) o[i][c] = 0.0f;
+    }
+    const TileWalk walk = walk_tiles<kSimtKeys>(p.mask, t.p_first, t.p_last);
+    for (int w = 0; w < walk.count; ++w) {
+        const int key0 = walk.tile(w) * kSimtKeys;
+        __syncthreads();  // the previous tile has been read
+        for (int x = tid; x < kSimtKeys * (D / 4); x += kSimtThreads) {
+            const int i = x / (D / 4), c = (x % (D / 4)) * 4, key = key0 + i;
+            float4 kv = make_float4(0.0f, 0.0f, 0.0f, 0.0f), vv = kv;
+            // keys no row of the tile sees are not looked up: their pages may be gone, and
+            // whatever a page holds past the length must not reach the sums
+            if (key <= t.p_last && (t.p_first - key < p.mask.window || key < p.mask.sinks)) {
+                const int page = p.cache.page_of(t.slot, key);
+                if (p.cache.page_ok(page)) {
+                    const size_t at =
+                        ((static_cast<size_t>(page) * p.cache.n_kv_heads + t.kvh) * ps + (key & (ps - 1))) * D + c;
+                    kv = load4(k_pages + at);
+                    vv = load4(v_pages + at);
+                } else if (c == 0 && blockIdx.y == 0 && p.err_count && (key & (ps - 1)) == 0) {
+                    atomicAdd(p.err_count, 1);
+                }
+            }
+            *reinterpret_cast<float4 *>(sk + i * P + c) = kv;
+            *reinterpret_cast<float4 *>(sv + i * P + c) = vv;
+        }
+        __syncthreads();
+        float s[4][4] = {};
+#pragma unroll 4
+        for (int c = 0; c < D; c += 4) {
+            float4 a[4], b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4 *>(sq + (ty * 4 + i) * P + c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4 *>(sk + (tx + 8 * j) * P + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
+                    s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
+                    s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
+                    s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int pos = t.p_first + (ty * 4 + i) / p.heads_per_tile;
+            float top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = key0 + tx + 8 * j;
+                bool ok = p.mask.sees(pos, key) && key <= t.p_last;
+                if (ok) ok = p.cache.page_ok(p.cache.page_of(t.slot, key));
+                s[i][j] = ok ? s[i][j] * p.scale_log2 : -INFINITY;
+                top = fmaxf(top, s[i][j]);
+            }
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, d));
+            const float old = m[i];
+            m[i] = fmaxf(m[i], top);
+            const float base = m[i] == -INFINITY ? 0.0f : m[i];
+            const float corr = fast_exp2(old - base);
+            l[i] *= corr;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float w_ = fast_exp2(s[i][j] - base);
+                l[i] += w_;
+                sp[(ty * 4 + i) * PP + tx + 8 * j] = w_;
+            }
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) o[i][c] *= corr;
+        }
+        __syncwarp();  // P's rows are read by the warp that wrote them
+#pragma unroll 2
+        for (int j = 0; j < kSimtKeys; j += 4) {
+            float4 w4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w4[i] = *reinterpret_cast<const float4 *>(sp + (ty * 4 + i) * PP + j);
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    const float4 v = *reinterpret_cast<const float4 *>(sv + (j + jj) * P + tx * 4 + 32 * c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float wi = jj == 0 ? w4[i].x : jj == 1 ? w4[i].y : jj == 2 ? w4[i].z : w4[i].w;
+                        o[i][4 * c] = fmaf(wi, v.x, o[i][4 * c]);
+                        o[i][4 * c + 1] = fmaf(wi, v.y, o[i][4 * c + 1]);
+                        o[i][4 * c + 2] = fmaf(wi, v.z, o[i][4 * c + 2]);
+                        o[i][4 * c + 3] = fmaf(wi, v.w, o[i][4 * c + 3]);
+                    }
+                }
+            }
+        }
+    }
+    T *out = static_cast<T *>(p.out);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = ty * 4 + i, tok = r / p.heads_per_tile, h = r % p.heads_per_tile;
+        float sum = l[i];
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(FULL_MASK, sum, d);
+        if (tok >= t.tokens || h >= t.heads) continue;
+        const float inv = 1.0f / sum;
+        T *row = out + ((t.row0 + t.token0 + tok) * p.n_q_heads + t.head0 + h) * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (sum != 0.0f)
+                v = make_float4(o[i][4 * c] * inv, o[i][4 * c + 1] * inv, o[i][4 * c + 2] * inv,
+                                o[i][4 * c + 3] * inv);
+            store4(row + tx * 4 + 32 * c, v);
+        }
+    }
+}
+
+template <typename T, int D>
+gdn_status launch_simt(PrefillParams p, cudaStream_t s) {
+    p.heads_per_tile = p.group < kSimtRows ? p.group : kSimtRows;
+    p.head_groups = (p.group + p.heads_per_tile - 1) / p.heads_per_tile;
+    p.tokens_per_tile = kSimtRows / p.heads_per_tile;
+    const long long tiles = p.seqs.total / p.tokens_per_tile + p.n_seqs;
+    const long long ys = static_cast<long long>(p.cache.n_kv_heads) * p.head_groups;
+    if (tiles > 0x7fffffffLL || ys > 65535) return GDN_ERR_UNSUPPORTED;
+    auto kernel = attn_prefill_simt_kernel<T, D>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, simt_smem<D>()) !=
+        cudaSuccess)
+        return GDN_ERR_LAUNCH;
+    kernel<<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(ys)), kSimtThreads,
+             simt_smem<D>(), s>>>(p);
+    return launch_status();
+}
+
+template <typename T>
+gdn_status launch_simt_dim(int d, const PrefillParams &p, cudaStream_t s) {
+    switch (d) {
+        case 64: return launch_simt<T, 64>(p, s);
+        case 128: return launch_simt<T, 128>(p, s);
+        default: return launch_simt<T, 256>(p, s);
+    }
+}
+
+}  // namespace
+
+unsigned read_and_clear_watchdog_attn_prefill(cudaStream_t s) {
+    unsigned flags = 0;
+    const unsigned zero = 0;
+    cudaMemcpyFromSymbolAsync(&flags, g_watchdog_attn_prefill, sizeof(flags), 0,
+                              cudaMemcpyDeviceToHost, s);
+    cudaMemcpyToSymbolAsync(g_watchdog_attn_prefill, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
+    cudaStreamSynchronize(s);
+    return flags;
+}
+
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+size_t gdn_attn_prefill_workspace_size(int n_seqs, int total_tokens, int n_q_heads, int n_kv_heads,
+                                       int head_dim) {
+    if (n_seqs < 0 || total_tokens < 0 || n_kv_heads < 1 || n_q_heads < 1 ||
+        n_q_heads % n_kv_heads != 0 || !supported_head_dim(head_dim))
+        return 0;
+    return 0;
+}
+
+gdn_status gdn_attn_prefill(const void *q, const void *k_pages, const void *v_pages,
+                            const int32_t *page_table, const int32_t *kv_lens, void *out,
+                            const int32_t *cu_seqlens, int n_seqs, int total_tokens,
+                            int max_tokens, int n_q_heads, int n_kv_heads, int head_dim,
+                            int page_size, int n_pages, int max_pages, int window, int n_sinks,
+                            float scale, int q_stride, int dtype, const int32_t *slots, int pool,
+                            int32_t *err_count, void *workspace, size_t workspace_bytes,
+                            gdn_stream_t stream) {
+    (void)workspace;
+    (void)workspace_bytes;
+    if (!q || !k_pages || !v_pages || !page_table || !kv_lens || !out) return GDN_ERR_NULL;
+    GDN_TRY(check_varlen(cu_seqlens, n_seqs, total_tokens, max_tokens));
+    if (n_q_heads < 1 || window < 0 || n_sinks < 0) return GDN_ERR_SHAPE;
+    GDN_TRY(check_cache(n_kv_heads, head_dim, page_size, n_pages, max_pages, dtype));
+    if (n_q_heads % n_kv_heads != 0) return GDN_ERR_SHAPE;
+    if (static_cast<long long>(n_q_heads) * head_dim > q_stride) return GDN_ERR_SHAPE;
+    GDN_TRY(check_pool(n_seqs, slots, pool));
+    const long long es = dtype_bytes(dtype);
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) ||
+        q_stride * es % 16 != 0)
+        return GDN_ERR_ALIGN;
+    if (n_seqs == 0 || total_tokens == 0) return GDN_OK;
+    PrefillParams p{};
+    p.cache = PagedCache{page_table, kv_lens, slots, pool, max_pages, n_pages, n_kv_heads,
+                         log2_of(page_size)};
+    p.mask = make_mask(window, n_sinks);
+    p.seqs = SeqMap{cu_seqlens, max_tokens, total_tokens};
+    p.q = q;
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.out = out;
+    p.n_seqs = n_seqs;
+    p.n_q_heads = n_q_heads;
+    p.group = n_q_heads / n_kv_heads;
+    p.q_stride = q_stride;
+    p.scale_log2 = scale * kLog2E;
+    p.err_count = err_count;
+    const cudaStream_t s = as_cuda(stream);
+    switch (dtype) {
+        case GDN_F32: return launch_simt_dim<float>(head_dim, p, s);
+        case GDN_F16: return launch_simt_dim<__half>(head_dim, p, s);
+        default: return launch_simt_dim<__nv_bfloat16>(head_dim, p, s);
+    }
+}
+
+}  // extern "C"

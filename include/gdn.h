@@ -87,7 +87,8 @@ int gdn_version(void);
 gdn_status gdn_device_error(gdn_stream_t stream);
 
 /* Self-test of the failure path above, for a caller's health check or a test suite.
- * Enqueues four one-thread kernels, one on each watchdog flag gdn_device_error() reads;
+ * Enqueues four one-thread kernels, one on each of the SSM block's watchdog flags that
+ * gdn_device_error() reads;
  * probe i (bit i of arm_mask set) waits, bounded by limit_us microseconds, for bytes
  * that no copy will bring -- the wait runs out, the probe raises its flag and skips its
  * guarded write, as a kernel whose copy never lands does. A probe whose bit is clear
@@ -586,6 +587,146 @@ gdn_status gdn_block_prefill_noalloc(const float *qkv, const float *conv_w, floa
                                      int conv_kernel, float scale, float l2_eps, float norm_eps,
                                      const int32_t *slots, int pool, int32_t *err_count,
                                      gdn_stream_t stream);
+
+/* ---------------------------------------------------------------- attention layers
+ * The attention layers of a hybrid model, beside its Gated-DeltaNet blocks: a paged
+ * key/value cache, attention of new tokens over it, and the bookkeeping of its pages.
+ * The pages have no counterpart; these calls share the conventions above (device
+ * pointers owned by the caller, an explicit stream, host validation, no allocation,
+ * slots / pool / err_count).
+ * - Types: dtype names the type of q, k, v, out and the pages of a call (a gdn_dtype).
+ *   Scores, softmax statistics and sums are fp32; out is rounded once.
+ * - Heads: query head h reads key head h / (n_q_heads / n_kv_heads) (consecutive query
+ *   heads share a key head; the recurrence's v-heads are tiled, vh % Hk, instead).
+ *   head_dim in {64, 128, 256}. Any head ratio.
+ * - Cache of a layer: k_pages and v_pages, [n_pages][n_kv_heads][page_size][head_dim],
+ *   page_size a power of two in [8, 256]; page_table int32 [pool][max_pages], kv_lens
+ *   int32 [pool]: position j of the sequence in slot s lies in page
+ *   page_table[s][j / page_size], row j % page_size. kv_lens counts the call's new tokens.
+ *   Both stay on the device; a sequence whose slot or length is out of range is skipped
+ *   (its rows are not written) and counted once in err_count.
+ * - Rows: q [rows][n_q_heads][head_dim] and k, v [rows][n_kv_heads][head_dim] may be
+ *   slices of a wider row (one projection's output): q_stride, k_stride, v_stride are the
+ *   elements from one row to the next, multiples of 16 bytes. out is dense.
+ * - Mask: the new tokens are a sequence's last ones, at positions kv_len - m .. kv_len - 1
+ *   for m of them. Position p sees key j when j <= p and (p - j < window, or
+ *   j < n_sinks, or window == 0): a causal mask, a sliding window of `window` positions
+ *   (p itself among them), and n_sinks first positions that stay visible. A row that sees
+ *   nothing (a position before 0) is zeros.
+ * - What a page holds past the sequence's length, or at keys that no row of the sequence
+ *   sees, has no effect, infinities and NaN included, and page ids before the window are
+ *   not read. (Between rows of one sequence that see different keys a masked key has
+ *   weight 0, so a value that is not finite at such a key gives NaN.) A visible page id
+ *   outside [0, n_pages) hides its keys and adds one or more to err_count. */
+
+typedef enum gdn_dtype { GDN_F32 = 0, GDN_F16 = 1, GDN_BF16 = 2 } gdn_dtype;
+
+/* Writes the new tokens' keys and values to their places in the pages. Sequence n owns
+ * rows cu_seqlens[n] .. cu_seqlens[n+1] - 1 of k and v (device int32[n_seqs + 1], checked
+ * on the device as for the ragged calls), or total_tokens / n_seqs rows each when
+ * cu_seqlens is NULL. A sequence with more new tokens than its length is skipped and
+ * counted; a row whose page id is out of range is dropped and counted. */
+gdn_status gdn_kv_append(const void *k, const void *v, void *k_pages, void *v_pages,
+                         const int32_t *page_table, const int32_t *kv_lens,
+                         const int32_t *cu_seqlens, int n_seqs, int total_tokens,
+                         int n_kv_heads, int head_dim, int page_size, int n_pages,
+                         int max_pages, int k_stride, int v_stride, int dtype,
+                         const int32_t *slots, int pool, int32_t *err_count,
+                         gdn_stream_t stream);
+
+/* Attention of the last n_tokens tokens (one, or a few draft tokens; at most 64) of every
+ * sequence over its cache: q, out [n_seqs][n_tokens][n_q_heads][head_dim]. Every visible
+ * key and value is read once per 16 rows of (token, head of a key head). The keys of the
+ * whole batch are dealt out evenly over the GPU, whatever the lengths, and partial
+ * results joined inside the call: one launch.
+ * workspace: gdn_attn_decode_workspace_size() bytes (0 for invalid sizes), 16-byte
+ * aligned, contents on entry irrelevant; calls that share one must not overlap. */
+size_t gdn_attn_decode_workspace_size(int n_seqs, int n_tokens, int n_q_heads, int n_kv_heads,
+                                      int head_dim);
+gdn_status gdn_attn_decode(const void *q, const void *k_pages, const void *v_pages,
+                           const int32_t *page_table, const int32_t *kv_lens, void *out,
+                           int n_seqs, int n_tokens, int n_q_heads, int n_kv_heads,
+                           int head_dim, int page_size, int n_pages, int max_pages, int window,
+                           int n_sinks, float scale, int q_stride, int dtype,
+                           const int32_t *slots, int pool, int32_t *err_count, void *workspace,
+                           size_t workspace_bytes, gdn_stream_t stream);
+
+/* Attention of a ragged batch of prompts, or chunks of prompts, over the cache (append
+ * first): q, out [total_tokens][n_q_heads][head_dim], sequence n owning rows
+ * cu_seqlens[n] .. cu_seqlens[n+1] - 1, the last ones of its kv_len positions; cu_seqlens,
+ * total_tokens and max_tokens as for the ragged calls.
+ * workspace: gdn_attn_prefill_workspace_size() bytes (may be 0, then NULL will do),
+ * otherwise as for gdn_attn_decode. */
+size_t gdn_attn_prefill_workspace_size(int n_seqs, int total_tokens, int n_q_heads,
+                                       int n_kv_heads, int head_dim);
+gdn_status gdn_attn_prefill(const void *q, const void *k_pages, const void *v_pages,
+                            const int32_t *page_table, const int32_t *kv_lens, void *out,
+                            const int32_t *cu_seqlens, int n_seqs, int total_tokens,
+                            int max_tokens, int n_q_heads, int n_kv_heads, int head_dim,
+                            int page_size, int n_pages, int max_pages, int window, int n_sinks,
+                            float scale, int q_stride, int dtype, const int32_t *slots, int pool,
+                            int32_t *err_count, void *workspace, size_t workspace_bytes,
+                            gdn_stream_t stream);
+
+/* Bookkeeping of the pages. page_refs int32 [n_pages] counts the table entries that hold
+ * a page (0: free); entries of a slot's row past its length are -1. `pages` is every
+ * layer's data in planes: [n_planes][n_pages][page_bytes], e.g. n_planes = 2 * layers with
+ * plane 2 l the K pages and 2 l + 1 the V pages of layer l, page_bytes (a multiple of 16)
+ * = n_kv_heads * page_size * head_dim * element size. One table serves all planes.
+ * Free pages are handed out lowest id first, in call order: the books come out the same
+ * every time. Slots within one call must be distinct.
+ * workspace (where taken): gdn_pages_workspace_size() bytes for the call's n_seqs (forks)
+ * and n_pages, 16-byte aligned, contents on entry irrelevant. */
+size_t gdn_pages_workspace_size(int n_seqs, int n_pages);
+
+/* Page dst[i] <- page src[i] in every plane (device int32[n_copies]); no page may be a
+ * destination twice, or a source and a destination. A pair out of range is skipped and
+ * counted. */
+gdn_status gdn_pages_copy(void *pages, const int32_t *src, const int32_t *dst, int n_copies,
+                          int n_planes, int n_pages, size_t page_bytes, int32_t *err_count,
+                          gdn_stream_t stream);
+
+/* Makes room for n_new[n] (device int32) more tokens of every sequence: its row gets the
+ * pages the new length needs and its kv_len grows. A last page that is partly full and
+ * shared is replaced by a copy of its own (the sharers keep the old one). A sequence asks
+ * for all its pages or none: when those asked for up to and including it in call order
+ * exceed the free pages, or its arguments are out of range (n_new < 0, past max_pages), it
+ * is left as it is and counted. Pages that become free are not handed out in the same
+ * call. */
+gdn_status gdn_pages_reserve(void *pages, int32_t *page_table, int32_t *kv_lens,
+                             int32_t *page_refs, const int32_t *n_new, int n_seqs,
+                             int page_size, int n_planes, int n_pages, size_t page_bytes,
+                             int max_pages, const int32_t *slots, int pool, int32_t *err_count,
+                             void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/* Slot children[i] becomes a copy of slot parents[i] (device int32[n_forks]): the full
+ * pages are shared, a partly full last page is copied to a free one. A child must be empty
+ * (kv_len 0) and no child may appear twice; a parent may have several children. A fork
+ * with a slot out of range, a child that is not empty or is its own parent, or no free
+ * page left for it (in call order) is skipped and counted. */
+gdn_status gdn_pages_fork(void *pages, int32_t *page_table, int32_t *kv_lens,
+                          int32_t *page_refs, const int32_t *parents, const int32_t *children,
+                          int n_forks, int page_size, int n_planes, int n_pages,
+                          size_t page_bytes, int max_pages, int pool, int32_t *err_count,
+                          void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/* Cuts every sequence to new_lens[n] tokens (device int32; NULL: 0, freeing the sequence;
+ * e.g. the rollback of rejected draft tokens): pages past it lose a holder, and are free
+ * when it was their last. A sequence with a slot out of range, or a new length below 0 or
+ * above its own, is skipped and counted. */
+gdn_status gdn_pages_truncate(int32_t *page_table, int32_t *kv_lens, int32_t *page_refs,
+                              const int32_t *new_lens, int n_seqs, int page_size, int n_pages,
+                              int max_pages, const int32_t *slots, int pool,
+                              int32_t *err_count, gdn_stream_t stream);
+
+/* Moves the pages in use to the pool's start: with L pages in use, those at or above L go,
+ * in ascending order, to the free ones below L. Tables and page_refs follow; n_live (device
+ * int32, may be NULL) receives L. The table's rows of all slots must be covered by
+ * page_refs (no entry may hold a page that counts as free). */
+gdn_status gdn_pages_compact(void *pages, int32_t *page_table, const int32_t *kv_lens,
+                             int32_t *page_refs, int page_size, int n_planes, int n_pages,
+                             size_t page_bytes, int max_pages, int pool, int32_t *n_live,
+                             void *workspace, size_t workspace_bytes, gdn_stream_t stream);
 
 #ifdef __cplusplus
 }
