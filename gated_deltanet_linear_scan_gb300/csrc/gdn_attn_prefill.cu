@@ -7,6 +7,7 @@
 // key head): the keys are read once for all of them, and a tile spans few positions, which
 // keeps the work wasted at the causal diagonal and at the window's edge small.
 #include "gdn_paged.cuh"
+#include "gdn_tc.cuh"
 
 namespace gdn {
 namespace {
@@ -267,6 +268,476 @@ gdn_status launch_simt_dim(int d, const PrefillParams &p, cudaStream_t s) {
     }
 }
 
+// ------------------------------------------------------------------ on the tensor cores
+
+// 16-bit types. A CTA takes kTiles tiles of 128 rows and walks the keys in tiles of 128:
+//   S = Q K^T      tcgen05, Q and K from shared memory, S in tensor memory
+//   P = 2^(scale log2(e) S - m)   four warps per row tile, one thread per row: the row's
+//                  maximum and sum need no exchange; P goes back to tensor memory over S,
+//                  in the cache's type (half a unit of the type per weight, which averages
+//                  out below the output's own rounding)
+//   O += P V       tcgen05, P from tensor memory, V from shared memory as it lies there
+//                  (rows are keys: the MN-major operand form, no transposition)
+// O stays in tensor memory. It is rescaled only when a row's maximum has grown by more than
+// 2^8 since the reference the weights use (they stay below 2^8, far inside both types).
+//
+// Two row tiles (head_dim 64, 128) share every key tile and alternate: one tile's softmax
+// runs while the tensor pipe works for the other. With head_dim 256 O fills half the tensor
+// memory, so there is one row tile and two S buffers: S of the next key tile is computed
+// during the softmax of this one.
+//
+// K and V stream through a ring of 16 KB slots (128 keys x 64 dimensions of K; all
+// dimensions of 16 KB / row bytes keys of V), loaded page by page by one warp.
+constexpr int kTcKeys = 128;
+constexpr int kTcRows = 128;
+constexpr int kSlotBytes = 16384;
+constexpr int kDescs = 8;
+constexpr float kLazy = 8.0f;  // log2 of the growth of a maximum that makes O rescale
+
+template <int D>
+struct Tc {
+    static constexpr int kTiles = D == 256 ? 1 : 2;
+    static constexpr int kBufs = D == 256 ? 2 : 1;          // S buffers of a row tile
+    static constexpr int kSubs = D / 64;                    // slots of a K (or V) tile
+    static constexpr int kVKeys = kSlotBytes / (2 * D);     // keys of a V slot
+    static constexpr int kQBytes = kTcRows * D * 2;         // of a row tile
+    static constexpr int kSlots = D == 64 ? 8 : 9;
+    static constexpr int kSmem = kTiles * kQBytes + kSlots * kSlotBytes + 1024;
+    static constexpr int kThreads = kTiles * 128 + 128;      // softmax; MMA, loads and two idle warps
+    static constexpr int kS = 0, kO = 256;                  // tensor-memory columns
+};
+
+// Where K and V tile j stand in the order of loading and use, of n tiles. Two row tiles:
+// K0 V0 K1 V1 .. ; one row tile with two S buffers: K0 K1 V0 K2 V1 .. V(n-1).
+template <int D>
+__device__ __forceinline__ int k_block(int j) {
+    return Tc<D>::kTiles == 2 ? 2 * j : (j == 0 ? 0 : 2 * j - 1);
+}
+template <int D>
+__device__ __forceinline__ int v_block(int j, int n) {
+    return Tc<D>::kTiles == 2 ? 2 * j + 1 : (j == n - 1 ? 2 * n - 1 : 2 * j + 2);
+}
+
+__device__ __forceinline__ void wait_or_flag(uint64_t *bar, uint32_t parity, volatile int *dead) {
+    if (*dead) return;
+    if (!mbar_wait(bar, parity)) {
+        *dead = 1;
+        atomicOr(&g_watchdog_attn_prefill, WD_STAGE_COPY);
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(Tc<D>::kThreads, 1)
+attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
+                       const __grid_constant__ CUtensorMap k_map,
+                       const __grid_constant__ CUtensorMap v_map, const PrefillParams p) {
+    using C = Tc<D>;
+    constexpr bool kBf16 = sizeof(T) == 2 && !__is_same(T, __half);
+    constexpr uint32_t kIdescS = tc::idesc_16bit(kBf16, kTcRows, kTcKeys, false);
+    constexpr uint32_t kIdescO = tc::idesc_16bit(kBf16, kTcRows, D, true);
+    extern __shared__ uint8_t dyn[];
+    uint8_t *smem =
+        reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+    uint8_t *ring = smem + C::kTiles * C::kQBytes;
+    __shared__ __align__(8) uint64_t slot_full[C::kSlots], slot_empty[C::kSlots];
+    __shared__ __align__(8) uint64_t q_full, s_full[2], p_ready[2], o_done[2], desc_full[kDescs];
+    __shared__ int2 descs[kDescs];  // first key and loaded 8-key blocks of a key tile
+    __shared__ uint32_t tmem_base;
+    __shared__ int sh_dead;
+
+    RowTile t;
+    if (!find_tile(p, t)) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = p.tokens_per_tile / C::kTiles;  // tokens of one 128-row tile
+    const int tiles = t.tokens > per ? 2 : 1;
+    const TileWalk walk = walk_tiles<kTcKeys>(p.mask, t.p_first, t.p_last);
+    const int n = walk.count;
+    // key tiles of row tile 0: those past its last position are left out
+    int n0 = n;
+    if (tiles == 2 && n > 0 && walk.tile(n - 1) * kTcKeys > t.p_first + per - 1) --n0;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(&slot_full[i], 1);
+            mbar_init(&slot_empty[i], 1);
+        }
+        for (int i = 0; i < kDescs; ++i) mbar_init(&desc_full[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_ready[i], 4);
+            mbar_init(&o_done[i], 1);
+        }
+        mbar_init(&q_full, 1);
+        fence_mbar_init();
+        sh_dead = 0;
+    }
+    if (warp == C::kTiles * 4) tc::tmem_alloc(&tmem_base, 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_base;
+
+    // Two row tiles: 384 threads of 168 registers; the softmax threads take 224 each, the
+    // third warp group keeps 56 (2 * 224 + 56 = 3 * 168).
+    if (warp >= C::kTiles * 4) {
+    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == C::kTiles * 4 + 1) {
+        // ---------------------------------------------------------- the loading warp
+        const int ps = 1 << p.cache.log2_ps;
+        const int bk = min(ps, kTcKeys), n_bk = kTcKeys / bk;       // K: keys of a load, loads
+        const int bv = min(ps, C::kVKeys), n_bv = C::kVKeys / bv;   // V, per slot
+        if (lane == 0 && n > 0) {
+            tma_prefetch_map(&k_map);
+            tma_prefetch_map(&v_map);
+            const int rows = p.heads_per_tile * per;
+            mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(tiles * rows) * D * 2u);
+            for (int i = 0; i < tiles; ++i)
+                for (int cb = 0; cb < D / 64; ++cb)
+                    tma_load_3d(smem + i * C::kQBytes + cb * kTcRows * 128, &q_map, cb * 64, t.head0,
+                                static_cast<int>(t.row0) + t.token0 + i * per, &q_full);
+        }
+        // page of this lane's keys of tile j (lanes below n_bk), -1: not loaded
+        auto page_at = [&](int j) -> int {
+            if (lane >= n_bk) return -1;
+            const int key = walk.tile(j) * kTcKeys + lane * bk;
+            if (key > t.p_last) return -1;
+            if (!(t.p_first - (key + bk - 1) < p.mask.window || key < p.mask.sinks)) return -1;
+            const int page = p.cache.page_of(t.slot, key);
+            return p.cache.page_ok(page) ? page : -2;
+        };
+        auto kind_of = [&](int b, int &j) -> bool {  // block b: true for K; its tile
+            if (C::kTiles == 2) {
+                j = b >> 1;
+                return (b & 1) == 0;
+            }
+            if (b == 0 || ((b & 1) && (b + 1) / 2 < n)) {
+                j = (b + 1) / 2;
+                return true;
+            }
+            j = b == 2 * n - 1 ? n - 1 : (b - 2) / 2;
+            return false;
+        };
+        int j = 0, g = 0;
+        bool is_k = kind_of(0, j);
+        int page = n > 0 ? page_at(j) : -1;
+        for (int b = 0; b < 2 * n; ++b) {
+            int next_j = 0;
+            const bool next_k = b + 1 < 2 * n ? kind_of(b + 1, next_j) : false;
+            const int next_page = b + 1 < 2 * n ? page_at(next_j) : -1;
+            const int key0 = walk.tile(j) * kTcKeys;
+            const unsigned have = __ballot_sync(FULL_MASK, page >= 0);
+            if (is_k) {
+                if (page == -2 && blockIdx.y == 0 && p.err_count) atomicAdd(p.err_count, 1);
+                if (lane == 0) {
+                    unsigned blocks = 0;
+                    for (int i = 0; i < kTcKeys / 8; ++i)
+                        if ((have >> (i * 8 / bk)) & 1u) blocks |= 1u << i;
+                    descs[j % kDescs] = make_int2(key0, static_cast<int>(blocks));
+                    mbar_arrive(&desc_full[j % kDescs]);
+                }
+            }
+            for (int s = 0; s < C::kSubs; ++s, ++g) {
+                const int slot = g % C::kSlots;
+                uint8_t *to = ring + slot * kSlotBytes;
+                if (g >= C::kSlots)
+                    wait_or_flag(&slot_empty[slot], ((g / C::kSlots) - 1) & 1, &sh_dead);
+                if (is_k) {
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&slot_full[slot], static_cast<uint32_t>(__popc(have) * bk) * 128u);
+                    __syncwarp();
+                    if (page >= 0)
+                        tma_load_2d(to + lane * bk * 128, &k_map, s * 64,
+                                    (page * p.cache.n_kv_heads + t.kvh) * ps + (key0 & (ps - 1)),
+                                    &slot_full[slot]);
+                } else {
+                    const int off = s * C::kVKeys + lane * bv;  // this lane's keys of the tile
+                    const int pg = __shfl_sync(FULL_MASK, page, (off / bk) & 31);
+                    const bool mine = lane < n_bv && pg >= 0;
+                    const unsigned loads = __popc(__ballot_sync(FULL_MASK, mine));
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&slot_full[slot], loads * static_cast<uint32_t>(bv) * D * 2u);
+                    __syncwarp();
+                    if (mine) {
+                        const int row = (pg * p.cache.n_kv_heads + t.kvh) * ps + ((key0 + off) & (ps - 1));
+#pragma unroll
+                        for (int cb = 0; cb < D / 64; ++cb)
+                            tma_load_2d(to + (cb * C::kVKeys + lane * bv) * 128, &v_map, cb * 64, row,
+                                        &slot_full[slot]);
+                    }
+                }
+            }
+            is_k = next_k;
+            j = next_j;
+            page = next_page;
+        }
+    } else if (warp == C::kTiles * 4) {
+        // ---------------------------------------------------------- the MMA warp
+        if (lane == 0 && n > 0) {
+            wait_or_flag(&q_full, 0, &sh_dead);
+            auto slot_of = [&](int block, int s, uint32_t &parity) {
+                const int g = block * C::kSubs + s;
+                parity = (g / C::kSlots) & 1;
+                return g % C::kSlots;
+            };
+            // S of row tile i over key tile j
+            auto issue_s = [&](int i, int j, bool release) {
+                const int buf = C::kBufs == 2 ? j & 1 : i;
+                const uint32_t q = smem_addr(smem + i * C::kQBytes);
+#pragma unroll
+                for (int s = 0; s < C::kSubs; ++s) {
+                    uint32_t parity;
+                    const int slot = slot_of(k_block<D>(j), s, parity);
+                    wait_or_flag(&slot_full[slot], parity, &sh_dead);
+                    tc::fence_after_sync();
+                    const uint32_t k = smem_addr(ring + slot * kSlotBytes);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        tc::mma_bf16(tmem + C::kS + buf * kTcKeys,
+                                     tc::smem_desc_sw128(q + s * kTcRows * 128 + x * 32),
+                                     tc::smem_desc_sw128(k + x * 32), kIdescS, s + x > 0);
+                    if (release) tc::mma_commit(&slot_empty[slot]);
+                }
+                tc::mma_commit(&s_full[buf]);
+            };
+            // O of row tile i += P V over key tile j
+            auto issue_o = [&](int i, int j, bool release) {
+                const int buf = C::kBufs == 2 ? j & 1 : i;
+                wait_or_flag(&p_ready[buf], (C::kBufs == 2 ? j >> 1 : j) & 1, &sh_dead);
+                tc::fence_after_sync();
+#pragma unroll
+                for (int s = 0; s < C::kSubs; ++s) {
+                    uint32_t parity;
+                    const int slot = slot_of(v_block<D>(j, n), s, parity);
+                    wait_or_flag(&slot_full[slot], parity, &sh_dead);
+                    tc::fence_after_sync();
+                    const uint32_t v = smem_addr(ring + slot * kSlotBytes);
+#pragma unroll
+                    for (int x = 0; x < C::kVKeys / 16; ++x)
+                        tc::mma_bf16_ts(tmem + C::kO + i * D,
+                                        tmem + C::kS + buf * kTcKeys + (s * C::kVKeys + x * 16) / 2,
+                                        tc::smem_desc_sw128_mn(v + x * 2048, C::kVKeys * 128), kIdescO,
+                                        j > 0 || s + x > 0);
+                    if (release) tc::mma_commit(&slot_empty[slot]);
+                }
+                tc::mma_commit(&o_done[i]);
+            };
+            if (C::kTiles == 2) {
+                if (n0 > 0) issue_s(0, 0, tiles == 1);
+                if (tiles == 2) issue_s(1, 0, true);
+                for (int j = 0; j < n; ++j) {
+                    if (j < n0) {
+                        issue_o(0, j, tiles == 1);
+                        if (j + 1 < n0) issue_s(0, j + 1, tiles == 1);
+                    }
+                    if (tiles == 2) {
+                        issue_o(1, j, true);
+                        if (j + 1 < n) issue_s(1, j + 1, true);
+                    }
+                }
+            } else {
+                issue_s(0, 0, true);
+                for (int j = 0; j < n; ++j) {
+                    if (j + 1 < n) issue_s(0, j + 1, true);
+                    issue_o(0, j, true);
+                }
+            }
+        }
+        __syncwarp();
+    }
+    } else {
+    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if (warp / 4 < tiles) {
+        // ---------------------------------------------------------- softmax, one row a thread
+        const int i = warp / 4, row = threadIdx.x & 127;
+        const int my_n = i == 0 ? n0 : n;
+        const int token = i * per + row / p.heads_per_tile;
+        const int head = row % p.heads_per_tile;
+        const int pos = t.p_first + token;
+        const int p_first = t.p_first + i * per;                      // of the row tile
+        const int p_last = min(p_first + per - 1, t.p_last);
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const bool positive = p.scale_log2 > 0.0f;
+        const float mult = positive ? p.scale_log2 : 1.0f;
+        float m = -INFINITY, l = 0.0f;
+        for (int j = 0; j < my_n; ++j) {
+            const int buf = C::kBufs == 2 ? j & 1 : i;
+            const uint32_t s_addr = tmem + lanes + C::kS + buf * kTcKeys;
+            wait_or_flag(&desc_full[j % kDescs], (j / kDescs) & 1, &sh_dead);
+            const int2 desc = descs[j % kDescs];
+            const int key0 = desc.x;
+            const unsigned blocks = static_cast<unsigned>(desc.y);
+            // V rows that no row of the CTA sees are cleared, so that whatever the page holds
+            // there (an infinity, a NaN) cannot reach O through a weight of 0
+            const bool alive = blocks == 0xFFFFu && key0 + kTcKeys - 1 <= t.p_last &&
+                               (t.p_first - key0 < p.mask.window || key0 + kTcKeys <= p.mask.sinks);
+            wait_or_flag(&s_full[buf], (C::kBufs == 2 ? j >> 1 : j) & 1, &sh_dead);
+            tc::fence_after_sync();
+            if (!alive && (i == 0 || j >= n0)) {
+                // (two S buffers: once the O product before this tile's is complete, the
+                // ring slots of V are at most one phase from the one waited for)
+                if (C::kBufs == 2 && j > 0) wait_or_flag(&o_done[0], (j - 1) & 1, &sh_dead);
+                const int key = key0 + row;
+                const bool dead = !((blocks >> (row >> 3)) & 1u) || key > t.p_last ||
+                                  !(t.p_first - key < p.mask.window || key < p.mask.sinks);
+#pragma unroll
+                for (int s = 0; s < C::kSubs; ++s) {
+                    const int g = v_block<D>(j, n) * C::kSubs + s;
+                    wait_or_flag(&slot_full[g % C::kSlots], (g / C::kSlots) & 1, &sh_dead);
+                    if (dead && row / C::kVKeys == s) {
+                        uint8_t *at = ring + (g % C::kSlots) * kSlotBytes + (row % C::kVKeys) * 128;
+                        for (int x = 0; x < D / 8; ++x)
+                            *reinterpret_cast<uint4 *>(at + (x >> 3) * C::kVKeys * 128 + (x & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    }
+                }
+                fence_proxy_async_smem();
+            }
+            uint32_t raw[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc::tmem_ld32_nowait(s_addr + c * 32, raw[c]);
+            tc::tmem_ld_wait();
+            float s[128];
+#pragma unroll
+            for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(raw[c >> 5][c & 31]);
+            if (!positive) {
+#pragma unroll
+                for (int c = 0; c < 128; ++c) s[c] *= p.scale_log2;
+            }
+            const bool clean = blocks == 0xFFFFu && key0 + kTcKeys - 1 <= p_first &&
+                               (p_last - key0 < p.mask.window || key0 + kTcKeys <= p.mask.sinks);
+            if (!clean) {
+#pragma unroll
+                for (int c = 0; c < 128; ++c) {
+                    const bool ok = ((blocks >> (c >> 3)) & 1u) && p.mask.sees(pos, key0 + c);
+                    if (!ok) s[c] = -INFINITY;
+                }
+            }
+            float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int c = 4; c < 128; ++c) top[c & 3] = fmaxf(top[c & 3], s[c]);
+            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            if (j == 0) {
+                m = mx;
+            } else {
+                const bool grow = (mx - m) * mult > kLazy;
+                if (__any_sync(FULL_MASK, grow)) {
+                    // O is complete up to the tile before: S of this tile was issued after it
+                    // (two S buffers: after the one before that, so its own arrival is awaited)
+                    if (C::kBufs == 2) {
+                        wait_or_flag(&o_done[0], (j - 1) & 1, &sh_dead);
+                        tc::fence_after_sync();
+                    }
+                    const float f = grow ? fast_exp2((m - mx) * mult) : 1.0f;
+                    if (grow) m = mx;
+                    l *= f;
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tc::tmem_ld32_nowait(tmem + lanes + C::kO + i * D + c, o);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                        tc::tmem_st32(tmem + lanes + C::kO + i * D + c, o);
+                    }
+                }
+            }
+            const float base = m == -INFINITY ? 0.0f : m * mult;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c = 0; c < 128; c += 64) {
+                uint32_t w[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                    const float a = fast_exp2(fmaf(s[c + 2 * x], mult, -base));
+                    const float b = fast_exp2(fmaf(s[c + 2 * x + 1], mult, -base));
+                    sum[(2 * x) & 3] += a;
+                    sum[(2 * x + 1) & 3] += b;
+                    w[x] = Elem<T>::pack(a, b);
+                }
+                tc::tmem_st32(s_addr + c / 2, w);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tc::tmem_st_wait();
+            tc::fence_before_sync();
+            __syncwarp();
+            // keeps this thread at most one phase behind o_done
+            if (C::kBufs == 2 && j > 0) wait_or_flag(&o_done[0], (j - 1) & 1, &sh_dead);
+            if (lane == 0) mbar_arrive(&p_ready[buf]);
+        }
+        // ---------------------------------------------------------- O out
+        T *out = static_cast<T *>(p.out) +
+                 ((t.row0 + t.token0 + token) * p.n_q_heads + t.head0 + head) * D;
+        const bool mine = token < t.tokens && row / p.heads_per_tile < per && head < t.heads;
+        if (my_n > 0) {
+            wait_or_flag(&o_done[i], (my_n - 1) & 1, &sh_dead);
+            tc::fence_after_sync();
+        }
+        const float inv = 1.0f / l;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            if (my_n > 0) {
+                tc::tmem_ld32_nowait(tmem + lanes + C::kO + i * D + c, o);
+                tc::tmem_ld_wait();
+            }
+            if (mine && !sh_dead) {
+#pragma unroll
+                for (int x = 0; x < 32; x += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        w[y] = l == 0.0f ? 0u
+                                         : Elem<T>::pack(__uint_as_float(o[x + 2 * y]) * inv,
+                                                         __uint_as_float(o[x + 2 * y + 1]) * inv);
+                    *reinterpret_cast<uint4 *>(out + c + x) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+        tc::fence_before_sync();
+    }
+    }
+    __syncthreads();
+    if (warp == C::kTiles * 4) {
+        tc::fence_after_sync();
+        tc::tmem_relinquish();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <typename T, int D>
+gdn_status launch_tc(PrefillParams p, int dtype, cudaStream_t s) {
+    using C = Tc<D>;
+    const int ps = 1 << p.cache.log2_ps;
+    p.heads_per_tile = p.group < kTcRows ? p.group : kTcRows;
+    p.head_groups = (p.group + p.heads_per_tile - 1) / p.heads_per_tile;
+    const int per = kTcRows / p.heads_per_tile;
+    p.tokens_per_tile = per * C::kTiles;
+    const long long tiles = p.seqs.total / p.tokens_per_tile + p.n_seqs;
+    const long long ys = static_cast<long long>(p.cache.n_kv_heads) * p.head_groups;
+    if (tiles > 0x7fffffffLL || ys > 65535) return GDN_ERR_UNSUPPORTED;
+    CUtensorMap q_map, k_map, v_map;
+    const uint64_t rows = static_cast<uint64_t>(p.cache.n_pages) * p.cache.n_kv_heads * ps;
+    GDN_TRY(encode_heads_map(&q_map, p.q, dtype, D, p.n_q_heads, static_cast<uint64_t>(p.seqs.total),
+                             static_cast<uint64_t>(p.q_stride) * 2, p.heads_per_tile, per));
+    GDN_TRY(encode_rows_map(&k_map, p.k_pages, dtype, D, rows, D * 2, ps < kTcKeys ? ps : kTcKeys));
+    GDN_TRY(encode_rows_map(&v_map, p.v_pages, dtype, D, rows, D * 2, ps < C::kVKeys ? ps : C::kVKeys));
+    auto kernel = attn_prefill_tc_kernel<T, D>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+        return GDN_ERR_LAUNCH;
+    kernel<<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(ys)), C::kThreads, C::kSmem, s>>>(
+        q_map, k_map, v_map, p);
+    return launch_status();
+}
+
+template <typename T>
+gdn_status launch_tc_dim(int d, const PrefillParams &p, int dtype, cudaStream_t s) {
+    switch (d) {
+        case 64: return launch_tc<T, 64>(p, dtype, s);
+        case 128: return launch_tc<T, 128>(p, dtype, s);
+        default: return launch_tc<T, 256>(p, dtype, s);
+    }
+}
+
 }  // namespace
 
 unsigned read_and_clear_watchdog_attn_prefill(cudaStream_t s) {
@@ -333,8 +804,8 @@ gdn_status gdn_attn_prefill(const void *q, const void *k_pages, const void *v_pa
     const cudaStream_t s = as_cuda(stream);
     switch (dtype) {
         case GDN_F32: return launch_simt_dim<float>(head_dim, p, s);
-        case GDN_F16: return launch_simt_dim<__half>(head_dim, p, s);
-        default: return launch_simt_dim<__nv_bfloat16>(head_dim, p, s);
+        case GDN_F16: return launch_tc_dim<__half>(head_dim, p, dtype, s);
+        default: return launch_tc_dim<__nv_bfloat16>(head_dim, p, dtype, s);
     }
 }
 
