@@ -287,10 +287,13 @@ gdn_status launch_simt_dim(int d, const PrefillParams &p, cudaStream_t s) {
 // during the softmax of this one.
 //
 // K and V stream through a ring of 16 KB slots (128 keys x 64 dimensions of K; all
-// dimensions of 16 KB / row bytes keys of V), loaded page by page by one warp.
+// dimensions of 16 KB / row bytes keys of V), loaded page by page by one warp. A V slot keeps
+// the pages' rows apart ([page][128-byte column][row]), so that one copy brings all of a
+// page's columns; the MMA's descriptor strides say where they lie.
 constexpr int kTcKeys = 128;
 constexpr int kTcRows = 128;
 constexpr int kSlotBytes = 16384;
+constexpr int kSlots = 8;
 constexpr int kDescs = 8;
 constexpr float kLazy = 8.0f;  // log2 of the growth of a maximum that makes O rescale
 
@@ -300,8 +303,8 @@ struct Tc {
     static constexpr int kBufs = D == 256 ? 2 : 1;          // S buffers of a row tile
     static constexpr int kSubs = D / 64;                    // slots of a K (or V) tile
     static constexpr int kVKeys = kSlotBytes / (2 * D);     // keys of a V slot
+    static constexpr int kLog2VKeys = D == 64 ? 7 : D == 128 ? 6 : 5;
     static constexpr int kQBytes = kTcRows * D * 2;         // of a row tile
-    static constexpr int kSlots = D == 64 ? 8 : 9;
     static constexpr int kSmem = kTiles * kQBytes + kSlots * kSlotBytes + 1024;
     static constexpr int kThreads = kTiles * 128 + 128;      // softmax; MMA, loads and two idle warps
     static constexpr int kS = 0, kO = 256;                  // tensor-memory columns
@@ -318,12 +321,21 @@ __device__ __forceinline__ int v_block(int j, int n) {
     return Tc<D>::kTiles == 2 ? 2 * j + 1 : (j == n - 1 ? 2 * n - 1 : 2 * j + 2);
 }
 
+// Bounded wait; once one gave up, the CTA's later waits return at once and none of its rows
+// are written.
 __device__ __forceinline__ void wait_or_flag(uint64_t *bar, uint32_t parity, volatile int *dead) {
-    if (*dead) return;
+    if (mbar_test(bar, parity) || *dead) return;
     if (!mbar_wait(bar, parity)) {
         *dead = 1;
         atomicOr(&g_watchdog_attn_prefill, WD_STAGE_COPY);
     }
+}
+
+// Bits lo .. hi - 1 of a 32-bit word (any of them outside the word).
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
+    const uint32_t below = hi >= 32 ? 0xFFFFFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
+    const uint32_t skip = lo >= 32 ? 0xFFFFFFFFu : lo <= 0 ? 0u : (1u << lo) - 1u;
+    return below & ~skip;
 }
 
 template <typename T, int D>
@@ -332,14 +344,14 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                        const __grid_constant__ CUtensorMap k_map,
                        const __grid_constant__ CUtensorMap v_map, const PrefillParams p) {
     using C = Tc<D>;
-    constexpr bool kBf16 = sizeof(T) == 2 && !__is_same(T, __half);
+    constexpr bool kBf16 = !__is_same(T, __half);
     constexpr uint32_t kIdescS = tc::idesc_16bit(kBf16, kTcRows, kTcKeys, false);
     constexpr uint32_t kIdescO = tc::idesc_16bit(kBf16, kTcRows, D, true);
     extern __shared__ uint8_t dyn[];
     uint8_t *smem =
         reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
     uint8_t *ring = smem + C::kTiles * C::kQBytes;
-    __shared__ __align__(8) uint64_t slot_full[C::kSlots], slot_empty[C::kSlots];
+    __shared__ __align__(8) uint64_t slot_full[kSlots], slot_empty[kSlots];
     __shared__ __align__(8) uint64_t q_full, s_full[2], p_ready[2], o_done[2], desc_full[kDescs];
     __shared__ int2 descs[kDescs];  // first key and loaded 8-key blocks of a key tile
     __shared__ uint32_t tmem_base;
@@ -352,12 +364,14 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     const int tiles = t.tokens > per ? 2 : 1;
     const TileWalk walk = walk_tiles<kTcKeys>(p.mask, t.p_first, t.p_last);
     const int n = walk.count;
-    // key tiles of row tile 0: those past its last position are left out
+    // key tiles of row tile 0: a last one past its positions is left out
     int n0 = n;
     if (tiles == 2 && n > 0 && walk.tile(n - 1) * kTcKeys > t.p_first + per - 1) --n0;
+    const int log2_bv = min(p.cache.log2_ps, C::kLog2VKeys);  // keys of a V load
+    const int bv = 1 << log2_bv;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kSlots; ++i) {
+        for (int i = 0; i < kSlots; ++i) {
             mbar_init(&slot_full[i], 1);
             mbar_init(&slot_empty[i], 1);
         }
@@ -380,148 +394,159 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     // Two row tiles: 384 threads of 168 registers; the softmax threads take 224 each, the
     // third warp group keeps 56 (2 * 224 + 56 = 3 * 168).
     if (warp >= C::kTiles * 4) {
-    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == C::kTiles * 4 + 1) {
-        // ---------------------------------------------------------- the loading warp
-        const int ps = 1 << p.cache.log2_ps;
-        const int bk = min(ps, kTcKeys), n_bk = kTcKeys / bk;       // K: keys of a load, loads
-        const int bv = min(ps, C::kVKeys), n_bv = C::kVKeys / bv;   // V, per slot
-        if (lane == 0 && n > 0) {
-            tma_prefetch_map(&k_map);
-            tma_prefetch_map(&v_map);
-            const int rows = p.heads_per_tile * per;
-            mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(tiles * rows) * D * 2u);
-            for (int i = 0; i < tiles; ++i)
-                for (int cb = 0; cb < D / 64; ++cb)
-                    tma_load_3d(smem + i * C::kQBytes + cb * kTcRows * 128, &q_map, cb * 64, t.head0,
-                                static_cast<int>(t.row0) + t.token0 + i * per, &q_full);
-        }
-        // page of this lane's keys of tile j (lanes below n_bk), -1: not loaded
-        auto page_at = [&](int j) -> int {
-            if (lane >= n_bk) return -1;
-            const int key = walk.tile(j) * kTcKeys + lane * bk;
-            if (key > t.p_last) return -1;
-            if (!(t.p_first - (key + bk - 1) < p.mask.window || key < p.mask.sinks)) return -1;
-            const int page = p.cache.page_of(t.slot, key);
-            return p.cache.page_ok(page) ? page : -2;
-        };
-        auto kind_of = [&](int b, int &j) -> bool {  // block b: true for K; its tile
-            if (C::kTiles == 2) {
-                j = b >> 1;
-                return (b & 1) == 0;
+        if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        // The loading and the MMA warp run converged, with one elected lane issuing: the
+        // operands of a copy or an MMA are then the same in every lane, as the hardware
+        // wants them.
+        const bool leader = elect_one();
+        if (warp == C::kTiles * 4 + 1 && n > 0) {
+            // ------------------------------------------------------ the loading warp
+            const int ps = 1 << p.cache.log2_ps;
+            const int log2_bk = min(p.cache.log2_ps, 7);  // keys of a K load
+            const int bk = 1 << log2_bk, n_bk = kTcKeys >> log2_bk;
+            if (leader) {
+                tma_prefetch_map(&k_map);
+                tma_prefetch_map(&v_map);
+                mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(tiles * p.heads_per_tile * per) * D * 2u);
+                for (int i = 0; i < tiles; ++i)
+                    for (int cb = 0; cb < D / 64; ++cb)
+                        tma_load_3d(smem + i * C::kQBytes + cb * kTcRows * 128, &q_map, cb * 64,
+                                    t.head0, static_cast<int>(t.row0) + t.token0 + i * per, &q_full);
             }
-            if (b == 0 || ((b & 1) && (b + 1) / 2 < n)) {
-                j = (b + 1) / 2;
-                return true;
-            }
-            j = b == 2 * n - 1 ? n - 1 : (b - 2) / 2;
-            return false;
-        };
-        int j = 0, g = 0;
-        bool is_k = kind_of(0, j);
-        int page = n > 0 ? page_at(j) : -1;
-        for (int b = 0; b < 2 * n; ++b) {
-            int next_j = 0;
-            const bool next_k = b + 1 < 2 * n ? kind_of(b + 1, next_j) : false;
-            const int next_page = b + 1 < 2 * n ? page_at(next_j) : -1;
-            const int key0 = walk.tile(j) * kTcKeys;
-            const unsigned have = __ballot_sync(FULL_MASK, page >= 0);
-            if (is_k) {
-                if (page == -2 && blockIdx.y == 0 && p.err_count) atomicAdd(p.err_count, 1);
-                if (lane == 0) {
-                    unsigned blocks = 0;
-                    for (int i = 0; i < kTcKeys / 8; ++i)
-                        if ((have >> (i * 8 / bk)) & 1u) blocks |= 1u << i;
-                    descs[j % kDescs] = make_int2(key0, static_cast<int>(blocks));
-                    mbar_arrive(&desc_full[j % kDescs]);
+            __syncwarp();
+            // page of this lane's K load of tile j (lanes below n_bk); -1: not to be loaded,
+            // -2: out of range
+            auto page_at = [&](int j) -> int {
+                if (lane >= n_bk) return -1;
+                const int key = walk.tile(j) * kTcKeys + lane * bk;
+                if (key > t.p_last) return -1;
+                if (!(t.p_first - (key + bk - 1) < p.mask.window || key < p.mask.sinks)) return -1;
+                const int page = p.cache.page_of(t.slot, key);
+                return p.cache.page_ok(page) ? page : -2;
+            };
+            auto kind_of = [&](int b, int &j) -> bool {  // block b: true for K; its tile
+                if (C::kTiles == 2) {
+                    j = b >> 1;
+                    return (b & 1) == 0;
                 }
-            }
-            for (int s = 0; s < C::kSubs; ++s, ++g) {
-                const int slot = g % C::kSlots;
-                uint8_t *to = ring + slot * kSlotBytes;
-                if (g >= C::kSlots)
-                    wait_or_flag(&slot_empty[slot], ((g / C::kSlots) - 1) & 1, &sh_dead);
+                if (b == 0 || ((b & 1) && (b + 1) / 2 < n)) {
+                    j = (b + 1) / 2;
+                    return true;
+                }
+                j = b == 2 * n - 1 ? n - 1 : (b - 2) / 2;
+                return false;
+            };
+            int j, g = 0;
+            bool is_k = kind_of(0, j);
+            int page = page_at(j);
+            for (int b = 0; b < 2 * n; ++b) {
+                int next_j = 0;
+                const bool next_k = b + 1 < 2 * n && kind_of(b + 1, next_j);
+                const int next_page = b + 1 < 2 * n ? page_at(next_j) : -1;
+                const int key0 = walk.tile(j) * kTcKeys;
+                const unsigned have = __ballot_sync(FULL_MASK, page >= 0);
                 if (is_k) {
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(&slot_full[slot], static_cast<uint32_t>(__popc(have) * bk) * 128u);
+                    if (page == -2 && blockIdx.y == 0 && p.err_count) atomicAdd(p.err_count, 1);
+                    if (leader) {
+                        unsigned blocks = 0;
+                        for (int i = 0; i < kTcKeys / 8; ++i)
+                            if ((have >> ((i * 8) >> log2_bk)) & 1u) blocks |= 1u << i;
+                        descs[j % kDescs] = make_int2(key0, static_cast<int>(blocks));
+                        mbar_arrive(&desc_full[j % kDescs]);
+                    }
                     __syncwarp();
-                    if (page >= 0)
-                        tma_load_2d(to + lane * bk * 128, &k_map, s * 64,
-                                    (page * p.cache.n_kv_heads + t.kvh) * ps + (key0 & (ps - 1)),
-                                    &slot_full[slot]);
-                } else {
-                    const int off = s * C::kVKeys + lane * bv;  // this lane's keys of the tile
-                    const int pg = __shfl_sync(FULL_MASK, page, (off / bk) & 31);
-                    const bool mine = lane < n_bv && pg >= 0;
-                    const unsigned loads = __popc(__ballot_sync(FULL_MASK, mine));
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(&slot_full[slot], loads * static_cast<uint32_t>(bv) * D * 2u);
-                    __syncwarp();
-                    if (mine) {
-                        const int row = (pg * p.cache.n_kv_heads + t.kvh) * ps + ((key0 + off) & (ps - 1));
-#pragma unroll
-                        for (int cb = 0; cb < D / 64; ++cb)
-                            tma_load_2d(to + (cb * C::kVKeys + lane * bv) * 128, &v_map, cb * 64, row,
-                                        &slot_full[slot]);
+                }
+                const int row = (page * p.cache.n_kv_heads + t.kvh) * ps + (key0 & (ps - 1));
+                for (int s = 0; s < C::kSubs; ++s, ++g) {
+                    const int slot = g % kSlots;
+                    uint8_t *to = ring + slot * kSlotBytes;
+                    if (g >= kSlots) wait_or_flag(&slot_empty[slot], ((g / kSlots) - 1) & 1, &sh_dead);
+                    if (is_k) {
+                        if (leader)
+                            mbar_arrive_expect_tx(&slot_full[slot], static_cast<uint32_t>(__popc(have)) << (log2_bk + 7));
+                        __syncwarp();
+                        for (int i = 0; i < n_bk; ++i) {
+                            const int r = __shfl_sync(FULL_MASK, row, i);
+                            if (leader && ((have >> i) & 1u))
+                                tma_load_3d(to + (i << (log2_bk + 7)), &k_map, 0, r, s, &slot_full[slot]);
+                        }
+                    } else {
+                        // the loads of this slot's keys, from the pages of the K loads they lie in
+                        const int i0 = s << (C::kLog2VKeys - log2_bv), i1 = (s + 1) << (C::kLog2VKeys - log2_bv);
+                        int loads = 0;
+                        for (int i = i0; i < i1; ++i) loads += (have >> ((i << log2_bv) >> log2_bk)) & 1u;
+                        if (leader)
+                            mbar_arrive_expect_tx(&slot_full[slot], static_cast<uint32_t>(loads) * bv * D * 2u);
+                        __syncwarp();
+                        for (int i = i0; i < i1; ++i) {
+                            const int k = (i << log2_bv) >> log2_bk;
+                            const int r = __shfl_sync(FULL_MASK, row, k) + ((i << log2_bv) & (bk - 1));
+                            if (leader && ((have >> k) & 1u))
+                                tma_load_3d(to + (i - i0) * (bv * D * 2), &v_map, 0, r, 0, &slot_full[slot]);
+                        }
                     }
                 }
+                is_k = next_k;
+                j = next_j;
+                page = next_page;
             }
-            is_k = next_k;
-            j = next_j;
-            page = next_page;
-        }
-    } else if (warp == C::kTiles * 4) {
-        // ---------------------------------------------------------- the MMA warp
-        if (lane == 0 && n > 0) {
+        } else if (warp == C::kTiles * 4 && n > 0) {
+            // ------------------------------------------------------ the MMA warp
             wait_or_flag(&q_full, 0, &sh_dead);
-            auto slot_of = [&](int block, int s, uint32_t &parity) {
-                const int g = block * C::kSubs + s;
-                parity = (g / C::kSlots) & 1;
-                return g % C::kSlots;
-            };
+            const uint64_t q_desc = tc::smem_desc_sw128(smem_addr(smem));
+            const uint64_t k_desc = tc::smem_desc_sw128(smem_addr(ring));
+            // V lies page by page, every page's 128-byte columns one behind the other: 16 keys
+            // are two groups of 8 rows, in one page (bv >= 16) or in two
+            const uint64_t v_desc = tc::smem_desc_sw128_mn(smem_addr(ring), bv * 128, bv >= 16 ? 1024 : D * 16);
+            uint32_t v_step[C::kVKeys / 16];
+#pragma unroll
+            for (int x = 0; x < C::kVKeys / 16; ++x)
+                v_step[x] = (((x * 16) >> log2_bv) * (bv * D * 2) + ((x * 16) & (bv - 1)) * 128) >> 4;
             // S of row tile i over key tile j
             auto issue_s = [&](int i, int j, bool release) {
                 const int buf = C::kBufs == 2 ? j & 1 : i;
-                const uint32_t q = smem_addr(smem + i * C::kQBytes);
+                const uint32_t to = tmem + C::kS + buf * kTcKeys;
 #pragma unroll
                 for (int s = 0; s < C::kSubs; ++s) {
-                    uint32_t parity;
-                    const int slot = slot_of(k_block<D>(j), s, parity);
-                    wait_or_flag(&slot_full[slot], parity, &sh_dead);
+                    const int g = k_block<D>(j) * C::kSubs + s, slot = g % kSlots;
+                    wait_or_flag(&slot_full[slot], (g / kSlots) & 1, &sh_dead);
                     tc::fence_after_sync();
-                    const uint32_t k = smem_addr(ring + slot * kSlotBytes);
+                    if (leader) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        tc::mma_bf16(tmem + C::kS + buf * kTcKeys,
-                                     tc::smem_desc_sw128(q + s * kTcRows * 128 + x * 32),
-                                     tc::smem_desc_sw128(k + x * 32), kIdescS, s + x > 0);
-                    if (release) tc::mma_commit(&slot_empty[slot]);
+                        for (int x = 0; x < 4; ++x)
+                            tc::mma_bf16(to, q_desc + ((i * C::kQBytes + s * kTcRows * 128 + x * 32) >> 4),
+                                         k_desc + slot * (kSlotBytes >> 4) + x * 2, kIdescS, s + x > 0);
+                        if (release) tc::mma_commit(&slot_empty[slot]);
+                    }
+                    __syncwarp();
                 }
-                tc::mma_commit(&s_full[buf]);
+                if (leader) tc::mma_commit(&s_full[buf]);
+                __syncwarp();
             };
             // O of row tile i += P V over key tile j
             auto issue_o = [&](int i, int j, bool release) {
                 const int buf = C::kBufs == 2 ? j & 1 : i;
                 wait_or_flag(&p_ready[buf], (C::kBufs == 2 ? j >> 1 : j) & 1, &sh_dead);
-                tc::fence_after_sync();
 #pragma unroll
                 for (int s = 0; s < C::kSubs; ++s) {
-                    uint32_t parity;
-                    const int slot = slot_of(v_block<D>(j, n), s, parity);
-                    wait_or_flag(&slot_full[slot], parity, &sh_dead);
+                    const int g = v_block<D>(j, n) * C::kSubs + s, slot = g % kSlots;
+                    wait_or_flag(&slot_full[slot], (g / kSlots) & 1, &sh_dead);
                     tc::fence_after_sync();
-                    const uint32_t v = smem_addr(ring + slot * kSlotBytes);
+                    if (leader) {
 #pragma unroll
-                    for (int x = 0; x < C::kVKeys / 16; ++x)
-                        tc::mma_bf16_ts(tmem + C::kO + i * D,
-                                        tmem + C::kS + buf * kTcKeys + (s * C::kVKeys + x * 16) / 2,
-                                        tc::smem_desc_sw128_mn(v + x * 2048, C::kVKeys * 128), kIdescO,
-                                        j > 0 || s + x > 0);
-                    if (release) tc::mma_commit(&slot_empty[slot]);
+                        for (int x = 0; x < C::kVKeys / 16; ++x)
+                            tc::mma_bf16_ts(tmem + C::kO + i * D,
+                                            tmem + C::kS + buf * kTcKeys + (s * C::kVKeys + x * 16) / 2,
+                                            v_desc + slot * (kSlotBytes >> 4) + v_step[x], kIdescO,
+                                            j > 0 || s + x > 0);
+                        if (release) tc::mma_commit(&slot_empty[slot]);
+                    }
+                    __syncwarp();
                 }
-                tc::mma_commit(&o_done[i]);
+                if (leader) tc::mma_commit(&o_done[i]);
+                __syncwarp();
             };
-            if (C::kTiles == 2) {
+            if constexpr (C::kTiles == 2) {
                 if (n0 > 0) issue_s(0, 0, tiles == 1);
                 if (tiles == 2) issue_s(1, 0, true);
                 for (int j = 0; j < n; ++j) {
@@ -542,159 +567,174 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 }
             }
         }
-        __syncwarp();
-    }
     } else {
-    if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    if (warp / 4 < tiles) {
-        // ---------------------------------------------------------- softmax, one row a thread
-        const int i = warp / 4, row = threadIdx.x & 127;
-        const int my_n = i == 0 ? n0 : n;
-        const int token = i * per + row / p.heads_per_tile;
-        const int head = row % p.heads_per_tile;
-        const int pos = t.p_first + token;
-        const int p_first = t.p_first + i * per;                      // of the row tile
-        const int p_last = min(p_first + per - 1, t.p_last);
-        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const bool positive = p.scale_log2 > 0.0f;
-        const float mult = positive ? p.scale_log2 : 1.0f;
-        float m = -INFINITY, l = 0.0f;
-        for (int j = 0; j < my_n; ++j) {
-            const int buf = C::kBufs == 2 ? j & 1 : i;
-            const uint32_t s_addr = tmem + lanes + C::kS + buf * kTcKeys;
-            wait_or_flag(&desc_full[j % kDescs], (j / kDescs) & 1, &sh_dead);
-            const int2 desc = descs[j % kDescs];
-            const int key0 = desc.x;
-            const unsigned blocks = static_cast<unsigned>(desc.y);
-            // V rows that no row of the CTA sees are cleared, so that whatever the page holds
-            // there (an infinity, a NaN) cannot reach O through a weight of 0
-            const bool alive = blocks == 0xFFFFu && key0 + kTcKeys - 1 <= t.p_last &&
-                               (t.p_first - key0 < p.mask.window || key0 + kTcKeys <= p.mask.sinks);
-            wait_or_flag(&s_full[buf], (C::kBufs == 2 ? j >> 1 : j) & 1, &sh_dead);
-            tc::fence_after_sync();
-            if (!alive && (i == 0 || j >= n0)) {
-                // (two S buffers: once the O product before this tile's is complete, the
-                // ring slots of V are at most one phase from the one waited for)
+        if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        if (warp / 4 < tiles) {
+            // ------------------------------------------------------ softmax, one row a thread
+            const int i = warp / 4, row = threadIdx.x & 127;
+            const int my_n = i == 0 ? n0 : n;
+            const int token = i * per + row / p.heads_per_tile;
+            const int head = row % p.heads_per_tile;
+            const int pos = t.p_first + token;
+            const int p_first = t.p_first + i * per;  // of the row tile
+            const int p_last = min(p_first + per - 1, t.p_last);
+            const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+            const uint32_t o_addr = tmem + lanes + C::kO + i * D;
+            const bool positive = p.scale_log2 > 0.0f;
+            const float mult = positive ? p.scale_log2 : 1.0f;
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; j < my_n; ++j) {
+                const int buf = C::kBufs == 2 ? j & 1 : i;
+                const uint32_t s_addr = tmem + lanes + C::kS + buf * kTcKeys;
+                wait_or_flag(&desc_full[j % kDescs], (j / kDescs) & 1, &sh_dead);
+                const int2 desc = descs[j % kDescs];
+                const int key0 = desc.x;
+                const unsigned blocks = static_cast<unsigned>(desc.y);
+                // every row of the CTA, and of this row tile, sees every key of the tile
+                const bool alive = blocks == 0xFFFFu && key0 + kTcKeys - 1 <= t.p_last &&
+                                   (t.p_first - key0 < p.mask.window || key0 + kTcKeys <= p.mask.sinks);
+                const bool clean = blocks == 0xFFFFu && key0 + kTcKeys - 1 <= p_first &&
+                                   (p_last - key0 < p.mask.window || key0 + kTcKeys <= p.mask.sinks);
+                wait_or_flag(&s_full[buf], (C::kBufs == 2 ? j >> 1 : j) & 1, &sh_dead);
+                tc::fence_after_sync();
+                float s[128];
+                {
+                    uint32_t raw[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tc::tmem_ld32_nowait(s_addr + c * 32, raw[c]);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(raw[c >> 5][c & 31]);
+                }
+                if (!alive && (i == 0 || j >= n0)) {
+                    // V rows that no row of the CTA sees are cleared, so that whatever the page
+                    // holds there (an infinity, a NaN) cannot reach O through a weight of 0.
+                    // (Two S buffers: once the O product before this tile's is complete, the
+                    // ring slots of V are at most one phase from the one waited for.)
+                    if (C::kBufs == 2 && j > 0) wait_or_flag(&o_done[0], (j - 1) & 1, &sh_dead);
+                    const int key = key0 + row;
+                    const bool dead = !((blocks >> (row >> 3)) & 1u) || key > t.p_last ||
+                                      !(t.p_first - key < p.mask.window || key < p.mask.sinks);
+                    for (int y = 0; y < C::kSubs; ++y) {
+                        const int g = v_block<D>(j, n) * C::kSubs + y, slot = g % kSlots;
+                        wait_or_flag(&slot_full[slot], (g / kSlots) & 1, &sh_dead);
+                        if (dead && (row >> C::kLog2VKeys) == y) {
+                            const int r = row & (C::kVKeys - 1);
+                            uint8_t *at = ring + slot * kSlotBytes + (r >> log2_bv) * (bv * D * 2) + (r & (bv - 1)) * 128;
+                            for (int x = 0; x < D / 8; ++x)
+                                *reinterpret_cast<uint4 *>(at + (x >> 3) * bv * 128 + (x & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                if (!positive) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) s[c] *= p.scale_log2;
+                }
+                if (!clean) {
+                    // the keys this row sees: from its window's first to itself, and the sinks
+                    const int hi = pos - key0 + 1;
+                    const int lo = pos - key0 < p.mask.window ? 0 : pos - p.mask.window + 1 - key0;
+                    const int sink = min(p.mask.sinks - key0, hi);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t see = bits_between(lo - 32 * w, hi - 32 * w) | bits_between(0, sink - 32 * w);
+                        uint32_t there = 0;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if ((blocks >> (4 * w + x)) & 1u) there |= 0xFFu << (8 * x);
+                        see &= there;
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!(see & (1u << c))) s[32 * w + c] = -INFINITY;
+                    }
+                }
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 128; c += 8)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) top[x] = fmaxf(fmaxf(top[x], s[c + 2 * x]), s[c + 2 * x + 1]);
+                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                if (j == 0) {
+                    m = mx;
+                } else {
+                    const bool grow = (mx - m) * mult > kLazy;
+                    if (__any_sync(FULL_MASK, grow)) {
+                        // O is complete up to the tile before: S of this tile was issued after
+                        // it (two S buffers: after the one before that)
+                        if (C::kBufs == 2) {
+                            wait_or_flag(&o_done[0], (j - 1) & 1, &sh_dead);
+                            tc::fence_after_sync();
+                        }
+                        const float f = grow ? fast_exp2((m - mx) * mult) : 1.0f;
+                        if (grow) m = mx;
+                        l *= f;
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tc::tmem_ld32_nowait(o_addr + c, o);
+                            tc::tmem_ld_wait();
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                            tc::tmem_st32(o_addr + c, o);
+                        }
+                    }
+                }
+                const float base = m == -INFINITY ? 0.0f : m * mult;
+                const float2 mul2 = make_float2(mult, mult), sub2 = make_float2(-base, -base);
+                float2 sum[4] = {};
+#pragma unroll
+                for (int c = 0; c < 128; c += 64) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        float2 a = __ffma2_rn(make_float2(s[c + 2 * x], s[c + 2 * x + 1]), mul2, sub2);
+                        a.x = fast_exp2(a.x);
+                        a.y = fast_exp2(a.y);
+                        sum[x & 3] = __fadd2_rn(sum[x & 3], a);
+                        w[x] = Elem<T>::pack(a.x, a.y);
+                    }
+                    tc::tmem_st32(s_addr + c / 2, w);
+                }
+                sum[0] = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+                l += sum[0].x + sum[0].y;
+                tc::tmem_st_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                // keeps this thread at most one phase behind o_done
                 if (C::kBufs == 2 && j > 0) wait_or_flag(&o_done[0], (j - 1) & 1, &sh_dead);
-                const int key = key0 + row;
-                const bool dead = !((blocks >> (row >> 3)) & 1u) || key > t.p_last ||
-                                  !(t.p_first - key < p.mask.window || key < p.mask.sinks);
-#pragma unroll
-                for (int s = 0; s < C::kSubs; ++s) {
-                    const int g = v_block<D>(j, n) * C::kSubs + s;
-                    wait_or_flag(&slot_full[g % C::kSlots], (g / C::kSlots) & 1, &sh_dead);
-                    if (dead && row / C::kVKeys == s) {
-                        uint8_t *at = ring + (g % C::kSlots) * kSlotBytes + (row % C::kVKeys) * 128;
-                        for (int x = 0; x < D / 8; ++x)
-                            *reinterpret_cast<uint4 *>(at + (x >> 3) * C::kVKeys * 128 + (x & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
-                    }
-                }
-                fence_proxy_async_smem();
+                if (lane == 0) mbar_arrive(&p_ready[buf]);
             }
-            uint32_t raw[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tc::tmem_ld32_nowait(s_addr + c * 32, raw[c]);
-            tc::tmem_ld_wait();
-            float s[128];
-#pragma unroll
-            for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(raw[c >> 5][c & 31]);
-            if (!positive) {
-#pragma unroll
-                for (int c = 0; c < 128; ++c) s[c] *= p.scale_log2;
-            }
-            const bool clean = blocks == 0xFFFFu && key0 + kTcKeys - 1 <= p_first &&
-                               (p_last - key0 < p.mask.window || key0 + kTcKeys <= p.mask.sinks);
-            if (!clean) {
-#pragma unroll
-                for (int c = 0; c < 128; ++c) {
-                    const bool ok = ((blocks >> (c >> 3)) & 1u) && p.mask.sees(pos, key0 + c);
-                    if (!ok) s[c] = -INFINITY;
-                }
-            }
-            float top[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-            for (int c = 4; c < 128; ++c) top[c & 3] = fmaxf(top[c & 3], s[c]);
-            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-            if (j == 0) {
-                m = mx;
-            } else {
-                const bool grow = (mx - m) * mult > kLazy;
-                if (__any_sync(FULL_MASK, grow)) {
-                    // O is complete up to the tile before: S of this tile was issued after it
-                    // (two S buffers: after the one before that, so its own arrival is awaited)
-                    if (C::kBufs == 2) {
-                        wait_or_flag(&o_done[0], (j - 1) & 1, &sh_dead);
-                        tc::fence_after_sync();
-                    }
-                    const float f = grow ? fast_exp2((m - mx) * mult) : 1.0f;
-                    if (grow) m = mx;
-                    l *= f;
-#pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tc::tmem_ld32_nowait(tmem + lanes + C::kO + i * D + c, o);
-                        tc::tmem_ld_wait();
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                        tc::tmem_st32(tmem + lanes + C::kO + i * D + c, o);
-                    }
-                }
-            }
-            const float base = m == -INFINITY ? 0.0f : m * mult;
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int c = 0; c < 128; c += 64) {
-                uint32_t w[32];
-#pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    const float a = fast_exp2(fmaf(s[c + 2 * x], mult, -base));
-                    const float b = fast_exp2(fmaf(s[c + 2 * x + 1], mult, -base));
-                    sum[(2 * x) & 3] += a;
-                    sum[(2 * x + 1) & 3] += b;
-                    w[x] = Elem<T>::pack(a, b);
-                }
-                tc::tmem_st32(s_addr + c / 2, w);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tc::tmem_st_wait();
-            tc::fence_before_sync();
-            __syncwarp();
-            // keeps this thread at most one phase behind o_done
-            if (C::kBufs == 2 && j > 0) wait_or_flag(&o_done[0], (j - 1) & 1, &sh_dead);
-            if (lane == 0) mbar_arrive(&p_ready[buf]);
-        }
-        // ---------------------------------------------------------- O out
-        T *out = static_cast<T *>(p.out) +
-                 ((t.row0 + t.token0 + token) * p.n_q_heads + t.head0 + head) * D;
-        const bool mine = token < t.tokens && row / p.heads_per_tile < per && head < t.heads;
-        if (my_n > 0) {
-            wait_or_flag(&o_done[i], (my_n - 1) & 1, &sh_dead);
-            tc::fence_after_sync();
-        }
-        const float inv = 1.0f / l;
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
+            // ------------------------------------------------------ O out
+            T *out = static_cast<T *>(p.out) +
+                     ((t.row0 + t.token0 + token) * p.n_q_heads + t.head0 + head) * D;
+            const bool mine = token < t.tokens && row / p.heads_per_tile < per && head < t.heads;
             if (my_n > 0) {
-                tc::tmem_ld32_nowait(tmem + lanes + C::kO + i * D + c, o);
-                tc::tmem_ld_wait();
+                wait_or_flag(&o_done[i], (my_n - 1) & 1, &sh_dead);
+                tc::fence_after_sync();
             }
-            if (mine && !sh_dead) {
+            const float inv = 1.0f / l;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tc::tmem_ld32_nowait(o_addr + c, o);
+                tc::tmem_ld_wait();
+                if (mine && !sh_dead) {
 #pragma unroll
-                for (int x = 0; x < 32; x += 8) {
-                    uint32_t w[4];
+                    for (int x = 0; x < 32; x += 8) {
+                        uint32_t w[4];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        w[y] = l == 0.0f ? 0u
-                                         : Elem<T>::pack(__uint_as_float(o[x + 2 * y]) * inv,
-                                                         __uint_as_float(o[x + 2 * y + 1]) * inv);
-                    *reinterpret_cast<uint4 *>(out + c + x) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int y = 0; y < 4; ++y)
+                            w[y] = l == 0.0f ? 0u
+                                             : Elem<T>::pack(__uint_as_float(o[x + 2 * y]) * inv,
+                                                             __uint_as_float(o[x + 2 * y + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(out + c + x) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
                 }
             }
+            tc::fence_before_sync();
         }
-        tc::fence_before_sync();
-    }
     }
     __syncthreads();
     if (warp == C::kTiles * 4) {
@@ -719,8 +759,9 @@ gdn_status launch_tc(PrefillParams p, int dtype, cudaStream_t s) {
     const uint64_t rows = static_cast<uint64_t>(p.cache.n_pages) * p.cache.n_kv_heads * ps;
     GDN_TRY(encode_heads_map(&q_map, p.q, dtype, D, p.n_q_heads, static_cast<uint64_t>(p.seqs.total),
                              static_cast<uint64_t>(p.q_stride) * 2, p.heads_per_tile, per));
-    GDN_TRY(encode_rows_map(&k_map, p.k_pages, dtype, D, rows, D * 2, ps < kTcKeys ? ps : kTcKeys));
-    GDN_TRY(encode_rows_map(&v_map, p.v_pages, dtype, D, rows, D * 2, ps < C::kVKeys ? ps : C::kVKeys));
+    GDN_TRY(encode_blocks_map(&k_map, p.k_pages, dtype, D, rows, D * 2, ps < kTcKeys ? ps : kTcKeys, 1));
+    GDN_TRY(encode_blocks_map(&v_map, p.v_pages, dtype, D, rows, D * 2, ps < C::kVKeys ? ps : C::kVKeys,
+                              D / 64));
     auto kernel = attn_prefill_tc_kernel<T, D>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
         return GDN_ERR_LAUNCH;

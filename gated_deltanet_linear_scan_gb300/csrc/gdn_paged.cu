@@ -54,6 +54,16 @@ gdn_status encode_rows_map(CUtensorMap *map, const void *base, int dtype, int co
     return encode(map, base, dtype, 2, dims, strides, box);
 }
 
+gdn_status encode_blocks_map(CUtensorMap *map, const void *base, int dtype, int cols, uint64_t rows,
+                             uint64_t row_bytes, int box_rows, int box_blocks) {
+    const int per = 128 / dtype_bytes(dtype);
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(per), rows, static_cast<cuuint64_t>(cols / per)};
+    const cuuint64_t strides[2] = {row_bytes, 128};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(per), static_cast<cuuint32_t>(box_rows),
+                               static_cast<cuuint32_t>(box_blocks)};
+    return encode(map, base, dtype, 3, dims, strides, box);
+}
+
 gdn_status encode_heads_map(CUtensorMap *map, const void *base, int dtype, int cols, int heads,
                             uint64_t tokens, uint64_t token_bytes, int box_heads, int box_tokens) {
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(heads),

@@ -145,6 +145,11 @@ constexpr float kLog2E = 1.4426950408889634f;
 gdn_status encode_rows_map(CUtensorMap *map, const void *base, int dtype, int cols, uint64_t rows,
                            uint64_t row_bytes, int box_rows);
 
+// The same rows seen as [cols / box columns][rows][128 bytes], loaded in boxes of box_blocks x
+// box_rows x 128 bytes: the 128-byte columns of a few rows, one behind the other.
+gdn_status encode_blocks_map(CUtensorMap *map, const void *base, int dtype, int cols, uint64_t rows,
+                             uint64_t row_bytes, int box_rows, int box_blocks);
+
 // 3-D: [tokens][heads][cols], loaded in boxes of box_tokens x box_heads x 128 bytes (box row
 // t * box_heads + h), same swizzle.
 gdn_status encode_heads_map(CUtensorMap *map, const void *base, int dtype, int cols, int heads,

@@ -67,11 +67,11 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t start) {
 }
 
 // MN-major: rows are K indices, the 64 elements run along N; `block` bytes lie between one
-// block of 64 N elements and the next, a K step of 16 rows advances the address by 2048.
-__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t start, uint32_t block) {
+// block of 64 N elements and the next, `group` between one group of 8 rows and the next.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t start, uint32_t block, uint32_t group) {
     return static_cast<uint64_t>((start & 0x3FFFFu) >> 4) |
            static_cast<uint64_t>((block >> 4) & 0x3FFFu) << 16 |
-           static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 |
+           static_cast<uint64_t>((group >> 4) & 0x3FFFu) << 32 | static_cast<uint64_t>(1) << 46 |
            static_cast<uint64_t>(2) << 61;
 }
 
