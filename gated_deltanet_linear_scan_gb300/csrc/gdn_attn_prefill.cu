@@ -286,40 +286,31 @@ gdn_status launch_simt_dim(int d, const PrefillParams &p, cudaStream_t s) {
 // memory, so there is one row tile and two S buffers: S of the next key tile is computed
 // during the softmax of this one.
 //
-// K and V stream through a ring of 16 KB slots (128 keys x 64 dimensions of K; all
-// dimensions of 16 KB / row bytes keys of V), loaded page by page by one warp. A V slot keeps
-// the pages' rows apart ([page][128-byte column][row]), so that one copy brings all of a
-// page's columns; the MMA's descriptor strides say where they lie.
+// K and V stream through two rings of slots, each fed by a warp of its own (one warp's copies,
+// barriers and page lookups would take longer than the products: a copy costs its warp about
+// 60 cycles, a barrier 30 to 60). Pages are loaded one by one; a V slot keeps their rows apart
+// ([page][128-byte column][row]), so that one copy brings all of a page's columns, and the
+// MMA's descriptor strides say where they lie.
 constexpr int kTcKeys = 128;
 constexpr int kTcRows = 128;
-constexpr int kSlotBytes = 16384;
-constexpr int kSlots = 8;
 constexpr int kDescs = 8;
 constexpr float kLazy = 8.0f;  // log2 of the growth of a maximum that makes O rescale
 
 template <int D>
 struct Tc {
     static constexpr int kTiles = D == 256 ? 1 : 2;
-    static constexpr int kBufs = D == 256 ? 2 : 1;          // S buffers of a row tile
-    static constexpr int kSubs = D / 64;                    // slots of a K (or V) tile
-    static constexpr int kVKeys = kSlotBytes / (2 * D);     // keys of a V slot
-    static constexpr int kLog2VKeys = D == 64 ? 7 : D == 128 ? 6 : 5;
-    static constexpr int kQBytes = kTcRows * D * 2;         // of a row tile
-    static constexpr int kSmem = kTiles * kQBytes + kSlots * kSlotBytes + 1024;
-    static constexpr int kThreads = kTiles * 128 + 128;      // softmax; MMA, loads and two idle warps
-    static constexpr int kS = 0, kO = 256;                  // tensor-memory columns
+    static constexpr int kBufs = D == 256 ? 2 : 1;              // S buffers of a row tile
+    static constexpr int kSubs = D == 256 ? 2 : 1;              // slots of a K (or V) tile
+    static constexpr int kSlots = D == 64 ? 4 : 2;              // of each ring
+    static constexpr int kSlotBytes = kTcKeys * D * 2 / kSubs;
+    static constexpr int kCols = D / 64 / kSubs;                // 128-byte columns of a K slot
+    static constexpr int kVKeys = kTcKeys / kSubs;              // keys of a V slot
+    static constexpr int kLog2VKeys = kSubs == 2 ? 6 : 7;
+    static constexpr int kQBytes = kTcRows * D * 2;             // of a row tile
+    static constexpr int kSmem = kTiles * kQBytes + 2 * kSlots * kSlotBytes + 1024;
+    static constexpr int kThreads = kTiles * 128 + 128;         // softmax; MMA, K, V, an idle warp
+    static constexpr int kS = 0, kO = 256;                      // tensor-memory columns
 };
-
-// Where K and V tile j stand in the order of loading and use, of n tiles. Two row tiles:
-// K0 V0 K1 V1 .. ; one row tile with two S buffers: K0 K1 V0 K2 V1 .. V(n-1).
-template <int D>
-__device__ __forceinline__ int k_block(int j) {
-    return Tc<D>::kTiles == 2 ? 2 * j : (j == 0 ? 0 : 2 * j - 1);
-}
-template <int D>
-__device__ __forceinline__ int v_block(int j, int n) {
-    return Tc<D>::kTiles == 2 ? 2 * j + 1 : (j == n - 1 ? 2 * n - 1 : 2 * j + 2);
-}
 
 // Bounded wait; once one gave up, the CTA's later waits return at once and none of its rows
 // are written.
@@ -350,8 +341,10 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     extern __shared__ uint8_t dyn[];
     uint8_t *smem =
         reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
-    uint8_t *ring = smem + C::kTiles * C::kQBytes;
-    __shared__ __align__(8) uint64_t slot_full[kSlots], slot_empty[kSlots];
+    uint8_t *k_ring = smem + C::kTiles * C::kQBytes;
+    uint8_t *v_ring = k_ring + C::kSlots * C::kSlotBytes;
+    __shared__ __align__(8) uint64_t k_full[C::kSlots], k_empty[C::kSlots];
+    __shared__ __align__(8) uint64_t v_full[C::kSlots], v_empty[C::kSlots];
     __shared__ __align__(8) uint64_t q_full, s_full[2], p_ready[2], o_done[2], desc_full[kDescs];
     __shared__ int2 descs[kDescs];  // first key and loaded 8-key blocks of a key tile
     __shared__ uint32_t tmem_base;
@@ -371,9 +364,11 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     const int bv = 1 << log2_bv;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&slot_full[i], 1);
-            mbar_init(&slot_empty[i], 1);
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 1);
         }
         for (int i = 0; i < kDescs; ++i) mbar_init(&desc_full[i], 1);
         for (int i = 0; i < 2; ++i) {
@@ -399,14 +394,22 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         // operands of a copy or an MMA are then the same in every lane, as the hardware
         // wants them.
         const bool leader = elect_one();
+        const int ps = 1 << p.cache.log2_ps;
+        const int log2_bk = min(p.cache.log2_ps, 7);  // keys of a page's part of a key tile
+        const int bk = 1 << log2_bk, n_bk = kTcKeys >> log2_bk;
+        // The page of lane i's part of key tile j, or -1 for a part that nobody sees (its id
+        // is not read: pages before the window may be gone).
+        auto page_at = [&](int j) -> int {
+            if (lane >= n_bk) return -1;
+            const int key = walk.tile(j) * kTcKeys + lane * bk;
+            if (key > t.p_last) return -1;
+            if (!(t.p_first - (key + bk - 1) < p.mask.window || key < p.mask.sinks)) return -1;
+            return p.cache.page_of(t.slot, key);
+        };
         if (warp == C::kTiles * 4 + 1 && n > 0) {
-            // ------------------------------------------------------ the loading warp
-            const int ps = 1 << p.cache.log2_ps;
-            const int log2_bk = min(p.cache.log2_ps, 7);  // keys of a K load
-            const int bk = 1 << log2_bk, n_bk = kTcKeys >> log2_bk;
+            // ------------------------------------------------------ the K warp
             if (leader) {
                 tma_prefetch_map(&k_map);
-                tma_prefetch_map(&v_map);
                 mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(tiles * p.heads_per_tile * per) * D * 2u);
                 for (int i = 0; i < tiles; ++i)
                     for (int cb = 0; cb < D / 64; ++cb)
@@ -414,90 +417,94 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                                     t.head0, static_cast<int>(t.row0) + t.token0 + i * per, &q_full);
             }
             __syncwarp();
-            // page of this lane's K load of tile j (lanes below n_bk); -1: not to be loaded,
-            // -2: out of range
-            auto page_at = [&](int j) -> int {
-                if (lane >= n_bk) return -1;
-                const int key = walk.tile(j) * kTcKeys + lane * bk;
-                if (key > t.p_last) return -1;
-                if (!(t.p_first - (key + bk - 1) < p.mask.window || key < p.mask.sinks)) return -1;
-                const int page = p.cache.page_of(t.slot, key);
-                return p.cache.page_ok(page) ? page : -2;
-            };
-            auto kind_of = [&](int b, int &j) -> bool {  // block b: true for K; its tile
-                if (C::kTiles == 2) {
-                    j = b >> 1;
-                    return (b & 1) == 0;
-                }
-                if (b == 0 || ((b & 1) && (b + 1) / 2 < n)) {
-                    j = (b + 1) / 2;
-                    return true;
-                }
-                j = b == 2 * n - 1 ? n - 1 : (b - 2) / 2;
-                return false;
-            };
-            int j, g = 0;
-            bool is_k = kind_of(0, j);
-            int page = page_at(j);
-            for (int b = 0; b < 2 * n; ++b) {
-                int next_j = 0;
-                const bool next_k = b + 1 < 2 * n && kind_of(b + 1, next_j);
-                const int next_page = b + 1 < 2 * n ? page_at(next_j) : -1;
+            int page = page_at(0), slot = 0, round = 0;
+            for (int j = 0; j < n; ++j) {
+                const int next_page = j + 1 < n ? page_at(j + 1) : -1;
                 const int key0 = walk.tile(j) * kTcKeys;
-                const unsigned have = __ballot_sync(FULL_MASK, page >= 0);
-                if (is_k) {
-                    if (page == -2 && blockIdx.y == 0 && p.err_count) atomicAdd(p.err_count, 1);
-                    if (leader) {
-                        unsigned blocks = 0;
-                        for (int i = 0; i < kTcKeys / 8; ++i)
-                            if ((have >> ((i * 8) >> log2_bk)) & 1u) blocks |= 1u << i;
-                        descs[j % kDescs] = make_int2(key0, static_cast<int>(blocks));
-                        mbar_arrive(&desc_full[j % kDescs]);
-                    }
-                    __syncwarp();
+                const bool ok = p.cache.page_ok(page);
+                const unsigned have = __ballot_sync(FULL_MASK, ok);
+                if (!ok && blockIdx.y == 0 && p.err_count) {
+                    // a part that somebody sees, without a page
+                    const int key = key0 + lane * bk;
+                    if (lane < n_bk && key <= t.p_last &&
+                        (t.p_first - (key + bk - 1) < p.mask.window || key < p.mask.sinks))
+                        atomicAdd(p.err_count, 1);
                 }
                 const int row = (page * p.cache.n_kv_heads + t.kvh) * ps + (key0 & (ps - 1));
-                for (int s = 0; s < C::kSubs; ++s, ++g) {
-                    const int slot = g % kSlots;
-                    uint8_t *to = ring + slot * kSlotBytes;
-                    if (g >= kSlots) wait_or_flag(&slot_empty[slot], ((g / kSlots) - 1) & 1, &sh_dead);
-                    if (is_k) {
-                        if (leader)
-                            mbar_arrive_expect_tx(&slot_full[slot], static_cast<uint32_t>(__popc(have)) << (log2_bk + 7));
-                        __syncwarp();
+                if (leader) {
+                    unsigned blocks = 0;
+                    for (int i = 0; i < kTcKeys / 8; ++i)
+                        if ((have >> ((i * 8) >> log2_bk)) & 1u) blocks |= 1u << i;
+                    descs[j % kDescs] = make_int2(key0, static_cast<int>(blocks));
+                    mbar_arrive(&desc_full[j % kDescs]);
+                }
+                __syncwarp();
+                for (int s = 0; s < C::kSubs; ++s) {
+                    if (round > 0) wait_or_flag(&k_empty[slot], (round - 1) & 1, &sh_dead);
+                    uint8_t *to = k_ring + slot * C::kSlotBytes;
+                    if (leader)
+                        mbar_arrive_expect_tx(&k_full[slot], (static_cast<uint32_t>(__popc(have)) << (log2_bk + 7)) * C::kCols);
+                    if (n_bk == 1) {  // one page: its columns in one copy
+                        const int r = __shfl_sync(FULL_MASK, row, 0);
+                        if (leader && have) tma_load_3d(to, &k_map, 0, r, s * C::kCols, &k_full[slot]);
+                    } else {
                         for (int i = 0; i < n_bk; ++i) {
                             const int r = __shfl_sync(FULL_MASK, row, i);
-                            if (leader && ((have >> i) & 1u))
-                                tma_load_3d(to + (i << (log2_bk + 7)), &k_map, 0, r, s, &slot_full[slot]);
-                        }
-                    } else {
-                        // the loads of this slot's keys, from the pages of the K loads they lie in
-                        const int i0 = s << (C::kLog2VKeys - log2_bv), i1 = (s + 1) << (C::kLog2VKeys - log2_bv);
-                        int loads = 0;
-                        for (int i = i0; i < i1; ++i) loads += (have >> ((i << log2_bv) >> log2_bk)) & 1u;
-                        if (leader)
-                            mbar_arrive_expect_tx(&slot_full[slot], static_cast<uint32_t>(loads) * bv * D * 2u);
-                        __syncwarp();
-                        for (int i = i0; i < i1; ++i) {
-                            const int k = (i << log2_bv) >> log2_bk;
-                            const int r = __shfl_sync(FULL_MASK, row, k) + ((i << log2_bv) & (bk - 1));
-                            if (leader && ((have >> k) & 1u))
-                                tma_load_3d(to + (i - i0) * (bv * D * 2), &v_map, 0, r, 0, &slot_full[slot]);
+                            if (leader && ((have >> i) & 1u)) {
+#pragma unroll
+                                for (int c = 0; c < C::kCols; ++c)
+                                    tma_load_3d(to + c * kTcKeys * 128 + (i << (log2_bk + 7)), &k_map, 0, r,
+                                                s * C::kCols + c, &k_full[slot]);
+                            }
                         }
                     }
+                    __syncwarp();
+                    if (++slot == C::kSlots) {
+                        slot = 0;
+                        ++round;
+                    }
                 }
-                is_k = next_k;
-                j = next_j;
+                page = next_page;
+            }
+        } else if (warp == C::kTiles * 4 + 2 && n > 0) {
+            // ------------------------------------------------------ the V warp
+            if (leader) tma_prefetch_map(&v_map);
+            int page = page_at(0), slot = 0, round = 0;
+            for (int j = 0; j < n; ++j) {
+                const int next_page = j + 1 < n ? page_at(j + 1) : -1;
+                const int key0 = walk.tile(j) * kTcKeys;
+                const unsigned have = __ballot_sync(FULL_MASK, p.cache.page_ok(page));
+                const int row = (page * p.cache.n_kv_heads + t.kvh) * ps + (key0 & (ps - 1));
+                for (int s = 0; s < C::kSubs; ++s) {
+                    if (round > 0) wait_or_flag(&v_empty[slot], (round - 1) & 1, &sh_dead);
+                    uint8_t *to = v_ring + slot * C::kSlotBytes;
+                    // this slot's copies of bv keys, from the parts they lie in
+                    const int i0 = s << (C::kLog2VKeys - log2_bv), i1 = (s + 1) << (C::kLog2VKeys - log2_bv);
+                    const bool here = lane >= i0 && lane < i1 && ((have >> ((lane << log2_bv) >> log2_bk)) & 1u);
+                    const unsigned loads = __popc(__ballot_sync(FULL_MASK, here));
+                    if (leader) mbar_arrive_expect_tx(&v_full[slot], loads * static_cast<uint32_t>(bv) * D * 2u);
+                    for (int i = i0; i < i1; ++i) {
+                        const int part = (i << log2_bv) >> log2_bk;
+                        const int r = __shfl_sync(FULL_MASK, row, part) + ((i << log2_bv) & (bk - 1));
+                        if (leader && ((have >> part) & 1u))
+                            tma_load_3d(to + (i - i0) * (bv * D * 2), &v_map, 0, r, 0, &v_full[slot]);
+                    }
+                    __syncwarp();
+                    if (++slot == C::kSlots) {
+                        slot = 0;
+                        ++round;
+                    }
+                }
                 page = next_page;
             }
         } else if (warp == C::kTiles * 4 && n > 0) {
             // ------------------------------------------------------ the MMA warp
             wait_or_flag(&q_full, 0, &sh_dead);
             const uint64_t q_desc = tc::smem_desc_sw128(smem_addr(smem));
-            const uint64_t k_desc = tc::smem_desc_sw128(smem_addr(ring));
+            const uint64_t k_desc = tc::smem_desc_sw128(smem_addr(k_ring));
             // V lies page by page, every page's 128-byte columns one behind the other: 16 keys
             // are two groups of 8 rows, in one page (bv >= 16) or in two
-            const uint64_t v_desc = tc::smem_desc_sw128_mn(smem_addr(ring), bv * 128, bv >= 16 ? 1024 : D * 16);
+            const uint64_t v_desc = tc::smem_desc_sw128_mn(smem_addr(v_ring), bv * 128, bv >= 16 ? 1024 : D * 16);
             uint32_t v_step[C::kVKeys / 16];
 #pragma unroll
             for (int x = 0; x < C::kVKeys / 16; ++x)
@@ -508,20 +515,23 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 const uint32_t to = tmem + C::kS + buf * kTcKeys;
 #pragma unroll
                 for (int s = 0; s < C::kSubs; ++s) {
-                    const int g = k_block<D>(j) * C::kSubs + s, slot = g % kSlots;
-                    wait_or_flag(&slot_full[slot], (g / kSlots) & 1, &sh_dead);
+                    const int g = j * C::kSubs + s, slot = g % C::kSlots;
+                    wait_or_flag(&k_full[slot], (g / C::kSlots) & 1, &sh_dead);
                     tc::fence_after_sync();
                     if (leader) {
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            tc::mma_bf16(to, q_desc + ((i * C::kQBytes + s * kTcRows * 128 + x * 32) >> 4),
-                                         k_desc + slot * (kSlotBytes >> 4) + x * 2, kIdescS, s + x > 0);
-                        if (release) tc::mma_commit(&slot_empty[slot]);
+                        for (int c = 0; c < C::kCols; ++c)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                tc::mma_bf16(to,
+                                             q_desc + ((i * C::kQBytes + (s * C::kCols + c) * kTcRows * 128 + x * 32) >> 4),
+                                             k_desc + ((slot * C::kSlotBytes + c * kTcKeys * 128 + x * 32) >> 4),
+                                             kIdescS, s + c + x > 0);
+                        if (release) tc::mma_commit(&k_empty[slot]);
+                        if (s == C::kSubs - 1) tc::mma_commit(&s_full[buf]);
                     }
                     __syncwarp();
                 }
-                if (leader) tc::mma_commit(&s_full[buf]);
-                __syncwarp();
             };
             // O of row tile i += P V over key tile j
             auto issue_o = [&](int i, int j, bool release) {
@@ -529,22 +539,21 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 wait_or_flag(&p_ready[buf], (C::kBufs == 2 ? j >> 1 : j) & 1, &sh_dead);
 #pragma unroll
                 for (int s = 0; s < C::kSubs; ++s) {
-                    const int g = v_block<D>(j, n) * C::kSubs + s, slot = g % kSlots;
-                    wait_or_flag(&slot_full[slot], (g / kSlots) & 1, &sh_dead);
+                    const int g = j * C::kSubs + s, slot = g % C::kSlots;
+                    wait_or_flag(&v_full[slot], (g / C::kSlots) & 1, &sh_dead);
                     tc::fence_after_sync();
                     if (leader) {
 #pragma unroll
                         for (int x = 0; x < C::kVKeys / 16; ++x)
                             tc::mma_bf16_ts(tmem + C::kO + i * D,
                                             tmem + C::kS + buf * kTcKeys + (s * C::kVKeys + x * 16) / 2,
-                                            v_desc + slot * (kSlotBytes >> 4) + v_step[x], kIdescO,
+                                            v_desc + ((slot * C::kSlotBytes) >> 4) + v_step[x], kIdescO,
                                             j > 0 || s + x > 0);
-                        if (release) tc::mma_commit(&slot_empty[slot]);
+                        if (release) tc::mma_commit(&v_empty[slot]);
+                        if (s == C::kSubs - 1) tc::mma_commit(&o_done[i]);
                     }
                     __syncwarp();
                 }
-                if (leader) tc::mma_commit(&o_done[i]);
-                __syncwarp();
             };
             if constexpr (C::kTiles == 2) {
                 if (n0 > 0) issue_s(0, 0, tiles == 1);
@@ -616,11 +625,11 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                     const bool dead = !((blocks >> (row >> 3)) & 1u) || key > t.p_last ||
                                       !(t.p_first - key < p.mask.window || key < p.mask.sinks);
                     for (int y = 0; y < C::kSubs; ++y) {
-                        const int g = v_block<D>(j, n) * C::kSubs + y, slot = g % kSlots;
-                        wait_or_flag(&slot_full[slot], (g / kSlots) & 1, &sh_dead);
+                        const int g = j * C::kSubs + y, slot = g % C::kSlots;
+                        wait_or_flag(&v_full[slot], (g / C::kSlots) & 1, &sh_dead);
                         if (dead && (row >> C::kLog2VKeys) == y) {
                             const int r = row & (C::kVKeys - 1);
-                            uint8_t *at = ring + slot * kSlotBytes + (r >> log2_bv) * (bv * D * 2) + (r & (bv - 1)) * 128;
+                            uint8_t *at = v_ring + slot * C::kSlotBytes + (r >> log2_bv) * (bv * D * 2) + (r & (bv - 1)) * 128;
                             for (int x = 0; x < D / 8; ++x)
                                 *reinterpret_cast<uint4 *>(at + (x >> 3) * bv * 128 + (x & 7) * 16) =
                                     make_uint4(0, 0, 0, 0);
@@ -759,7 +768,8 @@ gdn_status launch_tc(PrefillParams p, int dtype, cudaStream_t s) {
     const uint64_t rows = static_cast<uint64_t>(p.cache.n_pages) * p.cache.n_kv_heads * ps;
     GDN_TRY(encode_heads_map(&q_map, p.q, dtype, D, p.n_q_heads, static_cast<uint64_t>(p.seqs.total),
                              static_cast<uint64_t>(p.q_stride) * 2, p.heads_per_tile, per));
-    GDN_TRY(encode_blocks_map(&k_map, p.k_pages, dtype, D, rows, D * 2, ps < kTcKeys ? ps : kTcKeys, 1));
+    GDN_TRY(encode_blocks_map(&k_map, p.k_pages, dtype, D, rows, D * 2, ps < kTcKeys ? ps : kTcKeys,
+                              ps < kTcKeys ? 1 : C::kCols));
     GDN_TRY(encode_blocks_map(&v_map, p.v_pages, dtype, D, rows, D * 2, ps < C::kVKeys ? ps : C::kVKeys,
                               D / 64));
     auto kernel = attn_prefill_tc_kernel<T, D>;
