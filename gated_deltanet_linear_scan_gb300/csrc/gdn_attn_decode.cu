@@ -384,6 +384,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                 walk = walk_tiles<KT>(p.mask, len - p.n_tokens, len - 1);
             }
         }
+        if (*static_cast<volatile int *>(&sh_dead)) drain_in_flight();
         return;
     }
 

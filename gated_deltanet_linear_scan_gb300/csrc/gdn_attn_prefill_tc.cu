@@ -1,0 +1,925 @@
+// gdn_attn_prefill_tc.cu -- prompt attention of 16-bit types on the tensor cores (sm_103a).
+//
+//   S = Q K^T      tcgen05, Q and K from shared memory, S in tensor memory
+//   P = 2^(scale log2(e) S - m)   four warps per row tile, one thread per row: the row's
+//                  maximum and sum need no exchange; P goes back to tensor memory over S,
+//                  in the cache's type (half a unit of the type per weight, which averages
+//                  out below the output's own rounding)
+//   O += P V       tcgen05, P from tensor memory, V from shared memory as it lies there
+//                  (rows are keys: the MN-major operand form, no transposition)
+//
+// O stays in tensor memory. It is rescaled only when a row's maximum has grown by more than
+// 2^8 since the reference the weights use (they stay below 2^8, far inside both types).
+//
+// A row tile is 128 rows: tokens x the heads of a key head. Two row tiles (head_dim 64, 128)
+// share every key tile of 128 keys and alternate: one tile's softmax runs while the tensor
+// pipe works for the other. With head_dim 256 O fills half the tensor memory, so there is one
+// row tile and two S buffers: S of the next key tile is computed during the softmax of this
+// one. Within a key tile, only the 32-key chunks that some row of the row tile sees are
+// multiplied and exponentiated.
+//
+// K and V stream through two rings of slots, each fed by a warp of its own (one warp's copies,
+// barriers and page lookups would take longer than the products: a copy costs its warp about
+// 60 cycles, a barrier 30 to 60). Pages are loaded one by one; a V slot keeps their rows apart
+// ([page][128-byte column][row]), so that one copy brings all of a page's columns, and the
+// MMA's descriptor strides say where they lie.
+//
+// CTAs are persistent: a scheduling warp takes the next pair of row tiles from the grid (the
+// hardware cancels the launch of a CTA that has not begun and hands over its index), looks
+// its sequence up and loads its Q, while the other warps are still busy with the one before.
+// Sequences go longest first, their last tokens first, so the work left at the end is small.
+#include "gdn_attn_prefill.cuh"
+#include "gdn_tc.cuh"
+
+#include <type_traits>
+
+namespace gdn {
+namespace {
+
+__device__ unsigned g_watchdog_attn_prefill;
+
+constexpr int kTcKeys = 128;
+constexpr int kTcRows = 128;
+constexpr int kChunk = 32;     // keys of a chunk
+constexpr int kNotes = 16;     // key tiles: more than K is ever ahead of the softmax
+constexpr int kWorks = 3;      // entries of the work ring
+constexpr float kLazy = 8.0f;  // log2 of the growth of a maximum that makes O rescale
+
+template <int D>
+struct Tc {
+    static constexpr int kTiles = D == 256 ? 1 : 2;
+    static constexpr int kBufs = D == 256 ? 2 : 1;              // S buffers of a row tile
+    // Slots of a K (or V) tile, and of the rings. head_dim 256 has room for one and a half K
+    // tiles: half of the next one arrives while this one is multiplied.
+    static constexpr int kSubs = D == 256 ? 2 : 1;
+    static constexpr int kKSlots = D == 64 ? 4 : D == 128 ? 2 : 3;
+    static constexpr int kVSlots = D == 64 ? 4 : 2;
+    static constexpr int kSlotBytes = kTcKeys * D * 2 / kSubs;
+    static constexpr int kCols = D / 64 / kSubs;                // 128-byte columns of a K slot
+    static constexpr int kVKeys = kTcKeys / kSubs;              // keys of a V slot
+    static constexpr int kLog2VKeys = kSubs == 2 ? 6 : 7;
+    static constexpr int kQBytes = kTcRows * D * 2;             // of a row tile
+    static constexpr int kSmem = kTiles * kQBytes + (kKSlots + kVSlots) * kSlotBytes + 1024;
+    static constexpr int kSoftmax = kTiles * 4;                 // softmax warps
+    // then the MMA, the K, the V and the scheduling warp
+    static constexpr int kMma = kSoftmax, kK = kMma + 1, kSched = kMma + 3;
+    static constexpr int kThreads = (kSoftmax + 4) * 32;
+    static constexpr int kS = 0, kO = 256;                      // tensor-memory columns
+    // batches up to this many sequences run longest first (what shared memory has left)
+    static constexpr int kTable = D == 256 ? 32 : kLongestFirstMaxSeqs;
+};
+
+// The sequences of a batch of up to N, in order of decreasing length.
+template <int N>
+struct SeqTable {
+    int row0[N], new_tokens[N], slot[N], len[N];
+    int order[N];      // sequence of rank r
+    int first[N + 1];  // blocks (pairs of row tiles) before rank r
+};
+
+// A pair of row tiles to compute.
+struct Work {
+    int valid;
+    int slot, row0, token0, tokens, kvh, head0, heads;
+    int p_first, p_last;      // positions of its first and last token
+    int n, n_sink, main0;     // its key tiles: a TileWalk
+    // row tile i sees tiles 0 .. head - 1 (its sinks) and begin .. end - 1 (its window)
+    int head[2], begin[2], end[2];
+
+    __device__ __forceinline__ int tile(int j) const { return j < n_sink ? j : main0 + j - n_sink; }
+    __device__ __forceinline__ bool active(int i, int j) const {
+        return j < end[i] && (j < head[i] || j >= begin[i]);
+    }
+    // The next tile of row tile i from j on (end[i] or more: none).
+    __device__ __forceinline__ int next(int i, int j) const {
+        return j < head[i] || j >= begin[i] ? j : begin[i];
+    }
+};
+
+// Positions of row tile i of a work item.
+__device__ __forceinline__ int tile_first(const Work &w, int i, int per) { return w.p_first + i * per; }
+__device__ __forceinline__ int tile_last(const Work &w, int i, int per) {
+    return min(w.p_first + (i + 1) * per - 1, w.p_last);
+}
+
+// The chunks [x, y) of the key tile at key0 that hold every key a position in [lo_p, hi_p] sees.
+__device__ __forceinline__ int2 chunks_seen(const AttnMask &mask, int key0, int lo_p, int hi_p) {
+    int a = kTcKeys, b = 0;
+    const int lo = mask.first(max(lo_p, 0));
+    if (lo < key0 + kTcKeys) {
+        a = max(lo - key0, 0);
+        b = min(hi_p - key0 + 1, kTcKeys);
+    }
+    const int sinks = min(mask.sinks, hi_p + 1) - key0;
+    if (sinks > 0) {
+        a = 0;
+        b = max(b, min(sinks, kTcKeys));
+    }
+    return make_int2(a / kChunk, (b + kChunk - 1) / kChunk);
+}
+
+// What the K warp notes about a key tile: bits 0..15 its 8-key blocks that were loaded, then
+// eight bits for each row tile.
+struct TileNote {
+    uint32_t bits;
+    __device__ __forceinline__ uint32_t of(int i) const { return bits >> (16 + 8 * i); }
+    __device__ __forceinline__ bool active(int i) const { return of(i) & 1u; }
+    __device__ __forceinline__ bool first(int i) const { return of(i) & 2u; }  // of the row tile's
+    __device__ __forceinline__ bool last(int i) const { return of(i) & 4u; }
+    __device__ __forceinline__ int begin(int i) const { return (of(i) >> 3) & 3u; }      // chunks
+    __device__ __forceinline__ int end(int i) const { return ((of(i) >> 5) & 3u) + 1; }
+    static __device__ __forceinline__ uint32_t make(bool first, bool last, int2 seen) {
+        return 1u | (first ? 2u : 0u) | (last ? 4u : 0u) | static_cast<uint32_t>(seen.x) << 3 |
+               static_cast<uint32_t>(seen.y - 1) << 5;
+    }
+};
+
+// Bounded wait; once one gave up, the CTA's later waits return at once and none of its rows
+// are written.
+__device__ __forceinline__ void wait_or_flag(uint64_t *bar, uint32_t parity, volatile int *dead) {
+    if (mbar_test(bar, parity) || *dead) return;
+    if (!mbar_wait(bar, parity)) {
+        *dead = 1;
+        atomicOr(&g_watchdog_attn_prefill, WD_STAGE_COPY);
+    }
+}
+
+// Bits lo .. hi - 1 of a 32-bit word (any of them outside the word).
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
+    const uint32_t below = hi >= 32 ? 0xFFFFFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
+    const uint32_t skip = lo >= 32 ? 0xFFFFFFFFu : lo <= 0 ? 0u : (1u << lo) - 1u;
+    return below & ~skip;
+}
+
+// Asks for the index of a CTA of this grid that has not begun, in place of its launch; the
+// answer (16 bytes) completes a phase of `bar`.
+__device__ __forceinline__ void ask_next_cta(void *answer, uint64_t *bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+        ::"r"(smem_addr(answer)), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// False when every CTA has begun.
+__device__ __forceinline__ bool next_cta(const void *answer, int &x) {
+    uint32_t ok, cx;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.b32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, h;\n\t}"
+        : "=r"(ok), "=r"(cx)
+        : "r"(smem_addr(answer))
+        : "memory");
+    x = static_cast<int>(cx);
+    return ok != 0;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(Tc<D>::kThreads, 1)
+attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
+                       const __grid_constant__ CUtensorMap k_map,
+                       const __grid_constant__ CUtensorMap v_map, const PrefillParams p) {
+    using C = Tc<D>;
+    constexpr bool kBf16 = !__is_same(T, __half);
+    constexpr uint32_t kIdescO = tc::idesc_16bit(kBf16, kTcRows, D, true);
+    extern __shared__ uint8_t dyn[];
+    uint8_t *smem =
+        reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+    uint8_t *k_ring = smem + C::kTiles * C::kQBytes;
+    uint8_t *v_ring = k_ring + C::kKSlots * C::kSlotBytes;
+    __shared__ __align__(8) uint64_t k_full[C::kKSlots], k_empty[C::kKSlots];
+    __shared__ __align__(8) uint64_t v_full[C::kVSlots], v_empty[C::kVSlots];
+    __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], o_done[2];
+    __shared__ __align__(8) uint64_t work_full[kWorks], work_empty[kWorks], answer_full;
+    __shared__ __align__(16) uint4 answer;
+    __shared__ Work works[kWorks];
+    __shared__ SeqTable<C::kTable> seqs;
+    __shared__ uint32_t notes[kNotes];
+    __shared__ uint32_t tmem_base;
+    __shared__ int sh_dead;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = p.tokens_per_tile / C::kTiles;            // tokens of a row tile
+    const int log2_bv = min(p.cache.log2_ps, C::kLog2VKeys);  // keys of a V load
+    const int bv = 1 << log2_bv;
+    const bool table = p.n_seqs <= C::kTable;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kKSlots; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
+        }
+        for (int i = 0; i < C::kVSlots; ++i) {
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_ready[i], 4);
+            mbar_init(&o_done[i], 1);
+        }
+        for (int i = 0; i < kWorks; ++i) {
+            mbar_init(&work_full[i], 1);
+            mbar_init(&work_empty[i], 3 + C::kSoftmax);
+        }
+        mbar_init(&answer_full, 1);
+        fence_mbar_init();
+        sh_dead = 0;
+    }
+    if (warp == C::kMma) tc::tmem_alloc(&tmem_base, 512);
+    // ---- the sequences, longest first
+    for (int n = threadIdx.x; n < p.n_seqs; n += C::kThreads) {
+        size_t row0 = 0;
+        int m = 0, slot = 0, len = 0;
+        const bool ok = p.seqs.range(n, row0, m) && p.cache.lookup(n, slot, len);
+        if (!ok && blockIdx.x == 0 && p.err_count) atomicAdd(p.err_count, 1);
+        if (table) {
+            seqs.row0[n] = static_cast<int>(row0);
+            seqs.new_tokens[n] = ok ? m : 0;
+            seqs.slot[n] = slot;
+            seqs.len[n] = ok ? len : 0;
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_base;
+    if (table) {
+        for (int n = threadIdx.x; n < p.n_seqs; n += C::kThreads) {
+            const int mine = seqs.len[n];
+            int rank = 0;
+            for (int o = 0; o < p.n_seqs; ++o) rank += seqs.len[o] > mine || (seqs.len[o] == mine && o < n);
+            seqs.order[rank] = n;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            int run = 0;
+            for (int r0 = 0; r0 < p.n_seqs; r0 += 32) {
+                const int r = r0 + lane;
+                const int own = r < p.n_seqs ? (seqs.new_tokens[seqs.order[r]] + p.tokens_per_tile - 1) / p.tokens_per_tile : 0;
+                int x = own;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(FULL_MASK, x, o);
+                    if (lane >= o) x += y;
+                }
+                if (r < p.n_seqs) seqs.first[r] = run + x - own;
+                run += __shfl_sync(FULL_MASK, x, 31);
+            }
+            if (lane == 0) seqs.first[p.n_seqs] = run;
+        }
+        __syncthreads();
+    }
+
+    // Two row tiles: 384 threads of 168 registers; the softmax threads take 200 each, the
+    // third warp group keeps 104 (2 * 200 + 104 = 3 * 168).
+    if (warp >= C::kSoftmax) {
+        if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        // These warps run converged, with one elected lane issuing: the operands of a copy or
+        // an MMA are then the same in every lane, as the hardware wants them.
+        const bool leader = elect_one();
+        if (warp == C::kSched) {
+            // ------------------------------------------------------ the scheduling warp
+            const int heads = p.cache.n_kv_heads * p.head_groups;
+            int q_uses[2] = {0, 0};
+            int id = blockIdx.x, ring = 0, round = 0, asked = 0;
+            for (;;) {
+                if (leader) {
+                    mbar_arrive_expect_tx(&answer_full, 16);
+                    ask_next_cta(&answer, &answer_full);
+                }
+                __syncwarp();
+                const int x = id / heads, y = id % heads;
+                int new_tokens = 0, row0 = 0, slot = 0, len = 0, block = 0;
+                if (table) {
+                    if (x < seqs.first[p.n_seqs]) {
+                        int lo = 0, hi = p.n_seqs;  // the last rank with first[rank] <= x
+                        while (hi - lo > 1) {
+                            const int mid = (lo + hi) / 2;
+                            if (seqs.first[mid] <= x) lo = mid;
+                            else hi = mid;
+                        }
+                        const int n = seqs.order[lo];
+                        new_tokens = seqs.new_tokens[n];
+                        row0 = seqs.row0[n];
+                        slot = seqs.slot[n];
+                        len = seqs.len[n];
+                        block = seqs.first[lo + 1] - 1 - x;
+                    }
+                } else {
+                    size_t at;
+                    const int n = warp_seq_of_slot(p.seqs.cu, p.n_seqs, p.tokens_per_tile, x);
+                    if (n >= 0 && p.seqs.range(n, at, new_tokens) && p.cache.lookup(n, slot, len)) {
+                        row0 = static_cast<int>(at);
+                        block = x - (row0 / p.tokens_per_tile + n);
+                    } else {
+                        new_tokens = 0;
+                    }
+                }
+                if (block * p.tokens_per_tile < new_tokens) {
+                    Work w;
+                    w.valid = 1;
+                    w.slot = slot;
+                    w.row0 = row0;
+                    w.token0 = block * p.tokens_per_tile;
+                    w.tokens = min(p.tokens_per_tile, new_tokens - w.token0);
+                    w.kvh = y / p.head_groups;
+                    const int hg = y % p.head_groups;
+                    w.head0 = w.kvh * p.group + hg * p.heads_per_tile;
+                    w.heads = min(p.heads_per_tile, p.group - hg * p.heads_per_tile);
+                    w.p_first = len - new_tokens + w.token0;
+                    w.p_last = w.p_first + w.tokens - 1;
+                    const TileWalk walk = walk_tiles<kTcKeys>(p.mask, w.p_first, w.p_last);
+                    w.n = walk.count;
+                    w.n_sink = walk.n_sink;
+                    w.main0 = walk.main0;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int first = tile_first(w, i, per), last = tile_last(w, i, per);
+                        if (i >= C::kTiles || i * per >= w.tokens || last < 0) {
+                            w.head[i] = w.begin[i] = w.end[i] = 0;
+                        } else {
+                            // (sinks past the walk's own sink tiles lie in its window part,
+                            // where tile j has number j: n_sink is main0 then)
+                            const int lo = p.mask.first(max(first, 0));
+                            w.head[i] = (min(p.mask.sinks, lo) + kTcKeys - 1) / kTcKeys;
+                            w.begin[i] = walk.n_sink + lo / kTcKeys - walk.main0;
+                            w.end[i] = walk.n_sink + last / kTcKeys + 1 - walk.main0;
+                        }
+                    }
+                    if (round > 0) wait_or_flag(&work_empty[ring], (round - 1) & 1, &sh_dead);
+                    if (leader) {
+                        works[ring] = w;
+                        mbar_arrive(&work_full[ring]);
+                    }
+                    __syncwarp();
+                    if (++ring == kWorks) {
+                        ring = 0;
+                        ++round;
+                    }
+                    // its Q, as the row tiles before let go of theirs
+#pragma unroll
+                    for (int i = 0; i < C::kTiles; ++i) {
+                        if (w.end[i] == 0) continue;
+                        if (q_uses[i] > 0) wait_or_flag(&q_empty[i], (q_uses[i] - 1) & 1, &sh_dead);
+                        ++q_uses[i];
+                        if (leader) {
+                            mbar_arrive_expect_tx(&q_full[i], static_cast<uint32_t>(p.heads_per_tile * per) * D * 2u);
+                            for (int cb = 0; cb < D / 64; ++cb)
+                                tma_load_3d(smem + i * C::kQBytes + cb * kTcRows * 128, &q_map, cb * 64,
+                                            w.head0, w.row0 + w.token0 + i * per, &q_full[i]);
+                        }
+                        __syncwarp();
+                    }
+                }
+                wait_or_flag(&answer_full, asked & 1, &sh_dead);
+                ++asked;
+                const bool more = next_cta(&answer, id) && !sh_dead;
+                fence_proxy_async_smem();  // read before the next answer overwrites it
+                __syncwarp();
+                if (!more) break;
+            }
+            if (round > 0) wait_or_flag(&work_empty[ring], (round - 1) & 1, &sh_dead);
+            if (leader) {
+                works[ring].valid = 0;
+                mbar_arrive(&work_full[ring]);
+            }
+            __syncwarp();
+        } else if (warp == C::kMma) {
+            // ------------------------------------------------------ the MMA warp
+            const uint64_t q_desc = tc::smem_desc_sw128(smem_addr(smem));
+            const uint64_t k_desc = tc::smem_desc_sw128(smem_addr(k_ring));
+            // V lies page by page, every page's 128-byte columns one behind the other: 16 keys
+            // are two groups of 8 rows, in one page (bv >= 16) or in two
+            const uint64_t v_desc = tc::smem_desc_sw128_mn(smem_addr(v_ring), bv * 128, bv >= 16 ? 1024 : D * 16);
+            uint32_t v_step[C::kVKeys / 16];  // from 16 keys to the next, in 16-byte units
+#pragma unroll
+            for (int x = 0; x < C::kVKeys / 16; ++x)
+                v_step[x] = (((x * 16) >> log2_bv) * (bv * D * 2) + ((x * 16) & (bv - 1)) * 128) >> 4;
+            int s_count = 0, o_count[2] = {0, 0}, q_count[2] = {0, 0};
+            // The note of key tile g (numbered over all work), once its K is there.
+            auto note_of = [&](int g) {
+                const int slot = (g * C::kSubs) % C::kKSlots;
+                wait_or_flag(&k_full[slot], (g * C::kSubs / C::kKSlots) & 1, &sh_dead);
+                // after a wait that gave up, no product is issued on a note never written
+                if (*static_cast<volatile int *>(&sh_dead)) return TileNote{0};
+                return TileNote{static_cast<volatile uint32_t *>(notes)[g % kNotes]};
+            };
+            // S of row tile i over key tile g
+            auto issue_s = [&](auto which, int g, TileNote note) {
+                constexpr int i = decltype(which)::value;
+                const int buf = C::kBufs == 2 ? s_count & 1 : i;
+                ++s_count;
+                if (note.first(i)) {
+                    wait_or_flag(&q_full[i], q_count[i] & 1, &sh_dead);
+                    ++q_count[i];
+                }
+                const bool release = i == 1 || !note.active(1), last = note.last(i);
+                const int from = note.begin(i) * kChunk;
+                const uint32_t to = tmem + C::kS + buf * kTcKeys + from;
+                const uint32_t idesc = tc::idesc_16bit(kBf16, kTcRows, 0, false) |
+                                       static_cast<uint32_t>(note.end(i) - note.begin(i)) << (17 + 2);
+#pragma unroll
+                for (int s = 0; s < C::kSubs; ++s) {
+                    const int slot = (g * C::kSubs + s) % C::kKSlots;
+                    if (s > 0) wait_or_flag(&k_full[slot], ((g * C::kSubs + s) / C::kKSlots) & 1, &sh_dead);
+                    tc::fence_after_sync();
+                    const uint64_t k = k_desc + ((slot * C::kSlotBytes + from * 128) >> 4);
+                    if (leader) {
+#pragma unroll
+                        for (int c = 0; c < C::kCols; ++c)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                tc::mma_bf16(to,
+                                             q_desc + ((i * C::kQBytes + (s * C::kCols + c) * kTcRows * 128 + x * 32) >> 4),
+                                             k + ((c * kTcKeys * 128 + x * 32) >> 4), idesc, s + c + x > 0);
+                        if (release) tc::mma_commit(&k_empty[slot]);
+                        if (s == C::kSubs - 1) {
+                            tc::mma_commit(&s_full[buf]);
+                            if (last) tc::mma_commit(&q_empty[i]);
+                        }
+                    }
+                    __syncwarp();
+                }
+            };
+            // O of row tile i += P V over key tile g
+            auto issue_o = [&](auto which, int g, TileNote note) {
+                constexpr int i = decltype(which)::value;
+                const int count = o_count[i]++;
+                const int buf = C::kBufs == 2 ? count & 1 : i;
+                const bool release = i == 1 || !note.active(1), first = note.first(i);
+                const int from = note.begin(i) * (kChunk / 16), to = note.end(i) * (kChunk / 16);
+                wait_or_flag(&p_ready[buf], (C::kBufs == 2 ? count >> 1 : count) & 1, &sh_dead);
+#pragma unroll
+                for (int s = 0; s < C::kSubs; ++s) {
+                    const int slot = (g * C::kSubs + s) % C::kVSlots;
+                    wait_or_flag(&v_full[slot], ((g * C::kSubs + s) / C::kVSlots) & 1, &sh_dead);
+                    tc::fence_after_sync();
+                    const uint64_t v = v_desc + ((slot * C::kSlotBytes) >> 4);
+                    const uint32_t pw = tmem + C::kS + buf * kTcKeys + s * C::kVKeys / 2;
+                    if (leader) {
+                        if (from == 0 && to == kTcKeys / 16) {
+#pragma unroll
+                            for (int x = 0; x < C::kVKeys / 16; ++x)
+                                tc::mma_bf16_ts(tmem + C::kO + i * D, pw + x * 8, v + v_step[x], kIdescO,
+                                                !first || s + x > 0);
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < C::kVKeys / 16; ++x) {
+                                const int key16 = s * (C::kVKeys / 16) + x;
+                                if (key16 >= from && key16 < to)
+                                    tc::mma_bf16_ts(tmem + C::kO + i * D, pw + x * 8, v + v_step[x], kIdescO,
+                                                    !first || key16 > from);
+                            }
+                        }
+                        if (release) tc::mma_commit(&v_empty[slot]);
+                        if (s == C::kSubs - 1) tc::mma_commit(&o_done[i]);
+                    }
+                    __syncwarp();
+                }
+            };
+            using Tile0 = std::integral_constant<int, 0>;
+            using Tile1 = std::integral_constant<int, 1>;
+            int base = 0;                         // key tiles of the work before
+            bool begun0 = false, begun1 = false;  // S of the work's first tile is already issued,
+            TileNote after{0};                    // whose note was read then (its K may be gone)
+            for (int ring = 0, round = 0;;) {
+                wait_or_flag(&work_full[ring], round & 1, &sh_dead);
+                const int n = works[ring].n;
+                if (!works[ring].valid || sh_dead) break;
+                const int next_ring = ring + 1 == kWorks ? 0 : ring + 1;
+                const int next_round = ring + 1 == kWorks ? round + 1 : round;
+                // Key tile by key tile, row tile 0 ahead of row tile 1 (the last of them that
+                // sees a tile lets its slots go), O of a tile and S of the next together: while
+                // one row tile multiplies, the other computes its weights.
+                TileNote note{0}, next{0};
+                if (n > 0) {
+                    note = after.bits != 0 ? after : note_of(base);
+                    after.bits = 0;
+                    if (!begun0 && note.active(0)) issue_s(Tile0{}, base, note);
+                    if (C::kTiles == 2 && !begun1 && note.active(1)) issue_s(Tile1{}, base, note);
+                    begun0 = begun1 = false;
+                }
+                for (int j = 0; j < n; ++j) {
+                    if (j + 1 < n) {
+                        next = note_of(base + j + 1);
+                    } else {
+                        next.bits = 0;
+                        if (C::kTiles == 2) {
+                            // the next work's first S, so that its softmax can begin while the
+                            // other row tile finishes here
+                            wait_or_flag(&work_full[next_ring], next_round & 1, &sh_dead);
+                            if (works[next_ring].valid && works[next_ring].n > 0 && !sh_dead)
+                                after = note_of(base + n);
+                        }
+                    }
+                    if constexpr (C::kTiles == 1) {
+                        if (next.active(0)) issue_s(Tile0{}, base + j + 1, next);
+                        issue_o(Tile0{}, base + j, note);
+                    } else {
+                        if (note.active(0)) issue_o(Tile0{}, base + j, note);
+                        if (next.active(0)) issue_s(Tile0{}, base + j + 1, next);
+                        if (after.active(0)) {
+                            issue_s(Tile0{}, base + n, after);
+                            begun0 = true;
+                        }
+                        if (note.active(1)) issue_o(Tile1{}, base + j, note);
+                        if (next.active(1)) issue_s(Tile1{}, base + j + 1, next);
+                        if (after.active(1)) {
+                            issue_s(Tile1{}, base + n, after);
+                            begun1 = true;
+                        }
+                    }
+                    note = next;
+                }
+                base += n;
+                if (leader) mbar_arrive(&work_empty[ring]);
+                __syncwarp();
+                ring = next_ring;
+                round = next_round;
+            }
+        } else if (warp < C::kSched) {
+            // ------------------------------------------------------ the K and the V warp
+            const bool is_k = warp == C::kK;
+            const int ps = 1 << p.cache.log2_ps;
+            const int log2_bk = min(p.cache.log2_ps, 7);  // keys of a page's part of a key tile
+            const int bk = 1 << log2_bk, n_bk = kTcKeys >> log2_bk;
+            if (leader) tma_prefetch_map(is_k ? &k_map : &v_map);
+            int base = 0, slot = 0, slot_round = 0;
+            for (int ring = 0, round = 0;;) {
+                wait_or_flag(&work_full[ring], round & 1, &sh_dead);
+                const Work w = works[ring];
+                if (!w.valid || sh_dead) break;
+                const int n = w.n, p_first = w.p_first, p_last = w.p_last, kvh = w.kvh;
+                // Whether someone sees keys of lane i's part of key tile j; its page if so (the
+                // ids of pages before the window, which may be gone, are not read).
+                auto seen = [&](int j) {
+                    const int key = w.tile(j) * kTcKeys + lane * bk;
+                    return lane < n_bk && key <= p_last &&
+                           (p_first - (key + bk - 1) < p.mask.window || key < p.mask.sinks);
+                };
+                auto page_at = [&](int j) {
+                    return j < n && seen(j) ? p.cache.page_of(w.slot, w.tile(j) * kTcKeys + lane * bk) : -1;
+                };
+                int page = page_at(0);
+                for (int j = 0; j < n; ++j) {
+                    const int next_page = page_at(j + 1);
+                    const int key0 = w.tile(j) * kTcKeys;
+                    const bool ok = p.cache.page_ok(page);
+                    const unsigned have = __ballot_sync(FULL_MASK, ok);
+                    const int row = (page * p.cache.n_kv_heads + kvh) * ps + (key0 & (ps - 1));
+                    if (is_k) {
+                        if (!ok && seen(j) && kvh == 0 && p.err_count) atomicAdd(p.err_count, 1);
+                        if (leader) {
+                            unsigned blocks = 0;
+                            for (int i = 0; i < kTcKeys / 8; ++i)
+                                if ((have >> ((i * 8) >> log2_bk)) & 1u) blocks |= 1u << i;
+#pragma unroll
+                            for (int i = 0; i < C::kTiles; ++i)
+                                if (w.active(i, j))
+                                    blocks |= TileNote::make(j == w.next(i, 0), w.next(i, j + 1) >= w.end[i],
+                                                             chunks_seen(p.mask, key0, tile_first(w, i, per),
+                                                                         tile_last(w, i, per)))
+                                              << (16 + 8 * i);
+                            notes[(base + j) % kNotes] = blocks;
+                        }
+                        __syncwarp();
+                    }
+                    for (int s = 0; s < C::kSubs; ++s) {
+                        uint64_t *full = is_k ? &k_full[slot] : &v_full[slot];
+                        if (slot_round > 0)
+                            wait_or_flag(is_k ? &k_empty[slot] : &v_empty[slot], (slot_round - 1) & 1, &sh_dead);
+                        if (is_k) {
+                            uint8_t *to = k_ring + slot * C::kSlotBytes;
+                            if (leader)
+                                mbar_arrive_expect_tx(full, (static_cast<uint32_t>(__popc(have)) << (log2_bk + 7)) * C::kCols);
+                            if (n_bk == 1) {  // one page: its columns in one copy
+                                const int r = __shfl_sync(FULL_MASK, row, 0);
+                                if (leader && have) tma_load_3d(to, &k_map, 0, r, s * C::kCols, full);
+                            } else {
+                                for (int i = 0; i < n_bk; ++i) {
+                                    const int r = __shfl_sync(FULL_MASK, row, i);
+                                    if (leader && ((have >> i) & 1u)) {
+#pragma unroll
+                                        for (int c = 0; c < C::kCols; ++c)
+                                            tma_load_3d(to + c * kTcKeys * 128 + (i << (log2_bk + 7)), &k_map, 0, r,
+                                                        s * C::kCols + c, full);
+                                    }
+                                }
+                            }
+                        } else {
+                            // this slot's copies of bv keys, from the parts they lie in
+                            uint8_t *to = v_ring + slot * C::kSlotBytes;
+                            const int i0 = s << (C::kLog2VKeys - log2_bv), i1 = (s + 1) << (C::kLog2VKeys - log2_bv);
+                            const bool here = lane >= i0 && lane < i1 && ((have >> ((lane << log2_bv) >> log2_bk)) & 1u);
+                            const unsigned loads = __popc(__ballot_sync(FULL_MASK, here));
+                            if (leader) mbar_arrive_expect_tx(full, loads * static_cast<uint32_t>(bv) * D * 2u);
+                            for (int i = i0; i < i1; ++i) {
+                                const int part = (i << log2_bv) >> log2_bk;
+                                const int r = __shfl_sync(FULL_MASK, row, part) + ((i << log2_bv) & (bk - 1));
+                                if (leader && ((have >> part) & 1u))
+                                    tma_load_3d(to + (i - i0) * (bv * D * 2), &v_map, 0, r, 0, full);
+                            }
+                        }
+                        __syncwarp();
+                        if (++slot == (is_k ? C::kKSlots : C::kVSlots)) {
+                            slot = 0;
+                            ++slot_round;
+                        }
+                    }
+                    page = next_page;
+                }
+                base += n;
+                if (leader) mbar_arrive(&work_empty[ring]);
+                __syncwarp();
+                if (++ring == kWorks) {
+                    ring = 0;
+                    ++round;
+                }
+            }
+        }
+    } else {
+        if constexpr (C::kTiles == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        // ---------------------------------------------------------- softmax, one row a thread
+        const int i = warp / 4, row = threadIdx.x & 127;
+        const int row_token = row / p.heads_per_tile, row_head = row % p.heads_per_tile;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t o_addr = tmem + lanes + C::kO + i * D;
+        const bool positive = p.scale_log2 > 0.0f;
+        const float mult = positive ? p.scale_log2 : 1.0f;
+        int base = 0, count = 0;  // key tiles of the work before, tiles of this row tile so far
+        for (int ring = 0, round = 0;;) {
+            wait_or_flag(&work_full[ring], round & 1, &sh_dead);
+            const Work &w = works[ring];
+            if (!w.valid || sh_dead) break;
+            const int head_tiles = w.head[i], begin_tile = w.begin[i], end_tile = w.end[i];
+            const int n_sink = w.n_sink, main0 = w.main0;
+            auto next_tile = [&](int j) { return j < head_tiles || j >= begin_tile ? j : begin_tile; };
+            const int token = i * per + row_token;
+            const int pos = w.p_first + token;
+            const int p_first = tile_first(w, i, per), p_last = tile_last(w, i, per);
+            const int all_first = w.p_first, all_last = w.p_last;
+            float m = -INFINITY, l = 0.0f;
+            bool begun = false;
+            for (int j = next_tile(0); j < end_tile; j = next_tile(j + 1)) {
+                const int buf = C::kBufs == 2 ? count & 1 : i;
+                const uint32_t s_addr = tmem + lanes + C::kS + buf * kTcKeys;
+                const int key0 = (j < n_sink ? j : main0 + j - n_sink) * kTcKeys;
+                wait_or_flag(&s_full[buf], (C::kBufs == 2 ? count >> 1 : count) & 1, &sh_dead);
+                tc::fence_after_sync();
+                // written before K was loaded, and K has been multiplied
+                const TileNote note{static_cast<volatile uint32_t *>(notes)[(base + j) % kNotes]};
+                const unsigned blocks = note.bits & 0xFFFFu;
+                const int2 seen = make_int2(note.begin(i), note.end(i));
+                // every row of the work sees every key of the tile
+                const bool alive = blocks == 0xFFFFu && key0 + kTcKeys - 1 <= all_last &&
+                                   (all_first - key0 < p.mask.window || key0 + kTcKeys <= p.mask.sinks);
+                if (!alive) {
+                    // V rows that no row of the work sees are cleared (by both row tiles, each
+                    // ahead of its own product), so that whatever the page holds there (an
+                    // infinity, a NaN) cannot reach O through a weight of 0.
+                    // (Two S buffers: once the O product before this tile's is complete, the
+                    // ring slots of V are at most one phase from the one waited for.)
+                    if (C::kBufs == 2 && begun) wait_or_flag(&o_done[0], (count - 1) & 1, &sh_dead);
+                    const int key = key0 + row;
+                    const bool dead = !((blocks >> (row >> 3)) & 1u) || key > all_last ||
+                                      !(all_first - key < p.mask.window || key < p.mask.sinks);
+                    for (int y = 0; y < C::kSubs; ++y) {
+                        const int g = (base + j) * C::kSubs + y, slot = g % C::kVSlots;
+                        wait_or_flag(&v_full[slot], (g / C::kVSlots) & 1, &sh_dead);
+                        if (dead && (row >> C::kLog2VKeys) == y) {
+                            const int r = row & (C::kVKeys - 1);
+                            uint8_t *at = v_ring + slot * C::kSlotBytes + (r >> log2_bv) * (bv * D * 2) + (r & (bv - 1)) * 128;
+                            for (int x = 0; x < D / 8; ++x)
+                                *reinterpret_cast<uint4 *>(at + (x >> 3) * bv * 128 + (x & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                // The reference of the weights, from the tile's maximum; O is rescaled when it
+                // moves by more than the allowance.
+                auto settle = [&](float mx) {
+                    if (!begun) {
+                        m = mx;
+                        return;
+                    }
+                    const bool grow = (mx - m) * mult > kLazy;
+                    if (__any_sync(FULL_MASK, grow)) {
+                        // O is complete up to the tile before: S of this tile was issued after
+                        // it (two S buffers: after the one before that)
+                        if (C::kBufs == 2) {
+                            wait_or_flag(&o_done[0], (count - 1) & 1, &sh_dead);
+                            tc::fence_after_sync();
+                        }
+                        const float f = grow ? fast_exp2((m - mx) * mult) : 1.0f;
+                        if (grow) m = mx;
+                        l *= f;
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tc::tmem_ld32_nowait(o_addr + c, o);
+                            tc::tmem_ld_wait();
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                            tc::tmem_st32(o_addr + c, o);
+                        }
+                    }
+                };
+                float2 sum[4] = {};
+                // weights of 32 scores, and their place in P
+                auto weigh = [&](const uint32_t (&s)[32], float2 mul2, float2 sub2, uint32_t to) {
+                    uint32_t pw[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        float2 a = __ffma2_rn(make_float2(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1])),
+                                              mul2, sub2);
+                        a.x = fast_exp2(a.x);
+                        a.y = fast_exp2(a.y);
+                        sum[x & 3] = __fadd2_rn(sum[x & 3], a);
+                        pw[x] = Elem<T>::pack(a.x, a.y);
+                    }
+                    tc::tmem_st16(to, pw);
+                };
+                auto top_of = [&](const uint32_t (&s)[32], float (&top)[4]) {
+#pragma unroll
+                    for (int x = 0; x < 32; x += 8)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            top[y] = fmaxf(fmaxf(top[y], __uint_as_float(s[x + 2 * y])), __uint_as_float(s[x + 2 * y + 1]));
+                };
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                const bool clean = positive && blocks == 0xFFFFu && key0 + kTcKeys - 1 <= p_first &&
+                                   (p_last - key0 < p.mask.window || key0 + kTcKeys <= p.mask.sinks);
+                if (clean) {
+                    // every row sees every key: the whole tile in registers
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tc::tmem_ld32_nowait(s_addr + c * kChunk, s[c]);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) top_of(s[c], top);
+                    settle(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+                    const float off = m == -INFINITY ? 0.0f : m * mult;
+                    const float2 mul2 = make_float2(mult, mult), sub2 = make_float2(-off, -off);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) weigh(s[c], mul2, sub2, s_addr + c * (kChunk / 2));
+                } else {
+                    // chunk by chunk, twice: the maximum, then the weights (a chunk's P lies over
+                    // scores that have been read)
+                    auto chunk = [&](int c, uint32_t (&s)[32]) {
+                        tc::tmem_ld32_nowait(s_addr + c * kChunk, s);
+                        const int at = key0 + c * kChunk;
+                        // the keys this row sees: from its window's first to itself, and the sinks
+                        const int hi = pos - at + 1;
+                        const int lo = pos - at < p.mask.window ? 0 : pos - p.mask.window + 1 - at;
+                        uint32_t see = bits_between(lo, hi) | bits_between(0, min(p.mask.sinks - at, hi));
+                        uint32_t there = 0;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if ((blocks >> (4 * c + x)) & 1u) there |= 0xFFu << (8 * x);
+                        see &= there;
+                        tc::tmem_ld_wait();
+                        if (!positive) {
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * p.scale_log2);
+                        }
+                        if (__any_sync(FULL_MASK, see != 0xFFFFFFFFu)) {
+#pragma unroll
+                            for (int x = 0; x < 32; ++x)
+                                if (!(see & (1u << x))) s[x] = __float_as_uint(-INFINITY);
+                        }
+                    };
+                    uint32_t s[32];
+#pragma unroll 1
+                    for (int c = seen.x; c < seen.y; ++c) {
+                        chunk(c, s);
+                        top_of(s, top);
+                    }
+                    settle(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+                    const float off = m == -INFINITY ? 0.0f : m * mult;
+                    const float2 mul2 = make_float2(mult, mult), sub2 = make_float2(-off, -off);
+#pragma unroll 1
+                    for (int c = seen.x; c < seen.y; ++c) {
+                        chunk(c, s);
+                        weigh(s, mul2, sub2, s_addr + c * (kChunk / 2));
+                    }
+                }
+                sum[0] = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+                l += sum[0].x + sum[0].y;
+                tc::tmem_st_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                // keeps this thread at most one phase behind o_done
+                if (C::kBufs == 2 && begun) wait_or_flag(&o_done[0], (count - 1) & 1, &sh_dead);
+                if (lane == 0) mbar_arrive(&p_ready[buf]);
+                begun = true;
+                ++count;
+            }
+            // ------------------------------------------------------ O out
+            if (i * per < w.tokens) {
+                T *out = static_cast<T *>(p.out) +
+                         (static_cast<size_t>(w.row0 + w.token0 + token) * p.n_q_heads + w.head0 + row_head) * D;
+                const bool mine = token < w.tokens && row_token < per && row_head < w.heads;
+                if (begun) {
+                    wait_or_flag(&o_done[i], (count - 1) & 1, &sh_dead);
+                    tc::fence_after_sync();
+                }
+                const float inv = 1.0f / l;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tc::tmem_ld32_nowait(o_addr + c, o);
+                    tc::tmem_ld_wait();
+                    if (mine && !sh_dead) {
+#pragma unroll
+                        for (int x = 0; x < 32; x += 8) {
+                            uint32_t pw[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                pw[y] = l == 0.0f ? 0u
+                                                  : Elem<T>::pack(__uint_as_float(o[x + 2 * y]) * inv,
+                                                                  __uint_as_float(o[x + 2 * y + 1]) * inv);
+                            *reinterpret_cast<uint4 *>(out + c + x) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+                        }
+                    }
+                }
+                tc::fence_before_sync();
+            }
+            base += w.n;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&work_empty[ring]);
+            if (++ring == kWorks) {
+                ring = 0;
+                ++round;
+            }
+        }
+    }
+    __syncthreads();
+    if (sh_dead) drain_in_flight();
+    if (warp == C::kMma) {
+        tc::fence_after_sync();
+        tc::tmem_relinquish();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <typename T, int D>
+gdn_status launch(PrefillParams p, int dtype, cudaStream_t s) {
+    using C = Tc<D>;
+    const int ps = 1 << p.cache.log2_ps;
+    p.heads_per_tile = p.group < kTcRows ? p.group : kTcRows;
+    p.head_groups = (p.group + p.heads_per_tile - 1) / p.heads_per_tile;
+    const int per = kTcRows / p.heads_per_tile;
+    p.tokens_per_tile = per * C::kTiles;
+    // every sequence's last block may be short: one block more than full ones each
+    const long long blocks = p.seqs.total / p.tokens_per_tile + p.n_seqs;
+    const long long grid = blocks * p.cache.n_kv_heads * p.head_groups;
+    if (grid > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+    CUtensorMap q_map, k_map, v_map;
+    const uint64_t rows = static_cast<uint64_t>(p.cache.n_pages) * p.cache.n_kv_heads * ps;
+    GDN_TRY(encode_heads_map(&q_map, p.q, dtype, D, p.n_q_heads, static_cast<uint64_t>(p.seqs.total),
+                             static_cast<uint64_t>(p.q_stride) * 2, p.heads_per_tile, per));
+    GDN_TRY(encode_blocks_map(&k_map, p.k_pages, dtype, D, rows, D * 2, ps < kTcKeys ? ps : kTcKeys,
+                              ps < kTcKeys ? 1 : C::kCols));
+    GDN_TRY(encode_blocks_map(&v_map, p.v_pages, dtype, D, rows, D * 2, ps < C::kVKeys ? ps : C::kVKeys,
+                              D / 64));
+    auto kernel = attn_prefill_tc_kernel<T, D>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+        return GDN_ERR_LAUNCH;
+    kernel<<<static_cast<unsigned>(grid), C::kThreads, C::kSmem, s>>>(q_map, k_map, v_map, p);
+    return launch_status();
+}
+
+template <typename T>
+gdn_status launch_dim(int d, const PrefillParams &p, int dtype, cudaStream_t s) {
+    switch (d) {
+        case 64: return launch<T, 64>(p, dtype, s);
+        case 128: return launch<T, 128>(p, dtype, s);
+        default: return launch<T, 256>(p, dtype, s);
+    }
+}
+
+}  // namespace
+
+gdn_status launch_attn_prefill_tc(const PrefillParams &p, int dtype, int head_dim, cudaStream_t s) {
+    return dtype == GDN_F16 ? launch_dim<__half>(head_dim, p, dtype, s)
+                            : launch_dim<__nv_bfloat16>(head_dim, p, dtype, s);
+}
+
+unsigned read_and_clear_watchdog_attn_prefill(cudaStream_t s) {
+    unsigned flags = 0;
+    const unsigned zero = 0;
+    cudaMemcpyFromSymbolAsync(&flags, g_watchdog_attn_prefill, sizeof(flags), 0,
+                              cudaMemcpyDeviceToHost, s);
+    cudaMemcpyToSymbolAsync(g_watchdog_attn_prefill, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
+    cudaStreamSynchronize(s);
+    return flags;
+}
+
+}  // namespace gdn

@@ -140,6 +140,14 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint64_t *bar, uint32_t parity,
     return true;
 }
 
+// For a CTA that leaves after a wait gave up: copies and tensor-core products it may still
+// have in flight finish within microseconds, long before this returns, so none of them
+// outlives the CTA's shared or tensor memory.
+__device__ __forceinline__ void drain_in_flight() {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 500000) __nanosleep(1000);
+}
+
 // 1-D bulk copy global -> shared (TMA engine), completion counted on `bar` in bytes.
 // dst and src 16-byte aligned, bytes a multiple of 16.
 __device__ __forceinline__ void bulk_g2s(void *dst, const void *src, uint32_t bytes,

@@ -145,3 +145,35 @@ def test_one_token_prompts_match_decode(cuda_lib):
     q = c.queries(rng, [1] * 3, 8)
     c.check(run(cuda_lib, c, q, [1] * 3, 8), q, [1] * 3, 128 ** -0.5, 0, 0, weights_16bit=True)
     c.check(decode(cuda_lib, c, q, 1, 8), q, [1] * 3, 128 ** -0.5, 0, 0)
+
+
+@pytest.mark.parametrize("dtype,d", [("float16", 64), ("bfloat16", 128), ("float16", 256),
+                                     ("float32", 64)])
+@pytest.mark.parametrize("n_seqs", [37, 300])
+def test_many_sequences(cuda_lib, dtype, d, n_seqs):
+    """Ragged batches below and above the size that is put in order of length, lengths on both
+    sides of the tiles' edges, sequences without new tokens among them; the same bits twice."""
+    rng = np.random.default_rng([n_seqs, d])
+    counts = [int(x) for x in rng.choice([0, 1, 2, 31, 32, 33, 64, 65, 127, 128, 129], n_seqs)]
+    lens = [m + int(rng.choice([0, 0, 1, 100, 128, 300])) for m in counts]
+    c = Cache(torch, rng, lens, 1, d, 32, dtype, pool=n_seqs + 5)
+    q = c.queries(rng, counts, 4)
+    a = run(cuda_lib, c, q, counts, 4, 70, 3)
+    c.check(a, q, counts, d ** -0.5, 70, 3, weights_16bit=True)
+    assert torch.equal(a, run(cuda_lib, c, q, counts, 4, 70, 3))
+    cuda_lib.gdn_device_error()
+
+
+@pytest.mark.parametrize("dtype,d,group", [("bfloat16", 64, 1), ("bfloat16", 128, 4),
+                                           ("float16", 128, 128), ("float16", 256, 7)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (40, 1), (130, 200), (256, 3)])
+def test_row_tiles_at_the_edges(cuda_lib, dtype, d, group, window, sinks):
+    """Row tiles whose window, sinks and diagonal fall into different key tiles, chunk by chunk."""
+    rng = np.random.default_rng([d, group, window])
+    counts = [260, 129, 70]
+    lens = [260, 640, 400]
+    c = Cache(torch, rng, lens, 1, d, 16, dtype)
+    q = c.queries(rng, counts, group)
+    out = run(cuda_lib, c, q, counts, group, window, sinks)
+    c.check(out, q, counts, d ** -0.5, window, sinks, weights_16bit=True)
+    cuda_lib.gdn_device_error()
