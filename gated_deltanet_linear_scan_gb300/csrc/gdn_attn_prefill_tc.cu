@@ -31,8 +31,6 @@
 #include "gdn_attn_prefill.cuh"
 #include "gdn_tc.cuh"
 
-#include <type_traits>
-
 namespace gdn {
 namespace {
 
@@ -401,7 +399,8 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
             for (int x = 0; x < C::kVKeys / 16; ++x)
                 v_step[x] = (((x * 16) >> log2_bv) * (bv * D * 2) + ((x * 16) & (bv - 1)) * 128) >> 4;
-            int s_count = 0, o_count[2] = {0, 0}, q_count[2] = {0, 0};
+            int s_count = 0, o_count = 0;         // products issued (one row tile: its buffer)
+            uint32_t o_phase = 0, q_phase = 0;    // bit i: of row tile i's p_ready, q_full
             // The note of key tile g (numbered over all work), once its K is there.
             auto note_of = [&](int g) {
                 const int slot = (g * C::kSubs) % C::kKSlots;
@@ -410,33 +409,34 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 if (*static_cast<volatile int *>(&sh_dead)) return TileNote{0};
                 return TileNote{static_cast<volatile uint32_t *>(notes)[g % kNotes]};
             };
-            // S of row tile i over key tile g
-            auto issue_s = [&](auto which, int g, TileNote note) {
-                constexpr int i = decltype(which)::value;
+            // S of row tile i over key tile g. (This code and issue_o's stand once, in rolled loops:
+            // unrolled for both row tiles the warp spent its time fetching instructions.)
+            auto issue_s = [&](int i, int g, TileNote note) {
                 const int buf = C::kBufs == 2 ? s_count & 1 : i;
                 ++s_count;
                 if (note.first(i)) {
-                    wait_or_flag(&q_full[i], q_count[i] & 1, &sh_dead);
-                    ++q_count[i];
+                    wait_or_flag(&q_full[i], (q_phase >> i) & 1, &sh_dead);
+                    q_phase ^= 1u << i;
                 }
                 const bool release = i == 1 || !note.active(1), last = note.last(i);
                 const int from = note.begin(i) * kChunk;
                 const uint32_t to = tmem + C::kS + buf * kTcKeys + from;
                 const uint32_t idesc = tc::idesc_16bit(kBf16, kTcRows, 0, false) |
                                        static_cast<uint32_t>(note.end(i) - note.begin(i)) << (17 + 2);
-#pragma unroll
+                const uint64_t q0 = q_desc + ((i * C::kQBytes) >> 4);
+#pragma unroll 1
                 for (int s = 0; s < C::kSubs; ++s) {
                     const int slot = (g * C::kSubs + s) % C::kKSlots;
                     if (s > 0) wait_or_flag(&k_full[slot], ((g * C::kSubs + s) / C::kKSlots) & 1, &sh_dead);
                     tc::fence_after_sync();
                     const uint64_t k = k_desc + ((slot * C::kSlotBytes + from * 128) >> 4);
+                    const uint64_t q = q0 + ((s * C::kCols * kTcRows * 128) >> 4);
                     if (leader) {
 #pragma unroll
                         for (int c = 0; c < C::kCols; ++c)
 #pragma unroll
                             for (int x = 0; x < 4; ++x)
-                                tc::mma_bf16(to,
-                                             q_desc + ((i * C::kQBytes + (s * C::kCols + c) * kTcRows * 128 + x * 32) >> 4),
+                                tc::mma_bf16(to, q + ((c * kTcRows * 128 + x * 32) >> 4),
                                              k + ((c * kTcKeys * 128 + x * 32) >> 4), idesc, s + c + x > 0);
                         if (release) tc::mma_commit(&k_empty[slot]);
                         if (s == C::kSubs - 1) {
@@ -448,33 +448,32 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 }
             };
             // O of row tile i += P V over key tile g
-            auto issue_o = [&](auto which, int g, TileNote note) {
-                constexpr int i = decltype(which)::value;
-                const int count = o_count[i]++;
-                const int buf = C::kBufs == 2 ? count & 1 : i;
+            auto issue_o = [&](int i, int g, TileNote note) {
+                const int buf = C::kBufs == 2 ? o_count & 1 : i;
+                const uint32_t phase = C::kBufs == 2 ? (o_count >> 1) & 1 : (o_phase >> i) & 1;
+                ++o_count;
+                o_phase ^= 1u << i;
                 const bool release = i == 1 || !note.active(1), first = note.first(i);
                 const int from = note.begin(i) * (kChunk / 16), to = note.end(i) * (kChunk / 16);
-                wait_or_flag(&p_ready[buf], (C::kBufs == 2 ? count >> 1 : count) & 1, &sh_dead);
-#pragma unroll
+                wait_or_flag(&p_ready[buf], phase, &sh_dead);
+#pragma unroll 1
                 for (int s = 0; s < C::kSubs; ++s) {
                     const int slot = (g * C::kSubs + s) % C::kVSlots;
                     wait_or_flag(&v_full[slot], ((g * C::kSubs + s) / C::kVSlots) & 1, &sh_dead);
                     tc::fence_after_sync();
                     const uint64_t v = v_desc + ((slot * C::kSlotBytes) >> 4);
-                    const uint32_t pw = tmem + C::kS + buf * kTcKeys + s * C::kVKeys / 2;
+                    const uint32_t pw = tmem + C::kS + buf * kTcKeys + s * C::kVKeys / 2, o = tmem + C::kO + i * D;
                     if (leader) {
                         if (from == 0 && to == kTcKeys / 16) {
 #pragma unroll
                             for (int x = 0; x < C::kVKeys / 16; ++x)
-                                tc::mma_bf16_ts(tmem + C::kO + i * D, pw + x * 8, v + v_step[x], kIdescO,
-                                                !first || s + x > 0);
+                                tc::mma_bf16_ts(o, pw + x * 8, v + v_step[x], kIdescO, !first || s + x > 0);
                         } else {
 #pragma unroll
                             for (int x = 0; x < C::kVKeys / 16; ++x) {
                                 const int key16 = s * (C::kVKeys / 16) + x;
                                 if (key16 >= from && key16 < to)
-                                    tc::mma_bf16_ts(tmem + C::kO + i * D, pw + x * 8, v + v_step[x], kIdescO,
-                                                    !first || key16 > from);
+                                    tc::mma_bf16_ts(o, pw + x * 8, v + v_step[x], kIdescO, !first || key16 > from);
                             }
                         }
                         if (release) tc::mma_commit(&v_empty[slot]);
@@ -483,11 +482,8 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                     __syncwarp();
                 }
             };
-            using Tile0 = std::integral_constant<int, 0>;
-            using Tile1 = std::integral_constant<int, 1>;
-            int base = 0;                         // key tiles of the work before
-            bool begun0 = false, begun1 = false;  // S of the work's first tile is already issued,
-            TileNote after{0};                    // whose note was read then (its K may be gone)
+            int base = 0;         // key tiles of the work before
+            TileNote carried{0};  // of the work's first tile, when its S is already issued
             for (int ring = 0, round = 0;;) {
                 wait_or_flag(&work_full[ring], round & 1, &sh_dead);
                 const int n = works[ring].n;
@@ -496,43 +492,36 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 const int next_round = ring + 1 == kWorks ? round + 1 : round;
                 // Key tile by key tile, row tile 0 ahead of row tile 1 (the last of them that
                 // sees a tile lets its slots go), O of a tile and S of the next together: while
-                // one row tile multiplies, the other computes its weights.
-                TileNote note{0}, next{0};
-                if (n > 0) {
-                    note = after.bits != 0 ? after : note_of(base);
-                    after.bits = 0;
-                    if (!begun0 && note.active(0)) issue_s(Tile0{}, base, note);
-                    if (C::kTiles == 2 && !begun1 && note.active(1)) issue_s(Tile1{}, base, note);
-                    begun0 = begun1 = false;
-                }
-                for (int j = 0; j < n; ++j) {
-                    if (j + 1 < n) {
-                        next = note_of(base + j + 1);
-                    } else {
-                        next.bits = 0;
-                        if (C::kTiles == 2) {
-                            // the next work's first S, so that its softmax can begin while the
-                            // other row tile finishes here
+                // one row tile multiplies, the other computes its weights. Two row tiles: the
+                // last step's S is the next work's first, so that its softmax can begin while the
+                // other row tile finishes here. One row tile: S goes ahead of O, into the other
+                // buffer.
+                TileNote note = carried, next{0};
+                carried.bits = 0;
+#pragma unroll 1
+                for (int j = note.bits != 0 || n == 0 ? 0 : -1; j < n; ++j) {
+                    auto look_ahead = [&] {
+                        if (j + 1 < n) {
+                            next = note_of(base + j + 1);
+                        } else if (C::kTiles == 2) {
                             wait_or_flag(&work_full[next_ring], next_round & 1, &sh_dead);
                             if (works[next_ring].valid && works[next_ring].n > 0 && !sh_dead)
-                                after = note_of(base + n);
+                                carried = note_of(base + n);
+                            next = carried;
+                        } else {
+                            next.bits = 0;
                         }
-                    }
+                    };
                     if constexpr (C::kTiles == 1) {
-                        if (next.active(0)) issue_s(Tile0{}, base + j + 1, next);
-                        issue_o(Tile0{}, base + j, note);
+                        look_ahead();
+                        if (next.active(0)) issue_s(0, base + j + 1, next);
+                        if (j >= 0) issue_o(0, base + j, note);
                     } else {
-                        if (note.active(0)) issue_o(Tile0{}, base + j, note);
-                        if (next.active(0)) issue_s(Tile0{}, base + j + 1, next);
-                        if (after.active(0)) {
-                            issue_s(Tile0{}, base + n, after);
-                            begun0 = true;
-                        }
-                        if (note.active(1)) issue_o(Tile1{}, base + j, note);
-                        if (next.active(1)) issue_s(Tile1{}, base + j + 1, next);
-                        if (after.active(1)) {
-                            issue_s(Tile1{}, base + n, after);
-                            begun1 = true;
+#pragma unroll 1
+                        for (int i = 0; i < 2; ++i) {
+                            if (note.active(i)) issue_o(i, base + j, note);
+                            if (i == 0) look_ahead();
+                            if (next.active(i)) issue_s(i, base + j + 1, next);
                         }
                     }
                     note = next;
