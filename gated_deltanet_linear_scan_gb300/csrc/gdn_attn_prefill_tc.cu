@@ -424,7 +424,7 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 const uint32_t idesc = tc::idesc_16bit(kBf16, kTcRows, 0, false) |
                                        static_cast<uint32_t>(note.end(i) - note.begin(i)) << (17 + 2);
                 const uint64_t q0 = q_desc + ((i * C::kQBytes) >> 4);
-#pragma unroll 1
+#pragma unroll
                 for (int s = 0; s < C::kSubs; ++s) {
                     const int slot = (g * C::kSubs + s) % C::kKSlots;
                     if (s > 0) wait_or_flag(&k_full[slot], ((g * C::kSubs + s) / C::kKSlots) & 1, &sh_dead);
@@ -456,7 +456,7 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 const bool release = i == 1 || !note.active(1), first = note.first(i);
                 const int from = note.begin(i) * (kChunk / 16), to = note.end(i) * (kChunk / 16);
                 wait_or_flag(&p_ready[buf], phase, &sh_dead);
-#pragma unroll 1
+#pragma unroll
                 for (int s = 0; s < C::kSubs; ++s) {
                     const int slot = (g * C::kSubs + s) % C::kVSlots;
                     wait_or_flag(&v_full[slot], ((g * C::kSubs + s) / C::kVSlots) & 1, &sh_dead);
@@ -555,28 +555,34 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 auto page_at = [&](int j) {
                     return j < n && seen(j) ? p.cache.page_of(w.slot, w.tile(j) * kTcKeys + lane * bk) : -1;
                 };
+                // what there is to say of tile j, whose parts `have` pages (one lane's business)
+                auto note_of = [&](int j, unsigned have) {
+                    unsigned note = 0;
+                    if (is_k && leader && j < n) {
+                        const int key0 = w.tile(j) * kTcKeys;
+                        for (int i = 0; i < kTcKeys / 8; ++i)
+                            if ((have >> ((i * 8) >> log2_bk)) & 1u) note |= 1u << i;
+#pragma unroll
+                        for (int i = 0; i < C::kTiles; ++i)
+                            if (w.active(i, j))
+                                note |= TileNote::make(j == w.next(i, 0), w.next(i, j + 1) >= w.end[i],
+                                                       chunks_seen(p.mask, key0, tile_first(w, i, per),
+                                                                   tile_last(w, i, per)))
+                                        << (16 + 8 * i);
+                    }
+                    __syncwarp();
+                    return note;
+                };
                 int page = page_at(0);
+                unsigned have = __ballot_sync(FULL_MASK, p.cache.page_ok(page));
+                unsigned note = note_of(0, have);
                 for (int j = 0; j < n; ++j) {
                     const int next_page = page_at(j + 1);
                     const int key0 = w.tile(j) * kTcKeys;
-                    const bool ok = p.cache.page_ok(page);
-                    const unsigned have = __ballot_sync(FULL_MASK, ok);
                     const int row = (page * p.cache.n_kv_heads + kvh) * ps + (key0 & (ps - 1));
                     if (is_k) {
-                        if (!ok && seen(j) && kvh == 0 && p.err_count) atomicAdd(p.err_count, 1);
-                        if (leader) {
-                            unsigned blocks = 0;
-                            for (int i = 0; i < kTcKeys / 8; ++i)
-                                if ((have >> ((i * 8) >> log2_bk)) & 1u) blocks |= 1u << i;
-#pragma unroll
-                            for (int i = 0; i < C::kTiles; ++i)
-                                if (w.active(i, j))
-                                    blocks |= TileNote::make(j == w.next(i, 0), w.next(i, j + 1) >= w.end[i],
-                                                             chunks_seen(p.mask, key0, tile_first(w, i, per),
-                                                                         tile_last(w, i, per)))
-                                              << (16 + 8 * i);
-                            notes[(base + j) % kNotes] = blocks;
-                        }
+                        if (!p.cache.page_ok(page) && seen(j) && kvh == 0 && p.err_count) atomicAdd(p.err_count, 1);
+                        if (leader) notes[(base + j) % kNotes] = note;
                         __syncwarp();
                     }
                     for (int s = 0; s < C::kSubs; ++s) {
@@ -622,6 +628,8 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                         }
                     }
                     page = next_page;
+                    have = __ballot_sync(FULL_MASK, p.cache.page_ok(page));
+                    note = note_of(j + 1, have);  // while the copies are on their way
                 }
                 base += n;
                 if (leader) mbar_arrive(&work_empty[ring]);
