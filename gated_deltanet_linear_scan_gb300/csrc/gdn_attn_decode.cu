@@ -8,7 +8,7 @@
 // of one small matrix product, so a key byte is read once for all of them.
 //
 // Work split. A unit is (sequence, key head, group of at most 16 rows); its keys are cut in
-// tiles (64 keys of a 16-bit type, 32 of fp32). The tiles of all units, in order, are dealt
+// tiles of 32 KB (64 KB for the widest heads). The tiles of all units, in order, are dealt
 // out evenly as one contiguous range per CTA, whatever the lengths: a ragged batch, one long
 // sequence and many short ones all keep every SM equally busy, with no host knowledge of the
 // lengths. A unit that crosses a range boundary leaves partial results (m, l, o) in the
@@ -36,15 +36,17 @@ constexpr int kThreads = kCompute + 32;         // and the loading warp
 constexpr int kRows = 16;                       // rows of a unit
 constexpr int kSMs = 152;
 constexpr int kMaxCtas = 2 * kSMs;
+constexpr int kJoin = 8;                        // partial results loaded together in a join
 
 // kHead: the unit's first tile lies in this CTA's range.
-enum : int { kFirst = 1, kLast = 2, kWhole = 4, kHead = 8 };
+enum : int { kFirst = 1, kLast = 2, kWhole = 4, kHead = 8 };  // kWhole, kHead: of a segment
 
-// What the loading warp tells the computing warps about a stage.
-struct Stage {
-    int seq, unit, len, key0, flags;
-    unsigned blocks;  // bit b: keys key0 + 8b .. + 7 lie in a page that was loaded
-    int c0, c1;       // CTAs sharing the unit (when it is not whole here)
+// What the loading warp tells the computing warps: about a stage (the first key of its tile,
+// and flags | blocks << 8, bit b of blocks: keys 8 b .. 8 b + 7 lie in a page that was
+// loaded), and about a segment, the part of a unit in this CTA's range.
+struct Segment {
+    int seq, kvh, head_group, token_group, len, flags;
+    int c0, c1;  // CTAs sharing the unit (when it is not whole here)
 };
 
 struct Params {
@@ -65,7 +67,8 @@ struct Params {
 template <typename T, int D, int RT>
 struct Geometry {
     static constexpr bool kF32 = sizeof(T) == 4;
-    static constexpr int KT = kF32 ? 32 : 64;                              // keys of a tile
+    // keys of a tile: 32 KB of K and V together, but for the widest heads (64 KB)
+    static constexpr int KT = (D == 64 ? 2 : 1) * (kF32 ? 32 : 64);
     static constexpr int kCols = D * static_cast<int>(sizeof(T)) / 128;    // 128-byte columns
     static constexpr int kPlane = KT * D * static_cast<int>(sizeof(T));    // a K (or V) tile
     static constexpr int QR = RT < 8 ? 8 : RT;                             // q rows kept (whole swizzle atoms)
@@ -76,6 +79,7 @@ struct Geometry {
     // shared memory of a CTA, less alignment slack and the static part
     static constexpr int kBudget = (kCtas == 1 ? 232448 : 115712) - 1024 - 2560;
     static constexpr int kStages = (kBudget - 2 * kQ - kExtra) / (2 * kPlane);
+    static constexpr int kWarpKeys = KT / kWarps;
     static constexpr int kSmem = kStages * 2 * kPlane + 2 * kQ + kExtra + 1024;
     static_assert(kStages >= 2, "two stages at least");
 };
@@ -85,7 +89,7 @@ struct Geometry {
 // Bounded wait; once one gave up the CTA's later waits return at once and nothing of the
 // units concerned is written.
 __device__ __forceinline__ void wait_or_flag(uint64_t *bar, uint32_t parity, volatile int *dead) {
-    if (*dead) return;
+    if (mbar_test(bar, parity) || *dead) return;
     if (!mbar_wait(bar, parity)) {
         *dead = 1;
         atomicOr(&g_watchdog_attn_decode, WD_STAGE_COPY);
@@ -142,23 +146,19 @@ __device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Byte offset of 16-byte chunk `chunk` of row `row` in a tile of `rows` rows stored as
-// 128-byte columns with the 128-byte swizzle.
-__device__ __forceinline__ uint32_t swizzled(int rows, int row, int chunk) {
-    return static_cast<uint32_t>((chunk >> 3) * rows * 128 + row * 128 +
-                                 (((chunk & 7) ^ (row & 7)) << 4));
-}
-
-// ------------------------------------------------------------------ the mask of one tile
-
-// Keys of the tile that no row of the unit sees: their V rows are cleared, so that whatever
-// the page holds there (an infinity, a NaN) cannot reach the sum through a weight of 0.
-__device__ __forceinline__ bool key_dead(const Params &p, const Stage &st, int i) {
-    const int key = st.key0 + i;
-    const int p_first = st.len - p.n_tokens, p_last = st.len - 1;
-    return !((st.blocks >> (i >> 3)) & 1u) || key > p_last ||
-           !(p_first - key < p.mask.window || key < p.mask.sinks);
-}
+// Shared-memory tiles keep the pages' parts apart, each `rows` rows of 128 bytes for every
+// 128-byte column ([part][column][row], the 128-byte swizzle within), as one copy per part
+// brings them. Byte offset of row `row`, and of its 16-byte chunk `chunk`.
+struct Tile {
+    int log2_rows;   // rows of a part
+    int part_bytes;  // of all columns of a part
+    __device__ __forceinline__ uint32_t row(int r) const {
+        return static_cast<uint32_t>((r >> log2_rows) * part_bytes + (r & ((1 << log2_rows) - 1)) * 128);
+    }
+    __device__ __forceinline__ uint32_t chunk(int r, int c) const {
+        return static_cast<uint32_t>(((c >> 3) << (log2_rows + 7)) + (((c & 7) ^ (r & 7)) << 4));
+    }
+};
 
 // A row's output from its sums; a row that saw nothing is 0.
 __device__ __forceinline__ float finish(float o, float l, float inv) { return l == 0.0f ? 0.0f : o * inv; }
@@ -194,18 +194,20 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     uint8_t *extra = q_smem + 2 * G::kQ;
 
     __shared__ __align__(8) uint64_t full[G::kStages], empty[G::kStages], q_empty[2];
-    __shared__ Stage stages[G::kStages];
-    __shared__ long long slab_sum[kThreads];
-    __shared__ long long sh_total, sh_seq_begin;
-    __shared__ int sh_seq, sh_dead, sh_join;
+    __shared__ int2 stages[G::kStages];
+    __shared__ Segment segments[2];
+    __shared__ unsigned warp_sum[kThreads / 32];
+    __shared__ int sh_seq, sh_slot, sh_len, sh_dead, sh_join;
+    __shared__ unsigned sh_seq_begin;
     __shared__ float red[kWarps][kRows];
     __shared__ __align__(16) float row_m[kRows], row_l[kRows];
+    __shared__ float join_part[kCompute / kRows][kRows];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int subs = p.head_groups * p.token_groups;
-    const int units = p.cache.n_kv_heads * subs;
+    const unsigned units = static_cast<unsigned>(p.cache.n_kv_heads * subs);
 
-    if (tid == 0) {
+    if (tid == kCompute) {
         for (int s = 0; s < G::kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], kWarps);
@@ -214,7 +216,6 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         mbar_init(&q_empty[1], kWarps);
         fence_mbar_init();
         sh_dead = 0;
-        sh_seq = -1;
         tma_prefetch_map(&q_map);
         tma_prefetch_map(&k_map);
         tma_prefetch_map(&v_map);
@@ -222,52 +223,51 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
 
     // Tiles of one unit of sequence n (1 when it sees nothing: its rows are zeros), 0 when
     // the sequence is skipped.
-    auto tiles_of = [&](int n, int &slot, int &len) -> int {
+    auto tiles_of = [&](int n, int &slot, int &len) -> unsigned {
         if (!p.cache.lookup(n, slot, len)) return 0;
-        return max(1, walk_tiles<KT>(p.mask, len - p.n_tokens, len - 1).count);
+        return static_cast<unsigned>(max(1, walk_tiles<KT>(p.mask, len - p.n_tokens, len - 1).count));
     };
 
-    // ---- this CTA's range of tiles: sums over slabs of sequences, then their prefixes
+    // ---- this CTA's range of tiles: a thread's slab of sequences, the slabs' prefixes
     const int per = (p.n_seqs + kThreads - 1) / kThreads;
     const int n0 = min(tid * per, p.n_seqs), n1 = min(n0 + per, p.n_seqs);
-    long long sum = 0;
+    unsigned sum = 0;
+    int slot0 = 0, len0 = 0;
     for (int n = n0; n < n1; ++n) {
-        int slot, len;
-        const int t = tiles_of(n, slot, len);
+        const unsigned t = tiles_of(n, slot0, len0);
         if (t == 0 && blockIdx.x == 0 && p.err_count) atomicAdd(p.err_count, 1);
-        sum += static_cast<long long>(t) * units;
+        sum += t * units;
     }
-    slab_sum[tid] = sum;
-    __syncthreads();
-    if (warp == 0) {
-        long long run = 0;
-        for (int base = 0; base < kThreads; base += 32) {
-            const long long own = slab_sum[base + lane];
-            long long x = own;
+    unsigned before = sum;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(FULL_MASK, x, o);
-                if (lane >= o) x += y;
-            }
-            slab_sum[base + lane] = run + x - own;
-            run += __shfl_sync(FULL_MASK, x, 31);
-        }
-        if (lane == 0) sh_total = run;
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned y = __shfl_up_sync(FULL_MASK, before, o);
+        if (lane >= o) before += y;
     }
+    if (lane == 31) warp_sum[warp] = before;
+    before -= sum;
     __syncthreads();
-    const long long total = sh_total;
-    // no range is empty: the CTAs of a split unit are consecutive and all of them arrive
-    const int ranges = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
-    if (static_cast<int>(blockIdx.x) >= ranges) return;
-    auto range_begin = [&](int c) { return total * c / ranges; };
-    const long long begin = range_begin(blockIdx.x), end = range_begin(blockIdx.x + 1);
-    if (begin >= slab_sum[tid] && begin < slab_sum[tid] + sum) {
-        long long at = slab_sum[tid];
+    unsigned total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        total += warp_sum[w];
+    }
+    // The ranges: no range is empty, so the CTAs of a split unit are consecutive and all of
+    // them arrive; the first `longer` hold one tile more.
+    const unsigned ranges = min(gridDim.x, total);
+    if (blockIdx.x >= ranges) return;
+    const unsigned each = total / ranges, longer = total - each * ranges;
+    auto range_begin = [&](unsigned c) { return c * each + min(c, longer); };
+    const unsigned begin = range_begin(blockIdx.x), end = range_begin(blockIdx.x + 1);
+    if (begin >= before && begin < before + sum) {
+        unsigned at = before;
         for (int n = n0; n < n1; ++n) {
-            int slot, len;
-            const long long w = static_cast<long long>(tiles_of(n, slot, len)) * units;
+            const unsigned w = (per == 1 ? sum : tiles_of(n, slot0, len0) * units);
             if (begin < at + w) {
                 sh_seq = n;
+                sh_slot = slot0;
+                sh_len = len0;
                 sh_seq_begin = at;
                 break;
             }
@@ -278,105 +278,107 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
 
     auto k_tile = [&](int s) { return smem + s * 2 * G::kPlane; };
     auto v_tile = [&](int s) { return smem + s * 2 * G::kPlane + G::kPlane; };
+    constexpr int kLog2KT = KT == 128 ? 7 : KT == 64 ? 6 : 5;
+    const int log2_box = min(p.cache.log2_ps, kLog2KT);  // keys of a page's part of a tile
+    const Tile tile{log2_box, D * static_cast<int>(sizeof(T)) << log2_box};
 
     if (warp == kWarps) {
         // ---------------------------------------------------------- the loading warp
+        // The warp runs converged, one elected lane issuing.
+        const bool leader = elect_one();
         const int ps = 1 << p.cache.log2_ps;
-        const int box = min(ps, KT);  // rows of one load
-        const int n_box = KT / box;   // loads of a tile's 128-byte column, one lane each
-        int n = sh_seq, slot = 0, len = 0;
-        long long seq_begin = sh_seq_begin, at = begin;
-        int tiles = tiles_of(n, slot, len);
+        const int box = 1 << log2_box, n_box = KT >> log2_box;
+        const unsigned lane_blocks = ((1u << (box / 8)) - 1u) << ((lane * (box / 8)) & 31);
+        int n = sh_seq, slot = sh_slot, len = sh_len;
+        unsigned seq_begin = sh_seq_begin, at = begin;
         TileWalk walk = walk_tiles<KT>(p.mask, len - p.n_tokens, len - 1);
-        int it = 0, seg = 0;
+        unsigned tiles = static_cast<unsigned>(max(1, walk.count));
+        unsigned unit = (at - seq_begin) / tiles;
+        int st = 0, seg = 0;
+        unsigned st_round = 0;
         while (at < end) {
-            const int unit = static_cast<int>((at - seq_begin) / tiles);
-            const long long unit_begin = seq_begin + static_cast<long long>(unit) * tiles;
-            const long long unit_end = unit_begin + tiles;
-            const long long seg_end = unit_end < end ? unit_end : end;
-            const int kvh = unit / subs, sub = unit % subs;
+            const unsigned unit_begin = seq_begin + unit * tiles, unit_end = unit_begin + tiles;
+            const unsigned seg_end = min(unit_end, end);
+            const int kvh = static_cast<int>(unit) / subs, sub = static_cast<int>(unit) % subs;
             const int hg = sub / p.token_groups, tg = sub % p.token_groups;
             const bool whole = at == unit_begin && seg_end == unit_end;
-            int c0 = 0, c1 = 0;
-            if (!whole) {
-                auto owner = [&](long long x) {
-                    int c = static_cast<int>(x * ranges / total);
-                    while (c + 1 < ranges && range_begin(c + 1) <= x) ++c;
-                    while (c > 0 && range_begin(c) > x) --c;
-                    return c;
-                };
-                c0 = owner(unit_begin);
-                c1 = owner(unit_end - 1);
-            }
-            int i = static_cast<int>(at - unit_begin);
-            // page of this lane's box of tile i, looked up one tile ahead of its load
+            // the page of lane i's part of a tile, looked up one tile ahead of its load; -1 for a
+            // part nobody sees (its id is not read: pages before the window may be gone)
             auto page_at = [&](int idx) -> int {
                 if (walk.count == 0 || lane >= n_box) return -1;
                 const int key = walk.tile(idx) * KT + lane * box;
-                const int p_first = len - p.n_tokens;
                 if (key > len - 1) return -1;
-                // pages wholly before the window may be gone already: not looked up
-                if (!(p_first - (key + box - 1) < p.mask.window || key < p.mask.sinks)) return -1;
+                if (!(len - p.n_tokens - (key + box - 1) < p.mask.window || key < p.mask.sinks)) return -1;
                 const int page = p.cache.page_of(slot, key);
-                if (p.cache.page_ok(page)) return page;
-                if (p.err_count && unit == 0) atomicAdd(p.err_count, 1);
-                return -1;
+                if (unit == 0 && p.err_count && !p.cache.page_ok(page)) atomicAdd(p.err_count, 1);
+                return page;
             };
+            int i = static_cast<int>(at - unit_begin);
             int page = page_at(i);
-            for (bool first = true; at < seg_end; ++at, ++i, ++it, first = false) {
-                const int s = it % G::kStages;
+            // the segment, and q
+            if (seg >= 2) wait_or_flag(&q_empty[seg & 1], ((seg >> 1) - 1) & 1, &sh_dead);
+            if (leader) {
+                Segment sg;
+                sg.seq = n;
+                sg.kvh = kvh;
+                sg.head_group = hg;
+                sg.token_group = tg;
+                sg.len = len;
+                sg.flags = (whole ? kWhole : 0) | (unit_begin >= begin ? kHead : 0);
+                sg.c0 = sg.c1 = 0;
+                if (!whole) {
+                    auto owner = [&](unsigned x) {
+                        const unsigned split = longer * (each + 1);
+                        return static_cast<int>(x < split ? x / (each + 1) : longer + (x - split) / each);
+                    };
+                    sg.c0 = owner(unit_begin);
+                    sg.c1 = owner(unit_end - 1);
+                }
+                segments[seg & 1] = sg;
+            }
+            for (bool first = true; at < seg_end; ++at, ++i, first = false) {
                 const int next_page = at + 1 < seg_end ? page_at(i + 1) : -1;
-                if (it >= G::kStages)
-                    wait_or_flag(&empty[s], ((it / G::kStages) - 1) & 1, &sh_dead);
-                if (first && seg >= 2) wait_or_flag(&q_empty[seg & 1], ((seg >> 1) - 1) & 1, &sh_dead);
-                const unsigned have = __ballot_sync(FULL_MASK, page >= 0);
+                if (st_round > 0) wait_or_flag(&empty[st], (st_round - 1) & 1, &sh_dead);
                 const int key0 = walk.count ? walk.tile(i) * KT : 0;
-                if (lane == 0) {
-                    Stage st;
-                    st.seq = n;
-                    st.unit = unit;
-                    st.len = len;
-                    st.key0 = key0;
-                    st.flags = (first ? kFirst : 0) | (at + 1 == seg_end ? kLast : 0) |
-                               (whole ? kWhole : 0) | (unit_begin >= begin ? kHead : 0);
-                    st.blocks = 0;
-                    for (int b = 0; b < KT / 8; ++b)
-                        if ((have >> (b * 8 / box)) & 1u) st.blocks |= 1u << b;
-                    st.c0 = c0;
-                    st.c1 = c1;
-                    stages[s] = st;
+                const bool ok = p.cache.page_ok(page);
+                const unsigned have = __ballot_sync(FULL_MASK, ok);
+                const unsigned blocks = __reduce_or_sync(FULL_MASK, ok ? lane_blocks : 0u);
+                const int row = (page * p.cache.n_kv_heads + kvh) * ps + (key0 & (ps - 1));
+                if (leader) {
+                    stages[st] = make_int2(key0, (first ? kFirst : 0) | (at + 1 == seg_end ? kLast : 0) |
+                                                     static_cast<int>(blocks << 8));
                     const int q_rows = p.heads_per_unit * p.tokens_per_unit;
                     mbar_arrive_expect_tx(
-                        &full[s], static_cast<uint32_t>(__popc(have) * box) * D * sizeof(T) * 2u +
-                                      (first ? static_cast<uint32_t>(q_rows) * D * sizeof(T) : 0u));
+                        &full[st], (static_cast<uint32_t>(__popc(have)) << log2_box) * D * sizeof(T) * 2u +
+                                       (first ? static_cast<uint32_t>(q_rows) * D * sizeof(T) : 0u));
                     if (first) {
                         const int head0 = kvh * p.group + hg * p.heads_per_unit;
                         const int token0 = n * p.n_tokens + tg * p.tokens_per_unit;
 #pragma unroll
                         for (int cb = 0; cb < G::kCols; ++cb)
                             tma_load_3d(q_smem + (seg & 1) * G::kQ + cb * G::QR * 128, &q_map,
-                                        cb * static_cast<int>(128 / sizeof(T)), head0, token0,
-                                        &full[s]);
+                                        cb * static_cast<int>(128 / sizeof(T)), head0, token0, &full[st]);
                     }
                 }
                 __syncwarp();
-                if (page >= 0) {
-                    const int row = (page * p.cache.n_kv_heads + kvh) * ps +
-                                    (ps > KT ? (key0 & (ps - 1)) : 0);
-#pragma unroll
-                    for (int cb = 0; cb < G::kCols; ++cb)
-                        tma_load_2d(k_tile(s) + cb * KT * 128 + lane * box * 128, &k_map,
-                                    cb * static_cast<int>(128 / sizeof(T)), row, &full[s]);
-#pragma unroll
-                    for (int cb = 0; cb < G::kCols; ++cb)
-                        tma_load_2d(v_tile(s) + cb * KT * 128 + lane * box * 128, &v_map,
-                                    cb * static_cast<int>(128 / sizeof(T)), row, &full[s]);
+                for (int b = 0; b < n_box; ++b) {
+                    const int r = __shfl_sync(FULL_MASK, row, b);
+                    if (leader && ((have >> b) & 1u)) {
+                        tma_load_3d(k_tile(st) + b * tile.part_bytes, &k_map, 0, r, 0, &full[st]);
+                        tma_load_3d(v_tile(st) + b * tile.part_bytes, &v_map, 0, r, 0, &full[st]);
+                    }
+                }
+                __syncwarp();
+                if (++st == G::kStages) {
+                    st = 0;
+                    ++st_round;
                 }
                 page = next_page;
             }
             ++seg;
-            if (at == unit_end && unit == units - 1 && at < end) {
+            if (at == unit_end && ++unit == units && at < end) {
                 seq_begin = unit_end;
+                unit = 0;
                 do {
                     tiles = tiles_of(++n, slot, len);
                 } while (tiles == 0 && n + 1 < p.n_seqs);
@@ -392,6 +394,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     const int n_tiles = static_cast<int>(end - begin);
     // 16-bit: NT tiles of 8 columns (a quarter of the head), rows lane/4 and lane/4 + 8
     constexpr int NT = D / 32;
+    constexpr int KN = G::kWarpKeys / 8;  // 8-key tiles of S of a warp
     float o16[G::kF32 ? 1 : NT][4];
     uint32_t qf[G::kF32 ? 1 : D / 16][4];
     // fp32: LPR threads to a row in the softmax; in P V a lane holds 4 columns, C4 lanes
@@ -401,33 +404,42 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     constexpr int NKG = 32 / C4;
     float o32[G::kF32 ? RT : 1][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-    int seg = 0;
+    Segment sg;
+    int pos0 = 0, pos1 = 0;  // positions of this thread's rows
+    int seg = 0, s = 0;
+    uint32_t phase = 0;
 
     for (int it = 0; it < n_tiles; ++it) {
-        const int s = it % G::kStages;
-        wait_or_flag(&full[s], (it / G::kStages) & 1, &sh_dead);
-        const Stage st = stages[s];
-        const int kvh = st.unit / subs, sub = st.unit % subs;
-        const int hg = sub / p.token_groups, tg = sub % p.token_groups;
-        const int p_first = st.len - p.n_tokens, p_last = st.len - 1;
-        const bool clean = st.blocks == (1u << (KT / 8)) - 1u && st.key0 + KT - 1 <= p_first &&
-                           (p_last - st.key0 < p.mask.window || st.key0 + KT <= p.mask.sinks);
-        // position of row r of the unit
-        auto position = [&](int r) { return p_first + tg * p.tokens_per_unit + r / p.heads_per_unit; };
-        auto sees = [&](int r, int i) {
-            return ((st.blocks >> (i >> 3)) & 1u) && p.mask.sees(position(r), st.key0 + i);
-        };
-        if (st.flags & kFirst) {
+        wait_or_flag(&full[s], phase, &sh_dead);
+        const int2 stage = stages[s];
+        const int key0 = stage.x, flags = stage.y;
+        const unsigned blocks = static_cast<unsigned>(stage.y) >> 8;
+        if (flags & kFirst) {
+            sg = segments[seg & 1];
             m0 = m1 = -INFINITY;
             l0 = l1 = 0.0f;
+            const int base = sg.len - p.n_tokens + sg.token_group * p.tokens_per_unit;
+            // 16-bit: rows lane / 4 and lane / 4 + 8; fp32: the row of this thread's scores
+            pos0 = base + (G::kF32 ? tid / LPR : lane >> 2) / p.heads_per_unit;
+            pos1 = base + ((lane >> 2) + 8) / p.heads_per_unit;
         }
+        const int p_first = sg.len - p.n_tokens, p_last = sg.len - 1;
+        const bool clean = blocks == (1u << (KT / 8)) - 1u && key0 + KT - 1 <= p_first &&
+                           (p_last - key0 < p.mask.window || key0 + KT <= p.mask.sinks);
         if (!clean) {
-            // this warp's keys of the tile
-            for (int i = warp * (KT / kWarps); i < (warp + 1) * (KT / kWarps); ++i) {
-                if (key_dead(p, st, i))
-                    for (int c = lane; c < G::kCols * 8; c += 32)
-                        *reinterpret_cast<uint4 *>(v_tile(s) + swizzled(KT, i, c)) =
-                            make_uint4(0, 0, 0, 0);
+            // Keys of this warp's part of the tile that no row of the unit sees: their V rows
+            // are cleared, so that whatever the page holds there (an infinity, a NaN) cannot
+            // reach the sum through a weight of 0.
+            const int i = warp * G::kWarpKeys + lane, key = key0 + i;
+            const bool dead = lane < G::kWarpKeys &&
+                              (!((blocks >> ((i >> 3) & 31)) & 1u) || key > p_last ||
+                               !(p_first - key < p.mask.window || key < p.mask.sinks));
+            unsigned left = __ballot_sync(FULL_MASK, dead);
+            while (left != 0) {
+                const int r = warp * G::kWarpKeys + __ffs(left) - 1;
+                left &= left - 1;
+                for (int c = lane; c < G::kCols * 8; c += 32)
+                    *reinterpret_cast<uint4 *>(v_tile(s) + tile.row(r) + tile.chunk(r, c)) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();  // before the stage's next copy overwrites them
         }
@@ -435,11 +447,12 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
 
         if constexpr (!G::kF32) {
             const uint32_t ks = smem_addr(k_tile(s)), vs = smem_addr(v_tile(s));
-            if (st.flags & kFirst) {
+            if (flags & kFirst) {
                 const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
+                const Tile q_tile{4, 0};
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    ldsm4(qf[kk], smem_addr(q_here) + swizzled(G::QR, r, 2 * kk + (lane >> 4)));
+                    ldsm4(qf[kk], smem_addr(q_here) + r * 128 + q_tile.chunk(r, 2 * kk + (lane >> 4)));
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_empty[seg & 1]);
 #pragma unroll
@@ -447,31 +460,45 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o16[j][e] = 0.0f;
             }
-            // S = Q K^T for 16 keys, two chains of products per 8 keys
-            float acc[2][2][4] = {};
-            const int key = warp * 16 + (lane & 7) + (lane >> 4) * 8;
+            // S = Q K^T for this warp's keys, 16 at a time (two chains of products per 8 keys)
+            float sc[KN][4];
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                uint32_t b[4];
-                ldsm4(b, ks + swizzled(KT, key, 2 * kk + ((lane >> 3) & 1)));
-                mma16816<T>(acc[kk & 1][0], qf[kk], b[0], b[1]);
-                mma16816<T>(acc[kk & 1][1], qf[kk], b[2], b[3]);
+            for (int h = 0; h < KN / 2; ++h) {
+                float acc[2][2][4] = {};
+                const int key = warp * G::kWarpKeys + h * 16 + (lane & 7) + (lane >> 4) * 8;
+                const uint32_t kr = ks + tile.row(key);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    uint32_t b[4];
+                    ldsm4(b, kr + tile.chunk(key, 2 * kk + ((lane >> 3) & 1)));
+                    mma16816<T>(acc[kk & 1][0], qf[kk], b[0], b[1]);
+                    mma16816<T>(acc[kk & 1][1], qf[kk], b[2], b[3]);
+                }
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sc[2 * h + b][e] = (acc[0][b][e] + acc[1][b][e]) * p.scale_log2;
+            }
+            if (!clean) {
+#pragma unroll
+                for (int b = 0; b < KN; ++b)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = warp * G::kWarpKeys + b * 8 + 2 * (lane & 3) + (e & 1);
+                        if (!((blocks >> (i >> 3)) & 1u) || !p.mask.sees(e < 2 ? pos0 : pos1, key0 + i))
+                            sc[b][e] = -INFINITY;
+                    }
             }
             const int r0 = lane >> 2;
-            float sc[2][4];
+            float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    sc[b][e] = (acc[0][b][e] + acc[1][b][e]) * p.scale_log2;
-                    if (!clean && !sees(e < 2 ? r0 : r0 + 8,
-                                        warp * 16 + b * 8 + 2 * (lane & 3) + (e & 1)))
-                        sc[b][e] = -INFINITY;
-                }
-            const float t0 =
-                group_max<4>(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1])));
-            const float t1 =
-                group_max<4>(fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3])));
+            for (int b = 0; b < KN; ++b) {
+                t0 = fmaxf(t0, fmaxf(sc[b][0], sc[b][1]));
+                t1 = fmaxf(t1, fmaxf(sc[b][2], sc[b][3]));
+            }
+            t0 = group_max<4>(t0);
+            t1 = group_max<4>(t1);
             if ((lane & 3) == 0) {
                 red[warp][r0] = t0;
                 red[warp][r0 + 8] = t1;
@@ -493,12 +520,12 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             l0 *= corr0;
             l1 *= corr1;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < KN; ++b) {
                 const float x0 = fast_exp2(sc[b][0] - base0), x1 = fast_exp2(sc[b][1] - base0);
                 const float y0 = fast_exp2(sc[b][2] - base1), y1 = fast_exp2(sc[b][3] - base1);
                 l0 += x0 + x1;
                 l1 += y0 + y1;
-                const int col = warp * 16 + b * 8 + 2 * (lane & 3);
+                const int col = warp * G::kWarpKeys + b * 8 + 2 * (lane & 3);
                 const uint32_t oa = static_cast<uint32_t>(r0 * (KT + 8) + col) * 2u;
                 const uint32_t ob = oa + 8 * (KT + 8) * 2u;
                 const uint32_t xh = Elem<T>::pack(x0, x1), yh = Elem<T>::pack(y0, y1);
@@ -524,10 +551,11 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                 ldsm4(ah, smem_addr(ph) + poff + kk * 32);
                 ldsm4(al, smem_addr(pl) + poff + kk * 32);
                 const int vrow = kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+                const uint32_t vr = vs + tile.row(vrow);
 #pragma unroll
                 for (int j = 0; j < NT; j += 2) {
                     uint32_t b[4];
-                    ldsm4_trans(b, vs + swizzled(KT, vrow, warp * NT + j + (lane >> 4)));
+                    ldsm4_trans(b, vr + tile.chunk(vrow, warp * NT + j + (lane >> 4)));
                     mma16816<T>(o16[j], ah, b[0], b[1]);
                     mma16816<T>(o16[j + 1], ah, b[2], b[3]);
                     mma16816<T>(o16[j], al, b[0], b[1]);
@@ -539,29 +567,31 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             // S, then P: [KT][RT]. Two buffers in turn: a warp may start on the next tile's
             // S while another still reads this tile's P
             float *sp = reinterpret_cast<float *>(extra) + (it & 1) * KT * RT;
-            if (st.flags & kFirst) {
+            if (flags & kFirst) {
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o32[r][e] = 0.0f;
             }
-            {
-                // lane: one key of the warp's 8 and a quarter of the dot product
-                const int i = warp * 8 + (lane & 7), quarter = lane >> 3;
+#pragma unroll 1
+            for (int h = 0; h < G::kWarpKeys / 8; ++h) {
+                // lane: one key of 8 and a quarter of the dot product
+                const int i = warp * G::kWarpKeys + h * 8 + (lane & 7), quarter = lane >> 3;
                 // the quarters' lanes start at chunks in different banks
                 const int turn = D >= 128 ? 2 * quarter : quarter >> 1;
+                const uint8_t *kr = k_tile(s) + tile.row(i);
+                const Tile q_tile{G::QR == 8 ? 3 : 4, 0};
                 float acc[RT];
 #pragma unroll
                 for (int r = 0; r < RT; ++r) acc[r] = 0.0f;
-#pragma unroll 4
+#pragma unroll (RT == 16 ? 1 : RT == 8 ? 2 : 4)
                 for (int c = 0; c < D / 16; ++c) {
                     const int chunk = quarter * (D / 16) + (c ^ turn);
-                    const float4 kv =
-                        *reinterpret_cast<const float4 *>(k_tile(s) + swizzled(KT, i, chunk));
+                    const float4 kv = *reinterpret_cast<const float4 *>(kr + tile.chunk(i, chunk));
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
                         const float4 qv =
-                            *reinterpret_cast<const float4 *>(q_here + swizzled(G::QR, r, chunk));
+                            *reinterpret_cast<const float4 *>(q_here + r * 128 + q_tile.chunk(r, chunk));
                         acc[r] = fmaf(qv.x, kv.x, acc[r]);
                         acc[r] = fmaf(qv.y, kv.y, acc[r]);
                         acc[r] = fmaf(qv.z, kv.z, acc[r]);
@@ -572,8 +602,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                 for (int r = 0; r < RT; ++r) {
                     acc[r] += __shfl_xor_sync(FULL_MASK, acc[r], 8);
                     acc[r] += __shfl_xor_sync(FULL_MASK, acc[r], 16);
-                    if ((r & 3) == quarter)
-                        sp[i * RT + r] = clean || sees(r, i) ? acc[r] * p.scale_log2 : -INFINITY;
+                    if ((r & 3) == quarter) sp[i * RT + r] = acc[r] * p.scale_log2;
                 }
             }
             named_barrier_sync(1, kCompute);
@@ -583,7 +612,9 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                 float top = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < KT / LPR; ++i) {
-                    x[i] = sp[(part + i * LPR) * RT + r];
+                    const int k = part + i * LPR;
+                    x[i] = sp[k * RT + r];
+                    if (!clean && (!((blocks >> (k >> 3)) & 1u) || !p.mask.sees(pos0, key0 + k))) x[i] = -INFINITY;
                     top = fmaxf(top, x[i]);
                 }
                 const float old = m0;
@@ -608,13 +639,13 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o32[r][e] *= corr;
                 }
-#pragma unroll 2
+#pragma unroll (RT == 16 ? 1 : RT == 8 ? 2 : 4)
                 for (int j = 0; j < KT / NKG; ++j) {
                     // for D = 64 two keys share a quarter-warp's read: 4 apart, so that
                     // the swizzle keeps them in different banks
                     const int i = NKG == 8 ? (kg >> 1) + 4 * (kg & 1) + 8 * j : kg + NKG * j;
                     const float4 vv = *reinterpret_cast<const float4 *>(
-                        v_tile(s) + swizzled(KT, i, warp * C4 + c4));
+                        v_tile(s) + tile.row(i) + tile.chunk(i, warp * C4 + c4));
 #pragma unroll
                     for (int r = 0; r < RT; r += 4) {
                         const float4 w = *reinterpret_cast<const float4 *>(sp + i * RT + r);
@@ -632,7 +663,11 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[s]);
-        if (!(st.flags & kLast)) continue;
+        if (++s == G::kStages) {
+            s = 0;
+            phase ^= 1;
+        }
+        if (!(flags & kLast)) continue;
 
         // ---------------------------------------------------------- the segment's end
         if constexpr (G::kF32) {
@@ -668,19 +703,19 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         }
         named_barrier_sync(1, kCompute);
 
-        const int heads = min(p.heads_per_unit, p.group - hg * p.heads_per_unit);
-        const int tokens = min(p.tokens_per_unit, p.n_tokens - tg * p.tokens_per_unit);
+        const int heads = min(p.heads_per_unit, p.group - sg.head_group * p.heads_per_unit);
+        const int tokens = min(p.tokens_per_unit, p.n_tokens - sg.token_group * p.tokens_per_unit);
         // output row of row r of the unit, or -1 for a row it has not
         auto out_row = [&](int r) -> long long {
             const int t = r / p.heads_per_unit, h = r % p.heads_per_unit;
             if (t >= tokens || h >= heads) return -1;
-            return (static_cast<long long>(st.seq) * p.n_tokens + tg * p.tokens_per_unit + t) *
-                       p.n_q_heads + kvh * p.group + hg * p.heads_per_unit + h;
+            return (static_cast<long long>(sg.seq) * p.n_tokens + sg.token_group * p.tokens_per_unit + t) *
+                       p.n_q_heads + sg.kvh * p.group + sg.head_group * p.heads_per_unit + h;
         };
         T *out = static_cast<T *>(p.out);
-        const bool whole = st.flags & kWhole;
+        const bool whole = sg.flags & kWhole;
         float *record = p.partials +
-                        static_cast<size_t>(2 * blockIdx.x + ((st.flags & kHead) ? 1 : 0)) * kRecord;
+                        static_cast<size_t>(2 * blockIdx.x + ((sg.flags & kHead) ? 1 : 0)) * kRecord;
         if constexpr (!G::kF32) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -732,50 +767,94 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         __threadfence();
         named_barrier_sync(2, kCompute);
         if (tid == 0) {
-            sh_join = last_arrival(p.counters + st.c0, p.nonce, st.c1 - st.c0 + 1);
+            sh_join = last_arrival(p.counters + sg.c0, p.nonce, sg.c1 - sg.c0 + 1);
             __threadfence();
         }
         named_barrier_sync(1, kCompute);
         if (!sh_join) continue;
+        // The records' weights first: thread (g, r) takes every kGroups-th record of row r, and
+        // leaves the weights in the records in place of the maxima. Then the rows, 4 columns a
+        // thread, kJoin records' loads together.
         auto record_of = [&](int c) {
             // the first CTA holds the unit in its second record: it begins in its range
-            return p.partials + static_cast<size_t>(2 * c + (c == st.c0 ? 1 : 0)) * kRecord;
+            return p.partials + static_cast<size_t>(2 * c + (c == sg.c0 ? 1 : 0)) * kRecord;
         };
-        for (int x = tid; x < kRows * (D / 4); x += kCompute) {
-            const int r = x / (D / 4), col = (x % (D / 4)) * 4;
-            const long long row = out_row(r);
-            if (row < 0) continue;
+        constexpr int kGroups = kCompute / kRows;
+        {
+            const int r = tid % kRows, g = tid / kRows;
             float top = -INFINITY;
-            bool dead = false;
 #pragma unroll 4
-            for (int c = st.c0; c <= st.c1; ++c) {
+            for (int c = sg.c0 + g; c <= sg.c1; c += kGroups)
                 top = fmaxf(top, __ldcg(record_of(c) + kRows * D + r));
-                dead |= __ldcg(record_of(c) + kRows * D + kRows + r) < 0.0f;
-            }
+            join_part[g][r] = top;
+            named_barrier_sync(2, kCompute);
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) top = fmaxf(top, join_part[k][r]);
             const float base = top == -INFINITY ? 0.0f : top;
             float l = 0.0f;
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            bool dead = false;
 #pragma unroll 4
-            for (int c = st.c0; c <= st.c1; ++c) {
-                const float w = fast_exp2(__ldcg(record_of(c) + kRows * D + r) - base);
-                const float4 a = __ldcg(reinterpret_cast<const float4 *>(record_of(c) + r * D + col));
-                l = fmaf(w, __ldcg(record_of(c) + kRows * D + kRows + r), l);
-                o.x = fmaf(w, a.x, o.x);
-                o.y = fmaf(w, a.y, o.y);
-                o.z = fmaf(w, a.z, o.z);
-                o.w = fmaf(w, a.w, o.w);
+            for (int c = sg.c0 + g; c <= sg.c1; c += kGroups) {
+                float *m = record_of(c) + kRows * D + r;
+                const float w = fast_exp2(__ldcg(m) - base), part = __ldcg(m + kRows);
+                __stcg(m, w);
+                l = fmaf(w, part, l);
+                dead |= part < 0.0f;
             }
-            if (dead) continue;
-            const float inv = 1.0f / l;
-            o = make_float4(finish(o.x, l, inv), finish(o.y, l, inv), finish(o.z, l, inv),
-                            finish(o.w, l, inv));
+            named_barrier_sync(1, kCompute);  // the maxima have been read
+            join_part[g][r] = dead ? -1.0f : l;
+            __threadfence_block();
+            named_barrier_sync(2, kCompute);
+            if (tid < kRows) {
+                float sum_l = 0.0f;
+                bool any_dead = false;
+#pragma unroll
+                for (int k = 0; k < kGroups; ++k) {
+                    any_dead |= join_part[k][tid] < 0.0f;
+                    sum_l += join_part[k][tid];
+                }
+                row_l[tid] = any_dead ? -1.0f : sum_l;
+            }
+            named_barrier_sync(1, kCompute);
+        }
+        const int n_items = tokens * p.heads_per_unit * (D / 4);
+#pragma unroll 1
+        for (int item = tid; item < n_items; item += kCompute) {
+            const int r = item / (D / 4), col = (item % (D / 4)) * 4;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+            for (int c = sg.c0; c <= sg.c1; c += kJoin) {
+                float4 x[kJoin];
+                float w[kJoin];
+#pragma unroll
+                for (int k = 0; k < kJoin; ++k) {
+                    const bool in = c + k <= sg.c1;
+                    const float *rec = record_of(in ? c + k : sg.c1);
+                    x[k] = __ldcg(reinterpret_cast<const float4 *>(rec + r * D + col));
+                    w[k] = in ? __ldcg(rec + kRows * D + r) : 0.0f;
+                }
+#pragma unroll
+                for (int k = 0; k < kJoin; ++k) {
+                    if (w[k] == 0.0f) continue;  // a record that saw nothing may hold anything
+                    o.x = fmaf(w[k], x[k].x, o.x);
+                    o.y = fmaf(w[k], x[k].y, o.y);
+                    o.z = fmaf(w[k], x[k].z, o.z);
+                    o.w = fmaf(w[k], x[k].w, o.w);
+                }
+            }
+            const long long row = out_row(r);
+            const float l = row_l[r], inv = 1.0f / l;
+            if (row < 0 || l < 0.0f) continue;
+            const float4 y = make_float4(finish(o.x, l, inv), finish(o.y, l, inv), finish(o.z, l, inv),
+                                         finish(o.w, l, inv));
             if constexpr (G::kF32) {
-                *reinterpret_cast<float4 *>(out + row * D + col) = o;
+                *reinterpret_cast<float4 *>(out + row * D + col) = y;
             } else {
                 *reinterpret_cast<uint2 *>(out + row * D + col) =
-                    make_uint2(Elem<T>::pack(o.x, o.y), Elem<T>::pack(o.z, o.w));
+                    make_uint2(Elem<T>::pack(y.x, y.y), Elem<T>::pack(y.z, y.w));
             }
         }
+        named_barrier_sync(2, kCompute);  // row_l has been read
     }
 }
 
@@ -920,17 +999,21 @@ gdn_status gdn_attn_decode(const void *q, const void *k_pages, const void *v_pag
     p.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + kCounterBytes);
     p.nonce = next_nonce();
 
+    // the ranges are counted in 32 bits (2^31 tiles are some 70 TB read in one call)
+    const int kt = (head_dim == 64 ? 2 : 1) * (dtype == GDN_F32 ? 32 : 64);
+    const long long widest = (static_cast<long long>(max_pages) * page_size + kt - 1) / kt + 2;
+    if (widest * n_kv_heads * sp.head_groups * sp.token_groups > 0x7fffffffLL / n_seqs)
+        return GDN_ERR_UNSUPPORTED;
     CUtensorMap q_map, k_map, v_map;
     const uint64_t rows = static_cast<uint64_t>(n_pages) * n_kv_heads * page_size;
-    const int kt = dtype == GDN_F32 ? 32 : 64;
-    const int box = page_size < kt ? page_size : kt;
+    const int box = page_size < kt ? page_size : kt, cols = head_dim * es / 128;
     GDN_TRY(encode_heads_map(&q_map, q, dtype, head_dim, n_q_heads,
                              static_cast<uint64_t>(n_seqs) * n_tokens,
                              static_cast<uint64_t>(q_stride) * es, sp.heads, sp.tokens));
-    GDN_TRY(encode_rows_map(&k_map, k_pages, dtype, head_dim, rows,
-                            static_cast<uint64_t>(head_dim) * es, box));
-    GDN_TRY(encode_rows_map(&v_map, v_pages, dtype, head_dim, rows,
-                            static_cast<uint64_t>(head_dim) * es, box));
+    GDN_TRY(encode_blocks_map(&k_map, k_pages, dtype, head_dim, rows,
+                              static_cast<uint64_t>(head_dim) * es, box, cols));
+    GDN_TRY(encode_blocks_map(&v_map, v_pages, dtype, head_dim, rows,
+                              static_cast<uint64_t>(head_dim) * es, box, cols));
     const cudaStream_t s = as_cuda(stream);
     switch (dtype) {
         case GDN_F32: return launch_dim<float>(head_dim, q_map, k_map, v_map, p, s);
