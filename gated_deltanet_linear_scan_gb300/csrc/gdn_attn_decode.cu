@@ -46,7 +46,7 @@ enum : int { kFirst = 1, kLast = 2, kWhole = 4, kHead = 8 };  // kWhole, kHead: 
 // loaded), and about a segment, the part of a unit in this CTA's range.
 struct Segment {
     int seq, kvh, head_group, token_group, len, flags;
-    int c0, c1;  // CTAs sharing the unit (when it is not whole here)
+    unsigned unit_begin, unit_end;  // the unit's tiles
 };
 
 struct Params {
@@ -96,20 +96,33 @@ __device__ __forceinline__ void wait_or_flag(uint64_t *bar, uint32_t parity, vol
     }
 }
 
-// One more of the `n` CTAs of a unit has stored its partial result. True in the CTA that
-// completes the count, which also clears the word. A word whose upper bits are not this
-// call's nonce counts as 0, so the workspace needs no initialisation; a captured call keeps
-// its nonce over its replays, each of which leaves the words cleared.
+// Counting the CTAs of a split unit that have stored their partial results. The word's upper
+// 48 bits say whose count it is: this call's nonce, or anything else, which counts as 0 (so the
+// workspace needs no initialisation). The CTA that completes the count clears the word; a
+// captured call keeps its nonce over its replays, each of which leaves the words cleared.
+// Ahead of the arrival a word seen untagged is tagged, so that an arrival is one addition.
+__device__ __forceinline__ bool tagged(unsigned long long word, unsigned long long nonce) {
+    return (word >> 16) == nonce;
+}
+
 __device__ __forceinline__ bool last_arrival(unsigned long long *word, unsigned long long nonce,
                                              int n) {
-    unsigned long long seen = *reinterpret_cast<volatile unsigned long long *>(word);
-    for (;;) {
-        const int count = (seen >> 16) == nonce ? static_cast<int>(seen & 0xFFFFu) : 0;
-        const unsigned long long next = count + 1 == n ? 0 : (nonce << 16) | (count + 1);
-        const unsigned long long was = atomicCAS(word, seen, next);
-        if (was == seen) return count + 1 == n;
-        seen = was;
+    unsigned long long seen = atomicAdd(word, 1ull);
+    if (!tagged(seen, nonce)) {  // the addition went to an untagged word: count again
+        seen = *reinterpret_cast<volatile unsigned long long *>(word);
+        for (;;) {
+            const unsigned long long next = tagged(seen, nonce) ? seen + 1 : (nonce << 16) | 1ull;
+            const unsigned long long was = atomicCAS(word, seen, next);
+            if (was == seen) {
+                seen = next - 1;
+                break;
+            }
+            seen = was;
+        }
     }
+    if (static_cast<int>(seen & 0xFFFFu) + 1 != n) return false;
+    atomicExch(word, 0ull);
+    return true;
 }
 
 // ------------------------------------------------------------------ matrix fragments
@@ -260,6 +273,10 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     const unsigned each = total / ranges, longer = total - each * ranges;
     auto range_begin = [&](unsigned c) { return c * each + min(c, longer); };
     const unsigned begin = range_begin(blockIdx.x), end = range_begin(blockIdx.x + 1);
+    auto owner = [&](unsigned x) {  // of tile x
+        const unsigned split = longer * (each + 1);
+        return static_cast<int>(x < split ? x / (each + 1) : longer + (x - split) / each);
+    };
     if (begin >= before && begin < before + sum) {
         unsigned at = before;
         for (int n = n0; n < n1; ++n) {
@@ -299,8 +316,13 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         while (at < end) {
             const unsigned unit_begin = seq_begin + unit * tiles, unit_end = unit_begin + tiles;
             const unsigned seg_end = min(unit_end, end);
-            const int kvh = static_cast<int>(unit) / subs, sub = static_cast<int>(unit) % subs;
-            const int hg = sub / p.token_groups, tg = sub % p.token_groups;
+            int kvh = static_cast<int>(unit), hg = 0, tg = 0;
+            if (subs > 1) {
+                kvh = static_cast<int>(unit) / subs;
+                const int sub = static_cast<int>(unit) - kvh * subs;
+                hg = sub / p.token_groups;
+                tg = sub - hg * p.token_groups;
+            }
             const bool whole = at == unit_begin && seg_end == unit_end;
             // the page of lane i's part of a tile, looked up one tile ahead of its load; -1 for a
             // part nobody sees (its id is not read: pages before the window may be gone)
@@ -325,15 +347,8 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                 sg.token_group = tg;
                 sg.len = len;
                 sg.flags = (whole ? kWhole : 0) | (unit_begin >= begin ? kHead : 0);
-                sg.c0 = sg.c1 = 0;
-                if (!whole) {
-                    auto owner = [&](unsigned x) {
-                        const unsigned split = longer * (each + 1);
-                        return static_cast<int>(x < split ? x / (each + 1) : longer + (x - split) / each);
-                    };
-                    sg.c0 = owner(unit_begin);
-                    sg.c1 = owner(unit_end - 1);
-                }
+                sg.unit_begin = unit_begin;
+                sg.unit_end = unit_end;
                 segments[seg & 1] = sg;
             }
             for (bool first = true; at < seg_end; ++at, ++i, first = false) {
@@ -405,7 +420,12 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     float o32[G::kF32 ? RT : 1][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
     Segment sg;
-    int pos0 = 0, pos1 = 0;  // positions of this thread's rows
+    // rows of this thread (16-bit: lane / 4 and lane / 4 + 8; fp32: the row of its scores):
+    // token and head in the unit, position
+    const int row0 = G::kF32 ? tid / LPR : lane >> 2, row1 = (lane >> 2) + 8;
+    const int tok0 = row0 / p.heads_per_unit, tok1 = row1 / p.heads_per_unit;
+    int pos0 = 0, pos1 = 0;
+    unsigned long long word_seen = 0;
     int seg = 0, s = 0;
     uint32_t phase = 0;
 
@@ -419,9 +439,10 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             m0 = m1 = -INFINITY;
             l0 = l1 = 0.0f;
             const int base = sg.len - p.n_tokens + sg.token_group * p.tokens_per_unit;
-            // 16-bit: rows lane / 4 and lane / 4 + 8; fp32: the row of this thread's scores
-            pos0 = base + (G::kF32 ? tid / LPR : lane >> 2) / p.heads_per_unit;
-            pos1 = base + ((lane >> 2) + 8) / p.heads_per_unit;
+pos0 = base + tok0;
+            pos1 = base + tok1;
+            if (tid == 0 && !(sg.flags & kWhole))
+                word_seen = *reinterpret_cast<volatile unsigned long long *>(p.counters + owner(sg.unit_begin));
         }
         const int p_first = sg.len - p.n_tokens, p_last = sg.len - 1;
         const bool clean = blocks == (1u << (KT / 8)) - 1u && key0 + KT - 1 <= p_first &&
@@ -434,12 +455,19 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             const bool dead = lane < G::kWarpKeys &&
                               (!((blocks >> ((i >> 3) & 31)) & 1u) || key > p_last ||
                                !(p_first - key < p.mask.window || key < p.mask.sinks));
-            unsigned left = __ballot_sync(FULL_MASK, dead);
-            while (left != 0) {
-                const int r = warp * G::kWarpKeys + __ffs(left) - 1;
-                left &= left - 1;
-                for (int c = lane; c < G::kCols * 8; c += 32)
-                    *reinterpret_cast<uint4 *>(v_tile(s) + tile.row(r) + tile.chunk(r, c)) = make_uint4(0, 0, 0, 0);
+            const unsigned left = __ballot_sync(FULL_MASK, dead);
+            if (left != 0) {
+                constexpr int kChunks = G::kCols * 8, kLanes = kChunks < 32 ? kChunks : 32;
+                constexpr int kStep = 32 / kLanes;  // rows at a time
+#pragma unroll 4
+                for (int x = lane / kLanes; x < G::kWarpKeys; x += kStep) {
+                    if (!((left >> x) & 1u)) continue;
+                    const int r = warp * G::kWarpKeys + x;
+                    uint8_t *row = v_tile(s) + tile.row(r);
+#pragma unroll
+                    for (int c = lane % kLanes; c < kChunks; c += kLanes)
+                        *reinterpret_cast<uint4 *>(row + tile.chunk(r, c)) = make_uint4(0, 0, 0, 0);
+                }
             }
             fence_proxy_async_smem();  // before the stage's next copy overwrites them
         }
@@ -481,16 +509,23 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                         sc[2 * h + b][e] = (acc[0][b][e] + acc[1][b][e]) * p.scale_log2;
             }
             if (!clean) {
+                // keys of the tile that a row sees: [lo, hi] and, up to hi, those below `sink`
+                const int hi0 = pos0 - key0, hi1 = pos1 - key0, sink = p.mask.sinks - key0;
+                const int lo0 = hi0 < p.mask.window ? 0 : hi0 - p.mask.window + 1;
+                const int lo1 = hi1 < p.mask.window ? 0 : hi1 - p.mask.window + 1;
 #pragma unroll
-                for (int b = 0; b < KN; ++b)
+                for (int b = 0; b < KN; ++b) {
+                    const int i0 = warp * G::kWarpKeys + b * 8;
+                    const bool there = (blocks >> (i0 >> 3)) & 1u;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int i = warp * G::kWarpKeys + b * 8 + 2 * (lane & 3) + (e & 1);
-                        if (!((blocks >> (i >> 3)) & 1u) || !p.mask.sees(e < 2 ? pos0 : pos1, key0 + i))
-                            sc[b][e] = -INFINITY;
+                        const int i = i0 + 2 * (lane & 3) + (e & 1);
+                        const bool ok = there && i <= (e < 2 ? hi0 : hi1) && (i >= (e < 2 ? lo0 : lo1) || i < sink);
+                        if (!ok) sc[b][e] = -INFINITY;
                     }
+                }
             }
-            const int r0 = lane >> 2;
+            const int r0 = row0;
             float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
             for (int b = 0; b < KN; ++b) {
@@ -573,7 +608,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o32[r][e] = 0.0f;
             }
-#pragma unroll 1
+#pragma unroll (RT <= 4 ? 2 : 1)
             for (int h = 0; h < G::kWarpKeys / 8; ++h) {
                 // lane: one key of 8 and a quarter of the dot product
                 const int i = warp * G::kWarpKeys + h * 8 + (lane & 7), quarter = lane >> 3;
@@ -663,6 +698,8 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[s]);
+        if ((flags & kFirst) && tid == 0 && !(sg.flags & kWhole) && !tagged(word_seen, p.nonce))
+            atomicCAS(p.counters + owner(sg.unit_begin), word_seen, p.nonce << 16);
         if (++s == G::kStages) {
             s = 0;
             phase ^= 1;
@@ -705,13 +742,14 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
 
         const int heads = min(p.heads_per_unit, p.group - sg.head_group * p.heads_per_unit);
         const int tokens = min(p.tokens_per_unit, p.n_tokens - sg.token_group * p.tokens_per_unit);
-        // output row of row r of the unit, or -1 for a row it has not
-        auto out_row = [&](int r) -> long long {
-            const int t = r / p.heads_per_unit, h = r % p.heads_per_unit;
-            if (t >= tokens || h >= heads) return -1;
-            return (static_cast<long long>(sg.seq) * p.n_tokens + sg.token_group * p.tokens_per_unit + t) *
-                       p.n_q_heads + sg.kvh * p.group + sg.head_group * p.heads_per_unit + h;
+        // output row of the unit's (token, head), or -1 for one it has not
+        const long long out_row0 =
+            (static_cast<long long>(sg.seq) * p.n_tokens + sg.token_group * p.tokens_per_unit) * p.n_q_heads +
+            sg.kvh * p.group + sg.head_group * p.heads_per_unit;
+        auto out_at = [&](int t, int h) -> long long {
+            return t < tokens && h < heads ? out_row0 + static_cast<long long>(t) * p.n_q_heads + h : -1;
         };
+        auto out_row = [&](int r) { return out_at(r / p.heads_per_unit, r % p.heads_per_unit); };
         T *out = static_cast<T *>(p.out);
         const bool whole = sg.flags & kWhole;
         float *record = p.partials +
@@ -719,8 +757,8 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         if constexpr (!G::kF32) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int r = (lane >> 2) + 8 * half;
-                const long long row = out_row(r);
+                const int r = half ? row1 : row0, t = half ? tok1 : tok0;
+                const long long row = out_at(t, r - t * p.heads_per_unit);
                 if (row < 0) continue;
                 const float l = row_l[r], inv = 1.0f / l;
 #pragma unroll
@@ -764,10 +802,11 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             // a length below zero marks a result that a wait gave up on
             __stcg(record + kRows * D + kRows + tid, sh_dead ? -1.0f : row_l[tid]);
         }
-        __threadfence();
-        named_barrier_sync(2, kCompute);
+named_barrier_sync(2, kCompute);
+        const int c0 = owner(sg.unit_begin), c1 = owner(sg.unit_end - 1);
         if (tid == 0) {
-            sh_join = last_arrival(p.counters + sg.c0, p.nonce, sg.c1 - sg.c0 + 1);
+            __threadfence();
+            sh_join = last_arrival(p.counters + c0, p.nonce, c1 - c0 + 1);
             __threadfence();
         }
         named_barrier_sync(1, kCompute);
@@ -777,14 +816,14 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         // thread, kJoin records' loads together.
         auto record_of = [&](int c) {
             // the first CTA holds the unit in its second record: it begins in its range
-            return p.partials + static_cast<size_t>(2 * c + (c == sg.c0 ? 1 : 0)) * kRecord;
+            return p.partials + static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * kRecord;
         };
         constexpr int kGroups = kCompute / kRows;
         {
             const int r = tid % kRows, g = tid / kRows;
             float top = -INFINITY;
 #pragma unroll 4
-            for (int c = sg.c0 + g; c <= sg.c1; c += kGroups)
+            for (int c = c0 + g; c <= c1; c += kGroups)
                 top = fmaxf(top, __ldcg(record_of(c) + kRows * D + r));
             join_part[g][r] = top;
             named_barrier_sync(2, kCompute);
@@ -794,7 +833,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             float l = 0.0f;
             bool dead = false;
 #pragma unroll 4
-            for (int c = sg.c0 + g; c <= sg.c1; c += kGroups) {
+            for (int c = c0 + g; c <= c1; c += kGroups) {
                 float *m = record_of(c) + kRows * D + r;
                 const float w = fast_exp2(__ldcg(m) - base), part = __ldcg(m + kRows);
                 __stcg(m, w);
@@ -823,13 +862,13 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             const int r = item / (D / 4), col = (item % (D / 4)) * 4;
             float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-            for (int c = sg.c0; c <= sg.c1; c += kJoin) {
+            for (int c = c0; c <= c1; c += kJoin) {
                 float4 x[kJoin];
                 float w[kJoin];
 #pragma unroll
                 for (int k = 0; k < kJoin; ++k) {
-                    const bool in = c + k <= sg.c1;
-                    const float *rec = record_of(in ? c + k : sg.c1);
+                    const bool in = c + k <= c1;
+                    const float *rec = record_of(in ? c + k : c1);
                     x[k] = __ldcg(reinterpret_cast<const float4 *>(rec + r * D + col));
                     w[k] = in ? __ldcg(rec + kRows * D + r) : 0.0f;
                 }
