@@ -32,10 +32,9 @@ __device__ unsigned g_watchdog_attn_decode;
 
 constexpr int kWarps = 4;                       // computing warps
 constexpr int kCompute = 32 * kWarps;           // their threads
-constexpr int kThreads = kCompute + 32;         // and the loading warp
 constexpr int kRows = 16;                       // rows of a unit
 constexpr int kSMs = 152;
-constexpr int kMaxCtas = 2 * kSMs;
+constexpr int kMaxCtas = 3 * kSMs;
 constexpr int kJoin = 8;                        // partial results loaded together in a join
 
 // kHead: the unit's first tile lies in this CTA's range.
@@ -46,7 +45,15 @@ enum : int { kFirst = 1, kLast = 2, kWhole = 4, kHead = 8 };  // kWhole, kHead: 
 // loaded), and about a segment, the part of a unit in this CTA's range.
 struct Segment {
     int seq, kvh, head_group, token_group, len, flags;
-    unsigned unit_begin, unit_end;  // the unit's tiles
+    int c0, c1;  // CTAs sharing the unit (when it is not whole here)
+
+    // output row of the unit's (token, head), or -1 for one it has not
+    template <typename P>
+    __device__ __forceinline__ long long out_row(const P &p, int t, int h) const {
+        const int token = token_group * p.tokens_per_unit + t, head = head_group * p.heads_per_unit + h;
+        if (t >= p.tokens_per_unit || token >= p.n_tokens || head >= p.group) return -1;
+        return (static_cast<long long>(seq) * p.n_tokens + token) * p.n_q_heads + kvh * p.group + head;
+    }
 };
 
 struct Params {
@@ -75,9 +82,15 @@ struct Geometry {
     static constexpr int kQ = QR * D * static_cast<int>(sizeof(T));
     static constexpr int kExtra = kF32 ? 2 * KT * RT * 4             // S, then P [key][row], two buffers
                                        : 2 * kRows * (KT + 8) * 2;   // P hi and lo [row][key]
-    static constexpr int kCtas = D == 256 ? 1 : 2;                   // per SM
+    // CTAs per SM. A tile's chain of steps is latency: the more chains side by side the better,
+    // as far as two stages and the registers of each allow.
+    static constexpr int kCtas = D == 256 ? 1 : kF32 && D == 64 && RT == 4 ? 3 : 2;
+    // Threads: the computing warps, the loading warp and, where it costs no registers (three
+    // CTAs of 5 warps fill the register file), a joining warp.
+    static constexpr bool kJoinWarp = kCtas != 3;
+    static constexpr int kThreads = kCompute + (kJoinWarp ? 64 : 32);
     // shared memory of a CTA, less alignment slack and the static part
-    static constexpr int kBudget = (kCtas == 1 ? 232448 : 115712) - 1024 - 2560;
+    static constexpr int kBudget = (kCtas == 1 ? 232448 : kCtas == 2 ? 115712 : 76800) - 1024 - 2048;
     static constexpr int kStages = (kBudget - 2 * kQ - kExtra) / (2 * kPlane);
     static constexpr int kWarpKeys = KT / kWarps;
     static constexpr int kSmem = kStages * 2 * kPlane + 2 * kQ + kExtra + 1024;
@@ -190,15 +203,108 @@ __device__ __forceinline__ float group_sum(float x) {
     return x;
 }
 
+// ------------------------------------------------------------------ the join of a split unit
+
+// By NT threads, once all of its CTAs have stored their partial results.
+template <typename T, int D, int NT, typename Sync>
+__device__ __forceinline__ void join_unit(const Params &p, const Segment &u, int tid, Sync sync,
+                                          float (*part_of)[kRows], float *l_of) {
+    constexpr int kRecord = kRows * (D + 2);
+    const int c0 = u.c0, c1 = u.c1;
+    T *out = static_cast<T *>(p.out);
+    // The records' weights first: thread (g, r) takes every kGroups-th record of row r, and
+    // leaves the weights in the records in place of the maxima. Then the rows, 4 columns a
+    // thread, kJoin records' loads together.
+    auto record_of = [&](int c) {
+        // the first CTA holds the unit in its second record: it begins in its range
+        return p.partials + static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * kRecord;
+    };
+    constexpr int kGroups = NT / kRows;
+    {
+        const int r = tid % kRows, g = tid / kRows;
+        float top = -INFINITY;
+#pragma unroll 4
+        for (int c = c0 + g; c <= c1; c += kGroups)
+            top = fmaxf(top, __ldcg(record_of(c) + kRows * D + r));
+        part_of[g][r] = top;
+        sync();
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) top = fmaxf(top, part_of[k][r]);
+        const float base = top == -INFINITY ? 0.0f : top;
+        float l = 0.0f;
+        bool dead = false;
+#pragma unroll 4
+        for (int c = c0 + g; c <= c1; c += kGroups) {
+            float *m = record_of(c) + kRows * D + r;
+            const float w = fast_exp2(__ldcg(m) - base), part = __ldcg(m + kRows);
+            __stcg(m, w);
+            l = fmaf(w, part, l);
+            dead |= part < 0.0f;
+        }
+        sync();  // the maxima have been read
+        part_of[g][r] = dead ? -1.0f : l;
+        __threadfence_block();
+        sync();
+        if (tid < kRows) {
+            float sum_l = 0.0f;
+            bool any_dead = false;
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) {
+                any_dead |= part_of[k][tid] < 0.0f;
+                sum_l += part_of[k][tid];
+            }
+            l_of[tid] = any_dead ? -1.0f : sum_l;
+        }
+        sync();
+    }
+    const int n_items = p.tokens_per_unit * p.heads_per_unit * (D / 4);
+#pragma unroll 1
+    for (int item = tid; item < n_items; item += NT) {
+        const int r = item / (D / 4), col = (item % (D / 4)) * 4;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+        for (int c = c0; c <= c1; c += kJoin) {
+            float4 x[kJoin];
+            float w[kJoin];
+#pragma unroll
+            for (int k = 0; k < kJoin; ++k) {
+                const bool in = c + k <= c1;
+                const float *rec = record_of(in ? c + k : c1);
+                x[k] = __ldcg(reinterpret_cast<const float4 *>(rec + r * D + col));
+                w[k] = in ? __ldcg(rec + kRows * D + r) : 0.0f;
+            }
+#pragma unroll
+            for (int k = 0; k < kJoin; ++k) {
+                if (w[k] == 0.0f) continue;  // a record that saw nothing may hold anything
+                o.x = fmaf(w[k], x[k].x, o.x);
+                o.y = fmaf(w[k], x[k].y, o.y);
+                o.z = fmaf(w[k], x[k].z, o.z);
+                o.w = fmaf(w[k], x[k].w, o.w);
+            }
+        }
+        const long long row = u.out_row(p, r / p.heads_per_unit, r % p.heads_per_unit);
+        const float l = l_of[r], inv = 1.0f / l;
+        if (row < 0 || l < 0.0f) continue;
+        const float4 y = make_float4(finish(o.x, l, inv), finish(o.y, l, inv), finish(o.z, l, inv),
+                                     finish(o.w, l, inv));
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4 *>(out + row * D + col) = y;
+        } else {
+            *reinterpret_cast<uint2 *>(out + row * D + col) =
+                make_uint2(Elem<T>::pack(y.x, y.y), Elem<T>::pack(y.z, y.w));
+        }
+    }
+}
+
 // ------------------------------------------------------------------ the kernel
 
 template <typename T, int D, int RT>
-__global__ void __launch_bounds__(kThreads, Geometry<T, D, RT>::kCtas)
+__global__ void __launch_bounds__(Geometry<T, D, RT>::kThreads, Geometry<T, D, RT>::kCtas)
 attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                    const __grid_constant__ CUtensorMap k_map,
                    const __grid_constant__ CUtensorMap v_map, const Params p) {
     using G = Geometry<T, D, RT>;
-    constexpr int KT = G::KT;
+    constexpr int KT = G::KT, kThreads = G::kThreads;
     constexpr int kRecord = kRows * (D + 2);  // floats of a partial result: o, then m, then l
     extern __shared__ uint8_t dyn[];
     uint8_t *smem =
@@ -206,15 +312,15 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     uint8_t *q_smem = smem + G::kStages * 2 * G::kPlane;
     uint8_t *extra = q_smem + 2 * G::kQ;
 
-    __shared__ __align__(8) uint64_t full[G::kStages], empty[G::kStages], q_empty[2];
+    __shared__ __align__(8) uint64_t full[G::kStages], empty[G::kStages], q_empty[2], early_ready;
     __shared__ int2 stages[G::kStages];
-    __shared__ Segment segments[2];
+    __shared__ Segment segments[2], early;
     __shared__ unsigned warp_sum[kThreads / 32];
     __shared__ int sh_seq, sh_slot, sh_len, sh_dead, sh_join;
     __shared__ unsigned sh_seq_begin;
     __shared__ float red[kWarps][kRows];
     __shared__ __align__(16) float row_m[kRows], row_l[kRows];
-    __shared__ float join_part[kCompute / kRows][kRows];
+    __shared__ float join_part[kCompute / kRows][kRows], early_part[2][kRows], early_l[kRows];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int subs = p.head_groups * p.token_groups;
@@ -227,6 +333,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         }
         mbar_init(&q_empty[0], kWarps);
         mbar_init(&q_empty[1], kWarps);
+        mbar_init(&early_ready, kWarps);
         fence_mbar_init();
         sh_dead = 0;
         tma_prefetch_map(&q_map);
@@ -339,18 +446,6 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             int page = page_at(i);
             // the segment, and q
             if (seg >= 2) wait_or_flag(&q_empty[seg & 1], ((seg >> 1) - 1) & 1, &sh_dead);
-            if (leader) {
-                Segment sg;
-                sg.seq = n;
-                sg.kvh = kvh;
-                sg.head_group = hg;
-                sg.token_group = tg;
-                sg.len = len;
-                sg.flags = (whole ? kWhole : 0) | (unit_begin >= begin ? kHead : 0);
-                sg.unit_begin = unit_begin;
-                sg.unit_end = unit_end;
-                segments[seg & 1] = sg;
-            }
             for (bool first = true; at < seg_end; ++at, ++i, first = false) {
                 const int next_page = at + 1 < seg_end ? page_at(i + 1) : -1;
                 if (st_round > 0) wait_or_flag(&empty[st], (st_round - 1) & 1, &sh_dead);
@@ -359,13 +454,17 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                 const unsigned have = __ballot_sync(FULL_MASK, ok);
                 const unsigned blocks = __reduce_or_sync(FULL_MASK, ok ? lane_blocks : 0u);
                 const int row = (page * p.cache.n_kv_heads + kvh) * ps + (key0 & (ps - 1));
+                for (int b = 0; b < n_box; ++b) {
+                    const int r = __shfl_sync(FULL_MASK, row, b);
+                    if (leader && ((have >> b) & 1u)) {
+                        tma_load_3d(k_tile(st) + b * tile.part_bytes, &k_map, 0, r, 0, &full[st]);
+                        tma_load_3d(v_tile(st) + b * tile.part_bytes, &v_map, 0, r, 0, &full[st]);
+                    }
+                }
                 if (leader) {
-                    stages[st] = make_int2(key0, (first ? kFirst : 0) | (at + 1 == seg_end ? kLast : 0) |
-                                                     static_cast<int>(blocks << 8));
-                    const int q_rows = p.heads_per_unit * p.tokens_per_unit;
-                    mbar_arrive_expect_tx(
-                        &full[st], (static_cast<uint32_t>(__popc(have)) << log2_box) * D * sizeof(T) * 2u +
-                                       (first ? static_cast<uint32_t>(q_rows) * D * sizeof(T) : 0u));
+                    // The stage is full once the copies have landed and this thread has arrived:
+                    // what there is to say of it is worked out while they are under way.
+                    uint32_t bytes = (static_cast<uint32_t>(__popc(have)) << log2_box) * D * sizeof(T) * 2u;
                     if (first) {
                         const int head0 = kvh * p.group + hg * p.heads_per_unit;
                         const int token0 = n * p.n_tokens + tg * p.tokens_per_unit;
@@ -373,15 +472,21 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                         for (int cb = 0; cb < G::kCols; ++cb)
                             tma_load_3d(q_smem + (seg & 1) * G::kQ + cb * G::QR * 128, &q_map,
                                         cb * static_cast<int>(128 / sizeof(T)), head0, token0, &full[st]);
+                        bytes += static_cast<uint32_t>(p.heads_per_unit * p.tokens_per_unit) * D * sizeof(T);
+                        Segment sg;
+                        sg.seq = n;
+                        sg.kvh = kvh;
+                        sg.head_group = hg;
+                        sg.token_group = tg;
+                        sg.len = len;
+                        sg.flags = (whole ? kWhole : 0) | (unit_begin >= begin ? kHead : 0);
+                        sg.c0 = whole ? 0 : owner(unit_begin);
+                        sg.c1 = whole ? 0 : owner(unit_end - 1);
+                        segments[seg & 1] = sg;
                     }
-                }
-                __syncwarp();
-                for (int b = 0; b < n_box; ++b) {
-                    const int r = __shfl_sync(FULL_MASK, row, b);
-                    if (leader && ((have >> b) & 1u)) {
-                        tma_load_3d(k_tile(st) + b * tile.part_bytes, &k_map, 0, r, 0, &full[st]);
-                        tma_load_3d(v_tile(st) + b * tile.part_bytes, &v_map, 0, r, 0, &full[st]);
-                    }
+                    stages[st] = make_int2(key0, (first ? kFirst : 0) | (at + 1 == seg_end ? kLast : 0) |
+                                                     static_cast<int>(blocks << 8));
+                    mbar_arrive_expect_tx(&full[st], bytes);
                 }
                 __syncwarp();
                 if (++st == G::kStages) {
@@ -402,6 +507,20 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             }
         }
         if (*static_cast<volatile int *>(&sh_dead)) drain_in_flight();
+        return;
+    }
+    if (G::kJoinWarp && warp == kWarps + 1) {
+        // ---------------------------------------------------------- the joining warp
+        wait_or_flag(&early_ready, 0, &sh_dead);
+        if (*static_cast<volatile int *>(&sh_dead) || (early.flags & kWhole)) return;
+        int last = 0;
+        if (lane == 0) {
+            __threadfence();
+            last = last_arrival(p.counters + early.c0, p.nonce, early.c1 - early.c0 + 1);
+            __threadfence();
+        }
+        if (__shfl_sync(FULL_MASK, last, 0))
+            join_unit<T, D, 32>(p, early, lane, [] { __syncwarp(); }, early_part, early_l);
         return;
     }
 
@@ -426,6 +545,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     const int tok0 = row0 / p.heads_per_unit, tok1 = row1 / p.heads_per_unit;
     int pos0 = 0, pos1 = 0;
     unsigned long long word_seen = 0;
+    bool had_early = false;
     int seg = 0, s = 0;
     uint32_t phase = 0;
 
@@ -442,17 +562,34 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
 pos0 = base + tok0;
             pos1 = base + tok1;
             if (tid == 0 && !(sg.flags & kWhole))
-                word_seen = *reinterpret_cast<volatile unsigned long long *>(p.counters + owner(sg.unit_begin));
+                word_seen = *reinterpret_cast<volatile unsigned long long *>(p.counters + sg.c0);
         }
         const int p_first = sg.len - p.n_tokens, p_last = sg.len - 1;
         const bool clean = blocks == (1u << (KT / 8)) - 1u && key0 + KT - 1 <= p_first &&
                            (p_last - key0 < p.mask.window || key0 + KT <= p.mask.sinks);
+        // The keys that P V takes, whole groups of kGroup: those between the first and the last
+        // that some row sees.
+        constexpr int kGroup = G::kF32 ? 8 : 16;
+        int g_lo = 0, g_hi = KT / kGroup;
         if (!clean) {
-            // Keys of this warp's part of the tile that no row of the unit sees: their V rows
-            // are cleared, so that whatever the page holds there (an infinity, a NaN) cannot
-            // reach the sum through a weight of 0.
+            const int lo = p.mask.first(max(p_first, 0)) - key0;  // of the window
+            int a = KT, b = 0;
+            if (lo < KT) {
+                a = max(lo, 0);
+                b = min(p_last - key0 + 1, KT);
+            }
+            const int sinks = min(p.mask.sinks, p_last + 1) - key0;
+            if (sinks > 0) {
+                a = 0;
+                b = max(b, min(sinks, KT));
+            }
+            g_lo = a / kGroup;
+            g_hi = (b + kGroup - 1) / kGroup;
+            // Keys of this warp's part of the tile, among those, that no row of the unit sees:
+            // their V rows are cleared, so that whatever the page holds there (an infinity, a
+            // NaN) cannot reach the sum through a weight of 0.
             const int i = warp * G::kWarpKeys + lane, key = key0 + i;
-            const bool dead = lane < G::kWarpKeys &&
+            const bool dead = lane < G::kWarpKeys && i / kGroup >= g_lo && i / kGroup < g_hi &&
                               (!((blocks >> ((i >> 3) & 31)) & 1u) || key > p_last ||
                                !(p_first - key < p.mask.window || key < p.mask.sinks));
             const unsigned left = __ballot_sync(FULL_MASK, dead);
@@ -582,6 +719,7 @@ pos0 = base + tok0;
                 ((lane & 7) + ((lane >> 3) & 1) * 8) * (KT + 8) + (lane >> 4) * 8) * 2u;
 #pragma unroll
             for (int kk = 0; kk < KT / 16; ++kk) {
+                if (kk < g_lo || kk >= g_hi) continue;
                 uint32_t ah[4], al[4];
                 ldsm4(ah, smem_addr(ph) + poff + kk * 32);
                 ldsm4(al, smem_addr(pl) + poff + kk * 32);
@@ -608,37 +746,59 @@ pos0 = base + tok0;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o32[r][e] = 0.0f;
             }
-#pragma unroll (RT <= 4 ? 2 : 1)
-            for (int h = 0; h < G::kWarpKeys / 8; ++h) {
-                // lane: one key of 8 and a quarter of the dot product
-                const int i = warp * G::kWarpKeys + h * 8 + (lane & 7), quarter = lane >> 3;
-                // the quarters' lanes start at chunks in different banks
-                const int turn = D >= 128 ? 2 * quarter : quarter >> 1;
-                const uint8_t *kr = k_tile(s) + tile.row(i);
-                const Tile q_tile{G::QR == 8 ? 3 : 4, 0};
-                float acc[RT];
+constexpr int KH = G::kWarpKeys / 8;  // keys of a lane
+            {
+                // lane: every 8th key of the warp's and a quarter of the dot product
+                const int i0 = warp * G::kWarpKeys + (lane & 7), quarter = lane >> 3;
+                // Chunk c of the quarter stands at its column's place (c & 7) ^ turn ^ (row & 7):
+                // the swizzle, the quarter's half of a column (D = 64) and a turn of its own
+                // that starts the quarters' lanes in different banks.
+                const int turn = D >= 128 ? 2 * quarter : 4 * (quarter & 1) + (quarter >> 1);
+                const uint32_t k_place = static_cast<uint32_t>(turn ^ (i0 & 7)) << 4;
+                const uint32_t q_place = static_cast<uint32_t>(turn) << 4;
+                constexpr int kQuarterCols = D >= 128 ? D / 128 : 1;  // 128-byte columns it touches
+                const int col0 = D >= 128 ? quarter * kQuarterCols : quarter >> 1;
+                const uint8_t *kr[KH];
 #pragma unroll
-                for (int r = 0; r < RT; ++r) acc[r] = 0.0f;
+                for (int h = 0; h < KH; ++h)
+                    kr[h] = k_tile(s) + tile.row(i0 + 8 * h) + (col0 << (log2_box + 7));
+                const uint8_t *qr = q_here + col0 * G::QR * 128;
+                float acc[KH][RT];
+#pragma unroll
+                for (int h = 0; h < KH; ++h)
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) acc[h][r] = 0.0f;
+#pragma unroll
+                for (int col = 0; col < kQuarterCols; ++col) {
 #pragma unroll (RT == 16 ? 1 : RT == 8 ? 2 : 4)
-                for (int c = 0; c < D / 16; ++c) {
-                    const int chunk = quarter * (D / 16) + (c ^ turn);
-                    const float4 kv = *reinterpret_cast<const float4 *>(kr + tile.chunk(i, chunk));
+                    for (int c = 0; c < (D >= 128 ? 8 : 4); ++c) {
+                        float4 kv[KH];
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        const float4 qv =
-                            *reinterpret_cast<const float4 *>(q_here + r * 128 + q_tile.chunk(r, chunk));
-                        acc[r] = fmaf(qv.x, kv.x, acc[r]);
-                        acc[r] = fmaf(qv.y, kv.y, acc[r]);
-                        acc[r] = fmaf(qv.z, kv.z, acc[r]);
-                        acc[r] = fmaf(qv.w, kv.w, acc[r]);
+                        for (int h = 0; h < KH; ++h)
+                            kv[h] = *reinterpret_cast<const float4 *>(kr[h] + (col << (log2_box + 7)) +
+                                                                      (k_place ^ (c << 4)));
+#pragma unroll
+                        for (int r = 0; r < RT; ++r) {
+                            const float4 qv = *reinterpret_cast<const float4 *>(
+                                qr + col * G::QR * 128 + r * 128 + (q_place ^ ((c ^ (r & 7)) << 4)));
+#pragma unroll
+                            for (int h = 0; h < KH; ++h) {
+                                acc[h][r] = fmaf(qv.x, kv[h].x, acc[h][r]);
+                                acc[h][r] = fmaf(qv.y, kv[h].y, acc[h][r]);
+                                acc[h][r] = fmaf(qv.z, kv[h].z, acc[h][r]);
+                                acc[h][r] = fmaf(qv.w, kv[h].w, acc[h][r]);
+                            }
+                        }
                     }
                 }
 #pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    acc[r] += __shfl_xor_sync(FULL_MASK, acc[r], 8);
-                    acc[r] += __shfl_xor_sync(FULL_MASK, acc[r], 16);
-                    if ((r & 3) == quarter) sp[i * RT + r] = acc[r] * p.scale_log2;
-                }
+                for (int h = 0; h < KH; ++h)
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        acc[h][r] += __shfl_xor_sync(FULL_MASK, acc[h][r], 8);
+                        acc[h][r] += __shfl_xor_sync(FULL_MASK, acc[h][r], 16);
+                        if ((r & 3) == quarter) sp[(i0 + 8 * h) * RT + r] = acc[h][r] * p.scale_log2;
+                    }
             }
             named_barrier_sync(1, kCompute);
             {
@@ -675,7 +835,7 @@ pos0 = base + tok0;
                     for (int e = 0; e < 4; ++e) o32[r][e] *= corr;
                 }
 #pragma unroll (RT == 16 ? 1 : RT == 8 ? 2 : 4)
-                for (int j = 0; j < KT / NKG; ++j) {
+                for (int j = g_lo * (8 / NKG); j < g_hi * (8 / NKG); ++j) {
                     // for D = 64 two keys share a quarter-warp's read: 4 apart, so that
                     // the swizzle keeps them in different banks
                     const int i = NKG == 8 ? (kg >> 1) + 4 * (kg & 1) + 8 * j : kg + NKG * j;
@@ -699,7 +859,7 @@ pos0 = base + tok0;
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[s]);
         if ((flags & kFirst) && tid == 0 && !(sg.flags & kWhole) && !tagged(word_seen, p.nonce))
-            atomicCAS(p.counters + owner(sg.unit_begin), word_seen, p.nonce << 16);
+            atomicCAS(p.counters + sg.c0, word_seen, p.nonce << 16);
         if (++s == G::kStages) {
             s = 0;
             phase ^= 1;
@@ -740,16 +900,6 @@ pos0 = base + tok0;
         }
         named_barrier_sync(1, kCompute);
 
-        const int heads = min(p.heads_per_unit, p.group - sg.head_group * p.heads_per_unit);
-        const int tokens = min(p.tokens_per_unit, p.n_tokens - sg.token_group * p.tokens_per_unit);
-        // output row of the unit's (token, head), or -1 for one it has not
-        const long long out_row0 =
-            (static_cast<long long>(sg.seq) * p.n_tokens + sg.token_group * p.tokens_per_unit) * p.n_q_heads +
-            sg.kvh * p.group + sg.head_group * p.heads_per_unit;
-        auto out_at = [&](int t, int h) -> long long {
-            return t < tokens && h < heads ? out_row0 + static_cast<long long>(t) * p.n_q_heads + h : -1;
-        };
-        auto out_row = [&](int r) { return out_at(r / p.heads_per_unit, r % p.heads_per_unit); };
         T *out = static_cast<T *>(p.out);
         const bool whole = sg.flags & kWhole;
         float *record = p.partials +
@@ -758,7 +908,7 @@ pos0 = base + tok0;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int r = half ? row1 : row0, t = half ? tok1 : tok0;
-                const long long row = out_at(t, r - t * p.heads_per_unit);
+                const long long row = sg.out_row(p, t, r - t * p.heads_per_unit);
                 if (row < 0) continue;
                 const float l = row_l[r], inv = 1.0f / l;
 #pragma unroll
@@ -779,7 +929,7 @@ pos0 = base + tok0;
                 const int col = (warp * C4 + lane) * 4;
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
-                    const long long row = out_row(r);
+                    const long long row = sg.out_row(p, r / p.heads_per_unit, r % p.heads_per_unit);
                     if (row < 0) continue;
                     if (whole) {
                         const float l = row_l[r], inv = 1.0f / l;
@@ -795,105 +945,36 @@ pos0 = base + tok0;
             }
         }
         if (whole) continue;
-
-        // ---------------------------------------------------------- the join
         if (tid < kRows) {
             __stcg(record + kRows * D + tid, row_m[tid]);
             // a length below zero marks a result that a wait gave up on
             __stcg(record + kRows * D + kRows + tid, sh_dead ? -1.0f : row_l[tid]);
         }
-named_barrier_sync(2, kCompute);
-        const int c0 = owner(sg.unit_begin), c1 = owner(sg.unit_end - 1);
+        // A range has at most two split units, its first and its last. The first one's arrival
+        // (a fence takes thousands of cycles while copies are under way) and join are left to
+        // the joining warp; the last one's are the CTA's last work.
+        if (it + 1 < n_tiles && G::kJoinWarp) {
+            if (tid == 0) early = sg;
+            had_early = true;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&early_ready);
+            continue;
+        }
+        named_barrier_sync(2, kCompute);
         if (tid == 0) {
             __threadfence();
-            sh_join = last_arrival(p.counters + c0, p.nonce, c1 - c0 + 1);
+            sh_join = last_arrival(p.counters + sg.c0, p.nonce, sg.c1 - sg.c0 + 1);
             __threadfence();
         }
         named_barrier_sync(1, kCompute);
-        if (!sh_join) continue;
-        // The records' weights first: thread (g, r) takes every kGroups-th record of row r, and
-        // leaves the weights in the records in place of the maxima. Then the rows, 4 columns a
-        // thread, kJoin records' loads together.
-        auto record_of = [&](int c) {
-            // the first CTA holds the unit in its second record: it begins in its range
-            return p.partials + static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)) * kRecord;
-        };
-        constexpr int kGroups = kCompute / kRows;
-        {
-            const int r = tid % kRows, g = tid / kRows;
-            float top = -INFINITY;
-#pragma unroll 4
-            for (int c = c0 + g; c <= c1; c += kGroups)
-                top = fmaxf(top, __ldcg(record_of(c) + kRows * D + r));
-            join_part[g][r] = top;
-            named_barrier_sync(2, kCompute);
-#pragma unroll
-            for (int k = 0; k < kGroups; ++k) top = fmaxf(top, join_part[k][r]);
-            const float base = top == -INFINITY ? 0.0f : top;
-            float l = 0.0f;
-            bool dead = false;
-#pragma unroll 4
-            for (int c = c0 + g; c <= c1; c += kGroups) {
-                float *m = record_of(c) + kRows * D + r;
-                const float w = fast_exp2(__ldcg(m) - base), part = __ldcg(m + kRows);
-                __stcg(m, w);
-                l = fmaf(w, part, l);
-                dead |= part < 0.0f;
-            }
-            named_barrier_sync(1, kCompute);  // the maxima have been read
-            join_part[g][r] = dead ? -1.0f : l;
-            __threadfence_block();
-            named_barrier_sync(2, kCompute);
-            if (tid < kRows) {
-                float sum_l = 0.0f;
-                bool any_dead = false;
-#pragma unroll
-                for (int k = 0; k < kGroups; ++k) {
-                    any_dead |= join_part[k][tid] < 0.0f;
-                    sum_l += join_part[k][tid];
-                }
-                row_l[tid] = any_dead ? -1.0f : sum_l;
-            }
-            named_barrier_sync(1, kCompute);
-        }
-        const int n_items = tokens * p.heads_per_unit * (D / 4);
-#pragma unroll 1
-        for (int item = tid; item < n_items; item += kCompute) {
-            const int r = item / (D / 4), col = (item % (D / 4)) * 4;
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 1
-            for (int c = c0; c <= c1; c += kJoin) {
-                float4 x[kJoin];
-                float w[kJoin];
-#pragma unroll
-                for (int k = 0; k < kJoin; ++k) {
-                    const bool in = c + k <= c1;
-                    const float *rec = record_of(in ? c + k : c1);
-                    x[k] = __ldcg(reinterpret_cast<const float4 *>(rec + r * D + col));
-                    w[k] = in ? __ldcg(rec + kRows * D + r) : 0.0f;
-                }
-#pragma unroll
-                for (int k = 0; k < kJoin; ++k) {
-                    if (w[k] == 0.0f) continue;  // a record that saw nothing may hold anything
-                    o.x = fmaf(w[k], x[k].x, o.x);
-                    o.y = fmaf(w[k], x[k].y, o.y);
-                    o.z = fmaf(w[k], x[k].z, o.z);
-                    o.w = fmaf(w[k], x[k].w, o.w);
-                }
-            }
-            const long long row = out_row(r);
-            const float l = row_l[r], inv = 1.0f / l;
-            if (row < 0 || l < 0.0f) continue;
-            const float4 y = make_float4(finish(o.x, l, inv), finish(o.y, l, inv), finish(o.z, l, inv),
-                                         finish(o.w, l, inv));
-            if constexpr (G::kF32) {
-                *reinterpret_cast<float4 *>(out + row * D + col) = y;
-            } else {
-                *reinterpret_cast<uint2 *>(out + row * D + col) =
-                    make_uint2(Elem<T>::pack(y.x, y.y), Elem<T>::pack(y.z, y.w));
-            }
-        }
-        named_barrier_sync(2, kCompute);  // row_l has been read
+        if (sh_join)
+            join_unit<T, D, kCompute>(p, sg, tid, [] { named_barrier_sync(2, kCompute); }, join_part, row_l);
+        named_barrier_sync(1, kCompute);  // row_l and join_part have been read
+    }
+    if (G::kJoinWarp && !had_early) {
+        if (tid == 0) early.flags = kWhole;  // nothing to join
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&early_ready);
     }
 }
 
@@ -942,7 +1023,7 @@ gdn_status launch(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap 
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem) !=
         cudaSuccess)
         return GDN_ERR_LAUNCH;
-    kernel<<<kSMs * G::kCtas, kThreads, G::kSmem, s>>>(q, k, v, p);
+    kernel<<<kSMs * G::kCtas, G::kThreads, G::kSmem, s>>>(q, k, v, p);
     return launch_status();
 }
 
