@@ -127,8 +127,7 @@ _SIGS = {
                                                  ctypes.c_size_t, _P], _I),
 }
 
-# gdn_dtype codes by torch type name.
-_DTYPES = {"float32": 0, "float16": 1, "bfloat16": 2}
+_DTYPES = {}  # gdn_dtype codes by torch type, filled on first use
 
 # Size of the fixed device scratch of gdn_block_prefill_noalloc (include/gdn.h).
 PREFILL_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -187,16 +186,21 @@ def _stream(stream):
 
 
 def _ptr(t, name, dtype=None, optional=False):
+    torch = _TORCH or _torch()
+    want = dtype or torch.float32
+    try:  # the ordinary case first: these checks are most of a small call's host time
+        if t.dtype == want and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if t is None:
         if optional:
             return None
         raise ValueError(f"{name} is required")
-    torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    want = dtype or torch.float32
     if t.dtype != want:
         raise TypeError(f"{name} must be {want}, got {t.dtype}")
     if not t.is_contiguous():
@@ -206,7 +210,11 @@ def _ptr(t, name, dtype=None, optional=False):
 
 def _dtype(t, name):
     """The gdn_dtype code of a tensor's type."""
-    code = _DTYPES.get(str(getattr(t, "dtype", None)).rpartition(".")[2])
+    dtype = getattr(t, "dtype", None)
+    if not _DTYPES:
+        torch = _torch()
+        _DTYPES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    code = _DTYPES.get(dtype)
     if code is None:
         raise TypeError(f"{name} must be a float32, float16 or bfloat16 tensor")
     return code
@@ -215,6 +223,16 @@ def _dtype(t, name):
 def _rows(t, name, dtype, heads, head_dim):
     """(data pointer, elements from row to row) of [rows][heads][head_dim], dense in its last
     two dimensions; the rows may be slices of wider ones."""
+    try:
+        if t.dtype == dtype and t.is_cuda:
+            if t.is_contiguous():
+                return t.data_ptr(), heads * head_dim
+            if t.dim() == 3:
+                row, head, elem = t.stride()
+                if elem == 1 and head == head_dim and tuple(t.shape[1:]) == (heads, head_dim):
+                    return t.data_ptr(), row if t.shape[0] > 1 else max(row, heads * head_dim)
+    except AttributeError:
+        pass
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
@@ -222,14 +240,10 @@ def _rows(t, name, dtype, heads, head_dim):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.is_contiguous():
-        return t.data_ptr(), heads * head_dim
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
-        raise ValueError(f"{name} must be contiguous or have shape [rows, {heads}, {head_dim}]")
-    row, head, elem = t.stride()
-    if (head_dim > 1 and elem != 1) or (heads > 1 and head != head_dim):
-        raise ValueError(f"{name} must be dense in its last two dimensions")
-    return t.data_ptr(), row if t.shape[0] > 1 else max(row, heads * head_dim)
+    if t.dim() == 3 and heads == 1 and t.shape[1:] == (1, head_dim) and t.stride(2) == 1:
+        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), head_dim)
+    raise ValueError(f"{name} must be contiguous, or of shape [rows, {heads}, {head_dim}] and dense in "
+                     "its last two dimensions")
 
 
 def _slots(slots):

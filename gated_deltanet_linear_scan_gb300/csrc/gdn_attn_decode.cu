@@ -1020,9 +1020,8 @@ gdn_status launch(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap 
                   cudaStream_t s) {
     using G = Geometry<T, D, RT>;
     auto kernel = attn_decode_kernel<T, D, RT>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem) !=
-        cudaSuccess)
-        return GDN_ERR_LAUNCH;
+    static std::atomic<unsigned long long> allowed{0};
+    GDN_TRY(allow_smem(kernel, G::kSmem, allowed));
     kernel<<<kSMs * G::kCtas, G::kThreads, G::kSmem, s>>>(q, k, v, p);
     return launch_status();
 }

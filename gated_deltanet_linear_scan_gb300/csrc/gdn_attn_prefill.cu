@@ -217,9 +217,8 @@ gdn_status launch_f32(PrefillParams p, cudaStream_t s) {
     const long long ys = static_cast<long long>(p.cache.n_kv_heads) * p.head_groups;
     if (tiles > 0x7fffffffLL || ys > 65535) return GDN_ERR_UNSUPPORTED;
     auto kernel = attn_prefill_f32_kernel<D>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, simt_smem<D>()) !=
-        cudaSuccess)
-        return GDN_ERR_LAUNCH;
+    static std::atomic<unsigned long long> allowed{0};
+    GDN_TRY(allow_smem(kernel, simt_smem<D>(), allowed));
     kernel<<<dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(ys)), kSimtThreads,
              simt_smem<D>(), s>>>(p);
     return launch_status();

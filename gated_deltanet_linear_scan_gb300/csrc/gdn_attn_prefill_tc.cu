@@ -887,8 +887,8 @@ gdn_status launch(PrefillParams p, int dtype, cudaStream_t s) {
     GDN_TRY(encode_blocks_map(&v_map, p.v_pages, dtype, D, rows, D * 2, ps < C::kVKeys ? ps : C::kVKeys,
                               D / 64));
     auto kernel = attn_prefill_tc_kernel<T, D>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
-        return GDN_ERR_LAUNCH;
+    static std::atomic<unsigned long long> allowed{0};
+    GDN_TRY(allow_smem(kernel, C::kSmem, allowed));
     kernel<<<static_cast<unsigned>(grid), C::kThreads, C::kSmem, s>>>(q_map, k_map, v_map, p);
     return launch_status();
 }

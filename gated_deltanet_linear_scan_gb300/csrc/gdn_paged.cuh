@@ -3,6 +3,7 @@
 // walk over the key tiles a batch of queries sees, and tensor-map (TMA) loads of pages.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -177,7 +178,22 @@ __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
-// ------------------------------------------------------------------ host checks
+// ------------------------------------------------------------------ host side
+
+// Raises a kernel's shared-memory limit, once per device and kernel (`done` is the kernel's
+// own: bit d for device d).
+template <typename Kernel>
+inline gdn_status allow_smem(Kernel kernel, int bytes, std::atomic<unsigned long long> &done) {
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return GDN_ERR_LAUNCH;
+    const unsigned long long bit = 1ull << (device & 63);
+    if (device < 64 && (done.load(std::memory_order_relaxed) & bit)) return GDN_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return GDN_ERR_LAUNCH;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return GDN_OK;
+}
+
 
 // Arguments every call on a paged cache shares.
 inline gdn_status check_cache(int n_kv_heads, int head_dim, int page_size, int n_pages,
