@@ -22,45 +22,74 @@ struct AppendParams {
     uint4 *k_pages, *v_pages;
     size_t k_row, v_row;  // 16-byte units between tokens
     int n_seqs, head_vec;  // 16-byte units of a head's row
+    int log2_parts;        // warps sharing a token
     int32_t *err_count;
 };
 
 constexpr int kAppendThreads = 128;
+constexpr int kAppendEach = 4;  // 16-byte units of a plane a lane holds at a time
 
-// One warp per new position: finds its sequence, its page, and copies every head's row.
-// Also, warp n checks sequence n and counts it when it is skipped.
+// A few warps per new position (four while the batch is small and latency counts, one when
+// there are enough tokens to fill the GPU). The rows are loaded first and find their place --
+// sequence, slot, length, page: four dependent loads -- while they are under way. Also, the
+// warp of number n checks sequence n, last, and counts it when it is skipped.
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
     const int lane = threadIdx.x & 31;
-    const long long w = static_cast<long long>(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    const long long warp = static_cast<long long>(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    const int part = static_cast<int>(warp & ((1 << p.log2_parts) - 1));
+    const long long w = warp >> p.log2_parts;
     // start and position of sequence n's first new row; false when it is skipped
     auto find = [&](int n, size_t &t0, int &m, int &slot, int &len) {
         return p.seqs.range(n, t0, m) && p.cache.lookup(n, slot, len) && m <= len;
     };
-    size_t t0;
-    int m, slot, len;
-    if (w < p.n_seqs && lane == 0 && p.err_count && !find(static_cast<int>(w), t0, m, slot, len))
-        atomicAdd(p.err_count, 1);
-    if (w >= p.seqs.total) return;
-    const int n = p.seqs.cu ? warp_seq_of_position(p.seqs.cu, p.n_seqs, w)
-                            : static_cast<int>(w / p.seqs.n_tokens);
-    if (n < 0 || !find(n, t0, m, slot, len) || w >= static_cast<long long>(t0) + m) return;
-    const int pos = len - m + static_cast<int>(w - static_cast<long long>(t0));
-    const int page = p.cache.page_of(slot, pos);
-    if (!p.cache.page_ok(page)) {
-        if (lane == 0 && p.err_count) atomicAdd(p.err_count, 1);
-        return;
+    if (w < p.seqs.total) {
+        const uint4 *k = p.k + w * p.k_row, *v = p.v + w * p.v_row;
+        const int vecs = p.cache.n_kv_heads * p.head_vec, step = 32 << p.log2_parts;
+        const int first = part * 32 + lane;
+        uint4 kx[kAppendEach], vx[kAppendEach];
+        auto load = [&](int i0) {
+#pragma unroll
+            for (int x = 0; x < kAppendEach; ++x) {
+                const int i = i0 + x * step;
+                if (i < vecs) {
+                    kx[x] = k[i];
+                    vx[x] = v[i];
+                }
+            }
+        };
+        load(first);
+        const int n = p.seqs.cu ? warp_seq_of_position(p.seqs.cu, p.n_seqs, w)
+                                : static_cast<int>(w / p.seqs.n_tokens);
+        size_t t0;
+        int m, slot, len;
+        if (n >= 0 && find(n, t0, m, slot, len) && w < static_cast<long long>(t0) + m) {
+            const int pos = len - m + static_cast<int>(w - static_cast<long long>(t0));
+            const int page = p.cache.page_of(slot, pos);
+            if (p.cache.page_ok(page)) {
+                const int ps = 1 << p.cache.log2_ps;
+                const size_t base =
+                    (static_cast<size_t>(page) * p.cache.n_kv_heads * ps + (pos & (ps - 1))) * p.head_vec;
+                for (int i0 = first; i0 < vecs; i0 += kAppendEach * step) {
+                    if (i0 != first) load(i0);
+#pragma unroll
+                    for (int x = 0; x < kAppendEach; ++x) {
+                        const int i = i0 + x * step;
+                        if (i >= vecs) break;
+                        const int h = i / p.head_vec;
+                        const size_t to = base + static_cast<size_t>(h) * ps * p.head_vec + (i - h * p.head_vec);
+                        p.k_pages[to] = kx[x];
+                        p.v_pages[to] = vx[x];
+                    }
+                }
+            } else if (part == 0 && lane == 0 && p.err_count) {
+                atomicAdd(p.err_count, 1);
+            }
+        }
     }
-    const int ps = 1 << p.cache.log2_ps;
-    const size_t base = (static_cast<size_t>(page) * p.cache.n_kv_heads * ps + (pos & (ps - 1))) *
-                        p.head_vec;
-    const uint4 *k = p.k + w * p.k_row, *v = p.v + w * p.v_row;
-    const int vecs = p.cache.n_kv_heads * p.head_vec;
-#pragma unroll 4
-    for (int i = lane; i < vecs; i += 32) {
-        const int h = i / p.head_vec, x = i - h * p.head_vec;
-        const size_t to = base + static_cast<size_t>(h) * ps * p.head_vec + x;
-        p.k_pages[to] = k[i];
-        p.v_pages[to] = v[i];
+    if (w < p.n_seqs && part == 0 && lane == 0 && p.err_count) {
+        size_t t0;
+        int m, slot, len;
+        if (!find(static_cast<int>(w), t0, m, slot, len)) atomicAdd(p.err_count, 1);
     }
 }
 
@@ -512,7 +541,9 @@ gdn_status gdn_kv_append(const void *k, const void *v, void *k_pages, void *v_pa
     p.n_seqs = n_seqs;
     p.head_vec = static_cast<int>(head_dim * es / 16);
     p.err_count = err_count;
-    const long long warps = total_tokens > n_seqs ? total_tokens : n_seqs;
+    p.log2_parts = total_tokens <= kSMs * 16 ? 2 : 0;
+    const long long warps = static_cast<long long>(total_tokens > n_seqs ? total_tokens : n_seqs)
+                            << p.log2_parts;
     const long long per = kAppendThreads / 32;
     kv_append_kernel<<<static_cast<unsigned>((warps + per - 1) / per), kAppendThreads, 0,
                        as_cuda(stream)>>>(p);
