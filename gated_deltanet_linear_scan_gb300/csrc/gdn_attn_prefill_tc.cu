@@ -469,11 +469,11 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                             for (int x = 0; x < C::kVKeys / 16; ++x)
                                 tc::mma_bf16_ts(o, pw + x * 8, v + v_step[x], kIdescO, !first || s + x > 0);
                         } else {
-#pragma unroll
-                            for (int x = 0; x < C::kVKeys / 16; ++x) {
-                                const int key16 = s * (C::kVKeys / 16) + x;
-                                if (key16 >= from && key16 < to)
-                                    tc::mma_bf16_ts(o, pw + x * 8, v + v_step[x], kIdescO, !first || key16 > from);
+                            const int x0 = max(from - s * (C::kVKeys / 16), 0), x1 = min(to - s * (C::kVKeys / 16), C::kVKeys / 16);
+#pragma unroll 1
+                            for (int x = x0; x < x1; ++x) {
+                                const uint32_t at = (((x * 16) >> log2_bv) * (bv * D * 2) + ((x * 16) & (bv - 1)) * 128) >> 4;
+                                tc::mma_bf16_ts(o, pw + x * 8, v + at, kIdescO, !first || s * (C::kVKeys / 16) + x > from);
                             }
                         }
                         if (release) tc::mma_commit(&v_empty[slot]);
@@ -692,8 +692,8 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                         if (dead && (row >> C::kLog2VKeys) == y) {
                             const int r = row & (C::kVKeys - 1);
                             uint8_t *at = v_ring + slot * C::kSlotBytes + (r >> log2_bv) * (bv * D * 2) + (r & (bv - 1)) * 128;
-                            for (int x = 0; x < D / 8; ++x)
-                                *reinterpret_cast<uint4 *>(at + (x >> 3) * bv * 128 + (x & 7) * 16) =
+                            for (int x = 0; x < D / 8; ++x)  // (the lanes' 16 bytes in different banks)
+                                *reinterpret_cast<uint4 *>(at + (x >> 3) * bv * 128 + ((x + row) & 7) * 16) =
                                     make_uint4(0, 0, 0, 0);
                         }
                     }
@@ -820,9 +820,14 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
             }
             // ------------------------------------------------------ O out
             if (i * per < w.tokens) {
-                T *out = static_cast<T *>(p.out) +
-                         (static_cast<size_t>(w.row0 + w.token0 + token) * p.n_q_heads + w.head0 + row_head) * D;
                 const bool mine = token < w.tokens && row_token < per && row_head < w.heads;
+                const long long at = mine ? static_cast<long long>(w.row0 + w.token0 + token) * p.n_q_heads + w.head0 + row_head : -1;
+                // Four lanes write a row's 64 bytes together, row after row of their four:
+                // eight lines a store instead of 32.
+                long long rows[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) rows[r] = __shfl_sync(FULL_MASK, at, (lane & ~3) + r);
+                T *out = static_cast<T *>(p.out) + (lane & 3) * 8;
                 if (begun) {
                     wait_or_flag(&o_done[i], (count - 1) & 1, &sh_dead);
                     tc::fence_after_sync();
@@ -833,18 +838,31 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                     uint32_t o[32];
                     tc::tmem_ld32_nowait(o_addr + c, o);
                     tc::tmem_ld_wait();
-                    if (mine && !sh_dead) {
+                    uint32_t pw[4][4];  // 16 bytes of this row at a time; then of the four lanes' rows
 #pragma unroll
-                        for (int x = 0; x < 32; x += 8) {
-                            uint32_t pw[4];
+                    for (int x = 0; x < 16; ++x)
+                        pw[x / 4][x % 4] = l == 0.0f ? 0u
+                                                     : Elem<T>::pack(__uint_as_float(o[2 * x]) * inv,
+                                                                     __uint_as_float(o[2 * x + 1]) * inv);
 #pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                pw[y] = l == 0.0f ? 0u
-                                                  : Elem<T>::pack(__uint_as_float(o[x + 2 * y]) * inv,
-                                                                  __uint_as_float(o[x + 2 * y + 1]) * inv);
-                            *reinterpret_cast<uint4 *>(out + c + x) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+                    for (int bit = 1; bit < 4; bit *= 2) {
+                        const bool upper = lane & bit;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            if (r & bit) continue;
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const uint32_t got = __shfl_xor_sync(FULL_MASK, upper ? pw[r][y] : pw[r | bit][y], bit);
+                                if (upper) pw[r][y] = got;
+                                else pw[r | bit][y] = got;
+                            }
                         }
                     }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (rows[r] >= 0 && !sh_dead)
+                            *reinterpret_cast<uint4 *>(out + rows[r] * D + c) =
+                                make_uint4(pw[r][0], pw[r][1], pw[r][2], pw[r][3]);
                 }
                 tc::fence_before_sync();
             }

@@ -45,15 +45,6 @@ gdn_status encode(CUtensorMap *map, const void *base, int dtype, int rank, const
 
 }  // namespace
 
-gdn_status encode_rows_map(CUtensorMap *map, const void *base, int dtype, int cols, uint64_t rows,
-                           uint64_t row_bytes, int box_rows) {
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), rows};
-    const cuuint64_t strides[1] = {row_bytes};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / dtype_bytes(dtype)),
-                               static_cast<cuuint32_t>(box_rows)};
-    return encode(map, base, dtype, 2, dims, strides, box);
-}
-
 gdn_status encode_blocks_map(CUtensorMap *map, const void *base, int dtype, int cols, uint64_t rows,
                              uint64_t row_bytes, int box_rows, int box_blocks) {
     const int per = 128 / dtype_bytes(dtype);

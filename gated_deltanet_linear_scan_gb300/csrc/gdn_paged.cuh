@@ -108,7 +108,6 @@ struct Elem<__nv_bfloat16> {
     static __device__ __forceinline__ float2 unpack(uint32_t v) {
         return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
     }
-    static __device__ __forceinline__ __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
 };
 
 template <>
@@ -121,12 +120,6 @@ struct Elem<__half> {
     static __device__ __forceinline__ float2 unpack(uint32_t v) {
         return __half22float2(*reinterpret_cast<const __half2 *>(&v));
     }
-    static __device__ __forceinline__ __half from(float x) { return __float2half_rn(x); }
-};
-
-template <>
-struct Elem<float> {
-    static __device__ __forceinline__ float from(float x) { return x; }
 };
 
 // 2^x (the softmax works in base 2: exp(scale s - m) = 2^(scale log2(e) s - m log2(e))).
@@ -140,14 +133,10 @@ constexpr float kLog2E = 1.4426950408889634f;
 
 // ------------------------------------------------------------------ tensor maps
 
-// Encodes a 2-D tensor map of `rows` rows of `cols` elements, loaded in boxes of
-// box_rows rows by 128 bytes with the 128-byte swizzle: 16-byte chunk c of row r lands at
-// byte r * 128 + ((c ^ (r & 7)) << 4) of a 1024-byte aligned box.
-gdn_status encode_rows_map(CUtensorMap *map, const void *base, int dtype, int cols, uint64_t rows,
-                           uint64_t row_bytes, int box_rows);
-
-// The same rows seen as [cols / box columns][rows][128 bytes], loaded in boxes of box_blocks x
-// box_rows x 128 bytes: the 128-byte columns of a few rows, one behind the other.
+// Encodes a 3-D tensor map of `rows` rows of `cols` elements, seen as [columns of 128 bytes]
+// [rows][128 bytes] and loaded in boxes of box_blocks x box_rows x 128 bytes: the columns of a
+// few rows, one behind the other, with the 128-byte swizzle: 16-byte chunk c of row r lands at
+// byte r * 128 + ((c ^ (r & 7)) << 4) of a 1024-byte aligned column.
 gdn_status encode_blocks_map(CUtensorMap *map, const void *base, int dtype, int cols, uint64_t rows,
                              uint64_t row_bytes, int box_rows, int box_blocks);
 
@@ -155,15 +144,6 @@ gdn_status encode_blocks_map(CUtensorMap *map, const void *base, int dtype, int 
 // t * box_heads + h), same swizzle.
 gdn_status encode_heads_map(CUtensorMap *map, const void *base, int dtype, int cols, int heads,
                             uint64_t tokens, uint64_t token_bytes, int box_heads, int box_tokens);
-
-__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int c0, int c1,
-                                            uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_addr(bar))
-        : "memory");
-}
 
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int c0, int c1,
                                             int c2, uint64_t *bar) {
@@ -193,7 +173,6 @@ inline gdn_status allow_smem(Kernel kernel, int bytes, std::atomic<unsigned long
     done.fetch_or(bit, std::memory_order_relaxed);
     return GDN_OK;
 }
-
 
 // Arguments every call on a paged cache shares.
 inline gdn_status check_cache(int n_kv_heads, int head_dim, int page_size, int n_pages,
