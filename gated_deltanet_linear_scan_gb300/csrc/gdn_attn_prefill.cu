@@ -58,21 +58,27 @@ constexpr int kSimtKeys = 32;
 
 template <int D>
 constexpr int simt_smem() {
-    return ((kSimtRows + 2 * kSimtKeys) * (D + 4) + kSimtRows * (kSimtKeys + 4)) * 4;
+    return ((kSimtRows + 4 * kSimtKeys) * (D + 4) + kSimtRows * (kSimtKeys + 4)) * 4;
 }
 
 // 64 rows by 32 keys a step, everything in fp32: a thread holds 4 rows x 4 keys of S (8
 // lanes span the keys) and 4 rows x D/8 columns of O. Rows of shared memory are padded by 16
 // bytes, so the 8 lanes of a quarter-warp read different banks.
+//
+// The tensor cores have no fp32 product, so the FP32 pipes bound it (78 TFLOP/s), and before
+// them the reads of shared memory that feed them: 8 reads of 16 bytes for 64 multiply-adds of
+// S, 5 for 64 of O, at 4 cycles of the SM's one port a read. 16384 ragged prompt tokens: 5.47
+// ms at head_dim 128 with 32 heads (31.7 TFLOP/s), 1.51 ms at 64 with 16 (28.7), 9.25 ms at
+// 256 with 24 (28.1; 12.9 ms before K and V were loaded a tile ahead).
 template <int D>
 __global__ void __launch_bounds__(kSimtThreads)
 attn_prefill_f32_kernel(const PrefillParams p) {
     constexpr int P = D + 4, PP = kSimtKeys + 4;
     extern __shared__ __align__(16) float sm[];
-    float *sq = sm, *sk = sq + kSimtRows * P, *sv = sk + kSimtKeys * P, *sp = sv + kSimtKeys * P;
+    float *sq = sm, *skv = sq + kSimtRows * P, *sp = skv + 4 * kSimtKeys * P;  // K, V, twice
     RowTile t;
     if (!find_tile(p, t)) return;
-    const int tid = threadIdx.x, tx = tid & 7, ty = tid >> 3;
+    const int tid = threadIdx.x, lane = tid & 31, tx = tid & 7, ty = tid >> 3;
     const float *q = static_cast<const float *>(p.q);
     const float *k_pages = static_cast<const float *>(p.k_pages);
     const float *v_pages = static_cast<const float *>(p.v_pages);
@@ -95,29 +101,52 @@ attn_prefill_f32_kernel(const PrefillParams p) {
         for (int c = 0; c < D / 8; ++c) o[i][c] = 0.0f;
     }
     const TileWalk walk = walk_tiles<kSimtKeys>(p.mask, t.p_first, t.p_last);
+    // The page of this lane's key of tile w, -1 for keys that no row of the tile sees: they are
+    // not looked up, their pages may be gone, and whatever a page holds past the length must
+    // not reach the sums.
+    auto page_at = [&](int w) {
+        if (w >= walk.count) return -1;
+        const int key = walk.tile(w) * kSimtKeys + lane;
+        const bool seen = key <= t.p_last && (t.p_first - key < p.mask.window || key < p.mask.sinks);
+        const int page = seen ? p.cache.page_of(t.slot, key) : -1;
+        const bool ok = p.cache.page_ok(page);
+        if (__any_sync(FULL_MASK, seen && !ok) && tid == 0 && blockIdx.y == 0 && p.err_count)
+            atomicAdd(p.err_count, 1);
+        return ok ? page : -1;
+    };
+    // Asks for tile w's rows (keys that nobody sees are zeros); returns which keys are there.
+    auto load = [&](int w, int page) {
+        const unsigned there = __ballot_sync(FULL_MASK, page >= 0);
+        float *sk = skv + (w & 1) * 2 * kSimtKeys * P, *sv = sk + kSimtKeys * P;
+        const int in_page = (walk.tile(w) * kSimtKeys + lane) & (ps - 1);
+        const int row = ((page * p.cache.n_kv_heads) + t.kvh) * ps + in_page;  // (fits: the cache's rows do)
+#pragma unroll 4
+        for (int x = tid; x < kSimtKeys * (D / 4); x += kSimtThreads) {
+            const int i = x / (D / 4), c = (x % (D / 4)) * 4;
+            const size_t at = static_cast<size_t>(__shfl_sync(FULL_MASK, row, i)) * D + c;
+            if ((there >> i) & 1u) {
+                cp_async16(sk + i * P + c, k_pages + at);
+                cp_async16(sv + i * P + c, v_pages + at);
+            } else {
+                *reinterpret_cast<float4 *>(sk + i * P + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                *reinterpret_cast<float4 *>(sv + i * P + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+        }
+        return there;
+    };
+    // tile w + 1 is on its way while tile w is computed, and the pages of tile w + 2 are looked up
+    unsigned next_there = walk.count > 0 ? load(0, page_at(0)) : 0;
+    int next_page = page_at(1);
     for (int w = 0; w < walk.count; ++w) {
         const int key0 = walk.tile(w) * kSimtKeys;
-        __syncthreads();  // the previous tile has been read
-        for (int x = tid; x < kSimtKeys * (D / 4); x += kSimtThreads) {
-            const int i = x / (D / 4), c = (x % (D / 4)) * 4, key = key0 + i;
-            float4 kv = make_float4(0.0f, 0.0f, 0.0f, 0.0f), vv = kv;
-            // keys no row of the tile sees are not looked up: their pages may be gone, and
-            // whatever a page holds past the length must not reach the sums
-            if (key <= t.p_last && (t.p_first - key < p.mask.window || key < p.mask.sinks)) {
-                const int page = p.cache.page_of(t.slot, key);
-                if (p.cache.page_ok(page)) {
-                    const size_t at =
-                        ((static_cast<size_t>(page) * p.cache.n_kv_heads + t.kvh) * ps + (key & (ps - 1))) * D + c;
-                    kv = load_float4(k_pages + at);
-                    vv = load_float4(v_pages + at);
-                } else if (c == 0 && blockIdx.y == 0 && p.err_count && (key & (ps - 1)) == 0) {
-                    atomicAdd(p.err_count, 1);
-                }
-            }
-            *reinterpret_cast<float4 *>(sk + i * P + c) = kv;
-            *reinterpret_cast<float4 *>(sv + i * P + c) = vv;
+        const unsigned there = next_there;
+        const float *sk = skv + (w & 1) * 2 * kSimtKeys * P, *sv = sk + kSimtKeys * P;
+        cp_async_wait_all();
+        __syncthreads();  // this tile is there, and the one before has been read
+        if (w + 1 < walk.count) {
+            next_there = load(w + 1, next_page);
+            next_page = page_at(w + 2);
         }
-        __syncthreads();
         float s[4][4] = {};
 #pragma unroll 4
         for (int c = 0; c < D; c += 4) {
@@ -142,9 +171,8 @@ attn_prefill_f32_kernel(const PrefillParams p) {
             float top = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int key = key0 + tx + 8 * j;
-                bool ok = p.mask.sees(pos, key) && key <= t.p_last;
-                if (ok) ok = p.cache.page_ok(p.cache.page_of(t.slot, key));
+                const int k = tx + 8 * j;
+                const bool ok = ((there >> k) & 1u) && p.mask.sees(pos, key0 + k);
                 s[i][j] = ok ? s[i][j] * p.scale_log2 : -INFINITY;
                 top = fmaxf(top, s[i][j]);
             }

@@ -166,6 +166,9 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
                  : "memory");
 }
 
+// Waits for every cp_async16 of this thread.
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Arrive on `bar` once every cp_async16 this thread issued before has landed. The
 // arrival is not counted in advance (.noinc): `bar`'s expected count includes it.
 __device__ __forceinline__ void cp_async_arrive_noinc(uint64_t *bar) {
