@@ -28,6 +28,16 @@
 // hardware cancels the launch of a CTA that has not begun and hands over its index), looks
 // its sequence up and loads its Q, while the other warps are still busy with the one before.
 // Sequences go longest first, their last tokens first, so the work left at the end is small.
+//
+// Measured, with the rate of the visible pairs' products and its share of a large bf16 matrix
+// product's: 1500 tokens after 30000, 24 heads of 256, 720 us, 1575 TFLOP/s (0.84); 16384
+// tokens of 39 ragged prompts, 32 heads of 128, 193 us, 898 TFLOP/s (0.48); 4 x 4096 tokens
+// with a window of 1000, 16 heads of 64, 131 us, 452 TFLOP/s (0.24). Key tile by key tile, a
+// pair of row tiles takes 1.84 us at head_dim 128 and 1.55 at 64, where the tensor pipe is busy
+// for 1.07 and 0.67: S, its softmax, and O are a chain per row tile, and the warps of the two
+// softmaxes, the products and the copies, at different places of long unrolled code, wait
+// for instructions (two thirds of the time a scheduler issues nothing). A work's partial tiles,
+// its first Q and its output add two to three tiles' time to each.
 #include "gdn_attn_prefill.cuh"
 #include "gdn_tc.cuh"
 
@@ -63,7 +73,8 @@ struct Tc {
     static constexpr int kMma = kSoftmax, kK = kMma + 1, kSched = kMma + 3;
     static constexpr int kThreads = (kSoftmax + 4) * 32;
     static constexpr int kS = 0, kO = 256;                      // tensor-memory columns
-    // batches up to this many sequences run longest first (what shared memory has left)
+    // batches up to this many sequences run longest first (what shared memory has left): the 39
+    // ragged prompts above take 193 us, in batch order 233
     static constexpr int kTable = D == 256 ? 32 : kLongestFirstMaxSeqs;
 };
 

@@ -29,8 +29,10 @@ struct AppendParams {
 constexpr int kAppendThreads = 128;
 constexpr int kAppendEach = 4;  // 16-byte units of a plane a lane holds at a time
 
-// A few warps per new position (four while the batch is small and latency counts, one when
-// there are enough tokens to fill the GPU). The rows are loaded first and find their place --
+// A few warps per new position: four while the batch is small and latency counts, one when
+// there are enough tokens to fill the GPU (16 a SM). 64 tokens of 16 bf16 heads of 128: 2.7 us
+// with four, 3.2 with one; 16384 tokens of 8 f16 heads of 128: 20.7 us with one (0.95 of the
+// copy rate), 28.3 with four. The rows are loaded first and find their place --
 // sequence, slot, length, page: four dependent loads -- while they are under way. Also, the
 // warp of number n checks sequence n, last, and counts it when it is skipped.
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
@@ -397,7 +399,10 @@ struct MoveParams {
 constexpr int kMoveThreads = 256;
 constexpr int kMoveEach = 8;  // 16-byte loads in flight per thread
 
-// Pieces of 32 KB (a page of a plane, or part of one) dealt round-robin to the CTAs.
+// Pieces of 32 KB (a page of a plane, or part of one) dealt round-robin to the CTAs, all of a
+// piece's loads ahead of its stores. HBM bounds it: 64 forks of a partly full page in 8 planes
+// of 128 KB pages 24 us with their plan (0.8 of the copy rate); 0.53 GB of pages moved to make a
+// pool dense 175 us (0.89).
 __device__ __forceinline__ void move_pages(const MoveParams &p) {
     constexpr size_t kPiece = static_cast<size_t>(kMoveThreads) * kMoveEach;
     const int n = p.count ? *p.count : p.n_moves;
