@@ -8,10 +8,12 @@
 // of one small matrix product, so a key byte is read once for all of them.
 //
 // Work split. A unit is (sequence, key head, group of at most 16 rows); its keys are cut in
-// tiles of 32 KB (64 KB for the widest heads). The tiles of all units, in order, are dealt
-// out evenly as one contiguous range per CTA, whatever the lengths: a ragged batch, one long
-// sequence and many short ones all keep every SM equally busy, with no host knowledge of the
-// lengths. A unit that crosses a range boundary leaves partial results (m, l, o) in the
+// tiles of 32 KB (64 KB for the widest heads). The units, in order, each weighing its tiles and
+// one more for the turn to it, are dealt out evenly as one contiguous range per CTA, whatever
+// the lengths: a ragged batch, one long sequence and many short ones all keep every SM equally
+// busy, with no host knowledge of the lengths. (By tiles alone, the CTAs that got the short
+// sequences were last: windowed fp32 pool 56 us, 48 with the turn weighed as one tile, 50 as two;
+// 200 bf16 sequences of 16..2000 keys 149, 122, 129.) A unit that crosses a range boundary leaves partial results (m, l, o) in the
 // workspace; the CTA that arrives last on it joins them in CTA order, so the bits do not
 // depend on timing.
 //
@@ -22,15 +24,16 @@
 // running maximum is shared and O needs no join across warps.
 //
 // Measured (calls replayed back to back; the share is of the visible keys' and values' bytes
-// at the copy rate): 64 sequences of 64..8192 bf16 keys, 16 key heads of 128: 178 us, 0.92.
+// at the copy rate): 64 sequences of 64..8192 bf16 keys, 16 key heads of 128: 172 us, 0.95.
 // Four of 60 to 131 thousand f16 keys, 2 key heads of 256: 99 us, 0.87. 64 sequences with 4
 // draft tokens each, 4 key heads of 128: 60 us, 0.77. Units of a few tiles are bound by the
 // chain of steps of a tile and by the turn from unit to unit: a pool of 256 sequences with
-// windows of 1024 fp32 keys, 4 key heads of 64: 57 us, 0.57. One sequence of 1000 keys is
+// windows of 1024 fp32 keys, 4 key heads of 64: 48 us, 0.68. One sequence of 1000 keys is
 // launch, one tile's chain and the join: 10 us.
 #include <atomic>
 #include <ctime>
 
+#include "gdn_chunk_common.cuh"  // named_barrier_or
 #include "gdn_paged.cuh"
 
 namespace gdn {
@@ -44,9 +47,10 @@ constexpr int kRows = 16;                       // rows of a unit
 constexpr int kSMs = 152;
 constexpr int kMaxCtas = 3 * kSMs;
 constexpr int kJoin = 8;                        // partial results loaded together in a join
+constexpr unsigned kTurn = 1;                   // what a unit weighs besides its tiles, in tiles
 
-// kHead: the unit's first tile lies in this CTA's range.
-enum : int { kFirst = 1, kLast = 2, kWhole = 4, kHead = 8 };  // kWhole, kHead: of a segment
+// kHead: the unit's first tile lies in this CTA's range. kEnd: the range's last tile.
+enum : int { kFirst = 1, kLast = 2, kWhole = 4, kHead = 8, kEnd = 16 };  // kWhole, kHead: of a segment
 
 // What the loading warp tells the computing warps: about a stage (the first key of its tile,
 // and flags | blocks << 8, bit b of blocks: keys 8 b .. 8 b + 7 lie in a page that was
@@ -92,13 +96,13 @@ struct Geometry {
                                        : 2 * kRows * (KT + 8) * 2;   // P hi and lo [row][key]
     // CTAs per SM. A tile's chain of steps is latency: the more chains side by side the better,
     // as far as two stages and the registers of each allow. (The windowed fp32 pool above takes
-    // 57 us with three CTAs and 68 with two.)
+    // 48 us with three CTAs and 52 with two.)
     static constexpr int kCtas = D == 256 ? 1 : kF32 && D == 64 && RT == 4 ? 3 : 2;
     // Threads: the computing warps, the loading warp and, where it costs no registers (three
     // CTAs of 5 warps fill the register file), a joining warp: it waits for the other CTAs of
-    // the unit split at the range's start while the rest go on. (Windowed pools, bf16 with heads
-    // of 64 and fp32 of 128: 38.1 and 113.9 us with it, 39.0 and 117.5 without; 200 ragged bf16
-    // sequences of up to 2000 keys: 147 against 145.)
+    // the unit split at the range's start while the rest go on. (Windowed bf16 pool with heads of
+    // 64: 33.7 us with it, 34.6 without; 200 ragged bf16 sequences of up to 2000 keys 121.8 and
+    // 123.4.)
     static constexpr bool kJoinWarp = kCtas != 3;
     static constexpr int kThreads = kCompute + (kJoinWarp ? 64 : 32);
     // shared memory of a CTA, less alignment slack and the static part
@@ -368,7 +372,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     for (int n = n0; n < n1; ++n) {
         const unsigned t = tiles_of(n, slot0, len0);
         if (t == 0 && blockIdx.x == 0 && p.err_count) atomicAdd(p.err_count, 1);
-        sum += t * units;
+        if (t != 0) sum += (t + kTurn) * units;
     }
     unsigned before = sum;
 #pragma unroll
@@ -385,21 +389,26 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         if (w < warp) before += warp_sum[w];
         total += warp_sum[w];
     }
-    // The ranges: no range is empty, so the CTAs of a split unit are consecutive and all of
-    // them arrive; the first `longer` hold one tile more.
-    const unsigned ranges = min(gridDim.x, total);
+    // The ranges, in units' weights: a unit is kTurn places without a tile, then its tiles. No
+    // range is without a tile, so the CTAs of a split unit are consecutive and all of them
+    // arrive; the first `longer` are one place longer.
+    const unsigned ranges = min(gridDim.x, total / (1 + kTurn));
     if (blockIdx.x >= ranges) return;
     const unsigned each = total / ranges, longer = total - each * ranges;
     auto range_begin = [&](unsigned c) { return c * each + min(c, longer); };
     const unsigned begin = range_begin(blockIdx.x), end = range_begin(blockIdx.x + 1);
-    auto owner = [&](unsigned x) {  // of tile x
+    auto owner = [&](unsigned x) {  // of place x
         const unsigned split = longer * (each + 1);
         return static_cast<int>(x < split ? x / (each + 1) : longer + (x - split) / each);
     };
     if (begin >= before && begin < before + sum) {
         unsigned at = before;
         for (int n = n0; n < n1; ++n) {
-            const unsigned w = (per == 1 ? sum : tiles_of(n, slot0, len0) * units);
+            unsigned w = sum;
+            if (per != 1) {
+                const unsigned t = tiles_of(n, slot0, len0);
+                w = t == 0 ? 0 : (t + kTurn) * units;
+            }
             if (begin < at + w) {
                 sh_seq = n;
                 sh_slot = slot0;
@@ -429,11 +438,14 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         unsigned seq_begin = sh_seq_begin, at = begin;
         TileWalk walk = walk_tiles<KT>(p.mask, len - p.n_tokens, len - 1);
         unsigned tiles = static_cast<unsigned>(max(1, walk.count));
-        unsigned unit = (at - seq_begin) / tiles;
+        unsigned unit = (at - seq_begin) / (tiles + kTurn);
         int st = 0, seg = 0;
         unsigned st_round = 0;
         while (at < end) {
-            const unsigned unit_begin = seq_begin + unit * tiles, unit_end = unit_begin + tiles;
+            const unsigned unit_begin = seq_begin + unit * (tiles + kTurn) + kTurn;  // its first tile
+            const unsigned unit_end = unit_begin + tiles;
+            at = max(at, unit_begin);
+            if (at >= end) break;
             const unsigned seg_end = min(unit_end, end);
             int kvh = static_cast<int>(unit), hg = 0, tg = 0;
             if (subs > 1) {
@@ -496,7 +508,9 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                         sg.c1 = whole ? 0 : owner(unit_end - 1);
                         segments[seg & 1] = sg;
                     }
-                    stages[st] = make_int2(key0, (first ? kFirst : 0) | (at + 1 == seg_end ? kLast : 0) |
+                    const bool last = at + 1 == seg_end, at_end = end <= unit_end + kTurn;
+                    stages[st] = make_int2(key0, (first ? kFirst : 0) | (last ? kLast : 0) |
+                                                     (last && at_end ? kEnd : 0) |
                                                      static_cast<int>(blocks << 8));
                     mbar_arrive_expect_tx(&full[st], bytes);
                 }
@@ -537,7 +551,6 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     }
 
     // -------------------------------------------------------------- the computing warps
-    const int n_tiles = static_cast<int>(end - begin);
     // 16-bit: NT tiles of 8 columns (a quarter of the head), rows lane/4 and lane/4 + 8
     constexpr int NT = D / 32;
     constexpr int KN = G::kWarpKeys / 8;  // 8-key tiles of S of a warp
@@ -550,7 +563,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     constexpr int NKG = 32 / C4;
     float o32[G::kF32 ? RT : 1][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-    Segment sg;
+    Segment sg{};
     // rows of this thread (16-bit: lane / 4 and lane / 4 + 8; fp32: the row of its scores):
     // token and head in the unit, position
     const int row0 = G::kF32 ? tid / LPR : lane >> 2, row1 = (lane >> 2) + 8;
@@ -561,20 +574,28 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     int seg = 0, s = 0;
     uint32_t phase = 0;
 
-    for (int it = 0; it < n_tiles; ++it) {
+    bool more = true;  // tiles in this range
+    // A tile's first barrier also tells whether a wait gave up: then all warps leave together,
+    // before anything that was read of the stage is relied on.
+    auto gave_up = [&](int flags) {
+        if (chunk::named_barrier_or(1, kCompute, *static_cast<volatile int *>(&sh_dead) != 0)) return true;
+        if ((flags & kFirst) && tid == 0 && !(sg.flags & kWhole))
+            word_seen = *reinterpret_cast<volatile unsigned long long *>(p.counters + sg.c0);
+        return false;
+    };
+    for (int it = 0; more; ++it) {
         wait_or_flag(&full[s], phase, &sh_dead);
         const int2 stage = stages[s];
         const int key0 = stage.x, flags = stage.y;
         const unsigned blocks = static_cast<unsigned>(stage.y) >> 8;
+        more = !(flags & kEnd);
         if (flags & kFirst) {
             sg = segments[seg & 1];
             m0 = m1 = -INFINITY;
             l0 = l1 = 0.0f;
             const int base = sg.len - p.n_tokens + sg.token_group * p.tokens_per_unit;
-pos0 = base + tok0;
+            pos0 = base + tok0;
             pos1 = base + tok1;
-            if (tid == 0 && !(sg.flags & kWhole))
-                word_seen = *reinterpret_cast<volatile unsigned long long *>(p.counters + sg.c0);
         }
         const int p_first = sg.len - p.n_tokens, p_last = sg.len - 1;
         const bool clean = blocks == (1u << (KT / 8)) - 1u && key0 + KT - 1 <= p_first &&
@@ -687,7 +708,7 @@ pos0 = base + tok0;
                 red[warp][r0] = t0;
                 red[warp][r0 + 8] = t1;
             }
-            named_barrier_sync(1, kCompute);
+            if (gave_up(flags)) break;
             const float old0 = m0, old1 = m1;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
@@ -758,7 +779,7 @@ pos0 = base + tok0;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o32[r][e] = 0.0f;
             }
-constexpr int KH = G::kWarpKeys / 8;  // keys of a lane
+            constexpr int KH = G::kWarpKeys / 8;  // keys of a lane
             {
                 // lane: every 8th key of the warp's and a quarter of the dot product
                 const int i0 = warp * G::kWarpKeys + (lane & 7), quarter = lane >> 3;
@@ -812,7 +833,7 @@ constexpr int KH = G::kWarpKeys / 8;  // keys of a lane
                         if ((r & 3) == quarter) sp[(i0 + 8 * h) * RT + r] = acc[h][r] * p.scale_log2;
                     }
             }
-            named_barrier_sync(1, kCompute);
+            if (gave_up(flags)) break;
             {
                 const int r = tid / LPR, part = tid % LPR;
                 float x[KT / LPR];
@@ -965,7 +986,7 @@ constexpr int KH = G::kWarpKeys / 8;  // keys of a lane
         // A range has at most two split units, its first and its last. The first one's arrival
         // (a fence takes thousands of cycles while copies are under way) and join are left to
         // the joining warp; the last one's are the CTA's last work.
-        if (it + 1 < n_tiles && G::kJoinWarp) {
+        if (more && G::kJoinWarp) {
             if (tid == 0) early = sg;
             had_early = true;
             __syncwarp();
@@ -1043,7 +1064,7 @@ gdn_status launch_rows(const CUtensorMap &q, const CUtensorMap &k, const CUtenso
                        const Params &p, cudaStream_t s) {
     if constexpr (sizeof(T) == 4) {
         // the FP32 pipes' work grows with the rows laid out: 3 rows a unit in the windowed pool
-        // take 57 us laid out for 4 and 175 for 16
+        // take 48 us laid out for 4 and 124 for 16
         const int rows = p.heads_per_unit * p.tokens_per_unit;
         if (rows <= 4) return launch<T, D, 4>(q, k, v, p, s);
         if (rows <= 8) return launch<T, D, 8>(q, k, v, p, s);
@@ -1134,7 +1155,7 @@ gdn_status gdn_attn_decode(const void *q, const void *k_pages, const void *v_pag
 
     // the ranges are counted in 32 bits (2^31 tiles are some 70 TB read in one call)
     const int kt = (head_dim == 64 ? 2 : 1) * (dtype == GDN_F32 ? 32 : 64);
-    const long long widest = (static_cast<long long>(max_pages) * page_size + kt - 1) / kt + 2;
+    const long long widest = (static_cast<long long>(max_pages) * page_size + kt - 1) / kt + 2 + kTurn;
     if (widest * n_kv_heads * sp.head_groups * sp.token_groups > 0x7fffffffLL / n_seqs)
         return GDN_ERR_UNSUPPORTED;
     CUtensorMap q_map, k_map, v_map;

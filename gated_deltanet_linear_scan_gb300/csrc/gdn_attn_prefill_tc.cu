@@ -42,6 +42,37 @@
 #include "gdn_tc.cuh"
 
 namespace gdn {
+namespace tc {
+
+// ---- 128-byte swizzled operands, as tensor-map loads leave them: 1024-byte aligned blocks
+// of rows of 128 bytes (64 16-bit elements), 16-byte chunk c of row r at chunk c ^ (r & 7).
+
+// K-major: rows are M or N indices, the 64 elements run along K; a K step of 16 elements
+// advances the start address by 32 bytes, 64 elements are the next block.
+__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t start) {
+    return static_cast<uint64_t>((start & 0x3FFFFu) >> 4) | static_cast<uint64_t>(1) << 16 |
+           static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 |
+           static_cast<uint64_t>(2) << 61;
+}
+
+// MN-major: rows are K indices, the 64 elements run along N; `block` bytes lie between one
+// block of 64 N elements and the next, `group` between one group of 8 rows and the next.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t start, uint32_t block, uint32_t group) {
+    return static_cast<uint64_t>((start & 0x3FFFFu) >> 4) |
+           static_cast<uint64_t>((block >> 4) & 0x3FFFu) << 16 |
+           static_cast<uint64_t>((group >> 4) & 0x3FFFu) << 32 | static_cast<uint64_t>(1) << 46 |
+           static_cast<uint64_t>(2) << 61;
+}
+
+// Instruction descriptor of a dense kind::f16 MMA, f32 accumulator, A and B both bf16 or
+// both f16, A K-major (or in tensor memory), B K-major or MN-major.
+__host__ __device__ constexpr uint32_t idesc_16bit(bool bf16, int m, int n, bool b_mn_major) {
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn_major ? 1u << 16 : 0u) |
+           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+}  // namespace tc
+
 namespace {
 
 __device__ unsigned g_watchdog_attn_prefill;

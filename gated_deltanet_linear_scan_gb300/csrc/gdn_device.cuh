@@ -65,30 +65,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Whether phase `parity` of `bar` has completed; does not suspend the thread.
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok));
-    return ok != 0;
-}
-
 // Waits for phase `parity` of `bar` to complete, for at most limit_ns. Returns false
 // if it gave up.
 __device__ __forceinline__ bool mbar_wait_for(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
@@ -140,14 +116,6 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint64_t *bar, uint32_t parity,
     return true;
 }
 
-// For a CTA that leaves after a wait gave up: copies and tensor-core products it may still
-// have in flight finish within microseconds, long before this returns, so none of them
-// outlives the CTA's shared or tensor memory.
-__device__ __forceinline__ void drain_in_flight() {
-    const uint64_t t0 = global_timer_ns();
-    while (global_timer_ns() - t0 < 500000) __nanosleep(1000);
-}
-
 // 1-D bulk copy global -> shared (TMA engine), completion counted on `bar` in bytes.
 // dst and src 16-byte aligned, bytes a multiple of 16.
 __device__ __forceinline__ void bulk_g2s(void *dst, const void *src, uint32_t bytes,
@@ -165,9 +133,6 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src)
                  : "memory");
 }
-
-// Waits for every cp_async16 of this thread.
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Arrive on `bar` once every cp_async16 this thread issued before has landed. The
 // arrival is not counted in advance (.noinc): `bar`'s expected count includes it.

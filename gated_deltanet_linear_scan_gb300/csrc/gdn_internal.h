@@ -176,8 +176,6 @@ unsigned read_and_clear_watchdog_recurrence(cudaStream_t s);
 unsigned read_and_clear_watchdog_block(cudaStream_t s);
 unsigned read_and_clear_watchdog_chunked(cudaStream_t s);
 unsigned read_and_clear_watchdog_chunked_ws(cudaStream_t s);
-unsigned read_and_clear_watchdog_attn_decode(cudaStream_t s);
-unsigned read_and_clear_watchdog_attn_prefill(cudaStream_t s);
 
 }  // namespace gdn
 

@@ -9,6 +9,7 @@
 
 #include "gdn_device.cuh"
 #include "gdn_internal.h"
+#include "gdn_paged.cuh"
 
 namespace gdn {
 namespace {

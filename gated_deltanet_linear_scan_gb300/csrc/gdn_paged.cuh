@@ -14,6 +14,10 @@
 
 namespace gdn {
 
+// Watchdog flags of the attention kernels' units (a bounded wait that gave up sets a bit).
+unsigned read_and_clear_watchdog_attn_decode(cudaStream_t s);
+unsigned read_and_clear_watchdog_attn_prefill(cudaStream_t s);
+
 inline bool supported_dtype(int dtype) {
     return dtype == GDN_F32 || dtype == GDN_F16 || dtype == GDN_BF16;
 }
@@ -157,6 +161,43 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
+
+// ------------------------------------------------------------------ waits and copies
+
+// Whether phase `parity` of `bar` has completed; does not suspend the thread.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
+}
+
+// For a CTA that leaves after a wait gave up: copies and tensor-core products it may still
+// have in flight finish within microseconds, long before this returns, so none of them
+// outlives the CTA's shared or tensor memory.
+__device__ __forceinline__ void drain_in_flight() {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 500000) __nanosleep(1000);
+}
+
+// Waits for every cp_async16 of this thread.
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // ------------------------------------------------------------------ host side
 
