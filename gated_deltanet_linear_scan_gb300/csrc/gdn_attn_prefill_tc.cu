@@ -34,9 +34,9 @@
 // tokens of 39 ragged prompts, 32 heads of 128, 193 us, 898 TFLOP/s (0.48); 4 x 4096 tokens
 // with a window of 1000, 16 heads of 64, 131 us, 452 TFLOP/s (0.24). Key tile by key tile, a
 // pair of row tiles takes 1.84 us at head_dim 128 and 1.55 at 64, where the tensor pipe is busy
-// for 1.07 and 0.67: S, its softmax, and O are a chain per row tile, and the warps of the two
-// softmaxes, the products and the copies, at different places of long unrolled code, wait
-// for instructions (two thirds of the time a scheduler issues nothing). A work's partial tiles,
+// for 1.07 and 0.67: S, its softmax, and O are a chain per row tile, and when the warps of the
+// two softmaxes run together, at different places of long unrolled code, they wait for
+// instructions (a scheduler issues in 36 to 43 % of its cycles). A work's partial tiles,
 // its first Q and its output add two to three tiles' time to each.
 #include "gdn_attn_prefill.cuh"
 #include "gdn_tc.cuh"
