@@ -716,11 +716,15 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                 m1 = fmaxf(m1, red[w][r0 + 8]);
             }
             // a row that has seen nothing yet keeps its weights at 2^-inf = 0
-            const float base0 = m0 == -INFINITY ? 0.0f : m0;
-            const float base1 = m1 == -INFINITY ? 0.0f : m1;
+            float base0 = m0 == -INFINITY ? 0.0f : m0;
+            float base1 = m1 == -INFINITY ? 0.0f : m1;
             const float corr0 = fast_exp2(old0 - base0), corr1 = fast_exp2(old1 - base1);
             // P is kept in two parts of the cache's type, hi + lo, so that rounding the
-            // weights adds nothing to the output's own rounding; the tensor pipe has room
+            // weights adds nothing to the output's own rounding; the tensor pipe has room.
+            // (float16's steps end at 2^-24, so its weights go up to 2^14 instead of 1: what is
+            // lost of a small one is 2^-39 of the largest. l carries the same factor.)
+            base0 -= Elem<T>::kWeightBits;
+            base1 -= Elem<T>::kWeightBits;
             uint8_t *ph = extra, *pl = extra + kRows * (KT + 8) * 2;
             l0 *= corr0;
             l1 *= corr1;

@@ -104,6 +104,7 @@ struct Elem;
 
 template <>
 struct Elem<__nv_bfloat16> {
+    static constexpr float kWeightBits = 0.0f;  // log2 of the largest weight held in two parts
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
         uint32_t r;
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -116,6 +117,7 @@ struct Elem<__nv_bfloat16> {
 
 template <>
 struct Elem<__half> {
+    static constexpr float kWeightBits = 14.0f;
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
         uint32_t r;
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
