@@ -9,7 +9,7 @@
 //                  (rows are keys: the MN-major operand form, no transposition)
 //
 // O stays in tensor memory. It is rescaled only when a row's maximum has grown by more than
-// 2^8 since the reference the weights use (they stay below 2^8, far inside both types).
+// 2^8 since the reference the weights use (they stay within 2^8 in bf16, 2^15 in f16).
 //
 // A row tile is 128 rows: tokens x the heads of a key head. Two row tiles (head_dim 64, 128)
 // share every key tile of 128 keys and alternate: one tile's softmax runs while the tensor
@@ -225,6 +225,10 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     using C = Tc<D>;
     constexpr bool kBf16 = !__is_same(T, __half);
     constexpr uint32_t kIdescO = tc::idesc_16bit(kBf16, kTcRows, D, true);
+    // log2 of the weight at the reference. float16's steps end at 2^-24: with 2^7, and the
+    // allowance of 2^8 on top, its weights use the type's whole range, and what is lost of a
+    // small one is 2^-32 of the largest. (l carries the same factor.)
+    constexpr float kWeightBits = kBf16 ? 0.0f : 7.0f;
     extern __shared__ uint8_t dyn[];
     uint8_t *smem =
         reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
@@ -804,7 +808,7 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
                     for (int c = 0; c < 4; ++c) top_of(s[c], top);
                     settle(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
-                    const float off = m == -INFINITY ? 0.0f : m * mult;
+                    const float off = (m == -INFINITY ? 0.0f : m * mult) - kWeightBits;
                     const float2 mul2 = make_float2(mult, mult), sub2 = make_float2(-off, -off);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) weigh(s[c], mul2, sub2, s_addr + c * (kChunk / 2));
@@ -841,7 +845,7 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                         top_of(s, top);
                     }
                     settle(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
-                    const float off = m == -INFINITY ? 0.0f : m * mult;
+                    const float off = (m == -INFINITY ? 0.0f : m * mult) - kWeightBits;
                     const float2 mul2 = make_float2(mult, mult), sub2 = make_float2(-off, -off);
 #pragma unroll 1
                     for (int c = seen.x; c < seen.y; ++c) {

@@ -69,3 +69,14 @@ def test_decode(cuda_lib, d, at, n_tokens):
     out = decode(cuda_lib, whole, np.tile(q, (n, 1, 1)), n_tokens, hkv, scale=1.0, slots=False)
     for i, got in enumerate(out.double().cpu().numpy().reshape(n, n_tokens, hkv, d)):
         agree(got, ref, q, c, 2.0 ** -39)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("at", [0, 70000])
+def test_prompt(cuda_lib, d, at):
+    """A few new tokens after a long history: one row tile sees all of it."""
+    rng = np.random.default_rng([d, at, 1])
+    c = strong_key(rng, 131071, 1, d, at)
+    q = ask(3, 2, d)
+    ref = attention(q, c.k[0], c.v[0], c.lens[0] - 3, 1.0, 0, 0)
+    agree(prefill(cuda_lib, c, q, [3], 2, scale=1.0).double().cpu().numpy(), ref, q, c, 2.0 ** -32)
