@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const Books b, const i
         const bool partial = len >= 0 && (len & ps_mask) != 0;
         const long long mine = rank;
         rank += partial;
-        if (len < 0 || rank > n_free) {
+        if (len < 0 || (partial && rank > n_free)) {
             ws.state[i] = -1;
             b.count_error();
             continue;

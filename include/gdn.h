@@ -702,8 +702,8 @@ gdn_status gdn_pages_reserve(void *pages, int32_t *page_table, int32_t *kv_lens,
 /* Slot children[i] becomes a copy of slot parents[i] (device int32[n_forks]): the full
  * pages are shared, a partly full last page is copied to a free one. A child must be empty
  * (kv_len 0) and no child may appear twice; a parent may have several children. A fork
- * with a slot out of range, a child that is not empty or is its own parent, or no free
- * page left for it (in call order) is skipped and counted. */
+ * with a slot out of range, a child that is not empty or is its own parent, or a partly
+ * full last page and no free page left for it (in call order) is skipped and counted. */
 gdn_status gdn_pages_fork(void *pages, int32_t *page_table, int32_t *kv_lens,
                           int32_t *page_refs, const int32_t *parents, const int32_t *children,
                           int n_forks, int page_size, int n_planes, int n_pages,
