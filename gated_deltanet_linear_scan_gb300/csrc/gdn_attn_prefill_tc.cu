@@ -174,14 +174,9 @@ struct TileNote {
     }
 };
 
-// Bounded wait; once one gave up, the CTA's later waits return at once and none of its rows
-// are written.
-__device__ __forceinline__ void wait_or_flag(uint64_t *bar, uint32_t parity, volatile int *dead) {
-    if (mbar_test(bar, parity) || *dead) return;
-    if (!mbar_wait(bar, parity)) {
-        *dead = 1;
-        atomicOr(&g_watchdog_attn_prefill, WD_STAGE_COPY);
-    }
+// False when a wait gave up: the warp then leaves for the CTA's end.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *dead) {
+    return gdn::warp_wait(bar, parity, dead, &g_watchdog_attn_prefill);
 }
 
 // Bits lo .. hi - 1 of a 32-bit word (any of them outside the word).
@@ -396,7 +391,7 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                             w.end[i] = walk.n_sink + last / kTcKeys + 1 - walk.main0;
                         }
                     }
-                    if (round > 0) wait_or_flag(&work_empty[ring], (round - 1) & 1, &sh_dead);
+                    if (round > 0 && !warp_wait(&work_empty[ring], (round - 1) & 1, &sh_dead)) goto leave;
                     if (leader) {
                         works[ring] = w;
                         mbar_arrive(&work_full[ring]);
@@ -410,7 +405,7 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
                     for (int i = 0; i < C::kTiles; ++i) {
                         if (w.end[i] == 0) continue;
-                        if (q_uses[i] > 0) wait_or_flag(&q_empty[i], (q_uses[i] - 1) & 1, &sh_dead);
+                        if (q_uses[i] > 0 && !warp_wait(&q_empty[i], (q_uses[i] - 1) & 1, &sh_dead)) goto leave;
                         ++q_uses[i];
                         if (leader) {
                             mbar_arrive_expect_tx(&q_full[i], static_cast<uint32_t>(p.heads_per_tile * per) * D * 2u);
@@ -421,14 +416,14 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                         __syncwarp();
                     }
                 }
-                wait_or_flag(&answer_full, asked & 1, &sh_dead);
+                if (!warp_wait(&answer_full, asked & 1, &sh_dead)) goto leave;
                 ++asked;
-                const bool more = next_cta(&answer, id) && !sh_dead;
+                const bool more = next_cta(&answer, id);
                 fence_proxy_async_smem();  // read before the next answer overwrites it
                 __syncwarp();
                 if (!more) break;
             }
-            if (round > 0) wait_or_flag(&work_empty[ring], (round - 1) & 1, &sh_dead);
+            if (round > 0 && !warp_wait(&work_empty[ring], (round - 1) & 1, &sh_dead)) goto leave;
             if (leader) {
                 works[ring].valid = 0;
                 mbar_arrive(&work_full[ring]);
@@ -447,13 +442,13 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 v_step[x] = (((x * 16) >> log2_bv) * (bv * D * 2) + ((x * 16) & (bv - 1)) * 128) >> 4;
             int s_count = 0, o_count = 0;         // products issued (one row tile: its buffer)
             uint32_t o_phase = 0, q_phase = 0;    // bit i: of row tile i's p_ready, q_full
+            // (The functions below return false when a wait gave up.)
             // The note of key tile g (numbered over all work), once its K is there.
-            auto note_of = [&](int g) {
+            auto note_of = [&](int g, TileNote &note) {
                 const int slot = (g * C::kSubs) % C::kKSlots;
-                wait_or_flag(&k_full[slot], (g * C::kSubs / C::kKSlots) & 1, &sh_dead);
-                // after a wait that gave up, no product is issued on a note never written
-                if (*static_cast<volatile int *>(&sh_dead)) return TileNote{0};
-                return TileNote{static_cast<volatile uint32_t *>(notes)[g % kNotes]};
+                if (!warp_wait(&k_full[slot], (g * C::kSubs / C::kKSlots) & 1, &sh_dead)) return false;
+                note.bits = static_cast<volatile uint32_t *>(notes)[g % kNotes];
+                return true;
             };
             // S of row tile i over key tile g. (This code and issue_o's stand once, in rolled loops:
             // unrolled for both row tiles the warp spent its time fetching instructions.)
@@ -461,7 +456,7 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 const int buf = C::kBufs == 2 ? s_count & 1 : i;
                 ++s_count;
                 if (note.first(i)) {
-                    wait_or_flag(&q_full[i], (q_phase >> i) & 1, &sh_dead);
+                    if (!warp_wait(&q_full[i], (q_phase >> i) & 1, &sh_dead)) return false;
                     q_phase ^= 1u << i;
                 }
                 const bool release = i == 1 || !note.active(1), last = note.last(i);
@@ -473,7 +468,7 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
                 for (int s = 0; s < C::kSubs; ++s) {
                     const int slot = (g * C::kSubs + s) % C::kKSlots;
-                    if (s > 0) wait_or_flag(&k_full[slot], ((g * C::kSubs + s) / C::kKSlots) & 1, &sh_dead);
+                    if (s > 0 && !warp_wait(&k_full[slot], ((g * C::kSubs + s) / C::kKSlots) & 1, &sh_dead)) return false;
                     tc::fence_after_sync();
                     const uint64_t k = k_desc + ((slot * C::kSlotBytes + from * 128) >> 4);
                     const uint64_t q = q0 + ((s * C::kCols * kTcRows * 128) >> 4);
@@ -492,6 +487,7 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                     }
                     __syncwarp();
                 }
+                return true;
             };
             // O of row tile i += P V over key tile g
             auto issue_o = [&](int i, int g, TileNote note) {
@@ -501,11 +497,11 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 o_phase ^= 1u << i;
                 const bool release = i == 1 || !note.active(1), first = note.first(i);
                 const int from = note.begin(i) * (kChunk / 16), to = note.end(i) * (kChunk / 16);
-                wait_or_flag(&p_ready[buf], phase, &sh_dead);
+                if (!warp_wait(&p_ready[buf], phase, &sh_dead)) return false;
 #pragma unroll
                 for (int s = 0; s < C::kSubs; ++s) {
                     const int slot = (g * C::kSubs + s) % C::kVSlots;
-                    wait_or_flag(&v_full[slot], ((g * C::kSubs + s) / C::kVSlots) & 1, &sh_dead);
+                    if (!warp_wait(&v_full[slot], ((g * C::kSubs + s) / C::kVSlots) & 1, &sh_dead)) return false;
                     tc::fence_after_sync();
                     const uint64_t v = v_desc + ((slot * C::kSlotBytes) >> 4);
                     const uint32_t pw = tmem + C::kS + buf * kTcKeys + s * C::kVKeys / 2, o = tmem + C::kO + i * D;
@@ -527,13 +523,14 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                     }
                     __syncwarp();
                 }
+                return true;
             };
             int base = 0;         // key tiles of the work before
             TileNote carried{0};  // of the work's first tile, when its S is already issued
             for (int ring = 0, round = 0;;) {
-                wait_or_flag(&work_full[ring], round & 1, &sh_dead);
+                if (!warp_wait(&work_full[ring], round & 1, &sh_dead)) goto leave;
                 const int n = works[ring].n;
-                if (!works[ring].valid || sh_dead) break;
+                if (!works[ring].valid) break;
                 const int next_ring = ring + 1 == kWorks ? 0 : ring + 1;
                 const int next_round = ring + 1 == kWorks ? round + 1 : round;
                 // Key tile by key tile, row tile 0 ahead of row tile 1 (the last of them that
@@ -547,27 +544,25 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll 1
                 for (int j = note.bits != 0 || n == 0 ? 0 : -1; j < n; ++j) {
                     auto look_ahead = [&] {
-                        if (j + 1 < n) {
-                            next = note_of(base + j + 1);
-                        } else if (C::kTiles == 2) {
-                            wait_or_flag(&work_full[next_ring], next_round & 1, &sh_dead);
-                            if (works[next_ring].valid && works[next_ring].n > 0 && !sh_dead)
-                                carried = note_of(base + n);
-                            next = carried;
-                        } else {
-                            next.bits = 0;
+                        if (j + 1 < n) return note_of(base + j + 1, next);
+                        if (C::kTiles == 2) {
+                            if (!warp_wait(&work_full[next_ring], next_round & 1, &sh_dead)) return false;
+                            if (works[next_ring].valid && works[next_ring].n > 0 && !note_of(base + n, carried))
+                                return false;
                         }
+                        next = carried;  // (one row tile: nothing)
+                        return true;
                     };
                     if constexpr (C::kTiles == 1) {
-                        look_ahead();
-                        if (next.active(0)) issue_s(0, base + j + 1, next);
-                        if (j >= 0) issue_o(0, base + j, note);
+                        if (!look_ahead()) goto leave;
+                        if (next.active(0) && !issue_s(0, base + j + 1, next)) goto leave;
+                        if (j >= 0 && !issue_o(0, base + j, note)) goto leave;
                     } else {
 #pragma unroll 1
                         for (int i = 0; i < 2; ++i) {
-                            if (note.active(i)) issue_o(i, base + j, note);
-                            if (i == 0) look_ahead();
-                            if (next.active(i)) issue_s(i, base + j + 1, next);
+                            if (note.active(i) && !issue_o(i, base + j, note)) goto leave;
+                            if (i == 0 && !look_ahead()) goto leave;
+                            if (next.active(i) && !issue_s(i, base + j + 1, next)) goto leave;
                         }
                     }
                     note = next;
@@ -587,9 +582,9 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
             if (leader) tma_prefetch_map(is_k ? &k_map : &v_map);
             int base = 0, slot = 0, slot_round = 0;
             for (int ring = 0, round = 0;;) {
-                wait_or_flag(&work_full[ring], round & 1, &sh_dead);
+                if (!warp_wait(&work_full[ring], round & 1, &sh_dead)) goto leave;
                 const Work w = works[ring];
-                if (!w.valid || sh_dead) break;
+                if (!w.valid) break;
                 const int n = w.n, p_first = w.p_first, p_last = w.p_last, kvh = w.kvh;
                 // Whether someone sees keys of lane i's part of key tile j; its page if so (the
                 // ids of pages before the window, which may be gone, are not read).
@@ -633,8 +628,9 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                     }
                     for (int s = 0; s < C::kSubs; ++s) {
                         uint64_t *full = is_k ? &k_full[slot] : &v_full[slot];
-                        if (slot_round > 0)
-                            wait_or_flag(is_k ? &k_empty[slot] : &v_empty[slot], (slot_round - 1) & 1, &sh_dead);
+                        if (slot_round > 0 &&
+                            !warp_wait(is_k ? &k_empty[slot] : &v_empty[slot], (slot_round - 1) & 1, &sh_dead))
+                            goto leave;
                         if (is_k) {
                             uint8_t *to = k_ring + slot * C::kSlotBytes;
                             if (leader)
@@ -697,9 +693,9 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         const float mult = positive ? p.scale_log2 : 1.0f;
         int base = 0, count = 0;  // key tiles of the work before, tiles of this row tile so far
         for (int ring = 0, round = 0;;) {
-            wait_or_flag(&work_full[ring], round & 1, &sh_dead);
+            if (!warp_wait(&work_full[ring], round & 1, &sh_dead)) goto leave;
             const Work &w = works[ring];
-            if (!w.valid || sh_dead) break;
+            if (!w.valid) break;
             const int head_tiles = w.head[i], begin_tile = w.begin[i], end_tile = w.end[i];
             const int n_sink = w.n_sink, main0 = w.main0;
             auto next_tile = [&](int j) { return j < head_tiles || j >= begin_tile ? j : begin_tile; };
@@ -713,7 +709,7 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 const int buf = C::kBufs == 2 ? count & 1 : i;
                 const uint32_t s_addr = tmem + lanes + C::kS + buf * kTcKeys;
                 const int key0 = (j < n_sink ? j : main0 + j - n_sink) * kTcKeys;
-                wait_or_flag(&s_full[buf], (C::kBufs == 2 ? count >> 1 : count) & 1, &sh_dead);
+                if (!warp_wait(&s_full[buf], (C::kBufs == 2 ? count >> 1 : count) & 1, &sh_dead)) goto leave;
                 tc::fence_after_sync();
                 // written before K was loaded, and K has been multiplied
                 const TileNote note{static_cast<volatile uint32_t *>(notes)[(base + j) % kNotes]};
@@ -728,13 +724,13 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                     // infinity, a NaN) cannot reach O through a weight of 0.
                     // (Two S buffers: once the O product before this tile's is complete, the
                     // ring slots of V are at most one phase from the one waited for.)
-                    if (C::kBufs == 2 && begun) wait_or_flag(&o_done[0], (count - 1) & 1, &sh_dead);
+                    if (C::kBufs == 2 && begun && !warp_wait(&o_done[0], (count - 1) & 1, &sh_dead)) goto leave;
                     const int key = key0 + row;
                     const bool dead = !((blocks >> (row >> 3)) & 1u) || key > all_last ||
                                       !(all_first - key < p.mask.window || key < p.mask.sinks);
                     for (int y = 0; y < C::kSubs; ++y) {
                         const int g = (base + j) * C::kSubs + y, slot = g % C::kVSlots;
-                        wait_or_flag(&v_full[slot], (g / C::kVSlots) & 1, &sh_dead);
+                        if (!warp_wait(&v_full[slot], (g / C::kVSlots) & 1, &sh_dead)) goto leave;
                         if (dead && (row >> C::kLog2VKeys) == y) {
                             const int r = row & (C::kVKeys - 1);
                             uint8_t *at = v_ring + slot * C::kSlotBytes + (r >> log2_bv) * (bv * D * 2) + (r & (bv - 1)) * 128;
@@ -746,18 +742,18 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                     fence_proxy_async_smem();
                 }
                 // The reference of the weights, from the tile's maximum; O is rescaled when it
-                // moves by more than the allowance.
+                // moves by more than the allowance. (False when a wait gave up.)
                 auto settle = [&](float mx) {
                     if (!begun) {
                         m = mx;
-                        return;
+                        return true;
                     }
                     const bool grow = (mx - m) * mult > kLazy;
                     if (__any_sync(FULL_MASK, grow)) {
                         // O is complete up to the tile before: S of this tile was issued after
                         // it (two S buffers: after the one before that)
                         if (C::kBufs == 2) {
-                            wait_or_flag(&o_done[0], (count - 1) & 1, &sh_dead);
+                            if (!warp_wait(&o_done[0], (count - 1) & 1, &sh_dead)) return false;
                             tc::fence_after_sync();
                         }
                         const float f = grow ? fast_exp2((m - mx) * mult) : 1.0f;
@@ -773,6 +769,7 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                             tc::tmem_st32(o_addr + c, o);
                         }
                     }
+                    return true;
                 };
                 float2 sum[4] = {};
                 // weights of 32 scores, and their place in P
@@ -807,7 +804,7 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                     tc::tmem_ld_wait();
 #pragma unroll
                     for (int c = 0; c < 4; ++c) top_of(s[c], top);
-                    settle(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+                    if (!settle(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])))) goto leave;
                     const float off = (m == -INFINITY ? 0.0f : m * mult) - kWeightBits;
                     const float2 mul2 = make_float2(mult, mult), sub2 = make_float2(-off, -off);
 #pragma unroll
@@ -844,7 +841,7 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                         chunk(c, s);
                         top_of(s, top);
                     }
-                    settle(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+                    if (!settle(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])))) goto leave;
                     const float off = (m == -INFINITY ? 0.0f : m * mult) - kWeightBits;
                     const float2 mul2 = make_float2(mult, mult), sub2 = make_float2(-off, -off);
 #pragma unroll 1
@@ -859,7 +856,7 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 tc::fence_before_sync();
                 __syncwarp();
                 // keeps this thread at most one phase behind o_done
-                if (C::kBufs == 2 && begun) wait_or_flag(&o_done[0], (count - 1) & 1, &sh_dead);
+                if (C::kBufs == 2 && begun && !warp_wait(&o_done[0], (count - 1) & 1, &sh_dead)) goto leave;
                 if (lane == 0) mbar_arrive(&p_ready[buf]);
                 begun = true;
                 ++count;
@@ -875,7 +872,7 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 for (int r = 0; r < 4; ++r) rows[r] = __shfl_sync(FULL_MASK, at, (lane & ~3) + r);
                 T *out = static_cast<T *>(p.out) + (lane & 3) * 8;
                 if (begun) {
-                    wait_or_flag(&o_done[i], (count - 1) & 1, &sh_dead);
+                    if (!warp_wait(&o_done[i], (count - 1) & 1, &sh_dead)) goto leave;
                     tc::fence_after_sync();
                 }
                 const float inv = 1.0f / l;
@@ -906,7 +903,7 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                     }
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        if (rows[r] >= 0 && !sh_dead)
+                        if (rows[r] >= 0)
                             *reinterpret_cast<uint4 *>(out + rows[r] * D + c) =
                                 make_uint4(pw[r][0], pw[r][1], pw[r][2], pw[r][3]);
                 }
@@ -921,6 +918,7 @@ attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
             }
         }
     }
+leave:
     __syncthreads();
     if (sh_dead) drain_in_flight();
     if (warp == C::kMma) {

@@ -179,6 +179,26 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
+// Bounded wait of a whole warp, in a CTA whose warps wait for one another. True when the phase
+// has completed; false when the wait gave up in some lane (which raises *watchdog) or was cut
+// short because another of the CTA's had (*dead): the whole warp then leaves its work. So a
+// warp only goes on with what has really arrived, and its lanes stay together whichever of
+// them gave up. (The votes cost the prompt attention 1 % at head_dim 128 and 3 % at 64.)
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *dead,
+                                          unsigned *watchdog) {
+    if (__all_sync(FULL_MASK, mbar_test(bar, parity))) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!__all_sync(FULL_MASK, mbar_try_wait(bar, parity))) {
+        const bool late = global_timer_ns() - t0 > WAIT_LIMIT_NS;
+        if (__any_sync(FULL_MASK, late || *dead)) {
+            if (late) atomicOr(watchdog, WD_STAGE_COPY);
+            *dead = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t ok;
