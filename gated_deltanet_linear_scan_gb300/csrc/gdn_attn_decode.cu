@@ -115,14 +115,9 @@ struct Geometry {
 
 // ------------------------------------------------------------------ waits
 
-// Bounded wait; once one gave up the CTA's later waits return at once and nothing of the
-// units concerned is written.
-__device__ __forceinline__ void wait_or_flag(uint64_t *bar, uint32_t parity, volatile int *dead) {
-    if (mbar_test(bar, parity) || *dead) return;
-    if (!mbar_wait(bar, parity)) {
-        *dead = 1;
-        atomicOr(&g_watchdog_attn_decode, WD_STAGE_COPY);
-    }
+// False when a wait gave up: the warp leaves, and nothing of the units concerned is written.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *dead) {
+    return gdn::warp_wait(bar, parity, dead, &g_watchdog_attn_decode);
 }
 
 // Counting the CTAs of a split unit that have stored their partial results. The word's upper
@@ -469,10 +464,10 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             int i = static_cast<int>(at - unit_begin);
             int page = page_at(i);
             // the segment, and q
-            if (seg >= 2) wait_or_flag(&q_empty[seg & 1], ((seg >> 1) - 1) & 1, &sh_dead);
+            if (seg >= 2 && !warp_wait(&q_empty[seg & 1], ((seg >> 1) - 1) & 1, &sh_dead)) goto leave;
             for (bool first = true; at < seg_end; ++at, ++i, first = false) {
                 const int next_page = at + 1 < seg_end ? page_at(i + 1) : -1;
-                if (st_round > 0) wait_or_flag(&empty[st], (st_round - 1) & 1, &sh_dead);
+                if (st_round > 0 && !warp_wait(&empty[st], (st_round - 1) & 1, &sh_dead)) goto leave;
                 const int key0 = walk.count ? walk.tile(i) * KT : 0;
                 const bool ok = p.cache.page_ok(page);
                 const unsigned have = __ballot_sync(FULL_MASK, ok);
@@ -532,13 +527,13 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                 walk = walk_tiles<KT>(p.mask, len - p.n_tokens, len - 1);
             }
         }
+    leave:
         if (*static_cast<volatile int *>(&sh_dead)) drain_in_flight();
         return;
     }
     if (G::kJoinWarp && warp == kWarps + 1) {
         // ---------------------------------------------------------- the joining warp
-        wait_or_flag(&early_ready, 0, &sh_dead);
-        if (*static_cast<volatile int *>(&sh_dead) || (early.flags & kWhole)) return;
+        if (!warp_wait(&early_ready, 0, &sh_dead) || (early.flags & kWhole)) return;
         int last = 0;
         if (lane == 0) {
             __threadfence();
@@ -575,16 +570,21 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     uint32_t phase = 0;
 
     bool more = true;  // tiles in this range
-    // A tile's first barrier also tells whether a wait gave up: then all warps leave together,
-    // before anything that was read of the stage is relied on.
-    auto gave_up = [&](int flags) {
-        if (chunk::named_barrier_or(1, kCompute, *static_cast<volatile int *>(&sh_dead) != 0)) return true;
+    bool gave_up = false;
+    // A tile's first barrier also tells whether some warp's wait for it gave up: then all
+    // computing warps leave together.
+    auto left_alone = [&](int flags) {
+        if (chunk::named_barrier_or(1, kCompute, false)) return true;
         if ((flags & kFirst) && tid == 0 && !(sg.flags & kWhole))
             word_seen = *reinterpret_cast<volatile unsigned long long *>(p.counters + sg.c0);
         return false;
     };
     for (int it = 0; more; ++it) {
-        wait_or_flag(&full[s], phase, &sh_dead);
+        if (!warp_wait(&full[s], phase, &sh_dead)) {
+            chunk::named_barrier_or(1, kCompute, true);
+            gave_up = true;
+            break;
+        }
         const int2 stage = stages[s];
         const int key0 = stage.x, flags = stage.y;
         const unsigned blocks = static_cast<unsigned>(stage.y) >> 8;
@@ -708,7 +708,10 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                 red[warp][r0] = t0;
                 red[warp][r0 + 8] = t1;
             }
-            if (gave_up(flags)) break;
+            if (left_alone(flags)) {
+                gave_up = true;
+                break;
+            }
             const float old0 = m0, old1 = m1;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
@@ -837,7 +840,10 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                         if ((r & 3) == quarter) sp[(i0 + 8 * h) * RT + r] = acc[h][r] * p.scale_log2;
                     }
             }
-            if (gave_up(flags)) break;
+            if (left_alone(flags)) {
+                gave_up = true;
+                break;
+            }
             {
                 const int r = tid / LPR, part = tid % LPR;
                 float x[KT / LPR];
@@ -953,9 +959,8 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                     const int col = (warp * NT + j) * 8 + 2 * (lane & 3);
                     const float x = o16[j][2 * half], y = o16[j][2 * half + 1];
                     if (whole) {
-                        if (!sh_dead)
-                            *reinterpret_cast<uint32_t *>(out + row * D + col) =
-                                Elem<T>::pack(finish(x, l, inv), finish(y, l, inv));
+                        *reinterpret_cast<uint32_t *>(out + row * D + col) =
+                            Elem<T>::pack(finish(x, l, inv), finish(y, l, inv));
                     } else {
                         __stcg(reinterpret_cast<float2 *>(record + r * D + col), make_float2(x, y));
                     }
@@ -970,10 +975,9 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                     if (row < 0) continue;
                     if (whole) {
                         const float l = row_l[r], inv = 1.0f / l;
-                        if (!sh_dead)
-                            *reinterpret_cast<float4 *>(out + row * D + col) =
-                                make_float4(finish(o32[r][0], l, inv), finish(o32[r][1], l, inv),
-                                            finish(o32[r][2], l, inv), finish(o32[r][3], l, inv));
+                        *reinterpret_cast<float4 *>(out + row * D + col) =
+                            make_float4(finish(o32[r][0], l, inv), finish(o32[r][1], l, inv),
+                                        finish(o32[r][2], l, inv), finish(o32[r][3], l, inv));
                     } else {
                         __stcg(reinterpret_cast<float4 *>(record + r * D + col),
                                make_float4(o32[r][0], o32[r][1], o32[r][2], o32[r][3]));
@@ -984,8 +988,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         if (whole) continue;
         if (tid < kRows) {
             __stcg(record + kRows * D + tid, row_m[tid]);
-            // a length below zero marks a result that a wait gave up on
-            __stcg(record + kRows * D + kRows + tid, sh_dead ? -1.0f : row_l[tid]);
+            __stcg(record + kRows * D + kRows + tid, row_l[tid]);
         }
         // A range has at most two split units, its first and its last. The first one's arrival
         // (a fence takes thousands of cycles while copies are under way) and join are left to
@@ -1013,6 +1016,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         __syncwarp();
         if (lane == 0) mbar_arrive(&early_ready);
     }
+    if (gave_up) drain_in_flight();  // (the loading warp may have left before)
 }
 
 // ------------------------------------------------------------------ host side

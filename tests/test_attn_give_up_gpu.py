@@ -13,6 +13,7 @@ import numpy as np
 import pytest
 
 from tests.attn_cases import Cache, attention, bound
+from tests.test_attn_decode_gpu import run as decode
 from tests.test_attn_prefill_gpu import run as prefill
 
 torch = pytest.importorskip("torch")
@@ -54,6 +55,11 @@ def build(name, where):
 @pytest.fixture(scope="module")
 def prompt_lib(tmp_path_factory):
     return build("give_up_prompt", tmp_path_factory.mktemp("prompt"))
+
+
+@pytest.fixture(scope="module")
+def decode_lib(tmp_path_factory):
+    return build("give_up_decode", tmp_path_factory.mktemp("decode"))
 
 
 class Wanted:
@@ -105,4 +111,41 @@ def test_prompt(cuda_lib, prompt_lib, monkeypatch, d, dtype):
     assert call.ended()[0] is False
     monkeypatch.undo()
     assert wanted.untouched(prefill(cuda_lib, c, q, counts, 10)) == 0
+    cuda_lib.gdn_device_error()
+
+
+DECODE = ["gdn_attn_decode", "gdn_attn_decode_workspace_size"]
+
+
+# warps of a CTA: four that compute, the loading warp, the joining one (fp32 with heads of 64 and
+# few rows has none)
+@pytest.mark.parametrize("d,dtype,warps", [(64, "float32", 5), (128, "float16", 6), (64, "bfloat16", 6),
+                                           (256, "bfloat16", 6), (128, "float32", 6)])
+def test_decode(cuda_lib, decode_lib, monkeypatch, d, dtype, warps):
+    """Units that are whole, split in two and split over many CTAs."""
+    rng = np.random.default_rng(d)
+    lens = [70000] + [int(x) for x in rng.integers(1, 1500, 600)] + [20000]
+    n, scale = len(lens), d ** -0.5
+    c = Cache(torch, rng, lens, 1, d, 64, dtype)
+    q = c.queries(rng, [1] * n, 2)
+    wanted = Wanted(c, q, [1] * n, scale, False)
+    call = Copy(cuda_lib, decode_lib, monkeypatch, DECODE)
+    for cta in (1, 20, 140):
+        for warp in range(warps):
+            for nth in (0, 1, 4, 11):
+                for lanes in (0xFFFFFFFF, 1 << (5 + 3 * nth) % 32):
+                    call.arm(cta, warp, nth, lanes)
+                    out = decode(cuda_lib, c, q, 1, 2)
+                    flag, waits = call.ended()
+                    assert flag == (waits > nth) and (flag or nth > 0)
+                    left = wanted.untouched(out)
+                    assert flag or left == 0
+                    # (what the joining warp waits for, and a loading warp at its last tile, may
+                    # come too late to matter)
+                    assert left > 0 or nth > 0 or warp >= 4
+    call.arm(-1, 0, 0, 0)
+    assert wanted.untouched(decode(cuda_lib, c, q, 1, 2)) == 0
+    assert call.ended()[0] is False
+    monkeypatch.undo()
+    assert wanted.untouched(decode(cuda_lib, c, q, 1, 2)) == 0
     cuda_lib.gdn_device_error()
