@@ -122,29 +122,22 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 
 // Counting the CTAs of a split unit that have stored their partial results. The word's upper
 // 48 bits say whose count it is: this call's nonce, or anything else, which counts as 0 (so the
-// workspace needs no initialisation). The CTA that completes the count clears the word; a
-// captured call keeps its nonce over its replays, each of which leaves the words cleared.
-// Ahead of the arrival a word seen untagged is tagged, so that an arrival is one addition.
+// workspace needs no initialisation). Every CTA tags a word that it sees untagged, then arrives
+// with one addition. The CTA that completes the count clears the word. A captured call keeps its
+// nonce over its replays; each leaves the words cleared, as a CTA that gave up a wait arrives at
+// the units it has not finished all the same, with a partial result marked as none.
 __device__ __forceinline__ bool tagged(unsigned long long word, unsigned long long nonce) {
     return (word >> 16) == nonce;
 }
 
-__device__ __forceinline__ bool last_arrival(unsigned long long *word, unsigned long long nonce,
-                                             int n) {
-    unsigned long long seen = atomicAdd(word, 1ull);
-    if (!tagged(seen, nonce)) {  // the addition went to an untagged word: count again
-        seen = *reinterpret_cast<volatile unsigned long long *>(word);
-        for (;;) {
-            const unsigned long long next = tagged(seen, nonce) ? seen + 1 : (nonce << 16) | 1ull;
-            const unsigned long long was = atomicCAS(word, seen, next);
-            if (was == seen) {
-                seen = next - 1;
-                break;
-            }
-            seen = was;
-        }
-    }
-    if (static_cast<int>(seen & 0xFFFFu) + 1 != n) return false;
+// `seen`: what the word held. (When it no longer does, another CTA has tagged it.)
+__device__ __forceinline__ void tag(unsigned long long *word, unsigned long long seen,
+                                    unsigned long long nonce) {
+    if (!tagged(seen, nonce)) atomicCAS(word, seen, nonce << 16);
+}
+
+__device__ __forceinline__ bool last_arrival(unsigned long long *word, int n) {
+    if (static_cast<int>(atomicAdd(word, 1ull) & 0xFFFFu) + 1 != n) return false;
     atomicExch(word, 0ull);
     return true;
 }
@@ -533,11 +526,15 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     }
     if (G::kJoinWarp && warp == kWarps + 1) {
         // ---------------------------------------------------------- the joining warp
-        if (!warp_wait(&early_ready, 0, &sh_dead) || (early.flags & kWhole)) return;
+        // The computing warps come to this barrier whether a wait of theirs gave up or not, which
+        // takes them a bounded wait or two; what they handed over before has to be counted.
+        bool ready = warp_wait(&early_ready, 0, &sh_dead);
+        for (int i = 0; i < 2 && !ready; ++i) ready = __all_sync(FULL_MASK, mbar_wait(&early_ready, 0));
+        if (!ready || (early.flags & kWhole)) return;
         int last = 0;
         if (lane == 0) {
             __threadfence();
-            last = last_arrival(p.counters + early.c0, p.nonce, early.c1 - early.c0 + 1);
+            last = last_arrival(p.counters + early.c0, early.c1 - early.c0 + 1);
             __threadfence();
         }
         if (__shfl_sync(FULL_MASK, last, 0))
@@ -566,6 +563,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     int pos0 = 0, pos1 = 0;
     unsigned long long word_seen = 0;
     bool had_early = false;
+    int handed = 0;  // split units this CTA has stored its part of
     int seg = 0, s = 0;
     uint32_t phase = 0;
 
@@ -901,8 +899,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[s]);
-        if ((flags & kFirst) && tid == 0 && !(sg.flags & kWhole) && !tagged(word_seen, p.nonce))
-            atomicCAS(p.counters + sg.c0, word_seen, p.nonce << 16);
+        if ((flags & kFirst) && tid == 0 && !(sg.flags & kWhole)) tag(p.counters + sg.c0, word_seen, p.nonce);
         if (++s == G::kStages) {
             s = 0;
             phase ^= 1;
@@ -986,6 +983,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             }
         }
         if (whole) continue;
+        ++handed;
         if (tid < kRows) {
             __stcg(record + kRows * D + tid, row_m[tid]);
             __stcg(record + kRows * D + kRows + tid, row_l[tid]);
@@ -1003,7 +1001,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         named_barrier_sync(2, kCompute);
         if (tid == 0) {
             __threadfence();
-            sh_join = last_arrival(p.counters + sg.c0, p.nonce, sg.c1 - sg.c0 + 1);
+            sh_join = last_arrival(p.counters + sg.c0, sg.c1 - sg.c0 + 1);
             __threadfence();
         }
         named_barrier_sync(1, kCompute);
@@ -1016,7 +1014,41 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         __syncwarp();
         if (lane == 0) mbar_arrive(&early_ready);
     }
-    if (gave_up) drain_in_flight();  // (the loading warp may have left before)
+    if (!gave_up) return;
+    if (tid == 0) {
+        // The units shared with other CTAs -- the range's first and last at most -- that this one
+        // has not stored its part of: their partial results are marked as none (a length below
+        // zero), so that nobody writes these units' rows, and counted.
+        int n = sh_seq, slot, len;
+        unsigned seq_begin = sh_seq_begin, unit_begin, unit_end;
+        auto find_unit = [&](unsigned place) {  // that holds this place, of this sequence or a later one
+            unsigned each_unit = tiles_of(n, slot, len);
+            while (each_unit == 0 || place - seq_begin >= (each_unit + kTurn) * units) {
+                if (each_unit != 0) seq_begin += (each_unit + kTurn) * units;
+                if (n + 1 == p.n_seqs) break;  // not reached: the range ends before the sequences do
+                each_unit = tiles_of(++n, slot, len);
+            }
+            unit_begin = seq_begin + (place - seq_begin) / (each_unit + kTurn) * (each_unit + kTurn) + kTurn;
+            unit_end = unit_begin + each_unit;
+        };
+        auto count_as_none = [&] {
+            const int c0 = owner(unit_begin), c1 = owner(unit_end - 1);
+            float *record = p.partials + static_cast<size_t>(2 * blockIdx.x + (unit_begin >= begin ? 1 : 0)) * kRecord;
+            for (int r = 0; r < kRows; ++r) __stcg(record + kRows * D + kRows + r, -1.0f);
+            unsigned long long *word = p.counters + c0;
+            tag(word, *reinterpret_cast<volatile unsigned long long *>(word), p.nonce);
+            __threadfence();
+            last_arrival(word, c1 - c0 + 1);
+        };
+        find_unit(begin);
+        const unsigned first = unit_begin;
+        const bool first_split = unit_begin < begin || unit_end > end;
+        if (first_split && handed == 0) count_as_none();
+        find_unit(end - 1);
+        if (unit_begin != first && unit_begin < end && unit_end > end && handed <= (first_split ? 1 : 0))
+            count_as_none();
+    }
+    drain_in_flight();  // (the loading warp may have left before)
 }
 
 // ------------------------------------------------------------------ host side

@@ -149,3 +149,47 @@ def test_decode(cuda_lib, decode_lib, monkeypatch, d, dtype, warps):
     monkeypatch.undo()
     assert wanted.untouched(decode(cuda_lib, c, q, 1, 2)) == 0
     cuda_lib.gdn_device_error()
+
+
+@pytest.mark.parametrize("d,dtype,warps", [(64, "float32", 5), (128, "bfloat16", 6), (256, "float16", 6)])
+@pytest.mark.parametrize("lens", [[150000], [70000, 900, 20000, 31000]])
+def test_replays_after_a_give_up(cuda_lib, decode_lib, monkeypatch, d, dtype, warps, lens):
+    """A captured decode call, replayed with and without a wait that gives up: every replay leaves
+    the workspace's counts (its first words, one per CTA) cleared, a replay in which a wait gave
+    up writes no wrong row, and the next one gives the bits of an undisturbed call."""
+    rng = np.random.default_rng([d, len(lens)])
+    n, scale, ctas = len(lens), d ** -0.5, 3 * 152
+    c = Cache(torch, rng, lens, 1, d, 64, dtype)
+    q = c.queries(rng, [1] * n, 2)
+    wanted = Wanted(c, q, [1] * n, scale, False)
+    clean = decode(cuda_lib, c, q, 1, 2)
+    assert wanted.untouched(clean) == 0
+    call = Copy(cuda_lib, decode_lib, monkeypatch, DECODE)
+    call.arm(-1, 0, 0, 0)
+    qd, out = c.dev(q), torch.empty_like(clean)
+    ws = torch.zeros(cuda_lib.gdn_attn_decode_workspace_size(n, 1, 2, 1, d), dtype=torch.uint8, device="cuda")
+    run = lambda: cuda_lib.gdn_attn_decode(  # noqa: E731
+        qd, c.k_pages, c.v_pages, c.d_table, c.d_lens, out, n, 1, 2, 1, d, 64, c.n_pages, c.max_pages,
+        0, 0, scale, ws, slots=c.d_slots, pool=c.pool)
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for cta in (0, 1, 77, 151):
+        for warp in range(warps):
+            for nth in (0, 2, 5):
+                call.arm(cta, warp, nth, 0xFFFFFFFF if nth else 1 << (3 * warp + 1))
+                out.fill_(float("nan"))
+                graph.replay()
+                flag, waits = call.ended()
+                assert flag == (waits > nth)
+                left = wanted.untouched(out)
+                assert flag or left == 0
+                where = f"after CTA {cta}, warp {warp}, wait {nth}"
+                assert not ws[:8 * ctas].any(), f"counts left {where}"
+                call.arm(-1, 0, 0, 0)
+                out.fill_(float("nan"))
+                graph.replay()
+                assert call.ended()[0] is False
+                assert torch.equal(out, clean), f"other bits {where}"
+                assert not ws[:8 * ctas].any()
