@@ -37,7 +37,7 @@ __all__ = [
     "gdn_kv_append", "gdn_attn_decode_workspace_size", "gdn_attn_decode",
     "gdn_attn_prefill_workspace_size", "gdn_attn_prefill", "gdn_pages_workspace_size",
     "gdn_pages_copy", "gdn_pages_reserve", "gdn_pages_fork", "gdn_pages_truncate",
-    "gdn_pages_compact",
+    "gdn_pages_compact", "gdn_selftest_attn_wait",
 ]
 
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_NULL", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_UNSUPPORTED",
@@ -116,6 +116,7 @@ _SIGS = {
     "gdn_attn_prefill_workspace_size": ([_I] * 5, ctypes.c_size_t),
     "gdn_attn_prefill": ([_P] * 7 + [_I] * 11 + [_F, _I, _I, _P, _I, _P, _P, ctypes.c_size_t, _P],
                          _I),
+    "gdn_selftest_attn_wait": ([ctypes.c_uint, ctypes.c_uint, _P, _P], _I),
     "gdn_pages_workspace_size": ([_I, _I], ctypes.c_size_t),
     "gdn_pages_copy": ([_P] * 3 + [_I] * 3 + [ctypes.c_size_t, _P, _P], _I),
     "gdn_pages_reserve": ([_P] * 5 + [_I] * 4 + [ctypes.c_size_t, _I, _P, _I, _P, _P,
@@ -765,6 +766,13 @@ def gdn_attn_prefill(q, k_pages, v_pages, page_table, kv_lens, out, cu_seqlens, 
         _dtype(k_pages, "k_pages"), _slots(slots), pool, _errc(err_count),
         None if workspace is None else _ws_ptr(workspace),
         0 if workspace is None else _ws_bytes(workspace), _stream(stream)))
+
+
+def gdn_selftest_attn_wait(arm_mask, limit_us, out, stream=None):
+    """gdn_selftest_bounded_wait for the attention calls: bit 0 of arm_mask and out[0] are the
+    decode attention's, bit 1 and out[1] the prompt attention's."""
+    _check("gdn_selftest_attn_wait", library().gdn_selftest_attn_wait(
+        int(arm_mask), int(limit_us), _ptr(out, "out"), _stream(stream)))
 
 
 def gdn_pages_workspace_size(n_seqs, n_pages):

@@ -1124,6 +1124,16 @@ gdn_status launch_dim(int d, const CUtensorMap &q, const CUtensorMap &k, const C
 
 }  // namespace
 
+// The bounded-wait self-test on this unit's watchdog flag (gdn_selftest_attn_wait).
+__global__ void wait_probe_kernel_attn_decode(int arm, unsigned long long limit_ns, float *out) {
+    bounded_wait_probe(arm != 0, limit_ns, &g_watchdog_attn_decode, WD_STAGE_COPY, out);
+}
+
+gdn_status launch_wait_probe_attn_decode(bool arm, uint64_t limit_ns, float *out, cudaStream_t s) {
+    wait_probe_kernel_attn_decode<<<1, 1, 0, s>>>(arm ? 1 : 0, limit_ns, out);
+    return launch_status();
+}
+
 unsigned read_and_clear_watchdog_attn_decode(cudaStream_t s) {
     unsigned flags = 0;
     const unsigned zero = 0;

@@ -971,6 +971,16 @@ gdn_status launch_attn_prefill_tc(const PrefillParams &p, int dtype, int head_di
                             : launch_dim<__nv_bfloat16>(head_dim, p, dtype, s);
 }
 
+// The bounded-wait self-test on this unit's watchdog flag (gdn_selftest_attn_wait).
+__global__ void wait_probe_kernel_attn_prefill(int arm, unsigned long long limit_ns, float *out) {
+    bounded_wait_probe(arm != 0, limit_ns, &g_watchdog_attn_prefill, WD_STAGE_COPY, out);
+}
+
+gdn_status launch_wait_probe_attn_prefill(bool arm, uint64_t limit_ns, float *out, cudaStream_t s) {
+    wait_probe_kernel_attn_prefill<<<1, 1, 0, s>>>(arm ? 1 : 0, limit_ns, out);
+    return launch_status();
+}
+
 unsigned read_and_clear_watchdog_attn_prefill(cudaStream_t s) {
     unsigned flags = 0;
     const unsigned zero = 0;

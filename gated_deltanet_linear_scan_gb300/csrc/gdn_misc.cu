@@ -420,6 +420,16 @@ gdn_status gdn_selftest_bounded_wait(unsigned arm_mask, unsigned limit_us, float
     return launch_wait_probe_chunked_ws(arm_mask & 8u, ns, out + 3, s);
 }
 
+gdn_status gdn_selftest_attn_wait(unsigned arm_mask, unsigned limit_us, float *out,
+                                  gdn_stream_t stream) {
+    if (!out) return GDN_ERR_NULL;
+    if (arm_mask > 3u || limit_us < 1 || limit_us > 2000000u) return GDN_ERR_SHAPE;
+    const cudaStream_t s = as_cuda(stream);
+    const uint64_t ns = 1000ull * limit_us;
+    GDN_TRY(launch_wait_probe_attn_decode(arm_mask & 1u, ns, out + 0, s));
+    return launch_wait_probe_attn_prefill(arm_mask & 2u, ns, out + 1, s);
+}
+
 gdn_status gdn_decay_gate(const float *alpha, const float *dt, const float *a, float *g,
                           int n_heads, int rows, gdn_stream_t stream) {
     if (!alpha || !dt || !a || !g) return GDN_ERR_NULL;

@@ -18,6 +18,10 @@ namespace gdn {
 unsigned read_and_clear_watchdog_attn_decode(cudaStream_t s);
 unsigned read_and_clear_watchdog_attn_prefill(cudaStream_t s);
 
+// Bounded-wait self-test kernels on these flags.
+gdn_status launch_wait_probe_attn_decode(bool arm, uint64_t limit_ns, float *out, cudaStream_t s);
+gdn_status launch_wait_probe_attn_prefill(bool arm, uint64_t limit_ns, float *out, cudaStream_t s);
+
 inline bool supported_dtype(int dtype) {
     return dtype == GDN_F32 || dtype == GDN_F16 || dtype == GDN_BF16;
 }

@@ -668,6 +668,12 @@ gdn_status gdn_attn_prefill(const void *q, const void *k_pages, const void *v_pa
                             int32_t *err_count, void *workspace, size_t workspace_bytes,
                             gdn_stream_t stream);
 
+/* gdn_selftest_bounded_wait for the two watchdog flags of these calls: probe 0 on the decode
+ * attention's, probe 1 on the prompt attention's.
+ * out: device float[2]; arm_mask in [0, 3]; limit_us in [1, 2000000]. */
+gdn_status gdn_selftest_attn_wait(unsigned arm_mask, unsigned limit_us, float *out,
+                                  gdn_stream_t stream);
+
 /* Bookkeeping of the pages. page_refs int32 [n_pages] counts the table entries that hold
  * a page (0: free); entries of a slot's row past its length are -1. `pages` is every
  * layer's data in planes: [n_planes][n_pages][page_bytes], e.g. n_planes = 2 * layers with
