@@ -210,7 +210,9 @@ def _ptr(t, name, dtype=None, optional=False):
 
 
 def _dtype(t, name):
-    """The gdn_dtype code of a tensor's type."""
+    """A tensor's type, and its gdn_dtype code."""
+    if t is None:
+        raise ValueError(f"{name} is required")
     dtype = getattr(t, "dtype", None)
     if not _DTYPES:
         torch = _torch()
@@ -218,7 +220,7 @@ def _dtype(t, name):
     code = _DTYPES.get(dtype)
     if code is None:
         raise TypeError(f"{name} must be a float32, float16 or bfloat16 tensor")
-    return code
+    return dtype, code
 
 
 def _rows(t, name, dtype, heads, head_dim):
@@ -234,6 +236,8 @@ def _rows(t, name, dtype, heads, head_dim):
                     return t.data_ptr(), row if t.shape[0] > 1 else max(row, heads * head_dim)
     except AttributeError:
         pass
+    if t is None:
+        raise ValueError(f"{name} is required")
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
@@ -714,15 +718,16 @@ def gdn_kv_append(k, v, k_pages, v_pages, page_table, kv_lens, cu_seqlens, n_seq
     """Write new tokens' keys and values into the pages (cu_seqlens None: the same number of
     rows for every sequence). k and v may be slices of wider rows."""
     pool = _pool(pool, n_seqs, slots)
+    dt, code = _dtype(k_pages, "k_pages")
     i32 = _torch().int32
-    kp, k_stride = _rows(k, "k", k_pages.dtype, n_kv_heads, head_dim)
-    vp, v_stride = _rows(v, "v", k_pages.dtype, n_kv_heads, head_dim)
+    kp, k_stride = _rows(k, "k", dt, n_kv_heads, head_dim)
+    vp, v_stride = _rows(v, "v", dt, n_kv_heads, head_dim)
     _check("gdn_kv_append", library().gdn_kv_append(
-        kp, vp, _ptr(k_pages, "k_pages", k_pages.dtype), _ptr(v_pages, "v_pages", k_pages.dtype),
+        kp, vp, _ptr(k_pages, "k_pages", dt), _ptr(v_pages, "v_pages", dt),
         _ptr(page_table, "page_table", i32), _ptr(kv_lens, "kv_lens", i32),
         _ptr(cu_seqlens, "cu_seqlens", i32, optional=True), n_seqs, total_tokens, n_kv_heads,
-        head_dim, page_size, n_pages, max_pages, k_stride, v_stride, _dtype(k_pages, "k_pages"),
-        _slots(slots), pool, _errc(err_count), _stream(stream)))
+        head_dim, page_size, n_pages, max_pages, k_stride, v_stride, code, _slots(slots), pool,
+        _errc(err_count), _stream(stream)))
 
 
 def gdn_attn_decode_workspace_size(n_seqs, n_tokens, n_q_heads, n_kv_heads, head_dim):
@@ -735,14 +740,15 @@ def gdn_attn_decode(q, k_pages, v_pages, page_table, kv_lens, out, n_seqs, n_tok
                     workspace, slots=None, pool=None, err_count=None, stream=None):
     """Attention of each sequence's last n_tokens tokens over its paged cache."""
     pool = _pool(pool, n_seqs, slots)
-    i32, dt = _torch().int32, k_pages.dtype
+    dt, code = _dtype(k_pages, "k_pages")
+    i32 = _torch().int32
     qp, q_stride = _rows(q, "q", dt, n_q_heads, head_dim)
     _check("gdn_attn_decode", library().gdn_attn_decode(
         qp, _ptr(k_pages, "k_pages", dt), _ptr(v_pages, "v_pages", dt),
         _ptr(page_table, "page_table", i32), _ptr(kv_lens, "kv_lens", i32), _ptr(out, "out", dt),
         n_seqs, n_tokens, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages, window,
-        n_sinks, scale, q_stride, _dtype(k_pages, "k_pages"), _slots(slots), pool,
-        _errc(err_count), _ws_ptr(workspace), _ws_bytes(workspace), _stream(stream)))
+        n_sinks, scale, q_stride, code, _slots(slots), pool, _errc(err_count), _ws_ptr(workspace),
+        _ws_bytes(workspace), _stream(stream)))
 
 
 def gdn_attn_prefill_workspace_size(n_seqs, total_tokens, n_q_heads, n_kv_heads, head_dim):
@@ -756,14 +762,15 @@ def gdn_attn_prefill(q, k_pages, v_pages, page_table, kv_lens, out, cu_seqlens, 
                      pool=None, err_count=None, stream=None):
     """Attention of a ragged batch of prompts (or chunks of prompts) over the paged cache."""
     pool = _pool(pool, n_seqs, slots)
-    i32, dt = _torch().int32, k_pages.dtype
+    dt, code = _dtype(k_pages, "k_pages")
+    i32 = _torch().int32
     qp, q_stride = _rows(q, "q", dt, n_q_heads, head_dim)
     _check("gdn_attn_prefill", library().gdn_attn_prefill(
         qp, _ptr(k_pages, "k_pages", dt), _ptr(v_pages, "v_pages", dt),
         _ptr(page_table, "page_table", i32), _ptr(kv_lens, "kv_lens", i32), _ptr(out, "out", dt),
         _ptr(cu_seqlens, "cu_seqlens", i32), n_seqs, total_tokens, max_tokens, n_q_heads,
         n_kv_heads, head_dim, page_size, n_pages, max_pages, window, n_sinks, scale, q_stride,
-        _dtype(k_pages, "k_pages"), _slots(slots), pool, _errc(err_count),
+        code, _slots(slots), pool, _errc(err_count),
         None if workspace is None else _ws_ptr(workspace),
         0 if workspace is None else _ws_bytes(workspace), _stream(stream)))
 
@@ -781,7 +788,7 @@ def gdn_pages_workspace_size(n_seqs, n_pages):
 
 def _page_data(pages):
     """The pages of every plane, of any type."""
-    return _ptr(pages, "pages", pages.dtype)
+    return _ptr(pages, "pages", getattr(pages, "dtype", None))
 
 
 def gdn_pages_copy(pages, src, dst, n_copies, n_planes, n_pages, page_bytes, err_count=None,
