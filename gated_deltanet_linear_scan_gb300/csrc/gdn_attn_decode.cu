@@ -1135,13 +1135,7 @@ gdn_status launch_wait_probe_attn_decode(bool arm, uint64_t limit_ns, float *out
 }
 
 unsigned read_and_clear_watchdog_attn_decode(cudaStream_t s) {
-    unsigned flags = 0;
-    const unsigned zero = 0;
-    cudaMemcpyFromSymbolAsync(&flags, g_watchdog_attn_decode, sizeof(flags), 0,
-                              cudaMemcpyDeviceToHost, s);
-    cudaMemcpyToSymbolAsync(g_watchdog_attn_decode, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
-    cudaStreamSynchronize(s);
-    return flags;
+    return read_and_clear_flag(g_watchdog_attn_decode, s);
 }
 
 }  // namespace gdn

@@ -982,13 +982,7 @@ gdn_status launch_wait_probe_attn_prefill(bool arm, uint64_t limit_ns, float *ou
 }
 
 unsigned read_and_clear_watchdog_attn_prefill(cudaStream_t s) {
-    unsigned flags = 0;
-    const unsigned zero = 0;
-    cudaMemcpyFromSymbolAsync(&flags, g_watchdog_attn_prefill, sizeof(flags), 0,
-                              cudaMemcpyDeviceToHost, s);
-    cudaMemcpyToSymbolAsync(g_watchdog_attn_prefill, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
-    cudaStreamSynchronize(s);
-    return flags;
+    return read_and_clear_flag(g_watchdog_attn_prefill, s);
 }
 
 }  // namespace gdn

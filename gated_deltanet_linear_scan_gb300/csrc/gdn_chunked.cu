@@ -572,12 +572,7 @@ gdn_status launch_wait_probe_chunked(bool arm, uint64_t limit_ns, float *out, cu
 }
 
 unsigned read_and_clear_watchdog_chunked(cudaStream_t s) {
-    unsigned flags = 0;
-    const unsigned zero = 0;
-    cudaMemcpyFromSymbolAsync(&flags, g_watchdog_chunked, sizeof(flags), 0, cudaMemcpyDeviceToHost, s);
-    cudaMemcpyToSymbolAsync(g_watchdog_chunked, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
-    cudaStreamSynchronize(s);
-    return flags;
+    return read_and_clear_flag(g_watchdog_chunked, s);
 }
 
 }  // namespace gdn

@@ -829,13 +829,7 @@ gdn_status launch_wait_probe_chunked_ws(bool arm, uint64_t limit_ns, float *out,
 }
 
 unsigned read_and_clear_watchdog_chunked_ws(cudaStream_t s) {
-    unsigned flags = 0;
-    const unsigned zero = 0;
-    cudaMemcpyFromSymbolAsync(&flags, g_watchdog_chunked_ws, sizeof(flags), 0,
-                              cudaMemcpyDeviceToHost, s);
-    cudaMemcpyToSymbolAsync(g_watchdog_chunked_ws, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
-    cudaStreamSynchronize(s);
-    return flags;
+    return read_and_clear_flag(g_watchdog_chunked_ws, s);
 }
 
 size_t ragged_chunked_ws_size(int n_seqs, long long total, int n_v_heads) {

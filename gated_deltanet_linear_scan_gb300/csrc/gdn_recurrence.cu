@@ -433,12 +433,7 @@ gdn_status launch_wait_probe_recurrence(bool arm, uint64_t limit_ns, float *out,
 }
 
 unsigned read_and_clear_watchdog_recurrence(cudaStream_t s) {
-    unsigned flags = 0;
-    const unsigned zero = 0;
-    cudaMemcpyFromSymbolAsync(&flags, g_watchdog, sizeof(flags), 0, cudaMemcpyDeviceToHost, s);
-    cudaMemcpyToSymbolAsync(g_watchdog, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
-    cudaStreamSynchronize(s);
-    return flags;
+    return read_and_clear_flag(g_watchdog, s);
 }
 
 namespace {
