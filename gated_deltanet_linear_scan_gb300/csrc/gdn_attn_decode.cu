@@ -13,9 +13,9 @@
 // the lengths: a ragged batch, one long sequence and many short ones all keep every SM equally
 // busy, with no host knowledge of the lengths. (By tiles alone, the CTAs that got the short
 // sequences were last: windowed fp32 pool 56 us, 48 with the turn weighed as one tile, 50 as two;
-// 200 bf16 sequences of 16..2000 keys 149, 122, 129.) A unit that crosses a range boundary leaves partial results (m, l, o) in the
-// workspace; the CTA that arrives last on it joins them in CTA order, so the bits do not
-// depend on timing.
+// 200 bf16 sequences of 16..2000 keys 149, 122, 129.) A unit that crosses a range boundary leaves
+// partial results (m, l, o) in the workspace; the CTA that arrives last on it joins them in CTA
+// order, so the bits do not depend on timing.
 //
 // Inside a CTA one warp walks the range and issues the TMA loads of the tiles' pages (and of
 // q at a unit's first tile) into a ring of stages; four warps compute. Each of the four
@@ -24,12 +24,15 @@
 // running maximum is shared and O needs no join across warps.
 //
 // Measured (calls replayed back to back; the share is of the visible keys' and values' bytes
-// at the copy rate): 64 sequences of 64..8192 bf16 keys, 16 key heads of 128: 172 us, 0.95.
-// Four of 60 to 131 thousand f16 keys, 2 key heads of 256: 99 us, 0.87. 64 sequences with 4
-// draft tokens each, 4 key heads of 128: 60 us, 0.77. Units of a few tiles are bound by the
-// chain of steps of a tile and by the turn from unit to unit: a pool of 256 sequences with
-// windows of 1024 fp32 keys, 4 key heads of 64: 48 us, 0.68. One sequence of 1000 keys is
-// launch, one tile's chain and the join: 10 us.
+// at the copy rate): 64 sequences of 64..8192 bf16 keys, 16 key heads of 128: 168-172 us, 0.95
+// to 0.97. Four of 60 to 131 thousand f16 keys, 2 key heads of 256: 99-100 us, 0.87. 64
+// sequences with 4 draft tokens each, 4 key heads of 128: 60-64 us, 0.72 to 0.77. A pool of 256
+// sequences with windows of 1024, 4 key heads of 64: fp32 48 us, 0.68; bf16 34 us, 0.48. One
+// sequence of 1000 keys: 10 us. What lies above the bytes' time is 5 to 18 us in all of these,
+// whatever that time is, and no pipe is busy in the short ones (tensor 23 %, issue 29 to 44 %),
+// which points to a cost of a call -- lookups ahead of the first copy, the turn from unit to unit,
+// joins, the spread of the CTAs' ends -- rather than to a rate. Its parts have not been measured
+// apart.
 #include <atomic>
 #include <ctime>
 
@@ -95,13 +98,14 @@ struct Geometry {
     static constexpr int kExtra = kF32 ? 2 * KT * RT * 4             // S, then P [key][row], two buffers
                                        : 2 * kRows * (KT + 8) * 2;   // P hi and lo [row][key]
     // CTAs per SM. A tile's chain of steps is latency: the more chains side by side the better,
-    // as far as two stages and the registers of each allow. (The windowed fp32 pool above takes
-    // 48 us with three CTAs and 52 with two.)
+    // as far as two stages and the registers of each allow. (fp32 heads of 64, three CTAs and
+    // two: the windowed pool above 47.8 and 51.4 us, 200 sequences of 16..2000 keys 42.8 and 44.9,
+    // 64 of up to 8192 49.6 both, four of 60 to 131 thousand 141 both.)
     static constexpr int kCtas = D == 256 ? 1 : kF32 && D == 64 && RT == 4 ? 3 : 2;
     // Threads: the computing warps, the loading warp and, where it costs no registers (three
     // CTAs of 5 warps fill the register file), a joining warp: it waits for the other CTAs of
     // the unit split at the range's start while the rest go on. (Windowed bf16 pool with heads of
-    // 64: 33.7 us with it, 34.6 without; 200 ragged bf16 sequences of up to 2000 keys 121.8 and
+    // 64: 33.6-34.2 us with it, 34.6 without; 200 ragged bf16 sequences of up to 2000 keys 121.8 and
     // 123.4.)
     static constexpr bool kJoinWarp = kCtas != 3;
     static constexpr int kThreads = kCompute + (kJoinWarp ? 64 : 32);

@@ -3,8 +3,8 @@
 //   S = Q K^T      tcgen05, Q and K from shared memory, S in tensor memory
 //   P = 2^(scale log2(e) S - m)   four warps per row tile, one thread per row: the row's
 //                  maximum and sum need no exchange; P goes back to tensor memory over S,
-//                  in the cache's type (half a unit of the type per weight, which averages
-//                  out below the output's own rounding)
+//                  in the cache's type: half a unit of the type per weight, which adds a
+//                  fifth to two fifths to the error of the output's own rounding
 //   O += P V       tcgen05, P from tensor memory, V from shared memory as it lies there
 //                  (rows are keys: the MN-major operand form, no transposition)
 //
@@ -31,12 +31,12 @@
 //
 // Measured, with the rate of the visible pairs' products and its share of a large bf16 matrix
 // product's: 1500 tokens after 30000, 24 heads of 256, 720 us, 1575 TFLOP/s (0.84); 16384
-// tokens of 39 ragged prompts, 32 heads of 128, 193 us, 898 TFLOP/s (0.48); 4 x 4096 tokens
-// with a window of 1000, 16 heads of 64, 131 us, 452 TFLOP/s (0.24). Key tile by key tile, a
-// pair of row tiles takes 1.84 us at head_dim 128 and 1.55 at 64, where the tensor pipe is busy
-// for 1.07 and 0.67: S, its softmax, and O are a chain per row tile, and when the warps of the
+// tokens of 39 ragged prompts, 32 heads of 128, 196 us, 884 TFLOP/s (0.47); 4 x 4096 tokens
+// with a window of 1000, 16 heads of 64, 136 us, 435 TFLOP/s (0.23). Key tile by key tile, a
+// pair of row tiles took 1.84 us at head_dim 128 and 1.55 at 64 (1 and 3 % less than now, before
+// every wait became a warp's vote), where the tensor pipe is busy for 1.07 and 0.67: S, its softmax, and O are a chain per row tile, and when the warps of the
 // two softmaxes run together, at different places of long unrolled code, they wait for
-// instructions (a scheduler issues in 36 to 43 % of its cycles). A work's partial tiles,
+// instructions (a scheduler issues in 35 to 43 % of its cycles). A work's partial tiles,
 // its first Q and its output add two to three tiles' time to each.
 #include "gdn_attn_prefill.cuh"
 #include "gdn_tc.cuh"
@@ -105,7 +105,8 @@ struct Tc {
     static constexpr int kThreads = (kSoftmax + 4) * 32;
     static constexpr int kS = 0, kO = 256;                      // tensor-memory columns
     // batches up to this many sequences run longest first (what shared memory has left): the 39
-    // ragged prompts above take 193 us, in batch order 233
+    // ragged prompts above took 193 us, in batch order 233; with heads of 256, 15 prompts of 12000
+    // tokens 147 and 162, 9 of as many 160 and 171
     static constexpr int kTable = D == 256 ? 32 : kLongestFirstMaxSeqs;
 };
 

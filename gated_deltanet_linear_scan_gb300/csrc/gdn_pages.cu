@@ -32,9 +32,10 @@ constexpr int kAppendEach = 4;  // 16-byte units of a plane a lane holds at a ti
 // A few warps per new position: four while the batch is small and latency counts, one when
 // there are enough tokens to fill the GPU (16 a SM). 64 tokens of 16 bf16 heads of 128: 2.7 us
 // with four, 3.2 with one; 16384 tokens of 8 f16 heads of 128: 20.7 us with one (0.95 of the
-// copy rate), 28.3 with four. The rows are loaded first and find their place --
-// sequence, slot, length, page: four dependent loads -- while they are under way. Also, the
-// warp of number n checks sequence n, last, and counts it when it is skipped.
+// copy rate, with most of what it writes left in L2; 24 to 28 us from a cold L2), 28.3 with
+// four. The rows are loaded first and find their place -- sequence, slot, length, page: four
+// dependent loads -- while they are under way. Also, the warp of number n checks sequence n,
+// last, and counts it when it is skipped.
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
     const int lane = threadIdx.x & 31;
     const long long warp = static_cast<long long>(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5);

@@ -595,7 +595,11 @@ gdn_status gdn_block_prefill_noalloc(const float *qkv, const float *conv_w, floa
  * pointers owned by the caller, an explicit stream, host validation, no allocation,
  * slots / pool / err_count).
  * - Types: dtype names the type of q, k, v, out and the pages of a call (a gdn_dtype).
- *   Scores, softmax statistics and sums are fp32; out is rounded once.
+ *   Scores, softmax statistics and sums are fp32; out is rounded once. The weights that
+ *   multiply the values are fp32 with fp32 pages. With 16-bit pages the decode attention
+ *   holds them in two parts of the type, far below out's own rounding; the prompt attention
+ *   in one, half a unit of the type a weight, so that its error against exact arithmetic is
+ *   a fifth to two fifths above that of rounding out alone.
  * - Heads: query head h reads key head h / (n_q_heads / n_kv_heads) (consecutive query
  *   heads share a key head; the recurrence's v-heads are tiled, vh % Hk, instead).
  *   head_dim in {64, 128, 256}. Any head ratio.
