@@ -6,8 +6,9 @@ cache, with random weights.
 
 A batch of prompts is read in, every sequence is forked into a second continuation, single
 tokens are decoded, drafts are verified and what the model did not agree with is rolled
-back (recurrent states by snapshot, cache by truncation), half of the sequences are
-released and the pages of the others moved together. Tokens, lengths and tables stay on the
+back (recurrent states by snapshot, cache by truncation), trees of drafts are read with a
+token sampled at every node and the path that the samples agree with is kept, half of the
+sequences are released and the pages of the others moved together. Tokens, lengths and tables stay on the
 device; torch multiplies the projections and holds the memory.
 """
 import math
@@ -60,6 +61,14 @@ class RecurrentLayer:
                 batch.n, x.shape[0], self.hk, self.h, self.s) // 4 + 1)
             gdn.gdn_block_prefill_varlen(*self._inputs(x), out, batch.cu, batch.n, x.shape[0],
                                          batch.longest, *self._sizes(), work, **common)
+        elif batch.parents is not None:
+            sizes = (batch.n, batch.tokens, self.hk, self.h, self.s)
+            self.tape = x.new_empty(gdn.gdn_block_tree_tape_size(*sizes) // 4)
+            work = x.new_empty(gdn.gdn_block_tree_workspace_size(*sizes) // 4)
+            inputs = self._inputs(x)
+            self.qkv = inputs[0]
+            gdn.gdn_block_tree(*inputs, out, batch.parents, *sizes, *self._sizes()[3:], self.tape,
+                               work, **common)
         elif batch.tokens == 1:
             gdn.gdn_block_decode(*self._inputs(x), out, batch.n, *self._sizes(), **common)
         else:
@@ -77,6 +86,13 @@ class RecurrentLayer:
                                  self.s, self.conv, self.conv_snaps, self.conv_dim, self.kernel,
                                  slots=batch.slots, pool=self.state.shape[0],
                                  err_count=batch.errors)
+
+    def commit(self, batch, accepted):
+        """Every sequence of a tree batch to the state behind its accepted path."""
+        gdn.gdn_block_tree_commit(self.qkv, self.conv, self.state, batch.parents, accepted, batch.n,
+                                  batch.tokens, self.hk, self.h, self.s, self.kernel, self.tape,
+                                  slots=batch.slots, pool=self.state.shape[0],
+                                  err_count=batch.errors)
 
     def copy_slots(self, parents, children):
         self.state[children.long()] = self.state[parents.long()]
@@ -112,6 +128,11 @@ class AttentionLayer:
         if batch.cu is not None:
             gdn.gdn_attn_prefill(q, *books, out, batch.cu, batch.n, x.shape[0], batch.longest,
                                  self.hq, hkv, d, *pages, *mask, **common)
+        elif batch.parents is not None:
+            work = torch.empty(gdn.gdn_attn_tree_workspace_size(
+                batch.n, batch.tokens, self.hq, hkv, d), device="cuda", dtype=torch.uint8)
+            gdn.gdn_attn_tree(q, *books, out, batch.parents, batch.n, batch.tokens, self.hq, hkv, d,
+                              *pages, *mask, work, **common)
         else:
             work = torch.empty(gdn.gdn_attn_decode_workspace_size(
                 batch.n, batch.tokens, self.hq, hkv, d), device="cuda", dtype=torch.uint8)
@@ -154,6 +175,20 @@ class Cache:
                                self.page_size, self.n_pages, self.max_pages, slots=slots,
                                pool=self.pool, err_count=errors)
 
+    def accept(self, batch, tokens, sampled):
+        """The path of every tree that the sampled tokens agree with: its rows moved together, the
+        others' dropped. (last nodes + 1, lengths of the paths, next tokens, paths)"""
+        n, m = tokens.shape
+        ints = lambda *shape: torch.empty(shape, device="cuda", dtype=torch.int32)  # noqa: E731
+        accepted, kept, new_lens, following, path = ints(n), ints(n), ints(n), ints(n), ints(n, m)
+        planes, n_pages, page_bytes, max_pages = self._data
+        gdn.gdn_tree_accept(batch.parents, tokens, sampled, accepted, kept, new_lens, following,
+                            path, n, m, self.planes, self.table, self.lens, self.n_kv_heads,
+                            self.page_size, planes, n_pages, page_bytes, max_pages,
+                            slots=batch.slots, pool=self.pool, err_count=batch.errors)
+        self.truncate(batch.slots, new_lens, batch.errors)
+        return accepted, kept, following, path
+
     def compact(self):
         gdn.gdn_pages_compact(self.planes, self.table, self.lens, self.refs, self.page_size,
                               *self._data, self.pool, self.work, n_live=self.live)
@@ -161,9 +196,10 @@ class Cache:
 
 class Batch:
     """What one step runs on: the slots, and the rows each of them has (ragged, or the same
-    number for all)."""
+    number for all: a chain, or a tree where `parents` says so)."""
 
-    def __init__(self, slots, errors, lengths=None, tokens=0):
+    def __init__(self, slots, errors, lengths=None, tokens=0, parents=None):
+        self.parents = parents
         self.slots, self.errors, self.n, self.tokens = slots, errors, slots.numel(), tokens
         self.cu, self.longest = None, tokens
         if lengths is not None:
@@ -221,6 +257,29 @@ class Server:
         self.cache.truncate(slots, self.cache.lens[slots.long()] - m + kept, self.errors)
         return logits, kept
 
+    def sample(self, logits, uniforms, rows_per_set=1, **settings):
+        """A token for every row of logits [rows][vocab]; the settings (temperature, top_k, top_p,
+        min_p) are tensors of one value per rows_per_set rows."""
+        rows, vocab = logits.shape
+        tokens = torch.empty(rows, device="cuda", dtype=torch.int32)
+        gdn.gdn_sample(logits, uniforms, tokens, rows, vocab, rows_per_set=rows_per_set,
+                       err_count=self.errors, **settings)
+        return tokens
+
+    def verify_tree(self, slots, tokens, parents, uniforms, **settings):
+        """Trees of drafts [n][m], node 0 certain: a token is sampled at every node from its uniform
+        number [n][m], and the path along which the samples agree with the drafts is kept. Returns
+        (logits [n][m][vocab], paths [n][m], their lengths, the next tokens)."""
+        n, m = tokens.shape
+        batch = Batch(slots, self.errors, tokens=m, parents=parents)
+        logits = self._step(batch, tokens.flatten())
+        sampled = self.sample(logits, uniforms.flatten(), rows_per_set=m, **settings)
+        accepted, kept, following, path = self.cache.accept(batch, tokens, sampled)
+        for layer in self.layers:
+            if isinstance(layer, RecurrentLayer):
+                layer.commit(batch, accepted)
+        return logits.view(n, m, -1), path, kept, following
+
     def fork(self, parents, children):
         self.cache.fork(parents, children, self.errors)
         for layer in self.layers:
@@ -257,6 +316,13 @@ def main():
     drafts = torch.cat([tokens[:, None], torch.randint(512, (8, 3), device="cuda")], 1)
     _, kept = server.verify(everyone, drafts)
     print("drafts kept, the certain token among them:", kept.tolist())
+    # trees: node 0 the certain token, three first guesses, two second ones behind each of two
+    parents = ints(-1, 0, 0, 0, 1, 1, 2, 2).repeat(8, 1)
+    drafts = torch.randint(512, (8, 8), device="cuda", dtype=torch.int32)
+    _, path, kept, following = server.verify_tree(
+        everyone, drafts, parents, torch.rand(8, 8, device="cuda"),
+        temperature=torch.full((8,), 0.8, device="cuda"), top_p=torch.full((8,), 0.95, device="cuda"))
+    print("nodes kept of every tree:", kept.tolist(), "next tokens:", following.tolist())
     server.release(slots)
     server.cache.compact()
     server.check()

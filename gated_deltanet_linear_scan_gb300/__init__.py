@@ -38,6 +38,9 @@ __all__ = [
     "gdn_attn_prefill_workspace_size", "gdn_attn_prefill", "gdn_pages_workspace_size",
     "gdn_pages_copy", "gdn_pages_reserve", "gdn_pages_fork", "gdn_pages_truncate",
     "gdn_pages_compact", "gdn_selftest_attn_wait",
+    "gdn_attn_tree_workspace_size", "gdn_attn_tree", "gdn_block_tree_tape_size",
+    "gdn_block_tree_workspace_size", "gdn_block_tree", "gdn_block_tree_commit", "gdn_tree_accept",
+    "gdn_sample", "MAX_TREE_NODES", "NO_NODE",
 ]
 
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_NULL", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_UNSUPPORTED",
@@ -126,12 +129,26 @@ _SIGS = {
     "gdn_pages_truncate": ([_P] * 4 + [_I] * 4 + [_P, _I, _P, _P], _I),
     "gdn_pages_compact": ([_P] * 4 + [_I] * 3 + [ctypes.c_size_t, _I, _I, _P, _P,
                                                  ctypes.c_size_t, _P], _I),
+    "gdn_attn_tree_workspace_size": ([_I] * 5, ctypes.c_size_t),
+    "gdn_attn_tree": ([_P] * 7 + [_I] * 10 + [_F, _I, _I, _P, _I, _P, _P, ctypes.c_size_t, _P], _I),
+    "gdn_block_tree_tape_size": ([_I] * 5, ctypes.c_size_t),
+    "gdn_block_tree_workspace_size": ([_I] * 5, ctypes.c_size_t),
+    "gdn_block_tree": ([_P] * 12 + [_I] * 6 + [_F, _F, _F, _P, _I, _P, _P, ctypes.c_size_t, _P,
+                                              ctypes.c_size_t, _P], _I),
+    "gdn_block_tree_commit": ([_P] * 5 + [_I] * 6 + [_P, _I, _P, _P, ctypes.c_size_t, _P], _I),
+    "gdn_tree_accept": ([_P] * 8 + [_I] * 2 + [_P] * 3 + [_I] * 4 + [ctypes.c_size_t, _I, _P, _I,
+                                                                  _P, _P], _I),
+    "gdn_sample": ([_P] * 7 + [_I] * 5 + [_P, _P], _I),
 }
 
 _DTYPES = {}  # gdn_dtype codes by torch type, filled on first use
 
 # Size of the fixed device scratch of gdn_block_prefill_noalloc (include/gdn.h).
 PREFILL_NOALLOC_SCRATCH_BYTES = 32 << 20
+
+# Trees of drafts (include/gdn.h): the most nodes of one, and the parent of a node that is not there.
+MAX_TREE_NODES = 64
+NO_NODE = -2
 
 
 def lib_path():
@@ -847,3 +864,107 @@ def gdn_pages_compact(pages, page_table, kv_lens, page_refs, page_size, n_planes
         _ptr(page_refs, "page_refs", i32), page_size, n_planes, n_pages, page_bytes, max_pages,
         pool, _ptr(n_live, "n_live", i32, optional=True), _ws_ptr(workspace),
         _ws_bytes(workspace), _stream(stream)))
+
+
+# ------------------------------------------------------------------ trees of drafts
+
+def gdn_attn_tree_workspace_size(n_seqs, n_nodes, n_q_heads, n_kv_heads, head_dim):
+    return library().gdn_attn_tree_workspace_size(n_seqs, n_nodes, n_q_heads, n_kv_heads, head_dim)
+
+
+def gdn_attn_tree(q, k_pages, v_pages, page_table, kv_lens, out, parents, n_seqs, n_nodes, n_q_heads,
+                  n_kv_heads, head_dim, page_size, n_pages, max_pages, window, n_sinks, scale,
+                  workspace, slots=None, pool=None, err_count=None, stream=None):
+    """Attention of the nodes of each sequence's tree over its paged cache, the nodes' own keys
+    being its last n_nodes rows."""
+    pool = _pool(pool, n_seqs, slots)
+    dt, code = _dtype(k_pages, "k_pages")
+    i32 = _torch().int32
+    qp, q_stride = _rows(q, "q", dt, n_q_heads, head_dim)
+    _check("gdn_attn_tree", library().gdn_attn_tree(
+        qp, _ptr(k_pages, "k_pages", dt), _ptr(v_pages, "v_pages", dt),
+        _ptr(page_table, "page_table", i32), _ptr(kv_lens, "kv_lens", i32), _ptr(out, "out", dt),
+        _ptr(parents, "parents", i32), n_seqs, n_nodes, n_q_heads, n_kv_heads, head_dim, page_size,
+        n_pages, max_pages, window, n_sinks, scale, q_stride, code, _slots(slots), pool,
+        _errc(err_count), _ws_ptr(workspace), _ws_bytes(workspace), _stream(stream)))
+
+
+def gdn_block_tree_tape_size(n_seqs, n_nodes, n_k_heads, n_v_heads, state_size):
+    return library().gdn_block_tree_tape_size(n_seqs, n_nodes, n_k_heads, n_v_heads, state_size)
+
+
+def gdn_block_tree_workspace_size(n_seqs, n_nodes, n_k_heads, n_v_heads, state_size):
+    return library().gdn_block_tree_workspace_size(n_seqs, n_nodes, n_k_heads, n_v_heads, state_size)
+
+
+def gdn_block_tree(qkv, conv_w, conv_state, alpha, b, dt, a, z, norm_w, state, out, parents, n_seqs,
+                   n_nodes, n_k_heads, n_v_heads, state_size, conv_kernel, scale, l2_eps, norm_eps,
+                   tape, workspace, slots=None, pool=None, err_count=None, stream=None):
+    """The block over a tree's nodes; states and conv histories are read only, and `tape` keeps
+    what gdn_block_tree_commit needs."""
+    pool = _pool(pool, n_seqs, slots)
+    _check("gdn_block_tree", library().gdn_block_tree(
+        _ptr(qkv, "qkv"), _ptr(conv_w, "conv_w"), _ptr(conv_state, "conv_state"),
+        _ptr(alpha, "alpha"), _ptr(b, "b"), _ptr(dt, "dt"), _ptr(a, "a"), _ptr(z, "z"),
+        _ptr(norm_w, "norm_w"), _ptr(state, "state"), _ptr(out, "out"),
+        _ptr(parents, "parents", _torch().int32), n_seqs, n_nodes, n_k_heads, n_v_heads, state_size,
+        conv_kernel, scale, l2_eps, norm_eps, _slots(slots), pool, _errc(err_count), _ws_ptr(tape),
+        _ws_bytes(tape), _ws_ptr(workspace), _ws_bytes(workspace), _stream(stream)))
+
+
+def gdn_block_tree_commit(qkv, conv_state, state, parents, accepted, n_seqs, n_nodes, n_k_heads,
+                          n_v_heads, state_size, conv_kernel, tape, slots=None, pool=None,
+                          err_count=None, stream=None):
+    """States and conv histories carried on along each tree's path to node accepted[n] - 1."""
+    pool = _pool(pool, n_seqs, slots)
+    i32 = _torch().int32
+    _check("gdn_block_tree_commit", library().gdn_block_tree_commit(
+        _ptr(qkv, "qkv"), _ptr(conv_state, "conv_state"), _ptr(state, "state"),
+        _ptr(parents, "parents", i32), _ptr(accepted, "accepted", i32), n_seqs, n_nodes, n_k_heads,
+        n_v_heads, state_size, conv_kernel, _slots(slots), pool, _errc(err_count), _ws_ptr(tape),
+        _ws_bytes(tape), _stream(stream)))
+
+
+def gdn_tree_accept(parents, tokens, sampled, accepted, n_kept, new_lens, next_tokens, path, n_seqs,
+                    n_nodes, pages=None, page_table=None, kv_lens=None, n_kv_heads=0, page_size=0,
+                    n_planes=0, n_pages=0, page_bytes=0, max_pages=0, slots=None, pool=None,
+                    err_count=None, stream=None):
+    """The path of each tree along which `sampled` agrees with `tokens`; its rows move together in
+    every plane of `pages` (None: nothing moves)."""
+    pool = _pool(pool, n_seqs, slots)
+    i32 = _torch().int32
+    _check("gdn_tree_accept", library().gdn_tree_accept(
+        _ptr(parents, "parents", i32), _ptr(tokens, "tokens", i32), _ptr(sampled, "sampled", i32),
+        _ptr(accepted, "accepted", i32), _ptr(n_kept, "n_kept", i32),
+        _ptr(new_lens, "new_lens", i32, optional=True), _ptr(next_tokens, "next_tokens", i32),
+        _ptr(path, "path", i32, optional=True), n_seqs, n_nodes,
+        None if pages is None else _page_data(pages),
+        _ptr(page_table, "page_table", i32, optional=True),
+        _ptr(kv_lens, "kv_lens", i32, optional=True), n_kv_heads, page_size, n_planes, n_pages,
+        page_bytes, max_pages, _slots(slots), pool, _errc(err_count), _stream(stream)))
+
+
+def _logits(t, vocab):
+    """(data pointer, elements from row to row, gdn_dtype code) of [rows][vocab]; the rows may be
+    slices of wider ones."""
+    _, code = _dtype(t, "logits")
+    if not t.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    if t.is_contiguous() and t.dim() != 2:
+        return t.data_ptr(), vocab, code
+    if t.dim() != 2 or t.shape[1] != vocab or (vocab > 1 and t.stride(1) != 1):
+        raise ValueError(f"logits must be contiguous, or of shape [rows, {vocab}] and dense in their rows")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), vocab), code
+
+
+def gdn_sample(logits, uniforms, tokens, rows, vocab, temperature=None, top_k=None, top_p=None,
+               min_p=None, rows_per_set=1, err_count=None, stream=None):
+    """A token for every row of logits from the row's uniform number; one temperature, top_k, top_p
+    and min_p per rows_per_set rows (None: 1, and no filter)."""
+    i32 = _torch().int32
+    ptr, stride, code = _logits(logits, vocab)
+    _check("gdn_sample", library().gdn_sample(
+        ptr, _ptr(uniforms, "uniforms"), _ptr(temperature, "temperature", optional=True),
+        _ptr(top_k, "top_k", i32, optional=True), _ptr(top_p, "top_p", optional=True),
+        _ptr(min_p, "min_p", optional=True), _ptr(tokens, "tokens", i32), rows, vocab, stride, code,
+        rows_per_set, _errc(err_count), _stream(stream)))

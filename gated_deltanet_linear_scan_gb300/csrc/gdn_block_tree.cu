@@ -1,0 +1,651 @@
+// gdn_block_tree.cu -- the Gated-DeltaNet block over a tree of drafted tokens, and the states
+// carried on along the accepted path (sm_103a).
+//
+// Every node continues its parent's state. With anc(i) the ancestors of node i, G_i the sum of
+// the log-decays on its path (itself included) and S0 the sequence's state,
+//   u_i = beta_i (v_i - e^{G_i} S0^T k_i - sum_{s in anc(i)} e^{G_i - G_s} (k_i . k_s) u_s)
+//   y_i = scale (e^{G_i} S0^T q_i + sum_{s in anc(i) and i} e^{G_i - G_s} (q_i . k_s) u_s)
+// is the recurrence unrolled: node i's state is e^{G_i} S0 + sum_{s} e^{G_i - G_s} k_s u_s^T.
+// So the state is read once for all nodes and not written: a tree of N nodes moves 1 / (N + 1) of
+// the bytes of a scan that keeps a snapshot per node. What an accepted path needs later are k, g
+// and u of its nodes (the tape): its state is one more rank-L update, read and written once.
+#include "gdn_tree.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr size_t kAlignFloats = 64;  // 256-byte sub-buffers
+
+__host__ __device__ constexpr size_t round_up(size_t n) { return (n + kAlignFloats - 1) / kAlignFloats * kAlignFloats; }
+
+// What the commit reads: k [n][N][Hk][S], g [n][N][H], u [n][N][H][S].
+struct Tape {
+    size_t k, g, u, floats;
+    Tape(size_t rows, int hk, int h, int s) {
+        k = 0;
+        g = k + round_up(rows * hk * s);
+        u = g + round_up(rows * h);
+        floats = u + round_up(rows * h * s);
+    }
+};
+
+// Scratch: q [n][N][Hk][S], v [n][N][H][S], beta [n][N][H], the products k_i.k_s and q_i.k_s
+// [n][Hk][N][N][2], and whether a node is there [n][N].
+struct Scratch {
+    size_t q, v, beta, gram, there, floats;
+    Scratch(size_t rows, int n_nodes, int hk, int h, int s) {
+        q = 0;
+        v = q + round_up(rows * hk * s);
+        beta = v + round_up(rows * h * s);
+        gram = beta + round_up(rows * h);
+        there = gram + round_up(rows * n_nodes * hk * 2);
+        floats = there + round_up(rows);
+    }
+};
+
+struct TreeParams {
+    const float *qkv, *conv_w, *conv_state, *alpha, *b, *dt, *a, *z, *norm_w, *state;
+    float *out;
+    const int32_t *parents, *slots;
+    int n_nodes, n_k_heads, n_v_heads, pool;
+    float scale, l2_eps, norm_eps;
+    int32_t *err_count;
+    float *k, *g, *u;             // the tape
+    float *q, *v, *beta, *gram;   // scratch
+    int *there;
+};
+
+// ------------------------------------------------------------------ conv, norms and gates
+
+// One warp per (head slice of S channels, kConvNodes nodes, sequence), lane L holding channels
+// [E L, E L + E). A node's taps are its own raw input and those of its nearest ancestors, the
+// conv history behind the root's; the arithmetic is the prefill block's, so a tree that is a chain
+// has its bits. The CTAs behind the slices' compute the gates. A node that is not there has zeros.
+constexpr int kConvWarps = 4;
+constexpr int kConvNodes = 4;
+
+template <int E, int K>
+__global__ void __launch_bounds__(32 * kConvWarps) tree_conv_kernel(const TreeParams p) {
+    constexpr int S = 32 * E, TAPS = K - 1;
+    __shared__ unsigned long long path_of[kMaxNodes];
+    __shared__ int up[kMaxNodes];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n = blockIdx.z, N = p.n_nodes, Hk = p.n_k_heads, H = p.n_v_heads;
+    const int slot = p.slots ? p.slots[n] : n;
+    const bool skip = slot < 0 || slot >= p.pool;
+    const bool counts = blockIdx.x == 0 && blockIdx.y == 0;
+    if (skip) {
+        if (counts && threadIdx.x == 0 && p.err_count) atomicAdd(p.err_count, 1);
+        return;
+    }
+    if (warp == 0) {
+        unsigned long long paths[2];
+        const bool bad = tree_paths(p.parents + static_cast<size_t>(n) * N, N, paths, path_of, up);
+        if (bad && counts && lane == 0 && p.err_count) atomicAdd(p.err_count, 1);
+    }
+    __syncthreads();
+    const int i0 = blockIdx.y * kConvNodes, i1 = min(N, i0 + kConvNodes);
+    const size_t row0 = static_cast<size_t>(n) * N;
+    const int slices = 2 * Hk + H;
+    if (blockIdx.x == gridDim.x - 1) {
+        // ---- the gates: g = a softplus(alpha + dt), beta = sigmoid(b)
+        for (int x = threadIdx.x; x < (i1 - i0) * H; x += 32 * kConvWarps) {
+            const int i = i0 + x / H, h = x % H;
+            const size_t at = (row0 + i) * H + h;
+            const bool here = path_of[i] != 0;
+            p.g[at] = here ? p.a[h] * softplus_guarded(p.alpha[at] + p.dt[h]) : 0.0f;
+            p.beta[at] = here ? 1.0f / (1.0f + expf(-p.b[at])) : 0.0f;
+            if (h == 0) p.there[row0 + i] = here;
+        }
+        return;
+    }
+    const int sl = blockIdx.x * kConvWarps + warp;  // this warp's head slice
+    if (sl >= slices) return;
+    const size_t conv_dim = static_cast<size_t>(slices) * S;
+    const size_t ch0 = static_cast<size_t>(sl) * S + E * lane;
+    float wc[K][E], hist[TAPS][E];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int t = 0; t < K; ++t) wc[t][e] = p.conv_w[(ch0 + e) * K + t];
+    const float *hs = p.conv_state + (static_cast<size_t>(slot) * conv_dim + ch0) * TAPS;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int t = 0; t < TAPS; ++t) hist[t][e] = hs[e * TAPS + t];
+    const float *x_ptr = p.qkv + row0 * conv_dim + ch0;
+    const bool is_qk = sl < 2 * Hk;  // uniform over the warp
+    float *dst = is_qk ? (sl < Hk ? p.q : p.k) + (row0 * Hk + sl % Hk) * S + E * lane
+                       : p.v + (row0 * H + (sl - 2 * Hk)) * S + E * lane;
+    const size_t dst_step = static_cast<size_t>(is_qk ? Hk : H) * S;
+#pragma unroll
+    for (int y = 0; y < kConvNodes; ++y) {
+        const int i = i0 + y;
+        if (i >= i1) break;  // uniform over the warp, as every condition below
+        float o[E];
+        unsigned long long path = path_of[i];
+        if (path == 0) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = 0.0f;
+        } else {
+            // taps[t]: of the t-th oldest input, taps[TAPS] the node's own
+            float taps[K][E];
+            int behind = 0;  // taps past the root
+#pragma unroll
+            for (int t = TAPS; t >= 0; --t) {
+                if (path != 0) {
+                    const int a = 63 - __clzll(static_cast<long long>(path));
+                    path &= ~(1ull << a);
+                    load_vec<E>(taps[t], x_ptr + static_cast<size_t>(a) * conv_dim);
+                } else {
+                    ++behind;
+#pragma unroll
+                    for (int h = 1; h <= TAPS; ++h)
+                        if (h == behind)
+#pragma unroll
+                            for (int e = 0; e < E; ++e) taps[t][e] = hist[TAPS - h][e];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                float pre = __fmul_rn(taps[TAPS][e], wc[K - 1][e]);
+#pragma unroll
+                for (int t = 0; t < TAPS; ++t) pre = __fmaf_rn(taps[t][e], wc[t][e], pre);
+                o[e] = silu(pre);
+            }
+            if (is_qk) {
+                float ss = 0.0f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) ss = __fmaf_rn(o[e], o[e], ss);
+                ss = warp_allsum(ss);
+                const float inv = 1.0f / fmaxf(sqrtf(ss), p.l2_eps);
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] *= inv;
+            }
+        }
+        store_vec<E>(dst + static_cast<size_t>(i) * dst_step, o);
+    }
+}
+
+// ------------------------------------------------------------------ products of the nodes
+
+// k_i.k_s and q_i.k_s of every node i with itself and its ancestors s, one warp per node at a
+// time. Grid: (k-head, sequence).
+constexpr int kGramWarps = 8;
+
+template <int E>
+__global__ void __launch_bounds__(32 * kGramWarps) tree_gram_kernel(const TreeParams p) {
+    constexpr int S = 32 * E;
+    __shared__ unsigned long long path_of[kMaxNodes];
+    __shared__ int up[kMaxNodes];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kh = blockIdx.x, n = blockIdx.y, N = p.n_nodes, Hk = p.n_k_heads;
+    const int slot = p.slots ? p.slots[n] : n;
+    if (slot < 0 || slot >= p.pool) return;
+    if (warp == 0) {
+        unsigned long long paths[2];
+        tree_paths(p.parents + static_cast<size_t>(n) * N, N, paths, path_of, up);
+    }
+    __syncthreads();
+    const size_t base = (static_cast<size_t>(n) * N * Hk + kh) * S + E * lane, step = static_cast<size_t>(Hk) * S;
+    float2 *gram = reinterpret_cast<float2 *>(p.gram) + (static_cast<size_t>(n) * Hk + kh) * N * N;
+    for (int i = warp; i < N; i += kGramWarps) {
+        unsigned long long path = path_of[i];
+        if (path == 0) continue;
+        float ki[E], qi[E];
+        load_vec<E>(ki, p.k + base + i * step);
+        load_vec<E>(qi, p.q + base + i * step);
+        while (path != 0) {
+            const int s = __ffsll(static_cast<long long>(path)) - 1;
+            path &= path - 1;
+            float ks[E];
+            load_vec<E>(ks, p.k + base + s * step);
+            float part[2] = {lane_dot<E>(ki, ks), lane_dot<E>(qi, ks)};
+            const float sum = warp_sum_packed<2>(part, lane);
+            const float other = __shfl_sync(FULL_MASK, sum, row_home_lane<2>(1));
+            if (lane == 0) gram[i * N + s] = make_float2(sum, other);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ the nodes over the state
+
+// Grid: (block of state rows, v-head, sequence), 128 threads. Rows j of the transposed state are
+// value channels, and independent of one another: a CTA takes JB of them. First the products of
+// its rows with all k_i and q_i (kTileRows of them at a time; a lane holds JB / 32 state rows and
+// a warp 8 of the vectors), then u, node after node, and y, all of them at once.
+constexpr int kStateThreads = 128;
+constexpr int kTileRows = 32;
+
+template <int E>
+struct StateSmem {
+    static constexpr int S = 32 * E;
+    static constexpr int JB = S >= 64 ? 64 : 32;
+    static constexpr int kPad = S + 4;  // lanes' 16-byte reads of their rows in different banks
+    static size_t bytes(int n) {
+        return sizeof(float) * (static_cast<size_t>(JB) * kPad + kTileRows * S + 2 * n * JB + 2 * n * n);
+    }
+};
+
+// The sums on the nodes' paths, in two parts (hi + lo, off by 2^-40 relative): their differences
+// e^{G_i - G_s} are then good to 2^-23 however long the path is.
+__device__ __forceinline__ void path_sum(unsigned long long path, const float *g, float &hi, float &lo) {
+    hi = lo = 0.0f;
+    while (path != 0) {
+        const int s = __ffsll(static_cast<long long>(path)) - 1;
+        path &= path - 1;
+        const float x = g[s], sum = __fadd_rn(hi, x), y = __fsub_rn(sum, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(sum, y)), __fsub_rn(x, y)));
+        hi = sum;
+    }
+}
+
+template <int E>
+__global__ void __launch_bounds__(kStateThreads) tree_state_kernel(const TreeParams p) {
+    using L = StateSmem<E>;
+    constexpr int S = L::S, JB = L::JB, JL = JB / 32, kPad = L::kPad;
+    extern __shared__ __align__(16) float smem[];
+    __shared__ unsigned long long path_of[kMaxNodes];
+    __shared__ int up[kMaxNodes];
+    __shared__ float g_of[kMaxNodes], hi_of[kMaxNodes], lo_of[kMaxNodes], beta_of[kMaxNodes], decay[kMaxNodes];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int j0 = blockIdx.x * JB, vh = blockIdx.y, n = blockIdx.z;
+    const int N = p.n_nodes, Hk = p.n_k_heads, H = p.n_v_heads, kh = vh % Hk;
+    const int slot = p.slots ? p.slots[n] : n;
+    if (slot < 0 || slot >= p.pool) return;
+    float *rows = smem;                       // [JB][kPad]
+    float *tile = rows + JB * kPad;           // [kTileRows][S]
+    float *d = tile + kTileRows * S;          // [2N][JB]: products with k, then u; with q
+    float2 *coef = reinterpret_cast<float2 *>(d + 2 * N * JB);  // [N][N]
+    const float *state = p.state + ((static_cast<size_t>(slot) * H + vh) * S + j0) * S;
+    for (int x = tid; x < JB * S / 4; x += kStateThreads) {
+        const int j = x / (S / 4), c = x % (S / 4);
+        *reinterpret_cast<float4 *>(rows + j * kPad + 4 * c) = *reinterpret_cast<const float4 *>(state + j * S + 4 * c);
+    }
+    const size_t row0 = static_cast<size_t>(n) * N;
+    if (warp == 0) {
+        unsigned long long paths[2];
+        tree_paths(p.parents + row0, N, paths, path_of, up);
+    }
+    if (tid < N) {
+        g_of[tid] = p.g[(row0 + tid) * H + vh];
+        beta_of[tid] = p.beta[(row0 + tid) * H + vh];
+    }
+    __syncthreads();
+    if (tid < N) {
+        path_sum(path_of[tid], g_of, hi_of[tid], lo_of[tid]);
+        decay[tid] = expf(hi_of[tid] + lo_of[tid]);
+    }
+    __syncthreads();
+    {
+        const float2 *gram = reinterpret_cast<const float2 *>(p.gram) + (static_cast<size_t>(n) * Hk + kh) * N * N;
+        for (int x = tid; x < N * N; x += kStateThreads) {
+            const int i = x / N, s = x % N;
+            if (!((path_of[i] >> s) & 1ull)) continue;
+            const float w = expf((hi_of[i] - hi_of[s]) + (lo_of[i] - lo_of[s]));
+            const float2 dot = gram[x];
+            coef[x] = make_float2(beta_of[i] * w * dot.x, w * dot.y);
+        }
+    }
+    // ---- the products with the state
+    for (int t0 = 0; t0 < 2 * N; t0 += kTileRows) {
+        __syncthreads();  // the tile before has been read
+        const int count = min(kTileRows, 2 * N - t0);
+        for (int x = tid; x < count * (S / 4); x += kStateThreads) {
+            const int r = x / (S / 4), c = x % (S / 4), i = t0 + r;
+            const float *src = (i < N ? p.k + ((row0 + i) * Hk + kh) * S : p.q + ((row0 + i - N) * Hk + kh) * S);
+            *reinterpret_cast<float4 *>(tile + r * S + 4 * c) = *reinterpret_cast<const float4 *>(src + 4 * c);
+        }
+        __syncthreads();
+        const float *mine = tile + warp * 8 * S;
+        if (warp * 8 < count) {
+            float acc[JL][8] = {};
+#pragma unroll 4
+            for (int c = 0; c < S; c += 4) {
+                float4 x[JL];
+#pragma unroll
+                for (int l = 0; l < JL; ++l) x[l] = *reinterpret_cast<const float4 *>(rows + (lane + 32 * l) * kPad + c);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const float4 y = *reinterpret_cast<const float4 *>(mine + r * S + c);
+#pragma unroll
+                    for (int l = 0; l < JL; ++l) {
+                        acc[l][r] = fmaf(x[l].x, y.x, acc[l][r]);
+                        acc[l][r] = fmaf(x[l].y, y.y, acc[l][r]);
+                        acc[l][r] = fmaf(x[l].z, y.z, acc[l][r]);
+                        acc[l][r] = fmaf(x[l].w, y.w, acc[l][r]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (warp * 8 + r < count)
+#pragma unroll
+                    for (int l = 0; l < JL; ++l) d[(t0 + warp * 8 + r) * JB + lane + 32 * l] = acc[l][r];
+        }
+    }
+    __syncthreads();
+    // ---- u, one thread a row, node after node
+    if (tid < JB) {
+        const float *v = p.v + (row0 * H + vh) * S + j0 + tid;
+        float *u_out = p.u + (row0 * H + vh) * S + j0 + tid;
+        const size_t step = static_cast<size_t>(H) * S;
+        float next = v[0];
+        for (int i = 0; i < N; ++i) {
+            const float vi = next;
+            if (i + 1 < N) next = v[(i + 1) * step];
+            unsigned long long path = path_of[i] & ~(1ull << i);
+            float u = beta_of[i] * (vi - decay[i] * d[i * JB + tid]);
+            while (path != 0) {
+                const int s = __ffsll(static_cast<long long>(path)) - 1;
+                path &= path - 1;
+                u = fmaf(-coef[i * N + s].x, d[s * JB + tid], u);
+            }
+            if (path_of[i] == 0) u = 0.0f;
+            d[i * JB + tid] = u;
+            u_out[i * step] = u;
+        }
+    }
+    __syncthreads();
+    // ---- y
+    for (int x = tid; x < N * JB; x += kStateThreads) {
+        const int i = x / JB, j = x % JB;
+        unsigned long long path = path_of[i];
+        float y = 0.0f;
+        if (path != 0) {
+            y = decay[i] * d[(N + i) * JB + j];
+            while (path != 0) {
+                const int s = __ffsll(static_cast<long long>(path)) - 1;
+                path &= path - 1;
+                y = fmaf(coef[i * N + s].y, d[s * JB + j], y);
+            }
+        }
+        p.out[((row0 + i) * H + vh) * S + j0 + j] = p.scale * y;
+    }
+}
+
+// ------------------------------------------------------------------ the gated norm
+
+// One warp per head row, as gdn_gated_norm; rows of nodes that are not there are zeros.
+constexpr int kNormThreads = 256;
+
+template <int E>
+__global__ void __launch_bounds__(kNormThreads) tree_norm_kernel(const TreeParams p, long long rows) {
+    constexpr int D = 32 * E;
+    const long long row = blockIdx.x * static_cast<long long>(kNormThreads / 32) + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    const int lane = threadIdx.x & 31;
+    float yv[E], zv[E], wv[E];
+    load_vec<E>(yv, p.out + row * D + lane * E);
+    load_vec<E>(zv, p.z + row * D + lane * E);
+    load_vec<E>(wv, p.norm_w + lane * E);
+    const long long node = row / p.n_v_heads;
+    if (p.slots) {
+        const int slot = p.slots[node / p.n_nodes];
+        if (slot < 0 || slot >= p.pool) return;
+    }
+    if (!p.there[node]) return;  // (y is zeros)
+    float ss = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) ss = __fmaf_rn(yv[e], yv[e], ss);
+    ss = warp_allsum(ss);
+    const float inv_rms = 1.0f / sqrtf(ss / static_cast<float>(D) + p.norm_eps);
+    float o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = yv[e] * inv_rms * wv[e] * silu(zv[e]);
+    store_vec<E>(p.out + row * D + lane * E, o);
+}
+
+// ------------------------------------------------------------------ the commit
+
+struct CommitParams {
+    const float *qkv;
+    float *conv_state, *state;
+    const int32_t *parents, *accepted, *slots;
+    int n_nodes, n_k_heads, n_v_heads, conv_dim, taps, pool;
+    int32_t *err_count;
+    const float *k, *g, *u;
+};
+
+// S <- e^{G_l} S0 + sum_{s on the path to l} e^{G_l - G_s} k_s u_s^T. Grid: (share, sequence); the
+// first `state_shares` shares are blocks of 64 state rows, 8 to a warp, held in registers while the
+// path's k and u pass through shared memory; the rest roll the conv history.
+constexpr int kCommitThreads = 256;
+constexpr int kCommitRows = 64;
+constexpr int kCommitNodes = 16;
+constexpr int kCommitChannels = kCommitThreads * 4;
+
+template <int E>
+__global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const CommitParams p, int state_shares) {
+    constexpr int S = 32 * E, R = 8;
+    constexpr int kRows = S < kCommitRows ? S : kCommitRows;  // rows of a share
+    constexpr int kPerHead = S / kRows;
+    __shared__ unsigned long long path_of[kMaxNodes];
+    __shared__ int up[kMaxNodes], walk[kMaxNodes];
+    __shared__ float g_of[kMaxNodes], weight[kMaxNodes + 1];
+    __shared__ __align__(16) float ks[kCommitNodes][S], us[kCommitNodes][kRows];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int n = blockIdx.y, N = p.n_nodes, Hk = p.n_k_heads, H = p.n_v_heads;
+    const int slot = p.slots ? p.slots[n] : n, share = blockIdx.x;
+    const int m = p.accepted[n];
+    const bool range = slot >= 0 && slot < p.pool && m >= 0 && m <= N;
+    if (range && m == 0) return;  // nothing accepted: the state stays
+    const size_t row0 = static_cast<size_t>(n) * N;
+    if (tid < 32 && range) {
+        unsigned long long paths[2];
+        tree_paths(p.parents + row0, N, paths, path_of, up);
+    }
+    __syncthreads();
+    const unsigned long long path = range ? path_of[m - 1] : 0;
+    if (path == 0) {  // out of range, or a node that is not there
+        if (share == 0 && tid == 0 && p.err_count) atomicAdd(p.err_count, 1);
+        return;
+    }
+    const int len = __popcll(path);
+    if (tid < kMaxNodes && ((path >> tid) & 1ull)) walk[__popcll(path & ((1ull << tid) - 1))] = tid;
+    if (share >= state_shares) {
+        __syncthreads();
+        for (int c = (share - state_shares) * kCommitChannels + tid;
+             c < min(p.conv_dim, (share - state_shares + 1) * kCommitChannels); c += kCommitThreads) {
+            float *hs = p.conv_state + (static_cast<size_t>(slot) * p.conv_dim + c) * p.taps;
+            // entry t is the path's input len - taps + t, or the old entry len + t before those:
+            // entries move down only
+            for (int t = 0; t < p.taps; ++t) {
+                const int at = len - p.taps + t;
+                hs[t] = at >= 0 ? p.qkv[(row0 + walk[at]) * p.conv_dim + c] : hs[len + t];
+            }
+        }
+        return;
+    }
+    const int vh = share / kPerHead, kh = vh % Hk, j0 = (share % kPerHead) * kRows;
+    float *rows = p.state + ((static_cast<size_t>(slot) * H + vh) * S + j0 + warp * R) * S + E * lane;
+    const bool busy = warp * R < kRows;
+    float x[R][E];
+    if (busy) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) load_vec<E>(x[r], rows + r * S);
+    }
+    if (tid < N) g_of[tid] = p.g[(row0 + tid) * H + vh];
+    __syncthreads();
+    // weight[i]: the decay behind node walk[i]; weight[len]: of the whole path
+    if (tid <= len) {
+        float sum = 0.0f;
+        for (int i = len - 1; i > (tid == len ? -1 : tid); --i) sum += g_of[walk[i]];
+        weight[tid] = expf(sum);
+    }
+    __syncthreads();
+    const float all = weight[len];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[r][e] = busy ? x[r][e] * all : 0.0f;
+    for (int a = 0; a < len; a += kCommitNodes) {
+        const int count = min(kCommitNodes, len - a);
+        for (int y = tid; y < count * S; y += kCommitThreads)
+            ks[y / S][y % S] = p.k[((row0 + walk[a + y / S]) * Hk + kh) * S + y % S];
+        for (int y = tid; y < count * kRows; y += kCommitThreads)
+            us[y / kRows][y % kRows] = weight[a + y / kRows] * p.u[((row0 + walk[a + y / kRows]) * H + vh) * S + j0 + y % kRows];
+        __syncthreads();
+        if (busy) {
+            for (int y = 0; y < count; ++y) {
+                float kc[E], uc[R];
+                load_vec<E>(kc, &ks[y][E * lane]);
+                load_vec<R>(uc, &us[y][warp * R]);
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) x[r][e] = fmaf(kc[e], uc[r], x[r][e]);
+            }
+        }
+        __syncthreads();
+    }
+    if (busy) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) store_vec<E>(rows + r * S, x[r]);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+template <int E, int K>
+gdn_status launch_conv(const TreeParams &p, int n_seqs, cudaStream_t s) {
+    const int slices = 2 * p.n_k_heads + p.n_v_heads;
+    const dim3 grid((slices + kConvWarps - 1) / kConvWarps + 1, (p.n_nodes + kConvNodes - 1) / kConvNodes, n_seqs);
+    tree_conv_kernel<E, K><<<grid, 32 * kConvWarps, 0, s>>>(p);
+    return launch_status();
+}
+
+template <int E>
+gdn_status launch_block(const TreeParams &p, int n_seqs, int conv_kernel, cudaStream_t s) {
+    switch (conv_kernel) {
+        case 2: GDN_TRY((launch_conv<E, 2>(p, n_seqs, s))); break;
+        case 3: GDN_TRY((launch_conv<E, 3>(p, n_seqs, s))); break;
+        case 4: GDN_TRY((launch_conv<E, 4>(p, n_seqs, s))); break;
+        case 5: GDN_TRY((launch_conv<E, 5>(p, n_seqs, s))); break;
+        case 6: GDN_TRY((launch_conv<E, 6>(p, n_seqs, s))); break;
+        case 7: GDN_TRY((launch_conv<E, 7>(p, n_seqs, s))); break;
+        default: GDN_TRY((launch_conv<E, 8>(p, n_seqs, s))); break;
+    }
+    tree_gram_kernel<E><<<dim3(p.n_k_heads, n_seqs), 32 * kGramWarps, 0, s>>>(p);
+    GDN_TRY(launch_status());
+    using L = StateSmem<E>;
+    const size_t smem = L::bytes(p.n_nodes);
+    if (cudaFuncSetAttribute(tree_state_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem)) != cudaSuccess)
+        return GDN_ERR_LAUNCH;
+    tree_state_kernel<E><<<dim3(L::S / L::JB, p.n_v_heads, n_seqs), kStateThreads, smem, s>>>(p);
+    GDN_TRY(launch_status());
+    const long long rows = static_cast<long long>(n_seqs) * p.n_nodes * p.n_v_heads;
+    tree_norm_kernel<E><<<static_cast<unsigned>((rows + kNormThreads / 32 - 1) / (kNormThreads / 32)),
+                          kNormThreads, 0, s>>>(p, rows);
+    return launch_status();
+}
+
+template <int E>
+gdn_status launch_commit(const CommitParams &p, int n_seqs, cudaStream_t s) {
+    constexpr int S = 32 * E, kRows = S < kCommitRows ? S : kCommitRows;
+    const int state_shares = p.n_v_heads * (S / kRows);
+    const int shares = state_shares + (p.conv_dim + kCommitChannels - 1) / kCommitChannels;
+    tree_commit_kernel<E><<<dim3(shares, n_seqs), kCommitThreads, 0, s>>>(p, state_shares);
+    return launch_status();
+}
+
+// Sizes that both calls share. (The grids' y and z are 16-bit, rows of heads 32-bit.)
+gdn_status check_sizes(int n_seqs, int n_nodes, int n_k_heads, int n_v_heads, int state_size, int conv_kernel) {
+    if (conv_kernel < 2 || conv_kernel > 8) return GDN_ERR_SHAPE;
+    GDN_TRY(check_heads(n_k_heads, n_v_heads, state_size));
+    if (n_seqs > 65535 || n_v_heads > 65535 ||
+        static_cast<long long>(n_seqs) * n_nodes * n_v_heads > 0x7fffffffLL)
+        return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+
+bool valid_sizes(int n_seqs, int n_nodes, int n_k_heads, int n_v_heads, int state_size) {
+    return n_seqs >= 0 && n_nodes >= 1 && n_nodes <= kMaxNodes &&
+           check_heads(n_k_heads, n_v_heads, state_size) == GDN_OK;
+}
+
+}  // namespace
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+size_t gdn_block_tree_tape_size(int n_seqs, int n_nodes, int n_k_heads, int n_v_heads, int state_size) {
+    if (!valid_sizes(n_seqs, n_nodes, n_k_heads, n_v_heads, state_size)) return 0;
+    return Tape(static_cast<size_t>(n_seqs) * n_nodes, n_k_heads, n_v_heads, state_size).floats * sizeof(float);
+}
+
+size_t gdn_block_tree_workspace_size(int n_seqs, int n_nodes, int n_k_heads, int n_v_heads, int state_size) {
+    if (!valid_sizes(n_seqs, n_nodes, n_k_heads, n_v_heads, state_size)) return 0;
+    return Scratch(static_cast<size_t>(n_seqs) * n_nodes, n_nodes, n_k_heads, n_v_heads, state_size).floats * sizeof(float);
+}
+
+gdn_status gdn_block_tree(const float *qkv, const float *conv_w, const float *conv_state,
+                          const float *alpha, const float *b, const float *dt, const float *a,
+                          const float *z, const float *norm_w, const float *state, float *out,
+                          const int32_t *parents, int n_seqs, int n_nodes, int n_k_heads,
+                          int n_v_heads, int state_size, int conv_kernel, float scale, float l2_eps,
+                          float norm_eps, const int32_t *slots, int pool, int32_t *err_count,
+                          void *tape, size_t tape_bytes, void *workspace, size_t workspace_bytes,
+                          gdn_stream_t stream) {
+    if (!qkv || !conv_w || !conv_state || !alpha || !b || !dt || !a || !z || !norm_w || !state || !out)
+        return GDN_ERR_NULL;
+    GDN_TRY(check_tree(parents, n_seqs, n_nodes));
+    GDN_TRY(check_sizes(n_seqs, n_nodes, n_k_heads, n_v_heads, state_size, conv_kernel));
+    GDN_TRY(check_pool(n_seqs, slots, pool));
+    if (!aligned16(qkv) || !aligned16(conv_w) || !aligned16(conv_state) || !aligned16(state) ||
+        !aligned16(z) || !aligned16(out) || !aligned16(norm_w))
+        return GDN_ERR_ALIGN;
+    if (n_seqs == 0) return GDN_OK;
+    if (!tape || !workspace) return GDN_ERR_NULL;
+    if (!aligned16(tape) || !aligned16(workspace)) return GDN_ERR_ALIGN;
+    const size_t rows = static_cast<size_t>(n_seqs) * n_nodes;
+    const Tape T(rows, n_k_heads, n_v_heads, state_size);
+    const Scratch W(rows, n_nodes, n_k_heads, n_v_heads, state_size);
+    if (tape_bytes < T.floats * sizeof(float) || workspace_bytes < W.floats * sizeof(float))
+        return GDN_ERR_SHAPE;
+    float *t = static_cast<float *>(tape), *w = static_cast<float *>(workspace);
+    const TreeParams p{qkv, conv_w, conv_state, alpha, b, dt, a, z, norm_w, state, out, parents,
+                       slots, n_nodes, n_k_heads, n_v_heads, pool, scale, l2_eps, norm_eps,
+                       err_count, t + T.k, t + T.g, t + T.u, w + W.q, w + W.v, w + W.beta,
+                       w + W.gram, reinterpret_cast<int *>(w + W.there)};
+    const cudaStream_t s = as_cuda(stream);
+    switch (state_size) {
+        case 32: return launch_block<1>(p, n_seqs, conv_kernel, s);
+        case 64: return launch_block<2>(p, n_seqs, conv_kernel, s);
+        case 128: return launch_block<4>(p, n_seqs, conv_kernel, s);
+        default: return launch_block<8>(p, n_seqs, conv_kernel, s);
+    }
+}
+
+gdn_status gdn_block_tree_commit(const float *qkv, float *conv_state, float *state,
+                                 const int32_t *parents, const int32_t *accepted, int n_seqs,
+                                 int n_nodes, int n_k_heads, int n_v_heads, int state_size,
+                                 int conv_kernel, const int32_t *slots, int pool, int32_t *err_count,
+                                 const void *tape, size_t tape_bytes, gdn_stream_t stream) {
+    if (!qkv || !conv_state || !state || !accepted) return GDN_ERR_NULL;
+    GDN_TRY(check_tree(parents, n_seqs, n_nodes));
+    GDN_TRY(check_sizes(n_seqs, n_nodes, n_k_heads, n_v_heads, state_size, conv_kernel));
+    GDN_TRY(check_pool(n_seqs, slots, pool));
+    if (!aligned16(state)) return GDN_ERR_ALIGN;
+    if (n_seqs == 0) return GDN_OK;
+    if (!tape) return GDN_ERR_NULL;
+    if (!aligned16(tape)) return GDN_ERR_ALIGN;
+    const Tape T(static_cast<size_t>(n_seqs) * n_nodes, n_k_heads, n_v_heads, state_size);
+    if (tape_bytes < T.floats * sizeof(float)) return GDN_ERR_SHAPE;
+    const float *t = static_cast<const float *>(tape);
+    const CommitParams p{qkv, conv_state, state, parents, accepted, slots, n_nodes, n_k_heads,
+                         n_v_heads, (2 * n_k_heads + n_v_heads) * state_size, conv_kernel - 1, pool,
+                         err_count, t + T.k, t + T.g, t + T.u};
+    const cudaStream_t s = as_cuda(stream);
+    switch (state_size) {
+        case 32: return launch_commit<1>(p, n_seqs, s);
+        case 64: return launch_commit<2>(p, n_seqs, s);
+        case 128: return launch_commit<4>(p, n_seqs, s);
+        default: return launch_commit<8>(p, n_seqs, s);
+    }
+}
+
+}  // extern "C"

@@ -22,6 +22,10 @@ unsigned read_and_clear_watchdog_attn_prefill(cudaStream_t s);
 gdn_status launch_wait_probe_attn_decode(bool arm, uint64_t limit_ns, float *out, cudaStream_t s);
 gdn_status launch_wait_probe_attn_prefill(bool arm, uint64_t limit_ns, float *out, cudaStream_t s);
 
+// The decode attention's flag on the current device, which the attention of trees shares (NULL
+// when the device does not say).
+unsigned *watchdog_attn_decode();
+
 inline bool supported_dtype(int dtype) {
     return dtype == GDN_F32 || dtype == GDN_F16 || dtype == GDN_BF16;
 }

@@ -738,6 +738,121 @@ gdn_status gdn_pages_compact(void *pages, int32_t *page_table, const int32_t *kv
                              size_t page_bytes, int max_pages, int pool, int32_t *n_live,
                              void *workspace, size_t workspace_bytes, gdn_stream_t stream);
 
+/* ---------------------------------------------------------------- trees of drafts
+ * One step of speculative decoding with a tree of drafted tokens per sequence: the model reads
+ * all nodes at once (gdn_block_tree in its recurrent layers, gdn_kv_append and gdn_attn_tree in
+ * its attention layers), a token is sampled at every node (gdn_sample), the path along which the
+ * samples agree with the drafts is kept (gdn_tree_accept, then gdn_pages_truncate with its
+ * new_lens) and the recurrent states are carried on along it (gdn_block_tree_commit). The pages
+ * have no counterpart; these calls share the conventions above.
+ * - A tree has n_nodes nodes, at most GDN_MAX_TREE_NODES. parents: device int32
+ *   [n_seqs][n_nodes]; node i's parent is a node below i, or -1 where node i continues the
+ *   sequence itself (a root; node 0 is the certain token, the last one sampled), or GDN_NO_NODE
+ *   where a smaller tree is padded. Any other value, or a parent that is not there, takes the
+ *   node and what hangs below it out, and counts the sequence once in err_count (of the calls
+ *   that read the whole tree: all but the commit).
+ * - Outputs at a node that is not there are zeros (0.0, not sums with zero weights: what its
+ *   inputs hold has no effect). */
+
+#define GDN_MAX_TREE_NODES 64
+#define GDN_NO_NODE (-2)
+
+/* Attention of a tree's nodes over the paged cache, as gdn_attn_decode is of a chain's tokens
+ * (the keys of all nodes appended first: kv_len counts n_nodes new rows, node i's in row
+ * base + i, base = kv_len - n_nodes). Node i's position is base + its depth; it sees what lies
+ * before base as a token at that position does (window, sinks), and of the tree itself and its
+ * ancestors (inside the window of their positions, or among the sinks). A sequence whose kv_len
+ * is below n_nodes is skipped and counted. A chain (parents -1, 0, 1, ...) gets
+ * gdn_attn_decode's results up to rounding.
+ * q, out [n_seqs][n_nodes][n_q_heads][head_dim]; other arguments, types and errors as
+ * gdn_attn_decode. With 16-bit types and more than 16 rows of (node, head of a key head) the
+ * weights are held as in the prompt attention.
+ * workspace: gdn_attn_tree_workspace_size() bytes, otherwise as for gdn_attn_decode. */
+size_t gdn_attn_tree_workspace_size(int n_seqs, int n_nodes, int n_q_heads, int n_kv_heads,
+                                    int head_dim);
+gdn_status gdn_attn_tree(const void *q, const void *k_pages, const void *v_pages,
+                         const int32_t *page_table, const int32_t *kv_lens, void *out,
+                         const int32_t *parents, int n_seqs, int n_nodes, int n_q_heads,
+                         int n_kv_heads, int head_dim, int page_size, int n_pages, int max_pages,
+                         int window, int n_sinks, float scale, int q_stride, int dtype,
+                         const int32_t *slots, int pool, int32_t *err_count, void *workspace,
+                         size_t workspace_bytes, gdn_stream_t stream);
+
+/* The whole block over a tree's nodes, each continuing its parent's state and conv history:
+ * gdn_block_prefill's steps along every path. Neither state nor conv_state is written: what an
+ * accepted path changes them by is kept on the tape, from which gdn_block_tree_commit carries
+ * them on. (A snapshot per node, as gdn_block_prefill_snapshots keeps for a chain, would be
+ * n_nodes states of every sequence and layer.)
+ * qkv [n_seqs][n_nodes][C], alpha, b [n_seqs][n_nodes][H], z, out [n_seqs][n_nodes][H][S]; the
+ * other arguments as for gdn_block_prefill (any K in [2, 8]).
+ * tape: gdn_block_tree_tape_size() bytes, written; one per layer, kept until the commit.
+ * workspace: gdn_block_tree_workspace_size() bytes, contents on entry irrelevant and garbage
+ * afterwards; layers may share it. Both 16-byte aligned, 0 bytes for invalid sizes. */
+size_t gdn_block_tree_tape_size(int n_seqs, int n_nodes, int n_k_heads, int n_v_heads,
+                                int state_size);
+size_t gdn_block_tree_workspace_size(int n_seqs, int n_nodes, int n_k_heads, int n_v_heads,
+                                     int state_size);
+gdn_status gdn_block_tree(const float *qkv, const float *conv_w, const float *conv_state,
+                          const float *alpha, const float *b, const float *dt, const float *a,
+                          const float *z, const float *norm_w, const float *state, float *out,
+                          const int32_t *parents, int n_seqs, int n_nodes, int n_k_heads,
+                          int n_v_heads, int state_size, int conv_kernel, float scale, float l2_eps,
+                          float norm_eps, const int32_t *slots, int pool, int32_t *err_count,
+                          void *tape, size_t tape_bytes, void *workspace, size_t workspace_bytes,
+                          gdn_stream_t stream);
+
+/* States and conv histories carried on along the accepted paths of the trees that the tape is
+ * of: accepted[n] (device int32) is the path's last node + 1, as gdn_tree_accept gives it; 0
+ * leaves the sequence as it is. qkv, parents, sizes and slots as in the gdn_block_tree call;
+ * state and conv_state in place. A sequence whose slot or accepted node is out of range, or not
+ * there, is left untouched and counted. */
+gdn_status gdn_block_tree_commit(const float *qkv, float *conv_state, float *state,
+                                 const int32_t *parents, const int32_t *accepted, int n_seqs,
+                                 int n_nodes, int n_k_heads, int n_v_heads, int state_size,
+                                 int conv_kernel, const int32_t *slots, int pool, int32_t *err_count,
+                                 const void *tape, size_t tape_bytes, gdn_stream_t stream);
+
+/* Acceptance: from node 0 on, the child (the lowest, if several) whose drafted token is the one
+ * sampled at its parent. tokens, sampled: device int32 [n_seqs][n_nodes]. Of every sequence:
+ * accepted: the path's last node + 1; n_kept: the path's length; next_tokens: the token sampled
+ * at its last node; path [n_seqs][n_nodes] (may be NULL): its nodes, then -1; new_lens: kv_len
+ * - n_nodes + n_kept, what gdn_pages_truncate takes. A sequence without a node 0 keeps nothing
+ * (accepted and n_kept 0, next token -1); one whose slot or length is out of range, or whose
+ * length is below n_nodes, also does and is counted (new_lens: its length, 0 without a slot).
+ * The rows of the path's nodes move together behind the cache's first kv_len - n_nodes, in every
+ * plane of `pages` ([n_planes][n_pages][n_kv_heads][page_size][row], page_bytes a multiple of
+ * n_kv_heads * page_size * 16; pages as for gdn_pages_reserve, which has made those the rows lie
+ * in the sequence's own). A row whose page id is out of range does not move and is counted.
+ * Without pages (n_planes 0) nothing moves; kv_lens and new_lens may then both be NULL. */
+gdn_status gdn_tree_accept(const int32_t *parents, const int32_t *tokens, const int32_t *sampled,
+                           int32_t *accepted, int32_t *n_kept, int32_t *new_lens,
+                           int32_t *next_tokens, int32_t *path, int n_seqs, int n_nodes,
+                           void *pages, const int32_t *page_table, const int32_t *kv_lens,
+                           int n_kv_heads, int page_size, int n_planes, int n_pages,
+                           size_t page_bytes, int max_pages, const int32_t *slots, int pool,
+                           int32_t *err_count, gdn_stream_t stream);
+
+/* A token for every row of logits [rows][vocab] (of dtype, rows row_stride elements apart, any
+ * alignment of the type), from one uniform number in [0, 1) per row: uniforms [rows], device
+ * fp32 (what lies outside is taken for the nearest inside, NaN for 0).
+ *   z_i = x_i / temperature; in the order of the logits, largest first and the lower index first
+ *   among equals, these are kept: the first top_k; of those, the fewest whose weights e^{z_i} add
+ *   up to top_p of theirs; and those of at least min_p of the largest weight (the first always).
+ *   tokens[r] = the first index whose running sum of the kept weights, in index order, exceeds
+ *   uniforms[r] times their sum.
+ * temperature, top_k, top_p, min_p: device arrays of one value per set of rows_per_set
+ * consecutive rows (e.g. a tree's nodes), or NULL: 1, and no filter. Temperature 0 takes the
+ * largest logit; top_k <= 0 or >= vocab, top_p >= 1 and min_p <= 0 filter nothing. NaN logits count
+ * as -infinity, which is never taken; +infinity leaves only the +infinities. A row without a logit
+ * above -infinity gets token -1; so does one whose temperature is negative or not finite, or
+ * whose top_p or min_p is NaN, which is counted in err_count. Weights are held to 2^-43 of the
+ * largest, so that tokens do not depend on the order of sums. vocab: at most 2^20, and what
+ * eight SMs' shared memory holds (some 390,000 of fp32), else GDN_ERR_UNSUPPORTED. */
+gdn_status gdn_sample(const void *logits, const float *uniforms, const float *temperature,
+                      const int32_t *top_k, const float *top_p, const float *min_p,
+                      int32_t *tokens, int rows, int vocab, int row_stride, int dtype,
+                      int rows_per_set, int32_t *err_count, gdn_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
