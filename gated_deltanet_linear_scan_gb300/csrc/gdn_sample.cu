@@ -153,9 +153,9 @@ struct Weigher {
         float r = __fadd_rn(__fmaf_rn(p.x, b, __fmaf_rn(p.x, q, -v)), __fmaf_rn(p.y, q, p.y));
         const float s = __fadd_rn(p.x, v);
         r = __fadd_rn(r, __fsub_rn(v, __fsub_rn(s, p.x)));
-        // in units of 2^-44: s is 24 bits of at least 2^-24
+        // in units of 2^-44: s is a multiple of 2^-24, and r (up to 2^-18) its own 24 bits
         const unsigned big = __float2uint_rz(s * 16777216.0f);
-        const int small = __float_as_int(__fmaf_rn(r, 17592186044416.0f, kMagic)) - __float_as_int(kMagic);
+        const int small = __float2int_rn(r * 17592186044416.0f);
         const u64 w = (static_cast<u64>(big) << 20) + static_cast<long long>(small);
         const int down = 1 - (n >> 8);
         return x == top ? 1ull << 43 : t > -44.0f && down < 64 ? w >> down : 0ull;

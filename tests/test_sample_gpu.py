@@ -212,6 +212,25 @@ def test_shares_are_the_weights(cuda_lib):
     assert np.abs(got - n * w / w.sum()).max() <= 1.0
 
 
+@pytest.mark.parametrize("dtype,temperature,top_p", [("float32", 1.3, 1.0), ("float32", 0.7, 0.97), ("bfloat16", 1.0, 1.0)])
+def test_many_numbers_over_a_flat_row(cuda_lib, dtype, temperature, top_p):
+    """Thousands of uniform numbers over one row whose tokens are all unlikely, so that errors of some
+    10^-7 in the weights or their sum would show."""
+    rng = np.random.default_rng(10)
+    n, vocab = 4000, 50021
+    t = typed(1.5 * rng.standard_normal(vocab), dtype)
+    u = rng.random(n).astype(np.float32)
+    got = sample(cuda_lib, t.cuda().repeat(n, 1), u, temperature=[temperature] * n, top_p=[top_p] * n)
+    x = t.double().numpy()
+    w = np.exp((x - x.max()) / np.float64(np.float32(temperature)))
+    order = np.argsort(-x, kind="stable")
+    before = np.cumsum(w[order]) - w[order]
+    kept = np.zeros(vocab, bool)
+    kept[order] = before < np.float64(np.float32(top_p)) * w.sum() if top_p < 1 else True
+    cdf = np.cumsum(np.where(kept, w, 0.0))
+    assert got == np.searchsorted(cdf, u.astype(np.float64) * cdf[-1], side="right").tolist()
+
+
 def test_captured_and_replayed_and_on_two_streams(cuda_lib):
     rng = np.random.default_rng(9)
     rows, vocab = 20, 20011
