@@ -11,10 +11,12 @@
 // uniform number within 10^-11 of it. (With weights of 24 bits, one row in some hundred of a
 // vocabulary of 100,000 would come out another token.)
 //
-// A cluster of 1 to 8 CTAs takes a row; each keeps its slice of the logits in shared memory as it
-// was loaded, so a row is read from HBM once, and every pass after the first runs from there. A
-// threshold is found by its key's bits, 11, 11 and 10 of them at a time: a histogram of counts
-// (top-k) or weights (top-p) per CTA, read across the cluster.
+// A cluster of 1 to 8 CTAs takes a row, a warp a stretch of it. The first pass finds the largest logit;
+// later ones read the row again from L1 and L2 (rows in flight fit there). The border of top-k or
+// top-p is found by two histograms of counts or weights, read across the cluster: bins of 1/32 in the
+// weight's logarithm from the largest down, then 2048 parts of the bin that holds the border, whose
+// smallest and largest logit are nearly always one value. What that leaves open (a part with two
+// values, a border 64 powers of two below the largest) goes by the bits of the keys, 11, 11 and 10.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -30,6 +32,7 @@ constexpr int kBins = 2048;
 constexpr int kPow = 256;            // entries of the table of powers
 constexpr int kMaxVocab = 1 << 20;   // weights of 2^43 stay below 2^63 in a sum
 constexpr int kAll = 0x7fffffff;
+constexpr int kSMs = 152;
 
 typedef unsigned long long u64;
 typedef unsigned __int128 u128;
@@ -106,15 +109,17 @@ struct Part {
 struct __align__(16) Shared {
     float2 powers[kPow];
     unsigned lo[2][kBins], hi[2][kBins];  // histograms, two in turn
-    Part parts[kMaxCluster * kWarps];
+    unsigned least[kBins], most[kBins];   // keys of a part's smallest and largest logit (as ~key, key)
+    Part parts[kMaxCluster * kWarps], own[kWarps];
     float tops[kMaxCluster];
+    int firsts[kMaxCluster];
     u64 scan[kWarps];
-    u64 above;       // what lies above the threshold's bin
-    int bin;         // the bin that holds the threshold
+    u64 before;      // what lies before the border's bin
+    int bin;         // the bin that holds the border
     float warp_top[kWarps];
+    int warp_first[kWarps];
     double log_min;  // T ln(min_p)
 };
-static_assert(sizeof(Shared) % 16 == 0, "the logits behind it are read 16 bytes at a time");
 
 // A float's place in the order of floats, as an unsigned number (-0 is +0); and back.
 __device__ __forceinline__ unsigned key_of(float x) {
@@ -178,6 +183,21 @@ __device__ __forceinline__ u64 warp_scan64(u64 x) {
     return x;
 }
 
+__device__ __forceinline__ int warp_scan(int x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(FULL_MASK, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+
+template <int N>
+struct Const {
+    static constexpr int value = N;
+};
+
 __device__ __forceinline__ void cluster_sync() {
     __syncwarp();
     cluster_arrive_release();
@@ -206,11 +226,10 @@ __device__ __forceinline__ u64 times(float f, u64 x, bool up) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, int cluster) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p, int cluster) {
     constexpr int kVec = Logit<T>::kVec;
     extern __shared__ __align__(16) uint8_t dyn[];
     Shared &sh = *reinterpret_cast<Shared *>(dyn);
-    uint4 *data = reinterpret_cast<uint4 *>(dyn + sizeof(Shared));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = blockIdx.x % cluster;
     const long long row = blockIdx.x / cluster;
@@ -221,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
     const float top_p = p.top_p ? p.top_p[set] : 1.0f;
     const float min_p = p.min_p ? p.min_p[set] : 0.0f;
     const int top_k = p.top_k ? p.top_k[set] : 0;
-    float u = p.uniforms ? p.uniforms[row] : 0.0f;
+    float u = p.uniforms[row];
     u = u < 1.0f ? (u > 0.0f ? u : 0.0f) : u >= 1.0f ? 0.99999994f : 0.0f;
     const bool valid = temperature >= 0.0f && temperature < INFINITY && top_p == top_p && min_p == min_p;
     if (!valid) {
@@ -231,80 +250,108 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
         }
         return;  // the whole cluster
     }
+    const bool greedy = temperature == 0.0f || min_p > 1.0f || top_k == 1;
 
-    // ---- this CTA's slice, in 16-byte parts of the row's own alignment
+    // ---- this CTA's slice, in 16-byte parts of the row's own alignment, and this warp's stretch of it
     const T *logits = static_cast<const T *>(p.logits) + row * p.stride;
     const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(logits) & 15u) / sizeof(T));
     const uint4 *vecs = reinterpret_cast<const uint4 *>(logits - shift);
     const int n_vecs = (shift + p.vocab + kVec - 1) / kVec;
     const int per_cta = (n_vecs + cluster - 1) / cluster;
     const int per_warp = (per_cta + kThreads - 1) / kThreads * 32;
-    const int cta0 = rank * per_cta, cta1 = min(n_vecs, cta0 + per_cta);
-    const int v0 = cta0 + warp * per_warp, v1 = min(cta1, v0 + per_warp);  // this warp's
-    for (int x = tid; x < kPow; x += kThreads) sh.powers[x] = make_float2(kPowers.hi[x], kPowers.lo[x]);
-    for (int x = tid; x < kBins; x += kThreads) sh.lo[0][x] = sh.hi[0][x] = sh.lo[1][x] = sh.hi[1][x] = 0;
-    float top = -INFINITY;
-    {
-        constexpr int kAhead = 4;
-        for (int v = v0 + lane; v < v1; v += 32 * kAhead) {
+    const int cta1 = min(n_vecs, (rank + 1) * per_cta);
+    const int v0 = min(cta1, rank * per_cta + warp * per_warp), v1 = min(cta1, v0 + per_warp);
+    auto sync = [&] {
+        if (cluster > 1) cluster_sync();
+        else __syncthreads();
+    };
+    // 16 bytes of the row; at its ends, -infinity in place of what is not the row's
+    auto load = [&](int v) {
+        const int first = v * kVec - shift;
+        if (first >= 0 && first + kVec <= p.vocab) return vecs[v];
+        T x[kVec];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+            x[e] = first + e >= 0 && first + e < p.vocab ? logits[first + e] : Logit<T>::none();
+        uint4 raw;
+        memcpy(&raw, x, 16);
+        return raw;
+    };
+    // f(logits, index of the first): the lane's logits, 16 bytes at a time, NaN as -infinity; AHEAD
+    // of them are loaded together
+    auto each = [&](auto ahead, int from, int to, auto f) {
+        constexpr int kAhead = decltype(ahead)::value;
+#pragma unroll 1
+        for (int v = from + lane; v < to; v += 32 * kAhead) {
             uint4 raw[kAhead];
 #pragma unroll
-            for (int y = 0; y < kAhead; ++y) {
-                const int at = v + 32 * y;
-                if (at >= v1) continue;
-                const int first = at * kVec - shift;
-                if (first >= 0 && first + kVec <= p.vocab) {
-                    raw[y] = __ldcs(vecs + at);
-                } else {  // the row's ends: what is not the row's counts as -infinity
-                    T x[kVec];
-#pragma unroll
-                    for (int e = 0; e < kVec; ++e)
-                        x[e] = first + e >= 0 && first + e < p.vocab ? logits[first + e] : Logit<T>::none();
-                    memcpy(&raw[y], x, 16);
-                }
-            }
+            for (int y = 0; y < kAhead; ++y)
+                if (v + 32 * y < to) raw[y] = load(v + 32 * y);
 #pragma unroll
             for (int y = 0; y < kAhead; ++y) {
-                const int at = v + 32 * y;
-                if (at >= v1) continue;
-                data[at - cta0] = raw[y];
+                if (v + 32 * y >= to) break;
                 float x[kVec];
                 Logit<T>::unpack(raw[y], x);
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) top = fmaxf(top, x[e]);  // (passes over NaN)
+                for (int e = 0; e < kVec; ++e) x[e] = fmaxf(x[e], -INFINITY);
+                f(x, (v + 32 * y) * kVec - shift);
             }
-        }
-    }
-    // A thread only ever reads what it has stored itself: no barrier for the data.
-    // f(x, index): every logit of the lane's, in index order; NaN is -infinity.
-    auto each = [&](auto f) {
-        for (int v = v0 + lane; v < v1; v += 32) {
-            float x[kVec];
-            Logit<T>::unpack(data[v - cta0], x);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) f(fmaxf(x[e], -INFINITY));
         }
     };
 
-    // ---- the largest logit
+    // ---- the largest logit, and (for a row that takes it) the first index that has it
+    float top = -INFINITY;
+    int first = kAll;
+    if (greedy) {
+        each(Const<4>(), v0, v1, [&](const float (&x)[kVec], int at) {
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
-    if (lane == 0) sh.warp_top[warp] = top;
+            for (int e = 0; e < kVec; ++e)
+                if (x[e] > top) {
+                    top = x[e];
+                    first = at + e;
+                }
+        });
+    } else {
+        for (int x = tid; x < kPow; x += kThreads) sh.powers[x] = make_float2(kPowers.hi[x], kPowers.lo[x]);
+        for (int x = tid; x < kBins; x += kThreads)
+            sh.lo[0][x] = sh.hi[0][x] = sh.lo[1][x] = sh.hi[1][x] = sh.least[x] = sh.most[x] = 0;
+        each(Const<4>(), v0, v1, [&](const float (&x)[kVec], int) {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) top = fmaxf(top, x[e]);
+        });
+    }
+    auto larger = [&](float other, int other_first) {
+        if (other > top || (other == top && other_first < first)) {
+            top = other;
+            first = other_first;
+        }
+    };
+    __syncwarp();
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        const float other = __shfl_xor_sync(FULL_MASK, top, o);
+        const int other_first = __shfl_xor_sync(FULL_MASK, first, o);
+        larger(other, other_first);
+    }
+    if (lane == 0) {
+        sh.warp_top[warp] = top;
+        sh.warp_first[warp] = first;
+    }
     if (tid == kThreads - 1 && min_p > 0.0f && min_p <= 1.0f)  // (64-bit arithmetic is slow: one thread's business)
         sh.log_min = static_cast<double>(temperature) * log(static_cast<double>(min_p));
     __syncthreads();
-    if (warp == 0) {
-        top = sh.warp_top[lane % kWarps];
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
-        if (lane < cluster) *in_cta(&sh.tops[rank], lane) = top;
+    for (int w = 0; w < kWarps; ++w) larger(sh.warp_top[w], sh.warp_first[w]);
+    if (cluster > 1) {
+        if (tid < cluster) {
+            *in_cta(&sh.tops[rank], tid) = top;
+            *in_cta(&sh.firsts[rank], tid) = first;
+        }
+        cluster_sync();
+        for (int r = 0; r < cluster; ++r) larger(sh.tops[r], sh.firsts[r]);
     }
-    cluster_sync();
-    top = -INFINITY;
-    for (int r = 0; r < cluster; ++r) top = fmaxf(top, sh.tops[r]);
-    if (top == -INFINITY) {  // nothing to choose from
-        if (rank == 0 && tid == 0) p.tokens[row] = -1;
-        cluster_sync();  // (no CTA leaves while another may write to it)
+    if (greedy || top == -INFINITY) {
+        if (rank == 0 && tid == 0) p.tokens[row] = top == -INFINITY ? -1 : first;
+        if (cluster > 1) cluster_sync();  // (no CTA leaves while another may write to it)
         return;
     }
 
@@ -313,28 +360,39 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
     weight.powers = sh.powers;
     {
         // log2(e) / T: the quotient, and the remainder's
-        constexpr float kLog2EHi = 1.44269502162933349609f, kLog2ELo = 1.925963033500e-8f;
-        const float t = temperature > 0.0f ? temperature : 1.0f, c = kLog2EHi / t;
+        constexpr float kLog2EHi = 1.44269502162933349609f, kLog2ELo = 1.92596298909e-8f;
+        const float c = kLog2EHi / temperature;
         weight.c_hi = fminf(c, 3.0e38f);
-        weight.c_lo = c < 3.0e38f ? __fadd_rn(__fmaf_rn(-c, t, kLog2EHi), kLog2ELo) / t : 0.0f;
+        weight.c_lo = c < 3.0e38f ? __fadd_rn(__fmaf_rn(-c, temperature, kLog2EHi), kLog2ELo) / temperature : 0.0f;
     }
 
     // ---- what is kept: x > cut, and the first `ties` of those equal to it
     float cut = -INFINITY;
     int ties = 0;
-    int turn = 0;  // histogram in use
 
-    // Each warp's sum over what is kept, and its count of those equal to the cut, to every CTA.
-    auto gather_parts = [&] {
+    // Of vectors from .. to - 1, by a whole warp: the weights above the cut, and how many equal it.
+    auto part_of = [&](int from, int to) {
         Part mine{0, 0, 0};
-        each([&](float x) {
-            if (x > cut) mine.sum += weight(x);
-            else if (ties > 0 && x == cut) ++mine.equal;
+        each(Const<2>(), from, to, [&](const float (&x)[kVec], int) {
+            bool any = false;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                any |= x[e] > cut;
+                mine.equal += x[e] == cut;
+            }
+            if (!any) return;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) mine.sum += x[e] > cut ? weight(x[e]) : 0ull;
         });
+        __syncwarp();
         mine.sum = warp_sum64(mine.sum);
         mine.equal = __reduce_add_sync(FULL_MASK, mine.equal);
+        return mine;
+    };
+    auto gather_parts = [&] {
+        const Part mine = part_of(v0, v1);
         if (lane < cluster) *in_cta(&sh.parts[rank * kWarps + warp], lane) = mine;
-        cluster_sync();
+        sync();
     };
     auto total_of = [&](u64 w_cut) {
         u64 sum = 0;
@@ -343,177 +401,237 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
             sum += sh.parts[x].sum;
             equal += sh.parts[x].equal;
         }
+        __syncwarp();
         sum = warp_sum64(sum);
         equal = __reduce_add_sync(FULL_MASK, equal);
         return sum + static_cast<u64>(min(equal, ties)) * w_cut;
     };
 
-    // The cut at which `target` is reached from the top (a count, or a sum of weights), among what
-    // is kept so far: the new cut and its ties.
-    auto descend = [&](bool by_weight, u64 target) {
-        const float old_cut = cut;
-        const int old_ties = ties;
-        const u64 w_old = by_weight && old_ties > 0 ? weight(old_cut) : 0;
-        unsigned prefix = 0;
-        for (int pass = 0; pass < 3; ++pass) {
-            const int down = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-            unsigned *lo = sh.lo[turn], *hi = sh.hi[turn];
-            auto add = [&](unsigned bin, u64 w) {
-                const unsigned l = static_cast<unsigned>(w), old = atomicAdd(lo + bin, l);
-                const unsigned h = static_cast<unsigned>(w >> 32) + (old + l < old ? 1u : 0u);
-                if (h != 0) atomicAdd(hi + bin, h);
-            };
-            each([&](float x) {
-                const unsigned key = key_of(x);
-                if (!(x > old_cut) || (pass > 0 && (key >> (down + bits)) != prefix)) return;
-                const unsigned bin = (key >> down) & ((1u << bits) - 1);
-                if (by_weight) add(bin, weight(x));
-                else atomicAdd(lo + bin, 1u);
-            });
-            if (by_weight && old_ties > 0 && rank == 0 && tid == 0) {
-                // those equal to the cut so far, of which only old_ties are kept
-                const unsigned key = key_of(old_cut);
-                if (pass == 0 || (key >> (down + bits)) == prefix)
-                    add((key >> down) & ((1u << bits) - 1), w_old * static_cast<u64>(old_ties));
-            }
-            cluster_sync();
-            // bins from the top: a thread takes four, the highest first
-            u64 own[4], sum = 0;
-            {
-                const int first = kBins - 4 - 4 * tid;
-                uint4 l = make_uint4(0, 0, 0, 0), h = l;
-                u64 a[4] = {0, 0, 0, 0};
-                for (int r = 0; r < cluster; ++r) {
-                    l = *reinterpret_cast<const uint4 *>(in_cta(lo, r) + first);
-                    h = by_weight ? *reinterpret_cast<const uint4 *>(in_cta(hi, r) + first) : make_uint4(0, 0, 0, 0);
-                    a[0] += static_cast<u64>(h.w) << 32 | l.w;
-                    a[1] += static_cast<u64>(h.z) << 32 | l.z;
-                    a[2] += static_cast<u64>(h.y) << 32 | l.y;
-                    a[3] += static_cast<u64>(h.x) << 32 | l.x;
-                }
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    own[y] = a[y];
-                    sum += a[y];
-                }
-            }
-            u64 before = warp_scan64(sum);
-            if (lane == 31) sh.scan[warp] = before;
-            before -= sum;
-            __syncthreads();
-            for (int w = 0; w < warp; ++w) before += sh.scan[w];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                if (before < target && target <= before + own[y]) {
-                    sh.bin = kBins - 1 - (4 * tid + y);
-                    sh.above = before;
-                }
-                before += own[y];
-            }
-            // the other histogram is the next pass's: everyone has read it before this pass's barrier
-            for (int x = tid; x < kBins; x += kThreads) sh.lo[turn ^ 1][x] = sh.hi[turn ^ 1][x] = 0;
-            turn ^= 1;
-            __syncthreads();
-            target -= sh.above;
-            prefix = prefix << bits | static_cast<unsigned>(sh.bin);
-            __syncthreads();
+    // ---- histograms
+    auto add = [&](int turn, unsigned bin, u64 w) {
+        const unsigned l = static_cast<unsigned>(w), old = atomicAdd(&sh.lo[turn][bin], l);
+        const unsigned h = static_cast<unsigned>(w >> 32) + (old + l < old ? 1u : 0u);
+        if (h != 0) atomicAdd(&sh.hi[turn][bin], h);
+    };
+    // The bin in which the running sum over the cluster's histograms reaches `target` (from bin 0 up,
+    // or from the last down), and what lies before it; false if none does. Clears the other
+    // histogram, which everybody has read before the barrier ahead of this call.
+    auto find = [&](int turn, bool by_weight, u64 target, bool down) {
+        const int at = down ? kBins - 4 - 4 * tid : 4 * tid;
+        u64 own[4] = {0, 0, 0, 0};
+        for (int r = 0; r < cluster; ++r) {
+            const uint4 l = *reinterpret_cast<const uint4 *>(in_cta(sh.lo[turn], r) + at);
+            uint4 h = make_uint4(0, 0, 0, 0);
+            if (by_weight) h = *reinterpret_cast<const uint4 *>(in_cta(sh.hi[turn], r) + at);
+            own[0] += static_cast<u64>(h.x) << 32 | l.x;
+            own[1] += static_cast<u64>(h.y) << 32 | l.y;
+            own[2] += static_cast<u64>(h.z) << 32 | l.z;
+            own[3] += static_cast<u64>(h.w) << 32 | l.w;
         }
-        cut = value_of(prefix);
-        if (by_weight) {
-            const u64 w = weight(cut);
-            ties = static_cast<int>((target + w - 1) / w);
-        } else {
-            ties = static_cast<int>(min(target, static_cast<u64>(kAll)));
+        const u64 sum = own[0] + own[1] + own[2] + own[3];
+        u64 before = warp_scan64(sum);
+        if (lane == 31) sh.scan[warp] = before;
+        if (tid == 0) sh.bin = -1;
+        before -= sum;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) before += sh.scan[w];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const u64 mine = down ? own[3 - y] : own[y];
+            if (before < target && target <= before + mine) {
+                sh.bin = down ? at + 3 - y : at + y;
+                sh.before = before;
+            }
+            before += mine;
         }
+        for (int x = tid; x < kBins; x += kThreads) sh.lo[turn ^ 1][x] = sh.hi[turn ^ 1][x] = 0;
+        __syncthreads();
+        return sh.bin >= 0;
     };
 
-    if (temperature == 0.0f || min_p > 1.0f || top_k == 1) {
-        cut = top;
-        ties = 1;
-    } else {
-        if (top_k > 0 && top_k < p.vocab) {
-            // (rows with fewer logits above -infinity keep them all)
-            int there = 0;
-            each([&](float x) { there += x > -INFINITY; });
-            there = __reduce_add_sync(FULL_MASK, there);
-            Part mine{static_cast<u64>(there), 0, 0};
-            if (lane < cluster) *in_cta(&sh.parts[rank * kWarps + warp], lane) = mine;
-            cluster_sync();
-            const u64 all = total_of(0);
-            cluster_sync();  // the parts have been read
-            if (static_cast<u64>(top_k) < all) descend(false, top_k);
-        }
-        if (top_p < 1.0f) {
-            gather_parts();
-            const u64 total = total_of(ties > 0 ? weight(cut) : 0);
-            cluster_sync();
-            const u64 want = top_p > 0.0f ? times(top_p, total, true) : 0;
-            descend(true, want > 0 ? want : 1);
-        }
-        if (min_p > 0.0f) {
-            // w >= min_p: x >= top + T ln(min_p)
-            const float least = __double2float_ru(static_cast<double>(top) + sh.log_min);
-            if (least > cut) {
-                cut = least;
-                ties = kAll;
+    // The cut at which `target` (a count, or a sum of weights) is reached from the top, among what is
+    // kept so far: the new cut and its ties. (A count that is not reached: all are kept.)
+    auto descend = [&](bool by_weight, u64 target) {
+        const float old_cut = cut;
+        // those equal to the cut so far, of which only `ties` are kept: one thread adds them
+        const bool old = by_weight && ties > 0 && rank == 0 && tid == 0;
+        const u64 w_old = old ? weight(old_cut) * static_cast<u64>(ties) : 0;
+        const float scale = weight.c_hi * 32.0f;
+        // bin and place in it (both roundings leave the order of logits as it is)
+        auto place = [&](float x) { return x == top ? 0.0f : fminf((top - x) * scale, static_cast<float>(kBins)); };
+        auto settle = [&](u64 rest) {
+            if (by_weight) {
+                const u64 w = weight(cut);
+                ties = static_cast<int>((rest + w - 1) / w);
+            } else {
+                ties = static_cast<int>(rest);
             }
+        };
+        each(Const<2>(), v0, v1, [&](const float (&x)[kVec], int) {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                const float f = place(x[e]);
+                if (!(x[e] > old_cut) || f >= static_cast<float>(kBins)) continue;
+                if (by_weight) add(0, static_cast<unsigned>(f), weight(x[e]));
+                else atomicAdd(&sh.lo[0][static_cast<unsigned>(f)], 1u);
+            }
+        });
+        if (old && place(old_cut) < static_cast<float>(kBins)) add(0, static_cast<unsigned>(place(old_cut)), w_old);
+        sync();
+        if (find(0, by_weight, target, false)) {
+            const u64 rest = target - sh.before;
+            const float bin = static_cast<float>(sh.bin);
+            auto note = [&](float x, float f, u64 w) {
+                const unsigned part = static_cast<unsigned>((f - bin) * kBins), key = key_of(x);  // (f - bin is exact)
+                if (by_weight) add(1, part, w);
+                else atomicAdd(&sh.lo[1][part], 1u);
+                atomicMax(&sh.least[part], ~key);
+                atomicMax(&sh.most[part], key);
+            };
+            each(Const<2>(), v0, v1, [&](const float (&x)[kVec], int) {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    const float f = place(x[e]);
+                    if (x[e] > old_cut && f >= bin && f < bin + 1.0f) note(x[e], f, by_weight ? weight(x[e]) : 0ull);
+                }
+            });
+            if (old) {
+                const float f = place(old_cut);
+                if (f >= bin && f < bin + 1.0f) note(old_cut, f, w_old);
+            }
+            sync();
+            const int part = find(1, by_weight, rest, false) ? sh.bin : 0;  // (the bin holds the border)
+            unsigned least = 0, most = 0;
+            for (int r = 0; r < cluster; ++r) {
+                least = max(least, *(in_cta(sh.least, r) + part));
+                most = max(most, *(in_cta(sh.most, r) + part));
+            }
+            const u64 left = rest - sh.before;
+            sync();  // the parts' keys, and the second histogram, have been read
+            for (int x = tid; x < kBins; x += kThreads)
+                sh.lo[1][x] = sh.hi[1][x] = sh.least[x] = sh.most[x] = 0;
+            __syncthreads();
+            if (~least == most) {
+                cut = value_of(most);
+                settle(left);
+                return;
+            }
+        } else {
+            sync();
+            for (int x = tid; x < kBins; x += kThreads) sh.lo[0][x] = sh.hi[0][x] = 0;
+            __syncthreads();
+        }
+        // by the keys' bits
+        unsigned prefix = 0;
+        bool found = true;
+#pragma unroll 1
+        for (int pass = 0; pass < 3 && found; ++pass) {
+            const int down = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11, turn = pass & 1;
+            auto mine = [&](unsigned key) { return pass == 0 || (key >> (down + bits)) == prefix; };
+            each(Const<2>(), v0, v1, [&](const float (&x)[kVec], int) {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    const unsigned key = key_of(x[e]);
+                    if (!(x[e] > old_cut) || !mine(key)) continue;
+                    const unsigned bin = (key >> down) & ((1u << bits) - 1);
+                    if (by_weight) add(turn, bin, weight(x[e]));
+                    else atomicAdd(&sh.lo[turn][bin], 1u);
+                }
+            });
+            if (old && mine(key_of(old_cut))) add(turn, (key_of(old_cut) >> down) & ((1u << bits) - 1), w_old);
+            sync();
+            found = find(turn, by_weight, target, true);
+            if (found) {
+                target -= sh.before;
+                prefix = prefix << bits | static_cast<unsigned>(sh.bin);
+            }
+        }
+        if (found) {
+            cut = value_of(prefix);
+            settle(target);
+        }
+        sync();
+        for (int x = tid; x < kBins; x += kThreads) sh.lo[0][x] = sh.hi[0][x] = 0;
+        __syncthreads();
+    };
+
+    if (top_k > 0 && top_k < p.vocab) descend(false, top_k);
+    if (top_p < 1.0f) {
+        gather_parts();
+        const u64 total = total_of(ties > 0 ? weight(cut) : 0);
+        const u64 want = top_p > 0.0f ? times(top_p, total, true) : 0;
+        descend(true, want > 0 ? want : 1);  // (its barriers come before the parts are written again)
+    }
+    if (min_p > 0.0f) {
+        // w >= min_p: x >= top + T ln(min_p)
+        const float least = __double2float_ru(static_cast<double>(top) + sh.log_min);
+        if (least > cut) {
+            cut = least;
+            ties = kAll;
         }
     }
 
-    // ---- the token
+    // ---- the token: the stretch in which the running sum exceeds the target, then 1 / 16 of it, then
+    // 32 parts of 16 bytes at a time, then the lane's, then its logits
     gather_parts();
     const u64 w_cut = ties > 0 ? weight(cut) : 0;
     const u64 target = times(u, total_of(w_cut), false);
-    // the warp in whose part the running sum exceeds the target: every warp looks at its own
-    {
-        u64 before = 0;
-        int equal = 0;
-        for (int x = lane; x < rank * kWarps + warp; x += 32) {
-            before += sh.parts[x].sum;
-            equal += sh.parts[x].equal;
+    u64 run = 0;   // weights above the cut before the stretch
+    int seen = 0;  // logits equal to it
+    auto upto = [&](u64 sum, int equal) { return sum + static_cast<u64>(min(equal, ties)) * w_cut; };
+    // which of `count` parts it is (by a whole warp); run and seen move on to it
+    auto pick = [&](const Part *parts, int count) {
+        for (int x0 = 0;; x0 += 32) {
+            Part mine{0, 0, 0};
+            if (x0 + lane < count) mine = parts[x0 + lane];
+            __syncwarp();
+            const u64 sums = warp_scan64(mine.sum);
+            const int equals = warp_scan(mine.equal);
+            const unsigned past = __ballot_sync(FULL_MASK, upto(run + sums, seen + equals) > target);
+            const int at = past != 0 ? __ffs(past) - 1 : 31;
+            run += __shfl_sync(FULL_MASK, past != 0 ? sums - mine.sum : sums, at);
+            seen += __shfl_sync(FULL_MASK, past != 0 ? equals - mine.equal : equals, at);
+            if (past != 0 || x0 + 32 >= count) return x0 + at;
         }
-        before = warp_sum64(before);
-        equal = __reduce_add_sync(FULL_MASK, equal);
-        const Part mine = sh.parts[rank * kWarps + warp];
-        const u64 from = before + static_cast<u64>(min(equal, ties)) * w_cut;
-        const u64 to = before + mine.sum + static_cast<u64>(min(equal + mine.equal, ties)) * w_cut;
-        if (from <= target && target < to) {
-            // 32 parts of 16 bytes at a time, then the lane's, then its logits
-            u64 run = before;
-            int seen = equal;
-            for (int v = v0; v < v1; v += 32) {
+    };
+    const int stretch = pick(sh.parts, cluster * kWarps);
+    if (stretch / kWarps == rank) {
+        const int begin = min(cta1, rank * per_cta + stretch % kWarps * per_warp), end = min(cta1, begin + per_warp);
+        const int each_warp = (end - begin + kThreads - 1) / kThreads * 32;
+        const int a = min(end, begin + warp * each_warp);
+        const Part mine = part_of(a, min(end, a + each_warp));
+        if (lane == 0) sh.own[warp] = mine;
+        __syncthreads();
+        if (warp == 0) {
+            const int from = begin + pick(sh.own, kWarps) * each_warp, to = min(end, from + each_warp);
+            for (int v = from; v < to; v += 32) {
                 float x[kVec];
                 u64 sum = 0;
                 int same = 0;
-                if (v + lane < v1) {
-                    Logit<T>::unpack(data[v + lane - cta0], x);
+                if (v + lane < to) {
+                    Logit<T>::unpack(load(v + lane), x);
 #pragma unroll
                     for (int e = 0; e < kVec; ++e) {
                         if (x[e] > cut) sum += weight(x[e]);
-                        else if (ties > 0 && x[e] == cut) ++same;
+                        else if (x[e] == cut) ++same;
                     }
                 }
+                __syncwarp();
                 const u64 sums = warp_scan64(sum);
-                int sames = same;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(FULL_MASK, sames, o);
-                    if (lane >= o) sames += y;
-                }
-                const u64 here = run + sums + static_cast<u64>(min(seen + sames, ties)) * w_cut;
-                const unsigned past = __ballot_sync(FULL_MASK, here > target);
+                const int sames = warp_scan(same);
+                const unsigned past = __ballot_sync(FULL_MASK, upto(run + sums, seen + sames) > target);
                 if (past != 0) {
                     if (lane == __ffs(past) - 1) {
                         u64 s = run + sums - sum;
                         int q = seen + sames - same;
-#pragma unroll 1
+                        bool done = false;
+#pragma unroll
                         for (int e = 0; e < kVec; ++e) {
-                            const float y = static_cast<float>(reinterpret_cast<const T *>(data + (v + lane - cta0))[e]);
-                            if (y > cut) s += weight(y);
-                            else if (ties > 0 && y == cut) ++q;
-                            if (s + static_cast<u64>(min(q, ties)) * w_cut > target) {
+                            if (x[e] > cut) s += weight(x[e]);
+                            else if (x[e] == cut) ++q;
+                            if (!done && upto(s, q) > target) {
                                 p.tokens[row] = (v + lane) * kVec + e - shift;
-                                break;
+                                done = true;
                             }
                         }
                     }
@@ -524,27 +642,22 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
             }
         }
     }
-    cluster_sync();  // no CTA leaves while another may read or write its shared memory
+    if (cluster > 1) cluster_sync();  // no CTA leaves while another may read or write its shared memory
 }
 
+// CTAs of a row: as many as give every SM its two, of at least 2048 logits each.
 template <typename T>
 gdn_status launch(const SampleParams &p, int rows, cudaStream_t s) {
-    constexpr int kVec = Logit<T>::kVec;
-    const long long vecs = (static_cast<long long>(p.vocab) + 2 * kVec - 2) / kVec;
-    auto bytes_of = [&](int cluster) { return sizeof(Shared) + static_cast<size_t>((vecs + cluster - 1) / cluster) * 16; };
-    constexpr size_t kMost = 232448;
-    int cluster = rows <= 64 ? 8 : 4;
-    while (cluster < kMaxCluster && bytes_of(cluster) > kMost) cluster *= 2;
-    while (cluster > 1 && vecs / cluster < 256) cluster /= 2;
-    const size_t smem = bytes_of(cluster);
-    if (smem > kMost || static_cast<long long>(rows) * cluster > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+    int cluster = kMaxCluster;
+    while (cluster > 1 && (static_cast<long long>(rows) * cluster > 2 * kSMs || p.vocab / cluster < 2048)) cluster /= 2;
+    if (static_cast<long long>(rows) * cluster > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
     auto kernel = sample_kernel<T>;
     static std::atomic<unsigned long long> allowed{0};
-    GDN_TRY(allow_smem(kernel, static_cast<int>(kMost), allowed));
+    GDN_TRY(allow_smem(kernel, static_cast<int>(sizeof(Shared)), allowed));
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(rows) * cluster);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = s;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;

@@ -846,8 +846,8 @@ gdn_status gdn_tree_accept(const int32_t *parents, const int32_t *tokens, const 
  * as -infinity, which is never taken; +infinity leaves only the +infinities. A row without a logit
  * above -infinity gets token -1; so does one whose temperature is negative or not finite, or
  * whose top_p or min_p is NaN, which is counted in err_count. Weights are held to 2^-43 of the
- * largest, so that tokens do not depend on the order of sums. vocab: at most 2^20, and what
- * eight SMs' shared memory holds (some 390,000 of fp32), else GDN_ERR_UNSUPPORTED. */
+ * largest, so that tokens do not depend on the order of sums. vocab: at most 2^20, else
+ * GDN_ERR_UNSUPPORTED. */
 gdn_status gdn_sample(const void *logits, const float *uniforms, const float *temperature,
                       const int32_t *top_k, const float *top_p, const float *min_p,
                       int32_t *tokens, int rows, int vocab, int row_stride, int dtype,
