@@ -12,11 +12,13 @@
 // vocabulary of 100,000 would come out another token.)
 //
 // A cluster of 1 to 8 CTAs takes a row, a warp a stretch of it. The first pass finds the largest logit;
-// later ones read the row again from L1 and L2 (rows in flight fit there). The border of top-k or
-// top-p is found by two histograms of counts or weights, read across the cluster: bins of 1/32 in the
-// weight's logarithm from the largest down, then 2048 parts of the bin that holds the border, whose
-// smallest and largest logit are nearly always one value. What that leaves open (a part with two
-// values, a border 64 powers of two below the largest) goes by the bits of the keys, 11, 11 and 10.
+// later ones read the row again from L1 and L2 (rows in flight fit there). Most tokens of a row are
+// so unlikely that one exponential in fp32 gives their weight to 2^-43 of the largest; the others
+// wait in a queue of the warp's until there are 32 of them. The border of top-k or top-p is found by
+// two histograms of counts or weights, read across the cluster: bins of 1/32 in the weight's logarithm
+// from the largest down, then 2048 parts of the bin that holds the border, whose smallest and largest
+// logit are nearly always one value. What that leaves open (a part with two values, a border 64 powers
+// of two below the largest) goes by the bits of the keys, 11, 11 and 10.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -53,41 +55,29 @@ struct PowTable {
         }
     }
 };
-__constant__ PowTable kPowers = PowTable();
+__device__ const PowTable kPowers = PowTable();  // (constant memory would serve one entry at a time)
 
+__device__ __forceinline__ float logit(float x) { return x; }
+__device__ __forceinline__ float logit(__half x) { return __half2float(x); }
+__device__ __forceinline__ float logit(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// 16 bytes of logits, NaN as -infinity.
 template <typename T>
-struct Logit;
-template <>
-struct Logit<float> {
-    static constexpr int kVec = 4;
-    static __device__ __forceinline__ float none() { return -INFINITY; }
-    static __device__ __forceinline__ void unpack(const uint4 &v, float (&x)[4]) {
-        x[0] = __uint_as_float(v.x);
-        x[1] = __uint_as_float(v.y);
-        x[2] = __uint_as_float(v.z);
-        x[3] = __uint_as_float(v.w);
-    }
-};
-template <typename T>
-struct Logit16 {
-    static constexpr int kVec = 8;
-    static __device__ __forceinline__ void unpack(const uint4 &v, float (&x)[8]) {
+struct Vec {
+    static constexpr int kSize = 16 / static_cast<int>(sizeof(T));
+    static __device__ __forceinline__ void unpack(const uint4 &v, float (&x)[kSize]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 f = Elem<T>::unpack(w[i]);
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
+            if constexpr (sizeof(T) == 4) {
+                x[i] = fmaxf(__uint_as_float(w[i]), -INFINITY);
+            } else {
+                const float2 f = Elem<T>::unpack(w[i]);
+                x[2 * i] = fmaxf(f.x, -INFINITY);
+                x[2 * i + 1] = fmaxf(f.y, -INFINITY);
+            }
         }
     }
-};
-template <>
-struct Logit<__nv_bfloat16> : Logit16<__nv_bfloat16> {
-    static __device__ __forceinline__ __nv_bfloat16 none() { return __ushort_as_bfloat16(0xFF80u); }
-};
-template <>
-struct Logit<__half> : Logit16<__half> {
-    static __device__ __forceinline__ __half none() { return __ushort_as_half(0xFC00u); }
 };
 
 struct SampleParams {
@@ -111,6 +101,7 @@ struct __align__(16) Shared {
     unsigned lo[2][kBins], hi[2][kBins];  // histograms, two in turn
     unsigned least[kBins], most[kBins];   // keys of a part's smallest and largest logit (as ~key, key)
     Part parts[kMaxCluster * kWarps], own[kWarps];
+    float queue[kWarps][64];
     float tops[kMaxCluster];
     int firsts[kMaxCluster];
     u64 scan[kWarps];
@@ -130,42 +121,54 @@ __device__ __forceinline__ float value_of(unsigned key) {
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
-// 2^43 e^{(x - top) / T}, rounded down: t = (x - top) log2(e) / T in two floats, 2^t from the table
-// and a polynomial. c_hi + c_lo is log2(e) / T.
+// Weights: 2^43 e^{(x - top) / T}. c_hi + c_lo is log2(e) / T; above `likely` the weight is more than
+// 2^-24 of the largest.
 struct Weigher {
-    float top, c_hi, c_lo;
-    const float2 *powers;
-
-    __device__ __forceinline__ u64 operator()(float x) const {
-        constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it leaves the nearest integer
-        constexpr float kLn2 = 0.693147182464599609375f, kLn2Lo = -1.90465429995776e-9f;
-        constexpr float kC2 = 0.2402265069591007f, kC3 = 0.05550410866482158f, kC4 = 0.009618129107628477f;
-        // d + dl = x - top, exactly
-        const float d = __fsub_rn(x, top), back = __fsub_rn(d, x);
-        const float dl = __fsub_rn(__fsub_rn(x, __fsub_rn(d, back)), __fadd_rn(top, back));
-        const float t = __fmul_rn(d, c_hi);
-        const float tl = __fmaf_rn(d, c_lo, __fmaf_rn(dl, c_hi, __fmaf_rn(d, c_hi, -t)));
-        const float y = __fmaf_rn(t, static_cast<float>(kPow), kMagic);
-        const int n = __float_as_int(y) - __float_as_int(kMagic);
-        const float f = __fmaf_rn(__fsub_rn(y, kMagic), -1.0f / kPow, t);
-        const float2 p = powers[n & (kPow - 1)];
-        // 2^{f + tl} = 1 + q + b
-        const float q = __fmul_rn(f, kLn2), g = __fadd_rn(f, tl);
-        float b = __fmaf_rn(tl, kLn2, __fmaf_rn(f, kLn2Lo, __fmaf_rn(f, kLn2, -q)));
-        b = __fmaf_rn(__fmul_rn(g, g), __fmaf_rn(g, __fmaf_rn(g, kC4, kC3), kC2), b);
-        // (p.x + p.y) (1 + q + b) = s + r
-        const float v = __fmul_rn(p.x, q);
-        float r = __fadd_rn(__fmaf_rn(p.x, b, __fmaf_rn(p.x, q, -v)), __fmaf_rn(p.y, q, p.y));
-        const float s = __fadd_rn(p.x, v);
-        r = __fadd_rn(r, __fsub_rn(v, __fsub_rn(s, p.x)));
-        // in units of 2^-44: s is a multiple of 2^-24, and r (up to 2^-18) its own 24 bits
-        const unsigned big = __float2uint_rz(s * 16777216.0f);
-        const int small = __float2int_rn(r * 17592186044416.0f);
-        const u64 w = (static_cast<u64>(big) << 20) + static_cast<long long>(small);
-        const int down = 1 - (n >> 8);
-        return x == top ? 1ull << 43 : t > -44.0f && down < 64 ? w >> down : 0ull;
-    }
+    float top, c_hi, c_lo, likely;
 };
+
+// The weight of a likely token: t = (x - top) log2(e) / T in two floats, 2^t from the table and a
+// polynomial, to 2^-44.
+__device__ __noinline__ u64 precise_weight(const Weigher w, float x) {
+    extern __shared__ __align__(16) uint8_t dyn[];
+    const float2 *powers = reinterpret_cast<const Shared *>(dyn)->powers;
+    constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it leaves the nearest integer
+    constexpr float kLn2 = 0.693147182464599609375f, kLn2Lo = -1.90465429995776e-9f;
+    constexpr float kC2 = 0.2402265069591007f, kC3 = 0.05550410866482158f, kC4 = 0.009618129107628477f;
+    // d + dl = x - top, exactly
+    const float d = __fsub_rn(x, w.top), back = __fsub_rn(d, x);
+    const float dl = __fsub_rn(__fsub_rn(x, __fsub_rn(d, back)), __fadd_rn(w.top, back));
+    const float t = __fmul_rn(d, w.c_hi);
+    const float tl = __fmaf_rn(d, w.c_lo, __fmaf_rn(dl, w.c_hi, __fmaf_rn(d, w.c_hi, -t)));
+    const float y = __fmaf_rn(t, static_cast<float>(kPow), kMagic);
+    const int n = __float_as_int(y) - __float_as_int(kMagic);
+    const float f = __fmaf_rn(__fsub_rn(y, kMagic), -1.0f / kPow, t);
+    const float2 p = powers[n & (kPow - 1)];
+    // 2^{f + tl} = 1 + q + b
+    const float q = __fmul_rn(f, kLn2), g = __fadd_rn(f, tl);
+    float b = __fmaf_rn(tl, kLn2, __fmaf_rn(f, kLn2Lo, __fmaf_rn(f, kLn2, -q)));
+    b = __fmaf_rn(__fmul_rn(g, g), __fmaf_rn(g, __fmaf_rn(g, kC4, kC3), kC2), b);
+    // (p.x + p.y) (1 + q + b) = s + r
+    const float v = __fmul_rn(p.x, q);
+    float r = __fadd_rn(__fmaf_rn(p.x, b, __fmaf_rn(p.x, q, -v)), __fmaf_rn(p.y, q, p.y));
+    const float s = __fadd_rn(p.x, v);
+    r = __fadd_rn(r, __fsub_rn(v, __fsub_rn(s, p.x)));
+    // in units of 2^-44: s is a multiple of 2^-24, and r (up to 2^-18) its own 24 bits
+    const unsigned big = __float2uint_rz(s * 16777216.0f);
+    const int small = __float2int_rn(r * 17592186044416.0f);
+    const u64 sum = (static_cast<u64>(big) << 20) + static_cast<long long>(small);
+    return x == w.top ? 1ull << 43 : sum >> (1 - (n >> 8));
+}
+
+// The weight of an unlikely one, below 2^19 and so the last bits of 2^23 more than it: fp32's 2^-20 of
+// it (its argument's rounding) is 2^-44 of the largest.
+constexpr unsigned kSmallBase = 0x4B000000u;  // 2^23
+__device__ __forceinline__ unsigned small_weight_bits(const Weigher &w, float x) {
+    return __float_as_uint(__fadd_rn(fast_exp2(__fmaf_rn(__fsub_rn(x, w.top), w.c_hi, 43.0f)), 8388608.0f));
+}
+__device__ __forceinline__ u64 weight_of(const Weigher &w, float x) {
+    return x > w.likely ? precise_weight(w, x) : small_weight_bits(w, x) - kSmallBase;
+}
 
 __device__ __forceinline__ u64 warp_sum64(u64 x) {
 #pragma unroll
@@ -225,9 +228,177 @@ __device__ __forceinline__ u64 times(float f, u64 x, bool up) {
     return static_cast<u64>(q) + (up && (q << down) != prod ? 1 : 0);
 }
 
+// Logits from .. to - 1 of a row, by a whole warp: f(x, index of the first), 16 bytes of them a lane
+// between the first and the last boundary of 16 and one a lane at the ends (-infinity where there is
+// none), the next loads ahead of this one's work.
+template <typename T, typename F>
+__device__ __forceinline__ void each_logit(const T *logits, int from, int to, F f) {
+    constexpr int kVec = Vec<T>::kSize, kAhead = 2;
+    const int lane = threadIdx.x & 31;
+    const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(logits + from) & 15u) / sizeof(T));
+    const int s0 = min(to, from + (shift ? kVec - shift : 0)), n = (to - s0) / kVec, s1 = s0 + n * kVec;
+    const uint4 *vecs = reinterpret_cast<const uint4 *>(logits + s0);
+    const uint4 none = [] {
+        const float x = -INFINITY;
+        const unsigned w = sizeof(T) == 4 ? __float_as_uint(x) : __is_same(T, __half) ? 0xFC00FC00u : 0xFF80FF80u;
+        return make_uint4(w, w, w, w);
+    }();
+    uint4 next[kAhead];
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) next[y] = lane + 32 * y < n ? vecs[lane + 32 * y] : none;
+    auto end = [&](int first, int last) {
+        const float x[1] = {first + lane < last ? fmaxf(logit(logits[first + lane]), -INFINITY) : -INFINITY};
+        f(x, first + lane);
+    };
+    if (from < s0) end(from, s0);
+#pragma unroll 1
+    for (int v = lane; v < n + lane; v += 32 * kAhead) {
+        uint4 raw[kAhead];
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+            raw[y] = next[y];
+            const int at = v + 32 * (kAhead + y);
+            next[y] = at < n ? vecs[at] : none;
+        }
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+            float x[kVec];
+            Vec<T>::unpack(raw[y], x);
+            f(x, s0 + (v + 32 * y) * kVec);
+        }
+    }
+    if (s1 < to) end(s1, to);
+}
+
+template <int N>
+__device__ __forceinline__ float top_of(const float (&x)[N]) {
+    float top = x[0];
+#pragma unroll
+    for (int e = 1; e < N; ++e) top = fmaxf(top, x[e]);
+    return top;
+}
+
+// Those of a warp's values that are picked, 32 at a time: f(x) for one a lane (all lanes but in
+// `finish`).
+struct Queue {
+    float *at;  // 64 floats of the warp's own
+    int count;
+    template <typename F>
+    __device__ __forceinline__ void push(bool picked, float x, F f) {
+        const int lane = threadIdx.x & 31;
+        const unsigned mask = __ballot_sync(FULL_MASK, picked);
+        if (mask == 0) return;
+        if (picked) at[count + __popc(mask & ((1u << lane) - 1))] = x;
+        count += __popc(mask);
+        if (count < 32) return;
+        __syncwarp();
+        const float mine = at[lane], rest = at[lane + 32];
+        count -= 32;
+        __syncwarp();
+        if (lane < count) at[lane] = rest;
+        f(mine);
+    }
+    template <typename F>
+    __device__ __forceinline__ void finish(F f) {
+        __syncwarp();
+        const int lane = threadIdx.x & 31;
+        if (lane < count) f(at[lane]);
+        __syncwarp();
+        count = 0;
+    }
+};
+
+// Of logits from .. to - 1, by a whole warp: the weights above the cut, and how many equal it.
+template <typename T>
+__device__ __noinline__ Part part_of(const T *logits, int from, int to, float cut, const Weigher w, float *room) {
+    Part mine{0, 0, 0};
+    Queue queue{room, 0};
+    auto add = [&](float x) { mine.sum += precise_weight(w, x); };
+    if (cut >= w.likely) {
+        // few are as large
+        each_logit(logits, from, to, [&](const auto &x, int) {
+            if (!__any_sync(FULL_MASK, top_of(x) >= cut)) return;
+#pragma unroll
+            for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(x[0])); ++e) {
+                mine.equal += x[e] == cut;
+                queue.push(x[e] > cut, x[e], add);
+            }
+        });
+    } else {
+        // (a lane's small weights add up to less than 2^32: at most 2^20 / 512 of them below 2^19)
+        unsigned small = 0;
+        each_logit(logits, from, to, [&](const auto &x, int) {
+            constexpr int N = static_cast<int>(sizeof(x) / sizeof(x[0]));
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const unsigned bits = small_weight_bits(w, x[e]) - kSmallBase;
+                small += x[e] > cut && !(x[e] > w.likely) ? bits : 0u;
+                mine.equal += x[e] == cut;
+            }
+            if (!__any_sync(FULL_MASK, top_of(x) > w.likely)) return;
+#pragma unroll
+            for (int e = 0; e < N; ++e) queue.push(x[e] > w.likely, x[e], add);
+        });
+        mine.sum += small;
+    }
+    queue.finish(add);
+    mine.sum = warp_sum64(mine.sum);
+    mine.equal = __reduce_add_sync(FULL_MASK, mine.equal);
+    return mine;
+}
+
+// The bin in which the running sum over the cluster's histograms (low words and, unless NULL, high
+// ones) reaches `target`, from bin 0 up or from the last down; what lies before it goes to sh.before;
+// -1 if none does. By the whole CTA. Clears histogram `clears` (and with the second the parts' keys),
+// which everybody has read before the barrier ahead of this call.
+__device__ __noinline__ int find_bin(unsigned *low, unsigned *high, int clears, u64 target, bool down, int cluster) {
+    extern __shared__ __align__(16) uint8_t dyn[];
+    Shared &sh = *reinterpret_cast<Shared *>(dyn);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int at = down ? kBins - 4 - 4 * tid : 4 * tid;
+    u64 own[4] = {0, 0, 0, 0};
+    for (int word = 0; word < (high ? 2 : 1); ++word) {
+        unsigned *const hist = word ? high : low;
+        for (int r0 = 0; r0 < cluster; r0 += 4) {  // four CTAs' at a time
+            uint4 x[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                x[y] = r0 + y < cluster ? *reinterpret_cast<const uint4 *>(in_cta(hist, r0 + y) + at) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                own[0] += static_cast<u64>(x[y].x) << (32 * word);
+                own[1] += static_cast<u64>(x[y].y) << (32 * word);
+                own[2] += static_cast<u64>(x[y].z) << (32 * word);
+                own[3] += static_cast<u64>(x[y].w) << (32 * word);
+            }
+        }
+    }
+    const u64 sum = own[0] + own[1] + own[2] + own[3];
+    u64 before = warp_scan64(sum);
+    if (lane == 31) sh.scan[warp] = before;
+    if (tid == 0) sh.bin = -1;
+    before -= sum;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) before += sh.scan[w];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        const u64 mine = down ? own[3 - y] : own[y];
+        if (before < target && target <= before + mine) {
+            sh.bin = down ? at + 3 - y : at + y;
+            sh.before = before;
+        }
+        before += mine;
+    }
+    for (int x = tid; x < kBins; x += kThreads) {
+        sh.lo[clears][x] = sh.hi[clears][x] = 0;
+        if (clears == 1) sh.least[x] = sh.most[x] = 0;
+    }
+    __syncthreads();
+    return sh.bin;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p, int cluster) {
-    constexpr int kVec = Logit<T>::kVec;
     extern __shared__ __align__(16) uint8_t dyn[];
     Shared &sh = *reinterpret_cast<Shared *>(dyn);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -251,146 +422,88 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         return;  // the whole cluster
     }
     const bool greedy = temperature == 0.0f || min_p > 1.0f || top_k == 1;
+    const bool by_count = top_k > 0 && top_k < p.vocab;
 
-    // ---- this CTA's slice, in 16-byte parts of the row's own alignment, and this warp's stretch of it
+    // ---- this CTA's slice of the row, and this warp's stretch of that
     const T *logits = static_cast<const T *>(p.logits) + row * p.stride;
-    const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(logits) & 15u) / sizeof(T));
-    const uint4 *vecs = reinterpret_cast<const uint4 *>(logits - shift);
-    const int n_vecs = (shift + p.vocab + kVec - 1) / kVec;
-    const int per_cta = (n_vecs + cluster - 1) / cluster;
+    const int per_cta = (p.vocab + cluster - 1) / cluster;
     const int per_warp = (per_cta + kThreads - 1) / kThreads * 32;
-    const int cta1 = min(n_vecs, (rank + 1) * per_cta);
-    const int v0 = min(cta1, rank * per_cta + warp * per_warp), v1 = min(cta1, v0 + per_warp);
+    const int cta1 = min(p.vocab, (rank + 1) * per_cta);
+    const int e0 = min(cta1, rank * per_cta + warp * per_warp), e1 = min(cta1, e0 + per_warp);
     auto sync = [&] {
         if (cluster > 1) cluster_sync();
         else __syncthreads();
     };
-    // 16 bytes of the row; at its ends, -infinity in place of what is not the row's
-    auto load = [&](int v) {
-        const int first = v * kVec - shift;
-        if (first >= 0 && first + kVec <= p.vocab) return vecs[v];
-        T x[kVec];
-#pragma unroll
-        for (int e = 0; e < kVec; ++e)
-            x[e] = first + e >= 0 && first + e < p.vocab ? logits[first + e] : Logit<T>::none();
-        uint4 raw;
-        memcpy(&raw, x, 16);
-        return raw;
-    };
-    // f(logits, index of the first): the lane's logits, 16 bytes at a time, NaN as -infinity; AHEAD
-    // of them are loaded together
-    auto each = [&](auto ahead, int from, int to, auto f) {
-        constexpr int kAhead = decltype(ahead)::value;
-#pragma unroll 1
-        for (int v = from + lane; v < to; v += 32 * kAhead) {
-            uint4 raw[kAhead];
-#pragma unroll
-            for (int y = 0; y < kAhead; ++y)
-                if (v + 32 * y < to) raw[y] = load(v + 32 * y);
-#pragma unroll
-            for (int y = 0; y < kAhead; ++y) {
-                if (v + 32 * y >= to) break;
-                float x[kVec];
-                Logit<T>::unpack(raw[y], x);
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) x[e] = fmaxf(x[e], -INFINITY);
-                f(x, (v + 32 * y) * kVec - shift);
-            }
-        }
-    };
-
-    // ---- the largest logit, and (for a row that takes it) the first index that has it
-    float top = -INFINITY;
-    int first = kAll;
-    if (greedy) {
-        each(Const<4>(), v0, v1, [&](const float (&x)[kVec], int at) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e)
-                if (x[e] > top) {
-                    top = x[e];
-                    first = at + e;
-                }
-        });
-    } else {
+    if (!greedy) {
         for (int x = tid; x < kPow; x += kThreads) sh.powers[x] = make_float2(kPowers.hi[x], kPowers.lo[x]);
-        for (int x = tid; x < kBins; x += kThreads)
-            sh.lo[0][x] = sh.hi[0][x] = sh.lo[1][x] = sh.hi[1][x] = sh.least[x] = sh.most[x] = 0;
-        each(Const<4>(), v0, v1, [&](const float (&x)[kVec], int) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) top = fmaxf(top, x[e]);
-        });
+        if (by_count || top_p < 1.0f)
+            for (int x = tid; x < kBins; x += kThreads)
+                sh.lo[0][x] = sh.hi[0][x] = sh.lo[1][x] = sh.hi[1][x] = sh.least[x] = sh.most[x] = 0;
     }
-    auto larger = [&](float other, int other_first) {
-        if (other > top || (other == top && other_first < first)) {
-            top = other;
-            first = other_first;
-        }
-    };
+
+    // ---- the largest logit
+    float top = -INFINITY;
+    each_logit(logits, e0, e1, [&](const auto &x, int) { top = fmaxf(top, top_of(x)); });
+    const float own_top = top;
     __syncwarp();
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        const float other = __shfl_xor_sync(FULL_MASK, top, o);
-        const int other_first = __shfl_xor_sync(FULL_MASK, first, o);
-        larger(other, other_first);
-    }
-    if (lane == 0) {
-        sh.warp_top[warp] = top;
-        sh.warp_first[warp] = first;
-    }
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
+    if (lane == 0) sh.warp_top[warp] = top;
+    const float warp_top = top;
     if (tid == kThreads - 1 && min_p > 0.0f && min_p <= 1.0f)  // (64-bit arithmetic is slow: one thread's business)
         sh.log_min = static_cast<double>(temperature) * log(static_cast<double>(min_p));
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w) larger(sh.warp_top[w], sh.warp_first[w]);
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh.warp_top[w]);
     if (cluster > 1) {
-        if (tid < cluster) {
-            *in_cta(&sh.tops[rank], tid) = top;
-            *in_cta(&sh.firsts[rank], tid) = first;
-        }
+        if (tid < cluster) *in_cta(&sh.tops[rank], tid) = top;
         cluster_sync();
-        for (int r = 0; r < cluster; ++r) larger(sh.tops[r], sh.firsts[r]);
+        for (int r = 0; r < cluster; ++r) top = fmaxf(top, sh.tops[r]);
     }
     if (greedy || top == -INFINITY) {
-        if (rank == 0 && tid == 0) p.tokens[row] = top == -INFINITY ? -1 : first;
-        if (cluster > 1) cluster_sync();  // (no CTA leaves while another may write to it)
+        // the first index that has it: of the warps that have seen it
+        int first = kAll;
+        if (top > -INFINITY && warp_top == top)
+            each_logit(logits, e0, e1, [&](const auto &x, int i) {
+                if (top_of(x) != top) return;
+#pragma unroll
+                for (int e = static_cast<int>(sizeof(x) / sizeof(x[0])) - 1; e >= 0; --e)
+                    if (x[e] == top) first = min(first, i + e);
+            });
+        __syncwarp();
+        first = __reduce_min_sync(FULL_MASK, first);
+        if (lane == 0) sh.warp_first[warp] = first;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) first = min(first, sh.warp_first[w]);
+        if (cluster > 1) {
+            if (tid == 0) *in_cta(&sh.firsts[rank], 0) = first;
+            cluster_sync();
+            if (rank == 0)
+                for (int r = 0; r < cluster; ++r) first = min(first, sh.firsts[r]);
+        }
+        if (rank == 0 && tid == 0) p.tokens[row] = first == kAll ? -1 : first;
         return;
     }
 
-    Weigher weight;
-    weight.top = top;
-    weight.powers = sh.powers;
+    Weigher weigher;
+    weigher.top = top;
     {
         // log2(e) / T: the quotient, and the remainder's
         constexpr float kLog2EHi = 1.44269502162933349609f, kLog2ELo = 1.92596298909e-8f;
         const float c = kLog2EHi / temperature;
-        weight.c_hi = fminf(c, 3.0e38f);
-        weight.c_lo = c < 3.0e38f ? __fadd_rn(__fmaf_rn(-c, temperature, kLog2EHi), kLog2ELo) / temperature : 0.0f;
+        weigher.c_hi = fminf(c, 3.0e38f);
+        // below the top itself, which is likely even where the difference rounds away
+        weigher.likely = fminf(top - 24.0f / weigher.c_hi, value_of(key_of(top) - (top == 0.0f ? 2 : 1)));
+        weigher.c_lo = c < 3.0e38f ? __fadd_rn(__fmaf_rn(-c, temperature, kLog2EHi), kLog2ELo) / temperature : 0.0f;
     }
+    auto weight = [&](float x) { return weight_of(weigher, x); };
+    Queue queue{sh.queue[warp], 0};
 
     // ---- what is kept: x > cut, and the first `ties` of those equal to it
     float cut = -INFINITY;
     int ties = 0;
 
-    // Of vectors from .. to - 1, by a whole warp: the weights above the cut, and how many equal it.
-    auto part_of = [&](int from, int to) {
-        Part mine{0, 0, 0};
-        each(Const<2>(), from, to, [&](const float (&x)[kVec], int) {
-            bool any = false;
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                any |= x[e] > cut;
-                mine.equal += x[e] == cut;
-            }
-            if (!any) return;
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) mine.sum += x[e] > cut ? weight(x[e]) : 0ull;
-        });
-        __syncwarp();
-        mine.sum = warp_sum64(mine.sum);
-        mine.equal = __reduce_add_sync(FULL_MASK, mine.equal);
-        return mine;
-    };
     auto gather_parts = [&] {
-        const Part mine = part_of(v0, v1);
+        const Part mine = part_of(logits, e0, e1, cut, weigher, queue.at);
         if (lane < cluster) *in_cta(&sh.parts[rank * kWarps + warp], lane) = mine;
         sync();
     };
@@ -413,50 +526,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         const unsigned h = static_cast<unsigned>(w >> 32) + (old + l < old ? 1u : 0u);
         if (h != 0) atomicAdd(&sh.hi[turn][bin], h);
     };
-    // The bin in which the running sum over the cluster's histograms reaches `target` (from bin 0 up,
-    // or from the last down), and what lies before it; false if none does. Clears the other
-    // histogram, which everybody has read before the barrier ahead of this call.
-    auto find = [&](int turn, bool by_weight, u64 target, bool down) {
-        const int at = down ? kBins - 4 - 4 * tid : 4 * tid;
-        u64 own[4] = {0, 0, 0, 0};
-        for (int r = 0; r < cluster; ++r) {
-            const uint4 l = *reinterpret_cast<const uint4 *>(in_cta(sh.lo[turn], r) + at);
-            uint4 h = make_uint4(0, 0, 0, 0);
-            if (by_weight) h = *reinterpret_cast<const uint4 *>(in_cta(sh.hi[turn], r) + at);
-            own[0] += static_cast<u64>(h.x) << 32 | l.x;
-            own[1] += static_cast<u64>(h.y) << 32 | l.y;
-            own[2] += static_cast<u64>(h.z) << 32 | l.z;
-            own[3] += static_cast<u64>(h.w) << 32 | l.w;
-        }
-        const u64 sum = own[0] + own[1] + own[2] + own[3];
-        u64 before = warp_scan64(sum);
-        if (lane == 31) sh.scan[warp] = before;
-        if (tid == 0) sh.bin = -1;
-        before -= sum;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) before += sh.scan[w];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            const u64 mine = down ? own[3 - y] : own[y];
-            if (before < target && target <= before + mine) {
-                sh.bin = down ? at + 3 - y : at + y;
-                sh.before = before;
-            }
-            before += mine;
-        }
-        for (int x = tid; x < kBins; x += kThreads) sh.lo[turn ^ 1][x] = sh.hi[turn ^ 1][x] = 0;
-        __syncthreads();
-        return sh.bin >= 0;
-    };
-
     // The cut at which `target` (a count, or a sum of weights) is reached from the top, among what is
-    // kept so far: the new cut and its ties. (A count that is not reached: all are kept.)
-    auto descend = [&](bool by_weight, u64 target) {
+    // kept so far: the new cut and its ties. (A count that is not reached: all are kept.) No weight
+    // before `least_t` (its logarithm) is needed to reach it.
+    auto descend = [&](bool by_weight, u64 target, float least_t) {
         const float old_cut = cut;
         // those equal to the cut so far, of which only `ties` are kept: one thread adds them
         const bool old = by_weight && ties > 0 && rank == 0 && tid == 0;
         const u64 w_old = old ? weight(old_cut) * static_cast<u64>(ties) : 0;
-        const float scale = weight.c_hi * 32.0f;
+        const float scale = weigher.c_hi * 32.0f;
         // bin and place in it (both roundings leave the order of logits as it is)
         auto place = [&](float x) { return x == top ? 0.0f : fminf((top - x) * scale, static_cast<float>(kBins)); };
         auto settle = [&](u64 rest) {
@@ -467,100 +545,125 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 ties = static_cast<int>(rest);
             }
         };
-        each(Const<2>(), v0, v1, [&](const float (&x)[kVec], int) {
+        // what lies below this bin is not needed
+        float end = fminf(ceilf(-least_t * 32.0f), static_cast<float>(kBins));
+        if (!by_weight && target <= static_cast<u64>(cluster * kThreads)) {
+            // as many logits as the threads have, their own largest, reach it in a bin: all bins up to
+            // that one hold enough
+            const float f = place(own_top);
+            if (f < static_cast<float>(kBins)) atomicAdd(&sh.least[static_cast<unsigned>(f)], 1u);
+            sync();
+            const int bin = find_bin(sh.least, nullptr, 0, target, false, cluster);
+            if (bin >= 0) end = static_cast<float>(bin + 1);
+        }
+        auto note = [&](float x) {
+            const unsigned bin = static_cast<unsigned>(place(x));
+            if (by_weight) add(0, bin, weight(x));
+            else atomicAdd(&sh.lo[0][bin], 1u);
+        };
+        each_logit(logits, e0, e1, [&](const auto &x, int) {
+            const float largest = top_of(x);
+            if (!__any_sync(FULL_MASK, largest > old_cut && place(largest) < end)) return;
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                const float f = place(x[e]);
-                if (!(x[e] > old_cut) || f >= static_cast<float>(kBins)) continue;
-                if (by_weight) add(0, static_cast<unsigned>(f), weight(x[e]));
-                else atomicAdd(&sh.lo[0][static_cast<unsigned>(f)], 1u);
-            }
+            for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(x[0])); ++e)
+                queue.push(x[e] > old_cut && place(x[e]) < end, x[e], note);
         });
-        if (old && place(old_cut) < static_cast<float>(kBins)) add(0, static_cast<unsigned>(place(old_cut)), w_old);
+        queue.finish(note);
+        if (old && place(old_cut) < end) add(0, static_cast<unsigned>(place(old_cut)), w_old);
         sync();
-        if (find(0, by_weight, target, false)) {
+        const int at = find_bin(sh.lo[0], by_weight ? sh.hi[0] : nullptr, 1, target, false, cluster);
+        if (at >= 0) {
             const u64 rest = target - sh.before;
-            const float bin = static_cast<float>(sh.bin);
-            auto note = [&](float x, float f, u64 w) {
-                const unsigned part = static_cast<unsigned>((f - bin) * kBins), key = key_of(x);  // (f - bin is exact)
+            const float bin = static_cast<float>(at);
+            auto note_part = [&](float x, u64 w) {
+                const unsigned part = static_cast<unsigned>((place(x) - bin) * kBins), key = key_of(x);  // (exact)
                 if (by_weight) add(1, part, w);
                 else atomicAdd(&sh.lo[1][part], 1u);
                 atomicMax(&sh.least[part], ~key);
                 atomicMax(&sh.most[part], key);
             };
-            each(Const<2>(), v0, v1, [&](const float (&x)[kVec], int) {
+            auto inside = [&](float x) {
+                const float f = place(x);
+                return f >= bin && f < bin + 1.0f;
+            };
+            auto note_it = [&](float x) { note_part(x, by_weight ? weight(x) : 0ull); };
+            each_logit(logits, e0, e1, [&](const auto &x, int) {
+                const float largest = top_of(x);
+                if (!__any_sync(FULL_MASK, largest > old_cut && place(largest) < bin + 1.0f)) return;
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const float f = place(x[e]);
-                    if (x[e] > old_cut && f >= bin && f < bin + 1.0f) note(x[e], f, by_weight ? weight(x[e]) : 0ull);
-                }
+                for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(x[0])); ++e)
+                    queue.push(x[e] > old_cut && inside(x[e]), x[e], note_it);
             });
-            if (old) {
-                const float f = place(old_cut);
-                if (f >= bin && f < bin + 1.0f) note(old_cut, f, w_old);
-            }
+            queue.finish(note_it);
+            if (old && inside(old_cut)) note_part(old_cut, w_old);
             sync();
-            const int part = find(1, by_weight, rest, false) ? sh.bin : 0;  // (the bin holds the border)
+            const int part = max(0, find_bin(sh.lo[1], by_weight ? sh.hi[1] : nullptr, 0, rest, false, cluster));  // (one holds the border)
             unsigned least = 0, most = 0;
             for (int r = 0; r < cluster; ++r) {
                 least = max(least, *(in_cta(sh.least, r) + part));
                 most = max(most, *(in_cta(sh.most, r) + part));
             }
             const u64 left = rest - sh.before;
-            sync();  // the parts' keys, and the second histogram, have been read
-            for (int x = tid; x < kBins; x += kThreads)
-                sh.lo[1][x] = sh.hi[1][x] = sh.least[x] = sh.most[x] = 0;
-            __syncthreads();
             if (~least == most) {
                 cut = value_of(most);
                 settle(left);
                 return;
             }
-        } else {
+        }
+        // by the keys' bits
+        auto clear = [&] {
             sync();
             for (int x = tid; x < kBins; x += kThreads) sh.lo[0][x] = sh.hi[0][x] = 0;
             __syncthreads();
-        }
-        // by the keys' bits
+        };
+        clear();
         unsigned prefix = 0;
         bool found = true;
 #pragma unroll 1
         for (int pass = 0; pass < 3 && found; ++pass) {
             const int down = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11, turn = pass & 1;
-            auto mine = [&](unsigned key) { return pass == 0 || (key >> (down + bits)) == prefix; };
-            each(Const<2>(), v0, v1, [&](const float (&x)[kVec], int) {
+            auto inside = [&](unsigned key) { return pass == 0 || (key >> (down + bits)) == prefix; };
+            auto bin_of = [&](unsigned key) { return (key >> down) & ((1u << bits) - 1); };
+            auto note_key = [&](float x) {
+                if (by_weight) add(turn, bin_of(key_of(x)), weight(x));
+                else atomicAdd(&sh.lo[turn][bin_of(key_of(x))], 1u);
+            };
+            each_logit(logits, e0, e1, [&](const auto &x, int) {
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const unsigned key = key_of(x[e]);
-                    if (!(x[e] > old_cut) || !mine(key)) continue;
-                    const unsigned bin = (key >> down) & ((1u << bits) - 1);
-                    if (by_weight) add(turn, bin, weight(x[e]));
-                    else atomicAdd(&sh.lo[turn][bin], 1u);
-                }
+                for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(x[0])); ++e)
+                    queue.push(x[e] > old_cut && inside(key_of(x[e])), x[e], note_key);
             });
-            if (old && mine(key_of(old_cut))) add(turn, (key_of(old_cut) >> down) & ((1u << bits) - 1), w_old);
+            queue.finish(note_key);
+            if (old && inside(key_of(old_cut))) add(turn, bin_of(key_of(old_cut)), w_old);
             sync();
-            found = find(turn, by_weight, target, true);
+            const int bin = find_bin(sh.lo[turn], by_weight ? sh.hi[turn] : nullptr, turn ^ 1, target, true, cluster);
+            found = bin >= 0;
             if (found) {
                 target -= sh.before;
-                prefix = prefix << bits | static_cast<unsigned>(sh.bin);
+                prefix = prefix << bits | static_cast<unsigned>(bin);
             }
         }
         if (found) {
             cut = value_of(prefix);
             settle(target);
         }
-        sync();
-        for (int x = tid; x < kBins; x += kThreads) sh.lo[0][x] = sh.hi[0][x] = 0;
-        __syncthreads();
+        clear();
     };
 
-    if (top_k > 0 && top_k < p.vocab) descend(false, top_k);
-    if (top_p < 1.0f) {
-        gather_parts();
-        const u64 total = total_of(ties > 0 ? weight(cut) : 0);
-        const u64 want = top_p > 0.0f ? times(top_p, total, true) : 0;
-        descend(true, want > 0 ? want : 1);  // (its barriers come before the parts are written again)
+#pragma unroll 1
+    for (int step = by_count ? 0 : 1; step < (top_p < 1.0f ? 2 : 1); ++step) {
+        u64 target = top_k;
+        float least_t = -INFINITY;
+        if (step == 1) {
+            gather_parts();
+            const u64 total = total_of(ties > 0 ? weight(cut) : 0);
+            const u64 want = top_p > 0.0f ? times(top_p, total, true) : 0;
+            // Where a weight times the vocabulary falls short of what may be left out, the border is behind
+            // (0.02: half a bin, and fp32's errors).
+            least_t = log2f(static_cast<float>(total - want) * 0x1p-43f / static_cast<float>(p.vocab)) - 0.02f;
+            target = want > 0 ? want : 1;
+        }
+        descend(step == 1, target, least_t);  // (its barriers come before the parts are written again)
     }
     if (min_p > 0.0f) {
         // w >= min_p: x >= top + T ln(min_p)
@@ -572,73 +675,58 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
 
     // ---- the token: the stretch in which the running sum exceeds the target, then 1 / 16 of it, then
-    // 32 parts of 16 bytes at a time, then the lane's, then its logits
+    // 32 logits at a time
     gather_parts();
     const u64 w_cut = ties > 0 ? weight(cut) : 0;
     const u64 target = times(u, total_of(w_cut), false);
     u64 run = 0;   // weights above the cut before the stretch
     int seen = 0;  // logits equal to it
     auto upto = [&](u64 sum, int equal) { return sum + static_cast<u64>(min(equal, ties)) * w_cut; };
-    // which of `count` parts it is (by a whole warp); run and seen move on to it
+    // which lane's running sum exceeds the target (-1: none); run and seen move on to it, or past all
+    auto advance = [&](u64 sum, int equal) {
+        const u64 sums = warp_scan64(sum);
+        const int equals = warp_scan(equal);
+        const unsigned past = __ballot_sync(FULL_MASK, upto(run + sums, seen + equals) > target);
+        const int at = past != 0 ? __ffs(past) - 1 : 31;
+        run += __shfl_sync(FULL_MASK, past != 0 ? sums - sum : sums, at);
+        seen += __shfl_sync(FULL_MASK, past != 0 ? equals - equal : equals, at);
+        return past != 0 ? at : -1;
+    };
+    // which of `count` parts it is (by a whole warp): a few consecutive ones a lane, then one by one
     auto pick = [&](const Part *parts, int count) {
-        for (int x0 = 0;; x0 += 32) {
-            Part mine{0, 0, 0};
-            if (x0 + lane < count) mine = parts[x0 + lane];
-            __syncwarp();
-            const u64 sums = warp_scan64(mine.sum);
-            const int equals = warp_scan(mine.equal);
-            const unsigned past = __ballot_sync(FULL_MASK, upto(run + sums, seen + equals) > target);
-            const int at = past != 0 ? __ffs(past) - 1 : 31;
-            run += __shfl_sync(FULL_MASK, past != 0 ? sums - mine.sum : sums, at);
-            seen += __shfl_sync(FULL_MASK, past != 0 ? equals - mine.equal : equals, at);
-            if (past != 0 || x0 + 32 >= count) return x0 + at;
+        const int each_lane = (count + 31) / 32, first = lane * each_lane;
+        u64 sum = 0;
+        int equal = 0;
+        for (int x = first; x < min(count, first + each_lane); ++x) {
+            sum += parts[x].sum;
+            equal += parts[x].equal;
         }
+        __syncwarp();
+        int x = max(advance(sum, equal), 0) * each_lane;
+        for (; x + 1 < count && upto(run + parts[x].sum, seen + parts[x].equal) <= target; ++x) {
+            run += parts[x].sum;
+            seen += parts[x].equal;
+        }
+        return x;
     };
     const int stretch = pick(sh.parts, cluster * kWarps);
     if (stretch / kWarps == rank) {
         const int begin = min(cta1, rank * per_cta + stretch % kWarps * per_warp), end = min(cta1, begin + per_warp);
         const int each_warp = (end - begin + kThreads - 1) / kThreads * 32;
         const int a = min(end, begin + warp * each_warp);
-        const Part mine = part_of(a, min(end, a + each_warp));
+        const Part mine = part_of(logits, a, min(end, a + each_warp), cut, weigher, queue.at);
         if (lane == 0) sh.own[warp] = mine;
         __syncthreads();
         if (warp == 0) {
             const int from = begin + pick(sh.own, kWarps) * each_warp, to = min(end, from + each_warp);
-            for (int v = from; v < to; v += 32) {
-                float x[kVec];
-                u64 sum = 0;
-                int same = 0;
-                if (v + lane < to) {
-                    Logit<T>::unpack(load(v + lane), x);
-#pragma unroll
-                    for (int e = 0; e < kVec; ++e) {
-                        if (x[e] > cut) sum += weight(x[e]);
-                        else if (x[e] == cut) ++same;
-                    }
-                }
+            for (int i = from + lane; i < to + lane; i += 32) {
+                const float x = i < to ? fmaxf(logit(logits[i]), -INFINITY) : -INFINITY;
+                const u64 w = x > cut ? weight(x) : 0;
                 __syncwarp();
-                const u64 sums = warp_scan64(sum);
-                const int sames = warp_scan(same);
-                const unsigned past = __ballot_sync(FULL_MASK, upto(run + sums, seen + sames) > target);
-                if (past != 0) {
-                    if (lane == __ffs(past) - 1) {
-                        u64 s = run + sums - sum;
-                        int q = seen + sames - same;
-                        bool done = false;
-#pragma unroll
-                        for (int e = 0; e < kVec; ++e) {
-                            if (x[e] > cut) s += weight(x[e]);
-                            else if (x[e] == cut) ++q;
-                            if (!done && upto(s, q) > target) {
-                                p.tokens[row] = (v + lane) * kVec + e - shift;
-                                done = true;
-                            }
-                        }
-                    }
-                    break;
-                }
-                run += __shfl_sync(FULL_MASK, sums, 31);
-                seen += __shfl_sync(FULL_MASK, sames, 31);
+                const int at = advance(w, x == cut);
+                if (at < 0) continue;
+                if (lane == at) p.tokens[row] = i;
+                break;
             }
         }
     }
