@@ -122,9 +122,11 @@ __device__ __forceinline__ float value_of(unsigned key) {
 }
 
 // Weights: 2^43 e^{(x - top) / T}. c_hi + c_lo is log2(e) / T; above `likely` the weight is more than
-// 2^-24 of the largest.
+// 2^-kLikely of the largest; k_hi + k_lo is kLikely - top (c_hi + c_lo).
+constexpr int kLikely = 20;
+constexpr float kExpShort = 7.14e-8f;  // log2 of what the exponential falls short by, over its range (measured: 4.95e-8)
 struct Weigher {
-    float top, c_hi, c_lo, likely;
+    float top, c_hi, c_lo, k_hi, k_lo, likely;
 };
 
 // The weight of a likely token: t = (x - top) log2(e) / T in two floats, 2^t from the table and a
@@ -160,14 +162,16 @@ __device__ __noinline__ u64 precise_weight(const Weigher w, float x) {
     return x == w.top ? 1ull << 43 : sum >> (1 - (n >> 8));
 }
 
-// The weight of an unlikely one, below 2^19 and so the last bits of 2^23 more than it: fp32's 2^-20 of
-// it (its argument's rounding) is 2^-44 of the largest.
+// The weight of an unlikely one, below 2^23 and so the last bits of 2^23 more than it. Its argument
+// is near 0 where the weight counts most, and all but exact there: the error is the exponential's,
+// 2^-22 of 2^-20 of the largest.
 constexpr unsigned kSmallBase = 0x4B000000u;  // 2^23
 __device__ __forceinline__ unsigned small_weight_bits(const Weigher &w, float x) {
-    return __float_as_uint(__fadd_rn(fast_exp2(__fmaf_rn(__fsub_rn(x, w.top), w.c_hi, 43.0f)), 8388608.0f));
+    const float t = __fadd_rn(__fmaf_rn(x, w.c_hi, w.k_hi), __fmaf_rn(x, w.c_lo, w.k_lo));
+    return __float_as_uint(__fmaf_rn(fast_exp2(t), static_cast<float>(1 << (43 - kLikely)), 8388608.0f));
 }
 __device__ __forceinline__ u64 weight_of(const Weigher &w, float x) {
-    return x > w.likely ? precise_weight(w, x) : small_weight_bits(w, x) - kSmallBase;
+    return x > w.likely ? precise_weight(w, x) : x > -INFINITY ? small_weight_bits(w, x) - kSmallBase : 0u;
 }
 
 __device__ __forceinline__ u64 warp_sum64(u64 x) {
@@ -325,8 +329,8 @@ __device__ __noinline__ Part part_of(const T *logits, int from, int to, float cu
             }
         });
     } else {
-        // (a lane's small weights add up to less than 2^32: at most 2^20 / 512 of them below 2^19)
-        unsigned small = 0;
+        // (small weights are below 2^23: 2^9 of them add up to less than 2^32)
+        unsigned small = 0, since = 0;
         each_logit(logits, from, to, [&](const auto &x, int) {
             constexpr int N = static_cast<int>(sizeof(x) / sizeof(x[0]));
 #pragma unroll
@@ -334,6 +338,11 @@ __device__ __noinline__ Part part_of(const T *logits, int from, int to, float cu
                 const unsigned bits = small_weight_bits(w, x[e]) - kSmallBase;
                 small += x[e] > cut && !(x[e] > w.likely) ? bits : 0u;
                 mine.equal += x[e] == cut;
+            }
+            since += N;
+            if (since >= 256) {
+                mine.sum += small;
+                small = since = 0;
             }
             if (!__any_sync(FULL_MASK, top_of(x) > w.likely)) return;
 #pragma unroll
@@ -349,9 +358,10 @@ __device__ __noinline__ Part part_of(const T *logits, int from, int to, float cu
 
 // The bin in which the running sum over the cluster's histograms (low words and, unless NULL, high
 // ones) reaches `target`, from bin 0 up or from the last down; what lies before it goes to sh.before;
-// -1 if none does. By the whole CTA. Clears histogram `clears` (and with the second the parts' keys),
+// -1 if none does. Bins from `limit` up are known to be empty. By the whole CTA. Clears histogram `clears` (and with the second the parts' keys),
 // which everybody has read before the barrier ahead of this call.
-__device__ __noinline__ int find_bin(unsigned *low, unsigned *high, int clears, u64 target, bool down, int cluster) {
+__device__ __noinline__ int find_bin(unsigned *low, unsigned *high, int clears, u64 target, bool down, int cluster,
+                                     int limit = kBins) {
     extern __shared__ __align__(16) uint8_t dyn[];
     Shared &sh = *reinterpret_cast<Shared *>(dyn);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -363,7 +373,7 @@ __device__ __noinline__ int find_bin(unsigned *low, unsigned *high, int clears, 
             uint4 x[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-                x[y] = r0 + y < cluster ? *reinterpret_cast<const uint4 *>(in_cta(hist, r0 + y) + at) : make_uint4(0, 0, 0, 0);
+                x[y] = r0 + y < cluster && at < limit ? *reinterpret_cast<const uint4 *>(in_cta(hist, r0 + y) + at) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 own[0] += static_cast<u64>(x[y].x) << (32 * word);
@@ -491,9 +501,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         constexpr float kLog2EHi = 1.44269502162933349609f, kLog2ELo = 1.92596298909e-8f;
         const float c = kLog2EHi / temperature;
         weigher.c_hi = fminf(c, 3.0e38f);
-        // below the top itself, which is likely even where the difference rounds away
-        weigher.likely = fminf(top - 24.0f / weigher.c_hi, value_of(key_of(top) - (top == 0.0f ? 2 : 1)));
         weigher.c_lo = c < 3.0e38f ? __fadd_rn(__fmaf_rn(-c, temperature, kLog2EHi), kLog2ELo) / temperature : 0.0f;
+        // below the top itself, which is likely even where the difference rounds away
+        weigher.likely = fminf(top - static_cast<float>(kLikely) / weigher.c_hi, value_of(key_of(top) - (top == 0.0f ? 2 : 1)));
+        // kLikely - top c, the product in two floats
+        const float prod = __fmul_rn(top, weigher.c_hi), rest = __fmaf_rn(top, weigher.c_lo, __fmaf_rn(top, weigher.c_hi, -prod));
+        const float k = __fsub_rn(static_cast<float>(kLikely), prod), back = __fsub_rn(k, static_cast<float>(kLikely));
+        const float err = __fsub_rn(__fsub_rn(static_cast<float>(kLikely), __fsub_rn(k, back)), __fadd_rn(prod, back));
+        weigher.k_hi = k;
+        weigher.k_lo = __fadd_rn(__fsub_rn(err, rest), kExpShort);
     }
     auto weight = [&](float x) { return weight_of(weigher, x); };
     Queue queue{sh.queue[warp], 0};
@@ -571,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         queue.finish(note);
         if (old && place(old_cut) < end) add(0, static_cast<unsigned>(place(old_cut)), w_old);
         sync();
-        const int at = find_bin(sh.lo[0], by_weight ? sh.hi[0] : nullptr, 1, target, false, cluster);
+        const int at = find_bin(sh.lo[0], by_weight ? sh.hi[0] : nullptr, 1, target, false, cluster, static_cast<int>(end));
         if (at >= 0) {
             const u64 rest = target - sh.before;
             const float bin = static_cast<float>(at);
@@ -733,10 +749,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     if (cluster > 1) cluster_sync();  // no CTA leaves while another may read or write its shared memory
 }
 
-// CTAs of a row: as many as give every SM its two, of at least 2048 logits each.
+// CTAs of a row: as many as give every SM its two, of at least 2048 logits each; eight, whose barriers
+// and histograms take as long as their passes, only where most of the GPU is idle anyway. (128000
+// bf16 logits by top-p: one row 32 us by eight and 34 by four, 16 rows 42 and 37, 64 rows 51 by four and
+// 88 by one; 1024 rows of 100003 in fp32 449 by one, 635 by four.)
 template <typename T>
 gdn_status launch(const SampleParams &p, int rows, cudaStream_t s) {
-    int cluster = kMaxCluster;
+    int cluster = rows <= 8 ? kMaxCluster : 4;
     while (cluster > 1 && (static_cast<long long>(rows) * cluster > 2 * kSMs || p.vocab / cluster < 2048)) cluster /= 2;
     if (static_cast<long long>(rows) * cluster > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
     auto kernel = sample_kernel<T>;
