@@ -1200,15 +1200,13 @@ gdn_status launch_dim(int d, const CUtensorMap &q, const CUtensorMap &k, const C
     }
 }
 
-// The call, of single tokens and chains (parents NULL) or of trees.
-template <bool TREE>
-gdn_status attn_decode_call(const void *q, const void *k_pages, const void *v_pages,
-                            const int32_t *page_table, const int32_t *kv_lens, void *out,
-                            const int32_t *parents, int n_seqs, int n_tokens, int n_q_heads,
-                            int n_kv_heads, int head_dim, int page_size, int n_pages, int max_pages,
-                            int window, int n_sinks, float scale, int q_stride, int dtype,
-                            const int32_t *slots, int pool, int32_t *err_count, void *workspace,
-                            size_t workspace_bytes, gdn_stream_t stream) {
+// The arguments of a call; `need`: bytes of workspace.
+inline gdn_status check_decode(const void *q, const void *k_pages, const void *v_pages,
+                               const int32_t *page_table, const int32_t *kv_lens, const void *out,
+                               int n_seqs, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim,
+                               int page_size, int n_pages, int max_pages, int window, int n_sinks,
+                               int q_stride, int dtype, const int32_t *slots, int pool,
+                               const void *workspace, size_t workspace_bytes, size_t need) {
     if (!q || !k_pages || !v_pages || !page_table || !kv_lens || !out) return GDN_ERR_NULL;
     if (n_seqs < 0 || n_tokens < 1 || n_q_heads < 1 || window < 0 || n_sinks < 0) return GDN_ERR_SHAPE;
     GDN_TRY(check_cache(n_kv_heads, head_dim, page_size, n_pages, max_pages, dtype));
@@ -1224,8 +1222,24 @@ gdn_status attn_decode_call(const void *q, const void *k_pages, const void *v_pa
     if (n_seqs == 0) return GDN_OK;
     if (!workspace) return GDN_ERR_NULL;
     if (!aligned16(workspace)) return GDN_ERR_ALIGN;
-    if (workspace_bytes < workspace_bytes_for(head_dim)) return GDN_ERR_SHAPE;
+    if (workspace_bytes < need) return GDN_ERR_SHAPE;
+    return GDN_OK;
+}
 
+// The call, of single tokens and chains (parents NULL) or of trees.
+template <bool TREE>
+gdn_status attn_decode_call(const void *q, const void *k_pages, const void *v_pages,
+                            const int32_t *page_table, const int32_t *kv_lens, void *out,
+                            const int32_t *parents, int n_seqs, int n_tokens, int n_q_heads,
+                            int n_kv_heads, int head_dim, int page_size, int n_pages, int max_pages,
+                            int window, int n_sinks, float scale, int q_stride, int dtype,
+                            const int32_t *slots, int pool, int32_t *err_count, void *workspace,
+                            size_t workspace_bytes, gdn_stream_t stream) {
+    GDN_TRY(check_decode(q, k_pages, v_pages, page_table, kv_lens, out, n_seqs, n_tokens, n_q_heads, n_kv_heads,
+                         head_dim, page_size, n_pages, max_pages, window, n_sinks, q_stride, dtype, slots, pool,
+                         workspace, workspace_bytes, workspace_bytes_for(head_dim)));
+    if (n_seqs == 0) return GDN_OK;
+    const int es = dtype_bytes(dtype);
     const int group = n_q_heads / n_kv_heads;
     const Split sp = split_rows(n_tokens, group);
     Params p{};
