@@ -21,6 +21,7 @@ struct TreeAttnParams {
     int heads_per_tile, tokens_per_tile;  // rows of a lane: nodes x heads
     int head_groups, blocks;              // of a key head
     int record_rows;                      // rows of a partial result: 128 or 256
+    int q_rows, q_bufs;                   // rows of a Q buffer; buffers
     float scale_log2;
     int32_t *err_count;
     unsigned *watchdog;

@@ -13,7 +13,7 @@
 // Two lanes (head_dim 64, 128) share the tensor pipe, each with its S, P and O, one's softmax running
 // while the pipe works for the other. With more than 128 rows in a block a lane has rows of its own
 // and both take every key tile; with at most 128 the lanes have the same rows and take the tiles in
-// turn, and lane 0 adds the two up at the end. Heads of 256 leave room for one lane with two S buffers.
+// turn, and the one whose turn was last adds the two up. Heads of 256 leave room for one lane with two S buffers.
 #include "gdn_attn_tc.cuh"
 #include "gdn_attn_tree.cuh"
 #include "gdn_tree.cuh"
@@ -25,20 +25,21 @@ constexpr int kSMs = 152;
 constexpr unsigned kTurn = 2;  // what a unit weighs besides its tiles, in tiles
 constexpr int kJoinParts = 16;
 
-template <int D>
+// EXTRA: with few rows, what their Q does not need of shared memory goes to the rings.
+template <int D, bool EXTRA>
 struct TreeTc {
     static constexpr int kLanes = D == 256 ? 1 : 2;
     static constexpr int kBufs = D == 256 ? 2 : 1;  // S buffers of a lane
     // Slots of a K (or V) tile, and of the rings, as the prompt attention's.
     static constexpr int kSubs = D == 256 ? 2 : 1;
-    static constexpr int kKSlots = D == 64 ? 4 : D == 128 ? 2 : 3;
-    static constexpr int kVSlots = D == 64 ? 4 : 2;
+    static constexpr int kKSlots = D == 64 ? (EXTRA ? 6 : 4) : D == 128 ? (EXTRA ? 3 : 2) : 3;
+    static constexpr int kVSlots = D == 64 ? (EXTRA ? 6 : 4) : EXTRA ? 3 : 2;
     static constexpr int kSlotBytes = kTcKeys * D * 2 / kSubs;
     static constexpr int kCols = D / 64 / kSubs;  // 128-byte columns of a K slot
     static constexpr int kVKeys = kTcKeys / kSubs;
     static constexpr int kLog2VKeys = kSubs == 2 ? 6 : 7;
-    static constexpr int kQBytes = kTcRows * D * 2;  // of a Q buffer; kLanes of them
-    static constexpr int kSmem = kLanes * kQBytes + (kKSlots + kVSlots) * kSlotBytes + 1024;
+    static constexpr int kRings = (kKSlots + kVSlots) * kSlotBytes;
+    static constexpr int kRoom = 232448 - 1024 - (D == 256 ? 2048 : 4864) - kRings;  // for Q
     static constexpr int kSoftmax = kLanes * 4;
     static constexpr int kMma = kSoftmax, kK = kMma + 1, kSched = kMma + 3;
     static constexpr int kThreads = (kSoftmax + 4) * 32;
@@ -59,16 +60,19 @@ struct Work {
     int whole, head;                                 // nothing of the unit elsewhere; it begins in this range
 
     __device__ __forceinline__ int tile(int j) const { return j < n_sink ? j : main0 + j - n_sink; }
-    __device__ __forceinline__ int first(int i) const { return turns ? j0 + i : j0; }
+    // lane i's first tile (the lanes' turns go on from one segment to the next), and from one to the next
+    __device__ __forceinline__ int first(int i) const { return turns ? j0 + ((g0 + i) & 1) : j0; }
     __device__ __forceinline__ int step() const { return turns ? 2 : 1; }
+    // whose turn the last tile is: that lane adds the other's sums to its own
+    __device__ __forceinline__ int adder() const { return (g0 + j1 - 1 - j0) & 1; }
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(TreeTc<D>::kThreads, 1)
+template <typename T, int D, bool EXTRA>
+__global__ void __launch_bounds__(TreeTc<D, EXTRA>::kThreads, 1)
 attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                     const __grid_constant__ CUtensorMap k_map,
                     const __grid_constant__ CUtensorMap v_map, const TreeAttnParams p) {
-    using C = TreeTc<D>;
+    using C = TreeTc<D, EXTRA>;
     constexpr int kWorks = C::kWorks;
     constexpr bool kBf16 = !__is_same(T, __half);
     constexpr uint32_t kIdescO = tc::idesc_16bit(kBf16, kTcRows, D, true);
@@ -77,17 +81,19 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     extern __shared__ uint8_t dyn[];
     uint8_t *smem =
         reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
-    uint8_t *k_ring = smem + C::kLanes * C::kQBytes;
+    const int q_bytes = p.q_rows * D * 2;  // of a Q buffer: [128-byte column][row]
+    uint8_t *const q_smem = smem;  // (a product reads 128 rows: past a smaller Q whatever lies behind it)
+    uint8_t *k_ring = smem + p.q_bufs * q_bytes;
     uint8_t *v_ring = k_ring + C::kKSlots * C::kSlotBytes;
     __shared__ __align__(8) uint64_t k_full[C::kKSlots], k_empty[C::kKSlots];
     __shared__ __align__(8) uint64_t v_full[C::kVSlots], v_empty[C::kVSlots];
     __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2], o_done[2];
-    __shared__ __align__(8) uint64_t work_full[kWorks], work_empty[kWorks], half_done, half_free;
+    __shared__ __align__(8) uint64_t work_full[kWorks], work_empty[kWorks], half_done[2], half_free[2];
     __shared__ Work works[kWorks];
     __shared__ unsigned long long trees[kWorks][kMaxNodes];  // the nodes' paths
     __shared__ int up_of[kMaxNodes];
     __shared__ uint32_t notes[kNotes];
-    __shared__ float2 half_ml[C::kLanes == 2 ? kTcRows : 1];
+    __shared__ float2 half_ml[2][C::kLanes == 2 ? kTcRows : 1];
     __shared__ unsigned warp_sum[C::kThreads / 32];
     __shared__ unsigned sh_seq_begin;
     __shared__ int sh_seq, sh_slot, sh_len;
@@ -120,8 +126,10 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
             mbar_init(&work_full[i], 1);
             mbar_init(&work_empty[i], 3 + C::kSoftmax);
         }
-        mbar_init(&half_done, 4);
-        mbar_init(&half_free, 4);
+        for (int i = 0; i < 2; ++i) {  // from lane i
+            mbar_init(&half_done[i], 4);
+            mbar_init(&half_free[i], 4);
+        }
         fence_mbar_init();
         sh_dead = 0;
         p.joins[blockIdx.x].c1 = -1;
@@ -240,7 +248,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 // rows of its own for each lane, or one Q for both: the buffers in turn
                 w.q_buf[0] = C::kLanes == 1 ? 0 : w.turns ? next_buf : 0;
                 w.q_buf[1] = C::kLanes == 1 ? 0 : w.turns ? next_buf : 1;
-                if (w.turns) next_buf ^= 1;
+                if (w.turns && p.q_bufs == 2) next_buf ^= 1;
                 if (round > 0 && !warp_wait(&work_empty[ring], (round - 1) & 1, &sh_dead, p.watchdog)) goto leave;
                 if (tree_of != n) {
                     tree_of = n;
@@ -285,7 +293,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                     if (leader) {
                         mbar_arrive_expect_tx(&q_full[b], static_cast<uint32_t>(p.heads_per_tile * per) * D * 2u);
                         for (int cb = 0; cb < D / 64; ++cb)
-                            tma_load_3d(smem + b * C::kQBytes + cb * kTcRows * 128, &q_map, cb * 64, w.head0,
+                            tma_load_3d(q_smem + b * q_bytes + cb * p.q_rows * 128, &q_map, cb * 64, w.head0,
                                         n * p.n_nodes + w.node0 + i * per, &q_full[b]);
                     }
                     __syncwarp();
@@ -309,7 +317,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
             __syncwarp();
         } else if (warp == C::kMma) {
             // ------------------------------------------------------ the MMA warp
-            const uint64_t q_desc = tc::smem_desc_sw128(smem_addr(smem));
+            const uint64_t q_desc = tc::smem_desc_sw128(smem_addr(q_smem));
             const uint64_t k_desc = tc::smem_desc_sw128(smem_addr(k_ring));
             // V lies page by page, every page's 128-byte columns one behind the other: 16 keys are two
             // groups of 8 rows, in one page (bv >= 16) or in two
@@ -353,20 +361,21 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 const uint32_t to = tmem + C::kS + buf * kTcKeys + from;
                 const uint32_t idesc = tc::idesc_16bit(kBf16, kTcRows, 0, false) |
                                        static_cast<uint32_t>(note.end(0) - note.begin(0)) << (17 + 2);
-                const uint64_t q0 = q_desc + ((q_buf * C::kQBytes) >> 4);
+                const uint64_t q0 = q_desc + ((q_buf * q_bytes) >> 4);
+                const int q_col = p.q_rows * 128;
 #pragma unroll
                 for (int s = 0; s < C::kSubs; ++s) {
                     const int slot = (g * C::kSubs + s) % C::kKSlots;
                     if (s > 0 && !warp_wait(&k_full[slot], ((g * C::kSubs + s) / C::kKSlots) & 1, &sh_dead, p.watchdog)) return false;
                     tc::fence_after_sync();
                     const uint64_t k = k_desc + ((slot * C::kSlotBytes + from * 128) >> 4);
-                    const uint64_t q = q0 + ((s * C::kCols * kTcRows * 128) >> 4);
+                    const uint64_t q = q0 + ((s * C::kCols * q_col) >> 4);
                     if (leader) {
 #pragma unroll
                         for (int c = 0; c < C::kCols; ++c)
 #pragma unroll
                             for (int x = 0; x < 4; ++x)
-                                tc::mma_bf16(to, q + ((c * kTcRows * 128 + x * 32) >> 4),
+                                tc::mma_bf16(to, q + ((c * q_col + x * 32) >> 4),
                                              k + ((c * kTcKeys * 128 + x * 32) >> 4), idesc, s + c + x > 0);
                         if (release) tc::mma_commit(&k_empty[slot]);
                         if (s == C::kSubs - 1) {
@@ -450,18 +459,21 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 if (!warp_wait(&work_full[n % kWorks], (n / kWorks) & 1, &sh_dead, p.watchdog)) goto leave;
                 if (!works[n % kWorks].valid) break;
                 const int j0 = works[n % kWorks].j0, j1 = works[n % kWorks].j1, turns = works[n % kWorks].turns;
+                const int g0 = works[n % kWorks].g0;
                 bool done;
 #pragma unroll 1
-                for (int i = 0; i < C::kLanes; ++i) {
+                for (int k = 0; k < C::kLanes; ++k) {
+                    // (this work's first; the other lane may go on to the next work's)
+                    const int i = C::kLanes == 1 ? 0 : (turns ? (g0 + k) & 1 : k);
                     if ((ahead >> i) & 1u) continue;
-                    if (!next_s(i, n, done)) goto leave;
+                    if (!next_s(i, C::kLanes == 1 ? n : n + 1, done)) goto leave;
                     ahead |= static_cast<uint32_t>(done) << i;
                 }
 #pragma unroll 1
                 for (int j = j0; j < j1; ++j) {
 #pragma unroll 1
                     for (int i = 0; i < C::kLanes; ++i) {
-                        if (turns && ((j - j0) & 1) != i) continue;
+                        if (turns && ((g0 + j - j0) & 1) != i) continue;
                         if constexpr (C::kLanes == 1) {
                             // into the other buffer, ahead of this tile's O
                             if (!next_s(0, n + 1, done) || !issue_o(0, n, j)) goto leave;
@@ -587,8 +599,8 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         const bool positive = p.scale_log2 > 0.0f;
         const float mult = positive ? p.scale_log2 : 1.0f;
         int count = 0;         // tiles of this lane so far
-        int halves = 0;        // works whose lanes took turns so far
-        bool owed = false;     // lane 1: its O may still be read by lane 0
+        int given = 0, taken = 0;  // times this lane's sums went to the other lane, and the other's came here
+        bool owed = false;         // the other lane may still be reading this one's O
         for (int ring = 0, round = 0;;) {
             if (!warp_wait(&work_full[ring], round & 1, &sh_dead, p.watchdog)) goto leave;
             const Work &w = works[ring];
@@ -597,6 +609,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
             const int base = w.base, len = w.len, g0 = w.g0 - w.j0, turns = w.turns;
             const int token = (turns ? 0 : i * per) + row_token;  // of the block
             const bool mine = row_token < per && token < w.nodes && row_head < w.heads;
+            const bool busy = __any_sync(FULL_MASK, mine);  // (else the warp only keeps the lane's steps)
             const unsigned long long path = mine ? trees[ring][w.node0 + token] : 0;
             // nodes that the row sees; nodes that are there
             unsigned long long tree = path;
@@ -708,62 +721,64 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                             top[y] = fmaxf(fmaxf(top[y], __uint_as_float(s[x + 2 * y])), __uint_as_float(s[x + 2 * y + 1]));
                 };
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                if (positive && clean) {
-                    // the whole tile in registers
-                    uint32_t s[4][32];
+                if (busy) {
+                    if (positive && clean) {
+                        // the whole tile in registers
+                        uint32_t s[4][32];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tc::tmem_ld32_nowait(s_addr + c * kChunk, s[c]);
-                    tc::tmem_ld_wait();
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) top_of(s[c], top);
-                    if (!settle(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])))) goto leave;
-                    const float off = (m == -INFINITY ? 0.0f : m * mult) - kWeightBits;
-                    const float2 mul2 = make_float2(mult, mult), sub2 = make_float2(-off, -off);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) weigh(s[c], mul2, sub2, s_addr + c * (kChunk / 2));
-                } else {
-                    // chunk by chunk, twice: the maximum, then the weights (a chunk's P lies over scores that
-                    // have been read)
-                    auto chunk = [&](int c, uint32_t (&s)[32]) {
-                        tc::tmem_ld32_nowait(s_addr + c * kChunk, s);
-                        const int at = key0 + c * kChunk;
-                        // the keys this row sees: before the tree from its window's first on and the sinks, then
-                        // of the tree
-                        const int hi = min(pos + 1, base) - at;
-                        const int lo = pos - at < p.mask.window ? 0 : pos - p.mask.window + 1 - at;
-                        uint32_t see = bits_between(lo, hi) | bits_between(0, min(p.mask.sinks - at, hi));
-                        const int shift = at - base;
-                        if (shift >= 0) see |= shift < 64 ? static_cast<uint32_t>(tree >> shift) : 0u;
-                        else if (shift > -32) see |= static_cast<uint32_t>(tree << -shift);
-                        uint32_t there = 0;
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            if ((blocks >> (4 * c + x)) & 1u) there |= 0xFFu << (8 * x);
-                        see &= there;
+                        for (int c = 0; c < 4; ++c) tc::tmem_ld32_nowait(s_addr + c * kChunk, s[c]);
                         tc::tmem_ld_wait();
-                        if (!positive) {
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * p.scale_log2);
-                        }
-                        if (__any_sync(FULL_MASK, see != 0xFFFFFFFFu)) {
+                        for (int c = 0; c < 4; ++c) top_of(s[c], top);
+                        if (!settle(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])))) goto leave;
+                        const float off = (m == -INFINITY ? 0.0f : m * mult) - kWeightBits;
+                        const float2 mul2 = make_float2(mult, mult), sub2 = make_float2(-off, -off);
 #pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                if (!(see & (1u << x))) s[x] = __float_as_uint(-INFINITY);
+                        for (int c = 0; c < 4; ++c) weigh(s[c], mul2, sub2, s_addr + c * (kChunk / 2));
+                    } else {
+                        // chunk by chunk, twice: the maximum, then the weights (a chunk's P lies over scores
+                        // that have been read)
+                        auto chunk = [&](int c, uint32_t (&s)[32]) {
+                            tc::tmem_ld32_nowait(s_addr + c * kChunk, s);
+                            const int at = key0 + c * kChunk;
+                            // the keys this row sees: before the tree from its window's first on and the sinks,
+                            // then of the tree
+                            const int hi = min(pos + 1, base) - at;
+                            const int lo = pos - at < p.mask.window ? 0 : pos - p.mask.window + 1 - at;
+                            uint32_t see = bits_between(lo, hi) | bits_between(0, min(p.mask.sinks - at, hi));
+                            const int shift = at - base;
+                            if (shift >= 0) see |= shift < 64 ? static_cast<uint32_t>(tree >> shift) : 0u;
+                            else if (shift > -32) see |= static_cast<uint32_t>(tree << -shift);
+                            uint32_t there = 0;
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                if ((blocks >> (4 * c + x)) & 1u) there |= 0xFFu << (8 * x);
+                            see &= there;
+                            tc::tmem_ld_wait();
+                            if (!positive) {
+#pragma unroll
+                                for (int x = 0; x < 32; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * p.scale_log2);
+                            }
+                            if (__any_sync(FULL_MASK, see != 0xFFFFFFFFu)) {
+#pragma unroll
+                                for (int x = 0; x < 32; ++x)
+                                    if (!(see & (1u << x))) s[x] = __float_as_uint(-INFINITY);
+                            }
+                        };
+                        uint32_t s[32];
+#pragma unroll 1
+                        for (int c = seen.x; c < seen.y; ++c) {
+                            chunk(c, s);
+                            top_of(s, top);
                         }
-                    };
-                    uint32_t s[32];
+                        if (!settle(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])))) goto leave;
+                        const float off = (m == -INFINITY ? 0.0f : m * mult) - kWeightBits;
+                        const float2 mul2 = make_float2(mult, mult), sub2 = make_float2(-off, -off);
 #pragma unroll 1
-                    for (int c = seen.x; c < seen.y; ++c) {
-                        chunk(c, s);
-                        top_of(s, top);
-                    }
-                    if (!settle(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])))) goto leave;
-                    const float off = (m == -INFINITY ? 0.0f : m * mult) - kWeightBits;
-                    const float2 mul2 = make_float2(mult, mult), sub2 = make_float2(-off, -off);
-#pragma unroll 1
-                    for (int c = seen.x; c < seen.y; ++c) {
-                        chunk(c, s);
-                        weigh(s, mul2, sub2, s_addr + c * (kChunk / 2));
+                        for (int c = seen.x; c < seen.y; ++c) {
+                            chunk(c, s);
+                            weigh(s, mul2, sub2, s_addr + c * (kChunk / 2));
+                        }
                     }
                 }
                 sum[0] = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
@@ -773,8 +788,8 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 __syncwarp();
                 // keeps this thread at most one phase behind o_done
                 if (C::kBufs == 2 && begun && !warp_wait(&o_done[0], (count - 1) & 1, &sh_dead, p.watchdog)) goto leave;
-                if (owed) {  // lane 0 has read this lane's O of the work before
-                    if (!warp_wait(&half_free, (halves - 1) & 1, &sh_dead, p.watchdog)) goto leave;
+                if (owed) {
+                    if (!warp_wait(&half_free[i], (given - 1) & 1, &sh_dead, p.watchdog)) goto leave;
                     owed = false;
                 }
                 if (lane == 0) mbar_arrive(&p_ready[buf]);
@@ -791,41 +806,39 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 l = 0.0f;
             }
             float f0 = 1.0f, f1 = 0.0f;
-            if (C::kLanes == 2 && turns) {
-                if (i == 1) {
-                    // what this lane has goes to lane 0
-                    if (owed) {  // (a work without a tile of this lane)
-                        if (!warp_wait(&half_free, (halves - 1) & 1, &sh_dead, p.watchdog)) goto leave;
-                    }
-                    half_ml[row] = make_float2(m, l);
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&half_done);
-                    owed = true;
-                    ++halves;
-                } else {
-                    if (!warp_wait(&half_done, halves & 1, &sh_dead, p.watchdog)) goto leave;
-                    tc::fence_after_sync();
-                    ++halves;
-                    const float2 ml = half_ml[row];
-                    const float both = fmaxf(m, ml.x);
-                    f0 = m == -INFINITY ? 0.0f : fast_exp2((m - both) * mult);
-                    f1 = ml.x == -INFINITY ? 0.0f : fast_exp2((ml.x - both) * mult);
-                    m = both;
-                    l = l * f0 + ml.y * f1;
-                }
+            const bool both = C::kLanes == 2 && turns && j1 - w.j0 > 1;  // both lanes have had tiles
+            const bool adds = !(C::kLanes == 2 && turns) || i == w.adder();
+            if (both && !adds) {
+                if (owed && !warp_wait(&half_free[i], (given - 1) & 1, &sh_dead, p.watchdog)) goto leave;  // (not reached: it has had a tile)
+                half_ml[i][row] = make_float2(m, l);
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&half_done[i]);
+                owed = true;
+                ++given;
+            } else if (both) {
+                if (!warp_wait(&half_done[i ^ 1], taken & 1, &sh_dead, p.watchdog)) goto leave;
+                tc::fence_after_sync();
+                ++taken;
+                const float2 ml = half_ml[i ^ 1][row];
+                const float top = fmaxf(m, ml.x);
+                f0 = m == -INFINITY ? 0.0f : fast_exp2((m - top) * mult);
+                f1 = ml.x == -INFINITY ? 0.0f : fast_exp2((ml.x - top) * mult);
+                m = top;
+                l = l * f0 + ml.y * f1;
             }
-            if (!(C::kLanes == 2 && turns && i == 1) && token - row_token < w.nodes) {
-                const bool add = C::kLanes == 2 && turns && __any_sync(FULL_MASK, f1 != 0.0f);
+            if (adds && busy) {
+                const bool add = both && __any_sync(FULL_MASK, f1 != 0.0f);
+                const uint32_t other_addr = tmem + lanes + C::kO + (i ^ 1) * D;
                 auto load = [&](int c, uint32_t (&o)[32]) {
                     tc::tmem_ld32_nowait(o_addr + c, o);
                     tc::tmem_ld_wait();
-                    if (C::kLanes == 2 && turns) {
+                    if (both) {
 #pragma unroll
                         for (int x = 0; x < 32; ++x) o[x] = f0 == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[x]) * f0);
                         if (add) {
                             uint32_t y[32];
-                            tc::tmem_ld32_nowait(o_addr + D + c, y);
+                            tc::tmem_ld32_nowait(other_addr + c, y);
                             tc::tmem_ld_wait();
 #pragma unroll
                             for (int x = 0; x < 32; ++x)
@@ -892,8 +905,10 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                     }
                 }
                 tc::fence_before_sync();
+            }
+            if (both && adds) {
                 __syncwarp();
-                if (C::kLanes == 2 && turns && lane == 0) mbar_arrive(&half_free);
+                if (lane == 0) mbar_arrive(&half_free[i ^ 1]);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&work_empty[ring]);
@@ -978,7 +993,7 @@ struct Rows {
 Rows rows_of(int n_nodes, int group, int head_dim) {
     Rows r;
     r.heads = group < kTcRows ? group : kTcRows;
-    r.nodes = kTcRows / r.heads;
+    r.nodes = kTcRows / r.heads < n_nodes ? kTcRows / r.heads : n_nodes;
     const int lanes = head_dim == 256 ? 1 : 2;
     r.blocks = (n_nodes + lanes * r.nodes - 1) / (lanes * r.nodes);
     r.record = lanes == 2 && n_nodes > r.nodes ? 2 * kTcRows : kTcRows;
@@ -987,10 +1002,12 @@ Rows rows_of(int n_nodes, int group, int head_dim) {
 
 constexpr size_t kJoinBytes = (kSMs * sizeof(TreeJoin) + 255) / 256 * 256;
 
-template <typename T, int D>
-gdn_status launch(const TreeAttnParams &p, int dtype, cudaStream_t s) {
-    using C = TreeTc<D>;
+template <typename T, int D, bool EXTRA>
+gdn_status launch(TreeAttnParams p, int dtype, cudaStream_t s) {
+    using C = TreeTc<D, EXTRA>;
     const int ps = 1 << p.cache.log2_ps;
+    const int q_bytes = p.q_rows * D * 2;
+    p.q_bufs = C::kLanes == 1 || 2 * q_bytes > C::kRoom ? 1 : 2;
     CUtensorMap q_map, k_map, v_map;
     const uint64_t rows = static_cast<uint64_t>(p.cache.n_pages) * p.cache.n_kv_heads * ps;
     GDN_TRY(encode_heads_map(&q_map, p.q, dtype, D, p.n_q_heads, static_cast<uint64_t>(p.n_seqs) * p.n_nodes,
@@ -998,21 +1015,28 @@ gdn_status launch(const TreeAttnParams &p, int dtype, cudaStream_t s) {
     GDN_TRY(encode_blocks_map(&k_map, p.k_pages, dtype, D, rows, D * 2, ps < kTcKeys ? ps : kTcKeys,
                               ps < kTcKeys ? 1 : C::kCols));
     GDN_TRY(encode_blocks_map(&v_map, p.v_pages, dtype, D, rows, D * 2, ps < C::kVKeys ? ps : C::kVKeys, D / 64));
-    auto kernel = attn_tree_tc_kernel<T, D>;
+    auto kernel = attn_tree_tc_kernel<T, D, EXTRA>;
     static std::atomic<unsigned long long> allowed{0};
-    GDN_TRY(allow_smem(kernel, C::kSmem, allowed));
-    kernel<<<kSMs, C::kThreads, C::kSmem, s>>>(q_map, k_map, v_map, p);
+    GDN_TRY(allow_smem(kernel, C::kRings + C::kRoom + 1024, allowed));
+    kernel<<<kSMs, C::kThreads, C::kRings + p.q_bufs * q_bytes + 1024, s>>>(q_map, k_map, v_map, p);
     GDN_TRY(launch_status());
     attn_tree_join_kernel<T, D><<<dim3(kSMs, kJoinParts), 128, 0, s>>>(p);
     return launch_status();
 }
 
+template <typename T, int D>
+gdn_status launch_rows(const TreeAttnParams &p, int dtype, cudaStream_t s) {
+    static_assert(TreeTc<D, false>::kRoom >= TreeTc<D, false>::kLanes * kTcRows * D * 2, "a whole Q for each lane");
+    const bool extra = p.blocks == 1 && p.record_rows == kTcRows && p.q_rows * D * 2 <= TreeTc<D, true>::kRoom;
+    return extra ? launch<T, D, true>(p, dtype, s) : launch<T, D, false>(p, dtype, s);
+}
+
 template <typename T>
 gdn_status launch_dim(int d, const TreeAttnParams &p, int dtype, cudaStream_t s) {
     switch (d) {
-        case 64: return launch<T, 64>(p, dtype, s);
-        case 128: return launch<T, 128>(p, dtype, s);
-        default: return launch<T, 256>(p, dtype, s);
+        case 64: return launch_rows<T, 64>(p, dtype, s);
+        case 128: return launch_rows<T, 128>(p, dtype, s);
+        default: return launch_rows<T, 256>(p, dtype, s);
     }
 }
 
@@ -1032,6 +1056,7 @@ gdn_status launch_attn_tree_tc(TreeAttnParams p, int dtype, int head_dim, void *
     p.head_groups = (p.group + r.heads - 1) / r.heads;
     p.blocks = r.blocks;
     p.record_rows = r.record;
+    p.q_rows = (r.heads * r.nodes + 7) / 8 * 8;
     // the ranges are counted in 32 bits
     const long long widest = ((static_cast<long long>(p.cache.max_pages) << p.cache.log2_ps) + kTcKeys - 1) / kTcKeys + 2 + kTurn;
     if (widest * p.cache.n_kv_heads * p.head_groups * p.blocks > 0x7fffffffLL / p.n_seqs) return GDN_ERR_UNSUPPORTED;
