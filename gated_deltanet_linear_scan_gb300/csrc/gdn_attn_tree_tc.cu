@@ -39,12 +39,12 @@ struct TreeTc {
     static constexpr int kVKeys = kTcKeys / kSubs;
     static constexpr int kLog2VKeys = kSubs == 2 ? 6 : 7;
     static constexpr int kRings = (kKSlots + kVSlots) * kSlotBytes;
-    static constexpr int kRoom = 232448 - 1024 - (D == 256 ? 2048 : 4864) - kRings;  // for Q
+    static constexpr int kRoom = 232448 - 1024 - (D == 256 ? 2048 : 5632) - kRings;  // for Q
     static constexpr int kSoftmax = kLanes * 4;
     static constexpr int kMma = kSoftmax, kK = kMma + 1, kSched = kMma + 3;
     static constexpr int kThreads = (kSoftmax + 4) * 32;
     static constexpr int kS = 0, kO = 256;  // tensor-memory columns
-    static constexpr int kWorks = D == 256 ? 2 : 3;  // entries of the work ring (what shared memory has left)
+    static constexpr int kWorks = D == 256 ? 2 : 4;  // entries of the work ring (what shared memory has left)
 };
 
 // A segment: the part of a unit in this CTA's range.
@@ -54,17 +54,17 @@ struct Work {
     int base, len;                                   // position of a root; cache rows
     int n_sink, main0;                               // the unit's key tiles: a TileWalk
     int j0, j1;                                      // those of the segment
-    int g0;                                          // number of the first over all segments
+    int g0, t0;                                      // numbers of the first tile, and lane's turn, over all segments
     int turns;                                       // the lanes take the tiles in turn
     int q_buf[2];                                    // the lanes' Q buffers
     int whole, head;                                 // nothing of the unit elsewhere; it begins in this range
 
     __device__ __forceinline__ int tile(int j) const { return j < n_sink ? j : main0 + j - n_sink; }
     // lane i's first tile (the lanes' turns go on from one segment to the next), and from one to the next
-    __device__ __forceinline__ int first(int i) const { return turns ? j0 + ((g0 + i) & 1) : j0; }
+    __device__ __forceinline__ int first(int i) const { return turns ? j0 + ((t0 + i) & 1) : j0; }
     __device__ __forceinline__ int step() const { return turns ? 2 : 1; }
     // whose turn the last tile is: that lane adds the other's sums to its own
-    __device__ __forceinline__ int adder() const { return (g0 + j1 - 1 - j0) & 1; }
+    __device__ __forceinline__ int adder() const { return (t0 + j1 - 1 - j0) & 1; }
 };
 
 template <typename T, int D, bool EXTRA>
@@ -206,7 +206,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         const bool leader = elect_one();  // these warps run converged, one elected lane issuing
         if (warp == C::kSched) {
             // ------------------------------------------------------ the scheduling warp
-            int ring = 0, round = 0, q_uses[2] = {0, 0}, next_buf = 0, g = 0;
+            int ring = 0, round = 0, q_uses[2] = {0, 0}, next_buf = 0, g = 0, t = 0;
             int n = sh_seq, slot = sh_slot, len = sh_len, tree_of = -1;
             unsigned seq_begin = sh_seq_begin, at = begin;
             TileWalk walk{0, 0, 0};
@@ -240,9 +240,11 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 w.main0 = walk.main0;
                 w.j0 = static_cast<int>(at - unit_begin);
                 w.j1 = static_cast<int>(seg_end - unit_begin);
-                w.g0 = g;
-                g += w.j1 - w.j0;
                 w.turns = C::kLanes == 2 && w.nodes <= per;
+                w.g0 = g;
+                w.t0 = t;
+                g += w.j1 - w.j0;
+                t += (w.j1 - w.j0) * (C::kLanes == 2 && !w.turns ? 2 : 1);
                 w.whole = at == unit_begin && seg_end == unit_end;
                 w.head = unit_begin >= begin;
                 // rows of its own for each lane, or one Q for both: the buffers in turn
@@ -326,57 +328,81 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
             for (int x = 0; x < C::kVKeys / 16; ++x)
                 v_step[x] = (((x * 16) >> log2_bv) * (bv * D * 2) + ((x * 16) & (bv - 1)) * 128) >> 4;
-            int s_count = 0, o_count = 0;         // products issued (one lane: its buffer)
-            uint32_t o_phase = 0, q_phase = 0;    // bit i: of lane i's p_ready; of Q buffer i's q_full
-            int q_work0 = -1, q_work1 = -1;       // the work whose Q has arrived in the buffers
-            int s_left0 = 0, s_left1 = 0;         // S products to come of an even, an odd work whose Q both lanes use
-            // The S products' own places: each lane's last one issued (work, tile), -1 before a work's first.
-            int s_work0 = 0, s_work1 = 0, s_tile0 = -1, s_tile1 = -1;
-            // (The functions below return false when a wait gave up. Their code stands once, in rolled
-            // loops.) S of lane i over tile j of work n
-            auto issue_s = [&](int i, int n, int j) {
-                const Work &w = works[n % kWorks];
-                const int g = w.g0 + j - w.j0, buf = C::kBufs == 2 ? s_count & 1 : i;
-                const int q_buf = w.q_buf[i], turns = w.turns, j1 = w.j1, count = w.j1 - w.j0;
-                ++s_count;
+            // The products run through all segments' tiles in one order, lane by lane in turn (a tile of rows
+            // of its own for each lane has a turn of both); with one lane, S buffer by S buffer. S runs
+            // kLanes turns ahead of O: a lane's next S is issued right behind its O.
+            struct Place {
+                int n, j, j1, g;    // segments begun; tile, the segment's end, the tile's number
+                int left;           // turns left of the tile
+                int turns, t;       // of the segment; the turn's number
+                bool over;
+            };
+            Place sp{0, 0, 0, 0, 0, 0, 0, false}, op{0, 0, 0, 0, 0, 0, 0, false};
+            uint32_t q_new = 0, q_phase = 0;  // bit b: Q buffer b's contents are still to be waited for; its phase
+            int q_bufs = 0, o_first = 0;      // bit i: lane i's buffer; tiles of the segment before op's
+            // (The functions below return false when a wait gave up.) Opens the next segment; over when none.
+            auto open = [&](Place &at) {
+                if (!warp_wait(&work_full[at.n % kWorks], (at.n / kWorks) & 1, &sh_dead, p.watchdog)) return false;
+                const Work &w = works[at.n % kWorks];
+                at.over = !w.valid;
+                at.j = w.j0;
+                at.j1 = w.j1;
+                at.g = w.g0;
+                at.turns = w.turns;
+                at.left = C::kLanes == 2 && !at.turns ? 2 : 1;
+                ++at.n;
+                return true;
+            };
+            auto step = [&](Place &at) {
+                ++at.t;
+                if (--at.left == 0) {
+                    ++at.j;
+                    ++at.g;
+                    at.left = C::kLanes == 2 && !at.turns ? 2 : 1;
+                }
+            };
+            auto next_s = [&] {
+                if (sp.over) return true;
+                if (sp.j == sp.j1) {
+                    if (!open(sp)) return false;
+                    if (sp.over) return true;
+                    const Work &w = works[(sp.n - 1) % kWorks];
+                    q_bufs = w.q_buf[0] | w.q_buf[1] << 1;
+                    q_new = C::kLanes == 1 ? 1u : sp.turns ? 1u << w.q_buf[0] : 3u;
+                }
+                const int i = C::kLanes == 1 ? 0 : sp.t & 1, buf = sp.t & 1, g = sp.g;
+                const int q_buf = (q_bufs >> i) & 1;
                 const int slot0 = (g * C::kSubs) % C::kKSlots;
                 if (!warp_wait(&k_full[slot0], (g * C::kSubs / C::kKSlots) & 1, &sh_dead, p.watchdog)) return false;
                 const TileNote note{static_cast<volatile uint32_t *>(notes)[g % kNotes]};
-                if ((q_buf ? q_work1 : q_work0) != n) {
+                if ((q_new >> q_buf) & 1u) {
                     if (!warp_wait(&q_full[q_buf], (q_phase >> q_buf) & 1, &sh_dead, p.watchdog)) return false;
                     q_phase ^= 1u << q_buf;
-                    if (q_buf) q_work1 = n;
-                    else q_work0 = n;
-                    if (n & 1) s_left1 = count;
-                    else s_left0 = count;
+                    q_new &= ~(1u << q_buf);
                 }
-                // K's last product: the lane's, or with rows of its own for each the second of the two (either
-                // lane may be the one ahead)
-                const int o_work = i ? s_work0 : s_work1, o_tile = i ? s_tile0 : s_tile1;
-                const bool release = C::kLanes == 1 || turns || o_work > n || (o_work == n && o_tile >= j);
-                // the Q buffer's last product: the lane's own, or of a Q that both use the last of all
-                bool last = j + 1 == j1;
-                if (turns) last = (n & 1 ? --s_left1 : --s_left0) == 0;
+                // the tile's last turn lets K go, the segment's last tile (of the lane, where it has a Q of its
+                // own) Q
+                const bool release = sp.left == 1, last = sp.j + 1 == sp.j1;
                 const int from = note.begin(0) * kChunk;
                 const uint32_t to = tmem + C::kS + buf * kTcKeys + from;
                 const uint32_t idesc = tc::idesc_16bit(kBf16, kTcRows, 0, false) |
                                        static_cast<uint32_t>(note.end(0) - note.begin(0)) << (17 + 2);
                 const uint64_t q0 = q_desc + ((q_buf * q_bytes) >> 4);
-                const int q_col = p.q_rows * 128;
+                const uint32_t q_col = p.q_rows * 8;  // 128-byte columns of Q, in 16-byte units
 #pragma unroll
                 for (int s = 0; s < C::kSubs; ++s) {
                     const int slot = (g * C::kSubs + s) % C::kKSlots;
                     if (s > 0 && !warp_wait(&k_full[slot], ((g * C::kSubs + s) / C::kKSlots) & 1, &sh_dead, p.watchdog)) return false;
                     tc::fence_after_sync();
                     const uint64_t k = k_desc + ((slot * C::kSlotBytes + from * 128) >> 4);
-                    const uint64_t q = q0 + ((s * C::kCols * q_col) >> 4);
+                    const uint64_t q = q0 + s * C::kCols * q_col;
                     if (leader) {
 #pragma unroll
                         for (int c = 0; c < C::kCols; ++c)
 #pragma unroll
                             for (int x = 0; x < 4; ++x)
-                                tc::mma_bf16(to, q + ((c * q_col + x * 32) >> 4),
-                                             k + ((c * kTcKeys * 128 + x * 32) >> 4), idesc, s + c + x > 0);
+                                tc::mma_bf16(to, q + (c * q_col + x * 2), k + ((c * kTcKeys * 128 + x * 32) >> 4), idesc,
+                                             s + c + x > 0);
                         if (release) tc::mma_commit(&k_empty[slot]);
                         if (s == C::kSubs - 1) {
                             tc::mma_commit(&s_full[buf]);
@@ -385,19 +411,15 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                     }
                     __syncwarp();
                 }
+                step(sp);
                 return true;
             };
-            // O of lane i += P V over tile j of work n
-            auto issue_o = [&](int i, int n, int j) {
-                const Work &w = works[n % kWorks];
-                const int g = w.g0 + j - w.j0, buf = C::kBufs == 2 ? o_count & 1 : i;
-                const uint32_t phase = C::kBufs == 2 ? (o_count >> 1) & 1 : (o_phase >> i) & 1;
-                const bool release = C::kLanes == 1 || w.turns || i == 1, first = j == w.first(i);
-                ++o_count;
-                o_phase ^= 1u << i;
+            auto next_o = [&] {
+                const int i = C::kLanes == 1 ? 0 : op.t & 1, buf = op.t & 1, g = op.g;
+                const bool first = op.turns ? o_first < 2 : o_first == 0, release = op.left == 1;
                 const TileNote note{static_cast<volatile uint32_t *>(notes)[g % kNotes]};
                 const int from = note.begin(0) * (kChunk / 16), to = note.end(0) * (kChunk / 16);
-                if (!warp_wait(&p_ready[buf], phase, &sh_dead, p.watchdog)) return false;
+                if (!warp_wait(&p_ready[buf], (op.t >> 1) & 1, &sh_dead, p.watchdog)) return false;
 #pragma unroll
                 for (int s = 0; s < C::kSubs; ++s) {
                     const int slot = (g * C::kSubs + s) % C::kVSlots;
@@ -414,8 +436,8 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                             const int x0 = max(from - s * (C::kVKeys / 16), 0), x1 = min(to - s * (C::kVKeys / 16), C::kVKeys / 16);
 #pragma unroll 1
                             for (int x = x0; x < x1; ++x) {
-                                const uint32_t step = (((x * 16) >> log2_bv) * (bv * D * 2) + ((x * 16) & (bv - 1)) * 128) >> 4;
-                                tc::mma_bf16_ts(o, pw + x * 8, v + step, kIdescO, !first || s * (C::kVKeys / 16) + x > from);
+                                const uint32_t at = (((x * 16) >> log2_bv) * (bv * D * 2) + ((x * 16) & (bv - 1)) * 128) >> 4;
+                                tc::mma_bf16_ts(o, pw + x * 8, v + at, kIdescO, !first || s * (C::kVKeys / 16) + x > from);
                             }
                         }
                         if (release) tc::mma_commit(&v_empty[slot]);
@@ -423,69 +445,28 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                     }
                     __syncwarp();
                 }
+                if (op.left == 1) ++o_first;
+                step(op);
                 return true;
             };
-            // Issues S of lane i's next tile, unless that lies behind work `most` (so that the work ring
-            // never waits for work that waits for it) or there is none; done: whether it did.
-            auto next_s = [&](int i, int most, bool &done) {
-                int n = i ? s_work1 : s_work0, tile = i ? s_tile1 : s_tile0;
-                done = false;
-                bool ok = true;
-                while (n <= most) {
-                    ok = warp_wait(&work_full[n % kWorks], (n / kWorks) & 1, &sh_dead, p.watchdog);
-                    if (!ok) break;
-                    const Work &w = works[n % kWorks];
-                    if (!w.valid) break;
-                    const int j = tile < 0 ? w.first(i) : tile + w.step();
-                    if (j < w.j1) {
-                        tile = j;
-                        done = true;
-                        break;
+#pragma unroll 1
+            for (int i = 0; i < C::kLanes; ++i)
+                if (!next_s()) goto leave;
+            for (;;) {
+                if (op.j == op.j1) {
+                    if (op.n > 0) {
+                        if (leader) mbar_arrive(&work_empty[(op.n - 1) % kWorks]);
+                        __syncwarp();
                     }
-                    tile = -1;
-                    ++n;
+                    o_first = 0;
+                    if (!open(op)) goto leave;
+                    if (op.over) break;
                 }
-                if (i) {
-                    s_work1 = n;
-                    s_tile1 = tile;
+                if constexpr (C::kLanes == 1) {
+                    if (!next_s() || !next_o()) goto leave;  // into the other buffer, ahead of this tile's O
                 } else {
-                    s_work0 = n;
-                    s_tile0 = tile;
+                    if (!next_o() || !next_s()) goto leave;
                 }
-                return ok && (!done || issue_s(i, n, tile));
-            };
-            uint32_t ahead = 0;  // bit i: an S product of lane i waits for its O
-            for (int n = 0;; ++n) {
-                if (!warp_wait(&work_full[n % kWorks], (n / kWorks) & 1, &sh_dead, p.watchdog)) goto leave;
-                if (!works[n % kWorks].valid) break;
-                const int j0 = works[n % kWorks].j0, j1 = works[n % kWorks].j1, turns = works[n % kWorks].turns;
-                const int g0 = works[n % kWorks].g0;
-                bool done;
-#pragma unroll 1
-                for (int k = 0; k < C::kLanes; ++k) {
-                    // (this work's first; the other lane may go on to the next work's)
-                    const int i = C::kLanes == 1 ? 0 : (turns ? (g0 + k) & 1 : k);
-                    if ((ahead >> i) & 1u) continue;
-                    if (!next_s(i, C::kLanes == 1 ? n : n + 1, done)) goto leave;
-                    ahead |= static_cast<uint32_t>(done) << i;
-                }
-#pragma unroll 1
-                for (int j = j0; j < j1; ++j) {
-#pragma unroll 1
-                    for (int i = 0; i < C::kLanes; ++i) {
-                        if (turns && ((g0 + j - j0) & 1) != i) continue;
-                        if constexpr (C::kLanes == 1) {
-                            // into the other buffer, ahead of this tile's O
-                            if (!next_s(0, n + 1, done) || !issue_o(0, n, j)) goto leave;
-                            ahead = done;
-                        } else {
-                            if (!issue_o(i, n, j) || !next_s(i, n + 1, done)) goto leave;
-                            ahead = (ahead & ~(1u << i)) | static_cast<uint32_t>(done) << i;
-                        }
-                    }
-                }
-                if (leader) mbar_arrive(&work_empty[n % kWorks]);
-                __syncwarp();
             }
         } else {
             // ------------------------------------------------------ the K and the V warp
@@ -623,8 +604,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                     }
                 }
             }
-            const unsigned long long nodes = __ballot_sync(FULL_MASK, trees[ring][lane] != 0) |
-                static_cast<unsigned long long>(__ballot_sync(FULL_MASK, trees[ring][lane + 32] != 0)) << 32;
+            const bool any_node = __any_sync(FULL_MASK, (trees[ring][lane] | trees[ring][lane + 32]) != 0);
             const int pos = base + __popcll(path) - 1;
             float m = -INFINITY, l = 0.0f;
             bool begun = false;
@@ -642,7 +622,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 const bool clean = blocks == 0xFFFFu && key0 + kTcKeys - 1 < base &&
                                    (len - 1 - key0 < p.mask.window || key0 + kTcKeys <= p.mask.sinks);
                 // every key is seen by some row of the tree
-                const bool alive = blocks == 0xFFFFu && key0 + kTcKeys - 1 < base && nodes != 0 &&
+                const bool alive = blocks == 0xFFFFu && key0 + kTcKeys - 1 < base && any_node &&
                                    (base - key0 < p.mask.window || key0 + kTcKeys <= p.mask.sinks);
                 if (!alive) {
                     // V rows that no row of the tree sees are cleared (by both lanes where both multiply
@@ -652,9 +632,9 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                     // from the one waited for.)
                     if (C::kBufs == 2 && begun && !warp_wait(&o_done[0], (count - 1) & 1, &sh_dead, p.watchdog)) goto leave;
                     const int key = key0 + row;
-                    const bool dead = !((blocks >> (row >> 3)) & 1u) || key >= len || nodes == 0 ||
+                    const bool dead = !((blocks >> (row >> 3)) & 1u) || key >= len || !any_node ||
                                       !(base - key < p.mask.window || key < p.mask.sinks) ||
-                                      (key >= base && !((nodes >> ((key - base) & 63)) & 1u));
+                                      (key >= base && trees[ring][(key - base) & 63] == 0);
                     for (int y = 0; y < C::kSubs; ++y) {
                         const int g = (g0 + j) * C::kSubs + y, slot = g % C::kVSlots;
                         if (!warp_wait(&v_full[slot], (g / C::kVSlots) & 1, &sh_dead, p.watchdog)) goto leave;
@@ -722,7 +702,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 };
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                 if (busy) {
-                    if (positive && clean) {
+                    if (!EXTRA && positive && clean) {
                         // the whole tile in registers
                         uint32_t s[4][32];
 #pragma unroll
@@ -737,9 +717,14 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                         for (int c = 0; c < 4; ++c) weigh(s[c], mul2, sub2, s_addr + c * (kChunk / 2));
                     } else {
                         // chunk by chunk, twice: the maximum, then the weights (a chunk's P lies over scores
-                        // that have been read)
+                        // that have been read). With few rows every tile goes this way: the one warp that has
+                        // rows waits for its instructions more than for its data, and this code stays near.
                         auto chunk = [&](int c, uint32_t (&s)[32]) {
                             tc::tmem_ld32_nowait(s_addr + c * kChunk, s);
+                            if (positive && clean) {
+                                tc::tmem_ld_wait();
+                                return;
+                            }
                             const int at = key0 + c * kChunk;
                             // the keys this row sees: before the tree from its window's first on and the sinks,
                             // then of the tree
@@ -830,79 +815,51 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
             if (adds && busy) {
                 const bool add = both && __any_sync(FULL_MASK, f1 != 0.0f);
                 const uint32_t other_addr = tmem + lanes + C::kO + (i ^ 1) * D;
-                auto load = [&](int c, uint32_t (&o)[32]) {
-                    tc::tmem_ld32_nowait(o_addr + c, o);
-                    tc::tmem_ld_wait();
-                    if (both) {
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) o[x] = f0 == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[x]) * f0);
-                        if (add) {
-                            uint32_t y[32];
-                            tc::tmem_ld32_nowait(other_addr + c, y);
-                            tc::tmem_ld_wait();
-#pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                if (f1 != 0.0f) o[x] = __float_as_uint(fmaf(__uint_as_float(y[x]), f1, __uint_as_float(o[x])));
-                        }
-                    }
-                };
-                if (w.whole) {
-                    const long long at = mine ? (static_cast<long long>(w.seq) * p.n_nodes + w.node0 + token) * p.n_q_heads + w.head0 + row_head : -1;
-                    // Four lanes write a row's 64 bytes together, row after row of their four: eight lines a
-                    // store instead of 32.
-                    long long rows[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) rows[r] = __shfl_sync(FULL_MASK, at, (lane & ~3) + r);
-                    T *out = static_cast<T *>(p.out) + (lane & 3) * 8;
-                    const float inv = 1.0f / l;
+                // this lane's sums and the other's, 32 columns at a time, by factors
+                const float inv = w.whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+                const float2 mine2 = make_float2(f0 * inv, f0 * inv), other2 = make_float2(f1 * inv, f1 * inv);
+                T *out = static_cast<T *>(p.out) +
+                         ((static_cast<long long>(w.seq) * p.n_nodes + w.node0 + token) * p.n_q_heads + w.head0 + row_head) * D;
+                float *record = p.record(blockIdx.x, w.head ? 1 : 0, D);
+                const int r = (turns ? 0 : i * kTcRows) + row;
+                float *sums = record + static_cast<size_t>(r) * D;
+                const bool nothing = l == 0.0f;
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        load(c, o);
-                        uint32_t pw[4][4];  // 16 bytes of this row at a time; then of the four lanes' rows
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32], y[32];
+                    tc::tmem_ld32_nowait(o_addr + c, o);
+                    if (add) tc::tmem_ld32_nowait(other_addr + c, y);
+                    tc::tmem_ld_wait();
+                    float2 z[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                        z[x] = __fmul2_rn(make_float2(__uint_as_float(o[2 * x]), __uint_as_float(o[2 * x + 1])), mine2);
+                    if (add) {
 #pragma unroll
                         for (int x = 0; x < 16; ++x)
-                            pw[x / 4][x % 4] = l == 0.0f ? 0u
-                                                         : Elem<T>::pack(__uint_as_float(o[2 * x]) * inv,
-                                                                         __uint_as_float(o[2 * x + 1]) * inv);
-#pragma unroll
-                        for (int bit = 1; bit < 4; bit *= 2) {
-                            const bool upper = lane & bit;
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                if (r & bit) continue;
-#pragma unroll
-                                for (int y = 0; y < 4; ++y) {
-                                    const uint32_t got = __shfl_xor_sync(FULL_MASK, upper ? pw[r][y] : pw[r | bit][y], bit);
-                                    if (upper) pw[r][y] = got;
-                                    else pw[r | bit][y] = got;
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (rows[r] >= 0)
-                                *reinterpret_cast<uint4 *>(out + rows[r] * D + c) =
-                                    make_uint4(pw[r][0], pw[r][1], pw[r][2], pw[r][3]);
+                            z[x] = __ffma2_rn(make_float2(__uint_as_float(y[2 * x]), __uint_as_float(y[2 * x + 1])), other2, z[x]);
                     }
-                } else {
-                    float *record = p.record(blockIdx.x, w.head ? 1 : 0, D);
-                    const int r = (turns ? 0 : i * kTcRows) + row;
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        load(c, o);
-                        if (!mine) continue;
-                        float4 *to = reinterpret_cast<float4 *>(record + static_cast<size_t>(r) * D + c);
+                    if (!mine) continue;
+                    if (w.whole) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            uint4 pw;
+                            pw.x = nothing ? 0u : Elem<T>::pack(z[4 * x].x, z[4 * x].y);
+                            pw.y = nothing ? 0u : Elem<T>::pack(z[4 * x + 1].x, z[4 * x + 1].y);
+                            pw.z = nothing ? 0u : Elem<T>::pack(z[4 * x + 2].x, z[4 * x + 2].y);
+                            pw.w = nothing ? 0u : Elem<T>::pack(z[4 * x + 3].x, z[4 * x + 3].y);
+                            *reinterpret_cast<uint4 *>(out + c + 8 * x) = pw;
+                        }
+                    } else {
 #pragma unroll
                         for (int x = 0; x < 8; ++x)
-                            to[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
-                                                __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+                            *reinterpret_cast<float4 *>(sums + c + 4 * x) =
+                                make_float4(z[2 * x].x, z[2 * x].y, z[2 * x + 1].x, z[2 * x + 1].y);
                     }
-                    if (mine) {
-                        record[p.record_rows * D + r] = m == -INFINITY ? -INFINITY : m * mult;
-                        record[p.record_rows * (D + 1) + r] = l;
-                    }
+                }
+                if (!w.whole && mine) {
+                    record[p.record_rows * D + r] = m == -INFINITY ? -INFINITY : m * mult;
+                    record[p.record_rows * (D + 1) + r] = l;
                 }
                 tc::fence_before_sync();
             }
