@@ -19,15 +19,7 @@ unsigned read_and_clear_watchdog_attn_decode(cudaStream_t s) {
 
 unsigned *watchdog_attn_decode() {
     static std::atomic<unsigned *> known[64];
-    int device = 0;
-    if (cudaGetDevice(&device) != cudaSuccess) return nullptr;
-    unsigned *at = device < 64 ? known[device].load(std::memory_order_relaxed) : nullptr;
-    if (at != nullptr) return at;
-    void *found = nullptr;
-    if (cudaGetSymbolAddress(&found, g_watchdog_attn_decode) != cudaSuccess) return nullptr;
-    at = static_cast<unsigned *>(found);
-    if (device < 64) known[device].store(at, std::memory_order_relaxed);
-    return at;
+    return flag_address(g_watchdog_attn_decode, known);
 }
 
 }  // namespace gdn

@@ -22,6 +22,7 @@
 
 #include "gdn_device.cuh"
 #include "gdn_internal.h"
+#include "gdn_paged.cuh"  // flag_address
 
 namespace gdn {
 namespace {
@@ -722,6 +723,11 @@ gdn_status launch_wait_probe_block(bool arm, uint64_t limit_ns, float *out, cuda
 
 unsigned read_and_clear_watchdog_block(cudaStream_t s) {
     return read_and_clear_flag(g_watchdog, s);
+}
+
+unsigned *watchdog_block() {
+    static std::atomic<unsigned *> known[64];
+    return flag_address(g_watchdog, known);
 }
 
 }  // namespace gdn

@@ -9,6 +9,8 @@
 // So the state is read once for all nodes and not written: a tree of N nodes moves 1 / (N + 1) of
 // the bytes of a scan that keeps a snapshot per node. What an accepted path needs later are k, g
 // and u of its nodes (the tape): its state is one more rank-L update, read and written once.
+#include "gdn_paged.cuh"
+#include "gdn_tc.cuh"
 #include "gdn_tree.cuh"
 
 namespace gdn {
@@ -53,6 +55,7 @@ struct TreeParams {
     float *k, *g, *u;             // the tape
     float *q, *v, *beta, *gram;   // scratch
     int *there;
+    unsigned *watchdog;
 };
 
 // ------------------------------------------------------------------ conv, norms and gates
@@ -364,6 +367,244 @@ __global__ void __launch_bounds__(kStateThreads) tree_state_kernel(const TreePar
     }
 }
 
+// ------------------------------------------------------------------ the same on the tensor cores
+
+// State size 128: all products of a head's state with its nodes' k and q are one tcgen05 product
+// D = S [K; Q]^T, and the nodes' sums and the gated norm follow in the same CTA, so a state is read
+// once and y never leaves the SM. One CTA per (sequence, v-head), 256 threads; two CTAs share an SM
+// as long as 16 nodes fill half of tensor memory.
+//
+// The products keep fp32's precision: each operand is split into three bf16 parts, x = x1 + x2 + x3
+// (8 bits each, the rest below 2^-27 of x), and the six products of parts whose sizes multiply to
+// 2^-18 or more are summed in fp32; what is left out is below 2^-25 of |S| |k|. (Two parts would leave
+// 2^-16, a hundred times the error of fp32 arithmetic.) The state's parts lie in tensor memory (lane =
+// value channel j), the nodes' in shared memory: three images of [K; Q], K-major core matrices.
+// S1 and S2 multiply the first two images at once, into two column groups that are added up later.
+constexpr int kTcThreads = 256;
+constexpr uint32_t kColA = 0, kColD = 192;  // tensor memory: the state's parts, 64 columns each; D, two groups
+
+struct TcSmem {
+    int pad, rows;               // nodes, and vectors, of an image (a multiple of 8, of 16)
+    uint32_t images, coef, bytes;
+    __host__ __device__ explicit TcSmem(int n) {
+        pad = (n + 7) / 8 * 8;
+        rows = 2 * pad;
+        images = 65536;                                         // behind the state, [4][128 rows][128 bytes]
+        coef = images + 3u * static_cast<uint32_t>(rows) * 256u;
+        bytes = coef + static_cast<uint32_t>(n * n) * 8u;
+    }
+    __host__ __device__ uint32_t tmem_cols() const { return kColD + 2u * static_cast<uint32_t>(rows) <= 256u ? 256u : 512u; }
+};
+
+// x = p1 + p2 + p3 in bf16, two values to a word.
+__device__ __forceinline__ void split3(float a, float b, uint32_t &p1, uint32_t &p2, uint32_t &p3) {
+    p1 = tc::pack_bf16x2(a, b);
+    a = __fsub_rn(a, __uint_as_float(p1 << 16));
+    b = __fsub_rn(b, __uint_as_float(p1 & 0xFFFF0000u));
+    p2 = tc::pack_bf16x2(a, b);
+    a = __fsub_rn(a, __uint_as_float(p2 << 16));
+    b = __fsub_rn(b, __uint_as_float(p2 & 0xFFFF0000u));
+    p3 = tc::pack_bf16x2(a, b);
+}
+
+__global__ void __launch_bounds__(kTcThreads, 2) tree_state_tc_kernel(const __grid_constant__ CUtensorMap state_map,
+                                                                      const TreeParams p) {
+    constexpr int S = 128;
+    extern __shared__ uint8_t dyn[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+    __shared__ __align__(8) uint64_t state_full, d_full;
+    __shared__ uint32_t tmem_base;
+    __shared__ unsigned long long path_of[kMaxNodes];
+    __shared__ int up[kMaxNodes];
+    __shared__ float g_of[kMaxNodes], hi_of[kMaxNodes], lo_of[kMaxNodes], beta_of[kMaxNodes], decay[kMaxNodes];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int N = p.n_nodes, Hk = p.n_k_heads, H = p.n_v_heads;
+    const int vh = blockIdx.x % H, n = blockIdx.x / H, kh = vh % Hk;
+    const int slot = p.slots ? p.slots[n] : n;
+    if (slot < 0 || slot >= p.pool) return;
+    const TcSmem L(N);
+    float *d = reinterpret_cast<float *>(smem);  // later, over the state: [2N][128] products with k, then u; with q, then y
+    float2 *coef = reinterpret_cast<float2 *>(smem + L.coef);
+    const size_t row0 = static_cast<size_t>(n) * N;
+
+    if (tid == 0) {
+        mbar_init(&state_full, 1);
+        mbar_init(&d_full, 1);
+        fence_mbar_init();
+        mbar_arrive_expect_tx(&state_full, S * S * 4);
+        tma_load_3d(smem, &state_map, 0, (slot * H + vh) * S, 0, &state_full);
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(&tmem_base, L.tmem_cols());
+        tc::tmem_relinquish();  // (another CTA's turn)
+    }
+    if (warp == 2) {
+        unsigned long long paths[2];
+        tree_paths(p.parents + row0, N, paths, path_of, up);
+    }
+    if (tid >= 128 && tid < 128 + N) {
+        g_of[tid - 128] = p.g[(row0 + tid - 128) * H + vh];
+        beta_of[tid - 128] = p.beta[(row0 + tid - 128) * H + vh];
+    }
+    // ---- the images of [K; Q], rows past the nodes zero
+    for (int x = tid; x < L.rows * (S / 8); x += kTcThreads) {
+        const int r = x / (S / 8), c = x % (S / 8), i = r < L.pad ? r : r - L.pad;
+        float v[8] = {};
+        if (i < N) load_vec<8>(v, (r < L.pad ? p.k : p.q) + ((row0 + i) * Hk + kh) * S + 8 * c);
+        uint32_t w[3][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split3(v[2 * e], v[2 * e + 1], w[0][e], w[1][e], w[2][e]);
+        uint8_t *to = smem + L.images + tc::kmajor_offset16(r, 8 * c, 128, S / 8 * 128);
+#pragma unroll
+        for (int y = 0; y < 3; ++y)
+            *reinterpret_cast<uint4 *>(to + y * L.rows * 256) = make_uint4(w[y][0], w[y][1], w[y][2], w[y][3]);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_base;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const int half = warp >> 2, j = (warp & 3) * 32 + lane;  // state row of this thread, which half of its cells
+    if (tid < N) {
+        path_sum(path_of[tid], g_of, hi_of[tid], lo_of[tid]);
+        decay[tid] = expf(hi_of[tid] + lo_of[tid]);
+    }
+    // ---- the state's parts
+    bool ok = mbar_wait(&state_full, 0);
+    if (ok) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {  // 32 cells: a 128-byte column
+            const int col = 2 * half + b;
+            uint32_t w1[16], w2[16], w3[16];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float4 x = *reinterpret_cast<const float4 *>(smem + col * 16384 + j * 128 + ((c ^ (j & 7)) << 4));
+                split3(x.x, x.y, w1[2 * c], w2[2 * c], w3[2 * c]);
+                split3(x.z, x.w, w1[2 * c + 1], w2[2 * c + 1], w3[2 * c + 1]);
+            }
+            tc::tmem_st16(lanes + kColA + 16 * col, w1);
+            tc::tmem_st16(lanes + kColA + 64 + 16 * col, w2);
+            tc::tmem_st16(lanes + kColA + 128 + 16 * col, w3);
+        }
+        tc::tmem_st_wait();
+    }
+    fence_proxy_async_smem();  // the images, before the products read them
+    tc::fence_before_sync();
+    ok = __syncthreads_and(ok);
+    tc::fence_after_sync();
+    if (ok && warp == 0) {
+        if (elect_one()) {
+            const uint64_t image = tc::smem_desc(smem + L.images, 128, S / 8 * 128);
+            const uint32_t part = static_cast<uint32_t>(L.rows) * 256u >> 4;  // from an image to the next, in 16 bytes
+            const uint32_t wide = tc::idesc_bf16(128, 2 * L.rows), one = tc::idesc_bf16(128, L.rows);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {  // 16 cells at a time
+                const uint32_t a = tmem + kColA + 8 * x;
+                const uint64_t b = image + 16 * x;
+                tc::mma_bf16_ts(tmem + kColD, a, b, wide, x > 0);
+                tc::mma_bf16_ts(tmem + kColD, a + 64, b, wide, true);
+                tc::mma_bf16_ts(tmem + kColD, a, b + 2 * part, one, true);
+                tc::mma_bf16_ts(tmem + kColD, a + 128, b, one, true);
+            }
+            tc::mma_commit(&d_full);
+        }
+        __syncwarp();
+    }
+    // ---- meanwhile the nodes' weights for one another
+    {
+        const float2 *gram = reinterpret_cast<const float2 *>(p.gram) + (static_cast<size_t>(n) * Hk + kh) * N * N;
+        for (int x = tid; x < N * N; x += kTcThreads) {
+            const int i = x / N, s = x % N;
+            if (!((path_of[i] >> s) & 1ull)) continue;
+            const float w = expf((hi_of[i] - hi_of[s]) + (lo_of[i] - lo_of[s]));
+            const float2 dot = gram[x];
+            coef[x] = make_float2(beta_of[i] * w * dot.x, w * dot.y);
+        }
+    }
+    ok = ok && mbar_wait(&d_full, 0);
+    tc::fence_after_sync();
+    if (ok) {
+        // (the state's cells have been read: every thread has passed the barrier above)
+        for (int c = 16 * half; c < L.rows; c += 32) {
+            uint32_t x[16], y[16];
+            tc::tmem_ld16_nowait(lanes + kColD + c, x);
+            tc::tmem_ld16_nowait(lanes + kColD + L.rows + c, y);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int r = c + e, i = r < L.pad ? r : r - L.pad;
+                if (i < N) d[(r < L.pad ? i : N + i) * S + j] = __uint_as_float(x[e]) + __uint_as_float(y[e]);
+            }
+        }
+    }
+    tc::fence_before_sync();
+    ok = __syncthreads_and(ok);
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, L.tmem_cols());
+    }
+    if (!ok) {
+        if (tid == 0) atomicOr(p.watchdog, WD_STATE_COPY);
+        return;  // (nothing of this head is written)
+    }
+    // ---- u, one thread a row, node after node
+    if (tid < S) {
+        const size_t at = (row0 * H + vh) * S + tid, step = static_cast<size_t>(H) * S;
+        const float *v = p.v + at;
+        float *u_out = p.u + at;
+        float next = v[0];
+        for (int i = 0; i < N; ++i) {
+            const float vi = next;
+            if (i + 1 < N) next = v[(i + 1) * step];
+            unsigned long long path = path_of[i] & ~(1ull << i);
+            float u = beta_of[i] * (vi - decay[i] * d[i * S + tid]);
+            while (path != 0) {
+                const int s = __ffsll(static_cast<long long>(path)) - 1;
+                path &= path - 1;
+                u = fmaf(-coef[i * N + s].x, d[s * S + tid], u);
+            }
+            if (path_of[i] == 0) u = 0.0f;
+            d[i * S + tid] = u;
+            u_out[i * step] = u;
+        }
+    }
+    __syncthreads();
+    // ---- y and the gated norm, a warp a node: the lane's four channels
+    for (int i = warp; i < N; i += kTcThreads / 32) {
+        unsigned long long path = path_of[i];
+        const size_t at = ((row0 + i) * H + vh) * S + 4 * lane;
+        float y[4] = {};
+        if (path != 0) {
+            float zv[4], wv[4];
+            load_vec<4>(zv, p.z + at);
+            load_vec<4>(wv, p.norm_w + 4 * lane);
+            load_vec<4>(y, d + (N + i) * S + 4 * lane);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] *= decay[i];
+            while (path != 0) {
+                const int s = __ffsll(static_cast<long long>(path)) - 1;
+                path &= path - 1;
+                const float w = coef[i * N + s].y;
+                float u[4];
+                load_vec<4>(u, d + s * S + 4 * lane);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = fmaf(w, u[e], y[e]);
+            }
+            float ss = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                y[e] *= p.scale;
+                ss = __fmaf_rn(y[e], y[e], ss);
+            }
+            ss = warp_allsum(ss);
+            const float inv_rms = 1.0f / sqrtf(ss / static_cast<float>(S) + p.norm_eps);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = y[e] * inv_rms * wv[e] * silu(zv[e]);
+        }
+        store_vec<4>(p.out + at, y);
+    }
+}
+
 // ------------------------------------------------------------------ the gated norm
 
 // One warp per head row, as gdn_gated_norm; rows of nodes that are not there are zeros.
@@ -528,6 +769,18 @@ gdn_status launch_block(const TreeParams &p, int n_seqs, int conv_kernel, cudaSt
     }
     tree_gram_kernel<E><<<dim3(p.n_k_heads, n_seqs), 32 * kGramWarps, 0, s>>>(p);
     GDN_TRY(launch_status());
+    if constexpr (E == 4) {
+        // (a tensor map's rows are counted in 32 bits)
+        const long long state_rows = static_cast<long long>(p.pool) * p.n_v_heads * 128;
+        if (state_rows <= 0x7fffffffLL) {
+            CUtensorMap map;
+            GDN_TRY(encode_blocks_map(&map, p.state, GDN_F32, 128, static_cast<uint64_t>(state_rows), 512, 128, 4));
+            static std::atomic<unsigned long long> allowed{0};
+            GDN_TRY(allow_smem(tree_state_tc_kernel, static_cast<int>(TcSmem(kMaxNodes).bytes) + 1024, allowed));
+            tree_state_tc_kernel<<<static_cast<unsigned>(n_seqs) * p.n_v_heads, kTcThreads, TcSmem(p.n_nodes).bytes + 1024, s>>>(map, p);
+            return launch_status();
+        }
+    }
     using L = StateSmem<E>;
     const size_t smem = L::bytes(p.n_nodes);
     if (cudaFuncSetAttribute(tree_state_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -610,7 +863,8 @@ gdn_status gdn_block_tree(const float *qkv, const float *conv_w, const float *co
     const TreeParams p{qkv, conv_w, conv_state, alpha, b, dt, a, z, norm_w, state, out, parents,
                        slots, n_nodes, n_k_heads, n_v_heads, pool, scale, l2_eps, norm_eps,
                        err_count, t + T.k, t + T.g, t + T.u, w + W.q, w + W.v, w + W.beta,
-                       w + W.gram, reinterpret_cast<int *>(w + W.there)};
+                       w + W.gram, reinterpret_cast<int *>(w + W.there), watchdog_block()};
+    if (p.watchdog == nullptr) return GDN_ERR_LAUNCH;
     const cudaStream_t s = as_cuda(stream);
     switch (state_size) {
         case 32: return launch_block<1>(p, n_seqs, conv_kernel, s);

@@ -186,6 +186,9 @@ inline unsigned read_and_clear_flag(unsigned &flag, cudaStream_t s) {
     return flags;
 }
 
+// The fused block's flag, which the block over trees shares.
+unsigned *watchdog_block();
+
 // Per-translation-unit watchdog flags (a bounded wait that gave up sets a bit).
 unsigned read_and_clear_watchdog_recurrence(cudaStream_t s);
 unsigned read_and_clear_watchdog_block(cudaStream_t s);

@@ -245,6 +245,20 @@ inline gdn_status allow_smem(Kernel kernel, int bytes, std::atomic<unsigned long
     return GDN_OK;
 }
 
+// The address of a watchdog flag on the current device, for kernels of other units that share it
+// (NULL when the device does not say). `known`: the flag's own, by device.
+inline unsigned *flag_address(unsigned &flag, std::atomic<unsigned *> (&known)[64]) {
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return nullptr;
+    unsigned *at = device < 64 ? known[device].load(std::memory_order_relaxed) : nullptr;
+    if (at != nullptr) return at;
+    void *found = nullptr;
+    if (cudaGetSymbolAddress(&found, flag) != cudaSuccess) return nullptr;
+    at = static_cast<unsigned *>(found);
+    if (device < 64) known[device].store(at, std::memory_order_relaxed);
+    return at;
+}
+
 // Arguments every call on a paged cache shares.
 inline gdn_status check_cache(int n_kv_heads, int head_dim, int page_size, int n_pages,
                               int max_pages, int dtype) {
