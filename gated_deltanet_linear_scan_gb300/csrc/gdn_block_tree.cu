@@ -65,7 +65,16 @@ struct TreeParams {
 // conv history behind the root's; the arithmetic is the prefill block's, so a tree that is a chain
 // has its bits. The CTAs behind the slices' compute the gates. A node that is not there has zeros.
 constexpr int kConvWarps = 4;
-constexpr int kConvNodes = 4;
+constexpr int kConvNodes = 8;
+
+// N consecutive floats, 16-byte aligned where N is a multiple of 4.
+template <int N>
+__device__ __forceinline__ void load_run(float (&x)[N], const float *from) {
+    if constexpr (N % 4 == 0) load_vec<N>(x, from);
+    else
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = from[i];
+}
 
 template <int E, int K>
 __global__ void __launch_bounds__(32 * kConvWarps) tree_conv_kernel(const TreeParams p) {
@@ -106,16 +115,10 @@ __global__ void __launch_bounds__(32 * kConvWarps) tree_conv_kernel(const TreePa
     if (sl >= slices) return;
     const size_t conv_dim = static_cast<size_t>(slices) * S;
     const size_t ch0 = static_cast<size_t>(sl) * S + E * lane;
-    float wc[K][E], hist[TAPS][E];
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-#pragma unroll
-        for (int t = 0; t < K; ++t) wc[t][e] = p.conv_w[(ch0 + e) * K + t];
-    const float *hs = p.conv_state + (static_cast<size_t>(slot) * conv_dim + ch0) * TAPS;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-#pragma unroll
-        for (int t = 0; t < TAPS; ++t) hist[t][e] = hs[e * TAPS + t];
+    // the lane's weights [E][K] and history [E][TAPS], consecutive in memory
+    float wc[E * K], hist[E * TAPS];
+    load_run<E * K>(wc, p.conv_w + ch0 * K);
+    load_run<E * TAPS>(hist, p.conv_state + (static_cast<size_t>(slot) * conv_dim + ch0) * TAPS);
     const float *x_ptr = p.qkv + row0 * conv_dim + ch0;
     const bool is_qk = sl < 2 * Hk;  // uniform over the warp
     float *dst = is_qk ? (sl < Hk ? p.q : p.k) + (row0 * Hk + sl % Hk) * S + E * lane
@@ -146,14 +149,14 @@ __global__ void __launch_bounds__(32 * kConvWarps) tree_conv_kernel(const TreePa
                     for (int h = 1; h <= TAPS; ++h)
                         if (h == behind)
 #pragma unroll
-                            for (int e = 0; e < E; ++e) taps[t][e] = hist[TAPS - h][e];
+                            for (int e = 0; e < E; ++e) taps[t][e] = hist[e * TAPS + TAPS - h];
                 }
             }
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                float pre = __fmul_rn(taps[TAPS][e], wc[K - 1][e]);
+                float pre = __fmul_rn(taps[TAPS][e], wc[e * K + K - 1]);
 #pragma unroll
-                for (int t = 0; t < TAPS; ++t) pre = __fmaf_rn(taps[t][e], wc[t][e], pre);
+                for (int t = 0; t < TAPS; ++t) pre = __fmaf_rn(taps[t][e], wc[e * K + t], pre);
                 o[e] = silu(pre);
             }
             if (is_qk) {
@@ -172,41 +175,50 @@ __global__ void __launch_bounds__(32 * kConvWarps) tree_conv_kernel(const TreePa
 
 // ------------------------------------------------------------------ products of the nodes
 
-// k_i.k_s and q_i.k_s of every node i with itself and its ancestors s, one warp per node at a
-// time. Grid: (k-head, sequence).
+// k_i.k_s and q_i.k_s of every node i with itself and its ancestors s: the keys in shared memory, one
+// warp per node at a time, two ancestors together. Grid: (k-head, sequence).
 constexpr int kGramWarps = 8;
 
 template <int E>
 __global__ void __launch_bounds__(32 * kGramWarps) tree_gram_kernel(const TreeParams p) {
     constexpr int S = 32 * E;
+    extern __shared__ __align__(16) float keys[];  // [N][S]
     __shared__ unsigned long long path_of[kMaxNodes];
     __shared__ int up[kMaxNodes];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kh = blockIdx.x, n = blockIdx.y, N = p.n_nodes, Hk = p.n_k_heads;
     const int slot = p.slots ? p.slots[n] : n;
     if (slot < 0 || slot >= p.pool) return;
+    const size_t base = (static_cast<size_t>(n) * N * Hk + kh) * S, step = static_cast<size_t>(Hk) * S;
+    for (int x = threadIdx.x; x < N * (S / 4); x += 32 * kGramWarps)
+        *reinterpret_cast<float4 *>(keys + 4 * x) =
+            *reinterpret_cast<const float4 *>(p.k + base + (x / (S / 4)) * step + 4 * (x % (S / 4)));
     if (warp == 0) {
         unsigned long long paths[2];
         tree_paths(p.parents + static_cast<size_t>(n) * N, N, paths, path_of, up);
     }
     __syncthreads();
-    const size_t base = (static_cast<size_t>(n) * N * Hk + kh) * S + E * lane, step = static_cast<size_t>(Hk) * S;
     float2 *gram = reinterpret_cast<float2 *>(p.gram) + (static_cast<size_t>(n) * Hk + kh) * N * N;
     for (int i = warp; i < N; i += kGramWarps) {
         unsigned long long path = path_of[i];
         if (path == 0) continue;
         float ki[E], qi[E];
-        load_vec<E>(ki, p.k + base + i * step);
-        load_vec<E>(qi, p.q + base + i * step);
+        load_vec<E>(ki, keys + i * S + E * lane);
+        load_vec<E>(qi, p.q + base + i * step + E * lane);
         while (path != 0) {
             const int s = __ffsll(static_cast<long long>(path)) - 1;
             path &= path - 1;
-            float ks[E];
-            load_vec<E>(ks, p.k + base + s * step);
-            float part[2] = {lane_dot<E>(ki, ks), lane_dot<E>(qi, ks)};
-            const float sum = warp_sum_packed<2>(part, lane);
-            const float other = __shfl_sync(FULL_MASK, sum, row_home_lane<2>(1));
-            if (lane == 0) gram[i * N + s] = make_float2(sum, other);
+            const int t = path != 0 ? __ffsll(static_cast<long long>(path)) - 1 : s;
+            if (path != 0) path &= path - 1;
+            float ks[E], kt[E];
+            load_vec<E>(ks, keys + s * S + E * lane);
+            load_vec<E>(kt, keys + t * S + E * lane);
+            float part[4] = {lane_dot<E>(ki, ks), lane_dot<E>(qi, ks), lane_dot<E>(ki, kt), lane_dot<E>(qi, kt)};
+            const float sum = warp_sum_packed<4>(part, lane);
+            // sums 0 and 1 of s, 2 and 3 of t
+            const float next = __shfl_xor_sync(FULL_MASK, sum, row_home_lane<4>(1));
+            if (lane == row_home_lane<4>(0)) gram[i * N + s] = make_float2(sum, next);
+            if (lane == row_home_lane<4>(2)) gram[i * N + t] = make_float2(sum, next);
         }
     }
 }
@@ -510,16 +522,23 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_state_tc_kernel(const __gr
         }
         __syncwarp();
     }
-    // ---- meanwhile the nodes' weights for one another
-    {
-        const float2 *gram = reinterpret_cast<const float2 *>(p.gram) + (static_cast<size_t>(n) * Hk + kh) * N * N;
-        for (int x = tid; x < N * N; x += kTcThreads) {
-            const int i = x / N, s = x % N;
-            if (!((path_of[i] >> s) & 1ull)) continue;
-            const float w = expf((hi_of[i] - hi_of[s]) + (lo_of[i] - lo_of[s]));
-            const float2 dot = gram[x];
-            coef[x] = make_float2(beta_of[i] * w * dot.x, w * dot.y);
-        }
+    // ---- meanwhile the nodes' weights for one another, and their values
+    const float2 *gram = reinterpret_cast<const float2 *>(p.gram) + (static_cast<size_t>(n) * Hk + kh) * N * N;
+#pragma unroll 4
+    for (int x = tid; x < N * N; x += kTcThreads) {
+        const int i = x / N, s = x % N;
+        const float2 dot = gram[x];
+        if (!((path_of[i] >> s) & 1ull)) continue;
+        const float w = expf((hi_of[i] - hi_of[s]) + (lo_of[i] - lo_of[s]));
+        coef[x] = make_float2(beta_of[i] * w * dot.x, w * dot.y);
+    }
+    const int v_count = N * (S / 4);  // 16-byte parts of the nodes' values
+    float4 v_part[8];
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+        const int x = tid + y * kTcThreads;
+        if (x < v_count)
+            v_part[y] = *reinterpret_cast<const float4 *>(p.v + ((row0 + x / (S / 4)) * H + vh) * S + 4 * (x % (S / 4)));
     }
     ok = ok && mbar_wait(&d_full, 0);
     tc::fence_after_sync();
@@ -536,6 +555,12 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_state_tc_kernel(const __gr
                 if (i < N) d[(r < L.pad ? i : N + i) * S + j] = __uint_as_float(x[e]) + __uint_as_float(y[e]);
             }
         }
+        // the values over the images, which have been multiplied
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+            const int x = tid + y * kTcThreads;
+            if (x < v_count) *reinterpret_cast<float4 *>(smem + L.images + 16 * x) = v_part[y];
+        }
     }
     tc::fence_before_sync();
     ok = __syncthreads_and(ok);
@@ -547,21 +572,24 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_state_tc_kernel(const __gr
         if (tid == 0) atomicOr(p.watchdog, WD_STATE_COPY);
         return;  // (nothing of this head is written)
     }
-    // ---- u, one thread a row, node after node
+    // ---- u, one thread a row, node after node, four ancestors at a time
     if (tid < S) {
-        const size_t at = (row0 * H + vh) * S + tid, step = static_cast<size_t>(H) * S;
-        const float *v = p.v + at;
-        float *u_out = p.u + at;
-        float next = v[0];
+        const float *v = reinterpret_cast<const float *>(smem + L.images) + tid;
+        const size_t step = static_cast<size_t>(H) * S;
+        float *u_out = p.u + (row0 * H + vh) * S + tid;
         for (int i = 0; i < N; ++i) {
-            const float vi = next;
-            if (i + 1 < N) next = v[(i + 1) * step];
             unsigned long long path = path_of[i] & ~(1ull << i);
-            float u = beta_of[i] * (vi - decay[i] * d[i * S + tid]);
+            float u = beta_of[i] * (v[i * S] - decay[i] * d[i * S + tid]);
             while (path != 0) {
-                const int s = __ffsll(static_cast<long long>(path)) - 1;
-                path &= path - 1;
-                u = fmaf(-coef[i * N + s].x, d[s * S + tid], u);
+                float w[4], x[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int s = path != 0 ? __ffsll(static_cast<long long>(path)) - 1 : 0;
+                    w[y] = path != 0 ? coef[i * N + s].x : 0.0f;
+                    x[y] = d[s * S + tid];
+                    path &= path - 1;
+                }
+                u = fmaf(-w[0], x[0], fmaf(-w[1], x[1], u)) - fmaf(w[2], x[2], w[3] * x[3]);
             }
             if (path_of[i] == 0) u = 0.0f;
             d[i * S + tid] = u;
@@ -767,7 +795,10 @@ gdn_status launch_block(const TreeParams &p, int n_seqs, int conv_kernel, cudaSt
         case 7: GDN_TRY((launch_conv<E, 7>(p, n_seqs, s))); break;
         default: GDN_TRY((launch_conv<E, 8>(p, n_seqs, s))); break;
     }
-    tree_gram_kernel<E><<<dim3(p.n_k_heads, n_seqs), 32 * kGramWarps, 0, s>>>(p);
+    const size_t keys = static_cast<size_t>(p.n_nodes) * 32 * E * sizeof(float);
+    static std::atomic<unsigned long long> gram_allowed{0};
+    GDN_TRY(allow_smem(tree_gram_kernel<E>, kMaxNodes * 32 * E * static_cast<int>(sizeof(float)), gram_allowed));
+    tree_gram_kernel<E><<<dim3(p.n_k_heads, n_seqs), 32 * kGramWarps, keys, s>>>(p);
     GDN_TRY(launch_status());
     if constexpr (E == 4) {
         // (a tensor map's rows are counted in 32 bits)
