@@ -32,16 +32,16 @@ struct Tape {
 };
 
 // Scratch: q [n][N][Hk][S], v [n][N][H][S], beta [n][N][H], the products k_i.k_s and q_i.k_s
-// [n][Hk][N][N][2], and whether a node is there [n][N].
+// [n][Hk][N][N][2], and the nodes' paths [n][N] (0: not there).
 struct Scratch {
-    size_t q, v, beta, gram, there, floats;
+    size_t q, v, beta, gram, paths, floats;
     Scratch(size_t rows, int n_nodes, int hk, int h, int s) {
         q = 0;
         v = q + round_up(rows * hk * s);
         beta = v + round_up(rows * h * s);
         gram = beta + round_up(rows * h);
-        there = gram + round_up(rows * n_nodes * hk * 2);
-        floats = there + round_up(rows);
+        paths = gram + round_up(rows * n_nodes * hk * 2);
+        floats = paths + round_up(rows * 2);
     }
 };
 
@@ -54,7 +54,7 @@ struct TreeParams {
     int32_t *err_count;
     float *k, *g, *u;             // the tape
     float *q, *v, *beta, *gram;   // scratch
-    int *there;
+    unsigned long long *paths;
     unsigned *watchdog;
 };
 
@@ -94,6 +94,11 @@ __global__ void __launch_bounds__(32 * kConvWarps) tree_conv_kernel(const TreePa
         unsigned long long paths[2];
         const bool bad = tree_paths(p.parents + static_cast<size_t>(n) * N, N, paths, path_of, up);
         if (bad && counts && lane == 0 && p.err_count) atomicAdd(p.err_count, 1);
+        if (counts) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (lane + 32 * x < N) p.paths[static_cast<size_t>(n) * N + lane + 32 * x] = paths[x];
+        }
     }
     __syncthreads();
     const int i0 = blockIdx.y * kConvNodes, i1 = min(N, i0 + kConvNodes);
@@ -107,7 +112,6 @@ __global__ void __launch_bounds__(32 * kConvWarps) tree_conv_kernel(const TreePa
             const bool here = path_of[i] != 0;
             p.g[at] = here ? p.a[h] * softplus_guarded(p.alpha[at] + p.dt[h]) : 0.0f;
             p.beta[at] = here ? 1.0f / (1.0f + expf(-p.b[at])) : 0.0f;
-            if (h == 0) p.there[row0 + i] = here;
         }
         return;
     }
@@ -183,8 +187,6 @@ template <int E>
 __global__ void __launch_bounds__(32 * kGramWarps) tree_gram_kernel(const TreeParams p) {
     constexpr int S = 32 * E;
     extern __shared__ __align__(16) float keys[];  // [N][S]
-    __shared__ unsigned long long path_of[kMaxNodes];
-    __shared__ int up[kMaxNodes];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kh = blockIdx.x, n = blockIdx.y, N = p.n_nodes, Hk = p.n_k_heads;
     const int slot = p.slots ? p.slots[n] : n;
@@ -193,11 +195,8 @@ __global__ void __launch_bounds__(32 * kGramWarps) tree_gram_kernel(const TreePa
     for (int x = threadIdx.x; x < N * (S / 4); x += 32 * kGramWarps)
         *reinterpret_cast<float4 *>(keys + 4 * x) =
             *reinterpret_cast<const float4 *>(p.k + base + (x / (S / 4)) * step + 4 * (x % (S / 4)));
-    if (warp == 0) {
-        unsigned long long paths[2];
-        tree_paths(p.parents + static_cast<size_t>(n) * N, N, paths, path_of, up);
-    }
     __syncthreads();
+    const unsigned long long *path_of = p.paths + static_cast<size_t>(n) * N;
     float2 *gram = reinterpret_cast<float2 *>(p.gram) + (static_cast<size_t>(n) * Hk + kh) * N * N;
     for (int i = warp; i < N; i += kGramWarps) {
         unsigned long long path = path_of[i];
@@ -261,7 +260,6 @@ __global__ void __launch_bounds__(kStateThreads) tree_state_kernel(const TreePar
     constexpr int S = L::S, JB = L::JB, JL = JB / 32, kPad = L::kPad;
     extern __shared__ __align__(16) float smem[];
     __shared__ unsigned long long path_of[kMaxNodes];
-    __shared__ int up[kMaxNodes];
     __shared__ float g_of[kMaxNodes], hi_of[kMaxNodes], lo_of[kMaxNodes], beta_of[kMaxNodes], decay[kMaxNodes];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int j0 = blockIdx.x * JB, vh = blockIdx.y, n = blockIdx.z;
@@ -278,11 +276,8 @@ __global__ void __launch_bounds__(kStateThreads) tree_state_kernel(const TreePar
         *reinterpret_cast<float4 *>(rows + j * kPad + 4 * c) = *reinterpret_cast<const float4 *>(state + j * S + 4 * c);
     }
     const size_t row0 = static_cast<size_t>(n) * N;
-    if (warp == 0) {
-        unsigned long long paths[2];
-        tree_paths(p.parents + row0, N, paths, path_of, up);
-    }
     if (tid < N) {
+        path_of[tid] = p.paths[row0 + tid];
         g_of[tid] = p.g[(row0 + tid) * H + vh];
         beta_of[tid] = p.beta[(row0 + tid) * H + vh];
     }
@@ -397,13 +392,16 @@ constexpr uint32_t kColA = 0, kColD = 192;  // tensor memory: the state's parts,
 
 struct TcSmem {
     int pad, rows;               // nodes, and vectors, of an image (a multiple of 8, of 16)
-    uint32_t images, coef, bytes;
+    uint32_t images, weights_u, weights_y, anc, bytes;
     __host__ __device__ explicit TcSmem(int n) {
         pad = (n + 7) / 8 * 8;
         rows = 2 * pad;
-        images = 65536;                                         // behind the state, [4][128 rows][128 bytes]
-        coef = images + 3u * static_cast<uint32_t>(rows) * 256u;
-        bytes = coef + static_cast<uint32_t>(n * n) * 8u;
+        images = 65536;  // behind the state, [4][128 rows][128 bytes]
+        // of every node, its ancestors in order and itself, [n][pad]: their weights in u and in y, and which
+        weights_u = images + 3u * static_cast<uint32_t>(rows) * 256u;
+        weights_y = weights_u + static_cast<uint32_t>(n * pad) * 4u;
+        anc = weights_y + static_cast<uint32_t>(n * pad) * 4u;
+        bytes = anc + static_cast<uint32_t>(n * pad);
     }
     __host__ __device__ uint32_t tmem_cols() const { return kColD + 2u * static_cast<uint32_t>(rows) <= 256u ? 256u : 512u; }
 };
@@ -427,7 +425,6 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_state_tc_kernel(const __gr
     __shared__ __align__(8) uint64_t state_full, d_full;
     __shared__ uint32_t tmem_base;
     __shared__ unsigned long long path_of[kMaxNodes];
-    __shared__ int up[kMaxNodes];
     __shared__ float g_of[kMaxNodes], hi_of[kMaxNodes], lo_of[kMaxNodes], beta_of[kMaxNodes], decay[kMaxNodes];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int N = p.n_nodes, Hk = p.n_k_heads, H = p.n_v_heads;
@@ -435,8 +432,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_state_tc_kernel(const __gr
     const int slot = p.slots ? p.slots[n] : n;
     if (slot < 0 || slot >= p.pool) return;
     const TcSmem L(N);
-    float *d = reinterpret_cast<float *>(smem);  // later, over the state: [2N][128] products with k, then u; with q, then y
-    float2 *coef = reinterpret_cast<float2 *>(smem + L.coef);
+    float *d = reinterpret_cast<float *>(smem);  // later, over the state: [2N][128] products with k, then u; with q
+    float *weights_u = reinterpret_cast<float *>(smem + L.weights_u), *weights_y = reinterpret_cast<float *>(smem + L.weights_y);
+    uint8_t *anc = smem + L.anc;
     const size_t row0 = static_cast<size_t>(n) * N;
 
     if (tid == 0) {
@@ -446,30 +444,36 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_state_tc_kernel(const __gr
         mbar_arrive_expect_tx(&state_full, S * S * 4);
         tma_load_3d(smem, &state_map, 0, (slot * H + vh) * S, 0, &state_full);
     }
+    if (tid >= 128 && tid < 128 + N) {
+        const int i = tid - 128;
+        path_of[i] = p.paths[row0 + i];
+        g_of[i] = p.g[(row0 + i) * H + vh];
+        beta_of[i] = p.beta[(row0 + i) * H + vh];
+    }
+    // ---- the images of [K; Q], rows past the nodes zero: 8 cells of two rows a thread at a time
+    for (int x0 = tid; x0 < L.rows * (S / 8); x0 += 2 * kTcThreads) {
+        float v[2][8] = {};
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int x = x0 + y * kTcThreads, r = x / (S / 8), c = x % (S / 8), i = r < L.pad ? r : r - L.pad;
+            if (r < L.rows && i < N) load_vec<8>(v[y], (r < L.pad ? p.k : p.q) + ((row0 + i) * Hk + kh) * S + 8 * c);
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int x = x0 + y * kTcThreads, r = x / (S / 8), c = x % (S / 8);
+            if (r >= L.rows) break;
+            uint32_t w[3][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split3(v[y][2 * e], v[y][2 * e + 1], w[0][e], w[1][e], w[2][e]);
+            uint8_t *to = smem + L.images + tc::kmajor_offset16(r, 8 * c, 128, S / 8 * 128);
+#pragma unroll
+            for (int z = 0; z < 3; ++z)
+                *reinterpret_cast<uint4 *>(to + z * L.rows * 256) = make_uint4(w[z][0], w[z][1], w[z][2], w[z][3]);
+        }
+    }
     if (warp == 1) {
         tc::tmem_alloc(&tmem_base, L.tmem_cols());
         tc::tmem_relinquish();  // (another CTA's turn)
-    }
-    if (warp == 2) {
-        unsigned long long paths[2];
-        tree_paths(p.parents + row0, N, paths, path_of, up);
-    }
-    if (tid >= 128 && tid < 128 + N) {
-        g_of[tid - 128] = p.g[(row0 + tid - 128) * H + vh];
-        beta_of[tid - 128] = p.beta[(row0 + tid - 128) * H + vh];
-    }
-    // ---- the images of [K; Q], rows past the nodes zero
-    for (int x = tid; x < L.rows * (S / 8); x += kTcThreads) {
-        const int r = x / (S / 8), c = x % (S / 8), i = r < L.pad ? r : r - L.pad;
-        float v[8] = {};
-        if (i < N) load_vec<8>(v, (r < L.pad ? p.k : p.q) + ((row0 + i) * Hk + kh) * S + 8 * c);
-        uint32_t w[3][4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) split3(v[2 * e], v[2 * e + 1], w[0][e], w[1][e], w[2][e]);
-        uint8_t *to = smem + L.images + tc::kmajor_offset16(r, 8 * c, 128, S / 8 * 128);
-#pragma unroll
-        for (int y = 0; y < 3; ++y)
-            *reinterpret_cast<uint4 *>(to + y * L.rows * 256) = make_uint4(w[y][0], w[y][1], w[y][2], w[y][3]);
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -523,15 +527,6 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_state_tc_kernel(const __gr
         __syncwarp();
     }
     // ---- meanwhile the nodes' weights for one another, and their values
-    const float2 *gram = reinterpret_cast<const float2 *>(p.gram) + (static_cast<size_t>(n) * Hk + kh) * N * N;
-#pragma unroll 4
-    for (int x = tid; x < N * N; x += kTcThreads) {
-        const int i = x / N, s = x % N;
-        const float2 dot = gram[x];
-        if (!((path_of[i] >> s) & 1ull)) continue;
-        const float w = expf((hi_of[i] - hi_of[s]) + (lo_of[i] - lo_of[s]));
-        coef[x] = make_float2(beta_of[i] * w * dot.x, w * dot.y);
-    }
     const int v_count = N * (S / 4);  // 16-byte parts of the nodes' values
     float4 v_part[8];
 #pragma unroll
@@ -539,6 +534,26 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_state_tc_kernel(const __gr
         const int x = tid + y * kTcThreads;
         if (x < v_count)
             v_part[y] = *reinterpret_cast<const float4 *>(p.v + ((row0 + x / (S / 4)) * H + vh) * S + 4 * (x % (S / 4)));
+    }
+    const float2 *gram = reinterpret_cast<const float2 *>(p.gram) + (static_cast<size_t>(n) * Hk + kh) * N * N;
+#pragma unroll 4
+    for (int x = tid; x < N * L.pad; x += kTcThreads) {
+        const int i = x / L.pad, s = x - i * L.pad;
+        const unsigned long long path = path_of[i];
+        const float2 dot = s < N ? gram[i * N + s] : make_float2(0.0f, 0.0f);
+        if ((path >> s) & 1ull) {
+            const float w = expf((hi_of[i] - hi_of[s]) + (lo_of[i] - lo_of[s]));
+            const int at = i * L.pad + __popcll(path & ((1ull << s) - 1));
+            weights_u[at] = s == i ? 0.0f : -beta_of[i] * w * dot.x;
+            weights_y[at] = w * dot.y;
+            anc[at] = static_cast<uint8_t>(s);
+        }
+        // (places behind the path: the node itself with weights of zero)
+        const int behind = __popcll(path) + s;
+        if (behind < L.pad) {
+            weights_u[i * L.pad + behind] = weights_y[i * L.pad + behind] = 0.0f;
+            anc[i * L.pad + behind] = static_cast<uint8_t>(i);
+        }
     }
     ok = ok && mbar_wait(&d_full, 0);
     tc::fence_after_sync();
@@ -572,51 +587,66 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_state_tc_kernel(const __gr
         if (tid == 0) atomicOr(p.watchdog, WD_STATE_COPY);
         return;  // (nothing of this head is written)
     }
-    // ---- u, one thread a row, node after node, four ancestors at a time
+    // ---- u, one thread a row, node after node, four ancestors at a time; the other threads fetch what
+    // the norm needs
+    float zv[2][4], wv[4];
+    load_vec<4>(wv, p.norm_w + 4 * lane);
+    const size_t z_at = (row0 * H + vh) * S + 4 * lane, z_step = static_cast<size_t>(H) * S;
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+        if (warp + 8 * y < N) load_vec<4>(zv[y], p.z + z_at + (warp + 8 * y) * z_step);
     if (tid < S) {
         const float *v = reinterpret_cast<const float *>(smem + L.images) + tid;
-        const size_t step = static_cast<size_t>(H) * S;
         float *u_out = p.u + (row0 * H + vh) * S + tid;
         for (int i = 0; i < N; ++i) {
-            unsigned long long path = path_of[i] & ~(1ull << i);
-            float u = beta_of[i] * (v[i * S] - decay[i] * d[i * S + tid]);
-            while (path != 0) {
-                float w[4], x[4];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int s = path != 0 ? __ffsll(static_cast<long long>(path)) - 1 : 0;
-                    w[y] = path != 0 ? coef[i * N + s].x : 0.0f;
-                    x[y] = d[s * S + tid];
-                    path &= path - 1;
-                }
-                u = fmaf(-w[0], x[0], fmaf(-w[1], x[1], u)) - fmaf(w[2], x[2], w[3] * x[3]);
+            const unsigned long long path = path_of[i];
+            const int count = __popcll(path) - 1;  // ancestors
+            const float *w = weights_u + i * L.pad;
+            const uint32_t *which = reinterpret_cast<const uint32_t *>(anc + i * L.pad);
+            float u = beta_of[i] * (v[i * S] - decay[i] * d[i * S + tid]), u2 = 0.0f;
+            for (int k = 0; k < count; k += 4) {
+                const uint32_t a = which[k / 4];
+                const float4 x = *reinterpret_cast<const float4 *>(w + k);
+                u = fmaf(x.x, d[(a & 255u) * S + tid], u);
+                u2 = fmaf(x.y, d[((a >> 8) & 255u) * S + tid], u2);
+                u = fmaf(x.z, d[((a >> 16) & 255u) * S + tid], u);
+                u2 = fmaf(x.w, d[(a >> 24) * S + tid], u2);
             }
-            if (path_of[i] == 0) u = 0.0f;
+            u = path == 0 ? 0.0f : u + u2;
             d[i * S + tid] = u;
-            u_out[i * step] = u;
+            u_out[i * z_step] = u;
         }
     }
     __syncthreads();
     // ---- y and the gated norm, a warp a node: the lane's four channels
-    for (int i = warp; i < N; i += kTcThreads / 32) {
-        unsigned long long path = path_of[i];
-        const size_t at = ((row0 + i) * H + vh) * S + 4 * lane;
+    for (int i = warp, turn = 0; i < N; i += kTcThreads / 32, ++turn) {
+        const unsigned long long path = path_of[i];
         float y[4] = {};
         if (path != 0) {
-            float zv[4], wv[4];
-            load_vec<4>(zv, p.z + at);
-            load_vec<4>(wv, p.norm_w + 4 * lane);
+            float z[4];
+            if (turn < 2) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[e] = turn ? zv[1][e] : zv[0][e];
+            } else {
+                load_vec<4>(z, p.z + z_at + i * z_step);
+            }
             load_vec<4>(y, d + (N + i) * S + 4 * lane);
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] *= decay[i];
-            while (path != 0) {
-                const int s = __ffsll(static_cast<long long>(path)) - 1;
-                path &= path - 1;
-                const float w = coef[i * N + s].y;
-                float u[4];
-                load_vec<4>(u, d + s * S + 4 * lane);
+            const float *w = weights_y + i * L.pad;
+            const uint32_t *which = reinterpret_cast<const uint32_t *>(anc + i * L.pad);
+            const int count = __popcll(path);
+            for (int k = 0; k < count; k += 4) {
+                const uint32_t a = which[k / 4];
+                const float4 x = *reinterpret_cast<const float4 *>(w + k);
+                const float ws[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = fmaf(w, u[e], y[e]);
+                for (int m = 0; m < 4; ++m) {
+                    float u[4];
+                    load_vec<4>(u, d + ((a >> (8 * m)) & 255u) * S + 4 * lane);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = fmaf(ws[m], u[e], y[e]);
+                }
             }
             float ss = 0.0f;
 #pragma unroll
@@ -627,9 +657,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_state_tc_kernel(const __gr
             ss = warp_allsum(ss);
             const float inv_rms = 1.0f / sqrtf(ss / static_cast<float>(S) + p.norm_eps);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = y[e] * inv_rms * wv[e] * silu(zv[e]);
+            for (int e = 0; e < 4; ++e) y[e] = y[e] * inv_rms * wv[e] * silu(z[e]);
         }
-        store_vec<4>(p.out + at, y);
+        store_vec<4>(p.out + z_at + i * z_step, y);
     }
 }
 
@@ -653,7 +683,7 @@ __global__ void __launch_bounds__(kNormThreads) tree_norm_kernel(const TreeParam
         const int slot = p.slots[node / p.n_nodes];
         if (slot < 0 || slot >= p.pool) return;
     }
-    if (!p.there[node]) return;  // (y is zeros)
+    if (p.paths[node] == 0) return;  // (y is zeros)
     float ss = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) ss = __fmaf_rn(yv[e], yv[e], ss);
@@ -894,7 +924,7 @@ gdn_status gdn_block_tree(const float *qkv, const float *conv_w, const float *co
     const TreeParams p{qkv, conv_w, conv_state, alpha, b, dt, a, z, norm_w, state, out, parents,
                        slots, n_nodes, n_k_heads, n_v_heads, pool, scale, l2_eps, norm_eps,
                        err_count, t + T.k, t + T.g, t + T.u, w + W.q, w + W.v, w + W.beta,
-                       w + W.gram, reinterpret_cast<int *>(w + W.there), watchdog_block()};
+                       w + W.gram, reinterpret_cast<unsigned long long *>(w + W.paths), watchdog_block()};
     if (p.watchdog == nullptr) return GDN_ERR_LAUNCH;
     const cudaStream_t s = as_cuda(stream);
     switch (state_size) {
