@@ -31,16 +31,38 @@ struct Tape {
     }
 };
 
+// How the tensor-core path lays out what it prepares for a sequence and head, in bytes.
+struct TcSizes {
+    int pad, rows;                          // nodes, and vectors [K; Q], of an image: multiples of 8, of 16
+    uint32_t image, images;                 // of one part; of a (sequence, k-head)'s three
+    uint32_t weights_y, anc, beta, weights; // of a (sequence, v-head)'s: where what begins, and all
+    __host__ __device__ explicit TcSizes(int n) {
+        pad = (n + 7) / 8 * 8;
+        rows = 2 * pad;
+        image = static_cast<uint32_t>(rows) * 256u;
+        images = 3u * image;
+        weights_y = static_cast<uint32_t>(n * pad) * 4u;       // behind the weights in u, [n][pad]
+        anc = 2u * weights_y;                                  // which nodes they are of, [n][pad]
+        beta = anc + static_cast<uint32_t>(n * pad);           // [pad] each: beta, beta e^G, e^G, nodes on the path
+        weights = (beta + 16u * static_cast<uint32_t>(pad) + 15u) / 16u * 16u;
+    }
+};
+
 // Scratch: q [n][N][Hk][S], v [n][N][H][S], beta [n][N][H], the products k_i.k_s and q_i.k_s
-// [n][Hk][N][N][2], and the nodes' paths [n][N] (0: not there).
+// [n][Hk][N][N][2] or (states of 128) the images and weights of the tensor-core path, and the nodes' paths
+// [n][N] (0: not there).
 struct Scratch {
-    size_t q, v, beta, gram, paths, floats;
+    size_t q, v, beta, gram, weights, paths, floats;
     Scratch(size_t rows, int n_nodes, int hk, int h, int s) {
+        const size_t seqs = rows / n_nodes;
+        const TcSizes tc(n_nodes);
         q = 0;
         v = q + round_up(rows * hk * s);
         beta = v + round_up(rows * h * s);
         gram = beta + round_up(rows * h);
-        paths = gram + round_up(rows * n_nodes * hk * 2);
+        const size_t products = rows * n_nodes * hk * 2, images = seqs * hk * (tc.images / 4);
+        weights = gram + round_up(s == 128 && images > products ? images : products);
+        paths = weights + (s == 128 ? round_up(seqs * h * (tc.weights / 4)) : 0);
         floats = paths + round_up(rows * 2);
     }
 };
@@ -53,7 +75,8 @@ struct TreeParams {
     float scale, l2_eps, norm_eps;
     int32_t *err_count;
     float *k, *g, *u;             // the tape
-    float *q, *v, *beta, *gram;   // scratch
+    float *q, *v, *beta, *gram;   // scratch (gram: or the images)
+    uint8_t *weights;
     unsigned long long *paths;
     unsigned *watchdog;
 };
@@ -90,6 +113,24 @@ __global__ void __launch_bounds__(32 * kConvWarps) tree_conv_kernel(const TreePa
         if (counts && threadIdx.x == 0 && p.err_count) atomicAdd(p.err_count, 1);
         return;
     }
+    const int i0 = blockIdx.y * kConvNodes, i1 = min(N, i0 + kConvNodes);
+    const size_t row0 = static_cast<size_t>(n) * N;
+    const int slices = 2 * Hk + H, sl = blockIdx.x * kConvWarps + warp;  // this warp's head slice
+    const size_t conv_dim = static_cast<size_t>(slices) * S;
+    const size_t ch0 = static_cast<size_t>(sl) * S + E * lane;
+    const float *x_ptr = p.qkv + row0 * conv_dim + ch0;
+    // the lane's weights [E][K] and history [E][TAPS], consecutive in memory, and the nodes' own inputs:
+    // on their way while the paths are worked out (states of 256: no registers for the inputs)
+    constexpr bool kEarly = E <= 4;
+    float wc[E * K], hist[E * TAPS], own[kEarly ? kConvNodes : 1][E];
+    if (sl < slices) {
+        load_run<E * K>(wc, p.conv_w + ch0 * K);
+        load_run<E * TAPS>(hist, p.conv_state + (static_cast<size_t>(slot) * conv_dim + ch0) * TAPS);
+        if constexpr (kEarly)
+#pragma unroll
+            for (int y = 0; y < kConvNodes; ++y)
+                if (i0 + y < i1) load_vec<E>(own[y], x_ptr + static_cast<size_t>(i0 + y) * conv_dim);
+    }
     if (warp == 0) {
         unsigned long long paths[2];
         const bool bad = tree_paths(p.parents + static_cast<size_t>(n) * N, N, paths, path_of, up);
@@ -101,9 +142,6 @@ __global__ void __launch_bounds__(32 * kConvWarps) tree_conv_kernel(const TreePa
         }
     }
     __syncthreads();
-    const int i0 = blockIdx.y * kConvNodes, i1 = min(N, i0 + kConvNodes);
-    const size_t row0 = static_cast<size_t>(n) * N;
-    const int slices = 2 * Hk + H;
     if (blockIdx.x == gridDim.x - 1) {
         // ---- the gates: g = a softplus(alpha + dt), beta = sigmoid(b)
         for (int x = threadIdx.x; x < (i1 - i0) * H; x += 32 * kConvWarps) {
@@ -115,15 +153,7 @@ __global__ void __launch_bounds__(32 * kConvWarps) tree_conv_kernel(const TreePa
         }
         return;
     }
-    const int sl = blockIdx.x * kConvWarps + warp;  // this warp's head slice
     if (sl >= slices) return;
-    const size_t conv_dim = static_cast<size_t>(slices) * S;
-    const size_t ch0 = static_cast<size_t>(sl) * S + E * lane;
-    // the lane's weights [E][K] and history [E][TAPS], consecutive in memory
-    float wc[E * K], hist[E * TAPS];
-    load_run<E * K>(wc, p.conv_w + ch0 * K);
-    load_run<E * TAPS>(hist, p.conv_state + (static_cast<size_t>(slot) * conv_dim + ch0) * TAPS);
-    const float *x_ptr = p.qkv + row0 * conv_dim + ch0;
     const bool is_qk = sl < 2 * Hk;  // uniform over the warp
     float *dst = is_qk ? (sl < Hk ? p.q : p.k) + (row0 * Hk + sl % Hk) * S + E * lane
                        : p.v + (row0 * H + (sl - 2 * Hk)) * S + E * lane;
@@ -134,28 +164,34 @@ __global__ void __launch_bounds__(32 * kConvWarps) tree_conv_kernel(const TreePa
         if (i >= i1) break;  // uniform over the warp, as every condition below
         float o[E];
         unsigned long long path = path_of[i];
-        if (path == 0) {
+        const int depth = __popcll(path);
+        if (depth == 0) {
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] = 0.0f;
         } else {
-            // taps[t]: of the t-th oldest input, taps[TAPS] the node's own
-            float taps[K][E];
-            int behind = 0;  // taps past the root
+            float taps[K][E];  // [t]: of the t-th oldest input, [TAPS] the node's own
+            if constexpr (kEarly) {
 #pragma unroll
-            for (int t = TAPS; t >= 0; --t) {
+                for (int e = 0; e < E; ++e) taps[TAPS][e] = own[y][e];
+            } else {
+                load_vec<E>(taps[TAPS], x_ptr + static_cast<size_t>(i) * conv_dim);
+            }
+            path &= ~(1ull << i);
+#pragma unroll
+            for (int t = TAPS - 1; t >= 0; --t)
                 if (path != 0) {
                     const int a = 63 - __clzll(static_cast<long long>(path));
                     path &= ~(1ull << a);
                     load_vec<E>(taps[t], x_ptr + static_cast<size_t>(a) * conv_dim);
-                } else {
-                    ++behind;
-#pragma unroll
-                    for (int h = 1; h <= TAPS; ++h)
-                        if (h == behind)
-#pragma unroll
-                            for (int e = 0; e < E; ++e) taps[t][e] = hist[e * TAPS + TAPS - h];
                 }
-            }
+            // past the root: the history, newest last
+#pragma unroll
+            for (int d = 1; d <= TAPS; ++d)
+                if (depth == d)
+#pragma unroll
+                    for (int t = 0; t <= TAPS - d; ++t)
+#pragma unroll
+                        for (int e = 0; e < E; ++e) taps[t][e] = hist[e * TAPS + t + d - 1];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 float pre = __fmul_rn(taps[TAPS][e], wc[e * K + K - 1]);
@@ -378,8 +414,8 @@ __global__ void __launch_bounds__(kStateThreads) tree_state_kernel(const TreePar
 
 // State size 128: all products of a head's state with its nodes' k and q are one tcgen05 product
 // D = S [K; Q]^T, and the nodes' sums and the gated norm follow in the same CTA, so a state is read
-// once and y never leaves the SM. One CTA per (sequence, v-head), 256 threads; two CTAs share an SM
-// as long as 16 nodes fill half of tensor memory.
+// once and y never leaves the SM. 256 threads take (sequence, v-head) after (sequence, v-head); two CTAs
+// share an SM as long as 16 nodes fill half of tensor memory.
 //
 // The products keep fp32's precision: each operand is split into three bf16 parts, x = x1 + x2 + x3
 // (8 bits each, the rest below 2^-27 of x), and the six products of parts whose sizes multiply to
@@ -387,24 +423,41 @@ __global__ void __launch_bounds__(kStateThreads) tree_state_kernel(const TreePar
 // 2^-16, a hundred times the error of fp32 arithmetic.) The state's parts lie in tensor memory (lane =
 // value channel j), the nodes' in shared memory: three images of [K; Q], K-major core matrices.
 // S1 and S2 multiply the first two images at once, into two column groups that are added up later.
+//
+// A kernel ahead of it, per (sequence, k-head), writes the images, and for every v-head of the k-head
+// solves the nodes' triangular system: with A[i][s] = beta_i e^{G_i - G_s} k_i.k_s (s above i) and
+// T = (I + A)^-1,
+//   R_s = beta_s (v_s - e^{G_s} S0^T k_s),   u_i = sum_{s on the path to i} T[i][s] R_s,
+//   y_i = scale (e^{G_i} S0^T q_i + sum_s W[i][s] R_s),   W = B T, B[i][s] = e^{G_i - G_s} q_i.k_s,
+// so that over the state all nodes are independent of one another. T and W are lists along the paths.
+//
+// 64 sequences of 16 nodes, 16 k- and 32 v-heads: 114 us, of which the convolution takes 28, the
+// kernel ahead 29 and this one 56 (it reads 198 MB and writes 19 in that time: 3.9 TB/s; between
+// barriers its 16 warps an SM issue in 4 cycles of 10). Node after node over the state instead of T: 122
+// us. One sequence of 48 nodes: 39 us instead of 45, 13 of them here.
 constexpr int kTcThreads = 256;
 constexpr uint32_t kColA = 0, kColD = 192;  // tensor memory: the state's parts, 64 columns each; D, two groups
 
+// Shared memory of the state's kernel: the state, the images, the weights, D. Up to about 40 nodes D and
+// a second head's weights have places of their own, and what the next head needs is on its way as
+// soon as this one's products are under way; with more, D lies over the state.
 struct TcSmem {
-    int pad, rows;               // nodes, and vectors, of an image (a multiple of 8, of 16)
-    uint32_t images, weights_u, weights_y, anc, bytes;
-    __host__ __device__ explicit TcSmem(int n) {
-        pad = (n + 7) / 8 * 8;
-        rows = 2 * pad;
-        images = 65536;  // behind the state, [4][128 rows][128 bytes]
-        // of every node, its ancestors in order and itself, [n][pad]: their weights in u and in y, and which
-        weights_u = images + 3u * static_cast<uint32_t>(rows) * 256u;
-        weights_y = weights_u + static_cast<uint32_t>(n * pad) * 4u;
-        anc = weights_y + static_cast<uint32_t>(n * pad) * 4u;
-        bytes = anc + static_cast<uint32_t>(n * pad);
+    static constexpr uint32_t kMost = 225u * 1024u;
+    uint32_t images, weights, turn, d, bytes;  // turn: from a head's weights to the next one's
+    bool apart;
+    __host__ __device__ TcSmem(const TcSizes &z, int n) {
+        images = 65536;
+        weights = images + z.images;
+        const uint32_t two = weights + 2 * z.weights, all = two + 1024u * static_cast<uint32_t>(n);
+        apart = all <= kMost;
+        turn = apart ? z.weights : 0;
+        d = apart ? two : 0;
+        bytes = apart ? all : weights + z.weights;
     }
-    __host__ __device__ uint32_t tmem_cols() const { return kColD + 2u * static_cast<uint32_t>(rows) <= 256u ? 256u : 512u; }
 };
+__host__ __device__ inline uint32_t tmem_cols(const TcSizes &z) {
+    return kColD + 2u * static_cast<uint32_t>(z.rows) <= 256u ? 256u : 512u;
+}
 
 // x = p1 + p2 + p3 in bf16, two values to a word.
 __device__ __forceinline__ void split3(float a, float b, uint32_t &p1, uint32_t &p2, uint32_t &p3) {
@@ -417,249 +470,433 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t &p1, uint32_t 
     p3 = tc::pack_bf16x2(a, b);
 }
 
+// Images and weights. Grid: (k-head, sequence), 8 warps, or 16 where that leaves SMs idle. The nodes'
+// products, a warp a node; then, for a few v-heads at a time, A and B as lists along the paths, one
+// thread an entry, and T and W, all rows of one depth together.
+constexpr int kPrepThreads = 512;
+constexpr int kPrepHeads = 4;
+
+struct PrepSmem {
+    static constexpr int kLd = 128 + 4;       // floats of a vector: rows' 16-byte pieces in different banks
+    int heads;                                // at a time
+    uint32_t b, t, head, gram, anc, bytes;    // of a v-head: A, B and T, [N][pad]
+    __host__ __device__ explicit PrepSmem(int n) {
+        const uint32_t lists = TcSizes(n).weights_y;
+        b = lists;
+        t = 2 * lists;
+        head = 3 * lists;
+        heads = static_cast<int>(131072u / head);
+        heads = heads < 1 ? 1 : heads > kPrepHeads ? kPrepHeads : heads;
+        const uint32_t vectors = static_cast<uint32_t>(2 * n * kLd) * 4u, work = static_cast<uint32_t>(heads) * head;
+        gram = vectors > work ? vectors : work;  // behind the vectors, whose place A, B and T take
+        anc = gram + static_cast<uint32_t>(n * n) * 8u;
+        bytes = anc + lists / 4;
+    }
+};
+
+constexpr int kPrepSmem = 196608;  // no number of nodes needs more
+
+__global__ void __launch_bounds__(kPrepThreads, 2) tree_prepare_kernel(const TreeParams p) {
+    constexpr int S = 128, kLd = PrepSmem::kLd;
+    extern __shared__ __align__(16) uint8_t dyn[];
+    __shared__ unsigned long long path_of[kMaxNodes];
+    __shared__ int level[kMaxNodes + 1];      // [d]: where the nodes of depth d + 1 begin in by_depth
+    __shared__ uint8_t by_depth[kMaxNodes];
+    __shared__ float g_of[kPrepHeads][kMaxNodes], beta_of[kPrepHeads][kMaxNodes], hi_of[kPrepHeads][kMaxNodes], lo_of[kPrepHeads][kMaxNodes];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
+    const int kh = blockIdx.x, n = blockIdx.y, N = p.n_nodes, Hk = p.n_k_heads, H = p.n_v_heads;
+    const int slot = p.slots ? p.slots[n] : n;
+    if (slot < 0 || slot >= p.pool) return;
+    const TcSizes z(N);
+    const PrepSmem L(N);
+    float *rows = reinterpret_cast<float *>(dyn);  // k of all nodes, then q
+    float2 *gram = reinterpret_cast<float2 *>(dyn + L.gram);
+    uint8_t *anc = dyn + L.anc;  // [N][pad]: the path's nodes in order, then its first again
+    const size_t row0 = static_cast<size_t>(n) * N;
+    if (tid < N) path_of[tid] = p.paths[row0 + tid];
+    // ---- k and q, as they are and as images (rows past the nodes zero)
+    uint8_t *images = reinterpret_cast<uint8_t *>(p.gram) + (static_cast<size_t>(n) * Hk + kh) * z.images;
+    for (int x0 = tid; x0 < z.rows * (S / 8); x0 += 4 * threads) {
+        float v[4][8];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {  // (four pieces on their way together)
+            const int x = x0 + b * threads, r = x / S * 8 + x % 8, c = x / 8 % (S / 8), i = r < z.pad ? r : r - z.pad;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[b][e] = 0.0f;
+            if (r < z.rows && i < N) load_vec<8>(v[b], (r < z.pad ? p.k : p.q) + ((row0 + i) * Hk + kh) * S + 8 * c);
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int x = x0 + b * threads, r = x / S * 8 + x % 8, c = x / 8 % (S / 8), i = r < z.pad ? r : r - z.pad;
+            if (r >= z.rows) break;
+            if (i < N) store_vec<8>(rows + (r < z.pad ? i : N + i) * kLd + 8 * c, v[b]);
+            uint32_t w[3][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split3(v[b][2 * e], v[b][2 * e + 1], w[0][e], w[1][e], w[2][e]);
+            uint8_t *to = images + tc::kmajor_offset16(r, 8 * c, 128, S / 8 * 128);
+#pragma unroll
+            for (int y = 0; y < 3; ++y)
+                *reinterpret_cast<uint4 *>(to + y * z.image) = make_uint4(w[y][0], w[y][1], w[y][2], w[y][3]);
+        }
+    }
+    __syncthreads();
+    // ---- the paths as lists; the nodes by how deep they stand
+    for (int i = warp; i < N; i += threads / 32) {
+        const unsigned long long path = path_of[i];
+        for (int k = lane; k < z.pad; k += 32) {
+            if ((path >> k) & 1ull) anc[i * z.pad + __popcll(path & ((1ull << k) - 1))] = static_cast<uint8_t>(k);
+            if (k >= __popcll(path)) anc[i * z.pad + k] = path != 0 ? static_cast<uint8_t>(__ffsll(static_cast<long long>(path)) - 1) : 0;
+        }
+    }
+    if (tid < N) {
+        const int depth = __popcll(path_of[tid]);
+        int before = 0, upto = 0;  // nodes in front of this one; nodes that stand no deeper than tid + 1
+        for (int i = 0; i < N; ++i) {
+            const int other = __popcll(path_of[i]);
+            before += other < depth || (other == depth && i < tid);
+            upto += other <= tid;
+        }
+        by_depth[before] = static_cast<uint8_t>(tid);
+        level[tid] = upto;
+        if (tid == N - 1) level[N] = N;
+    }
+    __syncthreads();
+    for (int i = warp; i < N; i += threads / 32) {
+        const int count = __popcll(path_of[i]);
+        if (count == 0) continue;
+        float ki[4], qi[4];
+        load_vec<4>(ki, rows + i * kLd + 4 * lane);
+        load_vec<4>(qi, rows + (N + i) * kLd + 4 * lane);
+        for (int k = 0; k < count; k += 4) {
+            const uint32_t which = *reinterpret_cast<const uint32_t *>(anc + i * z.pad + k);
+            float part[8];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                float ks[4];
+                load_vec<4>(ks, rows + ((which >> (8 * m)) & 255u) * kLd + 4 * lane);
+                part[2 * m] = lane_dot<4>(ki, ks);
+                part[2 * m + 1] = lane_dot<4>(qi, ks);
+            }
+            const float sum = warp_sum_packed<8>(part, lane);
+            const float next = __shfl_xor_sync(FULL_MASK, sum, row_home_lane<8>(1));
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                if (lane == row_home_lane<8>(2 * m) && k + m < count)
+                    gram[i * N + ((which >> (8 * m)) & 255u)] = make_float2(sum, next);
+        }
+    }
+    const int groups = H / Hk;  // v-heads of this k-head: kh, kh + Hk, ..
+    const int at_once = min(L.heads, threads / kMaxNodes);
+    for (int h0 = 0; h0 < groups; h0 += at_once) {
+        const int heads = min(at_once, groups - h0);
+        __syncthreads();  // the products, or the v-heads before, are done with
+        auto out_of = [&](int h) { return p.weights + (static_cast<size_t>(n) * H + kh + (h0 + h) * Hk) * z.weights; };
+        // (a thread a node and v-head)
+        const int hx = tid / kMaxNodes, ix = tid % kMaxNodes;
+        if (hx < heads && ix < N) {
+            const size_t at = (row0 + ix) * H + kh + (h0 + hx) * Hk;
+            g_of[hx][ix] = p.g[at];
+            beta_of[hx][ix] = p.beta[at];
+        }
+        __syncthreads();
+        if (hx < heads && ix < z.pad) {
+            float hi = 0.0f, lo = 0.0f, beta = 0.0f;
+            if (ix < N) {
+                path_sum(path_of[ix], g_of[hx], hi, lo);
+                beta = beta_of[hx][ix];
+                hi_of[hx][ix] = hi;
+                lo_of[hx][ix] = lo;
+            }
+            const float decay = expf(hi + lo);
+            float *out = reinterpret_cast<float *>(out_of(hx) + z.beta);
+            out[ix] = beta;
+            out[z.pad + ix] = beta * decay;
+            out[2 * z.pad + ix] = decay;
+            reinterpret_cast<int *>(out)[3 * z.pad + ix] = ix < N ? __popcll(path_of[ix]) : 0;
+        }
+        __syncthreads();
+        for (int i = warp; i < N; i += threads / 32) {
+            const int count = __popcll(path_of[i]);
+            for (int k = lane; k < z.pad; k += 32) {
+                const int at = i * z.pad + k, s = anc[at];
+                const bool on = k < count - 1;  // (the node itself is taken apart)
+                const float2 dot = on ? gram[i * N + s] : make_float2(0.0f, 0.0f);
+                for (int h = 0; h < heads; ++h) {
+                    const float e = on ? expf((hi_of[h][i] - hi_of[h][s]) + (lo_of[h][i] - lo_of[h][s])) : 0.0f;
+                    float *list = reinterpret_cast<float *>(dyn + h * L.head);
+                    list[at] = on ? -beta_of[h][i] * e * dot.x : 0.0f;
+                    list[L.b / 4 + at] = on ? e * dot.y : k == count - 1 ? gram[i * N + i].y : 0.0f;
+                    list[L.t / 4 + at] = 0.0f;
+                    uint8_t *out = out_of(h);
+                    if (k % 4 == 0) *reinterpret_cast<uint32_t *>(out + z.anc + at) = *reinterpret_cast<const uint32_t *>(anc + at);
+                }
+            }
+        }
+        __syncthreads();
+        // T, kept like A: entry k of row i is the column of the path's k-th node, which is the k-th of
+        // the path of every node between the two as well. Rows of one depth need only those above: a
+        // lane an entry, 32 / width rows to a warp.
+        const int h = warp % heads, part = warp / heads, per = threads / 32 / heads;
+        const float *list = reinterpret_cast<const float *>(dyn + h * L.head);
+        float *t_of = reinterpret_cast<float *>(dyn + h * L.head + L.t);
+        for (int d = 1; d <= N && level[d - 1] < N; ++d) {
+            const int bits = d <= 8 ? 3 : d <= 16 ? 4 : 5, k = lane & ((1 << bits) - 1);
+            const int end = part < per ? level[d] : 0;
+            for (int r = level[d - 1] + (part << (5 - bits)) + (lane >> bits); r < end; r += per << (5 - bits)) {
+                const int at = by_depth[r] * z.pad;
+                float t[2] = {k == d - 1 ? 1.0f : 0.0f, k + 32 == d - 1 ? 1.0f : 0.0f};
+                for (int m0 = 0; m0 < d - 1; m0 += 4) {
+                    const uint32_t which = *reinterpret_cast<const uint32_t *>(anc + at + m0);
+                    float a[4];
+                    load_vec<4>(a, list + at + m0);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        const float *y = t_of + ((which >> (8 * m)) & 255u) * z.pad + k;
+                        t[0] = fmaf(a[m], y[0], t[0]);
+                        if (d > 32 && k + 32 < d) t[1] = fmaf(a[m], y[32], t[1]);
+                    }
+                }
+                if (k < d) t_of[at + k] = t[0];
+                if (k + 32 < d) t_of[at + k + 32] = t[1];
+            }
+            __syncthreads();
+        }
+        // W = B T, and both to their places
+        for (int i = warp; i < N; i += threads / 32) {
+            const int count = __popcll(path_of[i]), at = i * z.pad;
+            if (count == 0) continue;
+            for (int k = lane; k < z.pad; k += 32) {
+                for (int h = 0; h < heads; ++h) {
+                    const float *b_list = reinterpret_cast<const float *>(dyn + h * L.head + L.b);
+                    const float *t_list = reinterpret_cast<const float *>(dyn + h * L.head + L.t);
+                    float w = 0.0f;
+                    for (int m0 = 0; m0 < count; m0 += 4) {
+                        const uint32_t which = *reinterpret_cast<const uint32_t *>(anc + at + m0);
+                        float b[4];
+                        load_vec<4>(b, b_list + at + m0);
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) w = fmaf(b[m], t_list[((which >> (8 * m)) & 255u) * z.pad + k], w);
+                    }
+                    reinterpret_cast<float *>(out_of(h))[at + k] = t_list[at + k];
+                    reinterpret_cast<float *>(out_of(h) + z.weights_y)[at + k] = w;
+                }
+            }
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kTcThreads, 2) tree_state_tc_kernel(const __grid_constant__ CUtensorMap state_map,
-                                                                      const TreeParams p) {
+                                                                      const TreeParams p, int items) {
     constexpr int S = 128;
     extern __shared__ uint8_t dyn[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
-    __shared__ __align__(8) uint64_t state_full, d_full;
+    __shared__ __align__(8) uint64_t state_full, images_full, d_full;
     __shared__ uint32_t tmem_base;
-    __shared__ unsigned long long path_of[kMaxNodes];
-    __shared__ float g_of[kMaxNodes], hi_of[kMaxNodes], lo_of[kMaxNodes], beta_of[kMaxNodes], decay[kMaxNodes];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int N = p.n_nodes, Hk = p.n_k_heads, H = p.n_v_heads;
-    const int vh = blockIdx.x % H, n = blockIdx.x / H, kh = vh % Hk;
-    const int slot = p.slots ? p.slots[n] : n;
-    if (slot < 0 || slot >= p.pool) return;
-    const TcSmem L(N);
-    float *d = reinterpret_cast<float *>(smem);  // later, over the state: [2N][128] products with k, then u; with q
-    float *weights_u = reinterpret_cast<float *>(smem + L.weights_u), *weights_y = reinterpret_cast<float *>(smem + L.weights_y);
-    uint8_t *anc = smem + L.anc;
-    const size_t row0 = static_cast<size_t>(n) * N;
-
+    const TcSizes z(N);
+    const TcSmem L(z, N);
+    // the next head from `item` on whose sequence has a slot, or `items`
+    auto from = [&](int item) {
+        for (; item < items; item += gridDim.x) {
+            const int slot = p.slots ? p.slots[item / H] : item / H;
+            if (slot >= 0 && slot < p.pool) break;
+        }
+        return min(item, items);
+    };
+    auto load_state = [&](int item) {
+        const int slot = p.slots ? p.slots[item / H] : item / H;
+        mbar_arrive_expect_tx(&state_full, S * S * 4);
+        tma_load_3d(smem, &state_map, 0, (slot * H + item % H) * S, 0, &state_full);
+    };
+    auto load_images = [&](int item, int turn) {
+        const size_t image = static_cast<size_t>(item / H) * Hk + item % H % Hk;
+        mbar_arrive_expect_tx(&images_full, z.images + z.weights);
+        bulk_g2s(smem + L.images, reinterpret_cast<const uint8_t *>(p.gram) + image * z.images, z.images, &images_full);
+        bulk_g2s(smem + L.weights + turn * L.turn, p.weights + static_cast<size_t>(item) * z.weights, z.weights, &images_full);
+    };
+    int item = from(blockIdx.x);
+    if (item == items) return;
     if (tid == 0) {
         mbar_init(&state_full, 1);
+        mbar_init(&images_full, 1);
         mbar_init(&d_full, 1);
         fence_mbar_init();
-        mbar_arrive_expect_tx(&state_full, S * S * 4);
-        tma_load_3d(smem, &state_map, 0, (slot * H + vh) * S, 0, &state_full);
-    }
-    if (tid >= 128 && tid < 128 + N) {
-        const int i = tid - 128;
-        path_of[i] = p.paths[row0 + i];
-        g_of[i] = p.g[(row0 + i) * H + vh];
-        beta_of[i] = p.beta[(row0 + i) * H + vh];
-    }
-    // ---- the images of [K; Q], rows past the nodes zero: 8 cells of two rows a thread at a time
-    for (int x0 = tid; x0 < L.rows * (S / 8); x0 += 2 * kTcThreads) {
-        float v[2][8] = {};
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            const int x = x0 + y * kTcThreads, r = x / (S / 8), c = x % (S / 8), i = r < L.pad ? r : r - L.pad;
-            if (r < L.rows && i < N) load_vec<8>(v[y], (r < L.pad ? p.k : p.q) + ((row0 + i) * Hk + kh) * S + 8 * c);
-        }
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            const int x = x0 + y * kTcThreads, r = x / (S / 8), c = x % (S / 8);
-            if (r >= L.rows) break;
-            uint32_t w[3][4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) split3(v[y][2 * e], v[y][2 * e + 1], w[0][e], w[1][e], w[2][e]);
-            uint8_t *to = smem + L.images + tc::kmajor_offset16(r, 8 * c, 128, S / 8 * 128);
-#pragma unroll
-            for (int z = 0; z < 3; ++z)
-                *reinterpret_cast<uint4 *>(to + z * L.rows * 256) = make_uint4(w[z][0], w[z][1], w[z][2], w[z][3]);
-        }
+        load_state(item);
+        load_images(item, 0);
     }
     if (warp == 1) {
-        tc::tmem_alloc(&tmem_base, L.tmem_cols());
+        tc::tmem_alloc(&tmem_base, tmem_cols(z));
         tc::tmem_relinquish();  // (another CTA's turn)
     }
+    float norm_w[4];
+    load_vec<4>(norm_w, p.norm_w + 4 * lane);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = tmem_base;
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const int half = warp >> 2, j = (warp & 3) * 32 + lane;  // state row of this thread, which half of its cells
-    if (tid < N) {
-        path_sum(path_of[tid], g_of, hi_of[tid], lo_of[tid]);
-        decay[tid] = expf(hi_of[tid] + lo_of[tid]);
-    }
-    // ---- the state's parts
-    bool ok = mbar_wait(&state_full, 0);
-    if (ok) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {  // 32 cells: a 128-byte column
-            const int col = 2 * half + b;
-            uint32_t w1[16], w2[16], w3[16];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const float4 x = *reinterpret_cast<const float4 *>(smem + col * 16384 + j * 128 + ((c ^ (j & 7)) << 4));
-                split3(x.x, x.y, w1[2 * c], w2[2 * c], w3[2 * c]);
-                split3(x.z, x.w, w1[2 * c + 1], w2[2 * c + 1], w3[2 * c + 1]);
-            }
-            tc::tmem_st16(lanes + kColA + 16 * col, w1);
-            tc::tmem_st16(lanes + kColA + 64 + 16 * col, w2);
-            tc::tmem_st16(lanes + kColA + 128 + 16 * col, w3);
-        }
-        tc::tmem_st_wait();
-    }
-    fence_proxy_async_smem();  // the images, before the products read them
-    tc::fence_before_sync();
-    ok = __syncthreads_and(ok);
-    tc::fence_after_sync();
-    if (ok && warp == 0) {
-        if (elect_one()) {
-            const uint64_t image = tc::smem_desc(smem + L.images, 128, S / 8 * 128);
-            const uint32_t part = static_cast<uint32_t>(L.rows) * 256u >> 4;  // from an image to the next, in 16 bytes
-            const uint32_t wide = tc::idesc_bf16(128, 2 * L.rows), one = tc::idesc_bf16(128, L.rows);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {  // 16 cells at a time
-                const uint32_t a = tmem + kColA + 8 * x;
-                const uint64_t b = image + 16 * x;
-                tc::mma_bf16_ts(tmem + kColD, a, b, wide, x > 0);
-                tc::mma_bf16_ts(tmem + kColD, a + 64, b, wide, true);
-                tc::mma_bf16_ts(tmem + kColD, a, b + 2 * part, one, true);
-                tc::mma_bf16_ts(tmem + kColD, a + 128, b, one, true);
-            }
-            tc::mma_commit(&d_full);
-        }
-        __syncwarp();
-    }
-    // ---- meanwhile the nodes' weights for one another, and their values
-    const int v_count = N * (S / 4);  // 16-byte parts of the nodes' values
-    float4 v_part[8];
-#pragma unroll
-    for (int y = 0; y < 8; ++y) {
-        const int x = tid + y * kTcThreads;
-        if (x < v_count)
-            v_part[y] = *reinterpret_cast<const float4 *>(p.v + ((row0 + x / (S / 4)) * H + vh) * S + 4 * (x % (S / 4)));
-    }
-    const float2 *gram = reinterpret_cast<const float2 *>(p.gram) + (static_cast<size_t>(n) * Hk + kh) * N * N;
-#pragma unroll 4
-    for (int x = tid; x < N * L.pad; x += kTcThreads) {
-        const int i = x / L.pad, s = x - i * L.pad;
-        const unsigned long long path = path_of[i];
-        const float2 dot = s < N ? gram[i * N + s] : make_float2(0.0f, 0.0f);
-        if ((path >> s) & 1ull) {
-            const float w = expf((hi_of[i] - hi_of[s]) + (lo_of[i] - lo_of[s]));
-            const int at = i * L.pad + __popcll(path & ((1ull << s) - 1));
-            weights_u[at] = s == i ? 0.0f : -beta_of[i] * w * dot.x;
-            weights_y[at] = w * dot.y;
-            anc[at] = static_cast<uint8_t>(s);
-        }
-        // (places behind the path: the node itself with weights of zero)
-        const int behind = __popcll(path) + s;
-        if (behind < L.pad) {
-            weights_u[i * L.pad + behind] = weights_y[i * L.pad + behind] = 0.0f;
-            anc[i * L.pad + behind] = static_cast<uint8_t>(i);
-        }
-    }
-    ok = ok && mbar_wait(&d_full, 0);
-    tc::fence_after_sync();
-    if (ok) {
-        // (the state's cells have been read: every thread has passed the barrier above)
-        for (int c = 16 * half; c < L.rows; c += 32) {
-            uint32_t x[16], y[16];
-            tc::tmem_ld16_nowait(lanes + kColD + c, x);
-            tc::tmem_ld16_nowait(lanes + kColD + L.rows + c, y);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int r = c + e, i = r < L.pad ? r : r - L.pad;
-                if (i < N) d[(r < L.pad ? i : N + i) * S + j] = __uint_as_float(x[e]) + __uint_as_float(y[e]);
-            }
-        }
-        // the values over the images, which have been multiplied
+    const int v_count = N * (S / 4);
+    const size_t step = static_cast<size_t>(H) * S;
+    float *d = reinterpret_cast<float *>(smem + L.d);  // [2N][128]
+    bool ok = true;
+    for (int turn = 0, phase = 0; item < items && ok; turn ^= 1, phase ^= 1) {
+        const int after = from(item + gridDim.x);
+        const size_t at0 = (static_cast<size_t>(item / H) * N * H + item % H) * S;
+        // the nodes' values, 16 bytes a time, and gates of the warp's first node
+        float4 v_part[8];
 #pragma unroll
         for (int y = 0; y < 8; ++y) {
             const int x = tid + y * kTcThreads;
-            if (x < v_count) *reinterpret_cast<float4 *>(smem + L.images + 16 * x) = v_part[y];
+            if (x < v_count) v_part[y] = *reinterpret_cast<const float4 *>(p.v + at0 + x / (S / 4) * step + 4 * (x % (S / 4)));
         }
-    }
-    tc::fence_before_sync();
-    ok = __syncthreads_and(ok);
-    if (warp == 1) {
+        float gate[4] = {};
+        if (warp < N) load_vec<4>(gate, p.z + at0 + warp * step + 4 * lane);
+        // ---- the state's parts
+        ok = mbar_wait(&state_full, phase);
+        if (ok) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {  // 32 cells: a 128-byte column
+                const int col = 2 * half + b;
+                uint32_t w1[16], w2[16], w3[16];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float4 x = *reinterpret_cast<const float4 *>(smem + col * 16384 + j * 128 + ((c ^ (j & 7)) << 4));
+                    split3(x.x, x.y, w1[2 * c], w2[2 * c], w3[2 * c]);
+                    split3(x.z, x.w, w1[2 * c + 1], w2[2 * c + 1], w3[2 * c + 1]);
+                }
+                tc::tmem_st16(lanes + kColA + 16 * col, w1);
+                tc::tmem_st16(lanes + kColA + 64 + 16 * col, w2);
+                tc::tmem_st16(lanes + kColA + 128 + 16 * col, w3);
+            }
+            tc::tmem_st_wait();
+        }
+        ok = mbar_wait(&images_full, phase) && ok;
+        tc::fence_before_sync();
+        ok = __syncthreads_and(ok);
         tc::fence_after_sync();
-        tc::tmem_dealloc(tmem, L.tmem_cols());
-    }
-    if (!ok) {
-        if (tid == 0) atomicOr(p.watchdog, WD_STATE_COPY);
-        return;  // (nothing of this head is written)
-    }
-    // ---- u, one thread a row, node after node, four ancestors at a time; the other threads fetch what
-    // the norm needs
-    float zv[2][4], wv[4];
-    load_vec<4>(wv, p.norm_w + 4 * lane);
-    const size_t z_at = (row0 * H + vh) * S + 4 * lane, z_step = static_cast<size_t>(H) * S;
+        if (ok && warp == 0) {
+            if (elect_one()) {
+                const uint64_t image = tc::smem_desc(smem + L.images, 128, S / 8 * 128);
+                const uint32_t part = z.image >> 4;  // from an image to the next, in 16 bytes
+                const uint32_t wide = tc::idesc_bf16(128, 2 * z.rows), one = tc::idesc_bf16(128, z.rows);
 #pragma unroll
-    for (int y = 0; y < 2; ++y)
-        if (warp + 8 * y < N) load_vec<4>(zv[y], p.z + z_at + (warp + 8 * y) * z_step);
-    if (tid < S) {
-        const float *v = reinterpret_cast<const float *>(smem + L.images) + tid;
-        float *u_out = p.u + (row0 * H + vh) * S + tid;
-        for (int i = 0; i < N; ++i) {
-            const unsigned long long path = path_of[i];
-            const int count = __popcll(path) - 1;  // ancestors
-            const float *w = weights_u + i * L.pad;
-            const uint32_t *which = reinterpret_cast<const uint32_t *>(anc + i * L.pad);
-            float u = beta_of[i] * (v[i * S] - decay[i] * d[i * S + tid]), u2 = 0.0f;
-            for (int k = 0; k < count; k += 4) {
-                const uint32_t a = which[k / 4];
-                const float4 x = *reinterpret_cast<const float4 *>(w + k);
-                u = fmaf(x.x, d[(a & 255u) * S + tid], u);
-                u2 = fmaf(x.y, d[((a >> 8) & 255u) * S + tid], u2);
-                u = fmaf(x.z, d[((a >> 16) & 255u) * S + tid], u);
-                u2 = fmaf(x.w, d[(a >> 24) * S + tid], u2);
+                for (int x = 0; x < 8; ++x) {  // 16 cells at a time
+                    const uint32_t a = tmem + kColA + 8 * x;
+                    const uint64_t b = image + 16 * x;
+                    tc::mma_bf16_ts(tmem + kColD, a, b, wide, x > 0);
+                    tc::mma_bf16_ts(tmem + kColD, a + 64, b, wide, true);
+                    tc::mma_bf16_ts(tmem + kColD, a, b + 2 * part, one, true);
+                    tc::mma_bf16_ts(tmem + kColD, a + 128, b, one, true);
+                }
+                tc::mma_commit(&d_full);
+                if (L.apart && after < items) load_state(after);
             }
-            u = path == 0 ? 0.0f : u + u2;
-            d[i * S + tid] = u;
-            u_out[i * z_step] = u;
+            __syncwarp();
         }
-    }
-    __syncthreads();
-    // ---- y and the gated norm, a warp a node: the lane's four channels
-    for (int i = warp, turn = 0; i < N; i += kTcThreads / 32, ++turn) {
-        const unsigned long long path = path_of[i];
-        float y[4] = {};
-        if (path != 0) {
-            float z[4];
-            if (turn < 2) {
+        ok = ok && mbar_wait(&d_full, phase);
+        tc::fence_after_sync();
+        if (ok) {
+            // (the weights' other place was last read before the barrier above)
+            if (L.apart && tid == 0 && after < items) load_images(after, turn ^ 1);
+            for (int c = 16 * half; c < z.rows; c += 32) {
+                uint32_t x[16], y[16];
+                tc::tmem_ld16_nowait(lanes + kColD + c, x);
+                tc::tmem_ld16_nowait(lanes + kColD + z.rows + c, y);
+                tc::tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 4; ++e) z[e] = turn ? zv[1][e] : zv[0][e];
-            } else {
-                load_vec<4>(z, p.z + z_at + i * z_step);
-            }
-            load_vec<4>(y, d + (N + i) * S + 4 * lane);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] *= decay[i];
-            const float *w = weights_y + i * L.pad;
-            const uint32_t *which = reinterpret_cast<const uint32_t *>(anc + i * L.pad);
-            const int count = __popcll(path);
-            for (int k = 0; k < count; k += 4) {
-                const uint32_t a = which[k / 4];
-                const float4 x = *reinterpret_cast<const float4 *>(w + k);
-                const float ws[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    float u[4];
-                    load_vec<4>(u, d + ((a >> (8 * m)) & 255u) * S + 4 * lane);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = fmaf(ws[m], u[e], y[e]);
+                for (int e = 0; e < 16; ++e) {
+                    const int r = c + e, i = r < z.pad ? r : r - z.pad;
+                    if (i < N) d[(r < z.pad ? i : N + i) * S + j] = __uint_as_float(x[e]) + __uint_as_float(y[e]);
                 }
             }
-            float ss = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                y[e] *= p.scale;
-                ss = __fmaf_rn(y[e], y[e], ss);
-            }
-            ss = warp_allsum(ss);
-            const float inv_rms = 1.0f / sqrtf(ss / static_cast<float>(S) + p.norm_eps);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = y[e] * inv_rms * wv[e] * silu(z[e]);
         }
-        store_vec<4>(p.out + z_at + i * z_step, y);
+        tc::fence_before_sync();
+        ok = __syncthreads_and(ok);
+        tc::fence_after_sync();
+        if (!ok) break;  // (nothing of this head is written)
+        // ---- R over the products with k
+        const uint8_t *w = smem + L.weights + turn * L.turn;
+        const float *weights_u = reinterpret_cast<const float *>(w), *weights_y = reinterpret_cast<const float *>(w + z.weights_y);
+        const float *beta = reinterpret_cast<const float *>(w + z.beta);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+            const int x = tid + y * kTcThreads, i = x / (S / 4);
+            if (x >= v_count) break;
+            float4 r = *reinterpret_cast<const float4 *>(d + 4 * x);
+            const float b = beta[i], bd = -beta[z.pad + i];
+            r = make_float4(fmaf(bd, r.x, b * v_part[y].x), fmaf(bd, r.y, b * v_part[y].y),
+                            fmaf(bd, r.z, b * v_part[y].z), fmaf(bd, r.w, b * v_part[y].w));
+            *reinterpret_cast<float4 *>(d + 4 * x) = r;
+        }
+        __syncthreads();
+        // ---- u, y and the gated norm, a warp a node: the lane's four channels
+        for (int i = warp; i < N; i += kTcThreads / 32) {
+            const float *wu = weights_u + i * z.pad, *wy = weights_y + i * z.pad;
+            const uint32_t *which = reinterpret_cast<const uint32_t *>(w + z.anc + i * z.pad);
+            const int count = reinterpret_cast<const int *>(beta)[3 * z.pad + i];  // (0: no node)
+            float u[4] = {}, y[4] = {}, next_gate[4] = {};
+            if (i + kTcThreads / 32 < N) load_vec<4>(next_gate, p.z + at0 + (i + kTcThreads / 32) * step + 4 * lane);
+            if (count > 0) {
+                load_vec<4>(y, d + (N + i) * S + 4 * lane);
+                const float decay = beta[2 * z.pad + i];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] *= decay;
+                for (int k = 0; k < count; k += 4) {
+                    const uint32_t a = which[k / 4];
+                    float us[4], ys[4];
+                    load_vec<4>(us, wu + k);
+                    load_vec<4>(ys, wy + k);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        float r[4];
+                        load_vec<4>(r, d + ((a >> (8 * m)) & 255u) * S + 4 * lane);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            u[e] = fmaf(us[m], r[e], u[e]);
+                            y[e] = fmaf(ys[m], r[e], y[e]);
+                        }
+                    }
+                }
+                float ss = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    y[e] *= p.scale;
+                    ss = __fmaf_rn(y[e], y[e], ss);
+                }
+                ss = warp_allsum(ss);
+                const float inv_rms = 1.0f / sqrtf(ss / static_cast<float>(S) + p.norm_eps);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = y[e] * inv_rms * norm_w[e] * silu(gate[e]);
+            }
+            store_vec<4>(p.u + at0 + i * step + 4 * lane, u);
+            store_vec<4>(p.out + at0 + i * step + 4 * lane, y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) gate[e] = next_gate[e];
+        }
+        if (!L.apart) {  // D's and the weights' places are the next head's
+            fence_proxy_async_smem();
+            __syncthreads();
+            if (tid == 0 && after < items) {
+                load_state(after);
+                load_images(after, 0);
+            }
+        }
+        item = after;
+    }
+    if (!ok) {
+        // (no copy may still be on its way into a CTA that has ended)
+        mbar_wait(&state_full, 0);
+        mbar_wait(&state_full, 1);
+        mbar_wait(&images_full, 0);
+        mbar_wait(&images_full, 1);
+        if (tid == 0) atomicOr(p.watchdog, WD_STATE_COPY);
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, tmem_cols(z));
     }
 }
 
@@ -825,23 +1062,32 @@ gdn_status launch_block(const TreeParams &p, int n_seqs, int conv_kernel, cudaSt
         case 7: GDN_TRY((launch_conv<E, 7>(p, n_seqs, s))); break;
         default: GDN_TRY((launch_conv<E, 8>(p, n_seqs, s))); break;
     }
-    const size_t keys = static_cast<size_t>(p.n_nodes) * 32 * E * sizeof(float);
-    static std::atomic<unsigned long long> gram_allowed{0};
-    GDN_TRY(allow_smem(tree_gram_kernel<E>, kMaxNodes * 32 * E * static_cast<int>(sizeof(float)), gram_allowed));
-    tree_gram_kernel<E><<<dim3(p.n_k_heads, n_seqs), 32 * kGramWarps, keys, s>>>(p);
-    GDN_TRY(launch_status());
     if constexpr (E == 4) {
         // (a tensor map's rows are counted in 32 bits)
         const long long state_rows = static_cast<long long>(p.pool) * p.n_v_heads * 128;
         if (state_rows <= 0x7fffffffLL) {
             CUtensorMap map;
             GDN_TRY(encode_blocks_map(&map, p.state, GDN_F32, 128, static_cast<uint64_t>(state_rows), 512, 128, 4));
-            static std::atomic<unsigned long long> allowed{0};
-            GDN_TRY(allow_smem(tree_state_tc_kernel, static_cast<int>(TcSmem(kMaxNodes).bytes) + 1024, allowed));
-            tree_state_tc_kernel<<<static_cast<unsigned>(n_seqs) * p.n_v_heads, kTcThreads, TcSmem(p.n_nodes).bytes + 1024, s>>>(map, p);
+            static std::atomic<unsigned long long> allowed{0}, prepare_allowed{0};
+            GDN_TRY(allow_smem(tree_prepare_kernel, kPrepSmem, prepare_allowed));
+            GDN_TRY(allow_smem(tree_state_tc_kernel, TcSmem::kMost + 1024, allowed));
+            // all CTAs at once, and as many warps as that leaves
+            const long long ctas = static_cast<long long>(n_seqs) * p.n_k_heads;
+            const int threads = ctas <= 152 ? kPrepThreads : ctas <= 4 * 152 ? kPrepThreads / 2 : kPrepThreads / 4;
+            tree_prepare_kernel<<<dim3(p.n_k_heads, n_seqs), threads, PrepSmem(p.n_nodes).bytes, s>>>(p);
+            GDN_TRY(launch_status());
+            const TcSizes z(p.n_nodes);
+            const uint32_t smem = TcSmem(z, p.n_nodes).bytes + 1024;
+            const int items = n_seqs * p.n_v_heads, wide = 152 * (tmem_cols(z) <= 256 && smem <= 113 * 1024 ? 2 : 1);
+            tree_state_tc_kernel<<<items < wide ? items : wide, kTcThreads, smem, s>>>(map, p, items);
             return launch_status();
         }
     }
+    const size_t keys = static_cast<size_t>(p.n_nodes) * 32 * E * sizeof(float);
+    static std::atomic<unsigned long long> gram_allowed{0};
+    GDN_TRY(allow_smem(tree_gram_kernel<E>, kMaxNodes * 32 * E * static_cast<int>(sizeof(float)), gram_allowed));
+    tree_gram_kernel<E><<<dim3(p.n_k_heads, n_seqs), 32 * kGramWarps, keys, s>>>(p);
+    GDN_TRY(launch_status());
     using L = StateSmem<E>;
     const size_t smem = L::bytes(p.n_nodes);
     if (cudaFuncSetAttribute(tree_state_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -924,7 +1170,8 @@ gdn_status gdn_block_tree(const float *qkv, const float *conv_w, const float *co
     const TreeParams p{qkv, conv_w, conv_state, alpha, b, dt, a, z, norm_w, state, out, parents,
                        slots, n_nodes, n_k_heads, n_v_heads, pool, scale, l2_eps, norm_eps,
                        err_count, t + T.k, t + T.g, t + T.u, w + W.q, w + W.v, w + W.beta,
-                       w + W.gram, reinterpret_cast<unsigned long long *>(w + W.paths), watchdog_block()};
+                       w + W.gram, reinterpret_cast<uint8_t *>(w + W.weights),
+                       reinterpret_cast<unsigned long long *>(w + W.paths), watchdog_block()};
     if (p.watchdog == nullptr) return GDN_ERR_LAUNCH;
     const cudaStream_t s = as_cuda(stream);
     switch (state_size) {
