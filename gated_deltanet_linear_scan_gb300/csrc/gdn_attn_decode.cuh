@@ -40,6 +40,7 @@
 
 #include "gdn_chunk_common.cuh"  // named_barrier_or
 #include "gdn_paged.cuh"
+#include "gdn_tc.cuh"  // split3
 #include "gdn_tree.cuh"
 
 namespace gdn {
@@ -178,6 +179,18 @@ __device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// c += a b for operands of three bf16 parts each: the six products whose sizes multiply to 2^-18 or more,
+// the largest apart.
+__device__ __forceinline__ void mma_split3(float (&big)[4], float (&small)[4], const uint32_t (&a)[3][4],
+                                           const uint32_t (&b0)[3], const uint32_t (&b1)[3]) {
+    mma16816<__nv_bfloat16>(small, a[2], b0[0], b1[0]);
+    mma16816<__nv_bfloat16>(big, a[0], b0[0], b1[0]);
+    mma16816<__nv_bfloat16>(small, a[0], b0[2], b1[2]);
+    mma16816<__nv_bfloat16>(small, a[1], b0[1], b1[1]);
+    mma16816<__nv_bfloat16>(small, a[1], b0[0], b1[0]);
+    mma16816<__nv_bfloat16>(small, a[0], b0[1], b1[1]);
 }
 
 // Shared-memory tiles keep the pages' parts apart, each `rows` rows of 128 bytes for every
@@ -587,19 +600,26 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     // 16-bit: NT tiles of 8 columns (a quarter of the head), rows lane/4 and lane/4 + 8
     constexpr int NT = D / 32;
     constexpr int KN = G::kWarpKeys / 8;  // 8-key tiles of S of a warp
-    float o16[G::kF32 ? 1 : NT][4];
+    // fp32 trees of more than 8 rows a unit: the same fragments, of operands split into three bf16 parts
+    // (x = x1 + x2 + x3 with 8 bits each) and six products of them, which keeps fp32's precision (2^-25 of
+    // |x| |y| is left out). 96 padded trees of 9 nodes, 3 query heads a key head of 64, windows of 1024 of up
+    // to 16384 keys: 75 us, on the FP32 pipes 130. (Heads of 256: registers for Q's parts run out.)
+    constexpr bool kSplit = G::kF32 && TREE && RT == 16 && D <= 128;
+    constexpr bool kFrag = !G::kF32 || kSplit;
+    float o16[kFrag ? NT : 1][4];
     uint32_t qf[G::kF32 ? 1 : D / 16][4];
+    uint32_t q3[kSplit ? D / 16 : 1][3][4];
     // fp32: LPR threads to a row in the softmax; in P V a lane holds 4 columns, C4 lanes
     // span the quarter and NKG groups of lanes split the keys
     constexpr int LPR = kCompute / RT;
     constexpr int C4 = D / 16;
     constexpr int NKG = 32 / C4;
-    float o32[G::kF32 ? RT : 1][4];
+    float o32[kFrag ? 1 : RT][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
     Segment sg{};
     // rows of this thread (16-bit: lane / 4 and lane / 4 + 8; fp32: the row of its scores):
     // token and head in the unit, position
-    const int row0 = G::kF32 ? tid / LPR : lane >> 2, row1 = (lane >> 2) + 8;
+    const int row0 = kFrag ? lane >> 2 : tid / LPR, row1 = (lane >> 2) + 8;
     const int tok0 = row0 / p.heads_per_unit, tok1 = row1 / p.heads_per_unit;
     int pos0 = 0, pos1 = 0;
     unsigned long long tree0 = 0, tree1 = 0, nodes = 0;  // nodes that the rows see; that are there
@@ -656,7 +676,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                            (p_last - key0 < p.mask.window || key0 + KT <= p.mask.sinks);
         // The keys that P V takes, whole groups of kGroup: those between the first and the last
         // that some row sees.
-        constexpr int kGroup = G::kF32 ? 8 : 16;
+        constexpr int kGroup = kFrag ? 16 : 8;
         int g_lo = 0, g_hi = KT / kGroup;
         if (!clean) {
             const int lo = p.mask.first(max(p_first, 0)) - key0;  // of the window
@@ -698,9 +718,30 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         }
         const uint8_t *q_here = q_smem + (seg & 1) * G::kQ;
 
-        if constexpr (!G::kF32) {
+        if constexpr (kFrag) {
             const uint32_t ks = smem_addr(k_tile(s)), vs = smem_addr(v_tile(s));
-            if (flags & kFirst) {
+            if constexpr (kSplit) {
+                if (flags & kFirst) {
+                    // dims 4 t .. 4 t + 3 of every 16 are lane t's places 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of a
+                    // product, in Q and K alike
+                    const Tile q_tile{4, 0};
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int r = (lane >> 2) + 8 * h;
+                            const float4 x = *reinterpret_cast<const float4 *>(q_here + r * 128 + q_tile.chunk(r, 4 * kk + (lane & 3)));
+                            tc::split3(x.x, x.y, q3[kk][0][h], q3[kk][1][h], q3[kk][2][h]);
+                            tc::split3(x.z, x.w, q3[kk][0][2 + h], q3[kk][1][2 + h], q3[kk][2][2 + h]);
+                        }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&q_empty[seg & 1]);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o16[j][e] = 0.0f;
+                }
+            } else if (flags & kFirst) {
                 const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
                 const Tile q_tile{4, 0};
 #pragma unroll
@@ -715,23 +756,49 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             }
             // S = Q K^T for this warp's keys, 16 at a time (two chains of products per 8 keys)
             float sc[KN][4];
+            if constexpr (kSplit) {
 #pragma unroll
-            for (int h = 0; h < KN / 2; ++h) {
-                float acc[2][2][4] = {};
-                const int key = warp * G::kWarpKeys + h * 16 + (lane & 7) + (lane >> 4) * 8;
-                const uint32_t kr = ks + tile.row(key);
+                for (int b = 0; b < KN; ++b) {
+                    const int key = warp * G::kWarpKeys + b * 8 + (lane >> 2);
+                    const uint8_t *kr = k_tile(s) + tile.row(key);
+                    float big[4] = {}, small[4] = {};
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    uint32_t b[4];
-                    ldsm4(b, kr + tile.chunk(key, 2 * kk + ((lane >> 3) & 1)));
-                    mma16816<T>(acc[kk & 1][0], qf[kk], b[0], b[1]);
-                    mma16816<T>(acc[kk & 1][1], qf[kk], b[2], b[3]);
+                    for (int kk = 0; kk < D / 16; kk += 2) {
+                        // (of two 16 dims, odd keys read the second first: 8 lanes, 8 places of 16 bytes)
+                        const int odd = (lane >> 2) & 1;
+                        const float4 x = *reinterpret_cast<const float4 *>(kr + tile.chunk(key, 4 * (kk + odd) + (lane & 3)));
+                        const float4 y = *reinterpret_cast<const float4 *>(kr + tile.chunk(key, 4 * (kk + 1 - odd) + (lane & 3)));
+                        const float4 k2[2] = {odd ? y : x, odd ? x : y};
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            uint32_t b0[3], b1[3];
+                            tc::split3(k2[z].x, k2[z].y, b0[0], b0[1], b0[2]);
+                            tc::split3(k2[z].z, k2[z].w, b1[0], b1[1], b1[2]);
+                            mma_split3(big, small, q3[kk + z], b0, b1);
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[b][e] = (big[e] + small[e]) * p.scale_log2;
                 }
+            } else {
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                for (int h = 0; h < KN / 2; ++h) {
+                    float acc[2][2][4] = {};
+                    const int key = warp * G::kWarpKeys + h * 16 + (lane & 7) + (lane >> 4) * 8;
+                    const uint32_t kr = ks + tile.row(key);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sc[2 * h + b][e] = (acc[0][b][e] + acc[1][b][e]) * p.scale_log2;
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        uint32_t b[4];
+                        ldsm4(b, kr + tile.chunk(key, 2 * kk + ((lane >> 3) & 1)));
+                        mma16816<T>(acc[kk & 1][0], qf[kk], b[0], b[1]);
+                        mma16816<T>(acc[kk & 1][1], qf[kk], b[2], b[3]);
+                    }
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            sc[2 * h + b][e] = (acc[0][b][e] + acc[1][b][e]) * p.scale_log2;
+                }
             }
             if (!clean) {
                 // keys of the tile that a row sees: [lo, hi] and, up to hi, those below `sink`
@@ -785,9 +852,12 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             // weights adds nothing to the output's own rounding; the tensor pipe has room.
             // (float16's steps end at 2^-24, so its weights go up to 2^14 instead of 1: what is
             // lost of a small one is 2^-39 of the largest. l carries the same factor.)
-            base0 -= Elem<T>::kWeightBits;
-            base1 -= Elem<T>::kWeightBits;
-            uint8_t *ph = extra, *pl = extra + kRows * (KT + 8) * 2;
+            if constexpr (!kSplit) {
+                base0 -= Elem<T>::kWeightBits;
+                base1 -= Elem<T>::kWeightBits;
+            }
+            constexpr int kPart = kRows * (KT + 8) * 2;
+            uint8_t *ph = extra, *pl = extra + kPart;
             l0 *= corr0;
             l1 *= corr1;
 #pragma unroll
@@ -799,12 +869,23 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                 const int col = warp * G::kWarpKeys + b * 8 + 2 * (lane & 3);
                 const uint32_t oa = static_cast<uint32_t>(r0 * (KT + 8) + col) * 2u;
                 const uint32_t ob = oa + 8 * (KT + 8) * 2u;
-                const uint32_t xh = Elem<T>::pack(x0, x1), yh = Elem<T>::pack(y0, y1);
-                const float2 xf = Elem<T>::unpack(xh), yf = Elem<T>::unpack(yh);
-                *reinterpret_cast<uint32_t *>(ph + oa) = xh;
-                *reinterpret_cast<uint32_t *>(ph + ob) = yh;
-                *reinterpret_cast<uint32_t *>(pl + oa) = Elem<T>::pack(x0 - xf.x, x1 - xf.y);
-                *reinterpret_cast<uint32_t *>(pl + ob) = Elem<T>::pack(y0 - yf.x, y1 - yf.y);
+                if constexpr (kSplit) {
+                    uint32_t x3[3], y3[3];
+                    tc::split3(x0, x1, x3[0], x3[1], x3[2]);
+                    tc::split3(y0, y1, y3[0], y3[1], y3[2]);
+#pragma unroll
+                    for (int z = 0; z < 3; ++z) {
+                        *reinterpret_cast<uint32_t *>(ph + z * kPart + oa) = x3[z];
+                        *reinterpret_cast<uint32_t *>(ph + z * kPart + ob) = y3[z];
+                    }
+                } else {
+                    const uint32_t xh = Elem<T>::pack(x0, x1), yh = Elem<T>::pack(y0, y1);
+                    const float2 xf = Elem<T>::unpack(xh), yf = Elem<T>::unpack(yh);
+                    *reinterpret_cast<uint32_t *>(ph + oa) = xh;
+                    *reinterpret_cast<uint32_t *>(ph + ob) = yh;
+                    *reinterpret_cast<uint32_t *>(pl + oa) = Elem<T>::pack(x0 - xf.x, x1 - xf.y);
+                    *reinterpret_cast<uint32_t *>(pl + ob) = Elem<T>::pack(y0 - yf.x, y1 - yf.y);
+                }
             }
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -816,22 +897,48 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
             named_barrier_sync(2, kCompute);
             const uint32_t poff = static_cast<uint32_t>(
                 ((lane & 7) + ((lane >> 3) & 1) * 8) * (KT + 8) + (lane >> 4) * 8) * 2u;
+            if constexpr (kSplit) {
+                // the tile's sums apart, then added to O: the tensor cores' own additions round less well
+                float big[NT][4] = {}, small[NT][4] = {};
+#pragma unroll 1
+                for (int kk = g_lo; kk < g_hi; ++kk) {
+                    uint32_t a[3][4];
 #pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk) {
-                if (kk < g_lo || kk >= g_hi) continue;
-                uint32_t ah[4], al[4];
-                ldsm4(ah, smem_addr(ph) + poff + kk * 32);
-                ldsm4(al, smem_addr(pl) + poff + kk * 32);
-                const int vrow = kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
-                const uint32_t vr = vs + tile.row(vrow);
+                    for (int z = 0; z < 3; ++z) ldsm4(a[z], smem_addr(ph) + z * kPart + poff + kk * 32);
+                    const int i0 = kk * 16 + 2 * (lane & 3);  // keys i0, i0 + 1, i0 + 8, i0 + 9
+                    const uint8_t *vr = v_tile(s) + (lane >> 2 & 3) * 4;
 #pragma unroll
-                for (int j = 0; j < NT; j += 2) {
-                    uint32_t b[4];
-                    ldsm4_trans(b, vr + tile.chunk(vrow, warp * NT + j + (lane >> 4)));
-                    mma16816<T>(o16[j], ah, b[0], b[1]);
-                    mma16816<T>(o16[j + 1], ah, b[2], b[3]);
-                    mma16816<T>(o16[j], al, b[0], b[1]);
-                    mma16816<T>(o16[j + 1], al, b[2], b[3]);
+                    for (int j = 0; j < NT; ++j) {
+                        const int c = 2 * (warp * NT + j) + (lane >> 4);
+                        auto v = [&](int i) { return *reinterpret_cast<const float *>(vr + tile.row(i) + tile.chunk(i, c)); };
+                        uint32_t b0[3], b1[3];
+                        tc::split3(v(i0), v(i0 + 1), b0[0], b0[1], b0[2]);
+                        tc::split3(v(i0 + 8), v(i0 + 9), b1[0], b1[1], b1[2]);
+                        mma_split3(big[j], small[j], a, b0, b1);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o16[j][e] += big[j][e] + small[j][e];
+            } else {
+#pragma unroll
+                for (int kk = 0; kk < KT / 16; ++kk) {
+                    if (kk < g_lo || kk >= g_hi) continue;
+                    uint32_t ah[4], al[4];
+                    ldsm4(ah, smem_addr(ph) + poff + kk * 32);
+                    ldsm4(al, smem_addr(pl) + poff + kk * 32);
+                    const int vrow = kk * 16 + (lane & 7) + ((lane >> 3) & 1) * 8;
+                    const uint32_t vr = vs + tile.row(vrow);
+#pragma unroll
+                    for (int j = 0; j < NT; j += 2) {
+                        uint32_t b[4];
+                        ldsm4_trans(b, vr + tile.chunk(vrow, warp * NT + j + (lane >> 4)));
+                        mma16816<T>(o16[j], ah, b[0], b[1]);
+                        mma16816<T>(o16[j + 1], ah, b[2], b[3]);
+                        mma16816<T>(o16[j], al, b[0], b[1]);
+                        mma16816<T>(o16[j + 1], al, b[2], b[3]);
+                    }
                 }
             }
         } else {
@@ -975,7 +1082,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         if (!(flags & kLast)) continue;
 
         // ---------------------------------------------------------- the segment's end
-        if constexpr (G::kF32) {
+        if constexpr (!kFrag) {
             if (lane == 0) mbar_arrive(&q_empty[seg & 1]);
         }
         ++seg;
@@ -990,7 +1097,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                 l1 = 0.0f;
             }
         }
-        if constexpr (!G::kF32) {
+        if constexpr (kFrag) {
             const float a = group_sum<4>(l0), b = group_sum<4>(l1);
             if ((lane & 3) == 0) {
                 red[warp][lane >> 2] = a;
@@ -1022,7 +1129,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         const bool whole = sg.flags & kWhole;
         float *record = p.partials +
                         static_cast<size_t>(2 * blockIdx.x + ((sg.flags & kHead) ? 1 : 0)) * kRecord;
-        if constexpr (!G::kF32) {
+        if constexpr (kFrag) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int r = half ? row1 : row0, t = half ? tok1 : tok0;
@@ -1034,8 +1141,11 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                     const int col = (warp * NT + j) * 8 + 2 * (lane & 3);
                     const float x = o16[j][2 * half], y = o16[j][2 * half + 1];
                     if (whole) {
-                        *reinterpret_cast<uint32_t *>(out + row * D + col) =
-                            Elem<T>::pack(finish(x, l, inv), finish(y, l, inv));
+                        if constexpr (kSplit)
+                            *reinterpret_cast<float2 *>(out + row * D + col) = make_float2(finish(x, l, inv), finish(y, l, inv));
+                        else
+                            *reinterpret_cast<uint32_t *>(out + row * D + col) =
+                                Elem<T>::pack(finish(x, l, inv), finish(y, l, inv));
                     } else {
                         __stcg(reinterpret_cast<float2 *>(record + r * D + col), make_float2(x, y));
                     }

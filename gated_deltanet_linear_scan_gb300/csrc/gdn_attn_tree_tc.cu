@@ -922,14 +922,14 @@ __global__ void __launch_bounds__(128) attn_tree_join_kernel(const TreeAttnParam
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(FULL_MASK, l, o);
         float o[kCols] = {};
-#pragma unroll 4
+        // (all parts' loads on their way together; one that saw nothing may hold anything)
+#pragma unroll 8
         for (int c = c0; c <= join.c1; ++c) {
             const float f = weights[warp][c - c0];
-            if (f == 0.0f) continue;  // (that part saw nothing, and may hold anything)
             float x[kCols];
             load_vec<kCols>(x, record(c) + static_cast<size_t>(r) * D + lane * kCols);
 #pragma unroll
-            for (int e = 0; e < kCols; ++e) o[e] = fmaf(f, x[e], o[e]);
+            for (int e = 0; e < kCols; ++e) o[e] = f == 0.0f ? o[e] : fmaf(f, x[e], o[e]);
         }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         T *out = static_cast<T *>(p.out) +

@@ -459,17 +459,6 @@ __host__ __device__ inline uint32_t tmem_cols(const TcSizes &z) {
     return kColD + 2u * static_cast<uint32_t>(z.rows) <= 256u ? 256u : 512u;
 }
 
-// x = p1 + p2 + p3 in bf16, two values to a word.
-__device__ __forceinline__ void split3(float a, float b, uint32_t &p1, uint32_t &p2, uint32_t &p3) {
-    p1 = tc::pack_bf16x2(a, b);
-    a = __fsub_rn(a, __uint_as_float(p1 << 16));
-    b = __fsub_rn(b, __uint_as_float(p1 & 0xFFFF0000u));
-    p2 = tc::pack_bf16x2(a, b);
-    a = __fsub_rn(a, __uint_as_float(p2 << 16));
-    b = __fsub_rn(b, __uint_as_float(p2 & 0xFFFF0000u));
-    p3 = tc::pack_bf16x2(a, b);
-}
-
 // Images and weights. Grid: (k-head, sequence), 8 warps, or 16 where that leaves SMs idle. The nodes'
 // products, a warp a node; then, for a few v-heads at a time, A and B as lists along the paths, one
 // thread an entry, and T and W, all rows of one depth together.
@@ -532,7 +521,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) tree_prepare_kernel(const Tre
             if (i < N) store_vec<8>(rows + (r < z.pad ? i : N + i) * kLd + 8 * c, v[b]);
             uint32_t w[3][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) split3(v[b][2 * e], v[b][2 * e + 1], w[0][e], w[1][e], w[2][e]);
+            for (int e = 0; e < 4; ++e) tc::split3(v[b][2 * e], v[b][2 * e + 1], w[0][e], w[1][e], w[2][e]);
             uint8_t *to = images + tc::kmajor_offset16(r, 8 * c, 128, S / 8 * 128);
 #pragma unroll
             for (int y = 0; y < 3; ++y)
@@ -763,8 +752,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_state_tc_kernel(const __gr
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     const float4 x = *reinterpret_cast<const float4 *>(smem + col * 16384 + j * 128 + ((c ^ (j & 7)) << 4));
-                    split3(x.x, x.y, w1[2 * c], w2[2 * c], w3[2 * c]);
-                    split3(x.z, x.w, w1[2 * c + 1], w2[2 * c + 1], w3[2 * c + 1]);
+                    tc::split3(x.x, x.y, w1[2 * c], w2[2 * c], w3[2 * c]);
+                    tc::split3(x.z, x.w, w1[2 * c + 1], w2[2 * c + 1], w3[2 * c + 1]);
                 }
                 tc::tmem_st16(lanes + kColA + 16 * col, w1);
                 tc::tmem_st16(lanes + kColA + 64 + 16 * col, w2);

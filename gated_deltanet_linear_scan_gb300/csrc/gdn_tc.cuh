@@ -245,6 +245,17 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float even, float odd) {
     return r;
 }
 
+// x = p1 + p2 + p3 in bf16, two values to a word.
+__device__ __forceinline__ void split3(float a, float b, uint32_t &p1, uint32_t &p2, uint32_t &p3) {
+    p1 = pack_bf16x2(a, b);
+    a = __fsub_rn(a, __uint_as_float(p1 << 16));
+    b = __fsub_rn(b, __uint_as_float(p1 & 0xFFFF0000u));
+    p2 = pack_bf16x2(a, b);
+    a = __fsub_rn(a, __uint_as_float(p2 << 16));
+    b = __fsub_rn(b, __uint_as_float(p2 & 0xFFFF0000u));
+    p3 = pack_bf16x2(a, b);
+}
+
 // The split x = hi + lo of the 3xBF16 products, for a pair of values: hi = bf16(x)
 // and lo = bf16(x - hi), each pair packed as pack_bf16x2 packs it. hi is x rounded
 // to 8 significant bits, so x - hi (at most 2^-8 |x|) is exact in fp32, and hi + lo
