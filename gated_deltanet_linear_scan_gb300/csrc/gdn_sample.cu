@@ -6,19 +6,27 @@
 // what is kept in index order, exceeds u times the whole sum.
 //
 // Whether a sum falls short of a border decides the token, so the weights are held to 2^-43 of the
-// largest (e^{z} in two floats, then 64-bit integers): integer sums do not depend on their order,
+// sum (e^{z} in two floats, then 64-bit integers): integer sums do not depend on their order,
 // every pass over a row agrees with every other, and a wrong side of a border is as likely as a
 // uniform number within 10^-11 of it. (With weights of 24 bits, one row in some hundred of a
 // vocabulary of 100,000 would come out another token.)
 //
 // A cluster of 1 to 8 CTAs takes a row, a warp a stretch of it. The first pass finds the largest logit;
-// later ones read the row again from L1 and L2 (rows in flight fit there). Most tokens of a row are
-// so unlikely that one exponential in fp32 gives their weight to 2^-43 of the largest; the others
-// wait in a queue of the warp's until there are 32 of them. The border of top-k or top-p is found by
-// two histograms of counts or weights, read across the cluster: bins of 1/32 in the weight's logarithm
-// from the largest down, then 2048 parts of the bin that holds the border, whose smallest and largest
-// logit are nearly always one value. What that leaves open (a part with two values, a border 64 powers
-// of two below the largest) goes by the bits of the keys, 11, 11 and 10.
+// later ones read the row again from L2 (rows in flight fit there). Most tokens of a row are so unlikely
+// that one exponential in fp32 gives their weight as well as it has to be; the others wait in a queue of the
+// warp's until there are 32 of them. The border of top-k or top-p is found by two histograms of counts or
+// weights, read across the cluster: bins of 1/32 in the weight's logarithm from the largest down, as
+// far as they can be needed (a bound from the threads' largest logits, or from the sum of all weights), then
+// 2048 parts of the bin that holds the border, whose smallest and largest logit are nearly always one
+// value. What that leaves open (a part with two values, a border 64 powers of two below the largest) goes
+// by the bits of the keys, 11, 11 and 10. What the first histogram takes is listed in shared memory
+// where there is room, and the passes behind it read the list.
+//
+// Arithmetic on the logits bounds it, at 4 to 10 instructions of every lane a logit and pass. 1024 rows
+// of 100003 fp32 logits, 0.41 GB (61 us at the copy rate): the largest logit alone 100 us; temperature
+// 195, top-k of 50 219, top-p of 0.9 226, min-p 177, all 247 (without the lists 351, 449, 174, 592).
+// Flat rows cost more, as many tokens have weights that count: top-p of 0.98 at a temperature of 1.3 1.2
+// ms. One row of 128000 bf16 logits by top-p 27 us, nearly all of it barriers and latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -34,6 +42,8 @@ constexpr int kBins = 2048;
 constexpr int kPow = 256;            // entries of the table of powers
 constexpr int kMaxVocab = 1 << 20;   // weights of 2^43 stay below 2^63 in a sum
 constexpr int kAll = 0x7fffffff;
+constexpr int kQueue = 32 * 5;       // a warp's room for logits that wait for company
+constexpr int kListed = 416;        // of a warp's largest logits, kept in shared memory
 constexpr int kSMs = 152;
 
 typedef unsigned long long u64;
@@ -101,8 +111,10 @@ struct __align__(16) Shared {
     unsigned lo[2][kBins], hi[2][kBins];  // histograms, two in turn
     unsigned least[kBins], most[kBins];   // keys of a part's smallest and largest logit (as ~key, key)
     Part parts[kMaxCluster * kWarps], own[kWarps];
-    float queue[kWarps][64];
+    float queue[kWarps][kQueue];
+    float list[kWarps][kListed];
     float tops[kMaxCluster];
+    unsigned masses[kMaxCluster], warp_mass[kWarps];
     int firsts[kMaxCluster];
     u64 scan[kWarps];
     u64 before;      // what lies before the border's bin
@@ -121,12 +133,16 @@ __device__ __forceinline__ float value_of(unsigned key) {
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
-// Weights: 2^43 e^{(x - top) / T}. c_hi + c_lo is log2(e) / T; above `likely` the weight is more than
-// 2^-kLikely of the largest; k_hi + k_lo is kLikely - top (c_hi + c_lo).
-constexpr int kLikely = 20;
+// Weights: 2^{43 - shift} e^{(x - top) / T}, where 2^shift is no more than the sum of all over the largest
+// (the sum of the largest of all quarters of threads' logits is taken for it): what is below 2^-43 of the sum does
+// not count, and the flatter a row, the fewer of its tokens need a precise weight. c_hi + c_lo is
+// log2(e) / T; above `likely` the weight is more than 2^-bits of the largest, bits = kLikely - shift;
+// k_hi + k_lo is bits - top (c_hi + c_lo).
+constexpr int kUnits = 43, kLikely = 20;
 constexpr float kExpShort = 7.14e-8f;  // log2 of what the exponential falls short by, over its range (measured: 4.95e-8)
 struct Weigher {
     float top, c_hi, c_lo, k_hi, k_lo, likely;
+    int shift;
 };
 
 // The weight of a likely token: t = (x - top) log2(e) / T in two floats, 2^t from the table and a
@@ -159,7 +175,7 @@ __device__ __noinline__ u64 precise_weight(const Weigher w, float x) {
     const unsigned big = __float2uint_rz(s * 16777216.0f);
     const int small = __float2int_rn(r * 17592186044416.0f);
     const u64 sum = (static_cast<u64>(big) << 20) + static_cast<long long>(small);
-    return x == w.top ? 1ull << 43 : sum >> (1 - (n >> 8));
+    return x == w.top ? 1ull << (kUnits - w.shift) : sum >> (1 + w.shift - (n >> 8));
 }
 
 // The weight of an unlikely one, below 2^23 and so the last bits of 2^23 more than it. Its argument
@@ -168,7 +184,7 @@ __device__ __noinline__ u64 precise_weight(const Weigher w, float x) {
 constexpr unsigned kSmallBase = 0x4B000000u;  // 2^23
 __device__ __forceinline__ unsigned small_weight_bits(const Weigher &w, float x) {
     const float t = __fadd_rn(__fmaf_rn(x, w.c_hi, w.k_hi), __fmaf_rn(x, w.c_lo, w.k_lo));
-    return __float_as_uint(__fmaf_rn(fast_exp2(t), static_cast<float>(1 << (43 - kLikely)), 8388608.0f));
+    return __float_as_uint(__fmaf_rn(fast_exp2(t), static_cast<float>(1 << (kUnits - kLikely)), 8388608.0f));
 }
 __device__ __forceinline__ u64 weight_of(const Weigher &w, float x) {
     return x > w.likely ? precise_weight(w, x) : x > -INFINITY ? small_weight_bits(w, x) - kSmallBase : 0u;
@@ -235,9 +251,9 @@ __device__ __forceinline__ u64 times(float f, u64 x, bool up) {
 // Logits from .. to - 1 of a row, by a whole warp: f(x, index of the first), 16 bytes of them a lane
 // between the first and the last boundary of 16 and one a lane at the ends (-infinity where there is
 // none), the next loads ahead of this one's work.
-template <typename T, typename F>
+template <int kAhead = 2, typename T, typename F>
 __device__ __forceinline__ void each_logit(const T *logits, int from, int to, F f) {
-    constexpr int kVec = Vec<T>::kSize, kAhead = 2;
+    constexpr int kVec = Vec<T>::kSize;
     const int lane = threadIdx.x & 31;
     const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(logits + from) & 15u) / sizeof(T));
     const int s0 = min(to, from + (shift ? kVec - shift : 0)), n = (to - s0) / kVec, s1 = s0 + n * kVec;
@@ -283,24 +299,30 @@ __device__ __forceinline__ float top_of(const float (&x)[N]) {
 }
 
 // Those of a warp's values that are picked, 32 at a time: f(x) for one a lane (all lanes but in
-// `finish`).
+// `finish`), in no particular order.
 struct Queue {
-    float *at;  // 64 floats of the warp's own
+    float *at;  // kQueue floats of the warp's own
     int count;
-    template <typename F>
-    __device__ __forceinline__ void push(bool picked, float x, F f) {
-        const int lane = threadIdx.x & 31;
-        const unsigned mask = __ballot_sync(FULL_MASK, picked);
-        if (mask == 0) return;
-        if (picked) at[count + __popc(mask & ((1u << lane) - 1))] = x;
-        count += __popc(mask);
-        if (count < 32) return;
-        __syncwarp();
-        const float mine = at[lane], rest = at[lane + 32];
-        count -= 32;
-        __syncwarp();
-        if (lane < count) at[lane] = rest;
-        f(mine);
+    template <int N, typename P, typename F>
+    __device__ __forceinline__ void push(const float (&x)[N], P picked, F f) {
+        const unsigned below = (1u << (threadIdx.x & 31)) - 1;
+#pragma unroll
+        for (int e0 = 0; e0 < N; e0 += 4) {  // four values of a lane together
+            #pragma unroll
+            for (int e = e0; e < e0 + 4 && e < N; ++e) {
+                const bool mine = picked(x[e]);
+                const unsigned mask = __ballot_sync(FULL_MASK, mine);
+                if (mine) at[count + __popc(mask & below)] = x[e];
+                count += __popc(mask);
+            }
+            if (count < 32) continue;
+            __syncwarp();
+            do {
+                count -= 32;
+                f(at[count + (threadIdx.x & 31)]);
+            } while (count >= 32);
+            __syncwarp();
+        }
     }
     template <typename F>
     __device__ __forceinline__ void finish(F f) {
@@ -312,7 +334,109 @@ struct Queue {
     }
 };
 
+// The logits of a warp's stretch from some value on, where they have found room; more than kListed: not so.
+struct List {
+    float *at;
+    int count;
+    // `n` (of all lanes alike) values, one a lane
+    __device__ __forceinline__ void add(float x, int n) {
+        const int lane = threadIdx.x & 31;
+        if (count + n <= kListed && lane < n) at[count + lane] = x;
+        count = min(count + n, kListed + 1);
+    }
+    __device__ __forceinline__ bool whole() const { return count <= kListed; }
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const {
+        const int lane = threadIdx.x & 31;
+        for (int i = lane; i < count + lane; i += 32) {
+            const float x[1] = {i < count ? at[i] : -INFINITY};
+            f(x, 0);
+        }
+    }
+};
+
+// A histogram's bin: 64 bits in two words.
+__device__ __forceinline__ void add_weight(unsigned *lo, unsigned *hi, unsigned bin, u64 w) {
+    const unsigned l = static_cast<unsigned>(w), old = atomicAdd(&lo[bin], l);
+    const unsigned h = static_cast<unsigned>(w >> 32) + (old + l < old ? 1u : 0u);
+    if (h != 0) atomicAdd(&hi[bin], h);
+}
+
+// Histogram 0 by weight: bins from `split` on have weights below 2^24 only, whose lower 12 bits go to one
+// word and the rest to the other, which then needs no carry (2^20 of them fit).
+__device__ __forceinline__ unsigned split_bin(const Weigher &w) { return 32u * (kLikely - w.shift); }
+__device__ __forceinline__ void add_place(Shared &sh, const Weigher &w, unsigned bin, u64 weight) {
+    if (bin < split_bin(w)) {
+        add_weight(sh.lo[0], sh.hi[0], bin, weight);
+    } else {
+        atomicAdd(&sh.lo[0][bin], static_cast<unsigned>(weight) & 0xFFFu);
+        atomicAdd(&sh.hi[0][bin], static_cast<unsigned>(weight >> 12));
+    }
+}
+
+// A logit's bin of 1/32 in the logarithm of its weight, and its place in that (both roundings leave the
+// order of logits as it is).
+__device__ __forceinline__ float place_of(const Weigher &w, float x) {
+    return x == w.top ? 0.0f : fminf((w.top - x) * (w.c_hi * 32.0f), static_cast<float>(kBins));
+}
+
+// The weights of logits from .. to - 1, by a whole warp; the likely ones listed, and in histogram 0.
+template <typename T>
+__device__ __noinline__ u64 whole_part(const T *logits, int from, int to, const Weigher w, float *room, List &list) {
+    extern __shared__ __align__(16) uint8_t dyn[];
+    Shared &sh = *reinterpret_cast<Shared *>(dyn);
+    u64 sum = 0;
+    unsigned small = 0, since = 0;
+    Queue queue{room, 0};
+    List mine{list.at, 0};
+    auto weigh = [&](float x) {
+        const u64 weight = precise_weight(w, x);
+        sum += weight;
+        add_place(sh, w, static_cast<unsigned>(place_of(w, x)), weight);
+    };
+    auto add = [&](float x) {
+        weigh(x);
+        mine.add(x, 32);
+    };
+    each_logit(logits, from, to, [&](const auto &x, int) {
+        constexpr int N = static_cast<int>(sizeof(x) / sizeof(x[0]));
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const unsigned bits = small_weight_bits(w, x[e]) - kSmallBase;
+            small += x[e] > -INFINITY && !(x[e] > w.likely) ? bits : 0u;
+        }
+        since += N;
+        if (since >= 256) {
+            sum += small;
+            small = since = 0;
+        }
+        if (!__any_sync(FULL_MASK, top_of(x) > w.likely)) return;
+        queue.push(x, [&](float y) { return y > w.likely; }, add);
+    });
+    sum += small;
+    __syncwarp();
+    const int left = queue.count;
+    const float last = (threadIdx.x & 31) < left ? room[threadIdx.x & 31] : 0.0f;
+    queue.finish(weigh);
+    mine.add(last, left);
+    __syncwarp();
+    list.count = mine.count;
+    return warp_sum64(sum);
+}
+
 // Of logits from .. to - 1, by a whole warp: the weights above the cut, and how many equal it.
+__device__ __noinline__ Part part_of_list(const List list, float cut, const Weigher w) {
+    Part mine{0, 0, 0};
+    list.each([&](const auto &x, int) {
+        if (x[0] > cut) mine.sum += weight_of(w, x[0]);
+        mine.equal += x[0] == cut;
+    });
+    __syncwarp();
+    mine.sum = warp_sum64(mine.sum);
+    mine.equal = __reduce_add_sync(FULL_MASK, mine.equal);
+    return mine;
+}
+
 template <typename T>
 __device__ __noinline__ Part part_of(const T *logits, int from, int to, float cut, const Weigher w, float *room) {
     Part mine{0, 0, 0};
@@ -323,10 +447,8 @@ __device__ __noinline__ Part part_of(const T *logits, int from, int to, float cu
         each_logit(logits, from, to, [&](const auto &x, int) {
             if (!__any_sync(FULL_MASK, top_of(x) >= cut)) return;
 #pragma unroll
-            for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(x[0])); ++e) {
-                mine.equal += x[e] == cut;
-                queue.push(x[e] > cut, x[e], add);
-            }
+            for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(x[0])); ++e) mine.equal += x[e] == cut;
+            queue.push(x, [&](float y) { return y > cut; }, add);
         });
     } else {
         // (small weights are below 2^23: 2^9 of them add up to less than 2^32)
@@ -345,8 +467,7 @@ __device__ __noinline__ Part part_of(const T *logits, int from, int to, float cu
                 small = since = 0;
             }
             if (!__any_sync(FULL_MASK, top_of(x) > w.likely)) return;
-#pragma unroll
-            for (int e = 0; e < N; ++e) queue.push(x[e] > w.likely, x[e], add);
+            queue.push(x, [&](float y) { return y > w.likely; }, add);
         });
         mine.sum += small;
     }
@@ -358,10 +479,10 @@ __device__ __noinline__ Part part_of(const T *logits, int from, int to, float cu
 
 // The bin in which the running sum over the cluster's histograms (low words and, unless NULL, high
 // ones) reaches `target`, from bin 0 up or from the last down; what lies before it goes to sh.before;
-// -1 if none does. Bins from `limit` up are known to be empty. By the whole CTA. Clears histogram `clears` (and with the second the parts' keys),
+// -1 if none does. Bins from `limit` up are not needed; those from `split` up have 12 bits in their low word. By the whole CTA. Clears histogram `clears` (and with the second the parts' keys),
 // which everybody has read before the barrier ahead of this call.
 __device__ __noinline__ int find_bin(unsigned *low, unsigned *high, int clears, u64 target, bool down, int cluster,
-                                     int limit = kBins) {
+                                     int limit = kBins, int split = kBins) {
     extern __shared__ __align__(16) uint8_t dyn[];
     Shared &sh = *reinterpret_cast<Shared *>(dyn);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -369,6 +490,7 @@ __device__ __noinline__ int find_bin(unsigned *low, unsigned *high, int clears, 
     u64 own[4] = {0, 0, 0, 0};
     for (int word = 0; word < (high ? 2 : 1); ++word) {
         unsigned *const hist = word ? high : low;
+        const int up = word == 0 ? 0 : at < split ? 32 : 12;
         for (int r0 = 0; r0 < cluster; r0 += 4) {  // four CTAs' at a time
             uint4 x[4];
 #pragma unroll
@@ -376,10 +498,10 @@ __device__ __noinline__ int find_bin(unsigned *low, unsigned *high, int clears, 
                 x[y] = r0 + y < cluster && at < limit ? *reinterpret_cast<const uint4 *>(in_cta(hist, r0 + y) + at) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-                own[0] += static_cast<u64>(x[y].x) << (32 * word);
-                own[1] += static_cast<u64>(x[y].y) << (32 * word);
-                own[2] += static_cast<u64>(x[y].z) << (32 * word);
-                own[3] += static_cast<u64>(x[y].w) << (32 * word);
+                own[0] += static_cast<u64>(x[y].x) << up;
+                own[1] += static_cast<u64>(x[y].y) << up;
+                own[2] += static_cast<u64>(x[y].z) << up;
+                own[3] += static_cast<u64>(x[y].w) << up;
             }
         }
     }
@@ -452,9 +574,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
 
     // ---- the largest logit
-    float top = -INFINITY;
-    each_logit(logits, e0, e1, [&](const auto &x, int) { top = fmaxf(top, top_of(x)); });
-    const float own_top = top;
+    float own_tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // of four parts of the thread's logits
+    each_logit<4>(logits, e0, e1, [&](const auto &x, int) {
+#pragma unroll
+        for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(x[0])); ++e) own_tops[e & 3] = fmaxf(own_tops[e & 3], x[e]);
+    });
+    float top = top_of(own_tops);
     __syncwarp();
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
@@ -464,10 +589,31 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         sh.log_min = static_cast<double>(temperature) * log(static_cast<double>(min_p));
     __syncthreads();
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh.warp_top[w]);
+    // log2(e) / T: the quotient, and the remainder's
+    constexpr float kLog2EHi = 1.44269502162933349609f, kLog2ELo = 1.92596298909e-8f;
+    const float c = kLog2EHi / temperature, c_hi = fminf(c, 3.0e38f);
+    unsigned mass = 0;  // of the threads' largest logits, the largest 2^16
+    auto mass_of = [&](float x, float units) { return __float2uint_rn(units * fast_exp2(x == top ? 0.0f : (x - top) * c_hi)); };
+    if (!greedy) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mass += own_tops[e] == -INFINITY ? 0u : mass_of(own_tops[e], 65536.0f);
+        __syncwarp();
+        mass = __reduce_add_sync(FULL_MASK, mass);
+        if (lane == 0) sh.warp_mass[warp] = mass;
+        __syncthreads();
+        mass = 0;
+        for (int w = 0; w < kWarps; ++w) mass += sh.warp_mass[w];
+    }
     if (cluster > 1) {
-        if (tid < cluster) *in_cta(&sh.tops[rank], tid) = top;
+        if (tid < cluster) {
+            *in_cta(&sh.tops[rank], tid) = top;
+            *in_cta(&sh.masses[rank], tid) = mass;
+        }
         cluster_sync();
         for (int r = 0; r < cluster; ++r) top = fmaxf(top, sh.tops[r]);
+        mass = 0;
+        for (int r = 0; r < cluster && !greedy; ++r)
+            if (sh.tops[r] > -INFINITY) mass += mass_of(sh.tops[r], static_cast<float>(sh.masses[r]));
     }
     if (greedy || top == -INFINITY) {
         // the first index that has it: of the warps that have seen it
@@ -497,29 +643,29 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     Weigher weigher;
     weigher.top = top;
     {
-        // log2(e) / T: the quotient, and the remainder's
-        constexpr float kLog2EHi = 1.44269502162933349609f, kLog2ELo = 1.92596298909e-8f;
-        const float c = kLog2EHi / temperature;
-        weigher.c_hi = fminf(c, 3.0e38f);
+        weigher.shift = 31 - __clz(max(mass, 65536u) >> 16);
+        const float bits = static_cast<float>(kLikely - weigher.shift);
+        weigher.c_hi = c_hi;
         weigher.c_lo = c < 3.0e38f ? __fadd_rn(__fmaf_rn(-c, temperature, kLog2EHi), kLog2ELo) / temperature : 0.0f;
         // below the top itself, which is likely even where the difference rounds away
-        weigher.likely = fminf(top - static_cast<float>(kLikely) / weigher.c_hi, value_of(key_of(top) - (top == 0.0f ? 2 : 1)));
-        // kLikely - top c, the product in two floats
+        weigher.likely = fminf(top - bits / weigher.c_hi, value_of(key_of(top) - (top == 0.0f ? 2 : 1)));
+        // bits - top c, the product in two floats
         const float prod = __fmul_rn(top, weigher.c_hi), rest = __fmaf_rn(top, weigher.c_lo, __fmaf_rn(top, weigher.c_hi, -prod));
-        const float k = __fsub_rn(static_cast<float>(kLikely), prod), back = __fsub_rn(k, static_cast<float>(kLikely));
-        const float err = __fsub_rn(__fsub_rn(static_cast<float>(kLikely), __fsub_rn(k, back)), __fadd_rn(prod, back));
+        const float k = __fsub_rn(bits, prod), back = __fsub_rn(k, bits);
+        const float err = __fsub_rn(__fsub_rn(bits, __fsub_rn(k, back)), __fadd_rn(prod, back));
         weigher.k_hi = k;
         weigher.k_lo = __fadd_rn(__fsub_rn(err, rest), kExpShort);
     }
     auto weight = [&](float x) { return weight_of(weigher, x); };
     Queue queue{sh.queue[warp], 0};
+    List list{sh.list[warp], kListed + 1};
 
     // ---- what is kept: x > cut, and the first `ties` of those equal to it
     float cut = -INFINITY;
     int ties = 0;
 
     auto gather_parts = [&] {
-        const Part mine = part_of(logits, e0, e1, cut, weigher, queue.at);
+        const Part mine = list.whole() ? part_of_list(list, cut, weigher) : part_of(logits, e0, e1, cut, weigher, queue.at);
         if (lane < cluster) *in_cta(&sh.parts[rank * kWarps + warp], lane) = mine;
         sync();
     };
@@ -536,23 +682,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         return sum + static_cast<u64>(min(equal, ties)) * w_cut;
     };
 
-    // ---- histograms
-    auto add = [&](int turn, unsigned bin, u64 w) {
-        const unsigned l = static_cast<unsigned>(w), old = atomicAdd(&sh.lo[turn][bin], l);
-        const unsigned h = static_cast<unsigned>(w >> 32) + (old + l < old ? 1u : 0u);
-        if (h != 0) atomicAdd(&sh.hi[turn][bin], h);
+    // the logits that are still in question, or more
+    auto each_left = [&](auto f) {
+        if (list.whole()) list.each(f);
+        else each_logit(logits, e0, e1, f);
     };
+    auto add = [&](int turn, unsigned bin, u64 w) { add_weight(sh.lo[turn], sh.hi[turn], bin, w); };
+
+    // ---- histograms
     // The cut at which `target` (a count, or a sum of weights) is reached from the top, among what is
     // kept so far: the new cut and its ties. (A count that is not reached: all are kept.) No weight
-    // before `least_t` (its logarithm) is needed to reach it.
-    auto descend = [&](bool by_weight, u64 target, float least_t) {
+    // before `least_t` (its logarithm) is needed to reach it. counted: histogram 0 has the likely ones already.
+    auto descend = [&](bool by_weight, u64 target, float least_t, bool counted) {
         const float old_cut = cut;
         // those equal to the cut so far, of which only `ties` are kept: one thread adds them
         const bool old = by_weight && ties > 0 && rank == 0 && tid == 0;
         const u64 w_old = old ? weight(old_cut) * static_cast<u64>(ties) : 0;
-        const float scale = weigher.c_hi * 32.0f;
-        // bin and place in it (both roundings leave the order of logits as it is)
-        auto place = [&](float x) { return x == top ? 0.0f : fminf((top - x) * scale, static_cast<float>(kBins)); };
+        auto place = [&](float x) { return place_of(weigher, x); };
         auto settle = [&](u64 rest) {
             if (by_weight) {
                 const u64 w = weight(cut);
@@ -563,31 +709,59 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         };
         // what lies below this bin is not needed
         float end = fminf(ceilf(-least_t * 32.0f), static_cast<float>(kBins));
-        if (!by_weight && target <= static_cast<u64>(cluster * kThreads)) {
-            // as many logits as the threads have, their own largest, reach it in a bin: all bins up to
+        if (!by_weight && target <= static_cast<u64>(4 * cluster * kThreads)) {
+            // the largest of the threads' four parts, a logit each, reach it in a bin: all bins up to
             // that one hold enough
-            const float f = place(own_top);
-            if (f < static_cast<float>(kBins)) atomicAdd(&sh.least[static_cast<unsigned>(f)], 1u);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float f = place(own_tops[e]);
+                if (f < static_cast<float>(kBins)) atomicAdd(&sh.least[static_cast<unsigned>(f)], 1u);
+            }
             sync();
             const int bin = find_bin(sh.least, nullptr, 0, target, false, cluster);
             if (bin >= 0) end = static_cast<float>(bin + 1);
         }
-        auto note = [&](float x) {
-            const unsigned bin = static_cast<unsigned>(place(x));
-            if (by_weight) add(0, bin, weight(x));
-            else atomicAdd(&sh.lo[0][bin], 1u);
-        };
-        each_logit(logits, e0, e1, [&](const auto &x, int) {
-            const float largest = top_of(x);
-            if (!__any_sync(FULL_MASK, largest > old_cut && place(largest) < end)) return;
+        if (counted && end > static_cast<float>(split_bin(weigher) - 1)) {
+            // some that count are not likely
+            list.count = kListed + 1;
+            each_logit(logits, e0, e1, [&](const auto &x, int) {
 #pragma unroll
-            for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(x[0])); ++e)
-                queue.push(x[e] > old_cut && place(x[e]) < end, x[e], note);
-        });
-        queue.finish(note);
-        if (old && place(old_cut) < end) add(0, static_cast<unsigned>(place(old_cut)), w_old);
+                for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(x[0])); ++e) {
+                    const float f = place(x[e]);
+                    if (!(x[e] > weigher.likely) && f < end)
+                        add_place(sh, weigher, static_cast<unsigned>(f), small_weight_bits(weigher, x[e]) - kSmallBase);
+                }
+            });
+        }
+        if (!counted) {
+            auto note = [&](float x) {
+                const unsigned bin = static_cast<unsigned>(place(x));
+                if (by_weight) add_place(sh, weigher, bin, weight(x));
+                else atomicAdd(&sh.lo[0][bin], 1u);
+            };
+            const bool lists = !list.whole() && old_cut == -INFINITY;  // (not without those that equal the cut)
+            List kept{list.at, lists ? 0 : kListed + 1};
+            auto note_all = [&](float x) {
+                note(x);
+                kept.add(x, 32);
+            };
+            each_left([&](const auto &x, int) {
+                const float largest = top_of(x);
+                if (!__any_sync(FULL_MASK, largest > old_cut && place(largest) < end)) return;
+                queue.push(x, [&](float y) { return y > old_cut && place(y) < end; }, note_all);
+            });
+            __syncwarp();
+            const int left = queue.count;
+            const float last = lane < left ? queue.at[lane] : 0.0f;
+            queue.finish(note);
+            kept.add(last, left);
+            __syncwarp();
+            if (lists) list.count = kept.count;
+        }
+        if (old && place(old_cut) < end) add_place(sh, weigher, static_cast<unsigned>(place(old_cut)), w_old);
         sync();
-        const int at = find_bin(sh.lo[0], by_weight ? sh.hi[0] : nullptr, 1, target, false, cluster, static_cast<int>(end));
+        const int at = find_bin(sh.lo[0], by_weight ? sh.hi[0] : nullptr, 1, target, false, cluster, static_cast<int>(end),
+                                static_cast<int>(split_bin(weigher)));
         if (at >= 0) {
             const u64 rest = target - sh.before;
             const float bin = static_cast<float>(at);
@@ -603,12 +777,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 return f >= bin && f < bin + 1.0f;
             };
             auto note_it = [&](float x) { note_part(x, by_weight ? weight(x) : 0ull); };
-            each_logit(logits, e0, e1, [&](const auto &x, int) {
+            each_left([&](const auto &x, int) {
                 const float largest = top_of(x);
                 if (!__any_sync(FULL_MASK, largest > old_cut && place(largest) < bin + 1.0f)) return;
-#pragma unroll
-                for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(x[0])); ++e)
-                    queue.push(x[e] > old_cut && inside(x[e]), x[e], note_it);
+                queue.push(x, [&](float y) { return y > old_cut && inside(y); }, note_it);
             });
             queue.finish(note_it);
             if (old && inside(old_cut)) note_part(old_cut, w_old);
@@ -626,7 +798,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 return;
             }
         }
-        // by the keys' bits
+        // by the keys' bits (the border may lie below what is listed)
+        list.count = kListed + 1;
         auto clear = [&] {
             sync();
             for (int x = tid; x < kBins; x += kThreads) sh.lo[0][x] = sh.hi[0][x] = 0;
@@ -645,9 +818,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
                 else atomicAdd(&sh.lo[turn][bin_of(key_of(x))], 1u);
             };
             each_logit(logits, e0, e1, [&](const auto &x, int) {
-#pragma unroll
-                for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(x[0])); ++e)
-                    queue.push(x[e] > old_cut && inside(key_of(x[e])), x[e], note_key);
+                queue.push(x, [&](float y) { return y > old_cut && inside(key_of(y)); }, note_key);
             });
             queue.finish(note_key);
             if (old && inside(key_of(old_cut))) add(turn, bin_of(key_of(old_cut)), w_old);
@@ -671,15 +842,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         u64 target = top_k;
         float least_t = -INFINITY;
         if (step == 1) {
-            gather_parts();
+            if (by_count) {
+                gather_parts();
+            } else {
+                const Part mine{whole_part(logits, e0, e1, weigher, queue.at, list), 0, 0};
+                if (lane < cluster) *in_cta(&sh.parts[rank * kWarps + warp], lane) = mine;
+                sync();
+            }
             const u64 total = total_of(ties > 0 ? weight(cut) : 0);
             const u64 want = top_p > 0.0f ? times(top_p, total, true) : 0;
             // Where a weight times the vocabulary falls short of what may be left out, the border is behind
             // (0.02: half a bin, and fp32's errors).
-            least_t = log2f(static_cast<float>(total - want) * 0x1p-43f / static_cast<float>(p.vocab)) - 0.02f;
+            least_t = log2f(static_cast<float>(total - want) * 0x1p-43f / static_cast<float>(p.vocab)) + static_cast<float>(weigher.shift) - 0.02f;
             target = want > 0 ? want : 1;
         }
-        descend(step == 1, target, least_t);  // (its barriers come before the parts are written again)
+        descend(step == 1, target, least_t, step == 1 && !by_count);  // (its barriers come before the parts are written again)
     }
     if (min_p > 0.0f) {
         // w >= min_p: x >= top + T ln(min_p)
