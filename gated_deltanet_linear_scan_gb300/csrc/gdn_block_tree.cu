@@ -927,106 +927,240 @@ struct CommitParams {
     const float *qkv;
     float *conv_state, *state;
     const int32_t *parents, *accepted, *slots;
-    int n_nodes, n_k_heads, n_v_heads, conv_dim, taps, pool;
+    int n_seqs, n_nodes, n_k_heads, n_v_heads, conv_dim, taps, pool;
     int32_t *err_count;
     const float *k, *g, *u;
+    unsigned *watchdog;
 };
 
-// S <- e^{G_l} S0 + sum_{s on the path to l} e^{G_l - G_s} k_s u_s^T. Grid: (share, sequence); the
-// first `state_shares` shares are blocks of 64 state rows, 8 to a warp, held in registers while the
-// path's k and u pass through shared memory; the rest roll the conv history.
+// S <- e^{G_l} S0 + sum_{s on the path to l} e^{G_l - G_s} k_s u_s^T: the state in and out once bounds it.
+// Work is dealt out in blocks of 16 KB of state rows, a contiguous range to each of the first
+// `state_ctas` CTAs; a block's rows are fetched by a bulk copy, and its path's k, u and g into
+// registers, while the block before is worked on. 64 sequences, 32 heads of 128: 60 us, 0.71 of the copy rate (a CTA per 64
+// rows, each with its lookups, path and loads behind one another: 65). The other CTAs roll the conv history, a share of a sequence's channels each.
 constexpr int kCommitThreads = 256;
-constexpr int kCommitRows = 64;
 constexpr int kCommitNodes = 16;
 constexpr int kCommitChannels = kCommitThreads * 4;
+constexpr int kCommitCtas = 4;  // an SM (three, with room for those of the conv history: 65 us)
 
 template <int E>
-__global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const CommitParams p, int state_shares) {
-    constexpr int S = 32 * E, R = 8;
-    constexpr int kRows = S < kCommitRows ? S : kCommitRows;  // rows of a share
+struct CommitSmem {
+    static constexpr int S = 32 * E;
+    static constexpr int kRows = S == 64 ? 64 : 32;  // of a block
+    static constexpr int kBlock = kRows * S;
+    static constexpr int kBytes = (2 * kBlock + kCommitNodes * (S + 2 * kRows)) * 4;  // rows, k, u of two blocks
+};
+
+template <int E>
+__global__ void __launch_bounds__(kCommitThreads, E == 8 ? 2 : 4) tree_commit_kernel(const CommitParams p, int state_ctas) {
+    using L = CommitSmem<E>;
+    constexpr int S = L::S, kRows = L::kRows, R = kRows / 8;  // R rows a warp
     constexpr int kPerHead = S / kRows;
+    constexpr int kLoadsK = (kCommitNodes * S / 4 + kCommitThreads - 1) / kCommitThreads;
+    constexpr int kLoadsU = (kCommitNodes * kRows / 4 + kCommitThreads - 1) / kCommitThreads;
+    extern __shared__ __align__(128) float dyn_floats[];
+    float *const ks = dyn_floats + 2 * L::kBlock, *const us_of = ks + kCommitNodes * S;
+    __shared__ __align__(8) uint64_t full[2];
     __shared__ unsigned long long path_of[kMaxNodes];
     __shared__ int up[kMaxNodes], walk[kMaxNodes];
     __shared__ float g_of[kMaxNodes], weight[kMaxNodes + 1];
-    __shared__ __align__(16) float ks[kCommitNodes][S], us[kCommitNodes][kRows];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int n = blockIdx.y, N = p.n_nodes, Hk = p.n_k_heads, H = p.n_v_heads;
-    const int slot = p.slots ? p.slots[n] : n, share = blockIdx.x;
-    const int m = p.accepted[n];
-    const bool range = slot >= 0 && slot < p.pool && m >= 0 && m <= N;
-    if (range && m == 0) return;  // nothing accepted: the state stays
-    const size_t row0 = static_cast<size_t>(n) * N;
-    if (tid < 32 && range) {
-        unsigned long long paths[2];
-        tree_paths(p.parents + row0, N, paths, path_of, up);
-    }
-    __syncthreads();
-    const unsigned long long path = range ? path_of[m - 1] : 0;
-    if (path == 0) {  // out of range, or a node that is not there
-        if (share == 0 && tid == 0 && p.err_count) atomicAdd(p.err_count, 1);
-        return;
-    }
-    const int len = __popcll(path);
-    if (tid < kMaxNodes && ((path >> tid) & 1ull)) walk[__popcll(path & ((1ull << tid) - 1))] = tid;
-    if (share >= state_shares) {
+    const int N = p.n_nodes, Hk = p.n_k_heads, H = p.n_v_heads;
+    // The path to the accepted node of sequence n as `walk`, by the whole CTA; its length, 0 if nothing is
+    // accepted or the node is not there.
+    auto walk_of = [&](int n, bool counts) {
+        const int slot = p.slots ? p.slots[n] : n, m = p.accepted[n];
+        const bool range = slot >= 0 && slot < p.pool && m >= 0 && m <= N;
+        if (range && m == 0) return 0;
+        __syncthreads();  // (of the sequence before)
+        if (warp == 0 && range) {
+            unsigned long long paths[2];
+            tree_paths(p.parents + static_cast<size_t>(n) * N, N, paths, path_of, up);
+        }
         __syncthreads();
-        for (int c = (share - state_shares) * kCommitChannels + tid;
-             c < min(p.conv_dim, (share - state_shares + 1) * kCommitChannels); c += kCommitThreads) {
+        const unsigned long long path = range ? path_of[m - 1] : 0;
+        if (path == 0 && counts && tid == 0 && p.err_count) atomicAdd(p.err_count, 1);
+        if (tid < kMaxNodes && ((path >> tid) & 1ull)) walk[__popcll(path & ((1ull << tid) - 1))] = tid;
+        __syncthreads();
+        return __popcll(path);
+    };
+    if (static_cast<int>(blockIdx.x) >= state_ctas) {
+        // ---- the conv history
+        const int shares = (p.conv_dim + kCommitChannels - 1) / kCommitChannels;
+        const int n = (blockIdx.x - state_ctas) / shares, share = (blockIdx.x - state_ctas) % shares;
+        const int len = walk_of(n, share == 0);
+        if (len == 0) return;
+        const int slot = p.slots ? p.slots[n] : n;
+        for (int c = share * kCommitChannels + tid; c < min(p.conv_dim, (share + 1) * kCommitChannels); c += kCommitThreads) {
             float *hs = p.conv_state + (static_cast<size_t>(slot) * p.conv_dim + c) * p.taps;
             // entry t is the path's input len - taps + t, or the old entry len + t before those:
             // entries move down only
             for (int t = 0; t < p.taps; ++t) {
                 const int at = len - p.taps + t;
-                hs[t] = at >= 0 ? p.qkv[(row0 + walk[at]) * p.conv_dim + c] : hs[len + t];
+                hs[t] = at >= 0 ? p.qkv[(static_cast<size_t>(n) * N + walk[at]) * p.conv_dim + c] : hs[len + t];
             }
         }
         return;
     }
-    const int vh = share / kPerHead, kh = vh % Hk, j0 = (share % kPerHead) * kRows;
-    float *rows = p.state + ((static_cast<size_t>(slot) * H + vh) * S + j0 + warp * R) * S + E * lane;
-    const bool busy = warp * R < kRows;
-    float x[R][E];
-    if (busy) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) load_vec<E>(x[r], rows + r * S);
-    }
-    if (tid < N) g_of[tid] = p.g[(row0 + tid) * H + vh];
-    __syncthreads();
-    // weight[i]: the decay behind node walk[i]; weight[len]: of the whole path
-    if (tid <= len) {
-        float sum = 0.0f;
-        for (int i = len - 1; i > (tid == len ? -1 : tid); --i) sum += g_of[walk[i]];
-        weight[tid] = expf(sum);
-    }
-    __syncthreads();
-    const float all = weight[len];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[r][e] = busy ? x[r][e] * all : 0.0f;
-    for (int a = 0; a < len; a += kCommitNodes) {
-        const int count = min(kCommitNodes, len - a);
-        for (int y = tid; y < count * S; y += kCommitThreads)
-            ks[y / S][y % S] = p.k[((row0 + walk[a + y / S]) * Hk + kh) * S + y % S];
-        for (int y = tid; y < count * kRows; y += kCommitThreads)
-            us[y / kRows][y % kRows] = weight[a + y / kRows] * p.u[((row0 + walk[a + y / kRows]) * H + vh) * S + j0 + y % kRows];
-        __syncthreads();
-        if (busy) {
-            for (int y = 0; y < count; ++y) {
-                float kc[E], uc[R];
-                load_vec<E>(kc, &ks[y][E * lane]);
-                load_vec<R>(uc, &us[y][warp * R]);
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int e = 0; e < E; ++e) x[r][e] = fmaf(kc[e], uc[r], x[r][e]);
+    // ---- the states
+    const int blocks = H * kPerHead;  // of a sequence
+    const long long all = static_cast<long long>(p.n_seqs) * blocks;
+    const long long first = all * blockIdx.x / state_ctas, last = all * (blockIdx.x + 1) / state_ctas;
+    // a sequence's place, and block of it; sequences without a state to change (as far as that shows
+    // without their paths) are passed over
+    struct Place {
+        int n, r, left;  // left: blocks of the range from here on
+        float *rows;
+    };
+    auto settle = [&](Place &at) {
+        while (at.left > 0) {
+            if (at.r == blocks) {
+                at.r = 0;
+                ++at.n;
             }
+            const int slot = p.slots ? p.slots[at.n] : at.n, m = p.accepted[at.n];
+            if (slot >= 0 && slot < p.pool && m >= 1 && m <= N) {
+                at.rows = p.state + (static_cast<size_t>(slot) * blocks + at.r) * L::kBlock;
+                return;
+            }
+            at.left -= blocks - at.r;
+            at.r = blocks;
         }
-        __syncthreads();
+    };
+    auto behind = [&](Place at) {
+        ++at.r;
+        --at.left;
+        if (at.left > 0 && at.r < blocks) at.rows += L::kBlock;
+        else settle(at);
+        return at;
+    };
+    Place b{static_cast<int>(first / blocks), static_cast<int>(first % blocks), static_cast<int>(last - first), nullptr};
+    settle(b);
+    if (b.left <= 0) return;
+    if (tid == 0) {
+        mbar_init(&full[0], 1);
+        mbar_init(&full[1], 1);
+        fence_mbar_init();
     }
-    if (busy) {
+    auto fetch = [&](const Place &block, int turn) {
+        mbar_arrive_expect_tx(&full[turn], L::kBlock * 4);
+        bulk_g2s(dyn_floats + turn * L::kBlock, block.rows, L::kBlock * 4, &full[turn]);
+    };
+    if (tid == 0) fetch(b, 0);
+    int n = -1, len = 0, head = -1;  // head: whose k, weights and decay lie in shared memory
+    float g_next = 0.0f;
+    float4 k_next[kLoadsK], u_next[kLoadsU];
+    // the first nodes' u of a block of this sequence and, of another head, k and g
+    auto prefetch = [&](const Place &block) {
+        const size_t row0 = static_cast<size_t>(block.n) * N;
+        const int vh = block.r / kPerHead, j0 = block.r % kPerHead * kRows;
+        const int count = min(len, kCommitNodes);
 #pragma unroll
-        for (int r = 0; r < R; ++r) store_vec<E>(rows + r * S, x[r]);
+        for (int y = 0; y < kLoadsU; ++y) {
+            const int x = tid + y * kCommitThreads;
+            if (x < count * (kRows / 4))
+                u_next[y] = *reinterpret_cast<const float4 *>(p.u + ((row0 + walk[x / (kRows / 4)]) * H + vh) * S + j0 + 4 * (x % (kRows / 4)));
+        }
+        if (vh == head) return;
+        if (tid < N) g_next = p.g[(row0 + tid) * H + vh];
+#pragma unroll
+        for (int y = 0; y < kLoadsK; ++y) {
+            const int x = tid + y * kCommitThreads;
+            if (x < count * (S / 4))
+                k_next[y] = *reinterpret_cast<const float4 *>(p.k + ((row0 + walk[x / (S / 4)]) * Hk + vh % Hk) * S + 4 * (x % (S / 4)));
+        }
+    };
+    bool ok = true;
+    uint32_t phase = 0;  // bit t: of full[t]
+    for (int turn = 0; b.left > 0; turn ^= 1) {
+        if (b.n != n) {
+            n = b.n;
+            head = -1;
+            len = walk_of(n, false);  // (counted with the conv history)
+            if (len > 0) prefetch(b);
+        }
+        const Place after = behind(b);
+        float *const us = us_of + turn * kCommitNodes * kRows;
+        if (len > 0) {
+#pragma unroll
+            for (int y = 0; y < kLoadsU; ++y) {
+                const int x = tid + y * kCommitThreads;
+                if (x < min(len, kCommitNodes) * (kRows / 4)) *reinterpret_cast<float4 *>(us + 4 * x) = u_next[y];
+            }
+            if (b.r / kPerHead != head) {
+                head = len <= kCommitNodes ? b.r / kPerHead : -1;  // (a longer path's k pass through)
+                __syncthreads();  // the head before is done with
+                if (tid < N) g_of[tid] = g_next;
+#pragma unroll
+                for (int y = 0; y < kLoadsK; ++y) {
+                    const int x = tid + y * kCommitThreads;
+                    if (x < min(len, kCommitNodes) * (S / 4)) *reinterpret_cast<float4 *>(ks + 4 * x) = k_next[y];
+                }
+                __syncthreads();
+                // weight[i]: the decay behind node walk[i]; weight[len]: of the whole path
+                if (tid <= len) {
+                    float sum = 0.0f;
+                    for (int i = len - 1; i > (tid == len ? -1 : tid); --i) sum += g_of[walk[i]];
+                    weight[tid] = expf(sum);
+                }
+            }
+            if (after.left > 0 && after.n == n) prefetch(after);
+        }
+        ok = mbar_wait(&full[turn], (phase >> turn) & 1u);
+        phase ^= 1u << turn;
+        ok = __syncthreads_and(ok);
+        if (!ok) break;  // (this block keeps its state)
+        if (tid == 0 && after.left > 0) fetch(after, turn ^ 1);  // (its place has been read by all)
+        if (len > 0) {
+            const float *mine = dyn_floats + turn * L::kBlock + warp * R * S + E * lane;
+            const float decay = weight[len];
+            float x[R][E];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                load_vec<E>(x[r], mine + r * S);
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[r][e] *= decay;
+            }
+            const size_t row0 = static_cast<size_t>(n) * N;
+            const int vh = b.r / kPerHead, j0 = b.r % kPerHead * kRows;
+            for (int a = 0; a < len; a += kCommitNodes) {
+                const int count = min(kCommitNodes, len - a);
+                if (a > 0) {
+                    __syncthreads();
+                    for (int y = tid; y < count * (S / 4); y += kCommitThreads)
+                        *reinterpret_cast<float4 *>(ks + 4 * y) =
+                            *reinterpret_cast<const float4 *>(p.k + ((row0 + walk[a + y / (S / 4)]) * Hk + vh % Hk) * S + 4 * (y % (S / 4)));
+                    for (int y = tid; y < count * (kRows / 4); y += kCommitThreads)
+                        *reinterpret_cast<float4 *>(us + 4 * y) =
+                            *reinterpret_cast<const float4 *>(p.u + ((row0 + walk[a + y / (kRows / 4)]) * H + vh) * S + j0 + 4 * (y % (kRows / 4)));
+                    __syncthreads();
+                }
+                for (int y = 0; y < count; ++y) {
+                    float kc[E], uc[R];
+                    load_vec<E>(kc, ks + y * S + E * lane);
+                    load_vec<R>(uc, us + y * kRows + warp * R);
+                    const float w = weight[a + y];
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const float uw = uc[r] * w;
+#pragma unroll
+                        for (int e = 0; e < E; ++e) x[r][e] = fmaf(kc[e], uw, x[r][e]);
+                    }
+                }
+            }
+            float *to = b.rows + warp * R * S + E * lane;
+#pragma unroll
+            for (int r = 0; r < R; ++r) store_vec<E>(to + r * S, x[r]);
+        }
+        b = after;
+    }
+    if (!ok) {
+        // (no copy may still be on its way into a CTA that has ended)
+        mbar_wait(&full[0], 0);
+        mbar_wait(&full[0], 1);
+        mbar_wait(&full[1], 0);
+        mbar_wait(&full[1], 1);
+        if (tid == 0) atomicOr(p.watchdog, WD_STATE_COPY);
     }
 }
 
@@ -1091,11 +1225,16 @@ gdn_status launch_block(const TreeParams &p, int n_seqs, int conv_kernel, cudaSt
 }
 
 template <int E>
-gdn_status launch_commit(const CommitParams &p, int n_seqs, cudaStream_t s) {
-    constexpr int S = 32 * E, kRows = S < kCommitRows ? S : kCommitRows;
-    const int state_shares = p.n_v_heads * (S / kRows);
-    const int shares = state_shares + (p.conv_dim + kCommitChannels - 1) / kCommitChannels;
-    tree_commit_kernel<E><<<dim3(shares, n_seqs), kCommitThreads, 0, s>>>(p, state_shares);
+gdn_status launch_commit(const CommitParams &p, cudaStream_t s) {
+    using L = CommitSmem<E>;
+    const long long blocks = static_cast<long long>(p.n_seqs) * p.n_v_heads * (L::S / L::kRows);
+    const long long conv = static_cast<long long>(p.n_seqs) * ((p.conv_dim + kCommitChannels - 1) / kCommitChannels);
+    if (blocks > 0x7fffffffLL || conv > 0x7fff0000LL) return GDN_ERR_UNSUPPORTED;
+    constexpr int kCtas = 152 * (E == 8 ? 2 : kCommitCtas);
+    const int state_ctas = static_cast<int>(blocks < kCtas ? blocks : kCtas);
+    static std::atomic<unsigned long long> allowed{0};
+    GDN_TRY(allow_smem(tree_commit_kernel<E>, L::kBytes, allowed));
+    tree_commit_kernel<E><<<static_cast<unsigned>(state_ctas + conv), kCommitThreads, L::kBytes, s>>>(p, state_ctas);
     return launch_status();
 }
 
@@ -1187,15 +1326,16 @@ gdn_status gdn_block_tree_commit(const float *qkv, float *conv_state, float *sta
     const Tape T(static_cast<size_t>(n_seqs) * n_nodes, n_k_heads, n_v_heads, state_size);
     if (tape_bytes < T.floats * sizeof(float)) return GDN_ERR_SHAPE;
     const float *t = static_cast<const float *>(tape);
-    const CommitParams p{qkv, conv_state, state, parents, accepted, slots, n_nodes, n_k_heads,
+    const CommitParams p{qkv, conv_state, state, parents, accepted, slots, n_seqs, n_nodes, n_k_heads,
                          n_v_heads, (2 * n_k_heads + n_v_heads) * state_size, conv_kernel - 1, pool,
-                         err_count, t + T.k, t + T.g, t + T.u};
+                         err_count, t + T.k, t + T.g, t + T.u, watchdog_block()};
+    if (p.watchdog == nullptr) return GDN_ERR_LAUNCH;
     const cudaStream_t s = as_cuda(stream);
     switch (state_size) {
-        case 32: return launch_commit<1>(p, n_seqs, s);
-        case 64: return launch_commit<2>(p, n_seqs, s);
-        case 128: return launch_commit<4>(p, n_seqs, s);
-        default: return launch_commit<8>(p, n_seqs, s);
+        case 32: return launch_commit<1>(p, s);
+        case 64: return launch_commit<2>(p, s);
+        case 128: return launch_commit<4>(p, s);
+        default: return launch_commit<8>(p, s);
     }
 }
 

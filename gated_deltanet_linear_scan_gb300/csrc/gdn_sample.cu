@@ -929,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 // CTAs of a row: as many as give every SM its two, of at least 2048 logits each; eight, whose barriers
 // and histograms take as long as their passes, only where most of the GPU is idle anyway. (128000
 // bf16 logits by top-p: one row 32 us by eight and 34 by four, 16 rows 42 and 37, 64 rows 51 by four and
-// 88 by one; 1024 rows of 100003 in fp32 449 by one, 635 by four.)
+// 88 by one; 1024 rows of 100003 in fp32 250 by one, 295 by two, 462 by four.)
 template <typename T>
 gdn_status launch(const SampleParams &p, int rows, cudaStream_t s) {
     int cluster = rows <= 8 ? kMaxCluster : 4;
