@@ -8,8 +8,8 @@ A batch of prompts is read in, every sequence is forked into a second continuati
 tokens are decoded, drafts are verified and what the model did not agree with is rolled
 back (recurrent states by snapshot, cache by truncation), trees of drafts are read with a
 token sampled at every node and the path that the samples agree with is kept, half of the
-sequences are released and the pages of the others moved together. Tokens, lengths and tables stay on the
-device; torch multiplies the projections and holds the memory.
+sequences are released and the pages of the others moved together. Tokens, lengths and
+tables stay on the device; torch multiplies the projections and holds the memory.
 """
 import math
 import os

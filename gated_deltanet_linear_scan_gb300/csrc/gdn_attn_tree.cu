@@ -1,7 +1,7 @@
 // gdn_attn_tree.cu -- attention of a tree of drafted tokens over the paged cache: the call, and the
 // decode attention's kernel (gdn_attn_decode.cuh) in its tree form, for fp32 and for few rows. (Each 16
 // rows of (node, head) read the keys again there: more of them, in 16-bit types, are the tensor cores'
-// of gdn_attn_tree_tc.cu. In fp32 the FP32 pipes are about as long at work as the reading takes.)
+// of gdn_attn_tree_tc.cu. In fp32 the products bound the call, not the reading.)
 #include "gdn_attn_decode.cuh"
 #include "gdn_attn_tree.cuh"
 

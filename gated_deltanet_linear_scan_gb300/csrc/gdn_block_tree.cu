@@ -876,6 +876,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_state_tc_kernel(const __gr
     }
     if (!ok) {
         // (no copy may still be on its way into a CTA that has ended)
+        mbar_wait(&d_full, 0);
+        mbar_wait(&d_full, 1);
         mbar_wait(&state_full, 0);
         mbar_wait(&state_full, 1);
         mbar_wait(&images_full, 0);

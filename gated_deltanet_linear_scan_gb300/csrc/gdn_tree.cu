@@ -3,7 +3,9 @@
 //
 // A walk is at most 64 steps of a warp over nodes that lie in its registers, one vote a step. The
 // rows to move are few (a path's), so the call is latency: every CTA of a sequence walks for
-// itself, and moves its share of (plane, head, 16 bytes of a row).
+// itself, and moves its share of (plane, head, 16 bytes of a row). 64 trees of 16 with 16 planes of 8
+// heads' rows of 256 bytes: 5.4 us (the rows' bytes alone 1.1); one of 64: 6.9, a walk and a move behind
+// a launch.
 #include "gdn_paged.cuh"
 #include "gdn_tree.cuh"
 

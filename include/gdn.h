@@ -752,7 +752,9 @@ gdn_status gdn_pages_compact(void *pages, int32_t *page_table, const int32_t *kv
  *   node and what hangs below it out, and counts the sequence once in err_count (of the calls
  *   that read the whole tree: all but the commit).
  * - Outputs at a node that is not there are zeros (0.0, not sums with zero weights: what its
- *   inputs hold has no effect). */
+ *   inputs hold has no effect).
+ * - Outputs overlap no inputs. Sequences may share a slot where a call only reads it (gdn_attn_tree,
+ *   gdn_block_tree), not where it writes (the commit, and the pages of gdn_tree_accept). */
 
 #define GDN_MAX_TREE_NODES 64
 #define GDN_NO_NODE (-2)
@@ -845,8 +847,8 @@ gdn_status gdn_tree_accept(const int32_t *parents, const int32_t *tokens, const 
  * largest logit; top_k <= 0 or >= vocab, top_p >= 1 and min_p <= 0 filter nothing. NaN logits count
  * as -infinity, which is never taken; +infinity leaves only the +infinities. A row without a logit
  * above -infinity gets token -1; so does one whose temperature is negative or not finite, or
- * whose top_p or min_p is NaN, which is counted in err_count. Weights are held to 2^-43 of the
- * largest, so that tokens do not depend on the order of sums. vocab: at most 2^20, else
+ * whose top_p or min_p is NaN, which is counted in err_count. Weights are held to 2^-43 of
+ * their sum, as integers, so that tokens do not depend on the order of sums. vocab: at most 2^20, else
  * GDN_ERR_UNSUPPORTED. */
 gdn_status gdn_sample(const void *logits, const float *uniforms, const float *temperature,
                       const int32_t *top_k, const float *top_p, const float *min_p,

@@ -1,6 +1,6 @@
 """Sampling against the definition in 64 bits on the host: the tokens are equal.
 
-The kernel's weights are good to 2^-43 of the largest and a 64-bit form's to some 2^-50, so a row
+The kernel's weights are good to 2^-43 of their sum and a 64-bit form's to some 2^-50, so a row
 whose uniform number, or top-p border, falls within about 10^-11 of an edge could come out otherwise;
 of the some 10^5 rows here that is less than one in 10^4 runs, and the seeds are fixed."""
 import numpy as np
