@@ -99,6 +99,57 @@ __device__ __forceinline__ void load_run(float (&x)[N], const float *from) {
         for (int i = 0; i < N; ++i) x[i] = from[i];
 }
 
+// SiLU of a node's convolution, channels of a lane: `own` its own raw input, x_ptr node 0's. Conditions
+// are uniform over the warp.
+template <int E, int K>
+__device__ __forceinline__ void conv_node(const float *x_ptr, size_t conv_dim, int i, unsigned long long path,
+                                          const float (&wc)[E * K], const float (&hist)[E * (K - 1)],
+                                          const float (&own)[E], float (&o)[E]) {
+    constexpr int TAPS = K - 1;
+    const int depth = __popcll(path);
+    float taps[TAPS][E];  // [t]: of the t-th oldest input before its own
+    path &= ~(1ull << i);
+#pragma unroll
+    for (int t = TAPS - 1; t >= 0; --t)
+        if (path != 0) {
+            const int a = 63 - __clzll(static_cast<long long>(path));
+            path &= ~(1ull << a);
+            load_vec<E>(taps[t], x_ptr + static_cast<size_t>(a) * conv_dim);
+        }
+    // past the root: the history, newest last
+#pragma unroll
+    for (int d = 1; d <= TAPS; ++d)
+        if (depth == d)
+#pragma unroll
+            for (int t = 0; t <= TAPS - d; ++t)
+#pragma unroll
+                for (int e = 0; e < E; ++e) taps[t][e] = hist[e * TAPS + t + d - 1];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        float pre = __fmul_rn(own[e], wc[e * K + K - 1]);
+#pragma unroll
+        for (int t = 0; t < TAPS; ++t) pre = __fmaf_rn(taps[t][e], wc[e * K + t], pre);
+        o[e] = silu(pre);
+    }
+}
+
+// A vector over its length, by a whole warp.
+template <int E>
+__device__ __forceinline__ void normalise(float (&o)[E], float eps) {
+    float ss = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) ss = __fmaf_rn(o[e], o[e], ss);
+    ss = warp_allsum(ss);
+    const float inv = 1.0f / fmaxf(sqrtf(ss), eps);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= inv;
+}
+
+__device__ __forceinline__ float gate_of(const TreeParams &p, size_t at, int h) {
+    return p.a[h] * softplus_guarded(p.alpha[at] + p.dt[h]);
+}
+__device__ __forceinline__ float beta_of_node(const TreeParams &p, size_t at) { return 1.0f / (1.0f + expf(-p.b[at])); }
+
 template <int E, int K>
 __global__ void __launch_bounds__(32 * kConvWarps) tree_conv_kernel(const TreeParams p) {
     constexpr int S = 32 * E, TAPS = K - 1;
@@ -148,8 +199,8 @@ __global__ void __launch_bounds__(32 * kConvWarps) tree_conv_kernel(const TreePa
             const int i = i0 + x / H, h = x % H;
             const size_t at = (row0 + i) * H + h;
             const bool here = path_of[i] != 0;
-            p.g[at] = here ? p.a[h] * softplus_guarded(p.alpha[at] + p.dt[h]) : 0.0f;
-            p.beta[at] = here ? 1.0f / (1.0f + expf(-p.b[at])) : 0.0f;
+            p.g[at] = here ? gate_of(p, at, h) : 0.0f;
+            p.beta[at] = here ? beta_of_node(p, at) : 0.0f;
         }
         return;
     }
@@ -162,52 +213,17 @@ __global__ void __launch_bounds__(32 * kConvWarps) tree_conv_kernel(const TreePa
     for (int y = 0; y < kConvNodes; ++y) {
         const int i = i0 + y;
         if (i >= i1) break;  // uniform over the warp, as every condition below
-        float o[E];
-        unsigned long long path = path_of[i];
-        const int depth = __popcll(path);
-        if (depth == 0) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = 0.0f;
-        } else {
-            float taps[K][E];  // [t]: of the t-th oldest input, [TAPS] the node's own
+        float o[E] = {};
+        if (path_of[i] != 0) {
+            float mine[E];
             if constexpr (kEarly) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) taps[TAPS][e] = own[y][e];
+                for (int e = 0; e < E; ++e) mine[e] = own[y][e];
             } else {
-                load_vec<E>(taps[TAPS], x_ptr + static_cast<size_t>(i) * conv_dim);
+                load_vec<E>(mine, x_ptr + static_cast<size_t>(i) * conv_dim);
             }
-            path &= ~(1ull << i);
-#pragma unroll
-            for (int t = TAPS - 1; t >= 0; --t)
-                if (path != 0) {
-                    const int a = 63 - __clzll(static_cast<long long>(path));
-                    path &= ~(1ull << a);
-                    load_vec<E>(taps[t], x_ptr + static_cast<size_t>(a) * conv_dim);
-                }
-            // past the root: the history, newest last
-#pragma unroll
-            for (int d = 1; d <= TAPS; ++d)
-                if (depth == d)
-#pragma unroll
-                    for (int t = 0; t <= TAPS - d; ++t)
-#pragma unroll
-                        for (int e = 0; e < E; ++e) taps[t][e] = hist[e * TAPS + t + d - 1];
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                float pre = __fmul_rn(taps[TAPS][e], wc[e * K + K - 1]);
-#pragma unroll
-                for (int t = 0; t < TAPS; ++t) pre = __fmaf_rn(taps[t][e], wc[e * K + t], pre);
-                o[e] = silu(pre);
-            }
-            if (is_qk) {
-                float ss = 0.0f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) ss = __fmaf_rn(o[e], o[e], ss);
-                ss = warp_allsum(ss);
-                const float inv = 1.0f / fmaxf(sqrtf(ss), p.l2_eps);
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[e] *= inv;
-            }
+            conv_node<E, K>(x_ptr, conv_dim, i, path_of[i], wc, hist, mine, o);
+            if (is_qk) normalise<E>(o, p.l2_eps);
         }
         store_vec<E>(dst + static_cast<size_t>(i) * dst_step, o);
     }
@@ -485,50 +501,95 @@ struct PrepSmem {
 
 constexpr int kPrepSmem = 196608;  // no number of nodes needs more
 
-__global__ void __launch_bounds__(kPrepThreads, 2) tree_prepare_kernel(const TreeParams p) {
+template <int K>
+__global__ void __launch_bounds__(kPrepThreads, K <= 4 ? 2 : 1) tree_prepare_kernel(const TreeParams p, int prepares) {
     constexpr int S = 128, kLd = PrepSmem::kLd;
     extern __shared__ __align__(16) uint8_t dyn[];
+    constexpr int E = 4, TAPS = K - 1;
     __shared__ unsigned long long path_of[kMaxNodes];
+    __shared__ int up[kMaxNodes];
     __shared__ int level[kMaxNodes + 1];      // [d]: where the nodes of depth d + 1 begin in by_depth
     __shared__ uint8_t by_depth[kMaxNodes];
     __shared__ float g_of[kPrepHeads][kMaxNodes], beta_of[kPrepHeads][kMaxNodes], hi_of[kPrepHeads][kMaxNodes], lo_of[kPrepHeads][kMaxNodes];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
-    const int kh = blockIdx.x, n = blockIdx.y, N = p.n_nodes, Hk = p.n_k_heads, H = p.n_v_heads;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x, warps = threads / 32;
+    const int N = p.n_nodes, Hk = p.n_k_heads, H = p.n_v_heads;
+    const bool prepare = static_cast<int>(blockIdx.x) < prepares;
+    // the others: v-heads of a block of nodes of a sequence, one a warp
+    const int groups_v = (H + warps - 1) / warps, node_blocks = (N + kConvNodes - 1) / kConvNodes;
+    const int other = static_cast<int>(blockIdx.x) - prepares;
+    const int n = prepare ? blockIdx.x / Hk : other / (groups_v * node_blocks), kh = prepare ? blockIdx.x % Hk : 0;
     const int slot = p.slots ? p.slots[n] : n;
-    if (slot < 0 || slot >= p.pool) return;
+    const bool counts = prepare && kh == 0;
+    if (slot < 0 || slot >= p.pool) {
+        if (counts && tid == 0 && p.err_count) atomicAdd(p.err_count, 1);
+        return;
+    }
+    const size_t row0 = static_cast<size_t>(n) * N, conv_dim = static_cast<size_t>(2 * Hk + H) * S;
+    // this warp's head slice: of q (even warps) or k (odd ones), or of v; its weights [E][K] and history [E][TAPS]
+    const int vh_mine = other % groups_v * warps + warp;
+    const int slice = prepare ? (warp & 1) * Hk + kh : 2 * Hk + vh_mine;
+    const bool has_slice = prepare || vh_mine < H;
+    const size_t ch0 = static_cast<size_t>(slice) * S + E * lane;
+    const float *x_ptr = p.qkv + row0 * conv_dim + ch0;
+    float wc[E * K], hist[E * TAPS];
+    if (has_slice) {
+        load_run<E * K>(wc, p.conv_w + ch0 * K);
+        load_run<E * TAPS>(hist, p.conv_state + (static_cast<size_t>(slot) * conv_dim + ch0) * TAPS);
+    }
+    if (warp == 0) {
+        unsigned long long paths[2];
+        const bool bad = tree_paths(p.parents + row0, N, paths, path_of, up);
+        if (bad && counts && lane == 0 && p.err_count) atomicAdd(p.err_count, 1);
+    }
+    __syncthreads();
+    if (!prepare) {
+        if (!has_slice) return;
+        const int i0 = other / groups_v % node_blocks * kConvNodes, i1 = min(N, i0 + kConvNodes);
+#pragma unroll 2
+        for (int i = i0; i < i1; ++i) {
+            float o[E] = {};
+            if (path_of[i] != 0) {
+                float mine[E];
+                load_vec<E>(mine, x_ptr + static_cast<size_t>(i) * conv_dim);
+                conv_node<E, K>(x_ptr, conv_dim, i, path_of[i], wc, hist, mine, o);
+            }
+            store_vec<E>(p.v + ((row0 + i) * H + vh_mine) * S + E * lane, o);
+        }
+        return;
+    }
     const TcSizes z(N);
     const PrepSmem L(N);
     float *rows = reinterpret_cast<float *>(dyn);  // k of all nodes, then q
     float2 *gram = reinterpret_cast<float2 *>(dyn + L.gram);
     uint8_t *anc = dyn + L.anc;  // [N][pad]: the path's nodes in order, then its first again
-    const size_t row0 = static_cast<size_t>(n) * N;
-    if (tid < N) path_of[tid] = p.paths[row0 + tid];
-    // ---- k and q, as they are and as images (rows past the nodes zero)
-    uint8_t *images = reinterpret_cast<uint8_t *>(p.gram) + (static_cast<size_t>(n) * Hk + kh) * z.images;
-    for (int x0 = tid; x0 < z.rows * (S / 8); x0 += 4 * threads) {
-        float v[4][8];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {  // (four pieces on their way together)
-            const int x = x0 + b * threads, r = x / S * 8 + x % 8, c = x / 8 % (S / 8), i = r < z.pad ? r : r - z.pad;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[b][e] = 0.0f;
-            if (r < z.rows && i < N) load_vec<8>(v[b], (r < z.pad ? p.k : p.q) + ((row0 + i) * Hk + kh) * S + 8 * c);
+    // ---- k and q
+#pragma unroll 2
+    for (int i = warp >> 1; i < N; i += warps / 2) {
+        float o[E] = {};
+        if (path_of[i] != 0) {
+            float mine[E];
+            load_vec<E>(mine, x_ptr + static_cast<size_t>(i) * conv_dim);
+            conv_node<E, K>(x_ptr, conv_dim, i, path_of[i], wc, hist, mine, o);
+            normalise<E>(o, p.l2_eps);
         }
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int x = x0 + b * threads, r = x / S * 8 + x % 8, c = x / 8 % (S / 8), i = r < z.pad ? r : r - z.pad;
-            if (r >= z.rows) break;
-            if (i < N) store_vec<8>(rows + (r < z.pad ? i : N + i) * kLd + 8 * c, v[b]);
-            uint32_t w[3][4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) tc::split3(v[b][2 * e], v[b][2 * e + 1], w[0][e], w[1][e], w[2][e]);
-            uint8_t *to = images + tc::kmajor_offset16(r, 8 * c, 128, S / 8 * 128);
-#pragma unroll
-            for (int y = 0; y < 3; ++y)
-                *reinterpret_cast<uint4 *>(to + y * z.image) = make_uint4(w[y][0], w[y][1], w[y][2], w[y][3]);
-        }
+        store_vec<E>(rows + ((warp & 1) ? i : N + i) * kLd + E * lane, o);
+        if (warp & 1) store_vec<E>(p.k + ((row0 + i) * Hk + kh) * S + E * lane, o);
     }
     __syncthreads();
+    // ---- as images (rows past the nodes zero)
+    uint8_t *images = reinterpret_cast<uint8_t *>(p.gram) + (static_cast<size_t>(n) * Hk + kh) * z.images;
+    for (int x = tid; x < z.rows * (S / 8); x += threads) {
+        const int r = x / S * 8 + x % 8, c = x / 8 % (S / 8), i = r < z.pad ? r : r - z.pad;
+        float v[8] = {};
+        if (i < N) load_vec<8>(v, rows + (r < z.pad ? i : N + i) * kLd + 8 * c);
+        uint32_t w[3][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tc::split3(v[2 * e], v[2 * e + 1], w[0][e], w[1][e], w[2][e]);
+        uint8_t *to = images + tc::kmajor_offset16(r, 8 * c, 128, S / 8 * 128);
+#pragma unroll
+        for (int y = 0; y < 3; ++y)
+            *reinterpret_cast<uint4 *>(to + y * z.image) = make_uint4(w[y][0], w[y][1], w[y][2], w[y][3]);
+    }
     // ---- the paths as lists; the nodes by how deep they stand
     for (int i = warp; i < N; i += threads / 32) {
         const unsigned long long path = path_of[i];
@@ -584,8 +645,9 @@ __global__ void __launch_bounds__(kPrepThreads, 2) tree_prepare_kernel(const Tre
         const int hx = tid / kMaxNodes, ix = tid % kMaxNodes;
         if (hx < heads && ix < N) {
             const size_t at = (row0 + ix) * H + kh + (h0 + hx) * Hk;
-            g_of[hx][ix] = p.g[at];
-            beta_of[hx][ix] = p.beta[at];
+            const bool here = path_of[ix] != 0;
+            g_of[hx][ix] = p.g[at] = here ? gate_of(p, at, kh + (h0 + hx) * Hk) : 0.0f;
+            beta_of[hx][ix] = here ? beta_of_node(p, at) : 0.0f;
         }
         __syncthreads();
         if (hx < heads && ix < z.pad) {
@@ -1176,38 +1238,35 @@ gdn_status launch_conv(const TreeParams &p, int n_seqs, cudaStream_t s) {
     return launch_status();
 }
 
-template <int E>
-gdn_status launch_block(const TreeParams &p, int n_seqs, int conv_kernel, cudaStream_t s) {
-    switch (conv_kernel) {
-        case 2: GDN_TRY((launch_conv<E, 2>(p, n_seqs, s))); break;
-        case 3: GDN_TRY((launch_conv<E, 3>(p, n_seqs, s))); break;
-        case 4: GDN_TRY((launch_conv<E, 4>(p, n_seqs, s))); break;
-        case 5: GDN_TRY((launch_conv<E, 5>(p, n_seqs, s))); break;
-        case 6: GDN_TRY((launch_conv<E, 6>(p, n_seqs, s))); break;
-        case 7: GDN_TRY((launch_conv<E, 7>(p, n_seqs, s))); break;
-        default: GDN_TRY((launch_conv<E, 8>(p, n_seqs, s))); break;
-    }
+// States of 128, on the tensor cores.
+template <int K>
+gdn_status launch_tc(const TreeParams &p, int n_seqs, cudaStream_t s) {
+    CUtensorMap map;
+    GDN_TRY(encode_blocks_map(&map, p.state, GDN_F32, 128, static_cast<uint64_t>(p.pool) * p.n_v_heads * 128, 512, 128, 4));
+    static std::atomic<unsigned long long> allowed{0}, prepare_allowed{0};
+    GDN_TRY(allow_smem(tree_prepare_kernel<K>, kPrepSmem, prepare_allowed));
+    GDN_TRY(allow_smem(tree_state_tc_kernel, TcSmem::kMost + 1024, allowed));
+    // all CTAs that prepare at once, and as many warps as that leaves
+    const long long prepares = static_cast<long long>(n_seqs) * p.n_k_heads;
+    const int threads = prepares <= 152 ? kPrepThreads : prepares <= 4 * 152 ? kPrepThreads / 2 : kPrepThreads / 4, warps = threads / 32;
+    const long long others = static_cast<long long>(n_seqs) * ((p.n_v_heads + warps - 1) / warps) * ((p.n_nodes + kConvNodes - 1) / kConvNodes);
+    if (prepares + others > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+    tree_prepare_kernel<K><<<static_cast<unsigned>(prepares + others), threads, PrepSmem(p.n_nodes).bytes, s>>>(p, static_cast<int>(prepares));
+    GDN_TRY(launch_status());
+    const TcSizes z(p.n_nodes);
+    const uint32_t smem = TcSmem(z, p.n_nodes).bytes + 1024;
+    const int items = n_seqs * p.n_v_heads, wide = 152 * (tmem_cols(z) <= 256 && smem <= 113 * 1024 ? 2 : 1);
+    tree_state_tc_kernel<<<items < wide ? items : wide, kTcThreads, smem, s>>>(map, p, items);
+    return launch_status();
+}
+
+template <int E, int K>
+gdn_status launch_block_of(const TreeParams &p, int n_seqs, cudaStream_t s) {
     if constexpr (E == 4) {
         // (a tensor map's rows are counted in 32 bits)
-        const long long state_rows = static_cast<long long>(p.pool) * p.n_v_heads * 128;
-        if (state_rows <= 0x7fffffffLL) {
-            CUtensorMap map;
-            GDN_TRY(encode_blocks_map(&map, p.state, GDN_F32, 128, static_cast<uint64_t>(state_rows), 512, 128, 4));
-            static std::atomic<unsigned long long> allowed{0}, prepare_allowed{0};
-            GDN_TRY(allow_smem(tree_prepare_kernel, kPrepSmem, prepare_allowed));
-            GDN_TRY(allow_smem(tree_state_tc_kernel, TcSmem::kMost + 1024, allowed));
-            // all CTAs at once, and as many warps as that leaves
-            const long long ctas = static_cast<long long>(n_seqs) * p.n_k_heads;
-            const int threads = ctas <= 152 ? kPrepThreads : ctas <= 4 * 152 ? kPrepThreads / 2 : kPrepThreads / 4;
-            tree_prepare_kernel<<<dim3(p.n_k_heads, n_seqs), threads, PrepSmem(p.n_nodes).bytes, s>>>(p);
-            GDN_TRY(launch_status());
-            const TcSizes z(p.n_nodes);
-            const uint32_t smem = TcSmem(z, p.n_nodes).bytes + 1024;
-            const int items = n_seqs * p.n_v_heads, wide = 152 * (tmem_cols(z) <= 256 && smem <= 113 * 1024 ? 2 : 1);
-            tree_state_tc_kernel<<<items < wide ? items : wide, kTcThreads, smem, s>>>(map, p, items);
-            return launch_status();
-        }
+        if (static_cast<long long>(p.pool) * p.n_v_heads * 128 <= 0x7fffffffLL) return launch_tc<K>(p, n_seqs, s);
     }
+    GDN_TRY((launch_conv<E, K>(p, n_seqs, s)));
     const size_t keys = static_cast<size_t>(p.n_nodes) * 32 * E * sizeof(float);
     static std::atomic<unsigned long long> gram_allowed{0};
     GDN_TRY(allow_smem(tree_gram_kernel<E>, kMaxNodes * 32 * E * static_cast<int>(sizeof(float)), gram_allowed));
@@ -1224,6 +1283,19 @@ gdn_status launch_block(const TreeParams &p, int n_seqs, int conv_kernel, cudaSt
     tree_norm_kernel<E><<<static_cast<unsigned>((rows + kNormThreads / 32 - 1) / (kNormThreads / 32)),
                           kNormThreads, 0, s>>>(p, rows);
     return launch_status();
+}
+
+template <int E>
+gdn_status launch_block(const TreeParams &p, int n_seqs, int conv_kernel, cudaStream_t s) {
+    switch (conv_kernel) {
+        case 2: return launch_block_of<E, 2>(p, n_seqs, s);
+        case 3: return launch_block_of<E, 3>(p, n_seqs, s);
+        case 4: return launch_block_of<E, 4>(p, n_seqs, s);
+        case 5: return launch_block_of<E, 5>(p, n_seqs, s);
+        case 6: return launch_block_of<E, 6>(p, n_seqs, s);
+        case 7: return launch_block_of<E, 7>(p, n_seqs, s);
+        default: return launch_block_of<E, 8>(p, n_seqs, s);
+    }
 }
 
 template <int E>
