@@ -502,7 +502,7 @@ struct PrepSmem {
 constexpr int kPrepSmem = 196608;  // no number of nodes needs more
 
 template <int K>
-__global__ void __launch_bounds__(kPrepThreads, K <= 4 ? 2 : 1) tree_prepare_kernel(const TreeParams p, int prepares) {
+__global__ void __launch_bounds__(kPrepThreads, K <= 4 ? 2 : 1) tree_prepare_kernel(const TreeParams p, int prepares, int parts) {
     constexpr int S = 128, kLd = PrepSmem::kLd;
     extern __shared__ __align__(16) uint8_t dyn[];
     constexpr int E = 4, TAPS = K - 1;
@@ -517,9 +517,10 @@ __global__ void __launch_bounds__(kPrepThreads, K <= 4 ? 2 : 1) tree_prepare_ker
     // the others: v-heads of a block of nodes of a sequence, one a warp
     const int groups_v = (H + warps - 1) / warps, node_blocks = (N + kConvNodes - 1) / kConvNodes;
     const int other = static_cast<int>(blockIdx.x) - prepares;
-    const int n = prepare ? blockIdx.x / Hk : other / (groups_v * node_blocks), kh = prepare ? blockIdx.x % Hk : 0;
+    const int n = prepare ? blockIdx.x / (Hk * parts) : other / (groups_v * node_blocks), kh = prepare ? blockIdx.x % Hk : 0;
+    const int part = prepare ? blockIdx.x / Hk % parts : 0;  // of the v-heads; the first writes what all share
     const int slot = p.slots ? p.slots[n] : n;
-    const bool counts = prepare && kh == 0;
+    const bool counts = prepare && kh == 0 && part == 0;
     if (slot < 0 || slot >= p.pool) {
         if (counts && tid == 0 && p.err_count) atomicAdd(p.err_count, 1);
         return;
@@ -573,12 +574,12 @@ __global__ void __launch_bounds__(kPrepThreads, K <= 4 ? 2 : 1) tree_prepare_ker
             normalise<E>(o, p.l2_eps);
         }
         store_vec<E>(rows + ((warp & 1) ? i : N + i) * kLd + E * lane, o);
-        if (warp & 1) store_vec<E>(p.k + ((row0 + i) * Hk + kh) * S + E * lane, o);
+        if ((warp & 1) && part == 0) store_vec<E>(p.k + ((row0 + i) * Hk + kh) * S + E * lane, o);
     }
     __syncthreads();
     // ---- as images (rows past the nodes zero)
     uint8_t *images = reinterpret_cast<uint8_t *>(p.gram) + (static_cast<size_t>(n) * Hk + kh) * z.images;
-    for (int x = tid; x < z.rows * (S / 8); x += threads) {
+    for (int x = part == 0 ? tid : z.rows * (S / 8); x < z.rows * (S / 8); x += threads) {
         const int r = x / S * 8 + x % 8, c = x / 8 % (S / 8), i = r < z.pad ? r : r - z.pad;
         float v[8] = {};
         if (i < N) load_vec<8>(v, rows + (r < z.pad ? i : N + i) * kLd + 8 * c);
@@ -636,8 +637,8 @@ __global__ void __launch_bounds__(kPrepThreads, K <= 4 ? 2 : 1) tree_prepare_ker
         }
     }
     const int groups = H / Hk;  // v-heads of this k-head: kh, kh + Hk, ..
-    const int at_once = min(L.heads, threads / kMaxNodes);
-    for (int h0 = 0; h0 < groups; h0 += at_once) {
+    const int at_once = parts > 1 ? 1 : min(L.heads, threads / kMaxNodes);
+    for (int h0 = part * at_once; h0 < groups; h0 += parts * at_once) {
         const int heads = min(at_once, groups - h0);
         __syncthreads();  // the products, or the v-heads before, are done with
         auto out_of = [&](int h) { return p.weights + (static_cast<size_t>(n) * H + kh + (h0 + h) * Hk) * z.weights; };
@@ -1247,11 +1248,13 @@ gdn_status launch_tc(const TreeParams &p, int n_seqs, cudaStream_t s) {
     GDN_TRY(allow_smem(tree_prepare_kernel<K>, kPrepSmem, prepare_allowed));
     GDN_TRY(allow_smem(tree_state_tc_kernel, TcSmem::kMost + 1024, allowed));
     // all CTAs that prepare at once, and as many warps as that leaves
-    const long long prepares = static_cast<long long>(n_seqs) * p.n_k_heads;
+    const int groups = p.n_v_heads / p.n_k_heads;
+    const int parts = static_cast<long long>(n_seqs) * p.n_v_heads <= 152 ? groups : 1;  // (few trees: a CTA a v-head)
+    const long long prepares = static_cast<long long>(n_seqs) * p.n_k_heads * parts;
     const int threads = prepares <= 152 ? kPrepThreads : prepares <= 4 * 152 ? kPrepThreads / 2 : kPrepThreads / 4, warps = threads / 32;
     const long long others = static_cast<long long>(n_seqs) * ((p.n_v_heads + warps - 1) / warps) * ((p.n_nodes + kConvNodes - 1) / kConvNodes);
     if (prepares + others > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
-    tree_prepare_kernel<K><<<static_cast<unsigned>(prepares + others), threads, PrepSmem(p.n_nodes).bytes, s>>>(p, static_cast<int>(prepares));
+    tree_prepare_kernel<K><<<static_cast<unsigned>(prepares + others), threads, PrepSmem(p.n_nodes).bytes, s>>>(p, static_cast<int>(prepares), parts);
     GDN_TRY(launch_status());
     const TcSizes z(p.n_nodes);
     const uint32_t smem = TcSmem(z, p.n_nodes).bytes + 1024;
