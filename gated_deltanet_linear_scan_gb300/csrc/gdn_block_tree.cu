@@ -83,7 +83,7 @@ struct TreeParams {
 
 // ------------------------------------------------------------------ conv, norms and gates
 
-// One warp per (head slice of S channels, kConvNodes nodes, sequence), lane L holding channels
+// (Of other states than 128, whose nodes' sums have no tensor cores; the arithmetic is shared.) One warp per (head slice of S channels, kConvNodes nodes, sequence), lane L holding channels
 // [E L, E L + E). A node's taps are its own raw input and those of its nearest ancestors, the
 // conv history behind the root's; the arithmetic is the prefill block's, so a tree that is a chain
 // has its bits. The CTAs behind the slices' compute the gates. A node that is not there has zeros.
@@ -440,17 +440,17 @@ __global__ void __launch_bounds__(kStateThreads) tree_state_kernel(const TreePar
 // value channel j), the nodes' in shared memory: three images of [K; Q], K-major core matrices.
 // S1 and S2 multiply the first two images at once, into two column groups that are added up later.
 //
-// A kernel ahead of it, per (sequence, k-head), writes the images, and for every v-head of the k-head
-// solves the nodes' triangular system: with A[i][s] = beta_i e^{G_i - G_s} k_i.k_s (s above i) and
+// A kernel ahead of it convolves the values, and per (sequence, k-head) convolves q and k, writes the
+// images, and for every v-head of the k-head solves the nodes' triangular system: with A[i][s] = beta_i e^{G_i - G_s} k_i.k_s (s above i) and
 // T = (I + A)^-1,
 //   R_s = beta_s (v_s - e^{G_s} S0^T k_s),   u_i = sum_{s on the path to i} T[i][s] R_s,
 //   y_i = scale (e^{G_i} S0^T q_i + sum_s W[i][s] R_s),   W = B T, B[i][s] = e^{G_i - G_s} q_i.k_s,
 // so that over the state all nodes are independent of one another. T and W are lists along the paths.
 //
-// 64 sequences of 16 nodes, 16 k- and 32 v-heads: 114 us, of which the convolution takes 28, the
-// kernel ahead 29 and this one 56 (it reads 198 MB and writes 19 in that time: 3.9 TB/s; between
-// barriers its 16 warps an SM issue in 4 cycles of 10). Node after node over the state instead of T: 122
-// us. One sequence of 48 nodes: 39 us instead of 45, 13 of them here.
+// 64 sequences of 16 nodes, 16 k- and 32 v-heads: 102 us, of which the kernel ahead takes 44 (issue and
+// latency; with a kernel of its own for the convolution 28 and 29) and this one 56 (it reads 198 MB and
+// writes 19 in that time: 3.9 TB/s; between barriers its 16 warps an SM issue in 4 cycles of 10). One
+// sequence of 48 nodes: 36 us, 13 of them here. (Node after node over the state instead of T: 122 and 45.)
 constexpr int kTcThreads = 256;
 constexpr uint32_t kColA = 0, kColD = 192;  // tensor memory: the state's parts, 64 columns each; D, two groups
 
@@ -475,9 +475,11 @@ __host__ __device__ inline uint32_t tmem_cols(const TcSizes &z) {
     return kColD + 2u * static_cast<uint32_t>(z.rows) <= 256u ? 256u : 512u;
 }
 
-// Images and weights. Grid: (k-head, sequence), 8 warps, or 16 where that leaves SMs idle. The nodes'
-// products, a warp a node; then, for a few v-heads at a time, A and B as lists along the paths, one
-// thread an entry, and T and W, all rows of one depth together.
+// Convolution, images and weights. CTAs of (k-head, part of its v-heads, sequence): 4 warps, 8 or 16 where that
+// leaves SMs idle, and then with few sequences a part for every v-head. q and k, a warp a node; the
+// nodes' products, a warp a node; then, for a few v-heads at a time, A and B as lists along the
+// paths, one thread an entry, and T and W, all rows of one depth together. The CTAs behind them convolve the
+// values, a warp a v-head of up to kConvNodes nodes.
 constexpr int kPrepThreads = 512;
 constexpr int kPrepHeads = 4;
 
