@@ -48,22 +48,29 @@ struct TcSizes {
     }
 };
 
-// Scratch: q [n][N][Hk][S], v [n][N][H][S], beta [n][N][H], the products k_i.k_s and q_i.k_s
-// [n][Hk][N][N][2] or (states of 128) the images and weights of the tensor-core path, and the nodes' paths
+// Scratch: v [n][N][H][S] and, of states of 128, the images and weights of the tensor-core path; of others q
+// [n][N][Hk][S], beta [n][N][H], the products k_i.k_s and q_i.k_s [n][Hk][N][N][2] and the nodes' paths
 // [n][N] (0: not there).
 struct Scratch {
-    size_t q, v, beta, gram, weights, paths, floats;
+    size_t v, images, weights, q, beta, gram, paths, floats;
     Scratch(size_t rows, int n_nodes, int hk, int h, int s) {
         const size_t seqs = rows / n_nodes;
         const TcSizes tc(n_nodes);
-        q = 0;
-        v = q + round_up(rows * hk * s);
-        beta = v + round_up(rows * h * s);
-        gram = beta + round_up(rows * h);
-        const size_t products = rows * n_nodes * hk * 2, images = seqs * hk * (tc.images / 4);
-        weights = gram + round_up(s == 128 && images > products ? images : products);
-        paths = weights + (s == 128 ? round_up(seqs * h * (tc.weights / 4)) : 0);
-        floats = paths + round_up(rows * 2);
+        v = images = weights = q = beta = gram = paths = 0;
+        floats = round_up(rows * h * s);
+        auto take = [&](size_t &at, size_t n) {
+            at = floats;
+            floats += round_up(n);
+        };
+        if (s == 128) {
+            take(images, seqs * hk * (tc.images / 4));
+            take(weights, seqs * h * (tc.weights / 4));
+        } else {
+            take(q, rows * hk * s);
+            take(beta, rows * h);
+            take(gram, rows * n_nodes * hk * 2);
+            take(paths, rows * 2);
+        }
     }
 };
 
@@ -75,8 +82,8 @@ struct TreeParams {
     float scale, l2_eps, norm_eps;
     int32_t *err_count;
     float *k, *g, *u;             // the tape
-    float *q, *v, *beta, *gram;   // scratch (gram: or the images)
-    uint8_t *weights;
+    float *v, *q, *beta, *gram;   // scratch
+    uint8_t *images, *weights;
     unsigned long long *paths;
     unsigned *watchdog;
 };
@@ -580,7 +587,7 @@ __global__ void __launch_bounds__(kPrepThreads, K <= 4 ? 2 : 1) tree_prepare_ker
     }
     __syncthreads();
     // ---- as images (rows past the nodes zero)
-    uint8_t *images = reinterpret_cast<uint8_t *>(p.gram) + (static_cast<size_t>(n) * Hk + kh) * z.images;
+    uint8_t *images = p.images + (static_cast<size_t>(n) * Hk + kh) * z.images;
     for (int x = part == 0 ? tid : z.rows * (S / 8); x < z.rows * (S / 8); x += threads) {
         const int r = x / S * 8 + x % 8, c = x / 8 % (S / 8), i = r < z.pad ? r : r - z.pad;
         float v[8] = {};
@@ -766,7 +773,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) tree_state_tc_kernel(const __gr
     auto load_images = [&](int item, int turn) {
         const size_t image = static_cast<size_t>(item / H) * Hk + item % H % Hk;
         mbar_arrive_expect_tx(&images_full, z.images + z.weights);
-        bulk_g2s(smem + L.images, reinterpret_cast<const uint8_t *>(p.gram) + image * z.images, z.images, &images_full);
+        bulk_g2s(smem + L.images, p.images + image * z.images, z.images, &images_full);
         bulk_g2s(smem + L.weights + turn * L.turn, p.weights + static_cast<size_t>(item) * z.weights, z.weights, &images_full);
     };
     int item = from(blockIdx.x);
@@ -1265,12 +1272,9 @@ gdn_status launch_tc(const TreeParams &p, int n_seqs, cudaStream_t s) {
     return launch_status();
 }
 
+// Other states, on the FP32 pipes.
 template <int E, int K>
-gdn_status launch_block_of(const TreeParams &p, int n_seqs, cudaStream_t s) {
-    if constexpr (E == 4) {
-        // (a tensor map's rows are counted in 32 bits)
-        if (static_cast<long long>(p.pool) * p.n_v_heads * 128 <= 0x7fffffffLL) return launch_tc<K>(p, n_seqs, s);
-    }
+gdn_status launch_fp32(const TreeParams &p, int n_seqs, cudaStream_t s) {
     GDN_TRY((launch_conv<E, K>(p, n_seqs, s)));
     const size_t keys = static_cast<size_t>(p.n_nodes) * 32 * E * sizeof(float);
     static std::atomic<unsigned long long> gram_allowed{0};
@@ -1288,6 +1292,12 @@ gdn_status launch_block_of(const TreeParams &p, int n_seqs, cudaStream_t s) {
     tree_norm_kernel<E><<<static_cast<unsigned>((rows + kNormThreads / 32 - 1) / (kNormThreads / 32)),
                           kNormThreads, 0, s>>>(p, rows);
     return launch_status();
+}
+
+template <int E, int K>
+gdn_status launch_block_of(const TreeParams &p, int n_seqs, cudaStream_t s) {
+    if constexpr (E == 4) return launch_tc<K>(p, n_seqs, s);
+    else return launch_fp32<E, K>(p, n_seqs, s);
 }
 
 template <int E>
@@ -1362,6 +1372,8 @@ gdn_status gdn_block_tree(const float *qkv, const float *conv_w, const float *co
     GDN_TRY(check_tree(parents, n_seqs, n_nodes));
     GDN_TRY(check_sizes(n_seqs, n_nodes, n_k_heads, n_v_heads, state_size, conv_kernel));
     GDN_TRY(check_pool(n_seqs, slots, pool));
+    // (rows of a tensor map are counted in 32 bits; so many are a terabyte)
+    if (state_size == 128 && static_cast<long long>(pool) * n_v_heads * 128 > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
     if (!aligned16(qkv) || !aligned16(conv_w) || !aligned16(conv_state) || !aligned16(state) ||
         !aligned16(z) || !aligned16(out) || !aligned16(norm_w))
         return GDN_ERR_ALIGN;
@@ -1376,8 +1388,8 @@ gdn_status gdn_block_tree(const float *qkv, const float *conv_w, const float *co
     float *t = static_cast<float *>(tape), *w = static_cast<float *>(workspace);
     const TreeParams p{qkv, conv_w, conv_state, alpha, b, dt, a, z, norm_w, state, out, parents,
                        slots, n_nodes, n_k_heads, n_v_heads, pool, scale, l2_eps, norm_eps,
-                       err_count, t + T.k, t + T.g, t + T.u, w + W.q, w + W.v, w + W.beta,
-                       w + W.gram, reinterpret_cast<uint8_t *>(w + W.weights),
+                       err_count, t + T.k, t + T.g, t + T.u, w + W.v, w + W.q, w + W.beta, w + W.gram,
+                       reinterpret_cast<uint8_t *>(w + W.images), reinterpret_cast<uint8_t *>(w + W.weights),
                        reinterpret_cast<unsigned long long *>(w + W.paths), watchdog_block()};
     if (p.watchdog == nullptr) return GDN_ERR_LAUNCH;
     const cudaStream_t s = as_cuda(stream);

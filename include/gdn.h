@@ -786,7 +786,8 @@ gdn_status gdn_attn_tree(const void *q, const void *k_pages, const void *v_pages
  * them on. (A snapshot per node, as gdn_block_prefill_snapshots keeps for a chain, would be
  * n_nodes states of every sequence and layer.)
  * qkv [n_seqs][n_nodes][C], alpha, b [n_seqs][n_nodes][H], z, out [n_seqs][n_nodes][H][S]; the
- * other arguments as for gdn_block_prefill (any K in [2, 8]).
+ * other arguments as for gdn_block_prefill (any K in [2, 8]; with S = 128 a pool of 2^31 state rows,
+ * a terabyte, is GDN_ERR_UNSUPPORTED).
  * tape: gdn_block_tree_tape_size() bytes, written; one per layer, kept until the commit.
  * workspace: gdn_block_tree_workspace_size() bytes, contents on entry irrelevant and garbage
  * afterwards; layers may share it. Both 16-byte aligned, 0 bytes for invalid sizes. */

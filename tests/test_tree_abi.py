@@ -160,3 +160,8 @@ def test_binding_refuses_wrong_tensors():
         gdn.gdn_block_tree_commit(x, x, x, i, i, 1, 2, 1, 1, 32, 4, x, stream=0)
     with pytest.raises(ValueError):
         gdn.gdn_attn_tree(x, x, x, i, i, x, i, 1, 2, 1, 1, 64, 16, 1, 1, 0, 0, 1.0, x, stream=0)
+
+
+def test_pools_of_a_terabyte(lib):
+    assert block(lib, s=128, pool=1 << 22, h=4, slots=P) == UNSUP
+    assert block(lib, s=128, pool=1 << 22, h=4, slots=P, n=0) == UNSUP
