@@ -90,10 +90,11 @@ struct TreeParams {
 
 // ------------------------------------------------------------------ conv, norms and gates
 
-// (Of other states than 128, whose nodes' sums have no tensor cores; the arithmetic is shared.) One warp per (head slice of S channels, kConvNodes nodes, sequence), lane L holding channels
-// [E L, E L + E). A node's taps are its own raw input and those of its nearest ancestors, the
-// conv history behind the root's; the arithmetic is the prefill block's, so a tree that is a chain
-// has its bits. The CTAs behind the slices' compute the gates. A node that is not there has zeros.
+// (Of other states than 128, whose nodes' sums have no tensor cores; the arithmetic is shared.) One
+// warp per (head slice of S channels, kConvNodes nodes, sequence), lane L holding channels [E L, E L +
+// E). A node's taps are its own raw input and those of its nearest ancestors, the conv history behind
+// the root's; the arithmetic is the prefill block's, so a tree that is a chain has its bits. The CTAs
+// behind the slices' compute the gates. A node that is not there has zeros.
 constexpr int kConvWarps = 4;
 constexpr int kConvNodes = 8;
 
@@ -448,16 +449,17 @@ __global__ void __launch_bounds__(kStateThreads) tree_state_kernel(const TreePar
 // S1 and S2 multiply the first two images at once, into two column groups that are added up later.
 //
 // A kernel ahead of it convolves the values, and per (sequence, k-head) convolves q and k, writes the
-// images, and for every v-head of the k-head solves the nodes' triangular system: with A[i][s] = beta_i e^{G_i - G_s} k_i.k_s (s above i) and
-// T = (I + A)^-1,
+// images, and for every v-head of the k-head solves the nodes' triangular system: with A[i][s] =
+// beta_i e^{G_i - G_s} k_i.k_s (s above i) and T = (I + A)^-1,
 //   R_s = beta_s (v_s - e^{G_s} S0^T k_s),   u_i = sum_{s on the path to i} T[i][s] R_s,
 //   y_i = scale (e^{G_i} S0^T q_i + sum_s W[i][s] R_s),   W = B T, B[i][s] = e^{G_i - G_s} q_i.k_s,
 // so that over the state all nodes are independent of one another. T and W are lists along the paths.
 //
-// 64 sequences of 16 nodes, 16 k- and 32 v-heads: 102 us, of which the kernel ahead takes 44 (issue and
-// latency; with a kernel of its own for the convolution 28 and 29) and this one 56 (it reads 198 MB and
-// writes 19 in that time: 3.9 TB/s; between barriers its 16 warps an SM issue in 4 cycles of 10). One
-// sequence of 48 nodes: 36 us, 13 of them here. (Node after node over the state instead of T: 122 and 45.)
+// 64 sequences of 16 nodes, 16 k- and 32 v-heads: 102 us, of which the kernel ahead takes 44 (issue
+// and latency; with a kernel of its own for the convolution 28 and 29) and this one 56 (it reads 198
+// MB and writes 19 in that time: 3.9 TB/s; between barriers its 16 warps an SM issue in 4 cycles of
+// 10). One sequence of 48 nodes: 36 us, 13 of them here. (Node after node over the state instead of T:
+// 122 and 45.)
 constexpr int kTcThreads = 256;
 constexpr uint32_t kColA = 0, kColD = 192;  // tensor memory: the state's parts, 64 columns each; D, two groups
 
@@ -482,11 +484,11 @@ __host__ __device__ inline uint32_t tmem_cols(const TcSizes &z) {
     return kColD + 2u * static_cast<uint32_t>(z.rows) <= 256u ? 256u : 512u;
 }
 
-// Convolution, images and weights. CTAs of (k-head, part of its v-heads, sequence): 4 warps, 8 or 16 where that
-// leaves SMs idle, and then with few sequences a part for every v-head. q and k, a warp a node; the
-// nodes' products, a warp a node; then, for a few v-heads at a time, A and B as lists along the
-// paths, one thread an entry, and T and W, all rows of one depth together. The CTAs behind them convolve the
-// values, a warp a v-head of up to kConvNodes nodes.
+// Convolution, images and weights. CTAs of (k-head, part of its v-heads, sequence): 4 warps, 8 or 16
+// where that leaves SMs idle, and then with few sequences a part for every v-head. q and k, a warp a
+// node; the nodes' products, a warp a node; then, for a few v-heads at a time, A and B as lists along
+// the paths, one thread an entry, and T and W, all rows of one depth together. The CTAs behind them
+// convolve the values, a warp a v-head of up to kConvNodes nodes.
 constexpr int kPrepThreads = 512;
 constexpr int kPrepHeads = 4;
 
@@ -519,7 +521,8 @@ __global__ void __launch_bounds__(kPrepThreads, K <= 4 ? 2 : 1) tree_prepare_ker
     __shared__ int up[kMaxNodes];
     __shared__ int level[kMaxNodes + 1];      // [d]: where the nodes of depth d + 1 begin in by_depth
     __shared__ uint8_t by_depth[kMaxNodes];
-    __shared__ float g_of[kPrepHeads][kMaxNodes], beta_of[kPrepHeads][kMaxNodes], hi_of[kPrepHeads][kMaxNodes], lo_of[kPrepHeads][kMaxNodes];
+    __shared__ float g_of[kPrepHeads][kMaxNodes], beta_of[kPrepHeads][kMaxNodes];
+    __shared__ float hi_of[kPrepHeads][kMaxNodes], lo_of[kPrepHeads][kMaxNodes];  // the sums of g on the paths
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x, warps = threads / 32;
     const int N = p.n_nodes, Hk = p.n_k_heads, H = p.n_v_heads;
     const bool prepare = static_cast<int>(blockIdx.x) < prepares;
@@ -1007,11 +1010,12 @@ struct CommitParams {
     unsigned *watchdog;
 };
 
-// S <- e^{G_l} S0 + sum_{s on the path to l} e^{G_l - G_s} k_s u_s^T: the state in and out once bounds it.
-// Work is dealt out in blocks of 16 KB of state rows, a contiguous range to each of the first
+// S <- e^{G_l} S0 + sum_{s on the path to l} e^{G_l - G_s} k_s u_s^T: the state in and out once bounds
+// it. Work is dealt out in blocks of 16 KB of state rows, a contiguous range to each of the first
 // `state_ctas` CTAs; a block's rows are fetched by a bulk copy, and its path's k, u and g into
-// registers, while the block before is worked on. 64 sequences, 32 heads of 128: 60 us, 0.71 of the copy rate (a CTA per 64
-// rows, each with its lookups, path and loads behind one another: 65). The other CTAs roll the conv history, a share of a sequence's channels each.
+// registers, while the block before is worked on. 64 sequences, 32 heads of 128: 60 us, 0.71 of the
+// copy rate (a CTA per 64 rows, each with its lookups, path and loads behind one another: 65). The
+// other CTAs roll the conv history, a share of a sequence's channels each.
 constexpr int kCommitThreads = 256;
 constexpr int kCommitNodes = 16;
 constexpr int kCommitChannels = kCommitThreads * 4;
@@ -1261,9 +1265,11 @@ gdn_status launch_tc(const TreeParams &p, int n_seqs, cudaStream_t s) {
     const int parts = static_cast<long long>(n_seqs) * p.n_v_heads <= 152 ? groups : 1;  // (few trees: a CTA a v-head)
     const long long prepares = static_cast<long long>(n_seqs) * p.n_k_heads * parts;
     const int threads = prepares <= 152 ? kPrepThreads : prepares <= 4 * 152 ? kPrepThreads / 2 : kPrepThreads / 4, warps = threads / 32;
-    const long long others = static_cast<long long>(n_seqs) * ((p.n_v_heads + warps - 1) / warps) * ((p.n_nodes + kConvNodes - 1) / kConvNodes);
+    const int head_groups = (p.n_v_heads + warps - 1) / warps, node_blocks = (p.n_nodes + kConvNodes - 1) / kConvNodes;
+    const long long others = static_cast<long long>(n_seqs) * head_groups * node_blocks;
     if (prepares + others > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
-    tree_prepare_kernel<K><<<static_cast<unsigned>(prepares + others), threads, PrepSmem(p.n_nodes).bytes, s>>>(p, static_cast<int>(prepares), parts);
+    tree_prepare_kernel<K><<<static_cast<unsigned>(prepares + others), threads, PrepSmem(p.n_nodes).bytes, s>>>(
+        p, static_cast<int>(prepares), parts);
     GDN_TRY(launch_status());
     const TcSizes z(p.n_nodes);
     const uint32_t smem = TcSmem(z, p.n_nodes).bytes + 1024;
