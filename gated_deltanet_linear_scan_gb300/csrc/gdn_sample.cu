@@ -555,6 +555,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         }
         return;  // the whole cluster
     }
+    if (cluster > 1) {  // (waited for ahead of the first store to another CTA, behind the first pass over the row)
+        __syncwarp();
+        cluster_arrive_release();
+    }
     const bool greedy = temperature == 0.0f || min_p > 1.0f || top_k == 1;
     const bool by_count = top_k > 0 && top_k < p.vocab;
 
@@ -607,6 +611,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         for (int w = 0; w < kWarps; ++w) mass += sh.warp_mass[w];
     }
     if (cluster > 1) {
+        __syncwarp();
+        cluster_wait_acquire();  // every CTA of the cluster runs: until then it has no shared memory to write to
         if (tid < cluster) {
             *in_cta(&sh.tops[rank], tid) = top;
             *in_cta(&sh.masses[rank], tid) = mass;
