@@ -663,6 +663,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         const float err = __fsub_rn(__fsub_rn(bits, __fsub_rn(k, back)), __fadd_rn(prod, back));
         weigher.k_hi = k;
         weigher.k_lo = __fadd_rn(__fsub_rn(err, rest), kExpShort);
+        // An infinite top, or a product past the range: the floats next to such a top are 2^104 of z below
+        // it (infinitely far, of an infinite one), so every smaller logit has a weight of 0. The
+        // arguments are -infinity then, and none of their parts is NaN.
+        if (!(fabsf(prod) < INFINITY)) {
+            weigher.c_lo = weigher.k_lo = 0.0f;
+            weigher.k_hi = -INFINITY;
+        }
     }
     auto weight = [&](float x) { return weight_of(weigher, x); };
     Queue queue{sh.queue[warp], 0};
