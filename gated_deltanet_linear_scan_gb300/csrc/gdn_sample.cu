@@ -5,11 +5,15 @@
 // first `ties` of those equal to V; the token is the first index whose running sum of e^{z_i}, over
 // what is kept in index order, exceeds u times the whole sum.
 //
-// Whether a sum falls short of a border decides the token, so the weights are held to 2^-43 of the
-// sum (e^{z} in two floats, then 64-bit integers): integer sums do not depend on their order,
-// every pass over a row agrees with every other, and a wrong side of a border is as likely as a
-// uniform number within 10^-11 of it. (With weights of 24 bits, one row in some hundred of a
-// vocabulary of 100,000 would come out another token.)
+// Whether a sum falls short of a border decides the token, so the weights are 64-bit integers in units
+// of 2^-43 of the sum: integer sums do not depend on their order, and every pass over a row agrees
+// with every other. Weights above 2^-20 of the sum (e^{z} in two floats) are good to a unit, smaller
+// ones, of one exponential in fp32, to 2^-20 of themselves. So the edge between two tokens is off by at
+// most vocab 2^-43 + 2^-20 s of the sum, s the share of the small ones. Where logits differ most of
+// that cancels; it adds up where they repeat: 100,000 equal tokens beside one that is 2^20 times as
+// likely are 9 % of the sum, and at 2^-22.2 of a weight and half a unit the edges among them are off by
+// up to 3 10^-8, half a step of the uniform number. (With weights of 24 bits throughout, one row in some hundred
+// of a vocabulary of 100,000 would come out another token.)
 //
 // A cluster of 1 to 8 CTAs takes a row, a warp a stretch of it. The first pass finds the largest logit;
 // later ones read the row again from L2 (rows in flight fit there). Most tokens of a row are so unlikely
@@ -179,8 +183,10 @@ __device__ __noinline__ u64 precise_weight(const Weigher w, float x) {
 }
 
 // The weight of an unlikely one, below 2^23 and so the last bits of 2^23 more than it. Its argument
-// is near 0 where the weight counts most, and all but exact there: the error is the exponential's,
-// 2^-22 of 2^-20 of the largest.
+// is near 0 where the weight counts most, and all but exact there: the error is the exponential's
+// (over all floats of its range at most 2^-22.7, measured) and that of kExpShort, which it has not
+// everywhere: 2^-22.2 in all. Down to 2^-16 of the largest of these weights the two roundings of the
+// argument make it 2^-20.
 constexpr unsigned kSmallBase = 0x4B000000u;  // 2^23
 __device__ __forceinline__ unsigned small_weight_bits(const Weigher &w, float x) {
     const float t = __fadd_rn(__fmaf_rn(x, w.c_hi, w.k_hi), __fmaf_rn(x, w.c_lo, w.k_lo));

@@ -848,9 +848,12 @@ gdn_status gdn_tree_accept(const int32_t *parents, const int32_t *tokens, const 
  * largest logit; top_k <= 0 or >= vocab, top_p >= 1 and min_p <= 0 filter nothing. NaN logits count
  * as -infinity, which is never taken; +infinity leaves only the +infinities. A row without a logit
  * above -infinity gets token -1; so does one whose temperature is negative or not finite, or
- * whose top_p or min_p is NaN, which is counted in err_count. Weights are held to 2^-43 of
- * their sum, as integers, so that tokens do not depend on the order of sums. vocab: at most 2^20, else
- * GDN_ERR_UNSUPPORTED. */
+ * whose top_p or min_p is NaN, which is counted in err_count. Weights are integers, in units of
+ * at most 2^-43 of their sum, so that tokens do not depend on the order of sums. Those above 2^-20
+ * of the sum are good to a unit, a smaller one to half a unit and 2^-20 of itself: edges between tokens,
+ * and the border of top_p, are off by at most vocab * 2^-43 + 2^-20 * (the smaller ones' share) of
+ * the sum, and a number that falls closer to an edge than that may get the token beside it. vocab:
+ * at most 2^20, else GDN_ERR_UNSUPPORTED. */
 gdn_status gdn_sample(const void *logits, const float *uniforms, const float *temperature,
                       const int32_t *top_k, const float *top_p, const float *min_p,
                       int32_t *tokens, int rows, int vocab, int row_stride, int dtype,
