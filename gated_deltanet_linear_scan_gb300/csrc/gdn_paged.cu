@@ -36,11 +36,17 @@ gdn_status encode(CUtensorMap *map, const void *base, int dtype, int rank, const
     const EncodeTiled fn = encoder();
     if (fn == nullptr) return GDN_ERR_LAUNCH;
     const cuuint32_t unit[3] = {1, 1, 1};
-    const CUresult r =
-        fn(map, map_type(dtype), static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims,
-           strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? GDN_OK : GDN_ERR_LAUNCH;
+    auto encode_once = [&] {
+        return fn(map, map_type(dtype), static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims,
+                  strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    if (encode_once() == CUDA_SUCCESS) return GDN_OK;
+    // A driver call, it wants the device's context to be current, which in a host thread that has not
+    // used the GPU yet it is not: the runtime makes it so where the thread's device is set.
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess || cudaSetDevice(device) != cudaSuccess) return GDN_ERR_LAUNCH;
+    return encode_once() == CUDA_SUCCESS ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
 }  // namespace
