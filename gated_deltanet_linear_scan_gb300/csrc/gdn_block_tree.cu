@@ -1288,11 +1288,10 @@ gdn_status launch_fp32(const TreeParams &p, int n_seqs, cudaStream_t s) {
     tree_gram_kernel<E><<<dim3(p.n_k_heads, n_seqs), 32 * kGramWarps, keys, s>>>(p);
     GDN_TRY(launch_status());
     using L = StateSmem<E>;
-    const size_t smem = L::bytes(p.n_nodes);
-    if (cudaFuncSetAttribute(tree_state_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess)
-        return GDN_ERR_LAUNCH;
-    tree_state_kernel<E><<<dim3(L::S / L::JB, p.n_v_heads, n_seqs), kStateThreads, smem, s>>>(p);
+    // (the most that any tree takes: a limit of this call's own would be under another thread's larger one)
+    static std::atomic<unsigned long long> state_allowed{0};
+    GDN_TRY(allow_smem(tree_state_kernel<E>, static_cast<int>(L::bytes(kMaxNodes)), state_allowed));
+    tree_state_kernel<E><<<dim3(L::S / L::JB, p.n_v_heads, n_seqs), kStateThreads, L::bytes(p.n_nodes), s>>>(p);
     GDN_TRY(launch_status());
     const long long rows = static_cast<long long>(n_seqs) * p.n_nodes * p.n_v_heads;
     tree_norm_kernel<E><<<static_cast<unsigned>((rows + kNormThreads / 32 - 1) / (kNormThreads / 32)),
