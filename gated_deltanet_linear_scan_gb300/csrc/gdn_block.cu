@@ -649,10 +649,9 @@ gdn_status launch_block_persistent(BlockParams p, int n_seqs, cudaStream_t s, bo
     p.ratio = ratio;
     p.split = 1;
     const size_t smem = PLayout(S, ratio, stages).total;
-    if (cudaFuncSetAttribute(block_decode_persistent_kernel<E>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess)
-        return GDN_ERR_LAUNCH;
+    // (the most that any heads take: a limit of this call's own would be under another thread's larger one)
+    static std::atomic<unsigned long long> allowed{0};
+    GDN_TRY(allow_smem(block_decode_persistent_kernel<E>, kPSmemBudget, allowed));
     used = true;
     // Consecutive decode steps walk the groups in alternating directions. A step leaves
     // the state it wrote last (tens of MB) dirty in L2; the next step, walking the other
@@ -686,11 +685,8 @@ gdn_status launch_block(BlockParams p, int n_seqs, cudaStream_t s) {
     p.split = split;
     const int rb = S / split;
     const size_t smem = BlockSmem<E>::bytes(rb);
-    if (smem > 48 * 1024) {
-        if (cudaFuncSetAttribute(block_decode_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem)) != cudaSuccess)
-            return GDN_ERR_LAUNCH;
-    }
+    static std::atomic<unsigned long long> allowed{0};
+    GDN_TRY(allow_smem(block_decode_kernel<E>, static_cast<int>(BlockSmem<E>::bytes(S == 256 ? S / 2 : S)), allowed));
     const long long blocks = static_cast<long long>(n_seqs) * p.n_k_heads * ratio * split;
     if (blocks > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
