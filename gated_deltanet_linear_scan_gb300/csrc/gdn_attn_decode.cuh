@@ -38,6 +38,7 @@
 #include <atomic>
 #include <ctime>
 
+#include "gdn_attn_again.cuh"
 #include "gdn_chunk_common.cuh"  // named_barrier_or
 #include "gdn_paged.cuh"
 #include "gdn_tc.cuh"  // split3
@@ -89,6 +90,8 @@ struct Params {
     unsigned long long nonce;
     const int32_t *parents;          // [n_seqs][n_tokens], of a tree
     unsigned *watchdog;              // of a tree's call: the flag of the decode calls' unit
+    const void *q, *k_pages, *v_pages;  // of a tree's call, for rows that came out NaN
+    int q_stride;
 };
 
 // RT: rows the arithmetic is laid out for (16-bit types: always 16, one matrix fragment).
@@ -363,6 +366,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     __shared__ unsigned long long trees[TREE ? 2 : 1][TREE ? kMaxNodes : 1];  // paths, of a segment
     __shared__ unsigned long long path_of[TREE ? kMaxNodes : 1];              // the loading warp's
     __shared__ int up_of[TREE ? kMaxNodes : 1];
+    __shared__ int first_key[TREE ? 2 : 1];  // of the tiles of a segment, by turns
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // (A wait that gives up: the warp leaves, and nothing of the units concerned is written.)
@@ -1074,6 +1078,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[s]);
+        if (TREE && (flags & kFirst) && tid == 0) first_key[seg & 1] = key0;
         if ((flags & kFirst) && tid == 0 && !(sg.flags & kWhole)) tag(p.counters + sg.c0, word_seen, p.nonce);
         if (++s == G::kStages) {
             s = 0;
@@ -1129,6 +1134,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         const bool whole = sg.flags & kWhole;
         float *record = p.partials +
                         static_cast<size_t>(2 * blockIdx.x + ((sg.flags & kHead) ? 1 : 0)) * kRecord;
+        unsigned odd = 0;  // TREE: rows of which this thread has columns that came out NaN
         if constexpr (kFrag) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -1136,6 +1142,13 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                 const long long row = sg.out_row(p, t, r - t * p.heads_per_unit);
                 if (row < 0) continue;
                 const float l = row_l[r], inv = 1.0f / l;
+                if constexpr (TREE) {
+                    bool nan = false;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) nan |= o16[j][2 * half] != o16[j][2 * half] || o16[j][2 * half + 1] != o16[j][2 * half + 1];
+                    // (a length of 0: not there, or nothing seen; NaN: of weights that are)
+                    if (nan && l > 0.0f) odd |= 1u << r;
+                }
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
                     const int col = (warp * NT + j) * 8 + 2 * (lane & 3);
@@ -1158,6 +1171,9 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                 for (int r = 0; r < RT; ++r) {
                     const long long row = sg.out_row(p, r / p.heads_per_unit, r % p.heads_per_unit);
                     if (row < 0) continue;
+                    if (TREE && row_l[r] > 0.0f &&
+                        (o32[r][0] != o32[r][0] || o32[r][1] != o32[r][1] || o32[r][2] != o32[r][2] || o32[r][3] != o32[r][3]))
+                        odd |= 1u << r;
                     if (whole) {
                         const float l = row_l[r], inv = 1.0f / l;
                         *reinterpret_cast<float4 *>(out + row * D + col) =
@@ -1168,6 +1184,30 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                                make_float4(o32[r][0], o32[r][1], o32[r][2], o32[r][3]));
                     }
                 }
+            }
+        }
+        if constexpr (TREE) {
+            __syncwarp();
+            for (odd = __reduce_or_sync(FULL_MASK, odd); odd != 0; odd &= odd - 1) {
+                const int r = __ffs(odd) - 1;
+                const long long row = sg.out_row(p, r / p.heads_per_unit, r % p.heads_per_unit);
+                AgainRow<T> x;
+                x.q = static_cast<const T *>(p.q) + row / p.n_q_heads * p.q_stride + row % p.n_q_heads * D;
+                x.k_pages = static_cast<const T *>(p.k_pages);
+                x.v_pages = static_cast<const T *>(p.v_pages);
+                x.parents = p.parents + static_cast<size_t>(sg.seq) * p.n_tokens;
+                x.out = out + row * D;
+                x.record = whole ? nullptr : record + r * D;
+                x.slot = p.cache.slots ? p.cache.slots[sg.seq] : sg.seq;
+                x.kvh = sg.kvh;
+                x.node = sg.token_group * p.tokens_per_unit + r / p.heads_per_unit;
+                x.base = sg.len - p.n_tokens;
+                x.len = sg.len;
+                x.from = first_key[(seg & 1) ^ 1];  // (seg is the next one's)
+                x.to = key0 + KT;
+                x.scale_log2 = p.scale_log2;
+                x.l = row_l[r];
+                again<T, D, D / 4, kSplit>(p.cache, p.mask, x, warp * (D / 4));
             }
         }
         if (whole) continue;
@@ -1372,6 +1412,10 @@ gdn_status attn_decode_call(const void *q, const void *k_pages, const void *v_pa
     p.nonce = next_nonce();
     p.parents = parents;
     p.watchdog = TREE ? watchdog_attn_decode() : nullptr;
+    p.q = q;
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.q_stride = q_stride;
     if (TREE && p.watchdog == nullptr) return GDN_ERR_LAUNCH;
 
     // the ranges are counted in 32 bits (2^31 tiles are some 70 TB read in one call)

@@ -20,6 +20,7 @@
 // heads a key head over 16001..40000: 200-205, 0.39: two units a key head, of 256 and 128 rows, 2.1 us a
 // tile in both, of which the products are 1.1; neither fewer instructions, nor keys from L2, nor other weights in
 // the dealing changed that. One of 24 over 4000, heads of 256: 28, of which the join's launch is 4.
+#include "gdn_attn_again.cuh"
 #include "gdn_attn_tc.cuh"
 #include "gdn_attn_tree.cuh"
 #include "gdn_tree.cuh"
@@ -830,6 +831,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 const int r = (turns ? 0 : i * kTcRows) + row;
                 float *sums = record + static_cast<size_t>(r) * D;
                 const bool nothing = l == 0.0f;
+                bool nan = false;  // (for infinities of both signs, too)
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32], y[32];
@@ -846,6 +848,10 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                             z[x] = __ffma2_rn(make_float2(__uint_as_float(y[2 * x]), __uint_as_float(y[2 * x + 1])), other2, z[x]);
                     }
                     if (!mine) continue;
+                    float2 check = z[0];
+#pragma unroll
+                    for (int x = 1; x < 16; ++x) check = __fadd2_rn(check, z[x]);
+                    nan |= check.x + check.y != check.x + check.y;
                     if (w.whole) {
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
@@ -866,6 +872,28 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 if (!w.whole && mine) {
                     record[p.record_rows * D + r] = m == -INFINITY ? -INFINITY : m * mult;
                     record[p.record_rows * (D + 1) + r] = l;
+                }
+                __syncwarp();
+                for (unsigned odd = __ballot_sync(FULL_MASK, nan && l > 0.0f); odd != 0; odd &= odd - 1) {
+                    const int from = __ffs(odd) - 1;
+                    const int node = w.node0 + __shfl_sync(FULL_MASK, token, from), head = w.head0 + __shfl_sync(FULL_MASK, row_head, from);
+                    AgainRow<T> x;
+                    x.q = static_cast<const T *>(p.q) + (static_cast<size_t>(w.seq) * p.n_nodes + node) * p.q_stride + static_cast<size_t>(head) * D;
+                    x.k_pages = static_cast<const T *>(p.k_pages);
+                    x.v_pages = static_cast<const T *>(p.v_pages);
+                    x.parents = p.parents + static_cast<size_t>(w.seq) * p.n_nodes;
+                    x.out = static_cast<T *>(p.out) + ((static_cast<long long>(w.seq) * p.n_nodes + node) * p.n_q_heads + head) * D;
+                    x.record = w.whole ? nullptr : record + static_cast<size_t>(__shfl_sync(FULL_MASK, r, from)) * D;
+                    x.slot = w.slot;
+                    x.kvh = w.kvh;
+                    x.node = node;
+                    x.base = base;
+                    x.len = len;
+                    x.from = w.tile(w.j0) * kTcKeys;  // (nobody sees what lies between the sinks' tiles and the window's)
+                    x.to = (w.tile(j1 - 1) + 1) * kTcKeys;
+                    x.scale_log2 = p.scale_log2;
+                    x.l = __shfl_sync(FULL_MASK, l, from);
+                    again<T, D, D, false>(p.cache, p.mask, x, 0);
                 }
                 tc::fence_before_sync();
             }

@@ -620,7 +620,8 @@ gdn_status gdn_block_prefill_noalloc(const float *qkv, const float *conv_w, floa
  * - What a page holds past the sequence's length, or at keys that no row of the sequence
  *   sees, has no effect, infinities and NaN included, and page ids before the window are
  *   not read. (Between rows of one sequence that see different keys a masked key has
- *   weight 0, so a value that is not finite at such a key gives NaN.) A visible page id
+ *   weight 0, so a value that is not finite at such a key gives NaN; gdn_attn_tree's nodes
+ *   are spared that.) A visible page id
  *   outside [0, n_pages) hides its keys and adds one or more to err_count. */
 
 typedef enum gdn_dtype { GDN_F32 = 0, GDN_F16 = 1, GDN_BF16 = 2 } gdn_dtype;
@@ -766,6 +767,9 @@ gdn_status gdn_pages_compact(void *pages, int32_t *page_table, const int32_t *kv
  * ancestors (inside the window of their positions, or among the sinks). A sequence whose kv_len
  * is below n_nodes is skipped and counted. A chain (parents -1, 0, 1, ...) gets
  * gdn_attn_decode's results up to rounding.
+ * Values that are not finite reach the nodes that see them and no others. (Nodes that they have
+ * made NaN all the same are computed once more, key by key: calls with such values in some branch
+ * take longer.) With 16-bit types an infinity that a node sees may give it NaN.
  * q, out [n_seqs][n_nodes][n_q_heads][head_dim]; other arguments, types and errors as
  * gdn_attn_decode. With 16-bit types and more than 16 rows of (node, head of a key head) the
  * weights are held as in the prompt attention.
