@@ -2,7 +2,7 @@
 //
 // The tiled products multiply every row's weights with every value of a tile: 0 times an infinity or a NaN, at a
 // key that other nodes see and this one does not (a node of another branch), makes the row NaN. And three bf16
-// parts of a value that is not finite, or above bf16's range, are NaN themselves. What such a row should be is told
+// parts of a key or value that is not finite, or above bf16's range, are NaN themselves. What such a row should be is told
 // by the keys that it sees, from the pages. A warp takes a row: its NaN columns, if such a value stands in them at a
 // key that it does not see (else, with whole operands, they are rightly NaN), 32 keys at a time until they are NaN
 // all the same. All other rows pay a comparison a column. (Looking for such values ahead of the products cost calls
@@ -21,13 +21,14 @@ __device__ __forceinline__ void put_value(__half *to, float x) { *to = __float2h
 __device__ __forceinline__ void put_value(__nv_bfloat16 *to, float x) { *to = __float2bfloat16_rn(x); }
 
 // A node's row of a head, the part of its keys that it is summed over (from .. to - 1), and where that went: `out`
-// or, unless NULL, `record` (the sums of a split unit's part), whose row has the length l.
+// or, unless NULL, `record` (the sums of a split unit's part), whose row has the length l. Where that is NaN the
+// record's sums become relative to a maximum of their own; it and the length go to ml, unless that is NULL.
 template <typename T>
 struct AgainRow {
     const T *q, *k_pages, *v_pages;
     const int32_t *parents;  // of the sequence's nodes
     T *out;
-    float *record;
+    float *record, *ml;
     int slot, kvh, node, base, len, from, to;
     float scale_log2, l;
 };
@@ -134,7 +135,7 @@ __device__ __noinline__ void again(const PagedCache &cache, const AttnMask &mask
         bool open = false;  // whether some column can still be other than NaN
 #pragma unroll
         for (int x = 0; x < N; ++x) open |= wanted[x] && sums[x] == sums[x];
-        if (!__any_sync(FULL_MASK, open)) break;
+        if (!__any_sync(FULL_MASK, open) && (!PARTS || r.ml == nullptr)) break;
     }
 #pragma unroll
     for (int x = 0; x < N; ++x) {
@@ -143,11 +144,17 @@ __device__ __noinline__ void again(const PagedCache &cache, const AttnMask &mask
         const float y = sums[x] / l;
         if (r.record == nullptr) {
             put_value(r.out + column, y);
+        } else if (PARTS && r.l != r.l) {
+            __stcg(r.record + column, sums[x]);
         } else {
             // (a rounding more than the sums had: the largest floats stay finite)
             const float z = y * r.l;
             __stcg(r.record + column, fabsf(y) < INFINITY && !(fabsf(z) < INFINITY) ? copysignf(0x1.fffffep127f, z) : z);
         }
+    }
+    if (PARTS && r.ml != nullptr && lane == 0) {
+        r.ml[0] = m;
+        r.ml[1] = l;
     }
     __syncwarp();
 }

@@ -367,8 +367,11 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
     __shared__ unsigned long long path_of[TREE ? kMaxNodes : 1];              // the loading warp's
     __shared__ int up_of[TREE ? kMaxNodes : 1];
     __shared__ int first_key[TREE ? 2 : 1];  // of the tiles of a segment, by turns
+    // what the first warp's rows have for a maximum and length that are NaN (a length below 0: nothing)
+    __shared__ float again_ml[TREE ? kRows : 1][2];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (TREE && tid < kRows) again_ml[TREE ? tid : 0][1] = -1.0f;
     // (A wait that gives up: the warp leaves, and nothing of the units concerned is written.)
     unsigned *const watchdog = TREE ? p.watchdog : &g_watchdog_attn_decode;
     const int subs = p.head_groups * p.token_groups;
@@ -1146,8 +1149,8 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                     bool nan = false;
 #pragma unroll
                     for (int j = 0; j < NT; ++j) nan |= o16[j][2 * half] != o16[j][2 * half] || o16[j][2 * half + 1] != o16[j][2 * half + 1];
-                    // (a length of 0: not there, or nothing seen; NaN: of weights that are)
-                    if (nan && l > 0.0f) odd |= 1u << r;
+                    // (a length of 0: not there, or nothing seen; NaN: of weights that are, rightly unless keys have parts)
+                    if (nan && (l > 0.0f || (kSplit && l != l))) odd |= 1u << r;
                 }
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
@@ -1198,6 +1201,7 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
                 x.parents = p.parents + static_cast<size_t>(sg.seq) * p.n_tokens;
                 x.out = out + row * D;
                 x.record = whole ? nullptr : record + r * D;
+                x.ml = kSplit && warp == 0 && !whole && row_l[r] != row_l[r] ? again_ml[r] : nullptr;
                 x.slot = p.cache.slots ? p.cache.slots[sg.seq] : sg.seq;
                 x.kvh = sg.kvh;
                 x.node = sg.token_group * p.tokens_per_unit + r / p.heads_per_unit;
@@ -1213,8 +1217,16 @@ attn_decode_kernel(const __grid_constant__ CUtensorMap q_map,
         if (whole) continue;
         ++handed;
         if (tid < kRows) {
-            __stcg(record + kRows * D + tid, row_m[tid]);
-            __stcg(record + kRows * D + kRows + tid, row_l[tid]);
+            float m = row_m[tid], l = row_l[tid];
+            if constexpr (kSplit) {
+                if (again_ml[tid][1] >= 0.0f) {
+                    m = again_ml[tid][0];
+                    l = again_ml[tid][1];
+                    again_ml[tid][1] = -1.0f;
+                }
+            }
+            __stcg(record + kRows * D + tid, m);
+            __stcg(record + kRows * D + kRows + tid, l);
         }
         // A range has at most two split units, its first and its last. The first one's arrival
         // (a fence takes thousands of cycles while copies are under way) and join are left to

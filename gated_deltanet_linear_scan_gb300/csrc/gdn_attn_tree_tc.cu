@@ -883,6 +883,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                     x.v_pages = static_cast<const T *>(p.v_pages);
                     x.parents = p.parents + static_cast<size_t>(w.seq) * p.n_nodes;
                     x.out = static_cast<T *>(p.out) + ((static_cast<long long>(w.seq) * p.n_nodes + node) * p.n_q_heads + head) * D;
+                    x.ml = nullptr;
                     x.record = w.whole ? nullptr : record + static_cast<size_t>(__shfl_sync(FULL_MASK, r, from)) * D;
                     x.slot = w.slot;
                     x.kvh = w.kvh;

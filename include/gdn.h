@@ -767,7 +767,7 @@ gdn_status gdn_pages_compact(void *pages, int32_t *page_table, const int32_t *kv
  * ancestors (inside the window of their positions, or among the sinks). A sequence whose kv_len
  * is below n_nodes is skipped and counted. A chain (parents -1, 0, 1, ...) gets
  * gdn_attn_decode's results up to rounding.
- * Values that are not finite reach the nodes that see them and no others. (Nodes that they have
+ * Keys and values that are not finite reach the nodes that see them and no others. (Nodes that they have
  * made NaN all the same are computed once more, key by key: calls with such values in some branch
  * take longer.) With 16-bit types an infinity that a node sees may give it NaN.
  * q, out [n_seqs][n_nodes][n_q_heads][head_dim]; other arguments, types and errors as

@@ -1,4 +1,4 @@
-"""Values that are not finite at a node, or at a key that only some nodes' windows reach: the nodes
+"""Keys and values that are not finite at a node, or at a key that only some nodes' windows reach: the nodes
 that see it have what the formula gives there, all others are as if it were not."""
 import numpy as np
 import pytest
@@ -85,6 +85,22 @@ def test_values_of_one_branch(cuda_lib, dtype, d, n_nodes, group, window, sinks)
             put(c, x, base - window + 1, v=value, head=0, dim=17)
     out = Call(cuda_lib, c, q, trees, 2 * group, window, sinks).go()
     check(c, out, q, trees, window, sinks, two_parts=dtype != "float32")
+    cuda_lib.gdn_device_error()
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n_nodes,group", SIZES)
+def test_keys_of_one_branch(cuda_lib, dtype, d, n_nodes, group):
+    rng = np.random.default_rng([d, n_nodes, group])
+    lens = [n_nodes, 127 + n_nodes, 700]
+    c, trees, q = case(rng, lens, n_nodes, 2, group, d, 16, dtype, chain=0.3)
+    for x, value in enumerate([np.inf, -np.inf, np.nan]):
+        base = lens[x] - n_nodes
+        put(c, x, base + n_nodes - 1, k=value, head=1, dim=3)
+        put(c, x, base + n_nodes // 2, k=-value, v=value, head=0, dim=d - 1)
+    out = Call(cuda_lib, c, q, trees, 2 * group).go()
+    check(c, out, q, trees, 0, 0, two_parts=dtype != "float32")
     cuda_lib.gdn_device_error()
 
 
