@@ -31,6 +31,7 @@
 // 195, top-k of 50 219, top-p of 0.9 226, min-p 177, all 247 (without the lists 351, 449, 174, 592).
 // Flat rows cost more, as many tokens have weights that count: top-p of 0.98 at a temperature of 1.3 1.2
 // ms. One row of 128000 bf16 logits by top-p 27 us, nearly all of it barriers and latency.
+#include <cstddef>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -127,6 +128,10 @@ struct __align__(16) Shared {
     int warp_first[kWarps];
     double log_min;  // T ln(min_p)
 };
+// (read 16 bytes a time; two CTAs share an SM, which keeps 1 KB of each for itself)
+static_assert(offsetof(Shared, lo) % 16 == 0 && offsetof(Shared, hi) % 16 == 0 && offsetof(Shared, least) % 16 == 0 &&
+              offsetof(Shared, most) % 16 == 0, "histograms are read 16 bytes a time");
+static_assert(sizeof(Shared) <= 228 * 1024 / 2 - 1024, "two CTAs an SM");
 
 // A float's place in the order of floats, as an unsigned number (-0 is +0); and back.
 __device__ __forceinline__ unsigned key_of(float x) {
