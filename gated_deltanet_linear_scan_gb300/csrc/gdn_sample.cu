@@ -558,7 +558,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     const int top_k = p.top_k ? p.top_k[set] : 0;
     float u = p.uniforms[row];
     u = u < 1.0f ? (u > 0.0f ? u : 0.0f) : u >= 1.0f ? 0.99999994f : 0.0f;
-    const bool valid = temperature >= 0.0f && temperature < INFINITY && top_p == top_p && min_p == min_p;
+    // (from 2^100 on, logits further apart than the largest float could still both have weights)
+    const bool valid = temperature >= 0.0f && temperature < 0x1p100f && top_p == top_p && min_p == min_p;
     if (!valid) {
         if (rank == 0 && tid == 0) {
             p.tokens[row] = -1;

@@ -851,7 +851,7 @@ gdn_status gdn_tree_accept(const int32_t *parents, const int32_t *tokens, const 
  * consecutive rows (e.g. a tree's nodes), or NULL: 1, and no filter. Temperature 0 takes the
  * largest logit; top_k <= 0 or >= vocab, top_p >= 1 and min_p <= 0 filter nothing. NaN logits count
  * as -infinity, which is never taken; +infinity leaves only the +infinities. A row without a logit
- * above -infinity gets token -1; so does one whose temperature is negative or not finite, or
+ * above -infinity gets token -1; so does one whose temperature is negative or 2^100 or more, or
  * whose top_p or min_p is NaN, which is counted in err_count. Weights are integers, in units of
  * at most 2^-43 of their sum, so that tokens do not depend on the order of sums. Those above 2^-20
  * of the sum are good to a unit, a smaller one to half a unit and 2^-20 of itself: edges between tokens,
