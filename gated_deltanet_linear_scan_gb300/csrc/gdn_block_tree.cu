@@ -302,13 +302,16 @@ struct StateSmem {
 };
 
 // The sums on the nodes' paths, in two parts (hi + lo, off by 2^-40 relative): their differences
-// e^{G_i - G_s} are then good to 2^-23 however long the path is.
+// e^{G_i - G_s} are then good to 2^-23 however long the path is. A log-decay ends at -kForgets, where its node
+// forgets everything many times over: behind that node the sums' differences stay as good, however far below
+// (or at -infinity) it was.
+constexpr float kForgets = 16384.0f;
 __device__ __forceinline__ void path_sum(unsigned long long path, const float *g, float &hi, float &lo) {
     hi = lo = 0.0f;
     while (path != 0) {
         const int s = __ffsll(static_cast<long long>(path)) - 1;
         path &= path - 1;
-        const float x = g[s], sum = __fadd_rn(hi, x), y = __fsub_rn(sum, hi);
+        const float x = g[s] < -kForgets ? -kForgets : g[s], sum = __fadd_rn(hi, x), y = __fsub_rn(sum, hi);
         lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(sum, y)), __fsub_rn(x, y)));
         hi = sum;
     }
